@@ -15,13 +15,18 @@ from . import build as _build
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_WORKSPACE, ERR_CUDA, ERR_TIMEOUT = range(6)
 NORM_NONE, NORM_BATCH, NORM_LAYER, NORM_GROUP = 0, 1, 2, 3
 ACT_IDENTITY, ACT_RELU, ACT_TANH, ACT_SIGMOID = 0, 1, 2, 3
+ACT_GELU, ACT_SILU = 4, 5  # dense layers only
 FP32, BF16 = 0, 1
+FP16, E4M3 = 2, 3  # conv2d_mat only
 OP_FWD_TRAIN, OP_FWD_INFER, OP_BWD = 0, 1, 2
 
 EXPORTS = (
     "conv2d_out_hw", "conv2d_validate", "conv2d_workspace_size", "conv2d_fwd_train", "conv2d_fwd_infer",
     "conv2d_bwd", "conv2d_device_status", "conv2d_status_str", "conv2d_prof_enable", "conv2d_prof_read",
     "conv2d_fwd_train_noalloc", "conv2d_selftest_wait_limit",
+    "conv2d_q8_encode", "conv2d_q8_decode", "conv2d_rms_norm_fwd", "conv2d_rms_norm_bwd",
+    "conv2d_rms_norm_bwd_workspace_size", "conv2d_dense_fwd", "conv2d_dense_bwd", "conv2d_dense_fwd_workspace_size",
+    "conv2d_dense_bwd_workspace_size",
 )
 
 
@@ -29,6 +34,16 @@ class Conv2dDesc(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("N", "H", "W", "IC", "OC", "KH", "KW", "stride", "pad", "norm", "act",
                                               "dtype")] + [("eps", ctypes.c_float), ("momentum", ctypes.c_float),
                                                            ("bn_eval", ctypes.c_int32), ("groups", ctypes.c_int32)]
+
+
+class Mat(ctypes.Structure):
+    """conv2d_mat: a row-major matrix in device memory (ld 0: rows lie dense)."""
+    _fields_ = [("data", ctypes.c_void_p), ("ld", ctypes.c_int64), ("type", ctypes.c_int32), ("group", ctypes.c_int32),
+                ("scale", ctypes.c_void_p)]
+
+
+class DenseDesc(ctypes.Structure):
+    _fields_ = [("M", ctypes.c_int64)] + [(n, ctypes.c_int32) for n in ("K", "N", "act", "dtype", "accumulate")]
 
 
 class Conv2dError(RuntimeError):
@@ -67,6 +82,19 @@ def lib():
     L.conv2d_status_str.argtypes = [i32]
     L.conv2d_status_str.restype = ctypes.c_char_p
     L.conv2d_selftest_wait_limit.argtypes = [vp]
+    pm, pn, i64 = ctypes.POINTER(Mat), ctypes.POINTER(DenseDesc), ctypes.c_int64
+    L.conv2d_q8_encode.argtypes = [i64, i32, pm, pm, vp]
+    L.conv2d_q8_decode.argtypes = [i64, i32, pm, pm, vp]
+    L.conv2d_rms_norm_fwd.argtypes = [i64, i32, ctypes.c_float, pm, pm, vp, pm, pm, pm, vp, vp]
+    L.conv2d_rms_norm_bwd.argtypes = [i64, i32, pm, vp, vp, pm, pm, pm, vp, i32, vp, sz, vp]
+    L.conv2d_rms_norm_bwd_workspace_size.argtypes = [i64, i32]
+    L.conv2d_rms_norm_bwd_workspace_size.restype = sz
+    L.conv2d_dense_fwd.argtypes = [pn, pm, pm, vp, pm, pm, pm, vp, sz, vp]
+    L.conv2d_dense_bwd.argtypes = [pn, pm, pm, pm, pm, pm, pm, vp, vp, sz, vp]
+    L.conv2d_dense_fwd_workspace_size.argtypes = [pn, pm, pm]
+    L.conv2d_dense_fwd_workspace_size.restype = sz
+    L.conv2d_dense_bwd_workspace_size.argtypes = [pn, pm, pm, pm, pm, pm, pm, vp]
+    L.conv2d_dense_bwd_workspace_size.restype = sz
     L.conv2d_prof_enable.argtypes = [i32]
     L.conv2d_prof_read.argtypes = [ctypes.POINTER(ctypes.c_char_p), fp, i32]
     _lib = L
@@ -148,6 +176,55 @@ def conv2d_bwd(d, x, w, gamma, beta, pre_act, save_mean, save_inv_std, dy, dx, d
     return lib().conv2d_bwd(ctypes.byref(d), _ptr(x), _ptr(w), _ptr(gamma), _ptr(beta), _ptr(pre_act),
                             _ptr(save_mean), _ptr(save_inv_std), _ptr(dy), _ptr(dx), _ptr(dw), _ptr(dbias),
                             _ptr(dgamma), _ptr(dbeta), _ptr(ws), ws_bytes, _stream(stream))
+
+
+def _ref(m):
+    return None if m is None else ctypes.byref(m)
+
+
+def _ws(ws, ws_bytes):
+    return ws.numel() * ws.element_size() if ws_bytes is None and ws is not None else (ws_bytes or 0)
+
+
+def conv2d_q8_encode(rows, cols, x, q8, stream=None):
+    return lib().conv2d_q8_encode(rows, cols, _ref(x), _ref(q8), _stream(stream))
+
+
+def conv2d_q8_decode(rows, cols, q8, x, stream=None):
+    return lib().conv2d_q8_decode(rows, cols, _ref(q8), _ref(x), _stream(stream))
+
+
+def conv2d_rms_norm_fwd(rows, cols, eps, x, residual, gamma, h, y, q8, inv_rms, stream=None):
+    return lib().conv2d_rms_norm_fwd(rows, cols, eps, _ref(x), _ref(residual), _ptr(gamma), _ref(h), _ref(y), _ref(q8),
+                                     _ptr(inv_rms), _stream(stream))
+
+
+def conv2d_rms_norm_bwd_workspace_size(rows, cols):
+    return int(lib().conv2d_rms_norm_bwd_workspace_size(rows, cols))
+
+
+def conv2d_rms_norm_bwd(rows, cols, h, gamma, inv_rms, dy, dh, dx, dgamma, accumulate, ws, ws_bytes=None, stream=None):
+    return lib().conv2d_rms_norm_bwd(rows, cols, _ref(h), _ptr(gamma), _ptr(inv_rms), _ref(dy), _ref(dh), _ref(dx),
+                                     _ptr(dgamma), int(accumulate), _ptr(ws), _ws(ws, ws_bytes), _stream(stream))
+
+
+def conv2d_dense_fwd_workspace_size(d, x, w):
+    return int(lib().conv2d_dense_fwd_workspace_size(ctypes.byref(d), _ref(x), _ref(w)))
+
+
+def conv2d_dense_fwd(d, x, w, bias, residual, pre_act, y, ws, ws_bytes=None, stream=None):
+    return lib().conv2d_dense_fwd(ctypes.byref(d), _ref(x), _ref(w), _ptr(bias), _ref(residual), _ref(pre_act), _ref(y),
+                                  _ptr(ws), _ws(ws, ws_bytes), _stream(stream))
+
+
+def conv2d_dense_bwd_workspace_size(d, x, w, pre_act, dy, dx, dw, dbias):
+    return int(lib().conv2d_dense_bwd_workspace_size(ctypes.byref(d), _ref(x), _ref(w), _ref(pre_act), _ref(dy),
+                                                     _ref(dx), _ref(dw), _ptr(dbias)))
+
+
+def conv2d_dense_bwd(d, x, w, pre_act, dy, dx, dw, dbias, ws, ws_bytes=None, stream=None):
+    return lib().conv2d_dense_bwd(ctypes.byref(d), _ref(x), _ref(w), _ref(pre_act), _ref(dy), _ref(dx), _ref(dw),
+                                  _ptr(dbias), _ptr(ws), _ws(ws, ws_bytes), _stream(stream))
 
 
 def conv2d_device_status(stream=None):

@@ -20,6 +20,7 @@
 #include <mutex>
 
 #include "conv2d.h"
+#include "host.h"
 #include "kernels.h"
 
 using namespace c2d;
@@ -30,17 +31,12 @@ namespace {
 __device__ int g_error_word;
 
 constexpr int kMaxDevices = 64;
-constexpr size_t kMaxDynSmem = 232448;  // 227 KB opt-in per block
-
-struct DevInfo {
-  bool init = false;
-  int sms = 0;
-  int* err = nullptr;
-};
 std::mutex g_mu;
 DevInfo g_dev[kMaxDevices];
 
-int device_info(DevInfo** out) {
+}  // namespace
+
+int c2d::device_info(DevInfo** out) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return CONV2D_ERR_CUDA;
   if (dev < 0 || dev >= kMaxDevices) return CONV2D_ERR_UNSUPPORTED;
@@ -55,14 +51,14 @@ int device_info(DevInfo** out) {
   return CONV2D_OK;
 }
 
-// SM count used for sizing when no device is visible (workspace queries on a
-// machine without a GPU).
-int sms_for_sizing() {
+int c2d::sms_for_sizing() {
   DevInfo* d = nullptr;
   if (device_info(&d) == CONV2D_OK) return d->sms;
   cudaGetLastError();
   return 152;
 }
+
+namespace {
 
 // ------------------------------------------------------------ profiling ring
 constexpr int kProfCap = 256;
@@ -77,7 +73,9 @@ ProfRec g_prof[kProfCap];
 int g_prof_head = 0, g_prof_count = 0;
 bool g_prof_events = false;
 
-int prof_begin(const char* name, cudaStream_t st) {
+}  // namespace
+
+int c2d::prof_begin(const char* name, cudaStream_t st) {
   if (!g_prof_on) return -1;
   std::lock_guard<std::mutex> lk(g_prof_mu);
   if (!g_prof_events) {
@@ -98,25 +96,13 @@ int prof_begin(const char* name, cudaStream_t st) {
   cudaEventRecord(g_prof[slot].a, st);
   return slot;
 }
-void prof_end(int slot, cudaStream_t st) {
+void c2d::prof_end(int slot, cudaStream_t st) {
   if (slot < 0) return;
   cudaEventRecord(g_prof[slot].b, st);
 }
 
-#define LAUNCH(name, st, call)                \
-  do {                                        \
-    const int _slot = prof_begin(name, st);   \
-    const cudaError_t _e = (call);            \
-    prof_end(_slot, st);                      \
-    if (_e != cudaSuccess) return CONV2D_ERR_CUDA; \
-  } while (0)
-
 // ------------------------------------------------------------ tensor maps
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_fn() {
+EncodeTiledFn c2d::encode_fn() {
   static EncodeTiledFn fn = nullptr;
   static std::once_flag once;
   std::call_once(once, [] {
@@ -129,6 +115,8 @@ EncodeTiledFn encode_fn() {
   });
   return fn;
 }
+
+namespace {
 
 // 2-D row-major tensor [rows][cols], 128-byte swizzled boxes of
 // box_cols x box_rows; out-of-range elements read as zero.

@@ -186,12 +186,6 @@ struct WgradParams {
   int* err;
 };
 
-__host__ __device__ inline uint32_t tmem_cols_for(int cols) {
-  uint32_t c = 32;
-  while (c < static_cast<uint32_t>(cols)) c <<= 1;
-  return c;
-}
-
 __device__ __forceinline__ const ConvPhase& find_phase(const ConvGemmParams& p, int u) {
   int i = 0;
   while (i + 1 < p.num_phases && p.ph[i + 1].unit_begin <= u) ++i;

@@ -1,0 +1,405 @@
+// dense.cu - the dense layer's C entry points: validation, workspace plan,
+// choice of kernel and tile, tensor maps, and the launch sequence.
+//
+//   conv2d_dense_fwd: [decode / repack x, w] -> GEMM (epilogue: scales, bias,
+//                     z in 16 or 8 bits, activation, residual)
+//   conv2d_dense_bwd: [dz = dy act'(z), column sums -> dbias] -> [decode /
+//                     repack w -> dx GEMM] -> [decode / repack x -> dW GEMM
+//                     -> join of its splits]
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <climits>
+#include <cmath>
+
+#include "conv2d.h"
+#include "dense.h"
+#include "host.h"
+#include "rows.h"
+
+using namespace c2d;
+
+namespace {
+
+long ceil_div(long a, long b) { return (a + b - 1) / b; }
+long round_up(long a, long b) { return ceil_div(a, b) * b; }
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+long ld_of(const conv2d_mat* m, int cols) { return m->ld ? m->ld : cols; }
+
+// ------------------------------------------------------------------ tiles
+// The longest K loop (k-blocks of 64 rows) one accumulator sums for a weight gradient kept in fp32: the
+// tensor core's fp32 sums are not rounded to nearest and lose about 2^-25 of the sum at every MMA, so 4,096
+// rows (256 MMAs) stay below 1e-5; longer products are split and the splits joined with ordinary fp32 adds.
+constexpr int kFp32SplitKb = 64;
+
+struct GemmPlan {
+  bool pair;
+  int BN, cluster, splits, kb_total, kb_per_split, l_tiles, c_tiles, stages, grid;
+  size_t smem;
+};
+
+// Kernel, tile, cluster size and splits by an estimate of each choice's clocks: a CTA's k-block takes the
+// larger of its MMA time (128 x BN x 64 products at 4,096 a clock, half a pair's) and of bringing its operand
+// tiles (about 64 bytes a clock); units run in waves over the SMs. can_split: the product may be split over k
+// with fp32 partials in the workspace (weight gradients); max_kb: bound on one accumulator's k-blocks (0: none).
+GemmPlan plan_gemm(long lanes, long cols, int kb, bool c_mn, bool can_split, int max_kb, int sms) {
+  GemmPlan best = {};
+  double best_t = 1e300;
+  auto consider = [&](bool pair, int BN, int cl, int splits) {
+    GemmPlan g = {};
+    g.pair = pair;
+    g.BN = BN;
+    g.cluster = cl;
+    g.kb_total = kb;
+    g.kb_per_split = static_cast<int>(ceil_div(kb, splits));
+    g.splits = static_cast<int>(ceil_div(kb, g.kb_per_split));
+    if (max_kb > 0 && ceil_div(g.kb_per_split, cl) > max_kb) return;
+    g.l_tiles = static_cast<int>(ceil_div(lanes, pair ? 256 : 128));
+    g.c_tiles = static_cast<int>(ceil_div(cols, BN));
+    const double units = static_cast<double>(g.l_tiles) * g.c_tiles * g.splits;
+    if (units * cl > INT_MAX / 4) return;
+    const int per_cta = pair ? BN / 2 : BN;  // columns of C a CTA loads
+    const double block = std::max(2.0 * BN, 2.0 * (128 + per_cta));
+    const double loop = static_cast<double>(ceil_div(g.kb_per_split, cl)) * block;
+    const double epi = 20.0 * BN;  // TMEM to memory
+    double t;
+    if (pair) t = std::ceil(units / (sms / 2)) * std::max(loop, epi) + epi + 5000;
+    else t = std::ceil(units * cl / sms) * (loop + (cl > 1 ? epi / cl + 1500 : epi) + 1500) + 2000;
+    if (g.splits > 1) t += 4000 + static_cast<double>(lanes) * cols * 4 * 2 * g.splits / 3500;
+    if (t < best_t) {
+      best_t = t;
+      best = g;
+    }
+  };
+  for (int splits = 1; splits <= (can_split ? 512 : 1) && splits <= kb; splits += splits < 8 ? 1 : splits / 8) {
+    for (int BN : {256, 128}) consider(true, BN, 1, splits);
+    for (int BN : {128, 64, 32, 16}) {
+      if (c_mn && BN < 64) continue;  // MN-major tiles are panels of 64
+      for (int cl : {1, 2, 4, 8})
+        if (cl == 1 || ceil_div(kb, splits) >= 2 * cl) consider(false, BN, cl, splits);
+    }
+  }
+  const int stage = 128 * 128 + (best.pair ? best.BN / 2 : best.BN) * 128;
+  const int room = static_cast<int>(kMaxDynSmem) - 2048;
+  const long units = static_cast<long>(best.l_tiles) * best.c_tiles * best.splits;
+  if (best.pair) {
+    best.grid = 2 * static_cast<int>(std::min<long>(units, sms / 2));
+    best.stages = std::min(kDenseMaxStages, room / stage);
+  } else {
+    best.grid = static_cast<int>(units) * best.cluster;
+    // more CTAs than SMs: two a SM, so that one's epilogue runs beside the other's loop
+    const int budget = best.grid > sms ? room / 2 - 1024 : room;
+    const int need = static_cast<int>(ceil_div(best.kb_per_split, best.cluster));
+    best.stages = std::max(2, std::min({kDenseMaxStages, budget / stage, need}));
+    if (best.cluster > 1) best.stages = std::max<int>(best.stages, static_cast<int>(ceil_div(best.BN * 512, stage)));
+  }
+  best.smem = static_cast<size_t>(best.stages) * stage + 1024 + 512;  // alignment slack, barriers
+  return best;
+}
+
+// ------------------------------------------------------------------ tensor maps
+// Row-major matrix [rows][cols] of row length ld as a GEMM operand, 128-byte swizzle: K-major, boxes of 128
+// bytes x box_rows; MN-major, boxes of 64 elements x 64 rows.
+bool encode_operand(CUtensorMap* m, const void* base, int type, long rows, long cols, long ld, bool mn, int box_rows) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  const int es = type == CONV2D_E4M3 ? 1 : 2;
+  cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+  cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld) * es};
+  cuuint32_t box[2] = {static_cast<cuuint32_t>(128 / es), static_cast<cuuint32_t>(mn ? 64 : box_rows)};
+  cuuint32_t estr[2] = {1, 1};
+  const CUtensorMapDataType dt = type == CONV2D_E4M3   ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                                 : type == CONV2D_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                       : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  return fn(m, dt, 2, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// An operand ready for the tensor core: type BF16 / FP16 / E4M3, row length a multiple of 16 bytes.
+struct Operand {
+  const void* data;
+  int type;
+  long rows, cols, ld;
+};
+
+// out[m][n] = sum_k C[m][k] L[n][k]; l_mn / c_mn: the operand lies with k along its rows.
+int run_gemm(DenseGemmParams& p, const GemmPlan& g, const Operand& l, bool l_mn, const Operand& c, bool c_mn, int dt,
+             int epi, const char* name, const DevInfo* dev, cudaStream_t st) {
+  if (!encode_operand(&p.tl, l.data, l.type, l.rows, l.cols, l.ld, l_mn, 128) ||
+      !encode_operand(&p.tc, c.data, c.type, c.rows, c.cols, c.ld, c_mn, g.pair ? g.BN / 2 : g.BN))
+    return CONV2D_ERR_CUDA;
+  p.l_mn = l_mn;
+  p.c_mn = c_mn;
+  p.fp8 = l.type == CONV2D_E4M3;
+  p.fmt = l.type == CONV2D_BF16 ? 1u : 0u;
+  p.lanes = static_cast<int>(l_mn ? l.cols : l.rows);
+  p.cols = c_mn ? c.cols : c.rows;
+  p.l_tiles = g.l_tiles;
+  p.c_tiles = g.c_tiles;
+  p.splits = g.splits;
+  p.kb_total = g.kb_total;
+  p.kb_per_split = g.kb_per_split;
+  p.BN = g.BN;
+  p.stages = g.stages;
+  p.cluster = g.cluster;
+  p.err = dev->err;
+  LAUNCH(name, st, g.pair ? launch_dense_pair(p, dt, epi, g.grid, g.smem, st)
+                          : launch_dense_cluster(p, dt, epi, g.grid, g.smem, st));
+  return CONV2D_OK;
+}
+
+// ------------------------------------------------------------------ arguments
+int check_desc(const conv2d_dense_desc* d) {
+  if (!d || d->M < 0 || d->K < 1 || d->N < 1 || d->act < 0 || d->act > CONV2D_ACT_SILU ||
+      (d->dtype != CONV2D_BF16 && d->dtype != CONV2D_FP16))
+    return CONV2D_ERR_INVALID_ARG;
+  // TMA coordinates and tile counts are 32-bit
+  if (d->M > INT_MAX / 2 || d->K > (1 << 28) || d->N > (1 << 28)) return CONV2D_ERR_UNSUPPORTED;
+  return CONV2D_OK;
+}
+// The shape part of a matrix argument: type among the layer's, ld at least cols, known group.
+int check_shape(const conv2d_mat* m, int cols, int dtype, bool q8) {
+  if (!m || (m->ld != 0 && m->ld < cols)) return CONV2D_ERR_INVALID_ARG;
+  if (m->type == CONV2D_E4M3)
+    return q8 && (m->group == 0 || m->group == kQ8Group) ? CONV2D_OK : CONV2D_ERR_INVALID_ARG;
+  return m->type == dtype ? CONV2D_OK : CONV2D_ERR_INVALID_ARG;
+}
+int check_data(const conv2d_mat* m) {
+  return m->data && aligned16(m->data) && (m->type != CONV2D_E4M3 || m->scale) ? CONV2D_OK : CONV2D_ERR_INVALID_ARG;
+}
+
+// Whether x and w run as they are on the 8-bit tensor core path.
+bool both_8bit(const conv2d_mat* x, const conv2d_mat* w) {
+  return x->type == CONV2D_E4M3 && w->type == CONV2D_E4M3 && x->group == 0 && w->group == 0;
+}
+
+// ------------------------------------------------------------------ workspace
+struct Carver {
+  size_t total = 0;
+  size_t take(size_t bytes) {
+    const size_t at = total;
+    total += static_cast<size_t>(round_up(static_cast<long>(bytes), 256));
+    return at;
+  }
+};
+constexpr size_t kNone = ~static_cast<size_t>(0);
+
+// Where an operand has to be copied (decoded, or moved to rows of a multiple of 16 bytes): offset, else kNone.
+size_t plan_copy(Carver& c, const conv2d_mat* m, long rows, int cols, bool as_8bit) {
+  if (as_8bit) return ld_of(m, cols) % 16 == 0 ? kNone : c.take(static_cast<size_t>(rows) * round_up(cols, 16));
+  if (m->type != CONV2D_E4M3 && ld_of(m, cols) % 8 == 0) return kNone;
+  return c.take(static_cast<size_t>(rows) * round_up(cols, 8) * 2);
+}
+// The operand itself, or its copy in the workspace.
+int make_operand(Operand* o, const conv2d_mat* m, long rows, int cols, bool as_8bit, int dt, size_t off, void* ws,
+                 const char* name, cudaStream_t st) {
+  *o = {m->data, as_8bit ? static_cast<int>(CONV2D_E4M3) : dt, rows, cols, ld_of(m, cols)};
+  if (off == kNone) return CONV2D_OK;
+  char* to = static_cast<char*>(ws) + off;
+  o->data = to;
+  o->ld = round_up(cols, as_8bit ? 16 : 8);
+  if (as_8bit) LAUNCH(name, st, launch_move_bytes(m->data, ld_of(m, cols), rows, cols, to, o->ld, st));
+  else LAUNCH(name, st, launch_to_rows(*m, rows, cols, dt, to, o->ld, st));
+  return CONV2D_OK;
+}
+
+struct FwdPlan {
+  bool fp8;
+  size_t x, w, total;
+  GemmPlan g;
+};
+void plan_fwd(const conv2d_dense_desc& d, const conv2d_mat* x, const conv2d_mat* w, int sms, FwdPlan* pl) {
+  Carver c;
+  pl->fp8 = both_8bit(x, w);
+  pl->x = plan_copy(c, x, d.M, d.K, pl->fp8);
+  pl->w = plan_copy(c, w, d.N, d.K, pl->fp8);
+  pl->total = std::max<size_t>(c.total, 256);
+  pl->g = plan_gemm(d.N, d.M, static_cast<int>(ceil_div(d.K, pl->fp8 ? 128 : 64)), false, false, 0, sms);
+}
+
+struct BwdPlan {
+  bool dz_own;  // dz is formed in the workspace (else it is dy)
+  long lddz;
+  size_t dz, x, w, dpart, spart, total;
+  DactPlan dact;
+  GemmPlan gx, gw;
+};
+void plan_bwd(const conv2d_dense_desc& d, const conv2d_mat* x, const conv2d_mat* w, const conv2d_mat* dy, bool dx,
+              const conv2d_mat* dw, bool dbias, int sms, BwdPlan* pl) {
+  Carver c;
+  const bool gemm = dx || dw;
+  pl->lddz = round_up(d.N, 8);
+  pl->dz_own = gemm && (d.act != CONV2D_ACT_IDENTITY || ld_of(dy, d.N) % 8 != 0);
+  pl->dz = pl->dz_own ? c.take(static_cast<size_t>(d.M) * pl->lddz * 2) : kNone;
+  pl->dact = plan_dact(d.M, d.N, sms);
+  pl->dpart = dbias ? c.take(static_cast<size_t>(pl->dact.strips) * d.N * 4) : kNone;
+  pl->w = pl->x = pl->spart = kNone;
+  if (dx) {
+    pl->w = plan_copy(c, w, d.N, d.K, false);
+    pl->gx = plan_gemm(d.K, d.M, static_cast<int>(ceil_div(d.N, 64)), false, false, 0, sms);
+  }
+  if (dw) {
+    pl->x = plan_copy(c, x, d.M, d.K, false);
+    pl->gw = plan_gemm(d.K, d.N, static_cast<int>(ceil_div(d.M, 64)), true, true,
+                       dw->type == CONV2D_FP32 ? kFp32SplitKb : 0, sms);
+    if (pl->gw.splits > 1) pl->spart = c.take(static_cast<size_t>(pl->gw.splits) * d.N * d.K * 4);
+  }
+  pl->total = std::max<size_t>(c.total, 256);
+}
+
+int check_bwd_shapes(const conv2d_dense_desc* d, const conv2d_mat* x, const conv2d_mat* w, const conv2d_mat* z,
+                     const conv2d_mat* dy, const conv2d_mat* dx, const conv2d_mat* dw, const float* dbias) {
+  int rc = check_desc(d);
+  if (rc) return rc;
+  if (!dx && !dw && !dbias) return CONV2D_ERR_INVALID_ARG;
+  if ((rc = check_shape(dy, d->N, d->dtype, false))) return rc;
+  if (d->act != CONV2D_ACT_IDENTITY && (rc = check_shape(z, d->N, d->dtype, true))) return rc;
+  if (dx && ((rc = check_shape(dx, d->K, d->dtype, false)) || (rc = check_shape(w, d->K, d->dtype, true)))) return rc;
+  if (dw) {
+    if ((rc = check_shape(dw, d->K, dw->type == CONV2D_FP32 ? CONV2D_FP32 : d->dtype, false))) return rc;
+    if ((rc = check_shape(x, d->K, d->dtype, true))) return rc;
+  }
+  return CONV2D_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t conv2d_dense_fwd_workspace_size(const conv2d_dense_desc* d, const conv2d_mat* x, const conv2d_mat* w) {
+  if (check_desc(d) || check_shape(x, d->K, d->dtype, true) || check_shape(w, d->K, d->dtype, true)) return 0;
+  FwdPlan pl;
+  plan_fwd(*d, x, w, sms_for_sizing(), &pl);
+  return pl.total;
+}
+
+size_t conv2d_dense_bwd_workspace_size(const conv2d_dense_desc* d, const conv2d_mat* x, const conv2d_mat* w,
+                                       const conv2d_mat* pre_act, const conv2d_mat* dy, const conv2d_mat* dx,
+                                       const conv2d_mat* dw, const float* dbias) {
+  if (check_bwd_shapes(d, x, w, pre_act, dy, dx, dw, dbias)) return 0;
+  BwdPlan pl;
+  plan_bwd(*d, x, w, dy, dx != nullptr, dw, dbias != nullptr, sms_for_sizing(), &pl);
+  return pl.total;
+}
+
+int conv2d_dense_fwd(const conv2d_dense_desc* d, const conv2d_mat* x, const conv2d_mat* w, const float* bias,
+                     const conv2d_mat* residual, const conv2d_mat* pre_act, const conv2d_mat* y, void* ws,
+                     size_t ws_bytes, void* stream) {
+  int rc = check_desc(d);
+  if (rc) return rc;
+  if ((rc = check_shape(x, d->K, d->dtype, true)) || (rc = check_shape(w, d->K, d->dtype, true)) ||
+      (rc = check_shape(y, d->N, d->dtype, false)))
+    return rc;
+  if (residual && (rc = check_shape(residual, d->N, d->dtype, false))) return rc;
+  if (pre_act && ((rc = check_shape(pre_act, d->N, d->dtype, true)) ||
+                  (pre_act->type == CONV2D_E4M3 && pre_act->group != kQ8Group)))
+    return CONV2D_ERR_INVALID_ARG;
+  if (!aligned16(bias)) return CONV2D_ERR_INVALID_ARG;
+  if (d->M == 0) return CONV2D_OK;
+  for (const conv2d_mat* m : {x, w, y, residual, pre_act})
+    if (m && (rc = check_data(m))) return rc;
+  DevInfo* dev = nullptr;
+  if ((rc = device_info(&dev))) return rc;
+  FwdPlan pl;
+  plan_fwd(*d, x, w, dev->sms, &pl);
+  const bool uses_ws = pl.x != kNone || pl.w != kNone;
+  if (uses_ws && (!ws || ws_bytes < pl.total || (reinterpret_cast<uintptr_t>(ws) & 255u))) return CONV2D_ERR_WORKSPACE;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  Operand ox, ow;
+  if ((rc = make_operand(&ox, x, d->M, d->K, pl.fp8, d->dtype, pl.x, ws, "dense_x", st))) return rc;
+  if ((rc = make_operand(&ow, w, d->N, d->K, pl.fp8, d->dtype, pl.w, ws, "dense_w", st))) return rc;
+  DenseGemmParams p = {};
+  if (pl.fp8) {
+    p.ls = w->scale;
+    p.cs = x->scale;
+  }
+  p.bias = bias;
+  p.act = d->act;
+  if (residual) {
+    p.res = residual->data;
+    p.ldr = ld_of(residual, d->N);
+  }
+  if (pre_act) {
+    p.ldz = ld_of(pre_act, d->N);
+    if (pre_act->type == CONV2D_E4M3) {
+      p.zq = static_cast<uint8_t*>(pre_act->data);
+      p.zs = pre_act->scale;
+      p.zg = static_cast<int>(ceil_div(d->N, kQ8Group));
+    } else {
+      p.z = pre_act->data;
+    }
+  }
+  p.out = y->data;
+  p.ldo = ld_of(y, d->N);
+  return run_gemm(p, pl.g, ow, false, ox, false, d->dtype, kDenseForward, "dense_fwd", dev, st);
+}
+
+int conv2d_dense_bwd(const conv2d_dense_desc* d, const conv2d_mat* x, const conv2d_mat* w, const conv2d_mat* pre_act,
+                     const conv2d_mat* dy, const conv2d_mat* dx, const conv2d_mat* dw, float* dbias, void* ws,
+                     size_t ws_bytes, void* stream) {
+  int rc = check_bwd_shapes(d, x, w, pre_act, dy, dx, dw, dbias);
+  if (rc) return rc;
+  if (!aligned16(dbias)) return CONV2D_ERR_INVALID_ARG;
+  if (dw && (rc = check_data(dw))) return rc;
+  DevInfo* dev = nullptr;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (d->M == 0) {  // sums over no rows
+    if (d->accumulate || (!dw && !dbias)) return CONV2D_OK;
+    if ((rc = device_info(&dev))) return rc;
+    if (dw) LAUNCH("zero", st, launch_zero_rows(d->N, d->K, dw->type, dw->data, ld_of(dw, d->K), st));
+    if (dbias) LAUNCH("zero", st, launch_zero_rows(1, d->N, CONV2D_FP32, dbias, d->N, st));
+    return CONV2D_OK;
+  }
+  const bool act = d->act != CONV2D_ACT_IDENTITY;
+  if ((rc = check_data(dy)) || (act && (rc = check_data(pre_act)))) return rc;
+  if (dx && ((rc = check_data(dx)) || (rc = check_data(w)))) return rc;
+  if (dw && (rc = check_data(x))) return rc;
+  if ((rc = device_info(&dev))) return rc;
+  BwdPlan pl;
+  plan_bwd(*d, x, w, dy, dx != nullptr, dw, dbias != nullptr, dev->sms, &pl);
+  if (!ws || ws_bytes < pl.total || (reinterpret_cast<uintptr_t>(ws) & 255u)) return CONV2D_ERR_WORKSPACE;
+  char* base = static_cast<char*>(ws);
+
+  Operand odz = {dy->data, d->dtype, d->M, d->N, ld_of(dy, d->N)};
+  if (pl.dz_own || dbias) {
+    void* dz = pl.dz_own ? base + pl.dz : nullptr;
+    float* part = dbias ? reinterpret_cast<float*>(base + pl.dpart) : nullptr;
+    LAUNCH("dense_dact", st,
+           launch_dact(act ? pre_act : nullptr, *dy, d->M, d->N, d->dtype, d->act, dz, pl.lddz, part, pl.dact, st));
+    if (dbias)
+      LAUNCH("column_sum", st, launch_column_sum(part, pl.dact.strips, d->N, dbias, d->accumulate != 0, st));
+    if (dz) {
+      odz.data = dz;
+      odz.ld = pl.lddz;
+    }
+  }
+  if (dx) {
+    Operand ow;
+    if ((rc = make_operand(&ow, w, d->N, d->K, false, d->dtype, pl.w, ws, "dense_w", st))) return rc;
+    DenseGemmParams p = {};
+    p.out = dx->data;
+    p.ldo = ld_of(dx, d->K);
+    if ((rc = run_gemm(p, pl.gx, ow, true, odz, false, d->dtype, kDenseStore, "dense_dx", dev, st))) return rc;
+  }
+  if (dw) {
+    Operand ox;
+    if ((rc = make_operand(&ox, x, d->M, d->K, false, d->dtype, pl.x, ws, "dense_x", st))) return rc;
+    DenseGemmParams p = {};
+    const bool joined = pl.gw.splits > 1;
+    p.out = joined ? static_cast<void*>(base + pl.spart) : dw->data;
+    p.ldo = joined ? d->K : ld_of(dw, d->K);
+    p.out_f32 = joined || dw->type == CONV2D_FP32;
+    p.accumulate = !joined && d->accumulate;
+    p.split_stride = static_cast<long>(d->N) * d->K;
+    if ((rc = run_gemm(p, pl.gw, ox, true, odz, true, d->dtype, kDenseStore, "dense_dw", dev, st))) return rc;
+    if (joined)
+      LAUNCH("dense_dw_join", st,
+             launch_split_join(reinterpret_cast<float*>(base + pl.spart), pl.gw.splits, d->N, d->K, dw->type, dw->data,
+                               ld_of(dw, d->K), d->accumulate != 0, st));
+  }
+  return CONV2D_OK;
+}
+
+}  // extern "C"

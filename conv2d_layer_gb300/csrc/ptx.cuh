@@ -232,6 +232,13 @@ __device__ __forceinline__ void split_tf32x2(float x0, float x1, uint32_t& h0, u
 }
 
 // ---------------------------------------------------------------- tcgen05
+// TMEM columns to allocate for `cols` columns: a power of two, 32 at least.
+__host__ __device__ inline uint32_t tmem_cols_for(int cols) {
+  uint32_t c = 32;
+  while (c < static_cast<uint32_t>(cols)) c <<= 1;
+  return c;
+}
+
 __device__ __forceinline__ void tmem_alloc(uint32_t* slot, uint32_t ncols) {
   asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(slot)), "r"(ncols)
                : "memory");

@@ -1,0 +1,176 @@
+// q8.cuh - element types of the residual block's kernels: 16-byte vectors,
+// conversions, and the 8-bit format (e4m3 values, one power-of-two scale byte
+// for each group of columns of a row).
+#pragma once
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cstdint>
+#include <type_traits>
+
+namespace c2d {
+
+constexpr int kQ8Group = 32;  // columns that share a scale, when not a whole row
+
+template <typename T>
+__device__ __forceinline__ float to_f(T v) { return static_cast<float>(v); }
+template <typename T>
+__device__ __forceinline__ T from_f(float v);
+template <>
+__device__ __forceinline__ float from_f<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+template <>
+__device__ __forceinline__ __half from_f<__half>(float v) { return __float2half_rn(v); }
+// Decoded values, clamped to T's largest finite one: e4m3 rounding may carry a value close to it up to the
+// next power of two, which T does not hold. NaN passes.
+template <typename T>
+__device__ __forceinline__ T from_q8(float v) {
+  constexpr float top = sizeof(T) == 4 ? 3.402823466e38f : (std::is_same<T, __half>::value ? 65504.f : 3.3895313892515355e38f);
+  return from_f<T>(v > top ? top : (v < -top ? -top : v));
+}
+
+// V consecutive elements as fp32; V * sizeof(T) = 16 bytes (aligned) or V = 1.
+template <typename T, int V>
+struct Vec {
+  T e[V];
+};
+template <typename T, int V>
+__device__ __forceinline__ void ld_vec(const T* p, T (&e)[V]) {
+  if constexpr (V == 1) {
+    e[0] = *p;
+  } else {
+    static_assert(sizeof(T) * V == 16, "16-byte vectors");
+    *reinterpret_cast<uint4*>(e) = *reinterpret_cast<const uint4*>(p);
+  }
+}
+template <typename T, int V>
+__device__ __forceinline__ void st_vec(T* p, const T (&e)[V]) {
+  if constexpr (V == 1) *p = e[0];
+  else *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(e);
+}
+
+// Magnitude bits of a finite value, 0 for infinities and NaN: ordered like the magnitudes.
+__device__ __forceinline__ uint32_t finite_bits(float v) {
+  const uint32_t b = __float_as_uint(v) & 0x7fffffffu;
+  return b < 0x7f800000u ? b : 0u;
+}
+// Scale byte (e + 127) of a group whose largest finite magnitude has these bits: the smallest e in
+// [-126, 127] with amax <= 448 * 2^e, 448 = 1.75 * 2^8; e = 0 for an empty or zero group.
+__device__ __forceinline__ uint32_t q8_scale_byte(uint32_t amax_bits) {
+  if (amax_bits == 0u) return 127u;
+  const int e = static_cast<int>(amax_bits >> 23) - 8 + ((amax_bits & 0x7fffffu) > 0x600000u ? 1 : 0);
+  return static_cast<uint32_t>(e < 1 ? 1 : e);
+}
+__device__ __forceinline__ float q8_scale(uint32_t byte) { return __uint_as_float(byte << 23); }  // 2^(byte - 127)
+__device__ __forceinline__ float q8_inv_scale(uint32_t byte) { return __uint_as_float((254u - byte) << 23); }
+// Two values, already divided by their scale, to e4m3 (a in the low byte). The conversion saturates, so
+// an infinity is turned into NaN first: t * 0 + t.
+__device__ __forceinline__ uint32_t q8_pack2(float a, float b) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(__fmaf_rn(b, 0.f, b)), "f"(__fmaf_rn(a, 0.f, a)));
+  return r;
+}
+// The two e4m3 values of the low 16 bits.
+__device__ __forceinline__ float2 q8_unpack2(uint32_t v) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(v)));
+  return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+// Stores V e4m3 bytes of v[] * inv.
+template <int V>
+__device__ __forceinline__ void q8_store(uint8_t* p, const float (&v)[V], float inv) {
+  if constexpr (V == 1) {
+    *p = static_cast<uint8_t>(q8_pack2(v[0] * inv, 0.f));
+  } else if constexpr (V == 4) {
+    *reinterpret_cast<uint32_t*>(p) = q8_pack2(v[0] * inv, v[1] * inv) | q8_pack2(v[2] * inv, v[3] * inv) << 16;
+  } else {
+    static_assert(V == 8, "V is 1, 4 or 8");
+    uint2 w;
+    w.x = q8_pack2(v[0] * inv, v[1] * inv) | q8_pack2(v[2] * inv, v[3] * inv) << 16;
+    w.y = q8_pack2(v[4] * inv, v[5] * inv) | q8_pack2(v[6] * inv, v[7] * inv) << 16;
+    *reinterpret_cast<uint2*>(p) = w;
+  }
+}
+// Loads V e4m3 bytes as fp32 values times scale.
+template <int V>
+__device__ __forceinline__ void q8_load(const uint8_t* p, float (&v)[V], float scale) {
+  if constexpr (V == 1) {
+    v[0] = q8_unpack2(*p).x * scale;
+  } else {
+    uint32_t w[V / 4];
+    if constexpr (V == 4) w[0] = *reinterpret_cast<const uint32_t*>(p);
+    else {
+      static_assert(V == 8, "V is 1, 4 or 8");
+      *reinterpret_cast<uint2*>(w) = *reinterpret_cast<const uint2*>(p);
+    }
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) {
+      const float2 f = q8_unpack2(w[i / 2] >> (16 * (i & 1)));
+      v[2 * i] = f.x * scale;
+      v[2 * i + 1] = f.y * scale;
+    }
+  }
+}
+
+// ---------------------------------------------------------------- activations of the dense layer
+// In fp32 to about 1e-6 relative (1e-5 where |z| is in the tens and the result tiny), in the forms that lose
+// nothing near zero or in the tails: the outputs are rounded to 16 bits, but the bias gradient sums the
+// derivatives in fp32.
+__device__ __forceinline__ float sigmoid_f(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
+
+template <int A>
+__device__ __forceinline__ float dense_act(float z) {
+  if constexpr (A == 1) return z > 0.f ? z : (z <= 0.f ? 0.f : z);  // NaN passes
+  else if constexpr (A == 2) {
+    // tanh z = z (1 - z^2/3 + 2 z^4/15 - 17 z^6/315) below 1/4 (the next term is under 4e-7 of z), else
+    // (1 - e) / (1 + e) with e = exp(-2|z|) and z's sign
+    const float a = fabsf(z), s = z * z;
+    if (a < 0.25f) return z * (1.f + s * (-1.f / 3.f + s * (2.f / 15.f - s * (17.f / 315.f))));
+    const float e = __expf(-2.f * a);
+    return copysignf(__fdividef(1.f - e, 1.f + e), z);
+  } else if constexpr (A == 3) return sigmoid_f(z);
+  else if constexpr (A == 4) {
+    // z/2 (1 + tanh u) = z / (1 + exp(-2u)); past |z| = 16 the factor is 0 or 1 to fp32 (clamped, so that
+    // u does not overflow)
+    const float c = z > 16.f ? 16.f : (z < -16.f ? -16.f : z);
+    return z * sigmoid_f(1.5957691216f * c * (1.f + 0.044715f * c * c));
+  } else if constexpr (A == 5) return z * sigmoid_f(z);
+  else return z;
+}
+template <int A>
+__device__ __forceinline__ float dense_dact(float z) {
+  if constexpr (A == 1) return z > 0.f ? 1.f : (z <= 0.f ? 0.f : z);
+  else if constexpr (A == 2) {  // 1 - tanh^2 = 4 e / (1 + e)^2
+    const float e = __expf(-2.f * fabsf(z));
+    return __fdividef(4.f * e, (1.f + e) * (1.f + e));
+  } else if constexpr (A == 3) {  // s (1 - s) = e / (1 + e)^2, e = exp(-|z|)
+    const float e = __expf(-fabsf(z));
+    return __fdividef(e, (1.f + e) * (1.f + e));
+  } else if constexpr (A == 4) {
+    const float c = z > 16.f ? 16.f : (z < -16.f ? -16.f : z);
+    const float q = c * c;
+    const float s = sigmoid_f(1.5957691216f * c * (1.f + 0.044715f * q));
+    return s + c * s * (1.f - s) * (1.5957691216f * (1.f + 0.134145f * q));
+  } else if constexpr (A == 5) {
+    const float c = z > 88.f ? 88.f : (z < -88.f ? -88.f : z);
+    const float s = sigmoid_f(c);
+    return s * (1.f + c * (1.f - s));
+  } else return 1.f;
+}
+template <int A>
+struct DAct {
+  static constexpr int value = A;
+};
+template <typename F>
+__device__ __forceinline__ void with_dense_act(int act, F&& f) {
+  switch (act) {
+    case 1: f(DAct<1>{}); break;
+    case 2: f(DAct<2>{}); break;
+    case 3: f(DAct<3>{}); break;
+    case 4: f(DAct<4>{}); break;
+    case 5: f(DAct<5>{}); break;
+    default: f(DAct<0>{}); break;
+  }
+}
+
+}  // namespace c2d

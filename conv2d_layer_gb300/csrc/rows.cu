@@ -1,0 +1,919 @@
+// rows.cu - kernels over rows of features: RMS norm with the residual's
+// addition and its backward, 8-bit checkpoints (encode, decode), the backward
+// through a dense layer's activation, and the column sums and joins behind
+// them. All are bound by memory: each reads its inputs once and writes its
+// outputs once, in 16-byte accesses where the rows allow it (row starts on
+// 16-byte boundaries; V = 1 otherwise).
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <climits>
+#include <cmath>
+
+#include "host.h"
+#include "kernels.h"
+#include "q8.cuh"
+#include "rows.h"
+
+namespace c2d {
+namespace {
+
+constexpr long kMaxGridX = 0x7fffffffL;
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// Sum (or maximum of magnitude bits) over the TPR threads of a row; red: one word per warp. Every thread
+// of the row gets the result, formed in the same order by all.
+template <int TPR>
+__device__ __forceinline__ float row_sum(float v, float* red) {
+  v = warp_sum(v);
+  if constexpr (TPR > 32) {
+    const int warp = threadIdx.x >> 5;
+    __syncthreads();  // the last use of red is over
+    if ((threadIdx.x & 31) == 0) red[warp] = v;
+    __syncthreads();
+    v = 0.f;
+#pragma unroll
+    for (int i = 0; i < TPR / 32; ++i) v += red[i];
+  }
+  return v;
+}
+template <int TPR>
+__device__ __forceinline__ uint32_t row_max(uint32_t v, uint32_t* red) {
+  v = __reduce_max_sync(0xffffffffu, v);
+  if constexpr (TPR > 32) {
+    const int warp = threadIdx.x >> 5;
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) red[warp] = v;
+    __syncthreads();
+    v = 0u;
+#pragma unroll
+    for (int i = 0; i < TPR / 32; ++i) v = max(v, red[i]);
+  }
+  return v;
+}
+
+struct NormArgs {
+  const void *x, *r;
+  const float* gamma;
+  void *h, *y;
+  uint8_t *q, *qs;
+  float* inv;
+  long ldx, ldr, ldh, ldy, ldq;
+  long rows;
+  int cols, ng;  // ng: scale bytes a row
+  int group;     // 32 or 0 (whole row)
+  float eps;
+};
+
+// RMS norm forward (NORM) or 8-bit encode (!NORM) of one row by TPR threads; blocks of max(TPR, 256)
+// threads. The row is held in registers between its sum of squares and its output, U vectors a thread, so
+// memory is passed once; U = 0 is the form for rows longer than that, which reads the row again for each
+// phase (from L2, mostly). Threads hold neighbouring vectors, so a group of 32 columns lies in 32 / V
+// neighbouring lanes and its maximum is found by shuffles.
+template <typename T, int V, int TPR, int U, bool NORM>
+__global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) rows_fwd_kernel(const NormArgs a) {
+  pdl_entry();
+  constexpr int RPB = TPR < 256 ? 256 / TPR : 1;  // rows per block
+  static_assert(RPB == 1 || TPR == 32, "rows that share a block are one warp each");
+  constexpr int UC = U > 0 ? U : 1;
+  __shared__ float red[32];
+  const int t = RPB > 1 ? static_cast<int>(threadIdx.x) & 31 : static_cast<int>(threadIdx.x);
+  const long row = RPB > 1 ? static_cast<long>(blockIdx.x) * RPB + (threadIdx.x >> 5) : static_cast<long>(blockIdx.x);
+  if (row >= a.rows) return;  // whole warps; rows that use block barriers are whole blocks
+  const T* x = static_cast<const T*>(a.x) + row * a.ldx;
+  const T* r = a.r ? static_cast<const T*>(a.r) + row * a.ldr : nullptr;
+  T* h = a.h ? static_cast<T*>(a.h) + row * a.ldh : nullptr;
+  const int nv = (a.cols + V - 1) / V;
+  const int nu = U > 0 ? U : (nv + TPR - 1) / TPR;  // vectors a thread
+
+  float v[UC][V];
+  auto load = [&](int u, float (&o)[V]) {  // x + r as stored; zeros past the end
+    const int i = u * TPR + t;
+    if (i < nv) {
+      T e[V];
+      ld_vec<T, V>(x + static_cast<long>(i) * V, e);
+      if (r) {
+        T f[V];
+        ld_vec<T, V>(r + static_cast<long>(i) * V, f);
+#pragma unroll
+        for (int k = 0; k < V; ++k) e[k] = from_f<T>(to_f(e[k]) + to_f(f[k]));
+        st_vec<T, V>(h + static_cast<long>(i) * V, e);
+      }
+#pragma unroll
+      for (int k = 0; k < V; ++k) o[k] = to_f(e[k]);
+    } else {
+#pragma unroll
+      for (int k = 0; k < V; ++k) o[k] = 0.f;
+    }
+  };
+  auto reload = [&](int u, float (&o)[V]) {  // U = 0: this thread's own h (or x) again
+    const int i = u * TPR + t;
+    if (i < nv) {
+      T e[V];
+      ld_vec<T, V>((r ? static_cast<const T*>(h) : x) + static_cast<long>(i) * V, e);
+#pragma unroll
+      for (int k = 0; k < V; ++k) o[k] = to_f(e[k]);
+    } else {
+#pragma unroll
+      for (int k = 0; k < V; ++k) o[k] = 0.f;
+    }
+  };
+
+  float inv = 1.f;
+  if constexpr (NORM) {
+    float ss = 0.f;
+    if constexpr (U > 0) {
+#pragma unroll
+      for (int u = 0; u < UC; ++u) load(u, v[u]);
+#pragma unroll
+      for (int u = 0; u < UC; ++u)
+#pragma unroll
+        for (int k = 0; k < V; ++k) ss = fmaf(v[u][k], v[u][k], ss);
+    } else {
+      for (int u = 0; u < nu; ++u) {
+        load(u, v[0]);
+#pragma unroll
+        for (int k = 0; k < V; ++k) ss = fmaf(v[0][k], v[0][k], ss);
+      }
+    }
+    ss = row_sum<TPR>(ss, red);
+    inv = 1.f / sqrtf(ss / static_cast<float>(a.cols) + a.eps);
+    if (t == 0 && a.inv) a.inv[row] = inv;
+  } else if constexpr (U > 0) {
+#pragma unroll
+    for (int u = 0; u < UC; ++u) load(u, v[u]);
+  }
+  // y = gamma h s of vector u, in place
+  auto scale = [&](int u, float (&o)[V]) {
+    const int i = u * TPR + t;
+    if (!NORM || i >= nv) return;
+    const float* g = a.gamma + static_cast<long>(i) * V;
+    if constexpr (V >= 4) {
+#pragma unroll
+      for (int k = 0; k < V; k += 4) {
+        const float4 gv = *reinterpret_cast<const float4*>(g + k);
+        o[k] = o[k] * inv * gv.x;
+        o[k + 1] = o[k + 1] * inv * gv.y;
+        o[k + 2] = o[k + 2] * inv * gv.z;
+        o[k + 3] = o[k + 3] * inv * gv.w;
+      }
+    } else {
+      o[0] = o[0] * inv * g[0];
+    }
+  };
+  auto absmax = [&](const float (&o)[V]) {
+    uint32_t m = 0u;
+#pragma unroll
+    for (int k = 0; k < V; ++k) m = max(m, finite_bits(o[k]));
+    return m;
+  };
+  uint32_t rowbyte = 0u;
+  if (a.q && a.group == 0) {
+    uint32_t m = 0u;
+    if constexpr (U > 0) {
+#pragma unroll
+      for (int u = 0; u < UC; ++u) {
+        scale(u, v[u]);
+        m = max(m, absmax(v[u]));
+      }
+    } else {
+      for (int u = 0; u < nu; ++u) {
+        reload(u, v[0]);
+        scale(u, v[0]);
+        m = max(m, absmax(v[0]));
+      }
+    }
+    rowbyte = q8_scale_byte(row_max<TPR>(m, reinterpret_cast<uint32_t*>(red)));
+    if (t == 0) a.qs[row * a.ng] = static_cast<uint8_t>(rowbyte);
+  }
+  T* y = a.y ? static_cast<T*>(a.y) + row * a.ldy : nullptr;
+  uint8_t* q = a.q ? a.q + row * a.ldq : nullptr;
+  auto finish = [&](int u, float (&o)[V]) {
+    const int i = u * TPR + t;
+    if (y && i < nv) {
+      T e[V];
+#pragma unroll
+      for (int k = 0; k < V; ++k) e[k] = from_f<T>(o[k]);
+      st_vec<T, V>(y + static_cast<long>(i) * V, e);
+    }
+    if (q) {
+      uint32_t byte = rowbyte;
+      if (a.group != 0) {
+        uint32_t m = absmax(o);
+#pragma unroll
+        for (int s = 1; s < kQ8Group / V; s <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, s));
+        byte = q8_scale_byte(m);
+        if (i < nv && (t & (kQ8Group / V - 1)) == 0) a.qs[row * a.ng + i / (kQ8Group / V)] = static_cast<uint8_t>(byte);
+      }
+      if (i < nv) q8_store<V>(q + static_cast<long>(i) * V, o, q8_inv_scale(byte));
+    }
+  };
+  if constexpr (U > 0) {
+#pragma unroll
+    for (int u = 0; u < UC; ++u) {
+      if (!(a.q && a.group == 0)) scale(u, v[u]);
+      finish(u, v[u]);
+    }
+  } else {
+    for (int u = 0; u < nu; ++u) {
+      reload(u, v[0]);
+      scale(u, v[0]);
+      finish(u, v[0]);
+    }
+  }
+}
+
+template <typename T, int V, bool NORM>
+cudaError_t rows_fwd(const NormArgs& a, cudaStream_t st) {
+  const int nv = (a.cols + V - 1) / V;
+#define ROWS_FWD(TPR, U)                                                                       \
+  do {                                                                                         \
+    constexpr int nt = TPR < 256 ? 256 : TPR, rpb = nt / TPR;                                  \
+    return launch_k(rows_fwd_kernel<T, V, TPR, U, NORM>, dim3(static_cast<unsigned>((a.rows + rpb - 1) / rpb)), \
+                    dim3(nt), 0, st, 1, a);                                                    \
+  } while (0)
+  if (nv <= 32) ROWS_FWD(32, 1);
+  if (nv <= 64) ROWS_FWD(32, 2);
+  if (nv <= 128) ROWS_FWD(32, 4);
+  if (nv <= 256) ROWS_FWD(256, 1);
+  if (nv <= 512) ROWS_FWD(256, 2);
+  if (nv <= 1024) ROWS_FWD(256, 4);
+  if (nv <= 2048) ROWS_FWD(512, 4);
+  ROWS_FWD(1024, 0);
+#undef ROWS_FWD
+}
+
+// ------------------------------------------------------------------ RMS norm backward
+struct NormBwdArgs {
+  const void *h, *dy, *dh;
+  void* dx;
+  const float *gamma, *inv;
+  float* part;  // [gridDim.x][cols], null: no dgamma
+  long ldh, lddy, lddh, lddx;
+  long rows;
+  int cols;
+};
+
+// Blocks walk the rows (row = block, block + grid, ...), TPR threads a row, and keep gamma and the sums of
+// dgamma for their columns in registers. The vectors of the next row are in flight while this one is
+// reduced. U = 0: rows longer than the registers hold; each row is read twice and dgamma's sums live in
+// this block's row of `part`.
+template <typename T, int V, int TPR, int U>
+__global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) norm_bwd_kernel(const NormBwdArgs a) {
+  pdl_entry();
+  constexpr int RPB = TPR < 256 ? 256 / TPR : 1;
+  constexpr int UC = U > 0 ? U : 1;
+  extern __shared__ float sums[];  // RPB > 1 with dgamma: [RPB][cols]
+  __shared__ float red[32];
+  const int t = RPB > 1 ? static_cast<int>(threadIdx.x) & 31 : static_cast<int>(threadIdx.x);
+  const int wr = RPB > 1 ? static_cast<int>(threadIdx.x >> 5) : 0;
+  const int nv = (a.cols + V - 1) / V;
+  const float invD = 1.f / static_cast<float>(a.cols);
+  const T* hb = static_cast<const T*>(a.h);
+  const T* db = static_cast<const T*>(a.dy);
+  const T* sb = static_cast<const T*>(a.dh);
+  T* xb = static_cast<T*>(a.dx);
+  const long step = static_cast<long>(gridDim.x) * RPB;
+  const long row0 = static_cast<long>(blockIdx.x) * RPB + wr;
+
+  if constexpr (U > 0) {
+    float g[UC][V], acc[UC][V];
+#pragma unroll
+    for (int u = 0; u < UC; ++u)
+#pragma unroll
+      for (int k = 0; k < V; ++k) {
+        const int c = (u * TPR + t) * V + k;
+        g[u][k] = c < a.cols ? a.gamma[c] : 0.f;
+        acc[u][k] = 0.f;
+      }
+    T h[UC][V], d[UC][V], s[UC][V];
+    float inv = 0.f;
+    auto fetch = [&](long row) {
+      if (row < a.rows) inv = a.inv[row];
+#pragma unroll
+      for (int u = 0; u < UC; ++u) {
+        const int i = u * TPR + t;
+        if (row < a.rows && i < nv) {
+          ld_vec<T, V>(hb + row * a.ldh + static_cast<long>(i) * V, h[u]);
+          ld_vec<T, V>(db + row * a.lddy + static_cast<long>(i) * V, d[u]);
+          if (sb && xb) ld_vec<T, V>(sb + row * a.lddh + static_cast<long>(i) * V, s[u]);
+        } else {
+#pragma unroll
+          for (int k = 0; k < V; ++k) h[u][k] = d[u][k] = from_f<T>(0.f);
+        }
+      }
+    };
+    fetch(row0);
+    for (long row = row0; row < a.rows; row += step) {
+      float hf[UC][V], df[UC][V];
+      T sk[UC][V];
+      const float iv = inv;
+      float dot = 0.f;
+#pragma unroll
+      for (int u = 0; u < UC; ++u)
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+          hf[u][k] = to_f(h[u][k]) * iv;  // the normalised value
+          df[u][k] = to_f(d[u][k]);
+          sk[u][k] = s[u][k];
+          acc[u][k] = fmaf(df[u][k], hf[u][k], acc[u][k]);
+          df[u][k] *= g[u][k];
+          dot = fmaf(df[u][k], hf[u][k], dot);
+        }
+      fetch(row + step);
+      if (xb) {
+        dot = row_sum<TPR>(dot, red) * invD;
+#pragma unroll
+        for (int u = 0; u < UC; ++u) {
+          const int i = u * TPR + t;
+          if (i < nv) {
+            T o[V];
+#pragma unroll
+            for (int k = 0; k < V; ++k) {
+              float v = iv * fmaf(-hf[u][k], dot, df[u][k]);
+              if (sb) v += to_f(sk[u][k]);
+              o[k] = from_f<T>(v);
+            }
+            st_vec<T, V>(xb + row * a.lddx + static_cast<long>(i) * V, o);
+          }
+        }
+      }
+    }
+    if (!a.part) return;
+    float* part = a.part + static_cast<long>(blockIdx.x) * a.cols;
+    if constexpr (RPB > 1) {
+#pragma unroll
+      for (int u = 0; u < UC; ++u)
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+          const int c = (u * TPR + t) * V + k;
+          if (c < a.cols) sums[wr * a.cols + c] = acc[u][k];
+        }
+      __syncthreads();
+      for (int c = threadIdx.x; c < a.cols; c += 256) {
+        float v = 0.f;
+#pragma unroll
+        for (int w = 0; w < RPB; ++w) v += sums[w * a.cols + c];
+        part[c] = v;
+      }
+    } else {
+#pragma unroll
+      for (int u = 0; u < UC; ++u)
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+          const int c = (u * TPR + t) * V + k;
+          if (c < a.cols) part[c] = acc[u][k];
+        }
+    }
+  } else {
+    float* part = a.part ? a.part + static_cast<long>(blockIdx.x) * a.cols : nullptr;
+    if (part)
+      for (int i = t; i < nv; i += TPR)
+        for (int k = 0; k < V; ++k) part[static_cast<long>(i) * V + k] = 0.f;
+    for (long row = row0; row < a.rows; row += step) {
+      const float iv = a.inv[row];
+      float dot = 0.f;
+      for (int i = t; i < nv; i += TPR) {
+        T h[V], d[V];
+        ld_vec<T, V>(hb + row * a.ldh + static_cast<long>(i) * V, h);
+        ld_vec<T, V>(db + row * a.lddy + static_cast<long>(i) * V, d);
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+          const long c = static_cast<long>(i) * V + k;
+          const float hn = to_f(h[k]) * iv, dv = to_f(d[k]);
+          if (part) part[c] = fmaf(dv, hn, part[c]);
+          dot = fmaf(dv * a.gamma[c], hn, dot);
+        }
+      }
+      if (!xb) continue;
+      dot = row_sum<TPR>(dot, red) * invD;
+      for (int i = t; i < nv; i += TPR) {
+        T h[V], d[V], s[V], o[V];
+        ld_vec<T, V>(hb + row * a.ldh + static_cast<long>(i) * V, h);
+        ld_vec<T, V>(db + row * a.lddy + static_cast<long>(i) * V, d);
+        if (sb) ld_vec<T, V>(sb + row * a.lddh + static_cast<long>(i) * V, s);
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+          const long c = static_cast<long>(i) * V + k;
+          float v = iv * fmaf(-to_f(h[k]) * iv, dot, to_f(d[k]) * a.gamma[c]);
+          if (sb) v += to_f(s[k]);
+          o[k] = from_f<T>(v);
+        }
+        st_vec<T, V>(xb + row * a.lddx + static_cast<long>(i) * V, o);
+      }
+    }
+  }
+}
+
+// Blocks of the backward walk: two of 256 threads an SM fit their registers; fewer where the rows are few.
+int norm_bwd_grid(long rows, int sms) { return static_cast<int>(std::max<long>(1, std::min<long>(rows, 2L * sms))); }
+
+template <typename T, int V>
+cudaError_t norm_bwd(const NormBwdArgs& a, int grid, cudaStream_t st) {
+  const int nv = (a.cols + V - 1) / V;
+#define NORM_BWD(TPR, U)                                                                         \
+  do {                                                                                           \
+    constexpr int nt = TPR < 256 ? 256 : TPR;                                                    \
+    const size_t smem = nt > TPR && a.part ? static_cast<size_t>(nt / TPR) * a.cols * 4 : 0;     \
+    return launch_k(norm_bwd_kernel<T, V, TPR, U>, dim3(grid), dim3(nt), smem, st, 1, a);        \
+  } while (0)
+  if (nv <= 32) NORM_BWD(32, 1);
+  if (nv <= 64) NORM_BWD(32, 2);
+  if (nv <= 256) NORM_BWD(256, 1);
+  if (nv <= 512) NORM_BWD(256, 2);
+  if (nv <= 1024) NORM_BWD(512, 2);
+  if (nv <= 2048) NORM_BWD(1024, 2);
+  NORM_BWD(1024, 0);
+#undef NORM_BWD
+}
+
+// ------------------------------------------------------------------ decode / move
+// One vector of V elements a thread of a [rows][cols] matrix (E4M3 source: V bytes and their scale).
+template <typename T, int V, bool Q>
+__global__ void __launch_bounds__(256) to_rows_kernel(const void* x, long ldx, const uint8_t* scale, int group, int ng,
+                                                      long rows, int cols, T* out, long ldo) {
+  pdl_entry();
+  const int nv = (cols + V - 1) / V;
+  const long total = rows * nv;
+  for (long j = static_cast<long>(blockIdx.x) * 256 + threadIdx.x; j < total; j += static_cast<long>(gridDim.x) * 256) {
+    const long row = j / nv;
+    const int c = static_cast<int>(j - row * nv) * V;
+    T o[V];
+    if constexpr (Q) {
+      float v[V];
+      q8_load<V>(static_cast<const uint8_t*>(x) + row * ldx + c, v,
+                 q8_scale(scale[row * ng + (group ? c / kQ8Group : 0)]));
+#pragma unroll
+      for (int k = 0; k < V; ++k) o[k] = from_q8<T>(v[k]);
+    } else {
+      ld_vec<T, V>(static_cast<const T*>(x) + row * ldx + c, o);
+    }
+    st_vec<T, V>(out + row * ldo + c, o);
+  }
+}
+
+__global__ void __launch_bounds__(256) move_bytes_kernel(const uint8_t* x, long ldx, long rows, int cols, uint8_t* out,
+                                                         long ldo) {
+  pdl_entry();
+  const long total = rows * cols;
+  for (long j = static_cast<long>(blockIdx.x) * 256 + threadIdx.x; j < total; j += static_cast<long>(gridDim.x) * 256) {
+    const long row = j / cols;
+    const int c = static_cast<int>(j - row * cols);
+    out[row * ldo + c] = x[row * ldx + c];
+  }
+}
+
+int stream_grid(long items) { return static_cast<int>(std::max<long>(1, std::min<long>((items + 255) / 256, 152L * 64))); }
+
+bool vec_ok(const void* p, long ld, int es, int V) {
+  return reinterpret_cast<uintptr_t>(p) % 16 == 0 && (ld * es) % (static_cast<long>(V) * es) == 0;
+}
+
+template <typename T>
+cudaError_t to_rows(const conv2d_mat& x, long rows, int cols, void* out, long ldo, cudaStream_t st) {
+  constexpr int VV = 16 / sizeof(T);
+  const bool q = x.type == CONV2D_E4M3;
+  const long ldx = x.ld ? x.ld : cols, ld = ldo ? ldo : cols;
+  const int ng = x.group ? (cols + kQ8Group - 1) / kQ8Group : 1;
+  // whole vectors only: cols a multiple of the vector, and both rows' starts aligned to theirs
+  const bool vec = cols % VV == 0 && vec_ok(out, ld, sizeof(T), VV) && vec_ok(x.data, ldx, q ? 1 : sizeof(T), VV);
+  const long items = rows * (vec ? cols / VV : cols);
+  T* o = static_cast<T*>(out);
+#define TO_ROWS(V, Q)                                                                                              \
+  return launch_k(to_rows_kernel<T, V, Q>, dim3(stream_grid(items)), dim3(256), 0, st, 1,                         \
+                  static_cast<const void*>(x.data), ldx, static_cast<const uint8_t*>(x.scale), x.group, ng, rows, \
+                  cols, o, ld)
+  if (vec && q) TO_ROWS(VV, true);
+  if (vec) TO_ROWS(VV, false);
+  if (q) TO_ROWS(1, true);
+  TO_ROWS(1, false);
+#undef TO_ROWS
+}
+
+// ------------------------------------------------------------------ backward through the activation
+struct DactArgs {
+  const void *dy, *z;
+  const uint8_t* zs;
+  void* dz;
+  float* part;
+  long lddy, ldz, lddz;
+  long rows, rows_per_strip;
+  int cols, group, ng, act;
+};
+
+// A block is 32 lanes of V columns by 8 rows; it walks the rows of its strip and keeps the column sums of
+// the unrounded dz in registers, joined over the 8 row lanes at the end. ZK: 0 no activation, 1 z in T,
+// 2 z as E4M3.
+template <typename T, int V, int ZK>
+__global__ void __launch_bounds__(256) dact_kernel(const DactArgs a) {
+  pdl_entry();
+  __shared__ float sums[8][32 * V];
+  const int lane = threadIdx.x & 31, rl = threadIdx.x >> 5;
+  const int c = (static_cast<int>(blockIdx.x) * 32 + lane) * V;
+  const long r1 = min(a.rows, (static_cast<long>(blockIdx.y) + 1) * a.rows_per_strip);
+  float acc[V];
+#pragma unroll
+  for (int k = 0; k < V; ++k) acc[k] = 0.f;
+  if (c < a.cols) {
+    const T* dy = static_cast<const T*>(a.dy) + c;
+    T* dz = a.dz ? static_cast<T*>(a.dz) + c : nullptr;
+    with_dense_act(ZK ? a.act : 0, [&](auto act) {
+#pragma unroll 4
+      for (long r = blockIdx.y * a.rows_per_strip + rl; r < r1; r += 8) {
+        T d[V];
+        ld_vec<T, V>(dy + r * a.lddy, d);
+        [[maybe_unused]] float f[V];
+        if constexpr (ZK == 1) {
+          T e[V];
+          ld_vec<T, V>(static_cast<const T*>(a.z) + c + r * a.ldz, e);
+#pragma unroll
+          for (int k = 0; k < V; ++k) f[k] = to_f(e[k]);
+        } else if constexpr (ZK == 2) {
+          q8_load<V>(static_cast<const uint8_t*>(a.z) + c + r * a.ldz, f,
+                     q8_scale(a.zs[r * a.ng + (a.group ? c / kQ8Group : 0)]));
+        }
+        T o[V];
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+          float v = to_f(d[k]);
+          if constexpr (ZK) v *= dense_dact<decltype(act)::value>(f[k]);
+          acc[k] += v;
+          o[k] = from_f<T>(v);
+        }
+        if (dz) st_vec<T, V>(dz + r * a.lddz, o);
+      }
+    });
+  }
+  if (!a.part) return;
+#pragma unroll
+  for (int k = 0; k < V; ++k) sums[rl][lane * V + k] = acc[k];
+  __syncthreads();
+  for (int i = threadIdx.x; i < 32 * V; i += 256) {
+    const int col = static_cast<int>(blockIdx.x) * 32 * V + i;
+    if (col >= a.cols) continue;
+    float v = 0.f;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) v += sums[w][i];
+    a.part[static_cast<long>(blockIdx.y) * a.cols + col] = v;
+  }
+}
+
+template <typename T>
+cudaError_t dact(const DactArgs& a, int zk, int strips, cudaStream_t st) {
+  constexpr int VV = 16 / sizeof(T);
+  const bool vec = a.cols % VV == 0 && vec_ok(a.dy, a.lddy, sizeof(T), VV) &&
+                   (!a.dz || vec_ok(a.dz, a.lddz, sizeof(T), VV)) &&
+                   (zk == 0 || vec_ok(a.z, a.ldz, zk == 2 ? 1 : sizeof(T), VV));
+  const int V = vec ? VV : 1;
+  const dim3 grid(static_cast<unsigned>((a.cols + 32 * V - 1) / (32 * V)), static_cast<unsigned>(strips));
+#define DACT(V, ZK) return launch_k(dact_kernel<T, V, ZK>, grid, dim3(256), 0, st, 1, a)
+  if (vec) {
+    if (zk == 0) DACT(VV, 0);
+    if (zk == 1) DACT(VV, 1);
+    DACT(VV, 2);
+  }
+  if (zk == 0) DACT(1, 0);
+  if (zk == 1) DACT(1, 1);
+  DACT(1, 2);
+#undef DACT
+}
+
+// ------------------------------------------------------------------ column sums, joins, zeroes
+// 32 columns a block, 8 warps over the partials, then the 8 sums in order.
+__global__ void __launch_bounds__(256) column_sum_kernel(const float* part, int G, int cols, float* out,
+                                                         int accumulate) {
+  pdl_entry();
+  __shared__ float s[8][33];
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const int c = static_cast<int>(blockIdx.x) * 32 + lane;
+  float v = 0.f;
+  if (c < cols) {
+#pragma unroll 8
+    for (int g = w; g < G; g += 8) v += part[static_cast<long>(g) * cols + c];
+  }
+  s[w][lane] = v;
+  __syncthreads();
+  if (w == 0 && c < cols) {
+    float o = accumulate ? out[c] : 0.f;
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sum += s[i][lane];
+    out[c] = o + sum;
+  }
+}
+
+template <typename T, int V>
+__global__ void __launch_bounds__(256) split_join_kernel(const float* part, int splits, long rows, int cols, T* out,
+                                                         long ldo, int accumulate) {
+  pdl_entry();
+  const int nv = cols / V;
+  const long total = rows * nv, plane = rows * cols;
+  for (long j = static_cast<long>(blockIdx.x) * 256 + threadIdx.x; j < total; j += static_cast<long>(gridDim.x) * 256) {
+    const long row = j / nv;
+    const int c = static_cast<int>(j - row * nv) * V;
+    const float* p = part + row * cols + c;
+    float v[V];
+#pragma unroll
+    for (int k = 0; k < V; ++k) v[k] = 0.f;
+#pragma unroll 4
+    for (int s = 0; s < splits; ++s) {
+      float e[V];
+      if constexpr (V == 4) *reinterpret_cast<float4*>(e) = *reinterpret_cast<const float4*>(p + s * plane);
+      else e[0] = p[s * plane];
+#pragma unroll
+      for (int k = 0; k < V; ++k) v[k] += e[k];
+    }
+    T* o = out + row * ldo + c;
+#pragma unroll
+    for (int k = 0; k < V; ++k) o[k] = from_f<T>(accumulate ? to_f(o[k]) + v[k] : v[k]);
+  }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(256) zero_rows_kernel(long rows, int cols, T* out, long ld) {
+  pdl_entry();
+  const long total = rows * cols;
+  for (long j = static_cast<long>(blockIdx.x) * 256 + threadIdx.x; j < total; j += static_cast<long>(gridDim.x) * 256) {
+    const long row = j / cols;
+    out[row * ld + (j - row * cols)] = from_f<T>(0.f);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_to_rows(const conv2d_mat& x, long rows, int cols, int dt, void* out, long ldo, cudaStream_t st) {
+  if (dt == CONV2D_BF16) return to_rows<__nv_bfloat16>(x, rows, cols, out, ldo, st);
+  if (dt == CONV2D_FP16) return to_rows<__half>(x, rows, cols, out, ldo, st);
+  return to_rows<float>(x, rows, cols, out, ldo, st);
+}
+
+cudaError_t launch_move_bytes(const void* x, long ldx, long rows, int cols, void* out, long ldo, cudaStream_t st) {
+  return launch_k(move_bytes_kernel, dim3(stream_grid(rows * cols)), dim3(256), 0, st, 1,
+                  static_cast<const uint8_t*>(x), ldx, rows, cols, static_cast<uint8_t*>(out), ldo);
+}
+
+DactPlan plan_dact(long rows, int cols, int sms) {
+  // about eight blocks an SM, of 64 rows at least (eight passes, so that the joining at the end is small)
+  const long chunks = (cols + 255) / 256;
+  long strips = std::max<long>(1, 8L * sms / chunks);
+  strips = std::min(strips, (rows + 63) / 64);
+  strips = std::max<long>(1, std::min<long>(strips, 65535));
+  DactPlan p;
+  p.rows_per_strip = (rows + strips - 1) / strips;
+  p.strips = static_cast<int>((rows + p.rows_per_strip - 1) / p.rows_per_strip);
+  return p;
+}
+
+cudaError_t launch_dact(const conv2d_mat* z, const conv2d_mat& dy, long rows, int cols, int dt, int act, void* dz,
+                        long lddz, float* part, const DactPlan& pl, cudaStream_t st) {
+  DactArgs a = {};
+  a.dy = dy.data;
+  a.lddy = dy.ld ? dy.ld : cols;
+  int zk = 0;
+  if (z) {
+    zk = z->type == CONV2D_E4M3 ? 2 : 1;
+    a.z = z->data;
+    a.zs = z->scale;
+    a.ldz = z->ld ? z->ld : cols;
+    a.group = z->group;
+    a.ng = z->group ? (cols + kQ8Group - 1) / kQ8Group : 1;
+  }
+  a.dz = dz;
+  a.lddz = lddz;
+  a.part = part;
+  a.rows = rows;
+  a.rows_per_strip = pl.rows_per_strip;
+  a.cols = cols;
+  a.act = act;
+  return dt == CONV2D_BF16 ? dact<__nv_bfloat16>(a, zk, pl.strips, st) : dact<__half>(a, zk, pl.strips, st);
+}
+
+cudaError_t launch_column_sum(const float* part, int G, int cols, float* out, int accumulate, cudaStream_t st) {
+  return launch_k(column_sum_kernel, dim3((cols + 31) / 32), dim3(256), 0, st, 1, part, G, cols, out, accumulate);
+}
+
+template <typename T>
+static cudaError_t split_join(const float* part, int splits, long rows, int cols, T* out, long ldo, int accumulate,
+                              cudaStream_t st) {
+  if (cols % 4 == 0)  // the partials are dense, so every row of them starts on a 16-byte boundary
+    return launch_k(split_join_kernel<T, 4>, dim3(stream_grid(rows * (cols / 4))), dim3(256), 0, st, 1, part, splits,
+                    rows, cols, out, ldo, accumulate);
+  return launch_k(split_join_kernel<T, 1>, dim3(stream_grid(rows * cols)), dim3(256), 0, st, 1, part, splits, rows,
+                  cols, out, ldo, accumulate);
+}
+cudaError_t launch_split_join(const float* part, int splits, long rows, int cols, int type, void* out, long ldo,
+                              int accumulate, cudaStream_t st) {
+  if (type == CONV2D_FP32) return split_join(part, splits, rows, cols, static_cast<float*>(out), ldo, accumulate, st);
+  if (type == CONV2D_BF16)
+    return split_join(part, splits, rows, cols, static_cast<__nv_bfloat16*>(out), ldo, accumulate, st);
+  return split_join(part, splits, rows, cols, static_cast<__half*>(out), ldo, accumulate, st);
+}
+
+template <typename T>
+static cudaError_t zero_rows(long rows, int cols, T* out, long ld, cudaStream_t st) {
+  return launch_k(zero_rows_kernel<T>, dim3(stream_grid(rows * cols)), dim3(256), 0, st, 1, rows, cols, out, ld);
+}
+cudaError_t launch_zero_rows(long rows, int cols, int type, void* out, long ld, cudaStream_t st) {
+  if (type == CONV2D_FP32) return zero_rows(rows, cols, static_cast<float*>(out), ld, st);
+  if (type == CONV2D_BF16) return zero_rows(rows, cols, static_cast<__nv_bfloat16*>(out), ld, st);
+  return zero_rows(rows, cols, static_cast<__half*>(out), ld, st);
+}
+
+}  // namespace c2d
+
+// ------------------------------------------------------------------ C entry points
+using namespace c2d;
+
+namespace {
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool is_float(int type) { return type == CONV2D_FP32 || type == CONV2D_BF16 || type == CONV2D_FP16; }
+
+// A matrix argument: data present and aligned, ld at least cols, E4M3 with a known group and scales.
+int check_mat(const conv2d_mat* m, int cols) {
+  if (!m || !m->data || !aligned16(m->data)) return CONV2D_ERR_INVALID_ARG;
+  if (m->ld != 0 && m->ld < cols) return CONV2D_ERR_INVALID_ARG;
+  if (m->type == CONV2D_E4M3) {
+    if (!m->scale || (m->group != 0 && m->group != kQ8Group)) return CONV2D_ERR_INVALID_ARG;
+  } else if (!is_float(m->type)) {
+    return CONV2D_ERR_INVALID_ARG;
+  }
+  return CONV2D_OK;
+}
+long ld_of(const conv2d_mat* m, int cols) { return m->ld ? m->ld : cols; }
+
+// rows x cols within what the kernels index: 2^31 - 1 rows (one block each), byte offsets in 62 bits.
+int check_rows(int64_t rows, int32_t cols) {
+  if (rows < 0 || cols < 1) return CONV2D_ERR_INVALID_ARG;
+  if (rows > kMaxGridX || cols > (1 << 28)) return CONV2D_ERR_UNSUPPORTED;
+  return CONV2D_OK;
+}
+
+template <bool NORM>
+cudaError_t rows_fwd_any(const NormArgs& a, int type, cudaStream_t st) {
+  const int es = type == CONV2D_FP32 ? 4 : 2, VV = 16 / es;
+  bool vec = a.cols % VV == 0 && vec_ok(a.x, a.ldx, es, VV);
+  if (a.r) vec = vec && vec_ok(a.r, a.ldr, es, VV) && vec_ok(a.h, a.ldh, es, VV);
+  if (a.y) vec = vec && vec_ok(a.y, a.ldy, es, VV);
+  if (a.q) vec = vec && vec_ok(a.q, a.ldq, 1, VV);
+  switch (type) {
+    case CONV2D_BF16: return vec ? rows_fwd<__nv_bfloat16, 8, NORM>(a, st) : rows_fwd<__nv_bfloat16, 1, NORM>(a, st);
+    case CONV2D_FP16: return vec ? rows_fwd<__half, 8, NORM>(a, st) : rows_fwd<__half, 1, NORM>(a, st);
+    default: return vec ? rows_fwd<float, 4, NORM>(a, st) : rows_fwd<float, 1, NORM>(a, st);
+  }
+}
+
+}  // namespace
+
+extern "C" {
+
+int conv2d_q8_encode(int64_t rows, int32_t cols, const conv2d_mat* x, const conv2d_mat* q8, void* stream) {
+  int rc = check_rows(rows, cols);
+  if (rc) return rc;
+  if (rows == 0) return CONV2D_OK;
+  if ((rc = check_mat(x, cols)) || (rc = check_mat(q8, cols))) return rc;
+  if (!is_float(x->type) || q8->type != CONV2D_E4M3) return CONV2D_ERR_INVALID_ARG;
+  DevInfo* dev = nullptr;
+  if ((rc = device_info(&dev))) return rc;
+  NormArgs a = {};
+  a.x = x->data;
+  a.ldx = ld_of(x, cols);
+  a.q = static_cast<uint8_t*>(q8->data);
+  a.qs = q8->scale;
+  a.ldq = ld_of(q8, cols);
+  a.rows = rows;
+  a.cols = cols;
+  a.group = q8->group;
+  a.ng = q8->group ? (cols + kQ8Group - 1) / kQ8Group : 1;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  LAUNCH("q8_encode", st, rows_fwd_any<false>(a, x->type, st));
+  return CONV2D_OK;
+}
+
+int conv2d_q8_decode(int64_t rows, int32_t cols, const conv2d_mat* q8, const conv2d_mat* x, void* stream) {
+  int rc = check_rows(rows, cols);
+  if (rc) return rc;
+  if (rows == 0) return CONV2D_OK;
+  if ((rc = check_mat(x, cols)) || (rc = check_mat(q8, cols))) return rc;
+  if (!is_float(x->type) || q8->type != CONV2D_E4M3) return CONV2D_ERR_INVALID_ARG;
+  DevInfo* dev = nullptr;
+  if ((rc = device_info(&dev))) return rc;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  LAUNCH("q8_decode", st, launch_to_rows(*q8, rows, cols, x->type, x->data, x->ld, st));
+  return CONV2D_OK;
+}
+
+int conv2d_rms_norm_fwd(int64_t rows, int32_t cols, float eps, const conv2d_mat* x, const conv2d_mat* residual,
+                        const float* gamma, const conv2d_mat* h, const conv2d_mat* y, const conv2d_mat* q8,
+                        float* inv_rms, void* stream) {
+  int rc = check_rows(rows, cols);
+  if (rc) return rc;
+  if (!(eps > 0.f) || !std::isfinite(eps) || !gamma || !aligned16(gamma) || !aligned16(inv_rms))
+    return CONV2D_ERR_INVALID_ARG;
+  if ((residual == nullptr) != (h == nullptr) || (!y && !q8)) return CONV2D_ERR_INVALID_ARG;
+  if (rows == 0) return CONV2D_OK;
+  if ((rc = check_mat(x, cols))) return rc;
+  if (!is_float(x->type)) return CONV2D_ERR_INVALID_ARG;
+  for (const conv2d_mat* m : {residual, h, y})
+    if (m && ((rc = check_mat(m, cols)) || m->type != x->type)) return CONV2D_ERR_INVALID_ARG;
+  if (q8 && (check_mat(q8, cols) || q8->type != CONV2D_E4M3)) return CONV2D_ERR_INVALID_ARG;
+  DevInfo* dev = nullptr;
+  if ((rc = device_info(&dev))) return rc;
+  NormArgs a = {};
+  a.x = x->data;
+  a.ldx = ld_of(x, cols);
+  if (residual) {
+    a.r = residual->data;
+    a.ldr = ld_of(residual, cols);
+    a.h = h->data;
+    a.ldh = ld_of(h, cols);
+  }
+  a.gamma = gamma;
+  if (y) {
+    a.y = y->data;
+    a.ldy = ld_of(y, cols);
+  }
+  if (q8) {
+    a.q = static_cast<uint8_t*>(q8->data);
+    a.qs = q8->scale;
+    a.ldq = ld_of(q8, cols);
+    a.group = q8->group;
+    a.ng = q8->group ? (cols + kQ8Group - 1) / kQ8Group : 1;
+  }
+  a.inv = inv_rms;
+  a.rows = rows;
+  a.cols = cols;
+  a.eps = eps;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  LAUNCH("rms_norm_fwd", st, rows_fwd_any<true>(a, x->type, st));
+  return CONV2D_OK;
+}
+
+size_t conv2d_rms_norm_bwd_workspace_size(int64_t rows, int32_t cols) {
+  if (check_rows(rows, cols)) return 0;
+  return std::max<size_t>(256, static_cast<size_t>(norm_bwd_grid(rows, sms_for_sizing())) * cols * 4);
+}
+
+int conv2d_rms_norm_bwd(int64_t rows, int32_t cols, const conv2d_mat* h, const float* gamma, const float* inv_rms,
+                        const conv2d_mat* dy, const conv2d_mat* dh, const conv2d_mat* dx, float* dgamma,
+                        int accumulate, void* ws, size_t ws_bytes, void* stream) {
+  int rc = check_rows(rows, cols);
+  if (rc) return rc;
+  if ((!dx && !dgamma) || !gamma || !aligned16(gamma) || !aligned16(dgamma)) return CONV2D_ERR_INVALID_ARG;
+  DevInfo* dev = nullptr;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (rows == 0) {
+    if (!dgamma || accumulate) return CONV2D_OK;
+    if ((rc = device_info(&dev))) return rc;
+    LAUNCH("zero", st, launch_zero_rows(1, cols, CONV2D_FP32, dgamma, cols, st));
+    return CONV2D_OK;
+  }
+  if (!inv_rms || !aligned16(inv_rms)) return CONV2D_ERR_INVALID_ARG;
+  if ((rc = check_mat(h, cols)) || (rc = check_mat(dy, cols))) return rc;
+  if (!is_float(h->type) || dy->type != h->type) return CONV2D_ERR_INVALID_ARG;
+  for (const conv2d_mat* m : {dh, dx})
+    if (m && (check_mat(m, cols) || m->type != h->type)) return CONV2D_ERR_INVALID_ARG;
+  if ((rc = device_info(&dev))) return rc;
+  const size_t need = conv2d_rms_norm_bwd_workspace_size(rows, cols);
+  if (dgamma && (!ws || ws_bytes < need || (reinterpret_cast<uintptr_t>(ws) & 255u))) return CONV2D_ERR_WORKSPACE;
+  NormBwdArgs a = {};
+  a.h = h->data;
+  a.ldh = ld_of(h, cols);
+  a.dy = dy->data;
+  a.lddy = ld_of(dy, cols);
+  if (dx) {
+    a.dx = dx->data;
+    a.lddx = ld_of(dx, cols);
+  }
+  if (dh) {
+    a.dh = dh->data;
+    a.lddh = ld_of(dh, cols);
+  }
+  a.gamma = gamma;
+  a.inv = inv_rms;
+  a.part = dgamma ? static_cast<float*>(ws) : nullptr;
+  a.rows = rows;
+  a.cols = cols;
+  const int es = h->type == CONV2D_FP32 ? 4 : 2, VV = 16 / es;
+  bool vec = cols % VV == 0 && vec_ok(a.h, a.ldh, es, VV) && vec_ok(a.dy, a.lddy, es, VV);
+  if (a.dx) vec = vec && vec_ok(a.dx, a.lddx, es, VV);
+  if (a.dh) vec = vec && vec_ok(a.dh, a.lddh, es, VV);
+  const int grid = norm_bwd_grid(rows, dev->sms);
+  auto run = [&]() -> cudaError_t {
+    switch (h->type) {
+      case CONV2D_BF16: return vec ? norm_bwd<__nv_bfloat16, 8>(a, grid, st) : norm_bwd<__nv_bfloat16, 1>(a, grid, st);
+      case CONV2D_FP16: return vec ? norm_bwd<__half, 8>(a, grid, st) : norm_bwd<__half, 1>(a, grid, st);
+      default: return vec ? norm_bwd<float, 4>(a, grid, st) : norm_bwd<float, 1>(a, grid, st);
+    }
+  };
+  LAUNCH("rms_norm_bwd", st, run());
+  if (dgamma) LAUNCH("column_sum", st, launch_column_sum(a.part, grid, cols, dgamma, accumulate, st));
+  return CONV2D_OK;
+}
+
+}  // extern "C"

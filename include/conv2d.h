@@ -73,13 +73,26 @@ enum {
  * (GROUP with groups = 1 computes LAYER). */
 enum { CONV2D_NORM_NONE = 0, CONV2D_NORM_BATCH = 1, CONV2D_NORM_LAYER = 2, CONV2D_NORM_GROUP = 3 };
 
-/* Activation applied after (optional) normalization. */
-enum { CONV2D_ACT_IDENTITY = 0, CONV2D_ACT_RELU = 1, CONV2D_ACT_TANH = 2, CONV2D_ACT_SIGMOID = 3 };
+/* Activation applied after (optional) normalization. Conv layers take the
+ * first four. */
+enum {
+    CONV2D_ACT_IDENTITY = 0,
+    CONV2D_ACT_RELU = 1,
+    CONV2D_ACT_TANH = 2,
+    CONV2D_ACT_SIGMOID = 3,
+    CONV2D_ACT_GELU = 4, /* dense layers only: z/2 (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) */
+    CONV2D_ACT_SILU = 5  /* dense layers only: z / (1 + exp(-z)) */
+};
 
-/* Element type of x, w, pre_act, y, dy, dx. FP32 runs the contractions as
+/* Element types. Conv layers (x, w, pre_act, y, dy, dx): FP32 or BF16. FP32 runs the contractions as
  * 3xTF32 (split operands, fp32 accumulation) for fp32 accuracy; BF16 runs
  * bf16 x bf16 -> fp32 accumulation. */
-enum { CONV2D_FP32 = 0, CONV2D_BF16 = 1 };
+enum {
+    CONV2D_FP32 = 0,
+    CONV2D_BF16 = 1,
+    CONV2D_FP16 = 2, /* conv2d_mat only */
+    CONV2D_E4M3 = 3  /* conv2d_mat only: 8-bit floats (4 exponent, 3 mantissa bits, no infinities) with scales */
+};
 
 /* Operation selector for conv2d_workspace_size(). */
 enum { CONV2D_OP_FWD_TRAIN = 0, CONV2D_OP_FWD_INFER = 1, CONV2D_OP_BWD = 2 };
@@ -177,6 +190,114 @@ int conv2d_bwd(const conv2d_desc* desc, const void* x, const void* w, const floa
                const float* beta, const void* pre_act, const float* save_mean,
                const float* save_inv_std, const void* dy, void* dx, float* dw, float* dbias,
                float* dgamma, float* dbeta, void* ws, size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * The residual block: RMS norm, dense layer, 8-bit activation checkpoints.
+ *
+ * These calls take matrices of rows (tokens, or the pixels of an NHWC tensor:
+ * N*H*W rows of C columns) by columns (features), each described by a
+ * conv2d_mat. The conventions above hold (device pointers aligned to 16
+ * bytes, caller-owned memory, asynchronous on `stream`, status codes), with
+ * these differences: rows may be strided, a row count of zero is valid (the
+ * call writes nothing, except that gradients to be overwritten become zero),
+ * and gradients are accumulated only where `accumulate` is nonzero and
+ * overwritten otherwise.
+ *
+ * Sums (dot products, mean squares, column sums) are held in fp32; an output
+ * of fewer bits is rounded once, to nearest even. Results do not depend on
+ * timing: every sum is formed in a fixed order.
+ * ------------------------------------------------------------------------ */
+
+/* A row-major matrix in device memory.
+ *   type   FP32, BF16, FP16 or E4M3
+ *   ld     elements from the start of one row to the next, at least the
+ *          number of columns; 0 stands for the number of columns
+ *   group, scale   E4M3 only: columns that share a scale (32, or 0 for a whole
+ *          row) and the scales, one byte for each group, dense, row by row
+ *          ([rows][ceil(columns / group)]): byte s stands for 2^(s - 127).
+ *          The element (r, c) has the value data[r][c] * scale(r, c).
+ *          `scale` has no alignment rule. */
+typedef struct {
+    void* data;
+    int64_t ld;
+    int32_t type;
+    int32_t group;
+    uint8_t* scale;
+} conv2d_mat;
+
+/* 8-bit checkpoints. conv2d_q8_encode writes x (FP32, BF16 or FP16) as E4M3:
+ * the scale of a group is the smallest power of two (2^-126 .. 2^127) that
+ * keeps every finite value within 448 times the scale (1 for a group without
+ * a finite nonzero value); values are rounded to nearest even (relative error
+ * at most 2^-4 down to 2^-6 of the scale, absolute error at most 2^-10 of the
+ * scale below); infinities and NaN become NaN. conv2d_q8_decode writes the
+ * values it stands for, clamped to the largest finite value of the type (the
+ * rounding to 8 bits may carry a value past it): exact otherwise in FP32, and
+ * in BF16 for scales of 2^-124 or more; FP16 rounds what lies below its
+ * normal range. */
+int conv2d_q8_encode(int64_t rows, int32_t cols, const conv2d_mat* x, const conv2d_mat* q8, void* stream);
+int conv2d_q8_decode(int64_t rows, int32_t cols, const conv2d_mat* q8, const conv2d_mat* x, void* stream);
+
+/* Root-mean-square norm of the rows of h = x + residual:
+ *   s = 1 / sqrt(mean_j h_j^2 + eps),   y_j = gamma_j h_j s
+ *   x, residual, h, y   one type T of FP32, BF16, FP16. residual and h are
+ *                given together or both NULL (then h = x and is not written);
+ *                h is rounded to T, and the norm is taken of the rounded h.
+ *                h may be the same buffer as x or as residual.
+ *   q8           E4M3 form of y, from the unrounded y (see conv2d_q8_encode)
+ *   inv_rms [rows]  s, for conv2d_rms_norm_bwd
+ * y, q8 and inv_rms may be NULL; one of y and q8 is not. */
+int conv2d_rms_norm_fwd(int64_t rows, int32_t cols, float eps, const conv2d_mat* x, const conv2d_mat* residual,
+                        const float* gamma, const conv2d_mat* h, const conv2d_mat* y, const conv2d_mat* q8,
+                        float* inv_rms, void* stream);
+
+/* Bytes of workspace of conv2d_rms_norm_bwd (0 if the sizes are invalid). */
+size_t conv2d_rms_norm_bwd_workspace_size(int64_t rows, int32_t cols);
+
+/* Backward of conv2d_rms_norm_fwd. h, dy, dh, dx have one type T.
+ *   dx = s gamma dy - h s^3 mean_j(gamma_j dy_j h_j) + dh  (the gradient of x
+ *   and of residual); dgamma = sum over rows of dy h s.
+ * dh, the gradient that reaches h beside the norm, may be NULL, and may be
+ * the same buffer as dx. dx or dgamma may be NULL, not both. */
+int conv2d_rms_norm_bwd(int64_t rows, int32_t cols, const conv2d_mat* h, const float* gamma, const float* inv_rms,
+                        const conv2d_mat* dy, const conv2d_mat* dh, const conv2d_mat* dx, float* dgamma,
+                        int accumulate, void* ws, size_t ws_bytes, void* stream);
+
+/* Dense layer: y = act(z) + residual, z = x w^T + bias.
+ * x [M][K], w [N][K], residual, y, z [M][N]; dtype (BF16 or FP16) is the type
+ * of residual, y, dx, dy and of operands that are not E4M3. Products of BF16 /
+ * FP16 operands accumulate in fp32. Where x and w are both E4M3 with one
+ * scale a row, the product runs on the 8-bit operands and the scales are
+ * applied to its sums; any other E4M3 operand is decoded to dtype first. */
+typedef struct {
+    int64_t M;          /* rows of x and y */
+    int32_t K, N;       /* features in and out */
+    int32_t act, dtype;
+    int32_t accumulate; /* backward: add to dw and dbias (1) or overwrite them (0) */
+} conv2d_dense_desc;
+
+/* Bytes of workspace (0 if the arguments are invalid); of the matrices only
+ * data's alignment, ld, type and group are looked at. */
+size_t conv2d_dense_fwd_workspace_size(const conv2d_dense_desc* desc, const conv2d_mat* x, const conv2d_mat* w);
+size_t conv2d_dense_bwd_workspace_size(const conv2d_dense_desc* desc, const conv2d_mat* x, const conv2d_mat* w,
+                                       const conv2d_mat* pre_act, const conv2d_mat* dy, const conv2d_mat* dx,
+                                       const conv2d_mat* dw, const float* dbias);
+
+/* Forward. bias [N], residual and pre_act may be NULL. pre_act receives z for
+ * the backward pass, in dtype or as E4M3 with groups of 32; y is computed
+ * from the unrounded z. residual may be the same buffer as y. */
+int conv2d_dense_fwd(const conv2d_dense_desc* desc, const conv2d_mat* x, const conv2d_mat* w, const float* bias,
+                     const conv2d_mat* residual, const conv2d_mat* pre_act, const conv2d_mat* y, void* ws,
+                     size_t ws_bytes, void* stream);
+
+/* Backward: dz = dy act'(z), dx = dz w, dw = dz^T x, dbias = sum over rows of
+ * dz (the gradient of residual is dy itself). x, w and pre_act may be E4M3
+ * (checkpoints); pre_act may be NULL when act is IDENTITY. dz is stored in
+ * dtype for the two products (with IDENTITY dz is dy); dbias sums the
+ * unrounded dz. dx, dw, dbias may be NULL, not all; dw is FP32 or dtype. */
+int conv2d_dense_bwd(const conv2d_dense_desc* desc, const conv2d_mat* x, const conv2d_mat* w,
+                     const conv2d_mat* pre_act, const conv2d_mat* dy, const conv2d_mat* dx, const conv2d_mat* dw,
+                     float* dbias, void* ws, size_t ws_bytes, void* stream);
 
 /* Synchronises `stream`, then reads and clears this device's error word,
  * which kernels set when a bounded wait expires. Returns CONV2D_OK,
