@@ -541,7 +541,8 @@ __global__ void __launch_bounds__(256) dact_kernel(const DactArgs a) {
 #pragma unroll
         for (int k = 0; k < V; ++k) {
           float v = to_f(d[k]);
-          if constexpr (ZK) v *= dense_dact<decltype(act)::value>(f[k]);
+          // not contracted into the sum: the column sums are the same whether dz is written or not
+          if constexpr (ZK) v = __fmul_rn(v, dense_dact<decltype(act)::value>(f[k]));
           acc[k] += v;
           o[k] = from_f<T>(v);
         }
