@@ -43,7 +43,7 @@ struct GemmPlan {
 // larger of its MMA time (128 x BN x 64 products at 4,096 a clock, half a pair's) and of bringing its operand
 // tiles (about 64 bytes a clock); units run in waves over the SMs. can_split: the product may be split over k
 // with fp32 partials in the workspace (weight gradients); max_kb: bound on one accumulator's k-blocks (0: none).
-GemmPlan plan_gemm(long lanes, long cols, int kb, bool c_mn, bool can_split, int max_kb, int sms) {
+GemmPlan plan_gemm(long m, long n, int kb, bool r_mn, bool can_split, int max_kb, int sms) {
   GemmPlan best = {};
   double best_t = 1e300;
   auto consider = [&](bool pair, int BN, int cl, int splits) {
@@ -55,8 +55,8 @@ GemmPlan plan_gemm(long lanes, long cols, int kb, bool c_mn, bool can_split, int
     g.kb_per_split = static_cast<int>(ceil_div(kb, splits));
     g.splits = static_cast<int>(ceil_div(kb, g.kb_per_split));
     if (max_kb > 0 && ceil_div(g.kb_per_split, cl) > max_kb) return;
-    g.l_tiles = static_cast<int>(ceil_div(lanes, pair ? 256 : 128));
-    g.c_tiles = static_cast<int>(ceil_div(cols, BN));
+    g.l_tiles = static_cast<int>(pair ? ceil_div(m, 256) : ceil_div(n, 128));
+    g.c_tiles = static_cast<int>(ceil_div(pair ? n : m, BN));
     const double units = static_cast<double>(g.l_tiles) * g.c_tiles * g.splits;
     if (units * cl > INT_MAX / 4) return;
     const int per_cta = pair ? BN / 2 : BN;  // columns of C a CTA loads
@@ -66,7 +66,7 @@ GemmPlan plan_gemm(long lanes, long cols, int kb, bool c_mn, bool can_split, int
     double t;
     if (pair) t = std::ceil(units / (sms / 2)) * std::max(loop, epi) + epi + 5000;
     else t = std::ceil(units * cl / sms) * (loop + (cl > 1 ? epi / cl + 1500 : epi) + 1500) + 2000;
-    if (g.splits > 1) t += 4000 + static_cast<double>(lanes) * cols * 4 * 2 * g.splits / 3500;
+    if (g.splits > 1) t += 4000 + static_cast<double>(m) * n * 4 * 2 * g.splits / 3500;
     if (t < best_t) {
       best_t = t;
       best = g;
@@ -75,13 +75,13 @@ GemmPlan plan_gemm(long lanes, long cols, int kb, bool c_mn, bool can_split, int
   for (int splits = 1; splits <= (can_split ? 512 : 1) && splits <= kb; splits += splits < 8 ? 1 : splits / 8) {
     for (int BN : {256, 128}) consider(true, BN, 1, splits);
     for (int BN : {128, 64, 32, 16}) {
-      if (c_mn && BN < 64) continue;  // MN-major tiles are panels of 64
+      if (r_mn && BN < 64) continue;  // MN-major tiles are panels of 64
       for (int cl : {1, 2, 4, 8})
         if (cl == 1 || ceil_div(kb, splits) >= 2 * cl) consider(false, BN, cl, splits);
     }
   }
   const int stage = 128 * 128 + (best.pair ? best.BN / 2 : best.BN) * 128;
-  const int room = static_cast<int>(kMaxDynSmem) - 2048;
+  const int room = static_cast<int>(kMaxDynSmem) - 1536 - (best.pair ? kPairBuffers : 0);
   const long units = static_cast<long>(best.l_tiles) * best.c_tiles * best.splits;
   if (best.pair) {
     best.grid = 2 * static_cast<int>(std::min<long>(units, sms / 2));
@@ -94,7 +94,8 @@ GemmPlan plan_gemm(long lanes, long cols, int kb, bool c_mn, bool can_split, int
     best.stages = std::max(2, std::min({kDenseMaxStages, budget / stage, need}));
     if (best.cluster > 1) best.stages = std::max<int>(best.stages, static_cast<int>(ceil_div(best.BN * 512, stage)));
   }
-  best.smem = static_cast<size_t>(best.stages) * stage + 1024 + 512;  // alignment slack, barriers
+  // alignment slack, barriers
+  best.smem = static_cast<size_t>(best.stages) * stage + 1024 + 512 + (best.pair ? kPairBuffers : 0);
   return best;
 }
 
@@ -124,18 +125,23 @@ struct Operand {
   long rows, cols, ld;
 };
 
-// out[m][n] = sum_k C[m][k] L[n][k]; l_mn / c_mn: the operand lies with k along its rows.
-int run_gemm(DenseGemmParams& p, const GemmPlan& g, const Operand& l, bool l_mn, const Operand& c, bool c_mn, int dt,
+// out[m][n] = sum_k R[m][k] C[n][k]; r_mn / c_mn: the operand lies with k along its rows. The rows of the output
+// are the accumulator's lanes in the pair kernel and its columns in the cluster kernel.
+int run_gemm(DenseGemmParams& p, const GemmPlan& g, const Operand& r, bool r_mn, const Operand& c, bool c_mn, int dt,
              int epi, const char* name, const DevInfo* dev, cudaStream_t st) {
-  if (!encode_operand(&p.tl, l.data, l.type, l.rows, l.cols, l.ld, l_mn, 128) ||
-      !encode_operand(&p.tc, c.data, c.type, c.rows, c.cols, c.ld, c_mn, g.pair ? g.BN / 2 : g.BN))
+  const Operand &lo = g.pair ? r : c, &co = g.pair ? c : r;
+  p.l_mn = g.pair ? r_mn : c_mn;
+  p.c_mn = g.pair ? c_mn : r_mn;
+  if (!encode_operand(&p.tl, lo.data, lo.type, lo.rows, lo.cols, lo.ld, p.l_mn, 128) ||
+      !encode_operand(&p.tc, co.data, co.type, co.rows, co.cols, co.ld, p.c_mn, g.pair ? g.BN / 2 : g.BN))
     return CONV2D_ERR_CUDA;
-  p.l_mn = l_mn;
-  p.c_mn = c_mn;
-  p.fp8 = l.type == CONV2D_E4M3;
-  p.fmt = l.type == CONV2D_BF16 ? 1u : 0u;
-  p.lanes = static_cast<int>(l_mn ? l.cols : l.rows);
-  p.cols = c_mn ? c.cols : c.rows;
+  p.fp8 = r.type == CONV2D_E4M3;
+  p.fmt = r.type == CONV2D_BF16 ? 1u : 0u;
+  p.m = r_mn ? r.cols : r.rows;
+  p.n = static_cast<int>(c_mn ? c.cols : c.rows);
+  p.vec_out = p.ldo % (p.out_f32 ? 4 : 8) == 0;
+  p.vec_res = p.ldr % 8 == 0;
+  p.vec_z = p.ldz % (p.zq ? 16 : 8) == 0;
   p.l_tiles = g.l_tiles;
   p.c_tiles = g.c_tiles;
   p.splits = g.splits;
@@ -216,7 +222,7 @@ void plan_fwd(const conv2d_dense_desc& d, const conv2d_mat* x, const conv2d_mat*
   pl->x = plan_copy(c, x, d.M, d.K, pl->fp8);
   pl->w = plan_copy(c, w, d.N, d.K, pl->fp8);
   pl->total = std::max<size_t>(c.total, 256);
-  pl->g = plan_gemm(d.N, d.M, static_cast<int>(ceil_div(d.K, pl->fp8 ? 128 : 64)), false, false, 0, sms);
+  pl->g = plan_gemm(d.M, d.N, static_cast<int>(ceil_div(d.K, pl->fp8 ? 128 : 64)), false, false, 0, sms);
 }
 
 struct BwdPlan {
@@ -238,11 +244,11 @@ void plan_bwd(const conv2d_dense_desc& d, const conv2d_mat* x, const conv2d_mat*
   pl->w = pl->x = pl->spart = kNone;
   if (dx) {
     pl->w = plan_copy(c, w, d.N, d.K, false);
-    pl->gx = plan_gemm(d.K, d.M, static_cast<int>(ceil_div(d.N, 64)), false, false, 0, sms);
+    pl->gx = plan_gemm(d.M, d.K, static_cast<int>(ceil_div(d.N, 64)), false, false, 0, sms);
   }
   if (dw) {
     pl->x = plan_copy(c, x, d.M, d.K, false);
-    pl->gw = plan_gemm(d.K, d.N, static_cast<int>(ceil_div(d.M, 64)), true, true,
+    pl->gw = plan_gemm(d.N, d.K, static_cast<int>(ceil_div(d.M, 64)), true, true,
                        dw->type == CONV2D_FP32 ? kFp32SplitKb : 0, sms);
     if (pl->gw.splits > 1) pl->spart = c.take(static_cast<size_t>(pl->gw.splits) * d.N * d.K * 4);
   }
@@ -312,8 +318,8 @@ int conv2d_dense_fwd(const conv2d_dense_desc* d, const conv2d_mat* x, const conv
   if ((rc = make_operand(&ow, w, d->N, d->K, pl.fp8, d->dtype, pl.w, ws, "dense_w", st))) return rc;
   DenseGemmParams p = {};
   if (pl.fp8) {
-    p.ls = w->scale;
-    p.cs = x->scale;
+    p.ns = w->scale;
+    p.ms = x->scale;
   }
   p.bias = bias;
   p.act = d->act;
@@ -333,7 +339,7 @@ int conv2d_dense_fwd(const conv2d_dense_desc* d, const conv2d_mat* x, const conv
   }
   p.out = y->data;
   p.ldo = ld_of(y, d->N);
-  return run_gemm(p, pl.g, ow, false, ox, false, d->dtype, kDenseForward, "dense_fwd", dev, st);
+  return run_gemm(p, pl.g, ox, false, ow, false, d->dtype, kDenseForward, "dense_fwd", dev, st);
 }
 
 int conv2d_dense_bwd(const conv2d_dense_desc* d, const conv2d_mat* x, const conv2d_mat* w, const conv2d_mat* pre_act,
@@ -381,7 +387,7 @@ int conv2d_dense_bwd(const conv2d_dense_desc* d, const conv2d_mat* x, const conv
     DenseGemmParams p = {};
     p.out = dx->data;
     p.ldo = ld_of(dx, d->K);
-    if ((rc = run_gemm(p, pl.gx, ow, true, odz, false, d->dtype, kDenseStore, "dense_dx", dev, st))) return rc;
+    if ((rc = run_gemm(p, pl.gx, odz, false, ow, true, d->dtype, kDenseStore, "dense_dx", dev, st))) return rc;
   }
   if (dw) {
     Operand ox;
@@ -393,7 +399,7 @@ int conv2d_dense_bwd(const conv2d_dense_desc* d, const conv2d_mat* x, const conv
     p.out_f32 = joined || dw->type == CONV2D_FP32;
     p.accumulate = !joined && d->accumulate;
     p.split_stride = static_cast<long>(d->N) * d->K;
-    if ((rc = run_gemm(p, pl.gw, ox, true, odz, true, d->dtype, kDenseStore, "dense_dw", dev, st))) return rc;
+    if ((rc = run_gemm(p, pl.gw, odz, true, ox, true, d->dtype, kDenseStore, "dense_dw", dev, st))) return rc;
     if (joined)
       LAUNCH("dense_dw_join", st,
              launch_split_join(reinterpret_cast<float*>(base + pl.spart), pl.gw.splits, d->N, d->K, dw->type, dw->data,

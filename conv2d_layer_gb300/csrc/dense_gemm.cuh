@@ -1,26 +1,24 @@
 // dense_gemm.cuh - the dense layer's matrix products on the 5th-generation
-// tensor cores: out[m][n] = sum_k C[m][k] L[n][k] for the three products of a
+// tensor cores: out[m][n] = sum_k R[m][k] C[n][k] for the three products of a
 // dense layer's step,
-//   forward  y[M][N]  = x[M][K] w[N][K]^T           L = w,  C = x
-//   dx       [M][K]   = dz[M][N] w[N][K]            L = w (k along its rows), C = dz
-//   dW       [N][K]   = dz[M][N]^T x[M][K]          L = x (k along its rows), C = dz (likewise)
-// L, the operand that runs along the output's rows (its contiguous dimension),
-// takes the accumulator's lanes, C its columns. So the 32 lanes of an epilogue
-// warp hold 32 neighbouring elements of one output row: it writes (and reads
-// the residual) in whole sectors straight from the tensor memory layout, a
-// bias is one register, and a group of 32 columns that shares an 8-bit scale
-// is one warp, its maximum one redux instruction.
-//
+//   forward  y[M][N]  = x[M][K] w[N][K]^T           R = x,  C = w
+//   dx       [M][K]   = dz[M][N] w[N][K]            R = dz, C = w (k along its rows)
+//   dW       [N][K]   = dz[M][N]^T x[M][K]          R = dz, C = x (k along the rows of both)
 // Both operands come by TMA into 128-byte swizzled tiles, K-major or MN-major
 // as they lie in memory (no transposed copies); elements outside the matrices
 // read as zero, so no size needs to be a multiple of a tile.
 //
 // Two kernels:
-//   dense_pair_kernel     persistent CTA pairs (cta_group::2), 256 lanes x BN columns a unit, two
-//                         accumulators, so that the epilogue of a unit runs under the next one's MMAs
-//   dense_cluster_kernel  one unit of 128 lanes x BN columns for a cluster of `cluster` CTAs, which
-//                         split the K loop and join their sums through distributed shared memory in
-//                         rank order: for outputs too small to give every SM a unit of its own
+//   dense_pair_kernel     for outputs of many tiles: persistent CTA pairs (cta_group::2), 256 rows x BN columns a
+//                         unit, two accumulators, so that the epilogue of a unit runs under the next one's
+//                         MMAs. Rows of the output are accumulator lanes: a thread holds 32 neighbouring
+//                         columns of its row (an 8-bit group), packs them, and the warp turns 32 rows x
+//                         128 bytes around in shared memory so that memory is read and written in whole lines
+//   dense_cluster_kernel  for few rows or few tiles: one unit for a cluster of `cluster` CTAs, which split the
+//                         K loop and join their sums through distributed shared memory in rank order. Columns
+//                         of the output are accumulator lanes (128), rows its columns (16 to 128), so that one
+//                         token costs 16 MMA columns and not 128 lanes; a warp holds 32 neighbouring elements
+//                         of a row and accesses memory directly
 #pragma once
 #include "ptx.cuh"
 #include "q8.cuh"
@@ -29,21 +27,22 @@ namespace c2d {
 
 constexpr int kDenseThreads = 320;  // TMA warp, MMA warp, 8 epilogue warps
 constexpr int kDenseMaxStages = 10;
+constexpr int kPairBuffers = 8 * 4096;  // the pair kernel's epilogue: 4 KB a warp
 enum : int { kSiteDenseFull = 11, kSiteDenseEmpty = 12, kSiteDenseTFull = 13, kSiteDenseTEmpty = 14 };
 enum : int { kDenseForward = 0, kDenseStore = 1 };  // epilogues
 
 struct DenseGemmParams {
-  CUtensorMap tl, tc;
+  CUtensorMap tl, tc;   // the operands whose rows are the accumulator's lanes / columns
   int l_mn, c_mn;       // operand lies MN-major (its k index runs along memory rows)
   int fp8;              // e4m3 operands (K-major only)
   uint32_t fmt;         // instruction descriptor's operand format: fp16 0, bf16 1, e4m3 0
-  int lanes;            // n: length of an output row
-  long cols;            // m: output rows
+  int n;                // columns of the output
+  long m;               // rows of the output
   int l_tiles, c_tiles, splits;
   int kb_total, kb_per_split;  // k-blocks of 128 bytes: 64 16-bit or 128 8-bit elements
   int BN, stages, cluster;
-  // kDenseForward: v = acc * ls[n] * cs[m] + bias[n]; z = v; out = act(v) + res
-  const uint8_t *ls, *cs;
+  // kDenseForward: v = acc * ns[n] * ms[m] + bias[n]; z = v; out = act(v) + res
+  const uint8_t *ns, *ms;  // scale bytes of 8-bit operands (both or neither)
   const float* bias;
   int act;
   const void* res;
@@ -56,6 +55,7 @@ struct DenseGemmParams {
   long split_stride;
   void* out;
   long ldo;
+  int vec_out, vec_res, vec_z;  // rows of out / res / z (zq) start on 16-byte boundaries
   int* err;
 };
 
@@ -81,14 +81,14 @@ __device__ __forceinline__ float ld_shared_cluster_f32(uint32_t caddr) {
   return v;
 }
 
-// ---------------------------------------------------------------- epilogue
-// NC columns (output rows m0 ..) of one lane (output column n; off: n is past the row's end). Warp-collective
-// (the 8-bit form of z takes a maximum over the warp's 32 lanes, which are one group).
+// ---------------------------------------------------------------- epilogue of the cluster kernel
+// NC rows of the output (m0 ..) of one column (n; off: past the end) a thread. Warp-collective (the 8-bit form
+// of z takes a maximum over the warp's 32 columns, which are one group).
 template <typename T, int EPI, int NC>
 __device__ __forceinline__ void dense_epilogue(const DenseGemmParams& p, float (&v)[NC], int n, long m0, int split,
-                                               float lscale, float bias) {
-  const int nc = static_cast<int>(p.cols - m0 < NC ? p.cols - m0 : NC);  // uniform
-  const bool on = n < p.lanes;
+                                               float nscale, float bias) {
+  const int nc = static_cast<int>(p.m - m0 < NC ? p.m - m0 : NC);  // uniform
+  const bool on = n < p.n;
   if constexpr (EPI == kDenseForward) {
     T res[NC];
     if (p.res) {
@@ -97,9 +97,9 @@ __device__ __forceinline__ void dense_epilogue(const DenseGemmParams& p, float (
       for (int e = 0; e < NC; ++e)
         if (on && e < nc) res[e] = r[e * p.ldr];
     }
-    if (p.ls) {
+    if (p.ns) {
 #pragma unroll
-      for (int e = 0; e < NC; ++e) v[e] = e < nc ? v[e] * lscale * q8_scale(p.cs[m0 + e]) : 0.f;
+      for (int e = 0; e < NC; ++e) v[e] = e < nc ? v[e] * nscale * q8_scale(p.ms[m0 + e]) : 0.f;
     }
 #pragma unroll
     for (int e = 0; e < NC; ++e) v[e] += bias;
@@ -137,6 +137,235 @@ __device__ __forceinline__ void dense_epilogue(const DenseGemmParams& p, float (
 #pragma unroll
       for (int e = 0; e < NC; ++e)
         if (e < nc) o[e * p.ldo] = from_f<T>(p.accumulate ? to_f(o[e * p.ldo]) + v[e] : v[e]);
+    }
+  }
+}
+
+// ---------------------------------------------------------------- epilogue of the pair kernel
+// A warp's buffer of 32 rows x RB bytes (64 or 128) in shared memory; 16-byte pieces are swizzled so that a
+// thread's own row and the warp's whole lines are both accessed without bank conflicts.
+template <int RB>
+__device__ __forceinline__ uint32_t row_piece(int r, int j) {
+  return RB == 128 ? static_cast<uint32_t>(r * 128 + ((j ^ (r & 7)) << 4))
+                   : static_cast<uint32_t>(r * 64 + ((j ^ ((r >> 1) & 3)) << 4));
+}
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ void sts128(uint32_t a, const uint4& v) { st_shared_v4(a, v.x, v.y, v.z, v.w); }
+
+// The buffer's rows (nr of them) x nc elements of type E to memory at g (row length ld), whole lines at a
+// time; vec: rows start on 16-byte boundaries. accumulate: added to what is there (in fp32).
+template <typename E, int RB>
+__device__ __forceinline__ void rows_out(uint32_t buf, E* g, long ld, int nr, int nc, bool vec, bool accumulate,
+                                         int lane) {
+  constexpr int PE = 16 / static_cast<int>(sizeof(E)), PR = RB / 16;  // elements a piece, pieces a row
+  constexpr int RI = 32 / PR;                                         // rows an instruction
+  const int j = lane % PR;
+  const bool whole = vec && (j + 1) * PE <= nc;
+#pragma unroll
+  for (int i = 0; i < 32 / RI; ++i) {
+    const int r = i * RI + lane / PR;
+    if (r >= nr || j * PE >= nc) continue;
+    uint4 w = lds128(buf + row_piece<RB>(r, j));
+    E* o = g + r * ld + j * PE;
+    if constexpr (sizeof(E) > 1) {
+      if (accumulate) {
+        E* e = reinterpret_cast<E*>(&w);
+        if (whole) {
+          uint4 old = *reinterpret_cast<const uint4*>(o);
+          const E* f = reinterpret_cast<const E*>(&old);
+#pragma unroll
+          for (int k = 0; k < PE; ++k) e[k] = from_f<E>(to_f(f[k]) + to_f(e[k]));
+        } else {
+#pragma unroll
+          for (int k = 0; k < PE; ++k)
+            if (j * PE + k < nc) e[k] = from_f<E>(to_f(o[k]) + to_f(e[k]));
+        }
+      }
+    }
+    if (whole) {
+      *reinterpret_cast<uint4*>(o) = w;
+    } else {
+      const E* e = reinterpret_cast<const E*>(&w);
+#pragma unroll
+      for (int k = 0; k < PE; ++k)
+        if (j * PE + k < nc) o[k] = e[k];
+    }
+  }
+}
+// Packs 8 values as T.
+template <typename T>
+__device__ __forceinline__ uint4 pack8(const float* v) {
+  uint4 w;
+  T* e = reinterpret_cast<T*>(&w);
+#pragma unroll
+  for (int k = 0; k < 8; ++k) e[k] = from_f<T>(v[k]);
+  return w;
+}
+
+// A warp's 32 rows (m0 ..) x nhalf columns (n0 ..; a multiple of 64) of the accumulator at taddr.
+template <typename T, int EPI>
+__device__ __forceinline__ void pair_epilogue(const DenseGemmParams& p, uint32_t taddr, uint32_t buf, long m0, int n0,
+                                              int nhalf, int split, int lane) {
+  const int nr = static_cast<int>(p.m - m0 < 32 ? p.m - m0 : 32);
+  if (nr <= 0) return;  // uniform
+  if constexpr (EPI == kDenseForward) {
+    const float mscale = p.ms && lane < nr ? q8_scale(p.ms[m0 + lane]) : 1.f;
+#pragma unroll 1
+    for (int c = 0; c < nhalf; c += 64) {
+      const int n = n0 + c;
+      const int nc = p.n - n < 64 ? p.n - n : 64;
+      if (nc <= 0) return;
+      // the residual's lines are in flight while the sums are read and activated
+      uint4 res[8];
+      const int rj = lane & 7;
+      if (p.res && p.vec_res) {
+        const T* r = static_cast<const T*>(p.res) + m0 * p.ldr + n + rj * 8;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int row = i * 4 + (lane >> 3);
+          if (row < nr && (rj + 1) * 8 <= nc) res[i] = *reinterpret_cast<const uint4*>(r + row * p.ldr);
+        }
+      }
+      float v[64];
+      {
+        uint32_t a[32], b[32];
+        tmem_ld32(taddr + c, a);
+        tmem_ld32(taddr + c + 32, b);
+        tmem_ld_wait2(a, b);
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+          v[e] = __uint_as_float(a[e]);
+          v[32 + e] = __uint_as_float(b[e]);
+        }
+      }
+      if (p.ns) {
+#pragma unroll
+        for (int e = 0; e < 64; ++e)
+          if (e < nc) v[e] = v[e] * q8_scale(p.ns[n + e]) * mscale;
+      }
+      if (p.bias) {
+        if (nc == 64) {
+#pragma unroll
+          for (int e = 0; e < 64; e += 4) {
+            const float4 b = *reinterpret_cast<const float4*>(p.bias + n + e);
+            v[e] += b.x;
+            v[e + 1] += b.y;
+            v[e + 2] += b.z;
+            v[e + 3] += b.w;
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 64; ++e)
+            if (e < nc) v[e] += p.bias[n + e];
+        }
+      }
+      if (p.zq) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (h * 32 >= nc) break;  // uniform
+          uint32_t top = 0u;
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            const uint32_t b = finite_bits(v[32 * h + e]);
+            if (32 * h + e < nc) top = max(top, b);
+          }
+          const uint32_t byte = q8_scale_byte(top);
+          const float inv = q8_inv_scale(byte);
+          if (lane < nr) p.zs[(m0 + lane) * p.zg + n / kQ8Group + h] = static_cast<uint8_t>(byte);
+          uint32_t w[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float* x = v + 32 * h + 4 * e;
+            w[e] = q8_pack2(x[0] * inv, x[1] * inv) | q8_pack2(x[2] * inv, x[3] * inv) << 16;
+          }
+          st_shared_v4(buf + row_piece<64>(lane, 2 * h), w[0], w[1], w[2], w[3]);
+          st_shared_v4(buf + row_piece<64>(lane, 2 * h + 1), w[4], w[5], w[6], w[7]);
+        }
+        __syncwarp();
+        rows_out<uint8_t, 64>(buf, p.zq + m0 * p.ldz + n, p.ldz, nr, nc, p.vec_z, false, lane);
+        __syncwarp();
+      } else if (p.z) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sts128(buf + row_piece<128>(lane, j), pack8<T>(v + 8 * j));
+        __syncwarp();
+        rows_out<T, 128>(buf, static_cast<T*>(p.z) + m0 * p.ldz + n, p.ldz, nr, nc, p.vec_z, false, lane);
+        __syncwarp();
+      }
+      with_dense_act(p.act, [&](auto act) {
+#pragma unroll
+        for (int e = 0; e < 64; ++e) v[e] = dense_act<decltype(act)::value>(v[e]);
+      });
+      if (p.res) {
+        if (p.vec_res && nc == 64) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) sts128(buf + row_piece<128>(i * 4 + (lane >> 3), rj), res[i]);
+        } else {
+          for (int i = lane; i < 32 * 64; i += 32) {
+            const int row = i >> 6, col = i & 63;
+            if (row < nr && col < nc) {
+              const T x = static_cast<const T*>(p.res)[(m0 + row) * p.ldr + n + col];
+              uint16_t bits = *reinterpret_cast<const uint16_t*>(&x);
+              asm volatile("st.shared.b16 [%0], %1;" ::"r"(buf + row_piece<128>(row, col >> 3) + (col & 7) * 2), "h"(bits)
+                           : "memory");
+            }
+          }
+        }
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const uint4 w = lds128(buf + row_piece<128>(lane, j));
+          const T* e = reinterpret_cast<const T*>(&w);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) v[8 * j + k] += to_f(e[k]);
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) sts128(buf + row_piece<128>(lane, j), pack8<T>(v + 8 * j));
+      __syncwarp();
+      rows_out<T, 128>(buf, static_cast<T*>(p.out) + m0 * p.ldo + n, p.ldo, nr, nc, p.vec_out, false, lane);
+      __syncwarp();
+    }
+  } else {
+    if (p.out_f32) {
+      float* out = static_cast<float*>(p.out) + split * p.split_stride + m0 * p.ldo;
+#pragma unroll 1
+      for (int c = 0; c < nhalf; c += 32) {
+        const int n = n0 + c;
+        const int nc = p.n - n < 32 ? p.n - n : 32;
+        if (nc <= 0) return;
+        uint32_t a[32];
+        tmem_ld32(taddr + c, a);
+        tmem_ld_wait32(a);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) st_shared_v4(buf + row_piece<128>(lane, j), a[4 * j], a[4 * j + 1], a[4 * j + 2], a[4 * j + 3]);
+        __syncwarp();
+        rows_out<float, 128>(buf, out + n, p.ldo, nr, nc, p.vec_out, p.accumulate, lane);
+        __syncwarp();
+      }
+    } else {
+      T* out = static_cast<T*>(p.out) + m0 * p.ldo;
+#pragma unroll 1
+      for (int c = 0; c < nhalf; c += 64) {
+        const int n = n0 + c;
+        const int nc = p.n - n < 64 ? p.n - n : 64;
+        if (nc <= 0) return;
+        uint32_t a[32], b[32];
+        tmem_ld32(taddr + c, a);
+        tmem_ld32(taddr + c + 32, b);
+        tmem_ld_wait2(a, b);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          sts128(buf + row_piece<128>(lane, j), pack8<T>(reinterpret_cast<const float*>(a) + 8 * j));
+          sts128(buf + row_piece<128>(lane, 4 + j), pack8<T>(reinterpret_cast<const float*>(b) + 8 * j));
+        }
+        __syncwarp();
+        rows_out<T, 128>(buf, out + n, p.ldo, nr, nc, p.vec_out, p.accumulate, lane);
+        __syncwarp();
+      }
     }
   }
 }
@@ -199,7 +428,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1) dense_pair_kernel(const __gr
   const int BN = p.BN, S = p.stages;
   const uint32_t l_bytes = 128 * 128, c_bytes = static_cast<uint32_t>(BN / 2) * 128;  // this CTA's halves
   const uint32_t stage_bytes = l_bytes + c_bytes;
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + S * stage_bytes);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + S * stage_bytes + kPairBuffers);
   uint64_t* empty = full + kDenseMaxStages;
   uint64_t* tfull = empty + kDenseMaxStages;
   uint64_t* tempty = tfull + 2;
@@ -307,33 +536,19 @@ __global__ void __launch_bounds__(kDenseThreads, 1) dense_pair_kernel(const __gr
   } else {
     // two warps per TMEM lane quarter, one per half of the columns
     const int q = warp & 3, half = (warp - 2) >> 2;
+    const uint32_t buf0 = sbase + S * stage_bytes + static_cast<uint32_t>(warp - 2) * 4096u;
     int tc = 0;
     for (int u = cid; u < units; u += ncl, ++tc) {
       int lt, ct, split;
       dense_unit(p, u, lt, ct, split);
-      const int n = lt * 256 + static_cast<int>(rank) * 128 + q * 32 + lane;
-      float lscale = 1.f, bias = 0.f;
-      if (EPI == kDenseForward && n < p.lanes) {
-        if (p.ls) lscale = q8_scale(p.ls[n]);
-        if (p.bias) bias = p.bias[n];
-      }
       const int buf = tc & 1;
       int ok = 1;
       if (lane == 0) ok = wait(&tfull[buf], (tc >> 1) & 1, p.err, kSiteDenseTFull) ? 1 : 0;
       if (!__shfl_sync(0xffffffffu, ok, 0)) break;
       tc_fence_after();
-      const uint32_t t0 = tmem + (static_cast<uint32_t>(q * 32) << 16) + buf * BN;
-      for (int c = half * (BN / 2); c < (half + 1) * (BN / 2); c += 32) {
-        const long m0 = static_cast<long>(ct) * BN + c;
-        if (m0 >= p.cols) break;  // uniform
-        uint32_t r[32];
-        tmem_ld32(t0 + c, r);
-        tmem_ld_wait32(r);
-        float v[32];
-#pragma unroll
-        for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(r[e]);
-        dense_epilogue<T, EPI, 32>(p, v, n, m0, split, lscale, bias);
-      }
+      pair_epilogue<T, EPI>(p, tmem + (static_cast<uint32_t>(q * 32) << 16) + buf * BN + half * (BN / 2), buf0,
+                            static_cast<long>(lt) * 256 + rank * 128 + q * 32, ct * BN + half * (BN / 2), BN / 2, split,
+                            lane);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
@@ -440,9 +655,9 @@ __global__ void __launch_bounds__(kDenseThreads, 1) dense_cluster_kernel(const _
   } else {
     const int q = warp & 3, half = (warp - 2) >> 2;
     const int n = lt * 128 + q * 32 + lane;
-    float lscale = 1.f, bias = 0.f;
-    if (EPI == kDenseForward && CL == 1 && n < p.lanes) {
-      if (p.ls) lscale = q8_scale(p.ls[n]);
+    float nscale = 1.f, bias = 0.f;
+    if (EPI == kDenseForward && CL == 1 && n < p.n) {
+      if (p.ns) nscale = q8_scale(p.ns[n]);
       if (p.bias) bias = p.bias[n];
     }
     int ok = 1;
@@ -453,7 +668,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1) dense_cluster_kernel(const _
       float* part = reinterpret_cast<float*>(smem);  // CL > 1: [BN][128] sums over the ring, which is drained
       for (int c = half * 16; c < BN; c += 32) {
         const long m0 = static_cast<long>(ct) * BN + c;
-        if (m0 >= p.cols) break;  // uniform
+        if (m0 >= p.m) break;  // uniform
         uint32_t r[16];
         tmem_ld16(t0 + c, r);
         tmem_ld_wait(r);
@@ -461,7 +676,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1) dense_cluster_kernel(const _
 #pragma unroll
         for (int e = 0; e < 16; ++e) v[e] = kb1 > kb0 ? __uint_as_float(r[e]) : 0.f;
         if (CL == 1) {
-          dense_epilogue<T, EPI, 16>(p, v, n, m0, split, lscale, bias);
+          dense_epilogue<T, EPI, 16>(p, v, n, m0, split, nscale, bias);
         } else {
 #pragma unroll
           for (int e = 0; e < 16; ++e) part[(c + e) * 128 + q * 32 + lane] = v[e];
@@ -473,14 +688,14 @@ __global__ void __launch_bounds__(kDenseThreads, 1) dense_cluster_kernel(const _
     __syncthreads();
     cluster_sync();  // every CTA's sums are written
     // jobs of 4 columns x 32 lanes, spread over the cluster's warps
-    const int nc = static_cast<int>(min(static_cast<long>(BN), p.cols - static_cast<long>(ct) * BN));
+    const int nc = static_cast<int>(min(static_cast<long>(BN), p.m - static_cast<long>(ct) * BN));
     const int jobs = (nc + 3) / 4 * 4;
     for (int j = rank + CL * warp; j < jobs; j += CL * (kDenseThreads / 32)) {
       const int q = j & 3, c = (j >> 2) * 4;
       const int n = lt * 128 + q * 32 + lane;
-      float lscale = 1.f, bias = 0.f;
-      if (EPI == kDenseForward && n < p.lanes) {
-        if (p.ls) lscale = q8_scale(p.ls[n]);
+      float nscale = 1.f, bias = 0.f;
+      if (EPI == kDenseForward && n < p.n) {
+        if (p.ns) nscale = q8_scale(p.ns[n]);
         if (p.bias) bias = p.bias[n];
       }
       float v[4] = {0.f, 0.f, 0.f, 0.f};
@@ -491,7 +706,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1) dense_cluster_kernel(const _
 #pragma unroll
         for (int e = 0; e < 4; ++e) v[e] += ld_shared_cluster_f32(at + e * 512);
       }
-      dense_epilogue<T, EPI, 4>(p, v, n, static_cast<long>(ct) * BN + c, split, lscale, bias);
+      dense_epilogue<T, EPI, 4>(p, v, n, static_cast<long>(ct) * BN + c, split, nscale, bias);
     }
     __syncthreads();
     cluster_sync();  // nobody reads this CTA's sums any more

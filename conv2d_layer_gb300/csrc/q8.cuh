@@ -116,7 +116,19 @@ __device__ __forceinline__ void q8_load(const uint8_t* p, float (&v)[V], float s
 // In fp32 to about 1e-6 relative (1e-5 where |z| is in the tens and the result tiny), in the forms that lose
 // nothing near zero or in the tails: the outputs are rounded to 16 bits, but the bias gradient sums the
 // derivatives in fp32.
-__device__ __forceinline__ float sigmoid_f(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kGelu2 = 1.5957691216057308f;  // 2 sqrt(2/pi)
+__device__ __forceinline__ float sigmoid_f(float x) { return rcp(1.f + ex2(-kLog2e * x)); }
 
 template <int A>
 __device__ __forceinline__ float dense_act(float z) {
@@ -126,14 +138,14 @@ __device__ __forceinline__ float dense_act(float z) {
     // (1 - e) / (1 + e) with e = exp(-2|z|) and z's sign
     const float a = fabsf(z), s = z * z;
     if (a < 0.25f) return z * (1.f + s * (-1.f / 3.f + s * (2.f / 15.f - s * (17.f / 315.f))));
-    const float e = __expf(-2.f * a);
-    return copysignf(__fdividef(1.f - e, 1.f + e), z);
+    const float e = ex2(-2.f * kLog2e * a);
+    return copysignf((1.f - e) * rcp(1.f + e), z);
   } else if constexpr (A == 3) return sigmoid_f(z);
   else if constexpr (A == 4) {
     // z/2 (1 + tanh u) = z / (1 + exp(-2u)); past |z| = 16 the factor is 0 or 1 to fp32 (clamped, so that
     // u does not overflow)
     const float c = z > 16.f ? 16.f : (z < -16.f ? -16.f : z);
-    return z * sigmoid_f(1.5957691216f * c * (1.f + 0.044715f * c * c));
+    return z * rcp(1.f + ex2(c * fmaf(c * c, -kLog2e * kGelu2 * 0.044715f, -kLog2e * kGelu2)));
   } else if constexpr (A == 5) return z * sigmoid_f(z);
   else return z;
 }
@@ -141,16 +153,16 @@ template <int A>
 __device__ __forceinline__ float dense_dact(float z) {
   if constexpr (A == 1) return z > 0.f ? 1.f : (z <= 0.f ? 0.f : z);
   else if constexpr (A == 2) {  // 1 - tanh^2 = 4 e / (1 + e)^2
-    const float e = __expf(-2.f * fabsf(z));
-    return __fdividef(4.f * e, (1.f + e) * (1.f + e));
+    const float e = ex2(-2.f * kLog2e * fabsf(z)), r = rcp(1.f + e);
+    return 4.f * e * r * r;
   } else if constexpr (A == 3) {  // s (1 - s) = e / (1 + e)^2, e = exp(-|z|)
-    const float e = __expf(-fabsf(z));
-    return __fdividef(e, (1.f + e) * (1.f + e));
+    const float e = ex2(-kLog2e * fabsf(z)), r = rcp(1.f + e);
+    return e * r * r;
   } else if constexpr (A == 4) {
     const float c = z > 16.f ? 16.f : (z < -16.f ? -16.f : z);
     const float q = c * c;
-    const float s = sigmoid_f(1.5957691216f * c * (1.f + 0.044715f * q));
-    return s + c * s * (1.f - s) * (1.5957691216f * (1.f + 0.134145f * q));
+    const float s = rcp(1.f + ex2(c * fmaf(q, -kLog2e * kGelu2 * 0.044715f, -kLog2e * kGelu2)));
+    return s + c * s * (1.f - s) * fmaf(q, 3.f * 0.044715f * kGelu2, kGelu2);
   } else if constexpr (A == 5) {
     const float c = z > 88.f ? 88.f : (z < -88.f ? -88.f : z);
     const float s = sigmoid_f(c);
