@@ -41,9 +41,10 @@ struct GemmPlan {
 
 // Kernel, tile, cluster size and splits by an estimate of each choice's clocks: a CTA's k-block takes the
 // larger of its MMA time (128 x BN x 64 products at 4,096 a clock, half a pair's) and of bringing its operand
-// tiles (about 64 bytes a clock); units run in waves over the SMs. can_split: the product may be split over k
-// with fp32 partials in the workspace (weight gradients); max_kb: bound on one accumulator's k-blocks (0: none).
-GemmPlan plan_gemm(long m, long n, int kb, bool r_mn, bool can_split, int max_kb, int sms) {
+// tiles (about 64 bytes a clock); units run in waves over the SMs. Weight gradients may be split over k, with fp32
+// partials in the workspace; max_kb: bound on one accumulator's k-blocks (0: none).
+GemmPlan plan_gemm(int mode, long m, long n, int kb, int max_kb, int sms) {
+  const bool r_mn = dense_r_mn(mode), c_mn = dense_c_mn(mode), can_split = mode == kDenseDw;
   GemmPlan best = {};
   double best_t = 1e300;
   auto consider = [&](bool pair, int BN, int cl, int splits) {
@@ -73,14 +74,16 @@ GemmPlan plan_gemm(long m, long n, int kb, bool r_mn, bool can_split, int max_kb
     }
   };
   for (int splits = 1; splits <= (can_split ? 512 : 1) && splits <= kb; splits += splits < 8 ? 1 : splits / 8) {
-    for (int BN : {256, 128}) consider(true, BN, 1, splits);
+    for (int BN : {256, 224, 192, 160, 128}) consider(true, BN, 1, splits);
     for (int BN : {128, 64, 32, 16}) {
       if (r_mn && BN < 64) continue;  // MN-major tiles are panels of 64
       for (int cl : {1, 2, 4, 8})
         if (cl == 1 || ceil_div(kb, splits) >= 2 * cl) consider(false, BN, cl, splits);
     }
   }
-  const int stage = 128 * 128 + (best.pair ? best.BN / 2 : best.BN) * 128;
+  int c_rows = best.BN;  // columns of C a CTA brings: MN-major in whole panels of 64
+  if (best.pair) c_rows = c_mn ? static_cast<int>(round_up(best.BN / 2, 64)) : best.BN / 2;
+  const int stage = (128 + c_rows) * 128 * (best.pair ? kPairKps : 1);
   const int room = static_cast<int>(kMaxDynSmem) - 1536 - (best.pair ? kPairBuffers : 0);
   const long units = static_cast<long>(best.l_tiles) * best.c_tiles * best.splits;
   if (best.pair) {
@@ -125,17 +128,16 @@ struct Operand {
   long rows, cols, ld;
 };
 
-// out[m][n] = sum_k R[m][k] C[n][k]; r_mn / c_mn: the operand lies with k along its rows. The rows of the output
-// are the accumulator's lanes in the pair kernel and its columns in the cluster kernel.
-int run_gemm(DenseGemmParams& p, const GemmPlan& g, const Operand& r, bool r_mn, const Operand& c, bool c_mn, int dt,
-             int epi, const char* name, const DevInfo* dev, cudaStream_t st) {
+// out[m][n] = sum_k R[m][k] C[n][k]. The rows of the output are the accumulator's lanes in the pair kernel and its
+// columns in the cluster kernel.
+int run_gemm(DenseGemmParams& p, const GemmPlan& g, const Operand& r, const Operand& c, int dt, int mode,
+             const char* name, const DevInfo* dev, cudaStream_t st) {
+  const bool r_mn = dense_r_mn(mode), c_mn = dense_c_mn(mode);
   const Operand &lo = g.pair ? r : c, &co = g.pair ? c : r;
-  p.l_mn = g.pair ? r_mn : c_mn;
-  p.c_mn = g.pair ? c_mn : r_mn;
-  if (!encode_operand(&p.tl, lo.data, lo.type, lo.rows, lo.cols, lo.ld, p.l_mn, 128) ||
-      !encode_operand(&p.tc, co.data, co.type, co.rows, co.cols, co.ld, p.c_mn, g.pair ? g.BN / 2 : g.BN))
+  if (!encode_operand(&p.tl, lo.data, lo.type, lo.rows, lo.cols, lo.ld, g.pair ? r_mn : c_mn, 128) ||
+      !encode_operand(&p.tc, co.data, co.type, co.rows, co.cols, co.ld, g.pair ? c_mn : r_mn, g.pair ? g.BN / 2 : g.BN))
     return CONV2D_ERR_CUDA;
-  p.fp8 = r.type == CONV2D_E4M3;
+  const bool fp8 = r.type == CONV2D_E4M3;
   p.fmt = r.type == CONV2D_BF16 ? 1u : 0u;
   p.m = r_mn ? r.cols : r.rows;
   p.n = static_cast<int>(c_mn ? c.cols : c.rows);
@@ -151,8 +153,8 @@ int run_gemm(DenseGemmParams& p, const GemmPlan& g, const Operand& r, bool r_mn,
   p.stages = g.stages;
   p.cluster = g.cluster;
   p.err = dev->err;
-  LAUNCH(name, st, g.pair ? launch_dense_pair(p, dt, epi, g.grid, g.smem, st)
-                          : launch_dense_cluster(p, dt, epi, g.grid, g.smem, st));
+  LAUNCH(name, st, g.pair ? launch_dense_pair(p, dt, mode, fp8, g.grid, g.smem, st)
+                          : launch_dense_cluster(p, dt, mode, fp8, g.grid, g.smem, st));
   return CONV2D_OK;
 }
 
@@ -222,7 +224,7 @@ void plan_fwd(const conv2d_dense_desc& d, const conv2d_mat* x, const conv2d_mat*
   pl->x = plan_copy(c, x, d.M, d.K, pl->fp8);
   pl->w = plan_copy(c, w, d.N, d.K, pl->fp8);
   pl->total = std::max<size_t>(c.total, 256);
-  pl->g = plan_gemm(d.M, d.N, static_cast<int>(ceil_div(d.K, pl->fp8 ? 128 : 64)), false, false, 0, sms);
+  pl->g = plan_gemm(kDenseForward, d.M, d.N, static_cast<int>(ceil_div(d.K, pl->fp8 ? 128 : 64)), 0, sms);
 }
 
 struct BwdPlan {
@@ -244,11 +246,11 @@ void plan_bwd(const conv2d_dense_desc& d, const conv2d_mat* x, const conv2d_mat*
   pl->w = pl->x = pl->spart = kNone;
   if (dx) {
     pl->w = plan_copy(c, w, d.N, d.K, false);
-    pl->gx = plan_gemm(d.M, d.K, static_cast<int>(ceil_div(d.N, 64)), false, false, 0, sms);
+    pl->gx = plan_gemm(kDenseDx, d.M, d.K, static_cast<int>(ceil_div(d.N, 64)), 0, sms);
   }
   if (dw) {
     pl->x = plan_copy(c, x, d.M, d.K, false);
-    pl->gw = plan_gemm(d.N, d.K, static_cast<int>(ceil_div(d.M, 64)), true, true,
+    pl->gw = plan_gemm(kDenseDw, d.N, d.K, static_cast<int>(ceil_div(d.M, 64)),
                        dw->type == CONV2D_FP32 ? kFp32SplitKb : 0, sms);
     if (pl->gw.splits > 1) pl->spart = c.take(static_cast<size_t>(pl->gw.splits) * d.N * d.K * 4);
   }
@@ -339,7 +341,7 @@ int conv2d_dense_fwd(const conv2d_dense_desc* d, const conv2d_mat* x, const conv
   }
   p.out = y->data;
   p.ldo = ld_of(y, d->N);
-  return run_gemm(p, pl.g, ox, false, ow, false, d->dtype, kDenseForward, "dense_fwd", dev, st);
+  return run_gemm(p, pl.g, ox, ow, d->dtype, kDenseForward, "dense_fwd", dev, st);
 }
 
 int conv2d_dense_bwd(const conv2d_dense_desc* d, const conv2d_mat* x, const conv2d_mat* w, const conv2d_mat* pre_act,
@@ -387,7 +389,7 @@ int conv2d_dense_bwd(const conv2d_dense_desc* d, const conv2d_mat* x, const conv
     DenseGemmParams p = {};
     p.out = dx->data;
     p.ldo = ld_of(dx, d->K);
-    if ((rc = run_gemm(p, pl.gx, odz, false, ow, true, d->dtype, kDenseStore, "dense_dx", dev, st))) return rc;
+    if ((rc = run_gemm(p, pl.gx, odz, ow, d->dtype, kDenseDx, "dense_dx", dev, st))) return rc;
   }
   if (dw) {
     Operand ox;
@@ -399,7 +401,7 @@ int conv2d_dense_bwd(const conv2d_dense_desc* d, const conv2d_mat* x, const conv
     p.out_f32 = joined || dw->type == CONV2D_FP32;
     p.accumulate = !joined && d->accumulate;
     p.split_stride = static_cast<long>(d->N) * d->K;
-    if ((rc = run_gemm(p, pl.gw, odz, true, ox, true, d->dtype, kDenseStore, "dense_dw", dev, st))) return rc;
+    if ((rc = run_gemm(p, pl.gw, odz, ox, d->dtype, kDenseDw, "dense_dw", dev, st))) return rc;
     if (joined)
       LAUNCH("dense_dw_join", st,
              launch_split_join(reinterpret_cast<float*>(base + pl.spart), pl.gw.splits, d->N, d->K, dw->type, dw->data,

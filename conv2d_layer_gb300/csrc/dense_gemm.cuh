@@ -25,16 +25,20 @@
 
 namespace c2d {
 
-constexpr int kDenseThreads = 320;  // TMA warp, MMA warp, 8 epilogue warps
+constexpr int kClusterThreads = 320;  // TMA warp, MMA warp, 8 epilogue warps
+constexpr int kPairWarps = 16;        // epilogue warps of the pair kernel: four for each TMEM lane quarter
+constexpr int kPairThreads = 64 + 32 * kPairWarps;
 constexpr int kDenseMaxStages = 10;
-constexpr int kPairBuffers = 8 * 4096;  // the pair kernel's epilogue: 4 KB a warp
+constexpr int kPairKps = 2;  // k-blocks per stage
+constexpr int kPairBuffers = kPairWarps * 2048;  // the pair kernel's epilogue: 32 rows x 64 bytes a warp
 enum : int { kSiteDenseFull = 11, kSiteDenseEmpty = 12, kSiteDenseTFull = 13, kSiteDenseTEmpty = 14 };
-enum : int { kDenseForward = 0, kDenseStore = 1 };  // epilogues
+// The three products: how the operands lie (R is MN-major for dW, C for dx and dW) and the epilogue.
+enum : int { kDenseForward = 0, kDenseDx = 1, kDenseDw = 2 };
+__host__ __device__ constexpr bool dense_r_mn(int mode) { return mode == kDenseDw; }
+__host__ __device__ constexpr bool dense_c_mn(int mode) { return mode != kDenseForward; }
 
 struct DenseGemmParams {
   CUtensorMap tl, tc;   // the operands whose rows are the accumulator's lanes / columns
-  int l_mn, c_mn;       // operand lies MN-major (its k index runs along memory rows)
-  int fp8;              // e4m3 operands (K-major only)
   uint32_t fmt;         // instruction descriptor's operand format: fp16 0, bf16 1, e4m3 0
   int n;                // columns of the output
   long m;               // rows of the output
@@ -50,7 +54,7 @@ struct DenseGemmParams {
   uint8_t *zq, *zs;
   int zg;  // scale bytes a row of zq
   long ldr, ldz;
-  // kDenseStore: out = acc (+ out): type T, or fp32 when out_f32; split s at out + s * split_stride
+  // kDenseDx, kDenseDw: out = acc (+ out): type T, or fp32 when out_f32; split s at out + s * split_stride
   int out_f32, accumulate;
   long split_stride;
   void* out;
@@ -84,12 +88,12 @@ __device__ __forceinline__ float ld_shared_cluster_f32(uint32_t caddr) {
 // ---------------------------------------------------------------- epilogue of the cluster kernel
 // NC rows of the output (m0 ..) of one column (n; off: past the end) a thread. Warp-collective (the 8-bit form
 // of z takes a maximum over the warp's 32 columns, which are one group).
-template <typename T, int EPI, int NC>
+template <typename T, int MODE, int NC>
 __device__ __forceinline__ void dense_epilogue(const DenseGemmParams& p, float (&v)[NC], int n, long m0, int split,
                                                float nscale, float bias) {
   const int nc = static_cast<int>(p.m - m0 < NC ? p.m - m0 : NC);  // uniform
   const bool on = n < p.n;
-  if constexpr (EPI == kDenseForward) {
+  if constexpr (MODE == kDenseForward) {
     T res[NC];
     if (p.res) {
       const T* r = static_cast<const T*>(p.res) + m0 * p.ldr + n;
@@ -142,12 +146,12 @@ __device__ __forceinline__ void dense_epilogue(const DenseGemmParams& p, float (
 }
 
 // ---------------------------------------------------------------- epilogue of the pair kernel
-// A warp's buffer of 32 rows x RB bytes (64 or 128) in shared memory; 16-byte pieces are swizzled so that a
-// thread's own row and the warp's whole lines are both accessed without bank conflicts.
+// A warp's buffer of 32 rows x RB bytes (64 or 32) in shared memory; 16-byte pieces are swizzled so that a
+// thread's own row and the warp's whole rows are both accessed without bank conflicts.
 template <int RB>
 __device__ __forceinline__ uint32_t row_piece(int r, int j) {
-  return RB == 128 ? static_cast<uint32_t>(r * 128 + ((j ^ (r & 7)) << 4))
-                   : static_cast<uint32_t>(r * 64 + ((j ^ ((r >> 1) & 3)) << 4));
+  return RB == 64 ? static_cast<uint32_t>(r * 64 + ((j ^ ((r >> 1) & 3)) << 4))
+                  : static_cast<uint32_t>(r * 32 + ((j ^ ((r >> 2) & 1)) << 4));
 }
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
   uint4 v;
@@ -156,7 +160,7 @@ __device__ __forceinline__ uint4 lds128(uint32_t a) {
 }
 __device__ __forceinline__ void sts128(uint32_t a, const uint4& v) { st_shared_v4(a, v.x, v.y, v.z, v.w); }
 
-// The buffer's rows (nr of them) x nc elements of type E to memory at g (row length ld), whole lines at a
+// The buffer's rows (nr of them) x nc elements of type E to memory at g (row length ld), whole row segments at a
 // time; vec: rows start on 16-byte boundaries. accumulate: added to what is there (in fp32).
 template <typename E, int RB>
 __device__ __forceinline__ void rows_out(uint32_t buf, E* g, long ld, int nr, int nc, bool vec, bool accumulate,
@@ -165,12 +169,12 @@ __device__ __forceinline__ void rows_out(uint32_t buf, E* g, long ld, int nr, in
   constexpr int RI = 32 / PR;                                         // rows an instruction
   const int j = lane % PR;
   const bool whole = vec && (j + 1) * PE <= nc;
+  E* o = g + (lane / PR) * ld + j * PE;
 #pragma unroll
-  for (int i = 0; i < 32 / RI; ++i) {
+  for (int i = 0; i < 32 / RI; ++i, o += RI * ld) {
     const int r = i * RI + lane / PR;
     if (r >= nr || j * PE >= nc) continue;
     uint4 w = lds128(buf + row_piece<RB>(r, j));
-    E* o = g + r * ld + j * PE;
     if constexpr (sizeof(E) > 1) {
       if (accumulate) {
         E* e = reinterpret_cast<E*>(&w);
@@ -206,166 +210,152 @@ __device__ __forceinline__ uint4 pack8(const float* v) {
   return w;
 }
 
-// A warp's 32 rows (m0 ..) x nhalf columns (n0 ..; a multiple of 64) of the accumulator at taddr.
-template <typename T, int EPI>
-__device__ __forceinline__ void pair_epilogue(const DenseGemmParams& p, uint32_t taddr, uint32_t buf, long m0, int n0,
-                                              int nhalf, int split, int lane) {
-  const int nr = static_cast<int>(p.m - m0 < 32 ? p.m - m0 : 32);
-  if (nr <= 0) return;  // uniform
-  if constexpr (EPI == kDenseForward) {
-    const float mscale = p.ms && lane < nr ? q8_scale(p.ms[m0 + lane]) : 1.f;
-#pragma unroll 1
-    for (int c = 0; c < nhalf; c += 64) {
-      const int n = n0 + c;
-      const int nc = p.n - n < 64 ? p.n - n : 64;
-      if (nc <= 0) return;
-      // the residual's lines are in flight while the sums are read and activated
-      uint4 res[8];
-      const int rj = lane & 7;
-      if (p.res && p.vec_res) {
-        const T* r = static_cast<const T*>(p.res) + m0 * p.ldr + n + rj * 8;
+// A warp's 32 rows (m0 ..) x up to 32 columns (n ..) of the accumulator at taddr; nr rows and nc columns count.
+template <typename T, int MODE>
+__device__ __forceinline__ void pair_epilogue(const DenseGemmParams& p, uint32_t taddr, uint32_t buf, long m0, int n,
+                                              int nr, int nc, int split, float mscale, int lane) {
+  if constexpr (MODE == kDenseForward) {
+    // the residual's rows are in flight while the sums are read and activated
+    uint4 res[4];
+    const int rj = lane & 3;
+    const bool vres = p.vec_res && nc == 32;
+    if (p.res && vres) {
+      const T* r = static_cast<const T*>(p.res) + (m0 + (lane >> 2)) * p.ldr + n + rj * 8;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int row = i * 4 + (lane >> 3);
-          if (row < nr && (rj + 1) * 8 <= nc) res[i] = *reinterpret_cast<const uint4*>(r + row * p.ldr);
+      for (int i = 0; i < 4; ++i)
+        if (i * 8 + (lane >> 2) < nr) res[i] = *reinterpret_cast<const uint4*>(r + i * 8 * p.ldr);
+    }
+    float v[32];
+    {
+      uint32_t a[32];
+      tmem_ld32(taddr, a);
+      tmem_ld_wait32(a);
+#pragma unroll
+      for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(a[e]);
+    }
+    if (p.ns) {
+#pragma unroll
+      for (int e = 0; e < 32; ++e)
+        if (e < nc) v[e] = v[e] * q8_scale(p.ns[n + e]) * mscale;
+    }
+    if (p.bias) {
+      if (nc == 32) {
+#pragma unroll
+        for (int e = 0; e < 32; e += 4) {
+          const float4 b = *reinterpret_cast<const float4*>(p.bias + n + e);
+          v[e] += b.x;
+          v[e + 1] += b.y;
+          v[e + 2] += b.z;
+          v[e + 3] += b.w;
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 32; ++e)
+          if (e < nc) v[e] += p.bias[n + e];
+      }
+    }
+    if (p.zq) {
+      // The largest magnitude: fmaxf passes NaN over; only where an infinity is among the values are they
+      // looked at one by one.
+      float top = 0.f;
+      if (nc == 32) {
+#pragma unroll
+        for (int e = 0; e < 32; ++e) top = fmaxf(top, fabsf(v[e]));
+      } else {
+#pragma unroll
+        for (int e = 0; e < 32; ++e) top = e < nc ? fmaxf(top, fabsf(v[e])) : top;
+      }
+      uint32_t bits = __float_as_uint(top);
+      float inf0 = 0.f;  // times an infinity: NaN
+      if (bits == 0x7f800000u) {
+        bits = 0u;
+        for (int e = 0; e < 32; ++e)
+          if (e < nc) bits = max(bits, finite_bits(v[e]));
+        inf0 = 1.f;
+      }
+      const uint32_t byte = q8_scale_byte(bits);
+      const float inv = q8_inv_scale(byte);
+      if (lane < nr) p.zs[(m0 + lane) * p.zg + n / kQ8Group] = static_cast<uint8_t>(byte);
+      uint32_t w[8];
+      if (inf0 == 0.f) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float* x = v + 4 * e;
+          w[e] = q8_pack2_finite(x[0] * inv, x[1] * inv) | q8_pack2_finite(x[2] * inv, x[3] * inv) << 16;
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float* x = v + 4 * e;
+          w[e] = q8_pack2(x[0] * inv, x[1] * inv) | q8_pack2(x[2] * inv, x[3] * inv) << 16;
         }
       }
-      float v[64];
-      {
-        uint32_t a[32], b[32];
-        tmem_ld32(taddr + c, a);
-        tmem_ld32(taddr + c + 32, b);
-        tmem_ld_wait2(a, b);
-#pragma unroll
-        for (int e = 0; e < 32; ++e) {
-          v[e] = __uint_as_float(a[e]);
-          v[32 + e] = __uint_as_float(b[e]);
-        }
-      }
-      if (p.ns) {
-#pragma unroll
-        for (int e = 0; e < 64; ++e)
-          if (e < nc) v[e] = v[e] * q8_scale(p.ns[n + e]) * mscale;
-      }
-      if (p.bias) {
-        if (nc == 64) {
-#pragma unroll
-          for (int e = 0; e < 64; e += 4) {
-            const float4 b = *reinterpret_cast<const float4*>(p.bias + n + e);
-            v[e] += b.x;
-            v[e + 1] += b.y;
-            v[e + 2] += b.z;
-            v[e + 3] += b.w;
-          }
-        } else {
-#pragma unroll
-          for (int e = 0; e < 64; ++e)
-            if (e < nc) v[e] += p.bias[n + e];
-        }
-      }
-      if (p.zq) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          if (h * 32 >= nc) break;  // uniform
-          uint32_t top = 0u;
-#pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            const uint32_t b = finite_bits(v[32 * h + e]);
-            if (32 * h + e < nc) top = max(top, b);
-          }
-          const uint32_t byte = q8_scale_byte(top);
-          const float inv = q8_inv_scale(byte);
-          if (lane < nr) p.zs[(m0 + lane) * p.zg + n / kQ8Group + h] = static_cast<uint8_t>(byte);
-          uint32_t w[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float* x = v + 32 * h + 4 * e;
-            w[e] = q8_pack2(x[0] * inv, x[1] * inv) | q8_pack2(x[2] * inv, x[3] * inv) << 16;
-          }
-          st_shared_v4(buf + row_piece<64>(lane, 2 * h), w[0], w[1], w[2], w[3]);
-          st_shared_v4(buf + row_piece<64>(lane, 2 * h + 1), w[4], w[5], w[6], w[7]);
-        }
-        __syncwarp();
-        rows_out<uint8_t, 64>(buf, p.zq + m0 * p.ldz + n, p.ldz, nr, nc, p.vec_z, false, lane);
-        __syncwarp();
-      } else if (p.z) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) sts128(buf + row_piece<128>(lane, j), pack8<T>(v + 8 * j));
-        __syncwarp();
-        rows_out<T, 128>(buf, static_cast<T*>(p.z) + m0 * p.ldz + n, p.ldz, nr, nc, p.vec_z, false, lane);
-        __syncwarp();
-      }
-      with_dense_act(p.act, [&](auto act) {
-#pragma unroll
-        for (int e = 0; e < 64; ++e) v[e] = dense_act<decltype(act)::value>(v[e]);
-      });
-      if (p.res) {
-        if (p.vec_res && nc == 64) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) sts128(buf + row_piece<128>(i * 4 + (lane >> 3), rj), res[i]);
-        } else {
-          for (int i = lane; i < 32 * 64; i += 32) {
-            const int row = i >> 6, col = i & 63;
-            if (row < nr && col < nc) {
-              const T x = static_cast<const T*>(p.res)[(m0 + row) * p.ldr + n + col];
-              uint16_t bits = *reinterpret_cast<const uint16_t*>(&x);
-              asm volatile("st.shared.b16 [%0], %1;" ::"r"(buf + row_piece<128>(row, col >> 3) + (col & 7) * 2), "h"(bits)
-                           : "memory");
-            }
-          }
-        }
-        __syncwarp();
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const uint4 w = lds128(buf + row_piece<128>(lane, j));
-          const T* e = reinterpret_cast<const T*>(&w);
-#pragma unroll
-          for (int k = 0; k < 8; ++k) v[8 * j + k] += to_f(e[k]);
-        }
-      }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) sts128(buf + row_piece<128>(lane, j), pack8<T>(v + 8 * j));
+      st_shared_v4(buf + row_piece<32>(lane, 0), w[0], w[1], w[2], w[3]);
+      st_shared_v4(buf + row_piece<32>(lane, 1), w[4], w[5], w[6], w[7]);
       __syncwarp();
-      rows_out<T, 128>(buf, static_cast<T*>(p.out) + m0 * p.ldo + n, p.ldo, nr, nc, p.vec_out, false, lane);
+      rows_out<uint8_t, 32>(buf, p.zq + m0 * p.ldz + n, p.ldz, nr, nc, p.vec_z, false, lane);
+      __syncwarp();
+    } else if (p.z) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) sts128(buf + row_piece<64>(lane, j), pack8<T>(v + 8 * j));
+      __syncwarp();
+      rows_out<T, 64>(buf, static_cast<T*>(p.z) + m0 * p.ldz + n, p.ldz, nr, nc, p.vec_z, false, lane);
       __syncwarp();
     }
-  } else {
-    if (p.out_f32) {
-      float* out = static_cast<float*>(p.out) + split * p.split_stride + m0 * p.ldo;
-#pragma unroll 1
-      for (int c = 0; c < nhalf; c += 32) {
-        const int n = n0 + c;
-        const int nc = p.n - n < 32 ? p.n - n : 32;
-        if (nc <= 0) return;
-        uint32_t a[32];
-        tmem_ld32(taddr + c, a);
-        tmem_ld_wait32(a);
+    with_dense_act(p.act, [&](auto act) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) st_shared_v4(buf + row_piece<128>(lane, j), a[4 * j], a[4 * j + 1], a[4 * j + 2], a[4 * j + 3]);
+      for (int e = 0; e < 32; ++e) v[e] = dense_act<decltype(act)::value>(v[e]);
+    });
+    if (p.res) {
+      if (vres) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sts128(buf + row_piece<64>(i * 8 + (lane >> 2), rj), res[i]);
+      } else {
+        for (int row = 0; row < nr; ++row) {
+          if (lane >= nc) continue;
+          const T x = static_cast<const T*>(p.res)[(m0 + row) * p.ldr + n + lane];
+          asm volatile("st.shared.b16 [%0], %1;" ::"r"(buf + row_piece<64>(row, lane >> 3) + (lane & 7) * 2),
+                       "h"(*reinterpret_cast<const uint16_t*>(&x))
+                       : "memory");
+        }
+      }
+      __syncwarp();
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint4 w = lds128(buf + row_piece<64>(lane, j));
+        const T* e = reinterpret_cast<const T*>(&w);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[8 * j + k] += to_f(e[k]);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) sts128(buf + row_piece<64>(lane, j), pack8<T>(v + 8 * j));
+    __syncwarp();
+    rows_out<T, 64>(buf, static_cast<T*>(p.out) + m0 * p.ldo + n, p.ldo, nr, nc, p.vec_out, false, lane);
+    __syncwarp();
+  } else {
+    uint32_t a[32];
+    tmem_ld32(taddr, a);
+    tmem_ld_wait32(a);
+    if (p.out_f32) {
+      float* out = static_cast<float*>(p.out) + split * p.split_stride + m0 * p.ldo + n;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if (16 * h >= nc) break;  // uniform
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          st_shared_v4(buf + row_piece<64>(lane, j), a[16 * h + 4 * j], a[16 * h + 4 * j + 1], a[16 * h + 4 * j + 2],
+                       a[16 * h + 4 * j + 3]);
         __syncwarp();
-        rows_out<float, 128>(buf, out + n, p.ldo, nr, nc, p.vec_out, p.accumulate, lane);
+        rows_out<float, 64>(buf, out + 16 * h, p.ldo, nr, nc - 16 * h, p.vec_out, p.accumulate, lane);
         __syncwarp();
       }
     } else {
-      T* out = static_cast<T*>(p.out) + m0 * p.ldo;
-#pragma unroll 1
-      for (int c = 0; c < nhalf; c += 64) {
-        const int n = n0 + c;
-        const int nc = p.n - n < 64 ? p.n - n : 64;
-        if (nc <= 0) return;
-        uint32_t a[32], b[32];
-        tmem_ld32(taddr + c, a);
-        tmem_ld32(taddr + c + 32, b);
-        tmem_ld_wait2(a, b);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          sts128(buf + row_piece<128>(lane, j), pack8<T>(reinterpret_cast<const float*>(a) + 8 * j));
-          sts128(buf + row_piece<128>(lane, 4 + j), pack8<T>(reinterpret_cast<const float*>(b) + 8 * j));
-        }
-        __syncwarp();
-        rows_out<T, 128>(buf, out + n, p.ldo, nr, nc, p.vec_out, p.accumulate, lane);
-        __syncwarp();
-      }
+      for (int j = 0; j < 4; ++j) sts128(buf + row_piece<64>(lane, j), pack8<T>(reinterpret_cast<const float*>(a) + 8 * j));
+      __syncwarp();
+      rows_out<T, 64>(buf, static_cast<T*>(p.out) + m0 * p.ldo + n, p.ldo, nr, nc, p.vec_out, p.accumulate, lane);
+      __syncwarp();
     }
   }
 }
@@ -373,10 +363,10 @@ __device__ __forceinline__ void pair_epilogue(const DenseGemmParams& p, uint32_t
 // ---------------------------------------------------------------- operands
 // One k-block of an operand's `rows` rows from row r0 into shared memory at dst. K-major: one box of 128
 // bytes x rows. MN-major: panels of 64 rows (128 bytes) x 64 k, 8 KB each.
-template <bool PAIR>
-__device__ __forceinline__ void dense_load(const CUtensorMap* m, uint32_t dst, uint64_t* bar, uint32_t pbar, bool mn,
-                                           int kelem, int r0, int rows) {
-  if (mn) {
+template <bool PAIR, bool MN>
+__device__ __forceinline__ void dense_load(const CUtensorMap* m, uint32_t dst, uint64_t* bar, uint32_t pbar, int kelem,
+                                           int r0, int rows) {
+  if (MN) {
     for (int j = 0; j < rows; j += 64) {
       if (PAIR) tma_load_2d_pair(dst + j * 128, m, pbar, r0 + j, kelem);
       else tma_load_2d(dst + j * 128, m, bar, r0 + j, kelem);
@@ -386,23 +376,27 @@ __device__ __forceinline__ void dense_load(const CUtensorMap* m, uint32_t dst, u
     else tma_load_2d(dst, m, bar, kelem, r0);
   }
 }
-// The four MMAs of a k-block (32 bytes of k each: 16 16-bit or 32 8-bit elements).
-template <bool PAIR>
-__device__ __forceinline__ void dense_mma(const DenseGemmParams& p, uint32_t d, uint32_t l0, uint32_t c0,
-                                          uint32_t idesc, bool first) {
-  const uint32_t lstep = p.l_mn ? 2048u : 32u, cstep = p.c_mn ? 2048u : 32u;
-  const uint32_t llbo = p.l_mn ? 8192u : 16u, clbo = p.c_mn ? 8192u : 16u;
+// Descriptor of the ring's first tile of an operand. A stage, a k-block and a 32-byte step of k are added to
+// its address field (units of 16 bytes; the ring lies below 256 KB, so nothing carries into the next field):
+// what the issuing thread does between two MMAs is time that the tensor core may stand still (making the
+// descriptors anew for each MMA, with the layouts as variables, took 9728 x 2048 x 8192 from 179 to 210 us).
+template <bool MN>
+__device__ __forceinline__ uint64_t dense_desc(uint32_t addr) {
+  return sdesc_sw128(addr, MN ? 8192u : 16u, 1024);
+}
+// The MMAs of the k-block `offset` bytes into the ring: four of 32 bytes of k (16 16-bit or 32 8-bit elements).
+template <bool PAIR, bool FP8, bool LMN, bool CMN>
+__device__ __forceinline__ void dense_mma(uint64_t l, uint64_t c, uint32_t d, uint32_t offset, uint32_t idesc,
+                                          uint32_t acc) {
 #pragma unroll
   for (int kk = 0; kk < 4; ++kk) {
-    const uint64_t a = sdesc_sw128(l0 + kk * lstep, llbo, 1024);
-    const uint64_t b = sdesc_sw128(c0 + kk * cstep, clbo, 1024);
-    const uint32_t acc = first && kk == 0 ? 0u : 1u;
-    if (p.fp8) {
-      if (PAIR) mma_f8_pair(d, a, b, idesc, acc);
-      else mma_f8(d, a, b, idesc, acc);
+    const uint64_t a = l + (offset >> 4) + kk * (LMN ? 128 : 2), b = c + (offset >> 4) + kk * (CMN ? 128 : 2);
+    if (FP8) {
+      if (PAIR) mma_f8_pair(d, a, b, idesc, kk ? 1u : acc);
+      else mma_f8(d, a, b, idesc, kk ? 1u : acc);
     } else {
-      if (PAIR) mma_bf16_pair(d, a, b, idesc, acc);
-      else mma_bf16(d, a, b, idesc, acc);
+      if (PAIR) mma_bf16_pair(d, a, b, idesc, kk ? 1u : acc);
+      else mma_bf16(d, a, b, idesc, kk ? 1u : acc);
     }
   }
 }
@@ -421,13 +415,16 @@ __device__ __forceinline__ void dense_unit(const DenseGemmParams& p, int u, int&
   lt = l0 + i - ct * h;
 }
 
-template <typename T, int EPI>
-__global__ void __launch_bounds__(kDenseThreads, 1) dense_pair_kernel(const __grid_constant__ DenseGemmParams p) {
+template <typename T, int MODE, bool FP8>
+__global__ void __launch_bounds__(kPairThreads, 1) dense_pair_kernel(const __grid_constant__ DenseGemmParams p) {
+  constexpr bool RMN = dense_r_mn(MODE), CMN = dense_c_mn(MODE);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int BN = p.BN, S = p.stages;
-  const uint32_t l_bytes = 128 * 128, c_bytes = static_cast<uint32_t>(BN / 2) * 128;  // this CTA's halves
-  const uint32_t stage_bytes = l_bytes + c_bytes;
+  // this CTA's halves: 128 rows and BN / 2 columns (whole panels of 64 when MN-major)
+  const int c_rows = CMN ? (BN / 2 + 63) & ~63 : BN / 2;
+  const uint32_t l_bytes = 128 * 128, c_bytes = static_cast<uint32_t>(c_rows) * 128;
+  const uint32_t sub_bytes = l_bytes + c_bytes, stage_bytes = kPairKps * sub_bytes;
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + S * stage_bytes + kPairBuffers);
   uint64_t* empty = full + kDenseMaxStages;
   uint64_t* tfull = empty + kDenseMaxStages;
@@ -448,7 +445,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1) dense_pair_kernel(const __gr
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&tfull[b], 1);
-      mbar_init(&tempty[b], 16);  // one arrival per epilogue warp of both CTAs
+      mbar_init(&tempty[b], 2 * kPairWarps);  // one arrival per epilogue warp of both CTAs
     }
     fence_mbar_init();
     tma_prefetch_desc(&p.tl);
@@ -470,23 +467,28 @@ __global__ void __launch_bounds__(kDenseThreads, 1) dense_pair_kernel(const __gr
       int s = 0;
       uint32_t par = 0;
       bool alive = true;
-      const int kelems = p.fp8 ? 128 : 64;
+      const int kelems = FP8 ? 128 : 64;
       for (int u = cid; u < units && alive; u += ncl) {
         int lt, ct, split;
         dense_unit(p, u, lt, ct, split);
         const int kb0 = split * p.kb_per_split, kb1 = min(p.kb_total, kb0 + p.kb_per_split);
         const int lr = lt * 256 + static_cast<int>(rank) * 128, cr = ct * BN + static_cast<int>(rank) * (BN / 2);
-        for (int kb = kb0; kb < kb1; ++kb) {
+        for (int kb = kb0; kb < kb1; kb += kPairKps) {
+          const int nk = min(kPairKps, kb1 - kb);
           if (!wait(&empty[s], par ^ 1, p.err, kSiteDenseEmpty)) {
             alive = false;
             break;
           }
           // both members' loads complete on the even CTA's barrier, which expects them all
           const uint32_t bar = mapa_shared(smem_u32(&full[s]), 0);
-          if (leader) mbar_arrive_expect_tx(&full[s], 2 * stage_bytes);
-          const uint32_t l0 = sbase + s * stage_bytes;
-          dense_load<true>(&p.tl, l0, nullptr, bar, p.l_mn, kb * kelems, lr, 128);
-          dense_load<true>(&p.tc, l0 + l_bytes, nullptr, bar, p.c_mn, kb * kelems, cr, BN / 2);
+          if (leader) mbar_arrive_expect_tx(&full[s], 2 * nk * sub_bytes);
+#pragma unroll
+          for (int i = 0; i < kPairKps; ++i) {
+            if (i >= nk) break;
+            const uint32_t l0 = sbase + s * stage_bytes + i * sub_bytes;
+            dense_load<true, RMN>(&p.tl, l0, nullptr, bar, (kb + i) * kelems, lr, 128);
+            dense_load<true, CMN>(&p.tc, l0 + l_bytes, nullptr, bar, (kb + i) * kelems, cr, c_rows);
+          }
           if (++s == S) {
             s = 0;
             par ^= 1;
@@ -505,7 +507,8 @@ __global__ void __launch_bounds__(kDenseThreads, 1) dense_pair_kernel(const __gr
     }
   } else if (warp == 1) {
     if (lane == 0 && leader) {
-      const uint32_t idesc = idesc_f32acc(256, BN, p.fmt, p.l_mn, p.c_mn);
+      const uint32_t idesc = idesc_f32acc(256, BN, p.fmt, RMN, CMN);
+      const uint64_t l = dense_desc<RMN>(sbase), c = dense_desc<CMN>(sbase + l_bytes);
       int s = 0, tc = 0;
       uint32_t par = 0;
       bool alive = true;
@@ -516,14 +519,18 @@ __global__ void __launch_bounds__(kDenseThreads, 1) dense_pair_kernel(const __gr
         const int buf = tc & 1;
         if (!wait(&tempty[buf], ((tc >> 1) & 1) ^ 1, p.err, kSiteDenseTEmpty)) break;
         tc_fence_after();
-        for (int kb = kb0; kb < kb1; ++kb) {
+        for (int kb = kb0; kb < kb1; kb += kPairKps) {
+          const int nk = min(kPairKps, kb1 - kb);
           if (!wait(&full[s], par, p.err, kSiteDenseFull)) {
             alive = false;
             break;
           }
           tc_fence_after();
-          const uint32_t l0 = sbase + s * stage_bytes;
-          dense_mma<true>(p, tmem + buf * BN, l0, l0 + l_bytes, idesc, kb == kb0);
+#pragma unroll
+          for (int i = 0; i < kPairKps; ++i) {
+            if (i >= nk) break;
+            dense_mma<true, FP8, RMN, CMN>(l, c, tmem + buf * BN, s * stage_bytes + i * sub_bytes, idesc, kb + i > kb0);
+          }
           mma_commit_pair(&empty[s]);
           if (++s == S) {
             s = 0;
@@ -534,9 +541,9 @@ __global__ void __launch_bounds__(kDenseThreads, 1) dense_pair_kernel(const __gr
       }
     }
   } else {
-    // two warps per TMEM lane quarter, one per half of the columns
-    const int q = warp & 3, half = (warp - 2) >> 2;
-    const uint32_t buf0 = sbase + S * stage_bytes + static_cast<uint32_t>(warp - 2) * 4096u;
+    // four warps per TMEM lane quarter, which take the unit's columns 32 at a time in turn
+    const int q = warp & 3, part = (warp - 2) >> 2;
+    const uint32_t buf0 = sbase + S * stage_bytes + static_cast<uint32_t>(warp - 2) * 2048u;
     int tc = 0;
     for (int u = cid; u < units; u += ncl, ++tc) {
       int lt, ct, split;
@@ -546,9 +553,16 @@ __global__ void __launch_bounds__(kDenseThreads, 1) dense_pair_kernel(const __gr
       if (lane == 0) ok = wait(&tfull[buf], (tc >> 1) & 1, p.err, kSiteDenseTFull) ? 1 : 0;
       if (!__shfl_sync(0xffffffffu, ok, 0)) break;
       tc_fence_after();
-      pair_epilogue<T, EPI>(p, tmem + (static_cast<uint32_t>(q * 32) << 16) + buf * BN + half * (BN / 2), buf0,
-                            static_cast<long>(lt) * 256 + rank * 128 + q * 32, ct * BN + half * (BN / 2), BN / 2, split,
-                            lane);
+      const long m0 = static_cast<long>(lt) * 256 + rank * 128 + q * 32;
+      const int nr = static_cast<int>(min(p.m - m0, 32L));
+      const float mscale = MODE == kDenseForward && p.ms && lane < nr ? q8_scale(p.ms[m0 + lane]) : 1.f;
+      const int end = min(p.n, ct * BN + BN);
+      if (nr > 0) {  // uniform
+#pragma unroll 1
+        for (int n = ct * BN + part * 32; n < end; n += 128)
+          pair_epilogue<T, MODE>(p, tmem + (static_cast<uint32_t>(q * 32) << 16) + buf * BN + (n - ct * BN), buf0, m0, n,
+                                 nr, min(end - n, 32), split, mscale, lane);
+      }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
@@ -566,8 +580,9 @@ __global__ void __launch_bounds__(kDenseThreads, 1) dense_pair_kernel(const __gr
   }
 }
 
-template <typename T, int EPI>
-__global__ void __launch_bounds__(kDenseThreads, 1) dense_cluster_kernel(const __grid_constant__ DenseGemmParams p) {
+template <typename T, int MODE, bool FP8>
+__global__ void __launch_bounds__(kClusterThreads, 1) dense_cluster_kernel(const __grid_constant__ DenseGemmParams p) {
+  constexpr bool LMN = dense_c_mn(MODE), CMN = dense_r_mn(MODE);  // the lanes are the output's columns
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int BN = p.BN, S = p.stages, CL = p.cluster;
@@ -613,14 +628,14 @@ __global__ void __launch_bounds__(kDenseThreads, 1) dense_cluster_kernel(const _
     if (lane == 0) {
       int s = 0;
       uint32_t par = 0;
-      const int kelems = p.fp8 ? 128 : 64;
+      const int kelems = FP8 ? 128 : 64;
       int kb = kb0;
       for (; kb < kb1; ++kb) {
         if (!wait(&empty[s], par ^ 1, p.err, kSiteDenseEmpty)) break;
         mbar_arrive_expect_tx(&full[s], stage_bytes);
         const uint32_t l0 = sbase + s * stage_bytes;
-        dense_load<false>(&p.tl, l0, &full[s], 0u, p.l_mn, kb * kelems, lt * 128, 128);
-        dense_load<false>(&p.tc, l0 + l_bytes, &full[s], 0u, p.c_mn, kb * kelems, ct * BN, BN);
+        dense_load<false, LMN>(&p.tl, l0, &full[s], 0u, kb * kelems, lt * 128, 128);
+        dense_load<false, CMN>(&p.tc, l0 + l_bytes, &full[s], 0u, kb * kelems, ct * BN, BN);
         if (++s == S) {
           s = 0;
           par ^= 1;
@@ -635,14 +650,14 @@ __global__ void __launch_bounds__(kDenseThreads, 1) dense_cluster_kernel(const _
     }
   } else if (warp == 1) {
     if (lane == 0) {
-      const uint32_t idesc = idesc_f32acc(128, BN, p.fmt, p.l_mn, p.c_mn);
+      const uint32_t idesc = idesc_f32acc(128, BN, p.fmt, LMN, CMN);
+      const uint64_t l = dense_desc<LMN>(sbase), c = dense_desc<CMN>(sbase + l_bytes);
       int s = 0;
       uint32_t par = 0;
       for (int kb = kb0; kb < kb1; ++kb) {
         if (!wait(&full[s], par, p.err, kSiteDenseFull)) break;
         tc_fence_after();
-        const uint32_t l0 = sbase + s * stage_bytes;
-        dense_mma<false>(p, tmem, l0, l0 + l_bytes, idesc, kb == kb0);
+        dense_mma<false, FP8, LMN, CMN>(l, c, tmem, s * stage_bytes, idesc, kb > kb0);
         mma_commit(&empty[s]);
         if (++s == S) {
           s = 0;
@@ -656,7 +671,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1) dense_cluster_kernel(const _
     const int q = warp & 3, half = (warp - 2) >> 2;
     const int n = lt * 128 + q * 32 + lane;
     float nscale = 1.f, bias = 0.f;
-    if (EPI == kDenseForward && CL == 1 && n < p.n) {
+    if (MODE == kDenseForward && CL == 1 && n < p.n) {
       if (p.ns) nscale = q8_scale(p.ns[n]);
       if (p.bias) bias = p.bias[n];
     }
@@ -676,7 +691,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1) dense_cluster_kernel(const _
 #pragma unroll
         for (int e = 0; e < 16; ++e) v[e] = kb1 > kb0 ? __uint_as_float(r[e]) : 0.f;
         if (CL == 1) {
-          dense_epilogue<T, EPI, 16>(p, v, n, m0, split, nscale, bias);
+          dense_epilogue<T, MODE, 16>(p, v, n, m0, split, nscale, bias);
         } else {
 #pragma unroll
           for (int e = 0; e < 16; ++e) part[(c + e) * 128 + q * 32 + lane] = v[e];
@@ -690,11 +705,11 @@ __global__ void __launch_bounds__(kDenseThreads, 1) dense_cluster_kernel(const _
     // jobs of 4 columns x 32 lanes, spread over the cluster's warps
     const int nc = static_cast<int>(min(static_cast<long>(BN), p.m - static_cast<long>(ct) * BN));
     const int jobs = (nc + 3) / 4 * 4;
-    for (int j = rank + CL * warp; j < jobs; j += CL * (kDenseThreads / 32)) {
+    for (int j = rank + CL * warp; j < jobs; j += CL * (kClusterThreads / 32)) {
       const int q = j & 3, c = (j >> 2) * 4;
       const int n = lt * 128 + q * 32 + lane;
       float nscale = 1.f, bias = 0.f;
-      if (EPI == kDenseForward && n < p.n) {
+      if (MODE == kDenseForward && n < p.n) {
         if (p.ns) nscale = q8_scale(p.ns[n]);
         if (p.bias) bias = p.bias[n];
       }
@@ -706,7 +721,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1) dense_cluster_kernel(const _
 #pragma unroll
         for (int e = 0; e < 4; ++e) v[e] += ld_shared_cluster_f32(at + e * 512);
       }
-      dense_epilogue<T, EPI, 4>(p, v, n, static_cast<long>(ct) * BN + c, split, nscale, bias);
+      dense_epilogue<T, MODE, 4>(p, v, n, static_cast<long>(ct) * BN + c, split, nscale, bias);
     }
     __syncthreads();
     cluster_sync();  // nobody reads this CTA's sums any more

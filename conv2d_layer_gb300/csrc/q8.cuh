@@ -70,6 +70,12 @@ __device__ __forceinline__ uint32_t q8_pack2(float a, float b) {
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(__fmaf_rn(b, 0.f, b)), "f"(__fmaf_rn(a, 0.f, a)));
   return r;
 }
+// The same without infinities among the values (NaN converts to NaN).
+__device__ __forceinline__ uint32_t q8_pack2_finite(float a, float b) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
+  return r;
+}
 // The two e4m3 values of the low 16 bits.
 __device__ __forceinline__ float2 q8_unpack2(uint32_t v) {
   uint32_t h;
