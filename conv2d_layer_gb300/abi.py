@@ -178,24 +178,21 @@ def conv2d_bwd(d, x, w, gamma, beta, pre_act, save_mean, save_inv_std, dy, dx, d
                             _ptr(dgamma), _ptr(dbeta), _ptr(ws), ws_bytes, _stream(stream))
 
 
-def _ref(m):
-    return None if m is None else ctypes.byref(m)
-
-
 def _ws(ws, ws_bytes):
     return ws.numel() * ws.element_size() if ws_bytes is None and ws is not None else (ws_bytes or 0)
 
 
+# conv2d_mat and desc arguments are Mat and DenseDesc objects, which ctypes passes by reference, or None.
 def conv2d_q8_encode(rows, cols, x, q8, stream=None):
-    return lib().conv2d_q8_encode(rows, cols, _ref(x), _ref(q8), _stream(stream))
+    return lib().conv2d_q8_encode(rows, cols, x, q8, _stream(stream))
 
 
 def conv2d_q8_decode(rows, cols, q8, x, stream=None):
-    return lib().conv2d_q8_decode(rows, cols, _ref(q8), _ref(x), _stream(stream))
+    return lib().conv2d_q8_decode(rows, cols, q8, x, _stream(stream))
 
 
 def conv2d_rms_norm_fwd(rows, cols, eps, x, residual, gamma, h, y, q8, inv_rms, stream=None):
-    return lib().conv2d_rms_norm_fwd(rows, cols, eps, _ref(x), _ref(residual), _ptr(gamma), _ref(h), _ref(y), _ref(q8),
+    return lib().conv2d_rms_norm_fwd(rows, cols, eps, x, residual, _ptr(gamma), h, y, q8,
                                      _ptr(inv_rms), _stream(stream))
 
 
@@ -204,26 +201,26 @@ def conv2d_rms_norm_bwd_workspace_size(rows, cols):
 
 
 def conv2d_rms_norm_bwd(rows, cols, h, gamma, inv_rms, dy, dh, dx, dgamma, accumulate, ws, ws_bytes=None, stream=None):
-    return lib().conv2d_rms_norm_bwd(rows, cols, _ref(h), _ptr(gamma), _ptr(inv_rms), _ref(dy), _ref(dh), _ref(dx),
+    return lib().conv2d_rms_norm_bwd(rows, cols, h, _ptr(gamma), _ptr(inv_rms), dy, dh, dx,
                                      _ptr(dgamma), int(accumulate), _ptr(ws), _ws(ws, ws_bytes), _stream(stream))
 
 
 def conv2d_dense_fwd_workspace_size(d, x, w):
-    return int(lib().conv2d_dense_fwd_workspace_size(ctypes.byref(d), _ref(x), _ref(w)))
+    return int(lib().conv2d_dense_fwd_workspace_size(d, x, w))
 
 
 def conv2d_dense_fwd(d, x, w, bias, residual, pre_act, y, ws, ws_bytes=None, stream=None):
-    return lib().conv2d_dense_fwd(ctypes.byref(d), _ref(x), _ref(w), _ptr(bias), _ref(residual), _ref(pre_act), _ref(y),
+    return lib().conv2d_dense_fwd(d, x, w, _ptr(bias), residual, pre_act, y,
                                   _ptr(ws), _ws(ws, ws_bytes), _stream(stream))
 
 
 def conv2d_dense_bwd_workspace_size(d, x, w, pre_act, dy, dx, dw, dbias):
-    return int(lib().conv2d_dense_bwd_workspace_size(ctypes.byref(d), _ref(x), _ref(w), _ref(pre_act), _ref(dy),
-                                                     _ref(dx), _ref(dw), _ptr(dbias)))
+    return int(lib().conv2d_dense_bwd_workspace_size(d, x, w, pre_act, dy,
+                                                     dx, dw, _ptr(dbias)))
 
 
 def conv2d_dense_bwd(d, x, w, pre_act, dy, dx, dw, dbias, ws, ws_bytes=None, stream=None):
-    return lib().conv2d_dense_bwd(ctypes.byref(d), _ref(x), _ref(w), _ref(pre_act), _ref(dy), _ref(dx), _ref(dw),
+    return lib().conv2d_dense_bwd(d, x, w, pre_act, dy, dx, dw,
                                   _ptr(dbias), _ptr(ws), _ws(ws, ws_bytes), _stream(stream))
 
 

@@ -73,13 +73,23 @@ GemmPlan plan_gemm(int mode, long m, long n, int kb, int max_kb, int sms) {
       best = g;
     }
   };
-  for (int splits = 1; splits <= (can_split ? 512 : 1) && splits <= kb; splits += splits < 8 ? 1 : splits / 8) {
-    for (int BN : {256, 224, 192, 160, 128}) consider(true, BN, 1, splits);
-    for (int BN : {128, 64, 32, 16}) {
-      if (r_mn && BN < 64) continue;  // MN-major tiles are panels of 64
-      for (int cl : {1, 2, 4, 8})
-        if (cl == 1 || ceil_div(kb, splits) >= 2 * cl) consider(false, BN, cl, splits);
+  // splits to look at: none, the fewest that keep an accumulator within max_kb, and those that fill one to three
+  // waves of SMs (or pairs)
+  auto splits_of = [&](bool pair, int BN, int cl) {
+    consider(pair, BN, cl, 1);
+    if (!can_split) return;
+    if (max_kb > 0) consider(pair, BN, cl, static_cast<int>(ceil_div(kb, static_cast<long>(max_kb) * cl)));
+    const long tiles = pair ? ceil_div(m, 256) * ceil_div(n, BN) : ceil_div(n, 128) * ceil_div(m, BN) * cl;
+    for (int w = 1; w <= 3; ++w) {
+      const long s = std::min<long>(w * (pair ? sms / 2 : sms) / tiles, kb);
+      if (s > 1) consider(pair, BN, cl, static_cast<int>(s));
     }
+  };
+  for (int BN : {256, 224, 192, 160, 128}) splits_of(true, BN, 1);
+  for (int BN : {128, 64, 32, 16}) {
+    if (r_mn && BN < 64) continue;  // MN-major tiles are panels of 64
+    for (int cl : {1, 2, 4, 8})
+      if (cl == 1 || kb >= 2 * cl) splits_of(false, BN, cl);
   }
   int c_rows = best.BN;  // columns of C a CTA brings: MN-major in whole panels of 64
   if (best.pair) c_rows = c_mn ? static_cast<int>(round_up(best.BN / 2, 64)) : best.BN / 2;

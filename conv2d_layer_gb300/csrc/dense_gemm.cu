@@ -1,6 +1,7 @@
 // dense_gemm.cu - instantiation and launch of the dense layer's GEMM kernels.
 #include "dense.h"
 
+#include <atomic>
 #include <type_traits>
 
 #include "conv2d.h"
@@ -11,17 +12,30 @@ namespace c2d {
 
 namespace {
 
+// Lets a kernel take up to the block's opt-in limit of shared memory, once for each device.
+template <typename K>
+cudaError_t opt_in(K kernel, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess || (done.load(std::memory_order_relaxed) >> dev & 1)) return e;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kMaxDynSmem));
+  if (e == cudaSuccess) done.fetch_or(uint64_t(1) << dev);
+  return e;
+}
+
 template <typename T, int MODE, bool FP8>
 cudaError_t pair(const DenseGemmParams& p, int grid, size_t smem, cudaStream_t st) {
   const auto k = dense_pair_kernel<T, MODE, FP8>;
-  const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e = opt_in(k, done);
   return e != cudaSuccess ? e : launch_k(k, dim3(grid), dim3(kPairThreads), smem, st, 2, p);
 }
 
 template <typename T, int MODE, bool FP8>
 cudaError_t cluster(const DenseGemmParams& p, int grid, size_t smem, cudaStream_t st) {
   const auto k = dense_cluster_kernel<T, MODE, FP8>;
-  const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e = opt_in(k, done);
   return e != cudaSuccess ? e : launch_k(k, dim3(grid), dim3(kClusterThreads), smem, st, p.cluster, p);
 }
 

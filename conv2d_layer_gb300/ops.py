@@ -57,46 +57,70 @@ def q8_empty(rows, cols, group=GROUP, device="cuda"):
 
 
 # ------------------------------------------------------------------ checks
+# These run on every call, a small call's time is mostly theirs: the common path tests and returns, what is wrong
+# is found out afterwards.
 def _mat(t, name, rows, cols, dtypes, device):
     """A checked matrix argument as conv2d_mat."""
-    if isinstance(t, Q8):
-        if torch.float8_e4m3fn not in dtypes:
-            raise ValueError(f"{name}: an 8-bit matrix is not taken here")
-        q, scale, group = t
-        shape = (rows, q8_scales(cols, group))
-        if not isinstance(scale, torch.Tensor) or scale.dtype != torch.uint8 or tuple(scale.shape) != shape:
-            raise ValueError(f"{name}: scales are uint8 of shape {shape}")
-        if not scale.is_contiguous() or scale.device != device:
-            raise ValueError(f"{name}: scales must be contiguous and on {device}")
-        t = q
-    else:
-        scale, group = None, 0
-        if isinstance(t, torch.Tensor) and t.dtype == torch.float8_e4m3fn:
-            raise ValueError(f"{name}: 8-bit values need their scales (Q8)")
+    if type(t) is Q8:
+        return _mat_q8(t, name, rows, cols, dtypes, device)
+    if isinstance(t, torch.Tensor) and t.shape == (rows, cols) and t.dtype in dtypes and t.device == device \
+            and t.dtype in _TYPES:
+        ld, step = t.stride()
+        ptr = t.data_ptr()
+        if rows <= 1:
+            ld = cols
+        if (step == 1 or cols == 1) and ld >= cols and not ptr & 15:
+            return abi.Mat(ptr, ld, _TYPES[t.dtype], 0, None)
+    _refuse(t, name, rows, cols, dtypes, device)
+
+
+def _mat_q8(t, name, rows, cols, dtypes, device):
+    if torch.float8_e4m3fn not in dtypes:
+        raise ValueError(f"{name}: an 8-bit matrix is not taken here")
+    q, scale, group = t
+    shape = (rows, q8_scales(cols, group))
+    if not isinstance(scale, torch.Tensor) or scale.dtype != torch.uint8 or scale.shape != shape:
+        raise ValueError(f"{name}: scales are uint8 of shape {shape}")
+    if not scale.is_contiguous() or scale.device != device:
+        raise ValueError(f"{name}: scales must be contiguous and on {device}")
+    if isinstance(q, torch.Tensor) and q.shape == (rows, cols) and q.dtype == torch.float8_e4m3fn and q.device == device:
+        ld, step = q.stride()
+        ptr = q.data_ptr()
+        if rows <= 1:
+            ld = cols
+        if (step == 1 or cols == 1) and ld >= cols and not ptr & 15:
+            return abi.Mat(ptr, ld, abi.E4M3, group, scale.data_ptr())
+    _refuse(q, name, rows, cols, _E4M3, device)
+
+
+def _refuse(t, name, rows, cols, dtypes, device):
+    """Says what is wrong with a matrix argument."""
     if not isinstance(t, torch.Tensor):
         raise ValueError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
-    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
+    if tuple(t.shape) != (rows, cols):
         raise ValueError(f"{name}: shape {tuple(t.shape)} does not match {(rows, cols)}")
-    if t.dtype not in dtypes or (scale is not None and t.dtype != torch.float8_e4m3fn):
+    if t.dtype == torch.float8_e4m3fn and dtypes is not _E4M3:
+        raise ValueError(f"{name}: 8-bit values need their scales (Q8)")
+    if t.dtype not in dtypes:
         raise ValueError(f"{name}: dtype {t.dtype} is not one of {[str(d) for d in dtypes]}")
-    ld = t.stride(0) if rows > 1 else cols
-    if (cols > 1 and t.stride(1) != 1) or ld < cols:
-        raise ValueError(f"{name}: features must be contiguous and rows must not overlap (strides {t.stride()})")
     if t.device != device:
         raise ValueError(f"{name}: must be on {device} (got {t.device})")
-    ptr = t.data_ptr()
-    if ptr & 15:
+    if t.data_ptr() & 15:
         raise ValueError(f"{name}: must start on a 16-byte boundary")
-    if scale is not None:
-        return abi.Mat(ptr, ld, abi.E4M3, group, scale.data_ptr())
-    return abi.Mat(ptr, ld, _TYPES[t.dtype], 0, None)
+    raise ValueError(f"{name}: features must be contiguous and rows must not overlap (strides {t.stride()})")
+
+
+def _new(rows, cols, dtype, device):
+    """A new matrix and its conv2d_mat."""
+    t = torch.empty((rows, cols), dtype=dtype, device=device)
+    return t, abi.Mat(t.data_ptr(), cols, _TYPES[dtype], 0, None)
 
 
 def _vec(t, name, n, device):
     """A checked contiguous fp32 vector."""
     if not isinstance(t, torch.Tensor):
         raise ValueError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
-    if t.dtype != torch.float32 or t.dim() != 1 or t.shape[0] != n or not t.is_contiguous() or t.device != device:
+    if t.dtype != torch.float32 or t.shape != (n,) or not t.is_contiguous() or t.device != device:
         raise ValueError(f"{name}: expected a contiguous float32 tensor of shape ({n},) on {device}, got "
                          f"{t.dtype} {tuple(t.shape)} on {t.device}")
     if t.data_ptr() & 15:
@@ -106,14 +130,15 @@ def _vec(t, name, n, device):
 
 def _source(t, name, dtypes):
     """(rows, cols, device) of the argument the others are checked against."""
-    m = t.q if isinstance(t, Q8) else t
+    m = t.q if type(t) is Q8 else t
     if not isinstance(m, torch.Tensor):
         raise ValueError(f"{name}: expected a torch.Tensor or Q8, got {type(m).__name__}")
     if m.dim() != 2 or m.shape[1] < 1:
         raise ValueError(f"{name}: expected rows by at least one feature, got shape {tuple(m.shape)}")
     if m.dtype not in dtypes:
         raise ValueError(f"{name}: dtype {m.dtype} is not one of {[str(d) for d in dtypes]}")
-    return m.shape[0], m.shape[1], m.device
+    rows, cols = m.shape
+    return rows, cols, m.device
 
 
 def _streamed(f):
@@ -131,7 +156,7 @@ def _run(device, call, *args):
     """One library call on the current stream of `device`, where every checked tensor lies."""
     if device.type != "cuda":
         raise ValueError(f"the tensors must be in CUDA device memory (got {device})")
-    s = torch.cuda.current_stream(device).cuda_stream
+    s = torch._C._cuda_getCurrentRawStream(device.index)
     if torch.cuda.current_device() == device.index:
         abi.check(call(*args, stream=s), call.__name__)
     else:
@@ -158,7 +183,6 @@ _E4M3 = (torch.float8_e4m3fn,)
 def q8_encode(x, group=GROUP, out=None):
     """x [rows, cols] (fp32, bf16, fp16) in 8 bits, with one scale for `group` columns (32, or 0: a row)."""
     rows, cols, dev = _source(x, "x", _FLOATS)
-    q8_scales(cols, group)
     if out is None:
         out = q8_empty(rows, cols, group, dev)
     elif not isinstance(out, Q8):
@@ -176,9 +200,11 @@ def q8_decode(q8, dtype=torch.bfloat16, out=None):
     rows, cols, dev = _source(q8, "q8", _E4M3)
     if dtype not in _FLOATS:
         raise ValueError(f"dtype: one of {[str(d) for d in _FLOATS]}, got {dtype}")
+    mq = _mat(q8, "q8", rows, cols, _E4M3, dev)
     if out is None:
-        out = torch.empty((rows, cols), dtype=dtype, device=dev)
-    mq, mo = _mat(q8, "q8", rows, cols, _E4M3, dev), _mat(out, "out", rows, cols, (dtype,), dev)
+        out, mo = _new(rows, cols, dtype, dev)
+    else:
+        mo = _mat(out, "out", rows, cols, (dtype,), dev)
     _run(dev, abi.conv2d_q8_decode, rows, cols, mq, mo)
     return out
 
@@ -195,9 +221,11 @@ def rms_norm_fwd(x, gamma, eps=1e-6, residual=None, y=True, group=None, h=None, 
     dt = (x.dtype,)
     _vec(gamma, "gamma", cols, dev)
     if y is True:
-        y = torch.empty((rows, cols), dtype=x.dtype, device=dev)
+        y, my = _new(rows, cols, x.dtype, dev)
     elif y is False:
-        y = None
+        y = my = None
+    else:
+        my = _mat(y, "y", rows, cols, dt, dev)
     if q8 is None and group is not None:
         q8 = q8_empty(rows, cols, group, dev)
     elif q8 is not None and not isinstance(q8, Q8):
@@ -211,14 +239,14 @@ def rms_norm_fwd(x, gamma, eps=1e-6, residual=None, y=True, group=None, h=None, 
     else:
         mr = _mat(residual, "residual", rows, cols, dt, dev)
         if h is None:
-            h = torch.empty((rows, cols), dtype=x.dtype, device=dev)
-        mh = _mat(h, "h", rows, cols, dt, dev)
+            h, mh = _new(rows, cols, x.dtype, dev)
+        else:
+            mh = _mat(h, "h", rows, cols, dt, dev)
     if inv_rms is None:
         inv_rms = torch.empty(rows, dtype=torch.float32, device=dev)
     else:
         _vec(inv_rms, "inv_rms", rows, dev)
     mx = _mat(x, "x", rows, cols, dt, dev)
-    my = None if y is None else _mat(y, "y", rows, cols, dt, dev)
     mq = None if q8 is None else _mat(q8, "q8", rows, cols, _E4M3, dev)
     _run(dev, abi.conv2d_rms_norm_fwd, rows, cols, eps, mx, mr, gamma, mh, my, mq, inv_rms)
     return RmsNorm(x if residual is None else h, y, q8, inv_rms)
@@ -236,9 +264,11 @@ def rms_norm_bwd(h, gamma, inv_rms, dy, dh=None, dx=None, dgamma=None, need_dx=T
         raise ValueError("need_dx or need_dgamma")
     mh, md = _mat(h, "h", rows, cols, dt, dev), _mat(dy, "dy", rows, cols, dt, dev)
     ms = None if dh is None else _mat(dh, "dh", rows, cols, dt, dev)
+    mx = None
     if need_dx and dx is None:
-        dx = torch.empty((rows, cols), dtype=h.dtype, device=dev)
-    mx = _mat(dx, "dx", rows, cols, dt, dev) if need_dx else None
+        dx, mx = _new(rows, cols, h.dtype, dev)
+    elif need_dx:
+        mx = _mat(dx, "dx", rows, cols, dt, dev)
     accumulate = dgamma is not None
     if need_dgamma and dgamma is None:
         dgamma = torch.empty(cols, dtype=torch.float32, device=dev)
@@ -277,8 +307,9 @@ def dense_fwd(x, w, bias=None, act="identity", residual=None, save="none", dtype
         _vec(bias, "bias", N, dev)
     mr = None if residual is None else _mat(residual, "residual", M, N, dt, dev)
     if y is None:
-        y = torch.empty((M, N), dtype=dtype, device=dev)
-    my = _mat(y, "y", M, N, dt, dev)
+        y, my = _new(M, N, dtype, dev)
+    else:
+        my = _mat(y, "y", M, N, dt, dev)
     if save not in ("none", "full", "q8"):
         raise ValueError(f"save: none, full or q8, got {save!r}")
     if pre_act is None:
@@ -320,17 +351,19 @@ def dense_bwd(x, w, dy, pre_act=None, act="identity", need_dx=True, need_dw=True
     if any(given) and not all(given):
         raise ValueError("dw and dbias: hand in both to accumulate, or neither")
     accumulate = any(given)
+    mdx = mdw = db = None
     if need_dx and dx is None:
-        dx = torch.empty((M, K), dtype=dy.dtype, device=dev)
+        dx, mdx = _new(M, K, dy.dtype, dev)
+    elif need_dx:
+        mdx = _mat(dx, "dx", M, K, dt, dev)
     if need_dw and dw is None:
         if grad_dtype not in (torch.float32, dy.dtype):
             raise ValueError(f"grad_dtype: float32 or {dy.dtype}, got {grad_dtype}")
-        dw = torch.empty((N, K), dtype=grad_dtype, device=dev)
-    if need_dbias and dbias is None:
-        dbias = torch.empty(N, dtype=torch.float32, device=dev)
-    mdx = _mat(dx, "dx", M, K, dt, dev) if need_dx else None
-    mdw = _mat(dw, "dw", N, K, dt + (torch.float32,), dev) if need_dw else None
-    db = _vec(dbias, "dbias", N, dev) if need_dbias else None
+        dw, mdw = _new(N, K, grad_dtype, dev)
+    elif need_dw:
+        mdw = _mat(dw, "dw", N, K, dt + (torch.float32,), dev)
+    if need_dbias:
+        db = torch.empty(N, dtype=torch.float32, device=dev) if dbias is None else _vec(dbias, "dbias", N, dev)
     d = abi.DenseDesc(M, K, N, code, _TYPES[dy.dtype], int(accumulate))
     ws = _scratch(abi.conv2d_dense_bwd_workspace_size(d, mx, mw, mz, md, mdx, mdw, db), dev)
     _run(dev, abi.conv2d_dense_bwd, d, mx, mw, mz, md, mdx, mdw, db, ws)
