@@ -82,33 +82,42 @@ __device__ __forceinline__ float2 q8_unpack2(uint32_t v) {
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(v)));
   return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
-// Stores V e4m3 bytes of v[] * inv.
+__device__ __forceinline__ uint32_t q8_pack4(const float* v, float inv, bool finite) {
+  return finite ? q8_pack2_finite(v[0] * inv, v[1] * inv) | q8_pack2_finite(v[2] * inv, v[3] * inv) << 16
+                : q8_pack2(v[0] * inv, v[1] * inv) | q8_pack2(v[2] * inv, v[3] * inv) << 16;
+}
+// Stores V e4m3 bytes of v[] * inv; finite: no infinity among them.
 template <int V>
-__device__ __forceinline__ void q8_store(uint8_t* p, const float (&v)[V], float inv) {
+__device__ __forceinline__ void q8_store(uint8_t* p, const float (&v)[V], float inv, bool finite) {
   if constexpr (V == 1) {
     *p = static_cast<uint8_t>(q8_pack2(v[0] * inv, 0.f));
   } else if constexpr (V == 4) {
-    *reinterpret_cast<uint32_t*>(p) = q8_pack2(v[0] * inv, v[1] * inv) | q8_pack2(v[2] * inv, v[3] * inv) << 16;
+    *reinterpret_cast<uint32_t*>(p) = q8_pack4(v, inv, finite);
   } else {
     static_assert(V == 8, "V is 1, 4 or 8");
-    uint2 w;
-    w.x = q8_pack2(v[0] * inv, v[1] * inv) | q8_pack2(v[2] * inv, v[3] * inv) << 16;
-    w.y = q8_pack2(v[4] * inv, v[5] * inv) | q8_pack2(v[6] * inv, v[7] * inv) << 16;
-    *reinterpret_cast<uint2*>(p) = w;
+    *reinterpret_cast<uint2*>(p) = make_uint2(q8_pack4(v, inv, finite), q8_pack4(v + 4, inv, finite));
   }
 }
-// Loads V e4m3 bytes as fp32 values times scale.
+// V e4m3 bytes as they lie in memory, and their values times scale.
 template <int V>
-__device__ __forceinline__ void q8_load(const uint8_t* p, float (&v)[V], float scale) {
+struct Q8Raw {
+  uint32_t w[V < 4 ? 1 : V / 4];
+};
+template <int V>
+__device__ __forceinline__ Q8Raw<V> q8_load(const uint8_t* p) {
+  Q8Raw<V> r;
+  if constexpr (V == 1) r.w[0] = *p;
+  else if constexpr (V == 4) r.w[0] = *reinterpret_cast<const uint32_t*>(p);
+  else if constexpr (V == 8) *reinterpret_cast<uint2*>(r.w) = *reinterpret_cast<const uint2*>(p);
+  else *reinterpret_cast<uint4*>(r.w) = *reinterpret_cast<const uint4*>(p);
+  return r;
+}
+template <int V>
+__device__ __forceinline__ void q8_values(const Q8Raw<V>& r, float (&v)[V], float scale) {
   if constexpr (V == 1) {
-    v[0] = q8_unpack2(*p).x * scale;
+    v[0] = q8_unpack2(r.w[0]).x * scale;
   } else {
-    uint32_t w[V / 4];
-    if constexpr (V == 4) w[0] = *reinterpret_cast<const uint32_t*>(p);
-    else {
-      static_assert(V == 8, "V is 1, 4 or 8");
-      *reinterpret_cast<uint2*>(w) = *reinterpret_cast<const uint2*>(p);
-    }
+    const uint32_t* w = r.w;
 #pragma unroll
     for (int i = 0; i < V / 2; ++i) {
       const float2 f = q8_unpack2(w[i / 2] >> (16 * (i & 1)));

@@ -166,13 +166,22 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) rows_fwd_kernel(const N
       o[0] = o[0] * inv * g[0];
     }
   };
+  // Largest magnitude's bits; fmaxf passes NaN over, and infinities are looked for only where one shows.
   auto absmax = [&](const float (&o)[V]) {
+    float m = 0.f;
+#pragma unroll
+    for (int k = 0; k < V; ++k) m = fmaxf(m, fabsf(o[k]));
+    return __float_as_uint(m);
+  };
+  auto absmax_finite = [&](const float (&o)[V]) {
     uint32_t m = 0u;
 #pragma unroll
     for (int k = 0; k < V; ++k) m = max(m, finite_bits(o[k]));
     return m;
   };
+  constexpr uint32_t kInf = 0x7f800000u;
   uint32_t rowbyte = 0u;
+  bool finite = true;
   if (a.q && a.group == 0) {
     uint32_t m = 0u;
     if constexpr (U > 0) {
@@ -188,7 +197,23 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) rows_fwd_kernel(const N
         m = max(m, absmax(v[0]));
       }
     }
-    rowbyte = q8_scale_byte(row_max<TPR>(m, reinterpret_cast<uint32_t*>(red)));
+    m = row_max<TPR>(m, reinterpret_cast<uint32_t*>(red));
+    if (m == kInf) {  // the same for the whole row
+      finite = false;
+      m = 0u;
+      if constexpr (U > 0) {
+#pragma unroll
+        for (int u = 0; u < UC; ++u) m = max(m, absmax_finite(v[u]));
+      } else {
+        for (int u = 0; u < nu; ++u) {
+          reload(u, v[0]);
+          scale(u, v[0]);
+          m = max(m, absmax_finite(v[0]));
+        }
+      }
+      m = row_max<TPR>(m, reinterpret_cast<uint32_t*>(red));
+    }
+    rowbyte = q8_scale_byte(m);
     if (t == 0) a.qs[row * a.ng] = static_cast<uint8_t>(rowbyte);
   }
   T* y = a.y ? static_cast<T*>(a.y) + row * a.ldy : nullptr;
@@ -204,13 +229,21 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) rows_fwd_kernel(const N
     if (q) {
       uint32_t byte = rowbyte;
       if (a.group != 0) {
-        uint32_t m = absmax(o);
+        auto group_max = [](uint32_t m) {
 #pragma unroll
-        for (int s = 1; s < kQ8Group / V; s <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, s));
+          for (int s = 1; s < kQ8Group / V; s <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, s));
+          return m;
+        };
+        uint32_t m = group_max(absmax(o));
+        finite = true;
+        if (__any_sync(0xffffffffu, m == kInf)) {
+          finite = false;
+          m = group_max(absmax_finite(o));
+        }
         byte = q8_scale_byte(m);
         if (i < nv && (t & (kQ8Group / V - 1)) == 0) a.qs[row * a.ng + i / (kQ8Group / V)] = static_cast<uint8_t>(byte);
       }
-      if (i < nv) q8_store<V>(q + static_cast<long>(i) * V, o, q8_inv_scale(byte));
+      if (i < nv) q8_store<V>(q + static_cast<long>(i) * V, o, q8_inv_scale(byte), finite);
     }
   };
   if constexpr (U > 0) {
@@ -264,7 +297,7 @@ struct NormBwdArgs {
 // reduced. U = 0: rows longer than the registers hold; each row is read twice and dgamma's sums live in
 // this block's row of `part`.
 template <typename T, int V, int TPR, int U>
-__global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) norm_bwd_kernel(const NormBwdArgs a) {
+__global__ void __launch_bounds__(TPR < 256 ? 256 : TPR, TPR <= 256 ? 2 : 1) norm_bwd_kernel(const NormBwdArgs a) {
   pdl_entry();
   constexpr int RPB = TPR < 256 ? 256 / TPR : 1;
   constexpr int UC = U > 0 ? U : 1;
@@ -433,27 +466,48 @@ cudaError_t norm_bwd(const NormBwdArgs& a, int grid, cudaStream_t st) {
 }
 
 // ------------------------------------------------------------------ decode / move
-// One vector of V elements a thread of a [rows][cols] matrix (E4M3 source: V bytes and their scale).
+// V elements a thread and step of a [rows][cols] matrix, dense steps of the grid (E4M3 source: V bytes and
+// their scale; 16 with a 16-bit output, two vectors). rows * ceil(cols / V) below 2^31 (see to_rows).
 template <typename T, int V, bool Q>
 __global__ void __launch_bounds__(256) to_rows_kernel(const void* x, long ldx, const uint8_t* scale, int group, int ng,
-                                                      long rows, int cols, T* out, long ldo) {
+                                                      uint32_t total, int cols, FastDiv div_nv, T* out, long ldo) {
   pdl_entry();
-  const int nv = (cols + V - 1) / V;
-  const long total = rows * nv;
-  for (long j = static_cast<long>(blockIdx.x) * 256 + threadIdx.x; j < total; j += static_cast<long>(gridDim.x) * 256) {
-    const long row = j / nv;
-    const int c = static_cast<int>(j - row * nv) * V;
-    T o[V];
-    if constexpr (Q) {
-      float v[V];
-      q8_load<V>(static_cast<const uint8_t*>(x) + row * ldx + c, v,
-                 q8_scale(scale[row * ng + (group ? c / kQ8Group : 0)]));
+  constexpr int VO = V * sizeof(T) > 16 ? 16 / static_cast<int>(sizeof(T)) : V;  // elements a store
+  constexpr int N = 2;                                                          // steps in flight
+  const uint32_t step = gridDim.x * 256u;
+  for (uint32_t j0 = blockIdx.x * 256u + threadIdx.x; j0 < total; j0 += N * step) {
+    Q8Raw<V> raw[N];
+    T e[N][V];
+    float sc[N];
+    long row[N];
+    int c[N];
 #pragma unroll
-      for (int k = 0; k < V; ++k) o[k] = from_q8<T>(v[k]);
-    } else {
-      ld_vec<T, V>(static_cast<const T*>(x) + row * ldx + c, o);
+    for (int i = 0; i < N; ++i) {
+      const uint32_t j = j0 + i * step;
+      if (j >= total) break;
+      const uint32_t r = fdiv(j, div_nv);
+      row[i] = r;
+      c[i] = static_cast<int>(j - r * div_nv.d) * V;
+      if constexpr (Q) {
+        raw[i] = q8_load<V>(static_cast<const uint8_t*>(x) + row[i] * ldx + c[i]);
+        sc[i] = q8_scale(scale[row[i] * ng + (group ? c[i] / kQ8Group : 0)]);
+      } else {
+        ld_vec<T, V>(static_cast<const T*>(x) + row[i] * ldx + c[i], e[i]);
+      }
     }
-    st_vec<T, V>(out + row * ldo + c, o);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      if (j0 + i * step >= total) break;
+      if constexpr (Q) {
+        float v[V];
+        q8_values<V>(raw[i], v, sc[i]);
+#pragma unroll
+        for (int k = 0; k < V; ++k) e[i][k] = from_q8<T>(v[k]);
+      }
+      T* o = out + row[i] * ldo + c[i];
+#pragma unroll
+      for (int k = 0; k < V; k += VO) st_vec<T, VO>(o + k, *reinterpret_cast<const T(*)[VO]>(&e[i][k]));
+    }
   }
 }
 
@@ -476,23 +530,31 @@ bool vec_ok(const void* p, long ld, int es, int V) {
 
 template <typename T>
 cudaError_t to_rows(const conv2d_mat& x, long rows, int cols, void* out, long ldo, cudaStream_t st) {
-  constexpr int VV = 16 / sizeof(T);
+  constexpr int VV = 16 / sizeof(T), VQ = 16;
   const bool q = x.type == CONV2D_E4M3;
   const long ldx = x.ld ? x.ld : cols, ld = ldo ? ldo : cols;
   const int ng = x.group ? (cols + kQ8Group - 1) / kQ8Group : 1;
   // whole vectors only: cols a multiple of the vector, and both rows' starts aligned to theirs
-  const bool vec = cols % VV == 0 && vec_ok(out, ld, sizeof(T), VV) && vec_ok(x.data, ldx, q ? 1 : sizeof(T), VV);
-  const long items = rows * (vec ? cols / VV : cols);
-  T* o = static_cast<T*>(out);
+  const int V = q ? VQ : VV;
+  const bool vec = cols % V == 0 && vec_ok(out, ld, sizeof(T), VV) && vec_ok(x.data, ldx, q ? 1 : sizeof(T), V);
+  const int nv = vec ? cols / V : cols;
+  const long slab = std::max<long>(1, 0x7fffffffL / nv);  // rows a launch indexes in 31 bits
+  for (long r0 = 0; r0 < rows; r0 += slab) {
+    const long n = std::min(slab, rows - r0);
+    const uint32_t total = static_cast<uint32_t>(n * nv);
+    const dim3 grid(stream_grid((n * nv + 1) / 2));
+    const char* src = static_cast<const char*>(x.data) + r0 * ldx * (q ? 1 : static_cast<long>(sizeof(T)));
+    const uint8_t* sc = q ? x.scale + r0 * ng : nullptr;
+    T* o = static_cast<T*>(out) + r0 * ld;
+    const FastDiv div = make_fastdiv(static_cast<uint32_t>(nv));
 #define TO_ROWS(V, Q)                                                                                              \
-  return launch_k(to_rows_kernel<T, V, Q>, dim3(stream_grid(items)), dim3(256), 0, st, 1,                         \
-                  static_cast<const void*>(x.data), ldx, static_cast<const uint8_t*>(x.scale), x.group, ng, rows, \
-                  cols, o, ld)
-  if (vec && q) TO_ROWS(VV, true);
-  if (vec) TO_ROWS(VV, false);
-  if (q) TO_ROWS(1, true);
-  TO_ROWS(1, false);
+  launch_k(to_rows_kernel<T, V, Q>, grid, dim3(256), 0, st, 1, static_cast<const void*>(src), ldx, sc, x.group, ng, \
+           total, cols, div, o, ld)
+    const cudaError_t e = vec ? (q ? TO_ROWS(VQ, true) : TO_ROWS(VV, false)) : (q ? TO_ROWS(1, true) : TO_ROWS(1, false));
 #undef TO_ROWS
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
 }
 
 // ------------------------------------------------------------------ backward through the activation
@@ -510,8 +572,9 @@ struct DactArgs {
 // the unrounded dz in registers, joined over the 8 row lanes at the end. ZK: 0 no activation, 1 z in T,
 // 2 z as E4M3.
 template <typename T, int V, int ZK>
-__global__ void __launch_bounds__(256) dact_kernel(const DactArgs a) {
+__global__ void __launch_bounds__(256, 4) dact_kernel(const DactArgs a) {
   pdl_entry();
+  constexpr int N = 4;  // rows in flight
   __shared__ float sums[8][32 * V];
   const int lane = threadIdx.x & 31, rl = threadIdx.x >> 5;
   const int c = (static_cast<int>(blockIdx.x) * 32 + lane) * V;
@@ -521,32 +584,49 @@ __global__ void __launch_bounds__(256) dact_kernel(const DactArgs a) {
   for (int k = 0; k < V; ++k) acc[k] = 0.f;
   if (c < a.cols) {
     const T* dy = static_cast<const T*>(a.dy) + c;
+    const T* zt = static_cast<const T*>(a.z) + c;
+    const uint8_t* zq = static_cast<const uint8_t*>(a.z) + c;
+    const uint8_t* zs = a.zs + (a.group ? c / kQ8Group : 0);
     T* dz = a.dz ? static_cast<T*>(a.dz) + c : nullptr;
     with_dense_act(ZK ? a.act : 0, [&](auto act) {
-#pragma unroll 4
-      for (long r = blockIdx.y * a.rows_per_strip + rl; r < r1; r += 8) {
-        T d[V];
-        ld_vec<T, V>(dy + r * a.lddy, d);
-        [[maybe_unused]] float f[V];
-        if constexpr (ZK == 1) {
-          T e[V];
-          ld_vec<T, V>(static_cast<const T*>(a.z) + c + r * a.ldz, e);
+#pragma unroll 1
+      for (long r = blockIdx.y * a.rows_per_strip + rl; r < r1; r += 8 * N) {
+        T d[N][V];
+        [[maybe_unused]] T e[N][V];
+        [[maybe_unused]] Q8Raw<V> q[N];
+        [[maybe_unused]] uint32_t sb[N];
 #pragma unroll
-          for (int k = 0; k < V; ++k) f[k] = to_f(e[k]);
-        } else if constexpr (ZK == 2) {
-          q8_load<V>(static_cast<const uint8_t*>(a.z) + c + r * a.ldz, f,
-                     q8_scale(a.zs[r * a.ng + (a.group ? c / kQ8Group : 0)]));
+        for (int i = 0; i < N; ++i) {
+          const long ri = r + 8 * i;
+          if (ri >= r1) break;
+          ld_vec<T, V>(dy + ri * a.lddy, d[i]);
+          if constexpr (ZK == 1) ld_vec<T, V>(zt + ri * a.ldz, e[i]);
+          if constexpr (ZK == 2) {
+            q[i] = q8_load<V>(zq + ri * a.ldz);
+            sb[i] = zs[ri * a.ng];
+          }
         }
-        T o[V];
 #pragma unroll
-        for (int k = 0; k < V; ++k) {
-          float v = to_f(d[k]);
-          // not contracted into the sum: the column sums are the same whether dz is written or not
-          if constexpr (ZK) v = __fmul_rn(v, dense_dact<decltype(act)::value>(f[k]));
-          acc[k] += v;
-          o[k] = from_f<T>(v);
+        for (int i = 0; i < N; ++i) {
+          const long ri = r + 8 * i;
+          if (ri >= r1) break;
+          [[maybe_unused]] float f[V];
+          if constexpr (ZK == 1) {
+#pragma unroll
+            for (int k = 0; k < V; ++k) f[k] = to_f(e[i][k]);
+          }
+          if constexpr (ZK == 2) q8_values<V>(q[i], f, q8_scale(sb[i]));
+          T o[V];
+#pragma unroll
+          for (int k = 0; k < V; ++k) {
+            float v = to_f(d[i][k]);
+            // not contracted into the sum: the column sums are the same whether dz is written or not
+            if constexpr (ZK) v = __fmul_rn(v, dense_dact<decltype(act)::value>(f[k]));
+            acc[k] += v;
+            o[k] = from_f<T>(v);
+          }
+          if (dz) st_vec<T, V>(dz + ri * a.lddz, o);
         }
-        if (dz) st_vec<T, V>(dz + r * a.lddz, o);
       }
     });
   }
