@@ -79,6 +79,11 @@ __device__ __forceinline__ void mma_f8_pair(uint32_t d, uint64_t a, uint64_t b, 
       : "memory");
 }
 
+// Arrive on an mbarrier of the cluster (shared::cluster address) without ordering this thread's memory accesses.
+__device__ __forceinline__ void mbar_arrive_relaxed(uint32_t caddr) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(caddr) : "memory");
+}
+
 __device__ __forceinline__ float ld_shared_cluster_f32(uint32_t caddr) {
   float v;
   asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(caddr) : "memory");
@@ -123,7 +128,11 @@ __device__ __forceinline__ void dense_epilogue(const DenseGemmParams& p, float (
     }
     with_dense_act(p.act, [&](auto act) {
 #pragma unroll
-      for (int e = 0; e < NC; ++e) v[e] = dense_act<decltype(act)::value>(v[e]);
+      for (int e = 0; e < NC; e += 2) {
+        const float2 a = dense_act<decltype(act)::value>(make_float2(v[e], v[e + 1]));
+        v[e] = a.x;
+        v[e + 1] = a.y;
+      }
     });
     T* y = static_cast<T*>(p.out) + m0 * p.ldo + n;
 #pragma unroll
@@ -211,9 +220,10 @@ __device__ __forceinline__ uint4 pack8(const float* v) {
 }
 
 // A warp's 32 rows (m0 ..) x up to 32 columns (n ..) of the accumulator at taddr; nr rows and nc columns count.
-template <typename T, int MODE>
+// release() is called when the accumulator has been read.
+template <typename T, int MODE, typename F>
 __device__ __forceinline__ void pair_epilogue(const DenseGemmParams& p, uint32_t taddr, uint32_t buf, long m0, int n,
-                                              int nr, int nc, int split, float mscale, int lane) {
+                                              int nr, int nc, int split, float mscale, int lane, F&& release) {
   if constexpr (MODE == kDenseForward) {
     // the residual's rows are in flight while the sums are read and activated
     uint4 res[4];
@@ -230,6 +240,7 @@ __device__ __forceinline__ void pair_epilogue(const DenseGemmParams& p, uint32_t
       uint32_t a[32];
       tmem_ld32(taddr, a);
       tmem_ld_wait32(a);
+      release();
 #pragma unroll
       for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(a[e]);
     }
@@ -304,7 +315,11 @@ __device__ __forceinline__ void pair_epilogue(const DenseGemmParams& p, uint32_t
     }
     with_dense_act(p.act, [&](auto act) {
 #pragma unroll
-      for (int e = 0; e < 32; ++e) v[e] = dense_act<decltype(act)::value>(v[e]);
+      for (int e = 0; e < 32; e += 2) {
+        const float2 a = dense_act<decltype(act)::value>(make_float2(v[e], v[e + 1]));
+        v[e] = a.x;
+        v[e + 1] = a.y;
+      }
     });
     if (p.res) {
       if (vres) {
@@ -337,6 +352,7 @@ __device__ __forceinline__ void pair_epilogue(const DenseGemmParams& p, uint32_t
     uint32_t a[32];
     tmem_ld32(taddr, a);
     tmem_ld_wait32(a);
+    release();
     if (p.out_f32) {
       float* out = static_cast<float*>(p.out) + split * p.split_stride + m0 * p.ldo + n;
 #pragma unroll
@@ -557,17 +573,24 @@ __global__ void __launch_bounds__(kPairThreads, 1) dense_pair_kernel(const __gri
       const int nr = static_cast<int>(min(p.m - m0, 32L));
       const float mscale = MODE == kDenseForward && p.ms && lane < nr ? q8_scale(p.ms[m0 + lane]) : 1.f;
       const int end = min(p.n, ct * BN + BN);
-      if (nr > 0) {  // uniform
+      // Frees the accumulator for the unit after next, once its last columns are in registers: before they are
+      // written, and without waiting for what was (the arrival orders nothing but the TMEM reads; with release
+      // semantics it waited for the stores to reach L2, and held the next MMAs back by as much).
+      auto arrive = [&] {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_relaxed(mapa_shared(smem_u32(&tempty[buf]), 0));
+      };
+      const int n0 = ct * BN + part * 32;
+      if (nr <= 0 || n0 >= end) {  // uniform
+        arrive();
+      } else {
 #pragma unroll 1
-        for (int n = ct * BN + part * 32; n < end; n += 128)
+        for (int n = n0; n < end; n += 128)
           pair_epilogue<T, MODE>(p, tmem + (static_cast<uint32_t>(q * 32) << 16) + buf * BN + (n - ct * BN), buf0, m0, n,
-                                 nr, min(end - n, 32), split, mscale, lane);
-      }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        if (leader) mbar_arrive(&tempty[buf]);
-        else mbar_arrive_cluster(mapa_shared(smem_u32(&tempty[buf]), 0));
+                                 nr, min(end - n, 32), split, mscale, lane, [&] {
+                                   if (n + 128 >= end) arrive();
+                                 });
       }
     }
   }

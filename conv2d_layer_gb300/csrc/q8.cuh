@@ -29,6 +29,12 @@ __device__ __forceinline__ T from_q8(float v) {
   return from_f<T>(v > top ? top : (v < -top ? -top : v));
 }
 
+// The largest scale whose values (448 times it at most) T holds without clamping.
+template <typename T>
+__device__ __forceinline__ constexpr float q8_safe_scale() {
+  return std::is_same<T, __half>::value ? 128.f : 6.6461399789245794e35f;  // 2^7, 2^119
+}
+
 // V consecutive elements as fp32; V * sizeof(T) = 16 bytes (aligned) or V = 1.
 template <typename T, int V>
 struct Vec {
@@ -143,46 +149,73 @@ __device__ __forceinline__ float rcp(float x) {
 }
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kGelu2 = 1.5957691216057308f;  // 2 sqrt(2/pi)
-__device__ __forceinline__ float sigmoid_f(float x) { return rcp(1.f + ex2(-kLog2e * x)); }
 
+__device__ __forceinline__ float2 splat(float x) { return make_float2(x, x); }
+__device__ __forceinline__ float2 ex2_2(float2 x) { return make_float2(ex2(x.x), ex2(x.y)); }
+__device__ __forceinline__ float2 rcp_2(float2 x) { return make_float2(rcp(x.x), rcp(x.y)); }
+// x within [-b, b]; NaN passes.
+__device__ __forceinline__ float clamp_nan(float x, float b) {
+  float y;
+  asm("{\n\t.reg .f32 t;\n\tmin.NaN.f32 t, %1, %2;\n\tmax.NaN.f32 %0, t, %3;\n\t}" : "=f"(y) : "f"(x), "f"(b), "f"(-b));
+  return y;
+}
+__device__ __forceinline__ float2 clamp_nan(float2 x, float b) { return make_float2(clamp_nan(x.x, b), clamp_nan(x.y, b)); }
+
+// Two values at a time: the multiplications and additions go in packed f32x2 instructions.
 template <int A>
-__device__ __forceinline__ float dense_act(float z) {
-  if constexpr (A == 1) return z > 0.f ? z : (z <= 0.f ? 0.f : z);  // NaN passes
-  else if constexpr (A == 2) {
+__device__ __forceinline__ float2 dense_act(float2 z) {
+  if constexpr (A == 1) {  // NaN passes
+    return make_float2(z.x > 0.f ? z.x : (z.x <= 0.f ? 0.f : z.x), z.y > 0.f ? z.y : (z.y <= 0.f ? 0.f : z.y));
+  } else if constexpr (A == 2) {
     // tanh z = z (1 - z^2/3 + 2 z^4/15 - 17 z^6/315) below 1/4 (the next term is under 4e-7 of z), else
     // (1 - e) / (1 + e) with e = exp(-2|z|) and z's sign
-    const float a = fabsf(z), s = z * z;
-    if (a < 0.25f) return z * (1.f + s * (-1.f / 3.f + s * (2.f / 15.f - s * (17.f / 315.f))));
-    const float e = ex2(-2.f * kLog2e * a);
-    return copysignf((1.f - e) * rcp(1.f + e), z);
-  } else if constexpr (A == 3) return sigmoid_f(z);
-  else if constexpr (A == 4) {
+    const float2 a = make_float2(fabsf(z.x), fabsf(z.y)), s = __fmul2_rn(z, z);
+    const float2 e = ex2_2(__fmul2_rn(a, splat(-2.f * kLog2e)));
+    const float2 big = __fmul2_rn(__ffma2_rn(e, splat(-1.f), splat(1.f)), rcp_2(__fadd2_rn(e, splat(1.f))));
+    float2 p = __ffma2_rn(s, splat(-17.f / 315.f), splat(2.f / 15.f));
+    p = __ffma2_rn(s, p, splat(-1.f / 3.f));
+    p = __fmul2_rn(z, __ffma2_rn(s, p, splat(1.f)));
+    return make_float2(a.x < 0.25f ? p.x : copysignf(big.x, z.x), a.y < 0.25f ? p.y : copysignf(big.y, z.y));
+  } else if constexpr (A == 3) {
+    return rcp_2(__fadd2_rn(ex2_2(__fmul2_rn(z, splat(-kLog2e))), splat(1.f)));
+  } else if constexpr (A == 4) {
     // z/2 (1 + tanh u) = z / (1 + exp(-2u)); past |z| = 16 the factor is 0 or 1 to fp32 (clamped, so that
     // u does not overflow)
-    const float c = z > 16.f ? 16.f : (z < -16.f ? -16.f : z);
-    return z * rcp(1.f + ex2(c * fmaf(c * c, -kLog2e * kGelu2 * 0.044715f, -kLog2e * kGelu2)));
-  } else if constexpr (A == 5) return z * sigmoid_f(z);
-  else return z;
+    const float2 c = clamp_nan(z, 16.f);
+    const float2 u = __fmul2_rn(c, __ffma2_rn(__fmul2_rn(c, c), splat(-kLog2e * kGelu2 * 0.044715f), splat(-kLog2e * kGelu2)));
+    return __fmul2_rn(z, rcp_2(__fadd2_rn(ex2_2(u), splat(1.f))));
+  } else if constexpr (A == 5) {
+    return __fmul2_rn(z, rcp_2(__fadd2_rn(ex2_2(__fmul2_rn(z, splat(-kLog2e))), splat(1.f))));
+  } else {
+    return z;
+  }
 }
 template <int A>
-__device__ __forceinline__ float dense_dact(float z) {
-  if constexpr (A == 1) return z > 0.f ? 1.f : (z <= 0.f ? 0.f : z);
-  else if constexpr (A == 2) {  // 1 - tanh^2 = 4 e / (1 + e)^2
-    const float e = ex2(-2.f * kLog2e * fabsf(z)), r = rcp(1.f + e);
-    return 4.f * e * r * r;
-  } else if constexpr (A == 3) {  // s (1 - s) = e / (1 + e)^2, e = exp(-|z|)
-    const float e = ex2(-kLog2e * fabsf(z)), r = rcp(1.f + e);
-    return e * r * r;
-  } else if constexpr (A == 4) {
-    const float c = z > 16.f ? 16.f : (z < -16.f ? -16.f : z);
-    const float q = c * c;
-    const float s = rcp(1.f + ex2(c * fmaf(q, -kLog2e * kGelu2 * 0.044715f, -kLog2e * kGelu2)));
-    return s + c * s * (1.f - s) * fmaf(q, 3.f * 0.044715f * kGelu2, kGelu2);
-  } else if constexpr (A == 5) {
-    const float c = z > 88.f ? 88.f : (z < -88.f ? -88.f : z);
-    const float s = sigmoid_f(c);
-    return s * (1.f + c * (1.f - s));
-  } else return 1.f;
+__device__ __forceinline__ float2 dense_dact(float2 z) {
+  if constexpr (A == 1) {
+    return make_float2(z.x > 0.f ? 1.f : (z.x <= 0.f ? 0.f : z.x), z.y > 0.f ? 1.f : (z.y <= 0.f ? 0.f : z.y));
+  } else if constexpr (A == 2 || A == 3) {
+    // tanh: 1 - tanh^2 = 4 e / (1 + e)^2, e = exp(-2|z|); sigmoid: s (1 - s) = e / (1 + e)^2, e = exp(-|z|)
+    const float2 e = ex2_2(__fmul2_rn(make_float2(fabsf(z.x), fabsf(z.y)), splat(A == 2 ? -2.f * kLog2e : -kLog2e)));
+    const float2 r = rcp_2(__fadd2_rn(e, splat(1.f)));
+    return __fmul2_rn(__fmul2_rn(A == 2 ? __fmul2_rn(e, splat(4.f)) : e, r), r);
+  } else if constexpr (A == 4 || A == 5) {
+    // s + z s (1 - s) w, w = d(2u)/dz (gelu) or 1 (silu)
+    const float2 c = clamp_nan(z, A == 4 ? 16.f : 88.f);
+    float2 u, w;
+    if constexpr (A == 4) {
+      const float2 q = __fmul2_rn(c, c);
+      u = __fmul2_rn(c, __ffma2_rn(q, splat(-kLog2e * kGelu2 * 0.044715f), splat(-kLog2e * kGelu2)));
+      w = __fmul2_rn(c, __ffma2_rn(q, splat(3.f * 0.044715f * kGelu2), splat(kGelu2)));
+    } else {
+      u = __fmul2_rn(c, splat(-kLog2e));
+      w = c;
+    }
+    const float2 s = rcp_2(__fadd2_rn(ex2_2(u), splat(1.f)));
+    return __ffma2_rn(__fmul2_rn(s, w), __ffma2_rn(s, splat(-1.f), splat(1.f)), s);
+  } else {
+    return splat(1.f);
+  }
 }
 template <int A>
 struct DAct {

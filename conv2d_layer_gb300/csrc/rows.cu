@@ -70,101 +70,120 @@ struct NormArgs {
   float eps;
 };
 
-// RMS norm forward (NORM) or 8-bit encode (!NORM) of one row by TPR threads; blocks of max(TPR, 256)
-// threads. The row is held in registers between its sum of squares and its output, U vectors a thread, so
-// memory is passed once; U = 0 is the form for rows longer than that, which reads the row again for each
-// phase (from L2, mostly). Threads hold neighbouring vectors, so a group of 32 columns lies in 32 / V
+// RMS norm forward (NORM) or 8-bit encode (!NORM): TPR threads a row, blocks of max(TPR, 256) threads. Rows are
+// held in registers between their sum of squares and their output, U vectors a thread, so memory is passed once;
+// U = 0 is the form for rows longer than that, which reads the row again for each phase (from L2, mostly). NR
+// rows are in flight at once where a row is a vector or two a thread (one row of 512 bytes a warp left a
+// 200704 x 256 encode at 41 us). Threads hold neighbouring vectors, so a group of 32 columns lies in 32 / V
 // neighbouring lanes and its maximum is found by shuffles.
-template <typename T, int V, int TPR, int U, bool NORM>
+template <typename T, int V, int TPR, int U, int NR, bool NORM>
 __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) rows_fwd_kernel(const NormArgs a) {
   pdl_entry();
-  constexpr int RPB = TPR < 256 ? 256 / TPR : 1;  // rows per block
+  constexpr int RPB = TPR < 256 ? 256 / TPR : 1;  // groups of NR rows per block
   static_assert(RPB == 1 || TPR == 32, "rows that share a block are one warp each");
+  static_assert(U > 0 || NR == 1, "one row at a time where it is read again");
   constexpr int UC = U > 0 ? U : 1;
   __shared__ float red[32];
   const int t = RPB > 1 ? static_cast<int>(threadIdx.x) & 31 : static_cast<int>(threadIdx.x);
-  const long row = RPB > 1 ? static_cast<long>(blockIdx.x) * RPB + (threadIdx.x >> 5) : static_cast<long>(blockIdx.x);
-  if (row >= a.rows) return;  // whole warps; rows that use block barriers are whole blocks
-  const T* x = static_cast<const T*>(a.x) + row * a.ldx;
-  const T* r = a.r ? static_cast<const T*>(a.r) + row * a.ldr : nullptr;
-  T* h = a.h ? static_cast<T*>(a.h) + row * a.ldh : nullptr;
+  const long row0 = (static_cast<long>(blockIdx.x) * RPB + (RPB > 1 ? threadIdx.x >> 5 : 0)) * NR;
+  if (row0 >= a.rows) return;  // whole warps; rows that use block barriers are whole blocks
+  const int nr = static_cast<int>(min(a.rows - row0, static_cast<long>(NR)));
   const int nv = (a.cols + V - 1) / V;
   const int nu = U > 0 ? U : (nv + TPR - 1) / TPR;  // vectors a thread
+  const T* xb = static_cast<const T*>(a.x) + row0 * a.ldx;
+  const T* rb = static_cast<const T*>(a.r) + row0 * a.ldr;
+  T* hb = static_cast<T*>(a.h) + row0 * a.ldh;
 
-  float v[UC][V];
-  auto load = [&](int u, float (&o)[V]) {  // x + r as stored; zeros past the end
-    const int i = u * TPR + t;
-    if (i < nv) {
-      T e[V];
-      ld_vec<T, V>(x + static_cast<long>(i) * V, e);
-      if (r) {
-        T f[V];
-        ld_vec<T, V>(r + static_cast<long>(i) * V, f);
+  float v[NR][UC][V];
+  auto widen = [](const T (&e)[V], float (&o)[V]) {
 #pragma unroll
-        for (int k = 0; k < V; ++k) e[k] = from_f<T>(to_f(e[k]) + to_f(f[k]));
-        st_vec<T, V>(h + static_cast<long>(i) * V, e);
+    for (int k = 0; k < V; ++k) o[k] = to_f(e[k]);
+  };
+  // x + r as stored (h is written); zeros past the end
+  auto load_all = [&](int u0, int n) {
+    T e[NR][UC][V], f[NR][UC][V];
+#pragma unroll
+    for (int i = 0; i < NR; ++i)
+#pragma unroll
+      for (int u = 0; u < UC; ++u) {
+        const int c = ((u0 + u) * TPR + t);
+        if (i < nr && c < nv && u < n) {
+          ld_vec<T, V>(xb + i * a.ldx + static_cast<long>(c) * V, e[i][u]);
+          if (a.r) ld_vec<T, V>(rb + i * a.ldr + static_cast<long>(c) * V, f[i][u]);
+        } else {
+#pragma unroll
+          for (int k = 0; k < V; ++k) e[i][u][k] = f[i][u][k] = from_f<T>(0.f);
+        }
       }
 #pragma unroll
-      for (int k = 0; k < V; ++k) o[k] = to_f(e[k]);
-    } else {
+    for (int i = 0; i < NR; ++i)
 #pragma unroll
-      for (int k = 0; k < V; ++k) o[k] = 0.f;
-    }
+      for (int u = 0; u < UC; ++u) {
+        const int c = ((u0 + u) * TPR + t);
+        if (a.r) {
+#pragma unroll
+          for (int k = 0; k < V; ++k) e[i][u][k] = from_f<T>(to_f(e[i][u][k]) + to_f(f[i][u][k]));
+          if (i < nr && c < nv && u < n) st_vec<T, V>(hb + i * a.ldh + static_cast<long>(c) * V, e[i][u]);
+        }
+        widen(e[i][u], v[i][u]);
+      }
   };
-  auto reload = [&](int u, float (&o)[V]) {  // U = 0: this thread's own h (or x) again
-    const int i = u * TPR + t;
-    if (i < nv) {
+  auto reload = [&](int u) {  // U = 0: this thread's own h (or x) again
+    const int c = u * TPR + t;
+    if (c < nv) {
       T e[V];
-      ld_vec<T, V>((r ? static_cast<const T*>(h) : x) + static_cast<long>(i) * V, e);
-#pragma unroll
-      for (int k = 0; k < V; ++k) o[k] = to_f(e[k]);
+      ld_vec<T, V>((a.r ? static_cast<const T*>(hb) : xb) + static_cast<long>(c) * V, e);
+      widen(e, v[0][0]);
     } else {
 #pragma unroll
-      for (int k = 0; k < V; ++k) o[k] = 0.f;
+      for (int k = 0; k < V; ++k) v[0][0][k] = 0.f;
     }
   };
 
-  float inv = 1.f;
+  float inv[NR];
+#pragma unroll
+  for (int i = 0; i < NR; ++i) inv[i] = 1.f;
+  if constexpr (U > 0) load_all(0, UC);
   if constexpr (NORM) {
-    float ss = 0.f;
+    float ss[NR];
+#pragma unroll
+    for (int i = 0; i < NR; ++i) ss[i] = 0.f;
     if constexpr (U > 0) {
 #pragma unroll
-      for (int u = 0; u < UC; ++u) load(u, v[u]);
+      for (int i = 0; i < NR; ++i)
 #pragma unroll
-      for (int u = 0; u < UC; ++u)
+        for (int u = 0; u < UC; ++u)
 #pragma unroll
-        for (int k = 0; k < V; ++k) ss = fmaf(v[u][k], v[u][k], ss);
+          for (int k = 0; k < V; ++k) ss[i] = fmaf(v[i][u][k], v[i][u][k], ss[i]);
     } else {
       for (int u = 0; u < nu; ++u) {
-        load(u, v[0]);
+        load_all(u, 1);
 #pragma unroll
-        for (int k = 0; k < V; ++k) ss = fmaf(v[0][k], v[0][k], ss);
+        for (int k = 0; k < V; ++k) ss[0] = fmaf(v[0][0][k], v[0][0][k], ss[0]);
       }
     }
-    ss = row_sum<TPR>(ss, red);
-    inv = 1.f / sqrtf(ss / static_cast<float>(a.cols) + a.eps);
-    if (t == 0 && a.inv) a.inv[row] = inv;
-  } else if constexpr (U > 0) {
 #pragma unroll
-    for (int u = 0; u < UC; ++u) load(u, v[u]);
+    for (int i = 0; i < NR; ++i) {
+      inv[i] = 1.f / sqrtf(row_sum<TPR>(ss[i], red) / static_cast<float>(a.cols) + a.eps);
+      if (t == 0 && i < nr && a.inv) a.inv[row0 + i] = inv[i];
+    }
   }
-  // y = gamma h s of vector u, in place
-  auto scale = [&](int u, float (&o)[V]) {
-    const int i = u * TPR + t;
-    if (!NORM || i >= nv) return;
-    const float* g = a.gamma + static_cast<long>(i) * V;
+  // y = gamma h s of vector u, in place, for all NR rows (U = 0: of the one vector at hand)
+  auto scale = [&](int u, int slot) {
+    const int c = u * TPR + t;
+    if (!NORM || c >= nv) return;
+    const float* gp = a.gamma + static_cast<long>(c) * V;
+    float g[V];
     if constexpr (V >= 4) {
 #pragma unroll
-      for (int k = 0; k < V; k += 4) {
-        const float4 gv = *reinterpret_cast<const float4*>(g + k);
-        o[k] = o[k] * inv * gv.x;
-        o[k + 1] = o[k + 1] * inv * gv.y;
-        o[k + 2] = o[k + 2] * inv * gv.z;
-        o[k + 3] = o[k + 3] * inv * gv.w;
-      }
+      for (int k = 0; k < V; k += 4) *reinterpret_cast<float4*>(g + k) = *reinterpret_cast<const float4*>(gp + k);
     } else {
-      o[0] = o[0] * inv * g[0];
+      g[0] = gp[0];
     }
+#pragma unroll
+    for (int i = 0; i < NR; ++i)
+#pragma unroll
+      for (int k = 0; k < V; ++k) v[i][slot][k] = v[i][slot][k] * inv[i] * g[k];
   };
   // Largest magnitude's bits; fmaxf passes NaN over, and infinities are looked for only where one shows.
   auto absmax = [&](const float (&o)[V]) {
@@ -180,83 +199,96 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) rows_fwd_kernel(const N
     return m;
   };
   constexpr uint32_t kInf = 0x7f800000u;
-  uint32_t rowbyte = 0u;
-  bool finite = true;
+  uint32_t rowbyte[NR];
+  bool rowfinite[NR];
   if (a.q && a.group == 0) {
-    uint32_t m = 0u;
     if constexpr (U > 0) {
 #pragma unroll
-      for (int u = 0; u < UC; ++u) {
-        scale(u, v[u]);
-        m = max(m, absmax(v[u]));
-      }
-    } else {
-      for (int u = 0; u < nu; ++u) {
-        reload(u, v[0]);
-        scale(u, v[0]);
-        m = max(m, absmax(v[0]));
-      }
+      for (int u = 0; u < UC; ++u) scale(u, u);
     }
-    m = row_max<TPR>(m, reinterpret_cast<uint32_t*>(red));
-    if (m == kInf) {  // the same for the whole row
-      finite = false;
-      m = 0u;
+#pragma unroll
+    for (int i = 0; i < NR; ++i) {
+      uint32_t m = 0u;
       if constexpr (U > 0) {
 #pragma unroll
-        for (int u = 0; u < UC; ++u) m = max(m, absmax_finite(v[u]));
+        for (int u = 0; u < UC; ++u) m = max(m, absmax(v[i][u]));
       } else {
         for (int u = 0; u < nu; ++u) {
-          reload(u, v[0]);
-          scale(u, v[0]);
-          m = max(m, absmax_finite(v[0]));
+          reload(u);
+          scale(u, 0);
+          m = max(m, absmax(v[0][0]));
         }
       }
       m = row_max<TPR>(m, reinterpret_cast<uint32_t*>(red));
-    }
-    rowbyte = q8_scale_byte(m);
-    if (t == 0) a.qs[row * a.ng] = static_cast<uint8_t>(rowbyte);
-  }
-  T* y = a.y ? static_cast<T*>(a.y) + row * a.ldy : nullptr;
-  uint8_t* q = a.q ? a.q + row * a.ldq : nullptr;
-  auto finish = [&](int u, float (&o)[V]) {
-    const int i = u * TPR + t;
-    if (y && i < nv) {
-      T e[V];
+      rowfinite[i] = m != kInf;
+      if (m == kInf) {  // the same for the whole row
+        m = 0u;
+        if constexpr (U > 0) {
 #pragma unroll
-      for (int k = 0; k < V; ++k) e[k] = from_f<T>(o[k]);
-      st_vec<T, V>(y + static_cast<long>(i) * V, e);
-    }
-    if (q) {
-      uint32_t byte = rowbyte;
-      if (a.group != 0) {
-        auto group_max = [](uint32_t m) {
-#pragma unroll
-          for (int s = 1; s < kQ8Group / V; s <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, s));
-          return m;
-        };
-        uint32_t m = group_max(absmax(o));
-        finite = true;
-        if (__any_sync(0xffffffffu, m == kInf)) {
-          finite = false;
-          m = group_max(absmax_finite(o));
+          for (int u = 0; u < UC; ++u) m = max(m, absmax_finite(v[i][u]));
+        } else {
+          for (int u = 0; u < nu; ++u) {
+            reload(u);
+            scale(u, 0);
+            m = max(m, absmax_finite(v[0][0]));
+          }
         }
-        byte = q8_scale_byte(m);
-        if (i < nv && (t & (kQ8Group / V - 1)) == 0) a.qs[row * a.ng + i / (kQ8Group / V)] = static_cast<uint8_t>(byte);
+        m = row_max<TPR>(m, reinterpret_cast<uint32_t*>(red));
       }
-      if (i < nv) q8_store<V>(q + static_cast<long>(i) * V, o, q8_inv_scale(byte), finite);
+      rowbyte[i] = q8_scale_byte(m);
+      if (t == 0 && i < nr) a.qs[(row0 + i) * a.ng] = static_cast<uint8_t>(rowbyte[i]);
+    }
+  }
+  auto finish = [&](int u, int slot) {
+    const int c = u * TPR + t;
+#pragma unroll
+    for (int i = 0; i < NR; ++i) {
+      const bool on = i < nr && c < nv;
+      float(&o)[V] = v[i][slot];
+      if (a.y && on) {
+        T e[V];
+#pragma unroll
+        for (int k = 0; k < V; ++k) e[k] = from_f<T>(o[k]);
+        st_vec<T, V>(static_cast<T*>(a.y) + (row0 + i) * a.ldy + static_cast<long>(c) * V, e);
+      }
+      if (a.q) {
+        uint32_t byte = rowbyte[i];
+        bool finite = rowfinite[i];
+        if (a.group != 0) {
+          auto group_max = [](uint32_t m) {
+#pragma unroll
+            for (int s = 1; s < kQ8Group / V; s <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, s));
+            return m;
+          };
+          uint32_t m = group_max(absmax(o));
+          finite = true;
+          if (__any_sync(0xffffffffu, m == kInf)) {
+            finite = false;
+            m = group_max(absmax_finite(o));
+          }
+          byte = q8_scale_byte(m);
+          if (on && (t & (kQ8Group / V - 1)) == 0)
+            a.qs[(row0 + i) * a.ng + c / (kQ8Group / V)] = static_cast<uint8_t>(byte);
+        }
+        if (on) q8_store<V>(a.q + (row0 + i) * a.ldq + static_cast<long>(c) * V, o, q8_inv_scale(byte), finite);
+      }
     }
   };
   if constexpr (U > 0) {
 #pragma unroll
     for (int u = 0; u < UC; ++u) {
-      if (!(a.q && a.group == 0)) scale(u, v[u]);
-      finish(u, v[u]);
+      if (!(a.q && a.group == 0)) scale(u, u);
+      finish(u, u);
     }
   } else {
     for (int u = 0; u < nu; ++u) {
-      reload(u, v[0]);
-      scale(u, v[0]);
-      finish(u, v[0]);
+      if constexpr (NORM) {
+        reload(u);
+        scale(u, 0);
+      } else {
+        reload(u);
+      }
+      finish(u, 0);
     }
   }
 }
@@ -264,20 +296,20 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) rows_fwd_kernel(const N
 template <typename T, int V, bool NORM>
 cudaError_t rows_fwd(const NormArgs& a, cudaStream_t st) {
   const int nv = (a.cols + V - 1) / V;
-#define ROWS_FWD(TPR, U)                                                                       \
-  do {                                                                                         \
-    constexpr int nt = TPR < 256 ? 256 : TPR, rpb = nt / TPR;                                  \
-    return launch_k(rows_fwd_kernel<T, V, TPR, U, NORM>, dim3(static_cast<unsigned>((a.rows + rpb - 1) / rpb)), \
-                    dim3(nt), 0, st, 1, a);                                                    \
+#define ROWS_FWD(TPR, U, NR)                                                                                        \
+  do {                                                                                                              \
+    constexpr int nt = TPR < 256 ? 256 : TPR, rpb = nt / TPR * NR;                                                  \
+    return launch_k(rows_fwd_kernel<T, V, TPR, U, NR, NORM>, dim3(static_cast<unsigned>((a.rows + rpb - 1) / rpb)), \
+                    dim3(nt), 0, st, 1, a);                                                                         \
   } while (0)
-  if (nv <= 32) ROWS_FWD(32, 1);
-  if (nv <= 64) ROWS_FWD(32, 2);
-  if (nv <= 128) ROWS_FWD(32, 4);
-  if (nv <= 256) ROWS_FWD(256, 1);
-  if (nv <= 512) ROWS_FWD(256, 2);
-  if (nv <= 1024) ROWS_FWD(256, 4);
-  if (nv <= 2048) ROWS_FWD(512, 4);
-  ROWS_FWD(1024, 0);
+  if (nv <= 32) ROWS_FWD(32, 1, 4);
+  if (nv <= 64) ROWS_FWD(32, 2, 2);
+  if (nv <= 128) ROWS_FWD(32, 4, 1);
+  if (nv <= 256) ROWS_FWD(256, 1, 1);
+  if (nv <= 512) ROWS_FWD(256, 2, 1);
+  if (nv <= 1024) ROWS_FWD(256, 4, 1);
+  if (nv <= 2048) ROWS_FWD(512, 4, 1);
+  ROWS_FWD(1024, 0, 1);
 #undef ROWS_FWD
 }
 
@@ -467,7 +499,7 @@ cudaError_t norm_bwd(const NormBwdArgs& a, int grid, cudaStream_t st) {
 
 // ------------------------------------------------------------------ decode / move
 // V elements a thread and step of a [rows][cols] matrix, dense steps of the grid (E4M3 source: V bytes and
-// their scale; 16 with a 16-bit output, two vectors). rows * ceil(cols / V) below 2^31 (see to_rows).
+// their scale, two output vectors). rows * ceil(cols / V) below 2^31 (see to_rows).
 template <typename T, int V, bool Q>
 __global__ void __launch_bounds__(256) to_rows_kernel(const void* x, long ldx, const uint8_t* scale, int group, int ng,
                                                       uint32_t total, int cols, FastDiv div_nv, T* out, long ldo) {
@@ -501,8 +533,13 @@ __global__ void __launch_bounds__(256) to_rows_kernel(const void* x, long ldx, c
       if constexpr (Q) {
         float v[V];
         q8_values<V>(raw[i], v, sc[i]);
+        if (sc[i] > q8_safe_scale<T>()) {
 #pragma unroll
-        for (int k = 0; k < V; ++k) e[i][k] = from_q8<T>(v[k]);
+          for (int k = 0; k < V; ++k) e[i][k] = from_q8<T>(v[k]);
+        } else {
+#pragma unroll
+          for (int k = 0; k < V; ++k) e[i][k] = from_f<T>(v[k]);
+        }
       }
       T* o = out + row[i] * ldo + c[i];
 #pragma unroll
@@ -572,9 +609,9 @@ struct DactArgs {
 // the unrounded dz in registers, joined over the 8 row lanes at the end. ZK: 0 no activation, 1 z in T,
 // 2 z as E4M3.
 template <typename T, int V, int ZK>
-__global__ void __launch_bounds__(256, 4) dact_kernel(const DactArgs a) {
+__global__ void __launch_bounds__(256, 3) dact_kernel(const DactArgs a) {
   pdl_entry();
-  constexpr int N = 4;  // rows in flight
+  constexpr int N = ZK == 2 ? 3 : 4;  // rows in flight
   __shared__ float sums[8][32 * V];
   const int lane = threadIdx.x & 31, rl = threadIdx.x >> 5;
   const int c = (static_cast<int>(blockIdx.x) * 32 + lane) * V;
@@ -617,13 +654,23 @@ __global__ void __launch_bounds__(256, 4) dact_kernel(const DactArgs a) {
           }
           if constexpr (ZK == 2) q8_values<V>(q[i], f, q8_scale(sb[i]));
           T o[V];
+          // products are not contracted into the sums: the column sums are the same whether dz is written or not
+          if constexpr (V == 1) {
+            float v = to_f(d[i][0]);
+            if constexpr (ZK) v = __fmul_rn(v, dense_dact<decltype(act)::value>(make_float2(f[0], 0.f)).x);
+            acc[0] += v;
+            o[0] = from_f<T>(v);
+          } else {
 #pragma unroll
-          for (int k = 0; k < V; ++k) {
-            float v = to_f(d[i][k]);
-            // not contracted into the sum: the column sums are the same whether dz is written or not
-            if constexpr (ZK) v = __fmul_rn(v, dense_dact<decltype(act)::value>(f[k]));
-            acc[k] += v;
-            o[k] = from_f<T>(v);
+            for (int k = 0; k < V; k += 2) {
+              float2 v = make_float2(to_f(d[i][k]), to_f(d[i][k + 1]));
+              if constexpr (ZK) v = __fmul2_rn(v, dense_dact<decltype(act)::value>(make_float2(f[k], f[k + 1])));
+              const float2 sum = __fadd2_rn(make_float2(acc[k], acc[k + 1]), v);
+              acc[k] = sum.x;
+              acc[k + 1] = sum.y;
+              o[k] = from_f<T>(v.x);
+              o[k + 1] = from_f<T>(v.y);
+            }
           }
           if (dz) st_vec<T, V>(dz + ri * a.lddz, o);
         }
