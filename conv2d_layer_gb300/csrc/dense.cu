@@ -131,6 +131,26 @@ bool encode_operand(CUtensorMap* m, const void* base, int type, long rows, long 
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Output [splits][rows][cols] of row length ld for the pair kernel's stores: boxes of 32 rows x RB bytes, swizzled
+// over RB bytes (32 or 64).
+bool encode_output(CUtensorMap* m, const void* base, int type, long rows, long cols, long ld, long splits) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  const int es = type == CONV2D_E4M3 ? 1 : type == CONV2D_FP32 ? 4 : 2;
+  const int rb = type == CONV2D_E4M3 ? 32 : 64;
+  cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(splits)};
+  cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld) * es, static_cast<cuuint64_t>(ld) * rows * es};
+  cuuint32_t box[3] = {static_cast<cuuint32_t>(rb / es), 32, 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  const CUtensorMapDataType dt = type == CONV2D_E4M3   ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                                 : type == CONV2D_FP32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                 : type == CONV2D_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                       : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  return fn(m, dt, 3, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            rb == 32 ? CU_TENSOR_MAP_SWIZZLE_32B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // An operand ready for the tensor core: type BF16 / FP16 / E4M3, row length a multiple of 16 bytes.
 struct Operand {
   const void* data;
@@ -151,9 +171,16 @@ int run_gemm(DenseGemmParams& p, const GemmPlan& g, const Operand& r, const Oper
   p.fmt = r.type == CONV2D_BF16 ? 1u : 0u;
   p.m = r_mn ? r.cols : r.rows;
   p.n = static_cast<int>(c_mn ? c.cols : c.rows);
-  p.vec_out = p.ldo % (p.out_f32 ? 4 : 8) == 0;
   p.vec_res = p.ldr % 8 == 0;
-  p.vec_z = p.ldz % (p.zq ? 16 : 8) == 0;
+  if (g.pair) {
+    const int zt = p.zq ? static_cast<int>(CONV2D_E4M3) : dt, ot = p.out_f32 ? static_cast<int>(CONV2D_FP32) : dt;
+    const void* z = p.zq ? p.zq : p.z;
+    p.tma_out = p.ldo % (p.out_f32 ? 4 : 8) == 0;
+    p.tma_z = z && p.ldz % (p.zq ? 16 : 8) == 0;
+    if ((p.tma_out && !encode_output(&p.tout, p.out, ot, p.m, p.n, p.ldo, g.splits)) ||
+        (p.tma_z && !encode_output(&p.tz, z, zt, p.m, p.n, p.ldz, 1)))
+      return CONV2D_ERR_CUDA;
+  }
   p.l_tiles = g.l_tiles;
   p.c_tiles = g.c_tiles;
   p.splits = g.splits;

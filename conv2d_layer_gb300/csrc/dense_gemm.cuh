@@ -12,8 +12,8 @@
 //   dense_pair_kernel     for outputs of many tiles: persistent CTA pairs (cta_group::2), 256 rows x BN columns a
 //                         unit, two accumulators, so that the epilogue of a unit runs under the next one's
 //                         MMAs. Rows of the output are accumulator lanes: a thread holds 32 neighbouring
-//                         columns of its row (an 8-bit group), packs them, and the warp turns 32 rows x
-//                         128 bytes around in shared memory so that memory is read and written in whole lines
+//                         columns of its row (an 8-bit group) and packs them into a swizzled buffer of 32
+//                         rows x 64 bytes, which a TMA store writes
 //   dense_cluster_kernel  for few rows or few tiles: one unit for a cluster of `cluster` CTAs, which split the
 //                         K loop and join their sums through distributed shared memory in rank order. Columns
 //                         of the output are accumulator lanes (128), rows its columns (16 to 128), so that one
@@ -39,6 +39,8 @@ __host__ __device__ constexpr bool dense_c_mn(int mode) { return mode != kDenseF
 
 struct DenseGemmParams {
   CUtensorMap tl, tc;   // the operands whose rows are the accumulator's lanes / columns
+  // pair kernel: out and z (zq) as {columns, rows, splits} for stores of 32 rows x 64 bytes (zq: 32 bytes)
+  CUtensorMap tout, tz;
   uint32_t fmt;         // instruction descriptor's operand format: fp16 0, bf16 1, e4m3 0
   int n;                // columns of the output
   long m;               // rows of the output
@@ -59,7 +61,7 @@ struct DenseGemmParams {
   long split_stride;
   void* out;
   long ldo;
-  int vec_out, vec_res, vec_z;  // rows of out / res / z (zq) start on 16-byte boundaries
+  int tma_out, vec_res, tma_z;  // rows of out / res / z (zq) start on 16-byte boundaries: tout, tz are set
   int* err;
 };
 
@@ -78,6 +80,18 @@ __device__ __forceinline__ void mma_f8_pair(uint32_t d, uint64_t a, uint64_t b, 
       "l"(a), "l"(b), "r"(idesc), "r"(acc)
       : "memory");
 }
+
+// 3-D tiled store of a box from shared memory; part of the thread's current bulk group.
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* m, uint32_t src, int c0, int c1, int c2) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+                   reinterpret_cast<uint64_t>(m)),
+               "r"(src), "r"(c0), "r"(c1), "r"(c2)
+               : "memory");
+}
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+// Wait until this thread's bulk stores have read their shared memory / have completed.
+__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
 // Arrive on an mbarrier of the cluster (shared::cluster address) without ordering this thread's memory accesses.
 __device__ __forceinline__ void mbar_arrive_relaxed(uint32_t caddr) {
@@ -169,44 +183,56 @@ __device__ __forceinline__ uint4 lds128(uint32_t a) {
 }
 __device__ __forceinline__ void sts128(uint32_t a, const uint4& v) { st_shared_v4(a, v.x, v.y, v.z, v.w); }
 
-// The buffer's rows (nr of them) x nc elements of type E to memory at g (row length ld), whole row segments at a
-// time; vec: rows start on 16-byte boundaries. accumulate: added to what is there (in fp32).
+// The buffer's rows (nr of them) x nc elements of type E to memory at g (row length ld), element by element along
+// the rows: for rows that start off 16-byte boundaries, and for accumulating (added in fp32 to what is there).
 template <typename E, int RB>
-__device__ __forceinline__ void rows_out(uint32_t buf, E* g, long ld, int nr, int nc, bool vec, bool accumulate,
-                                         int lane) {
-  constexpr int PE = 16 / static_cast<int>(sizeof(E)), PR = RB / 16;  // elements a piece, pieces a row
-  constexpr int RI = 32 / PR;                                         // rows an instruction
-  const int j = lane % PR;
-  const bool whole = vec && (j + 1) * PE <= nc;
-  E* o = g + (lane / PR) * ld + j * PE;
-#pragma unroll
-  for (int i = 0; i < 32 / RI; ++i, o += RI * ld) {
-    const int r = i * RI + lane / PR;
-    if (r >= nr || j * PE >= nc) continue;
-    uint4 w = lds128(buf + row_piece<RB>(r, j));
-    if constexpr (sizeof(E) > 1) {
-      if (accumulate) {
-        E* e = reinterpret_cast<E*>(&w);
-        if (whole) {
-          uint4 old = *reinterpret_cast<const uint4*>(o);
-          const E* f = reinterpret_cast<const E*>(&old);
-#pragma unroll
-          for (int k = 0; k < PE; ++k) e[k] = from_f<E>(to_f(f[k]) + to_f(e[k]));
-        } else {
-#pragma unroll
-          for (int k = 0; k < PE; ++k)
-            if (j * PE + k < nc) e[k] = from_f<E>(to_f(o[k]) + to_f(e[k]));
-        }
-      }
-    }
-    if (whole) {
-      *reinterpret_cast<uint4*>(o) = w;
+__device__ __forceinline__ void rows_out(uint32_t buf, E* g, long ld, int nr, int nc, bool accumulate, int lane) {
+  constexpr int PE = 16 / static_cast<int>(sizeof(E));  // elements a piece
+  constexpr int W = RB / static_cast<int>(sizeof(E));   // elements a row: 32 or 16
+  const int col = lane % W;
+  if (col >= nc) return;
+#pragma unroll 4
+  for (int r = lane / W; r < nr; r += 32 / W) {
+    const uint32_t at = buf + row_piece<RB>(r, col / PE) + (col % PE) * static_cast<uint32_t>(sizeof(E));
+    E e;
+    if constexpr (sizeof(E) == 4) {
+      asm volatile("ld.shared.f32 %0, [%1];" : "=f"(e) : "r"(at) : "memory");
+    } else if constexpr (sizeof(E) == 2) {
+      uint16_t b;
+      asm volatile("ld.shared.u16 %0, [%1];" : "=h"(b) : "r"(at) : "memory");
+      e = *reinterpret_cast<const E*>(&b);
     } else {
-      const E* e = reinterpret_cast<const E*>(&w);
-#pragma unroll
-      for (int k = 0; k < PE; ++k)
-        if (j * PE + k < nc) o[k] = e[k];
+      uint32_t b;
+      asm volatile("ld.shared.u8 %0, [%1];" : "=r"(b) : "r"(at) : "memory");
+      e = static_cast<E>(b);
     }
+    E* o = g + r * ld + col;
+    if constexpr (sizeof(E) > 1) {
+      if (accumulate) e = from_f<E>(to_f(*o) + to_f(e));
+    }
+    *o = e;
+  }
+}
+// Takes the warp's buffer for writing: an earlier store has read it.
+__device__ __forceinline__ void buffer_take(int lane) {
+  if (lane == 0) bulk_wait_read();
+  __syncwarp();
+}
+// Stores the written buffer: by TMA (whole rows, clipped at the matrix's ends), or element by element.
+template <typename E, int RB>
+__device__ __forceinline__ void buffer_store(uint32_t buf, bool tma, const CUtensorMap* map, int n, long m0, int split,
+                                             E* g, long ld, int nr, int nc, bool accumulate, int lane) {
+  if (tma) {
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+      tma_store_3d(map, buf, n, static_cast<int>(m0), split);
+      bulk_commit();
+    }
+  } else {
+    __syncwarp();
+    rows_out<E, RB>(buf, g + m0 * ld + n, ld, nr, nc, accumulate, lane);
+    __syncwarp();
   }
 }
 // Packs 8 values as T.
@@ -301,17 +327,15 @@ __device__ __forceinline__ void pair_epilogue(const DenseGemmParams& p, uint32_t
           w[e] = q8_pack2(x[0] * inv, x[1] * inv) | q8_pack2(x[2] * inv, x[3] * inv) << 16;
         }
       }
+      buffer_take(lane);
       st_shared_v4(buf + row_piece<32>(lane, 0), w[0], w[1], w[2], w[3]);
       st_shared_v4(buf + row_piece<32>(lane, 1), w[4], w[5], w[6], w[7]);
-      __syncwarp();
-      rows_out<uint8_t, 32>(buf, p.zq + m0 * p.ldz + n, p.ldz, nr, nc, p.vec_z, false, lane);
-      __syncwarp();
+      buffer_store<uint8_t, 32>(buf, p.tma_z, &p.tz, n, m0, 0, p.zq, p.ldz, nr, nc, false, lane);
     } else if (p.z) {
+      buffer_take(lane);
 #pragma unroll
       for (int j = 0; j < 4; ++j) sts128(buf + row_piece<64>(lane, j), pack8<T>(v + 8 * j));
-      __syncwarp();
-      rows_out<T, 64>(buf, static_cast<T*>(p.z) + m0 * p.ldz + n, p.ldz, nr, nc, p.vec_z, false, lane);
-      __syncwarp();
+      buffer_store<T, 64>(buf, p.tma_z, &p.tz, n, m0, 0, static_cast<T*>(p.z), p.ldz, nr, nc, false, lane);
     }
     with_dense_act(p.act, [&](auto act) {
 #pragma unroll
@@ -321,6 +345,7 @@ __device__ __forceinline__ void pair_epilogue(const DenseGemmParams& p, uint32_t
         v[e + 1] = a.y;
       }
     });
+    buffer_take(lane);
     if (p.res) {
       if (vres) {
 #pragma unroll
@@ -345,33 +370,31 @@ __device__ __forceinline__ void pair_epilogue(const DenseGemmParams& p, uint32_t
     }
 #pragma unroll
     for (int j = 0; j < 4; ++j) sts128(buf + row_piece<64>(lane, j), pack8<T>(v + 8 * j));
-    __syncwarp();
-    rows_out<T, 64>(buf, static_cast<T*>(p.out) + m0 * p.ldo + n, p.ldo, nr, nc, p.vec_out, false, lane);
-    __syncwarp();
+    buffer_store<T, 64>(buf, p.tma_out, &p.tout, n, m0, 0, static_cast<T*>(p.out), p.ldo, nr, nc, false, lane);
   } else {
     uint32_t a[32];
     tmem_ld32(taddr, a);
     tmem_ld_wait32(a);
     release();
+    const bool tma = p.tma_out && !p.accumulate;
     if (p.out_f32) {
-      float* out = static_cast<float*>(p.out) + split * p.split_stride + m0 * p.ldo + n;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         if (16 * h >= nc) break;  // uniform
+        buffer_take(lane);
 #pragma unroll
         for (int j = 0; j < 4; ++j)
           st_shared_v4(buf + row_piece<64>(lane, j), a[16 * h + 4 * j], a[16 * h + 4 * j + 1], a[16 * h + 4 * j + 2],
                        a[16 * h + 4 * j + 3]);
-        __syncwarp();
-        rows_out<float, 64>(buf, out + 16 * h, p.ldo, nr, nc - 16 * h, p.vec_out, p.accumulate, lane);
-        __syncwarp();
+        buffer_store<float, 64>(buf, tma, &p.tout, n + 16 * h, m0, split,
+                                static_cast<float*>(p.out) + split * p.split_stride, p.ldo, nr, nc - 16 * h,
+                                p.accumulate, lane);
       }
     } else {
+      buffer_take(lane);
 #pragma unroll
       for (int j = 0; j < 4; ++j) sts128(buf + row_piece<64>(lane, j), pack8<T>(reinterpret_cast<const float*>(a) + 8 * j));
-      __syncwarp();
-      rows_out<T, 64>(buf, static_cast<T*>(p.out) + m0 * p.ldo + n, p.ldo, nr, nc, p.vec_out, p.accumulate, lane);
-      __syncwarp();
+      buffer_store<T, 64>(buf, tma, &p.tout, n, m0, 0, static_cast<T*>(p.out), p.ldo, nr, nc, p.accumulate, lane);
     }
   }
 }
@@ -466,6 +489,8 @@ __global__ void __launch_bounds__(kPairThreads, 1) dense_pair_kernel(const __gri
     fence_mbar_init();
     tma_prefetch_desc(&p.tl);
     tma_prefetch_desc(&p.tc);
+    if (p.tma_out) tma_prefetch_desc(&p.tout);
+    if (p.tma_z) tma_prefetch_desc(&p.tz);
   }
   if (warp == 1) {
     tmem_alloc_pair(slot, tcols);
@@ -593,6 +618,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) dense_pair_kernel(const __gri
                                  });
       }
     }
+    if (lane == 0) bulk_wait();  // the stores have read the buffers and are done
   }
   tc_fence_before();
   __syncthreads();
