@@ -96,19 +96,20 @@ GemmPlan plan_gemm(int mode, long m, long n, int kb, int max_kb, int sms) {
   const int stage = (128 + c_rows) * 128 * (best.pair ? kPairKps : 1);
   const int room = static_cast<int>(kMaxDynSmem) - 1536 - (best.pair ? kPairBuffers : 0);
   const long units = static_cast<long>(best.l_tiles) * best.c_tiles * best.splits;
+  const int join = best.cluster > 1 ? best.cluster * dense_own_cols(best.BN, best.cluster) * 512 : 0;
   if (best.pair) {
     best.grid = 2 * static_cast<int>(std::min<long>(units, sms / 2));
     best.stages = std::min(kDenseMaxStages, room / stage);
   } else {
     best.grid = static_cast<int>(units) * best.cluster;
     // more CTAs than SMs: two a SM, so that one's epilogue runs beside the other's loop
-    const int budget = best.grid > sms ? room / 2 - 1024 : room;
+    const int budget = (best.grid > sms ? room / 2 - 1024 : room) - join;
     const int need = static_cast<int>(ceil_div(best.kb_per_split, best.cluster));
     best.stages = std::max(2, std::min({kDenseMaxStages, budget / stage, need}));
-    if (best.cluster > 1) best.stages = std::max<int>(best.stages, static_cast<int>(ceil_div(best.BN * 512, stage)));
   }
   // alignment slack, barriers
-  best.smem = static_cast<size_t>(best.stages) * stage + 1024 + 512 + (best.pair ? kPairBuffers : 0);
+  best.smem = static_cast<size_t>(best.stages) * stage + 1024 + 512 +
+              (best.pair ? kPairBuffers : join);
   return best;
 }
 

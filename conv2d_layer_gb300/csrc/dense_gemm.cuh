@@ -98,9 +98,12 @@ __device__ __forceinline__ void mbar_arrive_relaxed(uint32_t caddr) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(caddr) : "memory");
 }
 
-__device__ __forceinline__ float ld_shared_cluster_f32(uint32_t caddr) {
+__device__ __forceinline__ void st_shared_cluster_f32(uint32_t caddr, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(caddr), "f"(v) : "memory");
+}
+__device__ __forceinline__ float ld_shared_f32(uint32_t addr) {
   float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(caddr) : "memory");
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
   return v;
 }
 
@@ -440,6 +443,9 @@ __device__ __forceinline__ void dense_mma(uint64_t l, uint64_t c, uint32_t d, ui
   }
 }
 
+// Columns of a unit that one CTA of its cluster joins: groups of four, owned in turn.
+__host__ __device__ constexpr int dense_own_cols(int BN, int cluster) { return (BN / 4 + cluster - 1) / cluster * 4; }
+
 // Unit u of the output: bands of 8 lane tiles are walked column tile by column tile, so that the units in
 // flight at one time share their operands in L2.
 __device__ __forceinline__ void dense_unit(const DenseGemmParams& p, int u, int& lt, int& ct, int& split) {
@@ -637,7 +643,10 @@ __global__ void __launch_bounds__(kClusterThreads, 1) dense_cluster_kernel(const
   const int BN = p.BN, S = p.stages, CL = p.cluster;
   const uint32_t l_bytes = 128 * 128, c_bytes = static_cast<uint32_t>(BN) * 128;
   const uint32_t stage_bytes = l_bytes + c_bytes;
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + S * stage_bytes);
+  // CL > 1: the sums that the cluster's CTAs hand this one, [CL][own_cols][128], behind the ring
+  const int own_cols = dense_own_cols(BN, CL);
+  const uint32_t join_bytes = CL > 1 ? static_cast<uint32_t>(CL * own_cols) * 512u : 0u;
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + S * stage_bytes + join_bytes);
   uint64_t* empty = full + kDenseMaxStages;
   uint64_t* tfull = empty + kDenseMaxStages;
   uint32_t* slot = reinterpret_cast<uint32_t*>(tfull + 1);
@@ -662,6 +671,7 @@ __global__ void __launch_bounds__(kClusterThreads, 1) dense_cluster_kernel(const
   }
   tc_fence_before();
   __syncthreads();
+  if (CL > 1) cluster_sync();  // the others have started: their shared memory may be written
   tc_fence_after();
   const uint32_t tmem = *slot;
   pdl_entry();  // the set-up above runs under the end of the kernel before
@@ -729,7 +739,7 @@ __global__ void __launch_bounds__(kClusterThreads, 1) dense_cluster_kernel(const
     if (__shfl_sync(0xffffffffu, ok, 0)) {
       tc_fence_after();
       const uint32_t t0 = tmem + (static_cast<uint32_t>(q * 32) << 16);
-      float* part = reinterpret_cast<float*>(smem);  // CL > 1: [BN][128] sums over the ring, which is drained
+      const uint32_t join = sbase + S * stage_bytes;
       for (int c = half * 16; c < BN; c += 32) {
         const long m0 = static_cast<long>(ct) * BN + c;
         if (m0 >= p.m) break;  // uniform
@@ -742,20 +752,29 @@ __global__ void __launch_bounds__(kClusterThreads, 1) dense_cluster_kernel(const
         if (CL == 1) {
           dense_epilogue<T, MODE, 16>(p, v, n, m0, split, nscale, bias);
         } else {
+          // columns are owned four at a time in turn; each goes to its owner's slot for this CTA
 #pragma unroll
-          for (int e = 0; e < 16; ++e) part[(c + e) * 128 + q * 32 + lane] = v[e];
+          for (int g = 0; g < 4; ++g) {
+            const int quad = c / 4 + g;
+            const uint32_t at = join + static_cast<uint32_t>(((rank * own_cols + quad / CL * 4) * 128 + q * 32 + lane) * 4);
+            const uint32_t to = mapa_shared(at, static_cast<uint32_t>(quad % CL));
+#pragma unroll
+            for (int e = 0; e < 4; ++e) st_shared_cluster_f32(to + e * 512, v[4 * g + e]);
+          }
         }
       }
     }
   }
   if (CL > 1) {
     __syncthreads();
-    cluster_sync();  // every CTA's sums are written
-    // jobs of 4 columns x 32 lanes, spread over the cluster's warps
+    cluster_sync();  // every CTA's sums have arrived; from here on a CTA reads its own shared memory only
+    // jobs of 4 columns x 32 lanes; the sums are added in rank order
     const int nc = static_cast<int>(min(static_cast<long>(BN), p.m - static_cast<long>(ct) * BN));
-    const int jobs = (nc + 3) / 4 * 4;
-    for (int j = rank + CL * warp; j < jobs; j += CL * (kClusterThreads / 32)) {
-      const int q = j & 3, c = (j >> 2) * 4;
+    const int quads = (nc + 3) / 4;
+    const int own = (quads - rank + CL - 1) / CL;  // quads rank, rank + CL, ...
+    const uint32_t join = sbase + S * stage_bytes;
+    for (int j = warp; j < own * 4; j += kClusterThreads / 32) {
+      const int q = j & 3, i = j >> 2;
       const int n = lt * 128 + q * 32 + lane;
       float nscale = 1.f, bias = 0.f;
       if (MODE == kDenseForward && n < p.n) {
@@ -763,17 +782,14 @@ __global__ void __launch_bounds__(kClusterThreads, 1) dense_cluster_kernel(const
         if (p.bias) bias = p.bias[n];
       }
       float v[4] = {0.f, 0.f, 0.f, 0.f};
-      const uint32_t off = sbase + static_cast<uint32_t>((c * 128 + q * 32 + lane) * 4);
+      const uint32_t at = join + static_cast<uint32_t>((i * 4 * 128 + q * 32 + lane) * 4);
 #pragma unroll 4
       for (int k = 0; k < CL; ++k) {
-        const uint32_t at = mapa_shared(off, static_cast<uint32_t>(k));
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] += ld_shared_cluster_f32(at + e * 512);
+        for (int e = 0; e < 4; ++e) v[e] += ld_shared_f32(at + static_cast<uint32_t>((k * own_cols + e) * 512));
       }
-      dense_epilogue<T, MODE, 4>(p, v, n, static_cast<long>(ct) * BN + c, split, nscale, bias);
+      dense_epilogue<T, MODE, 4>(p, v, n, static_cast<long>(ct) * BN + (i * CL + rank) * 4, split, nscale, bias);
     }
-    __syncthreads();
-    cluster_sync();  // nobody reads this CTA's sums any more
   }
   tc_fence_before();
   __syncthreads();
