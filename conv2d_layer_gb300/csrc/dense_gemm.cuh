@@ -47,6 +47,7 @@ struct DenseGemmParams {
   int l_tiles, c_tiles, splits;
   int kb_total, kb_per_split;  // k-blocks of 128 bytes: 64 16-bit or 128 8-bit elements
   int BN, stages, cluster;
+  int kps;  // k-blocks a stage of the cluster kernel
   // kDenseForward: v = acc * ns[n] * ms[m] + bias[n]; z = v; out = act(v) + res
   const uint8_t *ns, *ms;  // scale bytes of 8-bit operands (both or neither)
   const float* bias;
@@ -642,7 +643,8 @@ __global__ void __launch_bounds__(kClusterThreads, 1) dense_cluster_kernel(const
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int BN = p.BN, S = p.stages, CL = p.cluster;
   const uint32_t l_bytes = 128 * 128, c_bytes = static_cast<uint32_t>(BN) * 128;
-  const uint32_t stage_bytes = l_bytes + c_bytes;
+  const int KPS = p.kps;
+  const uint32_t sub_bytes = l_bytes + c_bytes, stage_bytes = KPS * sub_bytes;
   // CL > 1: the sums that the cluster's CTAs hand this one, [CL][own_cols][128], behind the ring
   const int own_cols = dense_own_cols(BN, CL);
   const uint32_t join_bytes = CL > 1 ? static_cast<uint32_t>(CL * own_cols) * 512u : 0u;
@@ -689,20 +691,24 @@ __global__ void __launch_bounds__(kClusterThreads, 1) dense_cluster_kernel(const
       uint32_t par = 0;
       const int kelems = FP8 ? 128 : 64;
       int kb = kb0;
-      for (; kb < kb1; ++kb) {
+      for (; kb < kb1; kb += KPS) {
         if (!wait(&empty[s], par ^ 1, p.err, kSiteDenseEmpty)) break;
-        mbar_arrive_expect_tx(&full[s], stage_bytes);
-        const uint32_t l0 = sbase + s * stage_bytes;
-        dense_load<false, LMN>(&p.tl, l0, &full[s], 0u, kb * kelems, lt * 128, 128);
-        dense_load<false, CMN>(&p.tc, l0 + l_bytes, &full[s], 0u, kb * kelems, ct * BN, BN);
+        const int nk = min(KPS, kb1 - kb);
+        mbar_arrive_expect_tx(&full[s], nk * sub_bytes);
+        for (int i = 0; i < nk; ++i) {
+          const uint32_t l0 = sbase + s * stage_bytes + i * sub_bytes;
+          dense_load<false, LMN>(&p.tl, l0, &full[s], 0u, (kb + i) * kelems, lt * 128, 128);
+          dense_load<false, CMN>(&p.tc, l0 + l_bytes, &full[s], 0u, (kb + i) * kelems, ct * BN, BN);
+        }
         if (++s == S) {
           s = 0;
           par ^= 1;
         }
       }
       if (kb < kb1) {  // gave up: the copies of the stages before land before the CTA goes on
-        for (int i = min(S, kb - kb0); i > 0; --i) {
-          const int j = (kb - kb0) - i;
+        const int n = (kb - kb0) / KPS;  // stages filled
+        for (int i = min(S, n); i > 0; --i) {
+          const int j = n - i;
           (void)wait(&full[j % S], static_cast<uint32_t>(j / S) & 1u, p.err, kSiteDenseFull);
         }
       }
@@ -713,10 +719,12 @@ __global__ void __launch_bounds__(kClusterThreads, 1) dense_cluster_kernel(const
       const uint64_t l = dense_desc<LMN>(sbase), c = dense_desc<CMN>(sbase + l_bytes);
       int s = 0;
       uint32_t par = 0;
-      for (int kb = kb0; kb < kb1; ++kb) {
+      for (int kb = kb0; kb < kb1; kb += KPS) {
         if (!wait(&full[s], par, p.err, kSiteDenseFull)) break;
         tc_fence_after();
-        dense_mma<false, FP8, LMN, CMN>(l, c, tmem, s * stage_bytes, idesc, kb > kb0);
+        const int nk = min(KPS, kb1 - kb);
+        for (int i = 0; i < nk; ++i)
+          dense_mma<false, FP8, LMN, CMN>(l, c, tmem, s * stage_bytes + i * sub_bytes, idesc, kb + i > kb0);
         mma_commit(&empty[s]);
         if (++s == S) {
           s = 0;
