@@ -66,6 +66,14 @@ struct DenseGemmParams {
   int* err;
 };
 
+// One thread of a converged warp, in a way that tells the compiler so: the operands of the copies and MMAs it
+// issues then stay in uniform registers.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t ok;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok));
+  return ok != 0;
+}
+
 // ---------------------------------------------------------------- tcgen05 forms the conv layers do not use
 __device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
   asm volatile(
@@ -511,7 +519,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) dense_pair_kernel(const __gri
   pdl_entry();  // the set-up above runs under the end of the kernel before
 
   if (warp == 0) {
-    if (lane == 0) {
+    if (elect_one()) {
       int s = 0;
       uint32_t par = 0;
       bool alive = true;
@@ -554,7 +562,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) dense_pair_kernel(const __gri
       }
     }
   } else if (warp == 1) {
-    if (lane == 0 && leader) {
+    if (leader && elect_one()) {
       const uint32_t idesc = idesc_f32acc(256, BN, p.fmt, RMN, CMN);
       const uint64_t l = dense_desc<RMN>(sbase), c = dense_desc<CMN>(sbase + l_bytes);
       int s = 0, tc = 0;
@@ -686,7 +694,7 @@ __global__ void __launch_bounds__(kClusterThreads, 1) dense_cluster_kernel(const
   const int kb1 = s0 + static_cast<int>(static_cast<long>(s1 - s0) * (rank + 1) / CL);
 
   if (warp == 0) {
-    if (lane == 0) {
+    if (elect_one()) {
       int s = 0;
       uint32_t par = 0;
       const int kelems = FP8 ? 128 : 64;
@@ -714,7 +722,7 @@ __global__ void __launch_bounds__(kClusterThreads, 1) dense_cluster_kernel(const
       }
     }
   } else if (warp == 1) {
-    if (lane == 0) {
+    if (elect_one()) {
       const uint32_t idesc = idesc_f32acc(128, BN, p.fmt, LMN, CMN);
       const uint64_t l = dense_desc<LMN>(sbase), c = dense_desc<CMN>(sbase + l_bytes);
       int s = 0;
