@@ -35,7 +35,7 @@ constexpr int kFp32SplitKb = 64;
 
 struct GemmPlan {
   bool pair;
-  int BN, cluster, kps, splits, kb_total, kb_per_split, l_tiles, c_tiles, stages, grid;
+  int BN, cluster, splits, kb_total, kb_per_split, l_tiles, c_tiles, stages, grid;
   size_t smem;
 };
 
@@ -94,8 +94,7 @@ GemmPlan plan_gemm(int mode, long m, long n, int kb, int max_kb, int sms) {
   int c_rows = best.BN;  // columns of C a CTA brings: MN-major in whole panels of 64
   if (best.pair) c_rows = c_mn ? static_cast<int>(round_up(best.BN / 2, 64)) : best.BN / 2;
   const int need = static_cast<int>(ceil_div(best.kb_per_split, best.cluster));  // k-blocks of a CTA
-  best.kps = best.pair ? kPairKps : need >= 4 ? 2 : 1;
-  const int stage = (128 + c_rows) * 128 * best.kps;
+  const int stage = (128 + c_rows) * 128;
   const int room = static_cast<int>(kMaxDynSmem) - 1536 - (best.pair ? kPairBuffers : 0);
   const long units = static_cast<long>(best.l_tiles) * best.c_tiles * best.splits;
   const int join = best.cluster > 1 ? best.cluster * dense_own_cols(best.BN, best.cluster) * 512 : 0;
@@ -106,7 +105,7 @@ GemmPlan plan_gemm(int mode, long m, long n, int kb, int max_kb, int sms) {
     best.grid = static_cast<int>(units) * best.cluster;
     // more CTAs than SMs: two a SM, so that one's epilogue runs beside the other's loop
     const int budget = (best.grid > sms ? room / 2 - 1024 : room) - join;
-    best.stages = std::max(2, std::min({kDenseMaxStages, budget / stage, static_cast<int>(ceil_div(need, best.kps))}));
+    best.stages = std::max(2, std::min({kDenseMaxStages, budget / stage, need}));
   }
   // alignment slack, barriers
   best.smem = static_cast<size_t>(best.stages) * stage + 1024 + 512 +
@@ -191,7 +190,6 @@ int run_gemm(DenseGemmParams& p, const GemmPlan& g, const Operand& r, const Oper
   p.BN = g.BN;
   p.stages = g.stages;
   p.cluster = g.cluster;
-  p.kps = g.kps;
   p.err = dev->err;
   LAUNCH(name, st, g.pair ? launch_dense_pair(p, dt, mode, fp8, g.grid, g.smem, st)
                           : launch_dense_cluster(p, dt, mode, fp8, g.grid, g.smem, st));

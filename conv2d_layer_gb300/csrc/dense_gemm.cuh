@@ -29,7 +29,6 @@ constexpr int kClusterThreads = 320;  // TMA warp, MMA warp, 8 epilogue warps
 constexpr int kPairWarps = 16;        // epilogue warps of the pair kernel: four for each TMEM lane quarter
 constexpr int kPairThreads = 64 + 32 * kPairWarps;
 constexpr int kDenseMaxStages = 10;
-constexpr int kPairKps = 2;  // k-blocks per stage
 constexpr int kPairBuffers = kPairWarps * 2048;  // the pair kernel's epilogue: 32 rows x 64 bytes a warp
 enum : int { kSiteDenseFull = 11, kSiteDenseEmpty = 12, kSiteDenseTFull = 13, kSiteDenseTEmpty = 14 };
 // The three products: how the operands lie (R is MN-major for dW, C for dx and dW) and the epilogue.
@@ -47,7 +46,6 @@ struct DenseGemmParams {
   int l_tiles, c_tiles, splits;
   int kb_total, kb_per_split;  // k-blocks of 128 bytes: 64 16-bit or 128 8-bit elements
   int BN, stages, cluster;
-  int kps;  // k-blocks a stage of the cluster kernel
   // kDenseForward: v = acc * ns[n] * ms[m] + bias[n]; z = v; out = act(v) + res
   const uint8_t *ns, *ms;  // scale bytes of 8-bit operands (both or neither)
   const float* bias;
@@ -478,7 +476,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) dense_pair_kernel(const __gri
   // this CTA's halves: 128 rows and BN / 2 columns (whole panels of 64 when MN-major)
   const int c_rows = CMN ? (BN / 2 + 63) & ~63 : BN / 2;
   const uint32_t l_bytes = 128 * 128, c_bytes = static_cast<uint32_t>(c_rows) * 128;
-  const uint32_t sub_bytes = l_bytes + c_bytes, stage_bytes = kPairKps * sub_bytes;
+  const uint32_t stage_bytes = l_bytes + c_bytes;
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + S * stage_bytes + kPairBuffers);
   uint64_t* empty = full + kDenseMaxStages;
   uint64_t* tfull = empty + kDenseMaxStages;
@@ -529,22 +527,17 @@ __global__ void __launch_bounds__(kPairThreads, 1) dense_pair_kernel(const __gri
         dense_unit(p, u, lt, ct, split);
         const int kb0 = split * p.kb_per_split, kb1 = min(p.kb_total, kb0 + p.kb_per_split);
         const int lr = lt * 256 + static_cast<int>(rank) * 128, cr = ct * BN + static_cast<int>(rank) * (BN / 2);
-        for (int kb = kb0; kb < kb1; kb += kPairKps) {
-          const int nk = min(kPairKps, kb1 - kb);
+        for (int kb = kb0; kb < kb1; ++kb) {
           if (!wait(&empty[s], par ^ 1, p.err, kSiteDenseEmpty)) {
             alive = false;
             break;
           }
           // both members' loads complete on the even CTA's barrier, which expects them all
           const uint32_t bar = mapa_shared(smem_u32(&full[s]), 0);
-          if (leader) mbar_arrive_expect_tx(&full[s], 2 * nk * sub_bytes);
-#pragma unroll
-          for (int i = 0; i < kPairKps; ++i) {
-            if (i >= nk) break;
-            const uint32_t l0 = sbase + s * stage_bytes + i * sub_bytes;
-            dense_load<true, RMN>(&p.tl, l0, nullptr, bar, (kb + i) * kelems, lr, 128);
-            dense_load<true, CMN>(&p.tc, l0 + l_bytes, nullptr, bar, (kb + i) * kelems, cr, c_rows);
-          }
+          if (leader) mbar_arrive_expect_tx(&full[s], 2 * stage_bytes);
+          const uint32_t l0 = sbase + s * stage_bytes;
+          dense_load<true, RMN>(&p.tl, l0, nullptr, bar, kb * kelems, lr, 128);
+          dense_load<true, CMN>(&p.tc, l0 + l_bytes, nullptr, bar, kb * kelems, cr, c_rows);
           if (++s == S) {
             s = 0;
             par ^= 1;
@@ -575,18 +568,13 @@ __global__ void __launch_bounds__(kPairThreads, 1) dense_pair_kernel(const __gri
         const int buf = tc & 1;
         if (!wait(&tempty[buf], ((tc >> 1) & 1) ^ 1, p.err, kSiteDenseTEmpty)) break;
         tc_fence_after();
-        for (int kb = kb0; kb < kb1; kb += kPairKps) {
-          const int nk = min(kPairKps, kb1 - kb);
+        for (int kb = kb0; kb < kb1; ++kb) {
           if (!wait(&full[s], par, p.err, kSiteDenseFull)) {
             alive = false;
             break;
           }
           tc_fence_after();
-#pragma unroll
-          for (int i = 0; i < kPairKps; ++i) {
-            if (i >= nk) break;
-            dense_mma<true, FP8, RMN, CMN>(l, c, tmem + buf * BN, s * stage_bytes + i * sub_bytes, idesc, kb + i > kb0);
-          }
+          dense_mma<true, FP8, RMN, CMN>(l, c, tmem + buf * BN, s * stage_bytes, idesc, kb > kb0);
           mma_commit_pair(&empty[s]);
           if (++s == S) {
             s = 0;
@@ -651,8 +639,7 @@ __global__ void __launch_bounds__(kClusterThreads, 1) dense_cluster_kernel(const
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int BN = p.BN, S = p.stages, CL = p.cluster;
   const uint32_t l_bytes = 128 * 128, c_bytes = static_cast<uint32_t>(BN) * 128;
-  const int KPS = p.kps;
-  const uint32_t sub_bytes = l_bytes + c_bytes, stage_bytes = KPS * sub_bytes;
+  const uint32_t stage_bytes = l_bytes + c_bytes;
   // CL > 1: the sums that the cluster's CTAs hand this one, [CL][own_cols][128], behind the ring
   const int own_cols = dense_own_cols(BN, CL);
   const uint32_t join_bytes = CL > 1 ? static_cast<uint32_t>(CL * own_cols) * 512u : 0u;
@@ -699,22 +686,19 @@ __global__ void __launch_bounds__(kClusterThreads, 1) dense_cluster_kernel(const
       uint32_t par = 0;
       const int kelems = FP8 ? 128 : 64;
       int kb = kb0;
-      for (; kb < kb1; kb += KPS) {
+      for (; kb < kb1; ++kb) {
         if (!wait(&empty[s], par ^ 1, p.err, kSiteDenseEmpty)) break;
-        const int nk = min(KPS, kb1 - kb);
-        mbar_arrive_expect_tx(&full[s], nk * sub_bytes);
-        for (int i = 0; i < nk; ++i) {
-          const uint32_t l0 = sbase + s * stage_bytes + i * sub_bytes;
-          dense_load<false, LMN>(&p.tl, l0, &full[s], 0u, (kb + i) * kelems, lt * 128, 128);
-          dense_load<false, CMN>(&p.tc, l0 + l_bytes, &full[s], 0u, (kb + i) * kelems, ct * BN, BN);
-        }
+        mbar_arrive_expect_tx(&full[s], stage_bytes);
+        const uint32_t l0 = sbase + s * stage_bytes;
+        dense_load<false, LMN>(&p.tl, l0, &full[s], 0u, kb * kelems, lt * 128, 128);
+        dense_load<false, CMN>(&p.tc, l0 + l_bytes, &full[s], 0u, kb * kelems, ct * BN, BN);
         if (++s == S) {
           s = 0;
           par ^= 1;
         }
       }
       if (kb < kb1) {  // gave up: the copies of the stages before land before the CTA goes on
-        const int n = (kb - kb0) / KPS;  // stages filled
+        const int n = kb - kb0;  // stages filled
         for (int i = min(S, n); i > 0; --i) {
           const int j = n - i;
           (void)wait(&full[j % S], static_cast<uint32_t>(j / S) & 1u, p.err, kSiteDenseFull);
@@ -727,12 +711,10 @@ __global__ void __launch_bounds__(kClusterThreads, 1) dense_cluster_kernel(const
       const uint64_t l = dense_desc<LMN>(sbase), c = dense_desc<CMN>(sbase + l_bytes);
       int s = 0;
       uint32_t par = 0;
-      for (int kb = kb0; kb < kb1; kb += KPS) {
+      for (int kb = kb0; kb < kb1; ++kb) {
         if (!wait(&full[s], par, p.err, kSiteDenseFull)) break;
         tc_fence_after();
-        const int nk = min(KPS, kb1 - kb);
-        for (int i = 0; i < nk; ++i)
-          dense_mma<false, FP8, LMN, CMN>(l, c, tmem, s * stage_bytes + i * sub_bytes, idesc, kb + i > kb0);
+        dense_mma<false, FP8, LMN, CMN>(l, c, tmem, s * stage_bytes, idesc, kb > kb0);
         mma_commit(&empty[s]);
         if (++s == S) {
           s = 0;
