@@ -39,10 +39,12 @@ struct GemmPlan {
   size_t smem;
 };
 
-// Kernel, tile, cluster size and splits by an estimate of each choice's clocks: a CTA's k-block takes the
-// larger of its MMA time (128 x BN x 64 products at 4,096 a clock, half a pair's) and of bringing its operand
-// tiles (about 64 bytes a clock); units run in waves over the SMs. Weight gradients may be split over k, with fp32
-// partials in the workspace; max_kb: bound on one accumulator's k-blocks (0: none).
+// Kernel, tile, cluster size and splits by an estimate of each choice's clocks, fitted to timings of square and
+// skewed products (16 to 8,192 in each direction; the choice was within 10 % of the fastest in all of them). A
+// k-block takes a CTA what its MMAs or its operands' way from L2 take, whichever is longer, which comes to a line
+// in BN; a unit has a fixed cost (launch, first operands, epilogue); clusters pay for joining their sums. Units
+// run in waves over the SMs; the pair kernel hides its epilogue under the next unit's loop. Weight gradients may
+// be split over k, with fp32 partials in the workspace; max_kb: bound on one accumulator's k-blocks (0: none).
 GemmPlan plan_gemm(int mode, long m, long n, int kb, int max_kb, int sms) {
   const bool r_mn = dense_r_mn(mode), c_mn = dense_c_mn(mode), can_split = mode == kDenseDw;
   GemmPlan best = {};
@@ -60,13 +62,16 @@ GemmPlan plan_gemm(int mode, long m, long n, int kb, int max_kb, int sms) {
     g.c_tiles = static_cast<int>(ceil_div(pair ? n : m, BN));
     const double units = static_cast<double>(g.l_tiles) * g.c_tiles * g.splits;
     if (units * cl > INT_MAX / 4) return;
-    const int per_cta = pair ? BN / 2 : BN;  // columns of C a CTA loads
-    const double block = std::max(2.0 * BN, 2.0 * (128 + per_cta));
-    const double loop = static_cast<double>(ceil_div(g.kb_per_split, cl)) * block;
-    const double epi = 20.0 * BN;  // TMEM to memory
+    const double loop = static_cast<double>(ceil_div(g.kb_per_split, cl));
     double t;
-    if (pair) t = std::ceil(units / (sms / 2)) * std::max(loop, epi) + epi + 5000;
-    else t = std::ceil(units * cl / sms) * (loop + (cl > 1 ? epi / cl + 1500 : epi) + 1500) + 2000;
+    if (pair) {
+      const double epi = 14.0 * BN;
+      t = 8300 + 12.0 * BN + std::ceil(units / (sms / 2)) * std::max(loop * (188 + 1.35 * BN), epi);
+    } else {
+      // CTAs that are resident at once: clusters of 4 and 8 leave SMs of a GPC over
+      const double fit = cl == 8 ? sms * 15 / 19 : cl == 4 ? sms * 18 / 19 : sms;
+      t = std::ceil(units * cl / fit) * (6300 + 38.0 * BN + loop * (300 + 0.45 * BN) + (cl > 1 ? 3500 + 22.0 * BN : 0));
+    }
     if (g.splits > 1) t += 4000 + static_cast<double>(m) * n * 4 * 2 * g.splits / 3500;
     if (t < best_t) {
       best_t = t;
@@ -103,9 +108,7 @@ GemmPlan plan_gemm(int mode, long m, long n, int kb, int max_kb, int sms) {
     best.stages = std::min(kDenseMaxStages, room / stage);
   } else {
     best.grid = static_cast<int>(units) * best.cluster;
-    // more CTAs than SMs: two a SM, so that one's epilogue runs beside the other's loop
-    const int budget = (best.grid > sms ? room / 2 - 1024 : room) - join;
-    best.stages = std::max(2, std::min({kDenseMaxStages, budget / stage, need}));
+    best.stages = std::max(2, std::min({kDenseMaxStages, (room - join) / stage, need}));
   }
   // alignment slack, barriers
   best.smem = static_cast<size_t>(best.stages) * stage + 1024 + 512 +
