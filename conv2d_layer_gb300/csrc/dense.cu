@@ -65,14 +65,14 @@ GemmPlan plan_gemm(int mode, long m, long n, int kb, int max_kb, int sms) {
     const double loop = static_cast<double>(ceil_div(g.kb_per_split, cl));
     double t;
     if (pair) {
-      const double epi = 14.0 * BN;
+      const double epi = 1500 + 10.0 * BN;
       t = 8300 + 12.0 * BN + std::ceil(units / (sms / 2)) * std::max(loop * (188 + 1.35 * BN), epi);
     } else {
       // CTAs that are resident at once: clusters of 4 and 8 leave SMs of a GPC over
       const double fit = cl == 8 ? sms * 15 / 19 : cl == 4 ? sms * 18 / 19 : sms;
-      t = std::ceil(units * cl / fit) * (6300 + 38.0 * BN + loop * (300 + 0.45 * BN) + (cl > 1 ? 3500 + 22.0 * BN : 0));
+      t = std::ceil(units * cl / fit) * (6300 + 38.0 * BN + loop * ((r_mn ? 480 : 300) + 0.45 * BN) + (cl > 1 ? 3500 + 22.0 * BN : 0));
     }
-    if (g.splits > 1) t += 4000 + static_cast<double>(m) * n * 4 * 2 * g.splits / 3500;
+    if (g.splits > 1) t += 4000 + static_cast<double>(m) * n * 4 * 2 * g.splits / 7000;
     if (t < best_t) {
       best_t = t;
       best = g;

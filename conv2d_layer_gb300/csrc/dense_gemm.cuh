@@ -361,12 +361,18 @@ __device__ __forceinline__ void pair_epilogue(const DenseGemmParams& p, uint32_t
 #pragma unroll
         for (int i = 0; i < 4; ++i) sts128(buf + row_piece<64>(i * 8 + (lane >> 2), rj), res[i]);
       } else {
-        for (int row = 0; row < nr; ++row) {
-          if (lane >= nc) continue;
-          const T x = static_cast<const T*>(p.res)[(m0 + row) * p.ldr + n + lane];
-          asm volatile("st.shared.b16 [%0], %1;" ::"r"(buf + row_piece<64>(row, lane >> 3) + (lane & 7) * 2),
-                       "h"(*reinterpret_cast<const uint16_t*>(&x))
-                       : "memory");
+        const uint16_t* r = reinterpret_cast<const uint16_t*>(p.res) + m0 * p.ldr + n + lane;
+#pragma unroll
+        for (int i = 0; i < 32; i += 8) {  // eight rows in flight
+          uint16_t x[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            if (i + k < nr && lane < nc) x[k] = r[(i + k) * p.ldr];
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            if (i + k < nr && lane < nc)
+              asm volatile("st.shared.b16 [%0], %1;" ::"r"(buf + row_piece<64>(i + k, lane >> 3) + (lane & 7) * 2), "h"(x[k])
+                           : "memory");
         }
       }
       __syncwarp();

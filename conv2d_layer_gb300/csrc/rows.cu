@@ -302,9 +302,10 @@ cudaError_t rows_fwd(const NormArgs& a, cudaStream_t st) {
     return launch_k(rows_fwd_kernel<T, V, TPR, U, NR, NORM>, dim3(static_cast<unsigned>((a.rows + rpb - 1) / rpb)), \
                     dim3(nt), 0, st, 1, a);                                                                         \
   } while (0)
-  if (nv <= 32) ROWS_FWD(32, 1, 4);
-  if (nv <= 64) ROWS_FWD(32, 2, 2);
-  if (nv <= 128) ROWS_FWD(32, 4, 1);
+  constexpr int E = V == 1 ? 2 : 1;  // single elements: more rows in flight
+  if (nv <= 32) ROWS_FWD(32, 1, 4 * E);
+  if (nv <= 64) ROWS_FWD(32, 2, 2 * E);
+  if (nv <= 128) ROWS_FWD(32, 4, E * E);
   if (nv <= 256) ROWS_FWD(256, 1, 1);
   if (nv <= 512) ROWS_FWD(256, 2, 1);
   if (nv <= 1024) ROWS_FWD(256, 4, 1);
@@ -548,14 +549,39 @@ __global__ void __launch_bounds__(256) to_rows_kernel(const void* x, long ldx, c
   }
 }
 
-__global__ void __launch_bounds__(256) move_bytes_kernel(const uint8_t* x, long ldx, long rows, int cols, uint8_t* out,
-                                                         long ldo) {
+// The same for rows that do not start on vector boundaries, or end within a vector: a warp takes 256 neighbouring
+// elements of a row, 32 at a time.
+template <typename T, bool Q>
+__global__ void __launch_bounds__(256) to_rows_ragged_kernel(const void* x, long ldx, const uint8_t* scale, int group,
+                                                             int ng, long rows, int cols, T* out, long ldo) {
   pdl_entry();
-  const long total = rows * cols;
-  for (long j = static_cast<long>(blockIdx.x) * 256 + threadIdx.x; j < total; j += static_cast<long>(gridDim.x) * 256) {
-    const long row = j / cols;
-    const int c = static_cast<int>(j - row * cols);
-    out[row * ldo + c] = x[row * ldx + c];
+  constexpr int N = 8;
+  const int lane = threadIdx.x & 31;
+  const int chunks = (cols + 32 * N - 1) / (32 * N);
+  const long total = rows * chunks;
+  for (long j = static_cast<long>(blockIdx.x) * 8 + (threadIdx.x >> 5); j < total; j += static_cast<long>(gridDim.x) * 8) {
+    const long row = chunks == 1 ? j : j / chunks;
+    const int c0 = static_cast<int>(j - row * chunks) * 32 * N + lane;
+    T e[N];
+    uint32_t raw[N], sb[N];
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      const int c = c0 + 32 * k;
+      if (c >= cols) continue;
+      if constexpr (Q) {
+        raw[k] = static_cast<const uint8_t*>(x)[row * ldx + c];
+        sb[k] = scale[row * ng + (group ? c / kQ8Group : 0)];
+      } else {
+        e[k] = static_cast<const T*>(x)[row * ldx + c];
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      const int c = c0 + 32 * k;
+      if (c >= cols) continue;
+      if constexpr (Q) e[k] = from_q8<T>(q8_unpack2(raw[k]).x * q8_scale(sb[k]));
+      out[row * ldo + c] = e[k];
+    }
   }
 }
 
@@ -574,7 +600,15 @@ cudaError_t to_rows(const conv2d_mat& x, long rows, int cols, void* out, long ld
   // whole vectors only: cols a multiple of the vector, and both rows' starts aligned to theirs
   const int V = q ? VQ : VV;
   const bool vec = cols % V == 0 && vec_ok(out, ld, sizeof(T), VV) && vec_ok(x.data, ldx, q ? 1 : sizeof(T), V);
-  const int nv = vec ? cols / V : cols;
+  if (!vec) {
+    const dim3 grid(static_cast<unsigned>(std::min<long>((rows * ((cols + 255) / 256) + 7) / 8, 152L * 64)));
+    T* o = static_cast<T*>(out);
+    const void* src = x.data;
+    const uint8_t* sc = x.scale;
+    return q ? launch_k(to_rows_ragged_kernel<T, true>, grid, dim3(256), 0, st, 1, src, ldx, sc, x.group, ng, rows, cols, o, ld)
+             : launch_k(to_rows_ragged_kernel<T, false>, grid, dim3(256), 0, st, 1, src, ldx, sc, x.group, ng, rows, cols, o, ld);
+  }
+  const int nv = cols / V;
   const long slab = std::max<long>(1, 0x7fffffffL / nv);  // rows a launch indexes in 31 bits
   for (long r0 = 0; r0 < rows; r0 += slab) {
     const long n = std::min(slab, rows - r0);
@@ -587,7 +621,7 @@ cudaError_t to_rows(const conv2d_mat& x, long rows, int cols, void* out, long ld
 #define TO_ROWS(V, Q)                                                                                              \
   launch_k(to_rows_kernel<T, V, Q>, grid, dim3(256), 0, st, 1, static_cast<const void*>(src), ldx, sc, x.group, ng, \
            total, cols, div, o, ld)
-    const cudaError_t e = vec ? (q ? TO_ROWS(VQ, true) : TO_ROWS(VV, false)) : (q ? TO_ROWS(1, true) : TO_ROWS(1, false));
+    const cudaError_t e = q ? TO_ROWS(VQ, true) : TO_ROWS(VV, false);
 #undef TO_ROWS
     if (e != cudaSuccess) return e;
   }
@@ -611,7 +645,7 @@ struct DactArgs {
 template <typename T, int V, int ZK>
 __global__ void __launch_bounds__(256, 3) dact_kernel(const DactArgs a) {
   pdl_entry();
-  constexpr int N = ZK == 2 ? 3 : 4;  // rows in flight
+  constexpr int N = V == 1 ? 8 : ZK == 2 ? 3 : 4;  // rows in flight
   __shared__ float sums[8][32 * V];
   const int lane = threadIdx.x & 31, rl = threadIdx.x >> 5;
   const int c = (static_cast<int>(blockIdx.x) * 32 + lane) * V;
@@ -781,8 +815,9 @@ cudaError_t launch_to_rows(const conv2d_mat& x, long rows, int cols, int dt, voi
 }
 
 cudaError_t launch_move_bytes(const void* x, long ldx, long rows, int cols, void* out, long ldo, cudaStream_t st) {
-  return launch_k(move_bytes_kernel, dim3(stream_grid(rows * cols)), dim3(256), 0, st, 1,
-                  static_cast<const uint8_t*>(x), ldx, rows, cols, static_cast<uint8_t*>(out), ldo);
+  const dim3 grid(static_cast<unsigned>(std::min<long>((rows * ((cols + 255) / 256) + 7) / 8, 152L * 64)));
+  return launch_k(to_rows_ragged_kernel<uint8_t, false>, grid, dim3(256), 0, st, 1, x, ldx,
+                  static_cast<const uint8_t*>(nullptr), 0, 1, rows, cols, static_cast<uint8_t*>(out), ldo);
 }
 
 DactPlan plan_dact(long rows, int cols, int sms) {
