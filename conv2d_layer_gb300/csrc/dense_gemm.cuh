@@ -255,22 +255,55 @@ __device__ __forceinline__ uint4 pack8(const float* v) {
   return w;
 }
 
+// The residual of 32 rows x 32 columns on its way to the buffer, in 16 registers: all of it as 16-byte pieces where
+// the rows allow it, else the elements of rows `from` .. from + 15, one column a lane.
+template <typename T>
+__device__ __forceinline__ void residual_load(const DenseGemmParams& p, uint32_t (&w)[16], long m0, int n, int nr, int nc,
+                                              int from, int lane) {
+  if (p.vec_res && nc == 32) {
+    const T* r = static_cast<const T*>(p.res) + (m0 + (lane >> 2)) * p.ldr + n + (lane & 3) * 8;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i * 8 + (lane >> 2) < nr)
+        *reinterpret_cast<uint4*>(w + 4 * i) = *reinterpret_cast<const uint4*>(r + i * 8 * p.ldr);
+  } else if (lane < nc) {
+    const uint16_t* r = reinterpret_cast<const uint16_t*>(p.res) + (m0 + from) * p.ldr + n + lane;
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if (from + i < nr) w[i] = r[i * p.ldr];
+  }
+}
+template <typename T>
+__device__ __forceinline__ void residual_store(const DenseGemmParams& p, uint32_t (&w)[16], uint32_t buf, long m0, int n,
+                                               int nr, int nc, int lane) {
+  if (p.vec_res && nc == 32) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      st_shared_v4(buf + row_piece<64>(i * 8 + (lane >> 2), lane & 3), w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+    return;
+  }
+#pragma unroll
+  for (int from = 0; from < 32; from += 16) {
+    if (from) residual_load<T>(p, w, m0, n, nr, nc, from, lane);
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if (from + i < nr && lane < nc)
+        asm volatile("st.shared.b16 [%0], %1;" ::"r"(buf + row_piece<64>(from + i, lane >> 3) + (lane & 7) * 2),
+                     "h"(static_cast<uint16_t>(w[i]))
+                     : "memory");
+  }
+}
+
 // A warp's 32 rows (m0 ..) x up to 32 columns (n ..) of the accumulator at taddr; nr rows and nc columns count.
-// release() is called when the accumulator has been read.
+// res: the residual's registers, loaded for these columns and left loading for the columns from n + 128 (the
+// warp's next), so that its way from memory is hidden by the main loop or by the columns before. release() is
+// called when the accumulator has been read.
 template <typename T, int MODE, typename F>
 __device__ __forceinline__ void pair_epilogue(const DenseGemmParams& p, uint32_t taddr, uint32_t buf, long m0, int n,
-                                              int nr, int nc, int split, float mscale, int lane, F&& release) {
+                                              int end, int nr, int split, float mscale, uint32_t (&res)[16], int lane,
+                                              F&& release) {
+  const int nc = min(end - n, 32);
   if constexpr (MODE == kDenseForward) {
-    // the residual's rows are in flight while the sums are read and activated
-    uint4 res[4];
-    const int rj = lane & 3;
-    const bool vres = p.vec_res && nc == 32;
-    if (p.res && vres) {
-      const T* r = static_cast<const T*>(p.res) + (m0 + (lane >> 2)) * p.ldr + n + rj * 8;
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (i * 8 + (lane >> 2) < nr) res[i] = *reinterpret_cast<const uint4*>(r + i * 8 * p.ldr);
-    }
     float v[32];
     {
       uint32_t a[32];
@@ -357,24 +390,8 @@ __device__ __forceinline__ void pair_epilogue(const DenseGemmParams& p, uint32_t
     });
     buffer_take(lane);
     if (p.res) {
-      if (vres) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) sts128(buf + row_piece<64>(i * 8 + (lane >> 2), rj), res[i]);
-      } else {
-        const uint16_t* r = reinterpret_cast<const uint16_t*>(p.res) + m0 * p.ldr + n + lane;
-#pragma unroll
-        for (int i = 0; i < 32; i += 8) {  // eight rows in flight
-          uint16_t x[8];
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-            if (i + k < nr && lane < nc) x[k] = r[(i + k) * p.ldr];
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-            if (i + k < nr && lane < nc)
-              asm volatile("st.shared.b16 [%0], %1;" ::"r"(buf + row_piece<64>(i + k, lane >> 3) + (lane & 7) * 2), "h"(x[k])
-                           : "memory");
-        }
-      }
+      residual_store<T>(p, res, buf, m0, n, nr, nc, lane);
+      if (n + 128 < end) residual_load<T>(p, res, m0, n + 128, nr, min(end - n - 128, 32), 0, lane);
       __syncwarp();
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -598,15 +615,19 @@ __global__ void __launch_bounds__(kPairThreads, 1) dense_pair_kernel(const __gri
     for (int u = cid; u < units; u += ncl, ++tc) {
       int lt, ct, split;
       dense_unit(p, u, lt, ct, split);
+      const long m0 = static_cast<long>(lt) * 256 + rank * 128 + q * 32;
+      const int nr = static_cast<int>(min(p.m - m0, 32L));
+      const float mscale = MODE == kDenseForward && p.ms && lane < nr ? q8_scale(p.ms[m0 + lane]) : 1.f;
+      const int end = min(p.n, ct * BN + BN);
+      const int n0 = ct * BN + part * 32;
+      uint32_t res[16];
+      if (MODE == kDenseForward && p.res && nr > 0 && n0 < end)
+        residual_load<T>(p, res, m0, n0, nr, min(end - n0, 32), 0, lane);
       const int buf = tc & 1;
       int ok = 1;
       if (lane == 0) ok = wait(&tfull[buf], (tc >> 1) & 1, p.err, kSiteDenseTFull) ? 1 : 0;
       if (!__shfl_sync(0xffffffffu, ok, 0)) break;
       tc_fence_after();
-      const long m0 = static_cast<long>(lt) * 256 + rank * 128 + q * 32;
-      const int nr = static_cast<int>(min(p.m - m0, 32L));
-      const float mscale = MODE == kDenseForward && p.ms && lane < nr ? q8_scale(p.ms[m0 + lane]) : 1.f;
-      const int end = min(p.n, ct * BN + BN);
       // Frees the accumulator for the unit after next, once its last columns are in registers: before they are
       // written, and without waiting for what was (the arrival orders nothing but the TMEM reads; with release
       // semantics it waited for the stores to reach L2, and held the next MMAs back by as much).
@@ -615,14 +636,13 @@ __global__ void __launch_bounds__(kPairThreads, 1) dense_pair_kernel(const __gri
         __syncwarp();
         if (lane == 0) mbar_arrive_relaxed(mapa_shared(smem_u32(&tempty[buf]), 0));
       };
-      const int n0 = ct * BN + part * 32;
       if (nr <= 0 || n0 >= end) {  // uniform
         arrive();
       } else {
 #pragma unroll 1
         for (int n = n0; n < end; n += 128)
           pair_epilogue<T, MODE>(p, tmem + (static_cast<uint32_t>(q * 32) << 16) + buf * BN + (n - ct * BN), buf0, m0, n,
-                                 nr, min(end - n, 32), split, mscale, lane, [&] {
+                                 end, nr, split, mscale, res, lane, [&] {
                                    if (n + 128 >= end) arrive();
                                  });
       }

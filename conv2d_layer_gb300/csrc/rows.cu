@@ -256,9 +256,13 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) rows_fwd_kernel(const N
         bool finite = rowfinite[i];
         if (a.group != 0) {
           auto group_max = [](uint32_t m) {
+            if constexpr (V == 1) {  // the group is the warp
+              return __reduce_max_sync(0xffffffffu, m);
+            } else {
 #pragma unroll
-            for (int s = 1; s < kQ8Group / V; s <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, s));
-            return m;
+              for (int s = 1; s < kQ8Group / V; s <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, s));
+              return m;
+            }
           };
           uint32_t m = group_max(absmax(o));
           finite = true;
@@ -498,6 +502,109 @@ cudaError_t norm_bwd(const NormBwdArgs& a, int grid, cudaStream_t st) {
 #undef NORM_BWD
 }
 
+// ------------------------------------------------------------------ 8 bits, 16-bit types in whole groups
+// 32 bytes at once (32-byte aligned): a whole sector a thread.
+__device__ __forceinline__ void ld_32b(const void* p, uint32_t (&w)[8]) {
+  asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+               : "l"(p));
+}
+__device__ __forceinline__ void st_32b(void* p, const uint32_t (&w)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+               "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+// Encode (ENC) or decode of rows of whole 32-column groups: two threads a group, 16 values each, two groups of a
+// thread in flight. total = rows * cols / 16 < 2^31; x rows on 32-byte, q rows on 16-byte boundaries.
+template <typename T, bool ENC>
+__global__ void __launch_bounds__(256) q8_flat_kernel(T* x, long ldx, uint8_t* q, long ldq, uint8_t* scale,
+                                                      uint32_t total, FastDiv div_nv) {
+  pdl_entry();
+  constexpr int N = 2;
+  const uint32_t step = gridDim.x * 256u;
+  const int ng = static_cast<int>(div_nv.d / 2);
+  for (uint32_t j0 = blockIdx.x * 256u + threadIdx.x; j0 < total; j0 += N * step) {
+    uint32_t w[N][8];
+    uint4 raw[N];
+    uint32_t sb[N];
+    long row[N];
+    int v[N];  // 16-value vector of the row
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const uint32_t j = j0 + i * step;
+      if (j >= total) break;
+      const uint32_t r = fdiv(j, div_nv);
+      row[i] = r;
+      v[i] = static_cast<int>(j - r * div_nv.d);
+      if constexpr (ENC) {
+        ld_32b(x + row[i] * ldx + v[i] * 16, w[i]);
+      } else {
+        raw[i] = *reinterpret_cast<const uint4*>(q + row[i] * ldq + v[i] * 16);
+        sb[i] = scale[row[i] * ng + (v[i] >> 1)];
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      if (j0 + i * step >= total) break;  // the two threads of a group go on together (total is even)
+      float f[16];
+      if constexpr (ENC) {
+        const T* e = reinterpret_cast<const T*>(w[i]);
+        float m = 0.f;
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          f[k] = to_f(e[k]);
+          m = fmaxf(m, fabsf(f[k]));
+        }
+        const uint32_t pair = 3u << (threadIdx.x & 30u);
+        uint32_t top = __float_as_uint(m);
+        top = max(top, __shfl_xor_sync(pair, top, 1));
+        bool finite = true;
+        if (top == 0x7f800000u) {
+          finite = false;
+          top = 0u;
+#pragma unroll
+          for (int k = 0; k < 16; ++k) top = max(top, finite_bits(f[k]));
+          top = max(top, __shfl_xor_sync(pair, top, 1));
+        }
+        const uint32_t byte = q8_scale_byte(top);
+        const float inv = q8_inv_scale(byte);
+        *reinterpret_cast<uint4*>(q + row[i] * ldq + v[i] * 16) =
+            make_uint4(q8_pack4(f, inv, finite), q8_pack4(f + 4, inv, finite), q8_pack4(f + 8, inv, finite),
+                       q8_pack4(f + 12, inv, finite));
+        if ((v[i] & 1) == 0) scale[row[i] * ng + (v[i] >> 1)] = static_cast<uint8_t>(byte);
+      } else {
+        const Q8Raw<16> rw = {{raw[i].x, raw[i].y, raw[i].z, raw[i].w}};
+        const float sc = q8_scale(sb[i]);
+        q8_values<16>(rw, f, sc);
+        T* e = reinterpret_cast<T*>(w[i]);
+        if (sc > q8_safe_scale<T>()) {
+#pragma unroll
+          for (int k = 0; k < 16; ++k) e[k] = from_q8<T>(f[k]);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 16; ++k) e[k] = from_f<T>(f[k]);
+        }
+        st_32b(x + row[i] * ldx + v[i] * 16, w[i]);
+      }
+    }
+  }
+}
+int stream_grid(long items) { return static_cast<int>(std::max<long>(1, std::min<long>((items + 255) / 256, 152L * 64))); }
+
+// Whether the flat kernel takes it, and its launch.
+template <typename T, bool ENC>
+bool q8_flat(const void* x, long ldx, const void* q, long ldq, uint8_t* scale, int group, long rows, int cols,
+             cudaStream_t st, cudaError_t* e) {
+  if (group != kQ8Group || cols % kQ8Group != 0 || ldx % 16 != 0 || ldq % 16 != 0 ||
+      reinterpret_cast<uintptr_t>(x) % 32 != 0 || rows * (cols / 16) > 0x7fffffffL)
+    return false;
+  const long total = rows * (cols / 16);
+  *e = launch_k(q8_flat_kernel<T, ENC>, dim3(stream_grid((total + 1) / 2)), dim3(256), 0, st, 1,
+                static_cast<T*>(const_cast<void*>(x)), ldx, static_cast<uint8_t*>(const_cast<void*>(q)), ldq, scale,
+                static_cast<uint32_t>(total), make_fastdiv(static_cast<uint32_t>(cols / 16)));
+  return true;
+}
+
 // ------------------------------------------------------------------ decode / move
 // V elements a thread and step of a [rows][cols] matrix, dense steps of the grid (E4M3 source: V bytes and
 // their scale, two output vectors). rows * ceil(cols / V) below 2^31 (see to_rows).
@@ -585,8 +692,6 @@ __global__ void __launch_bounds__(256) to_rows_ragged_kernel(const void* x, long
   }
 }
 
-int stream_grid(long items) { return static_cast<int>(std::max<long>(1, std::min<long>((items + 255) / 256, 152L * 64))); }
-
 bool vec_ok(const void* p, long ld, int es, int V) {
   return reinterpret_cast<uintptr_t>(p) % 16 == 0 && (ld * es) % (static_cast<long>(V) * es) == 0;
 }
@@ -598,6 +703,10 @@ cudaError_t to_rows(const conv2d_mat& x, long rows, int cols, void* out, long ld
   const long ldx = x.ld ? x.ld : cols, ld = ldo ? ldo : cols;
   const int ng = x.group ? (cols + kQ8Group - 1) / kQ8Group : 1;
   // whole vectors only: cols a multiple of the vector, and both rows' starts aligned to theirs
+  if constexpr (sizeof(T) == 2) {
+    cudaError_t e;
+    if (q && q8_flat<T, false>(out, ld, x.data, ldx, x.scale, x.group, rows, cols, st, &e)) return e;
+  }
   const int V = q ? VQ : VV;
   const bool vec = cols % V == 0 && vec_ok(out, ld, sizeof(T), VV) && vec_ok(x.data, ldx, q ? 1 : sizeof(T), V);
   if (!vec) {
@@ -954,7 +1063,15 @@ int conv2d_q8_encode(int64_t rows, int32_t cols, const conv2d_mat* x, const conv
   a.group = q8->group;
   a.ng = q8->group ? (cols + kQ8Group - 1) / kQ8Group : 1;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  LAUNCH("q8_encode", st, rows_fwd_any<false>(a, x->type, st));
+  auto run = [&]() -> cudaError_t {
+    cudaError_t e = cudaSuccess;
+    if (x->type == CONV2D_BF16 && q8_flat<__nv_bfloat16, true>(a.x, a.ldx, a.q, a.ldq, a.qs, a.group, rows, cols, st, &e))
+      return e;
+    if (x->type == CONV2D_FP16 && q8_flat<__half, true>(a.x, a.ldx, a.q, a.ldq, a.qs, a.group, rows, cols, st, &e))
+      return e;
+    return rows_fwd_any<false>(a, x->type, st);
+  };
+  LAUNCH("q8_encode", st, run());
   return CONV2D_OK;
 }
 
