@@ -35,24 +35,44 @@ __device__ __forceinline__ constexpr float q8_safe_scale() {
   return std::is_same<T, __half>::value ? 128.f : 6.6461399789245794e35f;  // 2^7, 2^119
 }
 
-// V consecutive elements as fp32; V * sizeof(T) = 16 bytes (aligned) or V = 1.
-template <typename T, int V>
-struct Vec {
-  T e[V];
-};
+// 32 bytes at once (32-byte aligned): a whole sector a thread.
+__device__ __forceinline__ void ld_32b(const void* p, uint32_t (&w)[8]) {
+  asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+               : "l"(p));
+}
+__device__ __forceinline__ void st_32b(void* p, const uint32_t (&w)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+               "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+// V consecutive elements; V * sizeof(T) = 32 or 16 bytes (aligned to as much) or V = 1.
 template <typename T, int V>
 __device__ __forceinline__ void ld_vec(const T* p, T (&e)[V]) {
   if constexpr (V == 1) {
     e[0] = *p;
+  } else if constexpr (sizeof(T) * V == 32) {
+    uint32_t w[8];
+    ld_32b(p, w);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) reinterpret_cast<uint32_t*>(e)[i] = w[i];
   } else {
-    static_assert(sizeof(T) * V == 16, "16-byte vectors");
+    static_assert(sizeof(T) * V == 16, "16- or 32-byte vectors");
     *reinterpret_cast<uint4*>(e) = *reinterpret_cast<const uint4*>(p);
   }
 }
 template <typename T, int V>
 __device__ __forceinline__ void st_vec(T* p, const T (&e)[V]) {
-  if constexpr (V == 1) *p = e[0];
-  else *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(e);
+  if constexpr (V == 1) {
+    *p = e[0];
+  } else if constexpr (sizeof(T) * V == 32) {
+    uint32_t w[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = reinterpret_cast<const uint32_t*>(e)[i];
+    st_32b(p, w);
+  } else {
+    *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(e);
+  }
 }
 
 // Magnitude bits of a finite value, 0 for infinities and NaN: ordered like the magnitudes.
@@ -99,9 +119,12 @@ __device__ __forceinline__ void q8_store(uint8_t* p, const float (&v)[V], float 
     *p = static_cast<uint8_t>(q8_pack2(v[0] * inv, 0.f));
   } else if constexpr (V == 4) {
     *reinterpret_cast<uint32_t*>(p) = q8_pack4(v, inv, finite);
-  } else {
-    static_assert(V == 8, "V is 1, 4 or 8");
+  } else if constexpr (V == 8) {
     *reinterpret_cast<uint2*>(p) = make_uint2(q8_pack4(v, inv, finite), q8_pack4(v + 4, inv, finite));
+  } else {
+    static_assert(V == 16, "V is 1, 4, 8 or 16");
+    *reinterpret_cast<uint4*>(p) = make_uint4(q8_pack4(v, inv, finite), q8_pack4(v + 4, inv, finite),
+                                              q8_pack4(v + 8, inv, finite), q8_pack4(v + 12, inv, finite));
   }
 }
 // V e4m3 bytes as they lie in memory, and their values times scale.

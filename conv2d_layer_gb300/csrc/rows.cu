@@ -2,8 +2,9 @@
 // addition and its backward, 8-bit checkpoints (encode, decode), the backward
 // through a dense layer's activation, and the column sums and joins behind
 // them. All are bound by memory: each reads its inputs once and writes its
-// outputs once, in 16-byte accesses where the rows allow it (row starts on
-// 16-byte boundaries; V = 1 otherwise).
+// outputs once, in accesses of 32 bytes (a sector) a thread where the rows
+// start on such boundaries, of 16 bytes where they start on those, element by
+// element (V = 1) otherwise.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -302,18 +303,24 @@ cudaError_t rows_fwd(const NormArgs& a, cudaStream_t st) {
   const int nv = (a.cols + V - 1) / V;
 #define ROWS_FWD(TPR, U, NR)                                                                                        \
   do {                                                                                                              \
-    constexpr int nt = TPR < 256 ? 256 : TPR, rpb = nt / TPR * NR;                                                  \
+    constexpr int nt = TPR < 256 ? 256 : TPR, rpb = nt / TPR * (NR);                                               \
     return launch_k(rows_fwd_kernel<T, V, TPR, U, NR, NORM>, dim3(static_cast<unsigned>((a.rows + rpb - 1) / rpb)), \
                     dim3(nt), 0, st, 1, a);                                                                         \
   } while (0)
-  constexpr int E = V == 1 ? 2 : 1;  // single elements: more rows in flight
-  if (nv <= 32) ROWS_FWD(32, 1, 4 * E);
-  if (nv <= 64) ROWS_FWD(32, 2, 2 * E);
-  if (nv <= 128) ROWS_FWD(32, 4, E * E);
+  // 16 to 32 values a thread where a warp takes a row (8 to 16 when they are loaded one by one); long rows are
+  // spread over 256 or 512 threads
+  if (nv <= 32) ROWS_FWD(32, 1, (V == 16 ? 2 : V == 1 ? 8 : 4));
+  if (nv <= 64) ROWS_FWD(32, 2, (V == 16 ? 1 : V == 1 ? 4 : 2));
+  if constexpr (V < 16)
+    if (nv <= 128) ROWS_FWD(32, 4, (V == 1 ? 4 : 1));
   if (nv <= 256) ROWS_FWD(256, 1, 1);
   if (nv <= 512) ROWS_FWD(256, 2, 1);
-  if (nv <= 1024) ROWS_FWD(256, 4, 1);
-  if (nv <= 2048) ROWS_FWD(512, 4, 1);
+  if constexpr (V == 16) {
+    if (nv <= 1024) ROWS_FWD(512, 2, 1);
+  } else {
+    if (nv <= 1024) ROWS_FWD(256, 4, 1);
+    if (nv <= 2048) ROWS_FWD(512, 4, 1);
+  }
   ROWS_FWD(1024, 0, 1);
 #undef ROWS_FWD
 }
@@ -329,11 +336,11 @@ struct NormBwdArgs {
   int cols;
 };
 
-// Blocks walk the rows (row = block, block + grid, ...), TPR threads a row, and keep gamma and the sums of
-// dgamma for their columns in registers. The vectors of the next row are in flight while this one is
-// reduced. U = 0: rows longer than the registers hold; each row is read twice and dgamma's sums live in
-// this block's row of `part`.
-template <typename T, int V, int TPR, int U>
+// Blocks walk the rows (row = block, block + grid, ...), TPR threads a row, and keep the sums of dgamma for their
+// columns in registers. AHEAD: gamma too, and the vectors of the next row are in flight while this one is reduced;
+// without it (rows whose values take the registers) gamma and dh are read where they are needed. U = 0: rows
+// longer than the registers hold; each row is read twice and dgamma's sums live in this block's row of `part`.
+template <typename T, int V, int TPR, int U, bool AHEAD>
 __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR, TPR <= 256 ? 2 : 1) norm_bwd_kernel(const NormBwdArgs a) {
   pdl_entry();
   constexpr int RPB = TPR < 256 ? 256 / TPR : 1;
@@ -352,16 +359,26 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR, TPR <= 256 ? 2 : 1) nor
   const long row0 = static_cast<long>(blockIdx.x) * RPB + wr;
 
   if constexpr (U > 0) {
-    float g[UC][V], acc[UC][V];
+    float g[AHEAD ? UC : 1][V], acc[UC][V];
+    auto load_gamma = [&](int u, float (&o)[V]) {
+      const int c = (u * TPR + t) * V;
 #pragma unroll
-    for (int u = 0; u < UC; ++u)
+      for (int k = 0; k < V; ++k) o[k] = 0.f;
+      if (c >= a.cols) return;
+      if constexpr (V >= 4) {
 #pragma unroll
-      for (int k = 0; k < V; ++k) {
-        const int c = (u * TPR + t) * V + k;
-        g[u][k] = c < a.cols ? a.gamma[c] : 0.f;
-        acc[u][k] = 0.f;
+        for (int k = 0; k < V; k += 4) *reinterpret_cast<float4*>(o + k) = *reinterpret_cast<const float4*>(a.gamma + c + k);
+      } else {
+        o[0] = a.gamma[c];
       }
-    T h[UC][V], d[UC][V], s[UC][V];
+    };
+#pragma unroll
+    for (int u = 0; u < UC; ++u) {
+      if constexpr (AHEAD) load_gamma(u, g[u]);
+#pragma unroll
+      for (int k = 0; k < V; ++k) acc[u][k] = 0.f;
+    }
+    T h[UC][V], d[UC][V], s[AHEAD ? UC : 1][V];
     float inv = 0.f;
     auto fetch = [&](long row) {
       if (row < a.rows) inv = a.inv[row];
@@ -371,42 +388,49 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR, TPR <= 256 ? 2 : 1) nor
         if (row < a.rows && i < nv) {
           ld_vec<T, V>(hb + row * a.ldh + static_cast<long>(i) * V, h[u]);
           ld_vec<T, V>(db + row * a.lddy + static_cast<long>(i) * V, d[u]);
-          if (sb && xb) ld_vec<T, V>(sb + row * a.lddh + static_cast<long>(i) * V, s[u]);
+          if constexpr (AHEAD)
+            if (sb && xb) ld_vec<T, V>(sb + row * a.lddh + static_cast<long>(i) * V, s[u]);
         } else {
 #pragma unroll
           for (int k = 0; k < V; ++k) h[u][k] = d[u][k] = from_f<T>(0.f);
         }
       }
     };
-    fetch(row0);
+    if constexpr (AHEAD) fetch(row0);
     for (long row = row0; row < a.rows; row += step) {
+      if constexpr (!AHEAD) fetch(row);
       float hf[UC][V], df[UC][V];
-      T sk[UC][V];
+      T sk[AHEAD ? UC : 1][V];
       const float iv = inv;
       float dot = 0.f;
 #pragma unroll
-      for (int u = 0; u < UC; ++u)
+      for (int u = 0; u < UC; ++u) {
+        float gu[V];
+        if constexpr (!AHEAD) load_gamma(u, gu);
 #pragma unroll
         for (int k = 0; k < V; ++k) {
           hf[u][k] = to_f(h[u][k]) * iv;  // the normalised value
           df[u][k] = to_f(d[u][k]);
-          sk[u][k] = s[u][k];
+          if constexpr (AHEAD) sk[u][k] = s[u][k];
           acc[u][k] = fmaf(df[u][k], hf[u][k], acc[u][k]);
-          df[u][k] *= g[u][k];
+          df[u][k] *= AHEAD ? g[AHEAD ? u : 0][k] : gu[k];
           dot = fmaf(df[u][k], hf[u][k], dot);
         }
-      fetch(row + step);
+      }
+      if constexpr (AHEAD) fetch(row + step);
       if (xb) {
         dot = row_sum<TPR>(dot, red) * invD;
 #pragma unroll
         for (int u = 0; u < UC; ++u) {
           const int i = u * TPR + t;
           if (i < nv) {
-            T o[V];
+            T o[V], sv[V];
+            if constexpr (!AHEAD)
+              if (sb) ld_vec<T, V>(sb + row * a.lddh + static_cast<long>(i) * V, sv);
 #pragma unroll
             for (int k = 0; k < V; ++k) {
               float v = iv * fmaf(-hf[u][k], dot, df[u][k]);
-              if (sb) v += to_f(sk[u][k]);
+              if (sb) v += to_f(AHEAD ? sk[AHEAD ? u : 0][k] : sv[k]);
               o[k] = from_f<T>(v);
             }
             st_vec<T, V>(xb + row * a.lddx + static_cast<long>(i) * V, o);
@@ -486,34 +510,29 @@ int norm_bwd_grid(long rows, int sms) { return static_cast<int>(std::max<long>(1
 template <typename T, int V>
 cudaError_t norm_bwd(const NormBwdArgs& a, int grid, cudaStream_t st) {
   const int nv = (a.cols + V - 1) / V;
-#define NORM_BWD(TPR, U)                                                                         \
+#define NORM_BWD(TPR, U, AHEAD)                                                                  \
   do {                                                                                           \
     constexpr int nt = TPR < 256 ? 256 : TPR;                                                    \
     const size_t smem = nt > TPR && a.part ? static_cast<size_t>(nt / TPR) * a.cols * 4 : 0;     \
-    return launch_k(norm_bwd_kernel<T, V, TPR, U>, dim3(grid), dim3(nt), smem, st, 1, a);        \
+    return launch_k(norm_bwd_kernel<T, V, TPR, U, AHEAD>, dim3(grid), dim3(nt), smem, st, 1, a); \
   } while (0)
-  if (nv <= 32) NORM_BWD(32, 1);
-  if (nv <= 64) NORM_BWD(32, 2);
-  if (nv <= 256) NORM_BWD(256, 1);
-  if (nv <= 512) NORM_BWD(256, 2);
-  if (nv <= 1024) NORM_BWD(512, 2);
-  if (nv <= 2048) NORM_BWD(1024, 2);
-  NORM_BWD(1024, 0);
+  if (nv <= 32) NORM_BWD(32, 1, true);
+  if constexpr (V < 16)
+    if (nv <= 64) NORM_BWD(32, 2, true);
+  if (nv <= 256) NORM_BWD(256, 1, true);
+  if constexpr (V < 16)
+    if (nv <= 512) NORM_BWD(256, 2, true);
+  if (nv <= 512) NORM_BWD(512, 1, true);
+  if constexpr (V < 16)
+    if (nv <= 1024) NORM_BWD(512, 2, true);
+  if (nv <= 1024) NORM_BWD(512, 2, false);
+  if constexpr (V < 16)
+    if (nv <= 2048) NORM_BWD(512, 4, false);
+  NORM_BWD(1024, 0, false);
 #undef NORM_BWD
 }
 
 // ------------------------------------------------------------------ 8 bits, 16-bit types in whole groups
-// 32 bytes at once (32-byte aligned): a whole sector a thread.
-__device__ __forceinline__ void ld_32b(const void* p, uint32_t (&w)[8]) {
-  asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
-               : "l"(p));
-}
-__device__ __forceinline__ void st_32b(void* p, const uint32_t (&w)[8]) {
-  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
-               "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
-               : "memory");
-}
 // Encode (ENC) or decode of rows of whole 32-column groups: two threads a group, 16 values each, two groups of a
 // thread in flight. total = rows * cols / 16 < 2^31; x rows on 32-byte, q rows on 16-byte boundaries.
 template <typename T, bool ENC>
@@ -692,8 +711,9 @@ __global__ void __launch_bounds__(256) to_rows_ragged_kernel(const void* x, long
   }
 }
 
+// Rows that start on boundaries of a vector of V elements of es bytes (the base at least on 16 bytes by contract).
 bool vec_ok(const void* p, long ld, int es, int V) {
-  return reinterpret_cast<uintptr_t>(p) % 16 == 0 && (ld * es) % (static_cast<long>(V) * es) == 0;
+  return reinterpret_cast<uintptr_t>(p) % (V * es > 16 ? 32 : 16) == 0 && ld % V == 0;
 }
 
 template <typename T>
@@ -752,9 +772,9 @@ struct DactArgs {
 // the unrounded dz in registers, joined over the 8 row lanes at the end. ZK: 0 no activation, 1 z in T,
 // 2 z as E4M3.
 template <typename T, int V, int ZK>
-__global__ void __launch_bounds__(256, 3) dact_kernel(const DactArgs a) {
+__global__ void __launch_bounds__(256, V == 16 ? 2 : 3) dact_kernel(const DactArgs a) {
   pdl_entry();
-  constexpr int N = V == 1 ? 8 : ZK == 2 ? 3 : 4;  // rows in flight
+  constexpr int N = V == 1 ? 6 : V == 16 ? 2 : 3;  // rows in flight
   __shared__ float sums[8][32 * V];
   const int lane = threadIdx.x & 31, rl = threadIdx.x >> 5;
   const int c = (static_cast<int>(blockIdx.x) * 32 + lane) * V;
@@ -834,24 +854,22 @@ __global__ void __launch_bounds__(256, 3) dact_kernel(const DactArgs a) {
   }
 }
 
+template <typename T, int V>
+cudaError_t dact_v(const DactArgs& a, int zk, int strips, cudaStream_t st) {
+  const dim3 grid(static_cast<unsigned>((a.cols + 32 * V - 1) / (32 * V)), static_cast<unsigned>(strips));
+  if (zk == 0) return launch_k(dact_kernel<T, V, 0>, grid, dim3(256), 0, st, 1, a);
+  if (zk == 1) return launch_k(dact_kernel<T, V, 1>, grid, dim3(256), 0, st, 1, a);
+  return launch_k(dact_kernel<T, V, 2>, grid, dim3(256), 0, st, 1, a);
+}
 template <typename T>
 cudaError_t dact(const DactArgs& a, int zk, int strips, cudaStream_t st) {
-  constexpr int VV = 16 / sizeof(T);
-  const bool vec = a.cols % VV == 0 && vec_ok(a.dy, a.lddy, sizeof(T), VV) &&
-                   (!a.dz || vec_ok(a.dz, a.lddz, sizeof(T), VV)) &&
-                   (zk == 0 || vec_ok(a.z, a.ldz, zk == 2 ? 1 : sizeof(T), VV));
-  const int V = vec ? VV : 1;
-  const dim3 grid(static_cast<unsigned>((a.cols + 32 * V - 1) / (32 * V)), static_cast<unsigned>(strips));
-#define DACT(V, ZK) return launch_k(dact_kernel<T, V, ZK>, grid, dim3(256), 0, st, 1, a)
-  if (vec) {
-    if (zk == 0) DACT(VV, 0);
-    if (zk == 1) DACT(VV, 1);
-    DACT(VV, 2);
-  }
-  if (zk == 0) DACT(1, 0);
-  if (zk == 1) DACT(1, 1);
-  DACT(1, 2);
-#undef DACT
+  auto ok = [&](int V) {
+    return a.cols % V == 0 && vec_ok(a.dy, a.lddy, sizeof(T), V) && (!a.dz || vec_ok(a.dz, a.lddz, sizeof(T), V)) &&
+           (zk == 0 || vec_ok(a.z, a.ldz, zk == 2 ? 1 : sizeof(T), V));
+  };
+  // 16 columns a lane only where a warp's 512 are there
+  if (a.cols >= 512 && ok(16)) return dact_v<T, 16>(a, zk, strips, st);
+  return ok(8) ? dact_v<T, 8>(a, zk, strips, st) : dact_v<T, 1>(a, zk, strips, st);
 }
 
 // ------------------------------------------------------------------ column sums, joins, zeroes
@@ -930,8 +948,9 @@ cudaError_t launch_move_bytes(const void* x, long ldx, long rows, int cols, void
 }
 
 DactPlan plan_dact(long rows, int cols, int sms) {
-  // about eight blocks an SM, of 64 rows at least (eight passes, so that the joining at the end is small)
-  const long chunks = (cols + 255) / 256;
+  // about eight blocks an SM, of 64 rows at least (eight passes, so that the joining at the end is small); a block
+  // is 256 columns wide, or 32 where the columns do not divide into vectors
+  const long chunks = cols % 8 == 0 ? (cols + 255) / 256 : (cols + 31) / 32;
   long strips = std::max<long>(1, 8L * sms / chunks);
   strips = std::min(strips, (rows + 63) / 64);
   strips = std::max<long>(1, std::min<long>(strips, 65535));
@@ -1027,17 +1046,35 @@ int check_rows(int64_t rows, int32_t cols) {
 }
 
 template <bool NORM>
+bool rows_fwd_ok(const NormArgs& a, int es, int V) {
+  return a.cols % V == 0 && vec_ok(a.x, a.ldx, es, V) && (!a.r || (vec_ok(a.r, a.ldr, es, V) && vec_ok(a.h, a.ldh, es, V))) &&
+         (!a.y || vec_ok(a.y, a.ldy, es, V)) && (!a.q || vec_ok(a.q, a.ldq, 1, V));
+}
+template <typename T, bool NORM>
+cudaError_t rows_fwd_vec(const NormArgs& a, cudaStream_t st) {
+  constexpr int es = sizeof(T);
+  if (rows_fwd_ok<NORM>(a, es, 32 / es)) return rows_fwd<T, 32 / es, NORM>(a, st);
+  if (rows_fwd_ok<NORM>(a, es, 16 / es)) return rows_fwd<T, 16 / es, NORM>(a, st);
+  return rows_fwd<T, 1, NORM>(a, st);
+}
+template <bool NORM>
 cudaError_t rows_fwd_any(const NormArgs& a, int type, cudaStream_t st) {
-  const int es = type == CONV2D_FP32 ? 4 : 2, VV = 16 / es;
-  bool vec = a.cols % VV == 0 && vec_ok(a.x, a.ldx, es, VV);
-  if (a.r) vec = vec && vec_ok(a.r, a.ldr, es, VV) && vec_ok(a.h, a.ldh, es, VV);
-  if (a.y) vec = vec && vec_ok(a.y, a.ldy, es, VV);
-  if (a.q) vec = vec && vec_ok(a.q, a.ldq, 1, VV);
-  switch (type) {
-    case CONV2D_BF16: return vec ? rows_fwd<__nv_bfloat16, 8, NORM>(a, st) : rows_fwd<__nv_bfloat16, 1, NORM>(a, st);
-    case CONV2D_FP16: return vec ? rows_fwd<__half, 8, NORM>(a, st) : rows_fwd<__half, 1, NORM>(a, st);
-    default: return vec ? rows_fwd<float, 4, NORM>(a, st) : rows_fwd<float, 1, NORM>(a, st);
-  }
+  if (type == CONV2D_BF16) return rows_fwd_vec<__nv_bfloat16, NORM>(a, st);
+  if (type == CONV2D_FP16) return rows_fwd_vec<__half, NORM>(a, st);
+  return rows_fwd_vec<float, NORM>(a, st);
+}
+
+template <typename T>
+cudaError_t norm_bwd_vec(const NormBwdArgs& a, int grid, cudaStream_t st) {
+  constexpr int es = sizeof(T);
+  auto ok = [&](int V) {
+    return a.cols % V == 0 && vec_ok(a.h, a.ldh, es, V) && vec_ok(a.dy, a.lddy, es, V) &&
+           (!a.dx || vec_ok(a.dx, a.lddx, es, V)) && (!a.dh || vec_ok(a.dh, a.lddh, es, V));
+  };
+  if constexpr (es == 2)  // fp32 rows of 32-byte vectors take more registers than they win
+    if (ok(32 / es)) return norm_bwd<T, 32 / es>(a, grid, st);
+  if (ok(16 / es)) return norm_bwd<T, 16 / es>(a, grid, st);
+  return norm_bwd<T, 1>(a, grid, st);
 }
 
 }  // namespace
@@ -1179,17 +1216,11 @@ int conv2d_rms_norm_bwd(int64_t rows, int32_t cols, const conv2d_mat* h, const f
   a.part = dgamma ? static_cast<float*>(ws) : nullptr;
   a.rows = rows;
   a.cols = cols;
-  const int es = h->type == CONV2D_FP32 ? 4 : 2, VV = 16 / es;
-  bool vec = cols % VV == 0 && vec_ok(a.h, a.ldh, es, VV) && vec_ok(a.dy, a.lddy, es, VV);
-  if (a.dx) vec = vec && vec_ok(a.dx, a.lddx, es, VV);
-  if (a.dh) vec = vec && vec_ok(a.dh, a.lddh, es, VV);
   const int grid = norm_bwd_grid(rows, dev->sms);
   auto run = [&]() -> cudaError_t {
-    switch (h->type) {
-      case CONV2D_BF16: return vec ? norm_bwd<__nv_bfloat16, 8>(a, grid, st) : norm_bwd<__nv_bfloat16, 1>(a, grid, st);
-      case CONV2D_FP16: return vec ? norm_bwd<__half, 8>(a, grid, st) : norm_bwd<__half, 1>(a, grid, st);
-      default: return vec ? norm_bwd<float, 4>(a, grid, st) : norm_bwd<float, 1>(a, grid, st);
-    }
+    if (h->type == CONV2D_BF16) return norm_bwd_vec<__nv_bfloat16>(a, grid, st);
+    if (h->type == CONV2D_FP16) return norm_bwd_vec<__half>(a, grid, st);
+    return norm_bwd_vec<float>(a, grid, st);
   };
   LAUNCH("rms_norm_bwd", st, run());
   if (dgamma) LAUNCH("column_sum", st, launch_column_sum(a.part, grid, cols, dgamma, accumulate, st));
