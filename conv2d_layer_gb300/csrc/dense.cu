@@ -36,7 +36,10 @@ constexpr int kFp32SplitKb = 64;
 struct GemmPlan {
   bool pair;
   int BN, cluster, splits, kb_total, kb_per_split, l_tiles, c_tiles, stages, grid;
+  int full, parts;    // pair kernel: units run whole, and into how many parts the others are cut
   size_t smem;
+  size_t join_bytes;  // workspace for the parts' sums, then their flags
+  size_t join_flags;  // number of flags
 };
 
 // Kernel, tile, cluster size and splits by an estimate of each choice's clocks, fitted to timings of square and
@@ -65,8 +68,22 @@ GemmPlan plan_gemm(int mode, long m, long n, int kb, int max_kb, int sms) {
     const double loop = static_cast<double>(ceil_div(g.kb_per_split, cl));
     double t;
     if (pair) {
-      const double epi = 1500 + 10.0 * BN;
-      t = 8300 + 12.0 * BN + std::ceil(units / (sms / 2)) * std::max(loop * (188 + 1.35 * BN), epi);
+      const double epi = 1500 + 10.0 * BN, block = 188 + 1.35 * BN, unit = std::max(loop * block, epi);
+      const long pairs = sms / 2, whole = static_cast<long>(units) / pairs, rem = static_cast<long>(units) % pairs;
+      t = 8300 + 12.0 * BN + whole * unit;
+      g.full = static_cast<int>(units);
+      g.parts = 1;
+      if (rem > 0) {
+        // a last wave that leaves half of the pairs or more idle is cut along k: a part's sums go through memory
+        // (about 3 us with the zeroing of the flags)
+        const int parts = static_cast<int>(std::min<long>(std::min<long>(4, pairs / rem), g.kb_total / 8));
+        const double cut = parts > 1 && g.splits == 1 && whole > 0 ? loop / parts * block + 9000 : 1e300;
+        if (cut < unit) {
+          g.full = static_cast<int>(whole * pairs);
+          g.parts = parts;
+        }
+        t += std::min(unit, cut);
+      }
     } else {
       // CTAs that are resident at once: clusters of 4 and 8 leave SMs of a GPC over
       const double fit = cl == 8 ? sms * 15 / 19 : cl == 4 ? sms * 18 / 19 : sms;
@@ -109,6 +126,11 @@ GemmPlan plan_gemm(int mode, long m, long n, int kb, int max_kb, int sms) {
   } else {
     best.grid = static_cast<int>(units) * best.cluster;
     best.stages = std::max(2, std::min({kDenseMaxStages, (room - join) / stage, need}));
+  }
+  if (best.parts > 1) {
+    const size_t rem = static_cast<size_t>(units - best.full) * (best.parts - 1) * 2;
+    best.join_bytes = rem * 128 * best.BN * 4;
+    best.join_flags = rem * kPairWarps;
   }
   // alignment slack, barriers
   best.smem = static_cast<size_t>(best.stages) * stage + 1024 + 512 +
@@ -164,7 +186,7 @@ struct Operand {
 
 // out[m][n] = sum_k R[m][k] C[n][k]. The rows of the output are the accumulator's lanes in the pair kernel and its
 // columns in the cluster kernel.
-int run_gemm(DenseGemmParams& p, const GemmPlan& g, const Operand& r, const Operand& c, int dt, int mode,
+int run_gemm(DenseGemmParams& p, const GemmPlan& g, const Operand& r, const Operand& c, int dt, int mode, void* join,
              const char* name, const DevInfo* dev, cudaStream_t st) {
   const bool r_mn = dense_r_mn(mode), c_mn = dense_c_mn(mode);
   const Operand &lo = g.pair ? r : c, &co = g.pair ? c : r;
@@ -184,6 +206,14 @@ int run_gemm(DenseGemmParams& p, const GemmPlan& g, const Operand& r, const Oper
     if ((p.tma_out && !encode_output(&p.tout, p.out, ot, p.m, p.n, p.ldo, g.splits)) ||
         (p.tma_z && !encode_output(&p.tz, z, zt, p.m, p.n, p.ldz, 1)))
       return CONV2D_ERR_CUDA;
+  }
+  p.full = g.full;
+  p.parts = g.parts;
+  if (g.parts > 1) {
+    p.join_part = static_cast<float*>(join);
+    p.join_flag = reinterpret_cast<uint32_t*>(static_cast<char*>(join) + g.join_bytes);
+    LAUNCH("zero", st, launch_zero_rows(1, static_cast<int>(g.join_flags), CONV2D_FP32, p.join_flag,
+                                        static_cast<long>(g.join_flags), st));
   }
   p.l_tiles = g.l_tiles;
   p.c_tiles = g.c_tiles;
@@ -254,9 +284,13 @@ int make_operand(Operand* o, const conv2d_mat* m, long rows, int cols, bool as_8
   return CONV2D_OK;
 }
 
+// Room for the cut units' sums and flags.
+size_t plan_join(Carver& c, const GemmPlan& g) { return g.parts > 1 ? c.take(g.join_bytes + g.join_flags * 4) : kNone; }
+void* at(void* ws, size_t off) { return off == kNone ? nullptr : static_cast<char*>(ws) + off; }
+
 struct FwdPlan {
   bool fp8;
-  size_t x, w, total;
+  size_t x, w, join, total;
   GemmPlan g;
 };
 void plan_fwd(const conv2d_dense_desc& d, const conv2d_mat* x, const conv2d_mat* w, int sms, FwdPlan* pl) {
@@ -264,14 +298,15 @@ void plan_fwd(const conv2d_dense_desc& d, const conv2d_mat* x, const conv2d_mat*
   pl->fp8 = both_8bit(x, w);
   pl->x = plan_copy(c, x, d.M, d.K, pl->fp8);
   pl->w = plan_copy(c, w, d.N, d.K, pl->fp8);
-  pl->total = std::max<size_t>(c.total, 256);
   pl->g = plan_gemm(kDenseForward, d.M, d.N, static_cast<int>(ceil_div(d.K, pl->fp8 ? 128 : 64)), 0, sms);
+  pl->join = plan_join(c, pl->g);
+  pl->total = std::max<size_t>(c.total, 256);
 }
 
 struct BwdPlan {
   bool dz_own;  // dz is formed in the workspace (else it is dy)
   long lddz;
-  size_t dz, x, w, dpart, spart, total;
+  size_t dz, x, w, dpart, spart, joinx, joinw, total;
   DactPlan dact;
   GemmPlan gx, gw;
 };
@@ -284,15 +319,17 @@ void plan_bwd(const conv2d_dense_desc& d, const conv2d_mat* x, const conv2d_mat*
   pl->dz = pl->dz_own ? c.take(static_cast<size_t>(d.M) * pl->lddz * 2) : kNone;
   pl->dact = plan_dact(d.M, d.N, sms);
   pl->dpart = dbias ? c.take(static_cast<size_t>(pl->dact.strips) * d.N * 4) : kNone;
-  pl->w = pl->x = pl->spart = kNone;
+  pl->w = pl->x = pl->spart = pl->joinx = pl->joinw = kNone;
   if (dx) {
     pl->w = plan_copy(c, w, d.N, d.K, false);
     pl->gx = plan_gemm(kDenseDx, d.M, d.K, static_cast<int>(ceil_div(d.N, 64)), 0, sms);
+    pl->joinx = plan_join(c, pl->gx);
   }
   if (dw) {
     pl->x = plan_copy(c, x, d.M, d.K, false);
     pl->gw = plan_gemm(kDenseDw, d.N, d.K, static_cast<int>(ceil_div(d.M, 64)),
                        dw->type == CONV2D_FP32 ? kFp32SplitKb : 0, sms);
+    pl->joinw = plan_join(c, pl->gw);
     if (pl->gw.splits > 1) pl->spart = c.take(static_cast<size_t>(pl->gw.splits) * d.N * d.K * 4);
   }
   pl->total = std::max<size_t>(c.total, 256);
@@ -353,7 +390,7 @@ int conv2d_dense_fwd(const conv2d_dense_desc* d, const conv2d_mat* x, const conv
   if ((rc = device_info(&dev))) return rc;
   FwdPlan pl;
   plan_fwd(*d, x, w, dev->sms, &pl);
-  const bool uses_ws = pl.x != kNone || pl.w != kNone;
+  const bool uses_ws = pl.x != kNone || pl.w != kNone || pl.join != kNone;
   if (uses_ws && (!ws || ws_bytes < pl.total || (reinterpret_cast<uintptr_t>(ws) & 255u))) return CONV2D_ERR_WORKSPACE;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   Operand ox, ow;
@@ -382,7 +419,7 @@ int conv2d_dense_fwd(const conv2d_dense_desc* d, const conv2d_mat* x, const conv
   }
   p.out = y->data;
   p.ldo = ld_of(y, d->N);
-  return run_gemm(p, pl.g, ox, ow, d->dtype, kDenseForward, "dense_fwd", dev, st);
+  return run_gemm(p, pl.g, ox, ow, d->dtype, kDenseForward, at(ws, pl.join), "dense_fwd", dev, st);
 }
 
 int conv2d_dense_bwd(const conv2d_dense_desc* d, const conv2d_mat* x, const conv2d_mat* w, const conv2d_mat* pre_act,
@@ -430,7 +467,7 @@ int conv2d_dense_bwd(const conv2d_dense_desc* d, const conv2d_mat* x, const conv
     DenseGemmParams p = {};
     p.out = dx->data;
     p.ldo = ld_of(dx, d->K);
-    if ((rc = run_gemm(p, pl.gx, odz, ow, d->dtype, kDenseDx, "dense_dx", dev, st))) return rc;
+    if ((rc = run_gemm(p, pl.gx, odz, ow, d->dtype, kDenseDx, at(ws, pl.joinx), "dense_dx", dev, st))) return rc;
   }
   if (dw) {
     Operand ox;
@@ -442,7 +479,7 @@ int conv2d_dense_bwd(const conv2d_dense_desc* d, const conv2d_mat* x, const conv
     p.out_f32 = joined || dw->type == CONV2D_FP32;
     p.accumulate = !joined && d->accumulate;
     p.split_stride = static_cast<long>(d->N) * d->K;
-    if ((rc = run_gemm(p, pl.gw, odz, ox, d->dtype, kDenseDw, "dense_dw", dev, st))) return rc;
+    if ((rc = run_gemm(p, pl.gw, odz, ox, d->dtype, kDenseDw, at(ws, pl.joinw), "dense_dw", dev, st))) return rc;
     if (joined)
       LAUNCH("dense_dw_join", st,
              launch_split_join(reinterpret_cast<float*>(base + pl.spart), pl.gw.splits, d->N, d->K, dw->type, dw->data,

@@ -30,7 +30,7 @@ constexpr int kPairWarps = 16;        // epilogue warps of the pair kernel: four
 constexpr int kPairThreads = 64 + 32 * kPairWarps;
 constexpr int kDenseMaxStages = 10;
 constexpr int kPairBuffers = kPairWarps * 2048;  // the pair kernel's epilogue: 32 rows x 64 bytes a warp
-enum : int { kSiteDenseFull = 11, kSiteDenseEmpty = 12, kSiteDenseTFull = 13, kSiteDenseTEmpty = 14 };
+enum : int { kSiteDenseFull = 11, kSiteDenseEmpty = 12, kSiteDenseTFull = 13, kSiteDenseTEmpty = 14, kSiteDenseJoin = 15 };
 // The three products: how the operands lie (R is MN-major for dW, C for dx and dW) and the epilogue.
 enum : int { kDenseForward = 0, kDenseDx = 1, kDenseDw = 2 };
 __host__ __device__ constexpr bool dense_r_mn(int mode) { return mode == kDenseDw; }
@@ -45,6 +45,13 @@ struct DenseGemmParams {
   long m;               // rows of the output
   int l_tiles, c_tiles, splits;
   int kb_total, kb_per_split;  // k-blocks of 128 bytes: 64 16-bit or 128 8-bit elements
+  // pair kernel: the units from `full` on (fewer than half the pairs, the last wave) are cut into `parts` along k,
+  // each run by a pair of its own; the one that ends up with the unit adds the others' sums from join_part
+  // [unit][parts - 1][2][BN / 32][4][32 columns][32 rows] once their flags [unit][parts - 1][2][kPairWarps] are 1.
+  // parts = 1: full is the number of units.
+  int full, parts;
+  float* join_part;
+  uint32_t* join_flag;
   int BN, stages, cluster;
   // kDenseForward: v = acc * ns[n] * ms[m] + bias[n]; z = v; out = act(v) + res
   const uint8_t *ns, *ms;  // scale bytes of 8-bit operands (both or neither)
@@ -296,12 +303,12 @@ __device__ __forceinline__ void residual_store(const DenseGemmParams& p, uint32_
 
 // A warp's 32 rows (m0 ..) x up to 32 columns (n ..) of the accumulator at taddr; nr rows and nc columns count.
 // res: the residual's registers, loaded for these columns and left loading for the columns from n + 128 (the
-// warp's next), so that its way from memory is hidden by the main loop or by the columns before. release() is
-// called when the accumulator has been read.
+// warp's next), so that its way from memory is hidden by the main loop or by the columns before. taken(a) is
+// called when the accumulator's columns are in a[] (it frees the accumulator, and adds other parts' sums).
 template <typename T, int MODE, typename F>
 __device__ __forceinline__ void pair_epilogue(const DenseGemmParams& p, uint32_t taddr, uint32_t buf, long m0, int n,
                                               int end, int nr, int split, float mscale, uint32_t (&res)[16], int lane,
-                                              F&& release) {
+                                              F&& taken) {
   const int nc = min(end - n, 32);
   if constexpr (MODE == kDenseForward) {
     float v[32];
@@ -309,7 +316,7 @@ __device__ __forceinline__ void pair_epilogue(const DenseGemmParams& p, uint32_t
       uint32_t a[32];
       tmem_ld32(taddr, a);
       tmem_ld_wait32(a);
-      release();
+      taken(a);
 #pragma unroll
       for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(a[e]);
     }
@@ -408,7 +415,7 @@ __device__ __forceinline__ void pair_epilogue(const DenseGemmParams& p, uint32_t
     uint32_t a[32];
     tmem_ld32(taddr, a);
     tmem_ld_wait32(a);
-    release();
+    taken(a);
     const bool tma = p.tma_out && !p.accumulate;
     if (p.out_f32) {
 #pragma unroll
@@ -490,6 +497,63 @@ __device__ __forceinline__ void dense_unit(const DenseGemmParams& p, int u, int&
   lt = l0 + i - ct * h;
 }
 
+// The it-th piece of work of pair cid of ncl: a unit, or in the last wave a part of one.
+struct DenseItem {
+  int lt, ct, split, kb0, kb1;
+  int tail, part;  // tail: index among the cut units, -1: a whole unit; part 0 ends up with the unit
+};
+__device__ __forceinline__ bool dense_item(const DenseGemmParams& p, int it, int cid, int ncl, DenseItem& o) {
+  const int u = cid + it * ncl;
+  if (u < p.full) {
+    dense_unit(p, u, o.lt, o.ct, o.split);
+    o.kb0 = o.split * p.kb_per_split;
+    o.kb1 = min(p.kb_total, o.kb0 + p.kb_per_split);
+    o.tail = -1;
+    o.part = 0;
+    return true;
+  }
+  if (p.parts <= 1) return false;
+  const int rem = p.l_tiles * p.c_tiles - p.full;
+  if (u >= p.full + ncl || cid >= rem * p.parts) return false;
+  // The pairs that wait for others' sums are the last ones: blocks start in the order of their index, so those that
+  // they wait for have started.
+  const int q = cid / rem;
+  o.tail = cid - q * rem;
+  o.part = q == p.parts - 1 ? 0 : q + 1;
+  dense_unit(p, p.full + o.tail, o.lt, o.ct, o.split);
+  o.kb0 = static_cast<int>(static_cast<long>(p.kb_total) * o.part / p.parts);
+  o.kb1 = static_cast<int>(static_cast<long>(p.kb_total) * (o.part + 1) / p.parts);
+  return true;
+}
+// The slot of a warp's sums of columns c .. c + 31 of its unit's tile (column-major, so that a warp's accesses are
+// whole lines).
+__device__ __forceinline__ float* join_slot(const DenseGemmParams& p, int tail, int part, int rank, int q, int c) {
+  const long tile = (static_cast<long>(tail) * (p.parts - 1) + part - 1) * 2 + rank;
+  return p.join_part + ((tile * (p.BN / 32) + c / 32) * 4 + q) * 1024;
+}
+__device__ __forceinline__ uint32_t* join_flag(const DenseGemmParams& p, int tail, int part, int rank, int warp) {
+  return p.join_flag + ((static_cast<long>(tail) * (p.parts - 1) + part - 1) * 2 + rank) * kPairWarps + warp;
+}
+__device__ __forceinline__ uint32_t ld_acquire(const uint32_t* p) {
+  uint32_t v;
+  asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
+__device__ __forceinline__ void st_release(uint32_t* p, uint32_t v) {
+  asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
+}
+// Bounded wait for a flag (see wait()).
+__device__ __forceinline__ bool wait_flag(const uint32_t* f, int* err) {
+  const uint64_t t0 = globaltimer();
+  for (uint32_t i = 1;; ++i) {
+    if (ld_acquire(f) == 1u) return true;
+    if ((i & 255u) == 0 && globaltimer() - t0 > kWaitLimitNs) {
+      atomicCAS(err, 0, kSiteDenseJoin);
+      return false;
+    }
+  }
+}
+
 template <typename T, int MODE, bool FP8>
 __global__ void __launch_bounds__(kPairThreads, 1) dense_pair_kernel(const __grid_constant__ DenseGemmParams p) {
   constexpr bool RMN = dense_r_mn(MODE), CMN = dense_c_mn(MODE);
@@ -510,7 +574,6 @@ __global__ void __launch_bounds__(kPairThreads, 1) dense_pair_kernel(const __gri
   const uint32_t rank = cluster_ctarank();
   const bool leader = rank == 0;
   const int cid = static_cast<int>(blockIdx.x >> 1), ncl = static_cast<int>(gridDim.x >> 1);
-  const int units = p.l_tiles * p.c_tiles * p.splits;
   const uint32_t tcols = tmem_cols_for(2 * BN);
 
   if (threadIdx.x == 0) {
@@ -545,12 +608,10 @@ __global__ void __launch_bounds__(kPairThreads, 1) dense_pair_kernel(const __gri
       uint32_t par = 0;
       bool alive = true;
       const int kelems = FP8 ? 128 : 64;
-      for (int u = cid; u < units && alive; u += ncl) {
-        int lt, ct, split;
-        dense_unit(p, u, lt, ct, split);
-        const int kb0 = split * p.kb_per_split, kb1 = min(p.kb_total, kb0 + p.kb_per_split);
-        const int lr = lt * 256 + static_cast<int>(rank) * 128, cr = ct * BN + static_cast<int>(rank) * (BN / 2);
-        for (int kb = kb0; kb < kb1; ++kb) {
+      DenseItem w;
+      for (int it = 0; alive && dense_item(p, it, cid, ncl, w); ++it) {
+        const int lr = w.lt * 256 + static_cast<int>(rank) * 128, cr = w.ct * BN + static_cast<int>(rank) * (BN / 2);
+        for (int kb = w.kb0; kb < w.kb1; ++kb) {
           if (!wait(&empty[s], par ^ 1, p.err, kSiteDenseEmpty)) {
             alive = false;
             break;
@@ -584,20 +645,18 @@ __global__ void __launch_bounds__(kPairThreads, 1) dense_pair_kernel(const __gri
       int s = 0, tc = 0;
       uint32_t par = 0;
       bool alive = true;
-      for (int u = cid; u < units && alive; u += ncl, ++tc) {
-        int lt, ct, split;
-        dense_unit(p, u, lt, ct, split);
-        const int kb0 = split * p.kb_per_split, kb1 = min(p.kb_total, kb0 + p.kb_per_split);
+      DenseItem w;
+      for (; alive && dense_item(p, tc, cid, ncl, w); ++tc) {
         const int buf = tc & 1;
         if (!wait(&tempty[buf], ((tc >> 1) & 1) ^ 1, p.err, kSiteDenseTEmpty)) break;
         tc_fence_after();
-        for (int kb = kb0; kb < kb1; ++kb) {
+        for (int kb = w.kb0; kb < w.kb1; ++kb) {
           if (!wait(&full[s], par, p.err, kSiteDenseFull)) {
             alive = false;
             break;
           }
           tc_fence_after();
-          dense_mma<true, FP8, RMN, CMN>(l, c, tmem + buf * BN, s * stage_bytes, idesc, kb > kb0);
+          dense_mma<true, FP8, RMN, CMN>(l, c, tmem + buf * BN, s * stage_bytes, idesc, kb > w.kb0);
           mma_commit_pair(&empty[s]);
           if (++s == S) {
             s = 0;
@@ -611,17 +670,16 @@ __global__ void __launch_bounds__(kPairThreads, 1) dense_pair_kernel(const __gri
     // four warps per TMEM lane quarter, which take the unit's columns 32 at a time in turn
     const int q = warp & 3, part = (warp - 2) >> 2;
     const uint32_t buf0 = sbase + S * stage_bytes + static_cast<uint32_t>(warp - 2) * 2048u;
-    int tc = 0;
-    for (int u = cid; u < units; u += ncl, ++tc) {
-      int lt, ct, split;
-      dense_unit(p, u, lt, ct, split);
-      const long m0 = static_cast<long>(lt) * 256 + rank * 128 + q * 32;
+    DenseItem w;
+    for (int tc = 0; dense_item(p, tc, cid, ncl, w); ++tc) {
+      const int ct = w.ct;
+      const long m0 = static_cast<long>(w.lt) * 256 + rank * 128 + q * 32;
       const int nr = static_cast<int>(min(p.m - m0, 32L));
       const float mscale = MODE == kDenseForward && p.ms && lane < nr ? q8_scale(p.ms[m0 + lane]) : 1.f;
       const int end = min(p.n, ct * BN + BN);
       const int n0 = ct * BN + part * 32;
       uint32_t res[16];
-      if (MODE == kDenseForward && p.res && nr > 0 && n0 < end)
+      if (MODE == kDenseForward && p.res && w.part == 0 && nr > 0 && n0 < end)
         residual_load<T>(p, res, m0, n0, nr, min(end - n0, 32), 0, lane);
       const int buf = tc & 1;
       int ok = 1;
@@ -636,13 +694,43 @@ __global__ void __launch_bounds__(kPairThreads, 1) dense_pair_kernel(const __gri
         __syncwarp();
         if (lane == 0) mbar_arrive_relaxed(mapa_shared(smem_u32(&tempty[buf]), 0));
       };
+      const uint32_t t0 = tmem + (static_cast<uint32_t>(q * 32) << 16) + buf * BN - ct * BN;
       if (nr <= 0 || n0 >= end) {  // uniform
         arrive();
+      } else if (w.part > 0) {
+        // a part of a cut unit: the sums go to the pair that ends up with it
+#pragma unroll 1
+        for (int n = n0; n < end; n += 128) {
+          uint32_t a[32];
+          tmem_ld32(t0 + n, a);
+          tmem_ld_wait32(a);
+          if (n + 128 >= end) arrive();
+          float* slot = join_slot(p, w.tail, w.part, static_cast<int>(rank), q, n - ct * BN) + lane;
+#pragma unroll
+          for (int e = 0; e < 32; ++e) slot[e * 32] = __uint_as_float(a[e]);
+        }
+        __threadfence();
+        __syncwarp();
+        if (lane == 0) st_release(join_flag(p, w.tail, w.part, static_cast<int>(rank), warp - 2), 1u);
       } else {
+        if (w.tail >= 0) {
+          ok = 1;
+          for (int j = 1; j < p.parts; ++j)
+            if (lane == 0 && ok) ok = wait_flag(join_flag(p, w.tail, j, static_cast<int>(rank), warp - 2), p.err) ? 1 : 0;
+          __syncwarp();
+        }
 #pragma unroll 1
         for (int n = n0; n < end; n += 128)
-          pair_epilogue<T, MODE>(p, tmem + (static_cast<uint32_t>(q * 32) << 16) + buf * BN + (n - ct * BN), buf0, m0, n,
-                                 end, nr, split, mscale, res, lane, [&] {
+          pair_epilogue<T, MODE>(p, t0 + n, buf0, m0, n, end, nr, w.split, mscale, res, lane,
+                                 [&](uint32_t (&a)[32]) {
+                                   if (w.tail >= 0) {
+                                     for (int j = 1; j < p.parts; ++j) {
+                                       const float* slot =
+                                           join_slot(p, w.tail, j, static_cast<int>(rank), q, n - ct * BN) + lane;
+#pragma unroll
+                                       for (int e = 0; e < 32; ++e) a[e] = __float_as_uint(__uint_as_float(a[e]) + __ldcg(slot + e * 32));
+                                     }
+                                   }
                                    if (n + 128 >= end) arrive();
                                  });
       }

@@ -253,6 +253,14 @@ def test_dense_fwd(M, K, N, dtype, act, has_bias, has_res, save, pad, bits8):
         assert bool(torch.as_strided(buf, (M, 3), (buf.stride(0), 1), buf.storage_offset() + N).isnan()[:M - 1].all())
 
 
+@pytest.mark.parametrize("M,K,N,dtype,act,has_res,save,bits8", [
+    (2600, 4096, 2048, BF, "gelu", True, "q8", False), (2601, 4100, 2050, HF, "silu", True, "full", False),
+    (2600, 8192, 2048, BF, "identity", False, "none", True), (8192, 2304, 2304, BF, "relu", False, "none", False)])
+def test_dense_fwd_cut_units(M, K, N, dtype, act, has_res, save, bits8):
+    """Outputs whose last wave of units leaves most of the SMs idle: its units are cut along k and joined."""
+    test_dense_fwd(M, K, N, dtype, act, True, has_res, save, 0, bits8)
+
+
 def test_dense_weights_in_8_bits_only():
     x, w = normal(1, 70, 200, dtype=BF), ops.q8_encode(normal(2, 96, 200, std=0.1), 32)
     y, _ = ops.dense_fwd(x, w)
@@ -343,6 +351,14 @@ def test_dense_bwd(M, K, N, dtype, act, q8, grad, pad):
     assert torch.equal(ops.dense_bwd(None, w, dy, z, act, need_dw=False, need_dbias=False)[0], dx)
     assert torch.equal(ops.dense_bwd(x, None, dy, z, act, need_dx=False, need_dbias=False, grad_dtype=grad)[1], dw)
     assert torch.equal(ops.dense_bwd(None, None, dy, z, act, need_dx=False, need_dw=False)[2], db)
+
+
+@pytest.mark.parametrize("M,K,N,dtype,act,q8,grad,pad", [
+    (2600, 2048, 4096, BF, "gelu", True, BF, 0),    # dx
+    (4096, 2601, 2050, HF, "identity", False, HF, 0),  # dw
+])
+def test_dense_bwd_cut_units(M, K, N, dtype, act, q8, grad, pad):
+    test_dense_bwd(M, K, N, dtype, act, q8, grad, pad)
 
 
 TINY_OF = {BF: 2.0 ** -133, HF: 2.0 ** -24, FP: 2.0 ** -149}
