@@ -112,6 +112,8 @@ __device__ __forceinline__ void mbar_arrive_relaxed(uint32_t caddr) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(caddr) : "memory");
 }
 
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 __device__ __forceinline__ void st_shared_cluster_f32(uint32_t caddr, float v) {
   asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(caddr), "f"(v) : "memory");
 }
@@ -782,7 +784,7 @@ __global__ void __launch_bounds__(kClusterThreads, 1) dense_cluster_kernel(const
   }
   tc_fence_before();
   __syncthreads();
-  if (CL > 1) cluster_sync();  // the others have started: their shared memory may be written
+  if (CL > 1) cluster_arrive();  // waited for before the other CTAs' shared memory is written
   tc_fence_after();
   const uint32_t tmem = *slot;
   pdl_entry();  // the set-up above runs under the end of the kernel before
@@ -848,7 +850,9 @@ __global__ void __launch_bounds__(kClusterThreads, 1) dense_cluster_kernel(const
     }
     int ok = 1;
     if (lane == 0) ok = wait(tfull, 0, p.err, kSiteDenseTFull) ? 1 : 0;
-    if (__shfl_sync(0xffffffffu, ok, 0)) {
+    ok = __shfl_sync(0xffffffffu, ok, 0);
+    if (CL > 1) cluster_wait();  // the others have started
+    if (ok) {
       tc_fence_after();
       const uint32_t t0 = tmem + (static_cast<uint32_t>(q * 32) << 16);
       const uint32_t join = sbase + S * stage_bytes;
@@ -878,6 +882,8 @@ __global__ void __launch_bounds__(kClusterThreads, 1) dense_cluster_kernel(const
     }
   }
   if (CL > 1) {
+    __syncwarp();
+    if (warp < 2) cluster_wait();
     __syncthreads();
     cluster_sync();  // every CTA's sums have arrived; from here on a CTA reads its own shared memory only
     // jobs of 4 columns x 32 lanes; the sums are added in rank order

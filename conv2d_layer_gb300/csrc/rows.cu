@@ -675,38 +675,55 @@ __global__ void __launch_bounds__(256) to_rows_kernel(const void* x, long ldx, c
   }
 }
 
-// The same for rows that do not start on vector boundaries, or end within a vector: a warp takes 256 neighbouring
-// elements of a row, 32 at a time.
-template <typename T, bool Q>
+// The same for rows that do not start on vector boundaries, or end within a vector: a warp takes 32 N W neighbouring
+// elements of a row, W neighbours a lane (W = 2: output rows start on boundaries of two elements).
+template <typename T, bool Q, int W>
 __global__ void __launch_bounds__(256) to_rows_ragged_kernel(const void* x, long ldx, const uint8_t* scale, int group,
                                                              int ng, long rows, int cols, T* out, long ldo) {
   pdl_entry();
-  constexpr int N = 8;
+  constexpr int N = 8 / W;
   const int lane = threadIdx.x & 31;
-  const int chunks = (cols + 32 * N - 1) / (32 * N);
+  const int chunks = (cols + 255) / 256;
   const long total = rows * chunks;
   for (long j = static_cast<long>(blockIdx.x) * 8 + (threadIdx.x >> 5); j < total; j += static_cast<long>(gridDim.x) * 8) {
     const long row = chunks == 1 ? j : j / chunks;
-    const int c0 = static_cast<int>(j - row * chunks) * 32 * N + lane;
-    T e[N];
+    const int c0 = static_cast<int>(j - row * chunks) * 256 + lane * W;
+    T e[N][W];
     uint32_t raw[N], sb[N];
 #pragma unroll
     for (int k = 0; k < N; ++k) {
-      const int c = c0 + 32 * k;
+      const int c = c0 + 32 * W * k;
       if (c >= cols) continue;
       if constexpr (Q) {
-        raw[k] = static_cast<const uint8_t*>(x)[row * ldx + c];
-        sb[k] = scale[row * ng + (group ? c / kQ8Group : 0)];
+        const uint8_t* p = static_cast<const uint8_t*>(x) + row * ldx + c;
+        raw[k] = p[0];
+        if (W == 2 && c + 1 < cols) raw[k] |= static_cast<uint32_t>(p[1]) << 8;
+        sb[k] = scale[row * ng + (group ? c / kQ8Group : 0)];  // c is even: both neighbours are of one group
       } else {
-        e[k] = static_cast<const T*>(x)[row * ldx + c];
+#pragma unroll
+        for (int w = 0; w < W; ++w)
+          if (w == 0 || c + w < cols) e[k][w] = static_cast<const T*>(x)[row * ldx + c + w];
       }
     }
 #pragma unroll
     for (int k = 0; k < N; ++k) {
-      const int c = c0 + 32 * k;
+      const int c = c0 + 32 * W * k;
       if (c >= cols) continue;
-      if constexpr (Q) e[k] = from_q8<T>(q8_unpack2(raw[k]).x * q8_scale(sb[k]));
-      out[row * ldo + c] = e[k];
+      if constexpr (Q) {
+        const float2 f = q8_unpack2(raw[k]);
+        const float sc = q8_scale(sb[k]);
+        e[k][0] = from_q8<T>(f.x * sc);
+        if constexpr (W == 2) e[k][1] = from_q8<T>(f.y * sc);
+      }
+      T* o = out + row * ldo + c;
+      if constexpr (W == 2 && sizeof(T) == 2) {
+        if (c + 1 < cols) *reinterpret_cast<uint32_t*>(o) = *reinterpret_cast<const uint32_t*>(e[k]);
+        else o[0] = e[k][0];
+      } else {
+#pragma unroll
+        for (int w = 0; w < W; ++w)
+          if (c + w < cols) o[w] = e[k][w];
+      }
     }
   }
 }
@@ -734,8 +751,15 @@ cudaError_t to_rows(const conv2d_mat& x, long rows, int cols, void* out, long ld
     T* o = static_cast<T*>(out);
     const void* src = x.data;
     const uint8_t* sc = x.scale;
-    return q ? launch_k(to_rows_ragged_kernel<T, true>, grid, dim3(256), 0, st, 1, src, ldx, sc, x.group, ng, rows, cols, o, ld)
-             : launch_k(to_rows_ragged_kernel<T, false>, grid, dim3(256), 0, st, 1, src, ldx, sc, x.group, ng, rows, cols, o, ld);
+#define RAGGED(Q, W)                                                                                                     \
+  return launch_k(to_rows_ragged_kernel<T, Q, W>, grid, dim3(256), 0, st, 1, src, ldx, sc, x.group, ng, rows, cols, o, ld)
+    if (sizeof(T) == 2 && ld % 2 == 0) {
+      if (q) RAGGED(true, 2);
+      RAGGED(false, 2);
+    }
+    if (q) RAGGED(true, 1);
+    RAGGED(false, 1);
+#undef RAGGED
   }
   const int nv = cols / V;
   const long slab = std::max<long>(1, 0x7fffffffL / nv);  // rows a launch indexes in 31 bits
@@ -943,7 +967,7 @@ cudaError_t launch_to_rows(const conv2d_mat& x, long rows, int cols, int dt, voi
 
 cudaError_t launch_move_bytes(const void* x, long ldx, long rows, int cols, void* out, long ldo, cudaStream_t st) {
   const dim3 grid(static_cast<unsigned>(std::min<long>((rows * ((cols + 255) / 256) + 7) / 8, 152L * 64)));
-  return launch_k(to_rows_ragged_kernel<uint8_t, false>, grid, dim3(256), 0, st, 1, x, ldx,
+  return launch_k(to_rows_ragged_kernel<uint8_t, false, 1>, grid, dim3(256), 0, st, 1, x, ldx,
                   static_cast<const uint8_t*>(nullptr), 0, 1, rows, cols, static_cast<uint8_t*>(out), ldo);
 }
 
