@@ -80,7 +80,7 @@ def build_binding(force=False):
     tmp = BINDING + ".tmp%d" % os.getpid()
     cmd = (["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
             "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch._C._GLIBCXX_USE_CXX11_ABI)] + ["-I" + i for i in inc]
-           + [BINDING_SRC, "-o", tmp, "-L" + os.path.join(top, "lib"), "-lc10", "-ltorch_cpu", "-ltorch_python",
+           + [BINDING_SRC, "-o", tmp, "-L" + os.path.join(top, "lib"), "-lc10", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python",
               "-lc10_cuda", "-ldl"])
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:

@@ -8,6 +8,7 @@
 // than CONV2D_OK goes to abi.check (Conv2dError).
 #include <Python.h>
 
+#include <ATen/cuda/EmptyTensor.h>
 #include <ATen/ops/empty.h>
 #include <c10/core/DeviceGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -156,7 +157,9 @@ float* vec_of(const at::Tensor& t, const char* name, int64_t n, at::Device dev) 
 }
 float* vec(PyObject* o, const char* name, int64_t n, at::Device dev) { return vec_of(tensor(o, name), name, n, dev); }
 
+// Straight from the CUDA allocator's factory: the dispatcher's way costs a call half as much again.
 at::Tensor make(at::IntArrayRef size, at::ScalarType t, at::Device dev) {
+  if (dev.is_cuda()) return at::detail::empty_cuda(size, t, dev, std::nullopt);
   return at::empty(size, at::TensorOptions().dtype(t).device(dev));
 }
 conv2d_mat new_mat(at::Tensor& t, int64_t rows, int64_t cols, at::ScalarType type, at::Device dev) {
