@@ -851,6 +851,7 @@ __global__ void __launch_bounds__(kClusterThreads, 1) dense_cluster_kernel(const
     int ok = 1;
     if (lane == 0) ok = wait(tfull, 0, p.err, kSiteDenseTFull) ? 1 : 0;
     ok = __shfl_sync(0xffffffffu, ok, 0);
+    pdl_release();
     if (CL > 1) cluster_wait();  // the others have started
     if (ok) {
       tc_fence_after();

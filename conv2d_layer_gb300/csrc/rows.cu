@@ -169,6 +169,7 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) rows_fwd_kernel(const N
       if (t == 0 && i < nr && a.inv) a.inv[row0 + i] = inv[i];
     }
   }
+  pdl_release();
   // y = gamma h s of vector u, in place, for all NR rows (U = 0: of the one vector at hand)
   auto scale = [&](int u, int slot) {
     const int c = u * TPR + t;
@@ -438,6 +439,7 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR, TPR <= 256 ? 2 : 1) nor
         }
       }
     }
+    pdl_release();
     if (!a.part) return;
     float* part = a.part + static_cast<long>(blockIdx.x) * a.cols;
     if constexpr (RPB > 1) {
@@ -539,6 +541,7 @@ template <typename T, bool ENC>
 __global__ void __launch_bounds__(256) q8_flat_kernel(T* x, long ldx, uint8_t* q, long ldq, uint8_t* scale,
                                                       uint32_t total, FastDiv div_nv) {
   pdl_entry();
+  pdl_release();
   constexpr int N = 2;
   const uint32_t step = gridDim.x * 256u;
   const int ng = static_cast<int>(div_nv.d / 2);
@@ -631,6 +634,7 @@ template <typename T, int V, bool Q>
 __global__ void __launch_bounds__(256) to_rows_kernel(const void* x, long ldx, const uint8_t* scale, int group, int ng,
                                                       uint32_t total, int cols, FastDiv div_nv, T* out, long ldo) {
   pdl_entry();
+  pdl_release();
   constexpr int VO = V * sizeof(T) > 16 ? 16 / static_cast<int>(sizeof(T)) : V;  // elements a store
   constexpr int N = 2;                                                          // steps in flight
   const uint32_t step = gridDim.x * 256u;
@@ -681,6 +685,7 @@ template <typename T, bool Q, int W>
 __global__ void __launch_bounds__(256) to_rows_ragged_kernel(const void* x, long ldx, const uint8_t* scale, int group,
                                                              int ng, long rows, int cols, T* out, long ldo) {
   pdl_entry();
+  pdl_release();
   constexpr int N = 8 / W;
   const int lane = threadIdx.x & 31;
   const int chunks = (cols + 255) / 256;
@@ -864,6 +869,7 @@ __global__ void __launch_bounds__(256, V == 16 ? 2 : 3) dact_kernel(const DactAr
       }
     });
   }
+  pdl_release();
   if (!a.part) return;
 #pragma unroll
   for (int k = 0; k < V; ++k) sums[rl][lane * V + k] = acc[k];
@@ -901,6 +907,7 @@ cudaError_t dact(const DactArgs& a, int zk, int strips, cudaStream_t st) {
 __global__ void __launch_bounds__(256) column_sum_kernel(const float* part, int G, int cols, float* out,
                                                          int accumulate) {
   pdl_entry();
+  pdl_release();
   __shared__ float s[8][33];
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int c = static_cast<int>(blockIdx.x) * 32 + lane;
@@ -924,6 +931,7 @@ template <typename T, int V>
 __global__ void __launch_bounds__(256) split_join_kernel(const float* part, int splits, long rows, int cols, T* out,
                                                          long ldo, int accumulate) {
   pdl_entry();
+  pdl_release();
   const int nv = cols / V;
   const long total = rows * nv, plane = rows * cols;
   for (long j = static_cast<long>(blockIdx.x) * 256 + threadIdx.x; j < total; j += static_cast<long>(gridDim.x) * 256) {
@@ -950,6 +958,7 @@ __global__ void __launch_bounds__(256) split_join_kernel(const float* part, int 
 template <typename T>
 __global__ void __launch_bounds__(256) zero_rows_kernel(long rows, int cols, T* out, long ld) {
   pdl_entry();
+  pdl_release();
   const long total = rows * cols;
   for (long j = static_cast<long>(blockIdx.x) * 256 + threadIdx.x; j < total; j += static_cast<long>(gridDim.x) * 256) {
     const long row = j / cols;
