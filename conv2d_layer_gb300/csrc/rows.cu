@@ -76,7 +76,8 @@ struct NormArgs {
 // U = 0 is the form for rows longer than that, which reads the row again for each phase (from L2, mostly). NR
 // rows are in flight at once where a row is a vector or two a thread (one row of 512 bytes a warp left a
 // 200704 x 256 encode at 41 us). Threads hold neighbouring vectors, so a group of 32 columns lies in 32 / V
-// neighbouring lanes and its maximum is found by shuffles.
+// neighbouring lanes and its maximum is found by shuffles. Bound by memory: 8192 x 4096 bf16 with the residual, y
+// and its 8-bit form moves 303 MB in 47 us, 0.95 of the measured copy rate.
 template <typename T, int V, int TPR, int U, int NR, bool NORM>
 __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) rows_fwd_kernel(const NormArgs a) {
   pdl_entry();
@@ -341,6 +342,8 @@ struct NormBwdArgs {
 // columns in registers. AHEAD: gamma too, and the vectors of the next row are in flight while this one is reduced;
 // without it (rows whose values take the registers) gamma and dh are read where they are needed. U = 0: rows
 // longer than the registers hold; each row is read twice and dgamma's sums live in this block's row of `part`.
+// Bound by memory: 8192 x 4096 bf16 with dh moves 268 MB in 46 us, 0.85 of the copy rate (64 us with one block of
+// 136 registers a thread an SM, before the registers were held to two).
 template <typename T, int V, int TPR, int U, bool AHEAD>
 __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR, TPR <= 256 ? 2 : 1) norm_bwd_kernel(const NormBwdArgs a) {
   pdl_entry();
@@ -536,7 +539,7 @@ cudaError_t norm_bwd(const NormBwdArgs& a, int grid, cudaStream_t st) {
 
 // ------------------------------------------------------------------ 8 bits, 16-bit types in whole groups
 // Encode (ENC) or decode of rows of whole 32-column groups: two threads a group, 16 values each, two groups of a
-// thread in flight. total = rows * cols / 16 < 2^31; x rows on 32-byte, q rows on 16-byte boundaries.
+// thread in flight (200704 x 256 there and back: 46.5 us, 0.99 of the copy rate; 59 us with 16-byte accesses). total = rows * cols / 16 < 2^31; x rows on 32-byte, q rows on 16-byte boundaries.
 template <typename T, bool ENC>
 __global__ void __launch_bounds__(256) q8_flat_kernel(T* x, long ldx, uint8_t* q, long ldq, uint8_t* scale,
                                                       uint32_t total, FastDiv div_nv) {
@@ -799,7 +802,8 @@ struct DactArgs {
 
 // A block is 32 lanes of V columns by 8 rows; it walks the rows of its strip and keeps the column sums of
 // the unrounded dz in registers, joined over the 8 row lanes at the end. ZK: 0 no activation, 1 z in T,
-// 2 z as E4M3.
+// 2 z as E4M3. Memory bounds it, with two special-function operations a value close behind (gelu): 4096 x 8192
+// from 8-bit z moves 169 MB in 34 us, 0.74 of the copy rate (16 columns a lane; 70 against 63 us with 8 at twice the rows).
 template <typename T, int V, int ZK>
 __global__ void __launch_bounds__(256, V == 16 ? 2 : 3) dact_kernel(const DactArgs a) {
   pdl_entry();
