@@ -3,9 +3,9 @@
 //
 //   conv2d_dense_fwd: [decode / repack x, w] -> GEMM (epilogue: scales, bias,
 //                     z in 16 or 8 bits, activation, residual)
-//   conv2d_dense_bwd: [dz = dy act'(z), column sums -> dbias] -> [decode /
-//                     repack w -> dx GEMM] -> [decode / repack x -> dW GEMM
-//                     -> join of its splits]
+//   conv2d_dense_bwd: [decode / repack w, x] and [dz = dy act'(z), column
+//                     partials] side by side -> dx GEMM, dW GEMM and column
+//                     sums (dbias) side by side -> [join of dW's splits]
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -187,7 +187,7 @@ struct Operand {
 // out[m][n] = sum_k R[m][k] C[n][k]. The rows of the output are the accumulator's lanes in the pair kernel and its
 // columns in the cluster kernel.
 int run_gemm(DenseGemmParams& p, const GemmPlan& g, const Operand& r, const Operand& c, int dt, int mode, void* join,
-             const char* name, const DevInfo* dev, cudaStream_t st) {
+             bool late, const char* name, const DevInfo* dev, cudaStream_t st) {
   const bool r_mn = dense_r_mn(mode), c_mn = dense_c_mn(mode);
   const Operand &lo = g.pair ? r : c, &co = g.pair ? c : r;
   if (!encode_operand(&p.tl, lo.data, lo.type, lo.rows, lo.cols, lo.ld, g.pair ? r_mn : c_mn, 128) ||
@@ -213,8 +213,11 @@ int run_gemm(DenseGemmParams& p, const GemmPlan& g, const Operand& r, const Oper
     p.join_part = static_cast<float*>(join);
     p.join_flag = reinterpret_cast<uint32_t*>(static_cast<char*>(join) + g.join_bytes);
     LAUNCH("zero", st, launch_zero_rows(1, static_cast<int>(g.join_flags), CONV2D_FP32, p.join_flag,
-                                        static_cast<long>(g.join_flags), st));
+                                        static_cast<long>(g.join_flags), late, st));
+    late = false;  // the flags are waited for
   }
+  p.late = late;
+  p.early = g.grid <= dev->sms * 3 / 4;
   p.l_tiles = g.l_tiles;
   p.c_tiles = g.c_tiles;
   p.splits = g.splits;
@@ -271,16 +274,18 @@ size_t plan_copy(Carver& c, const conv2d_mat* m, long rows, int cols, bool as_8b
   if (m->type != CONV2D_E4M3 && ld_of(m, cols) % 8 == 0) return kNone;
   return c.take(static_cast<size_t>(rows) * round_up(cols, 8) * 2);
 }
-// The operand itself, or its copy in the workspace.
+// The operand itself, or its copy in the workspace; *started: a kernel of this call has been launched.
 int make_operand(Operand* o, const conv2d_mat* m, long rows, int cols, bool as_8bit, int dt, size_t off, void* ws,
-                 const char* name, cudaStream_t st) {
+                 const char* name, bool* started, cudaStream_t st) {
   *o = {m->data, as_8bit ? static_cast<int>(CONV2D_E4M3) : dt, rows, cols, ld_of(m, cols)};
   if (off == kNone) return CONV2D_OK;
   char* to = static_cast<char*>(ws) + off;
   o->data = to;
   o->ld = round_up(cols, as_8bit ? 16 : 8);
-  if (as_8bit) LAUNCH(name, st, launch_move_bytes(m->data, ld_of(m, cols), rows, cols, to, o->ld, st));
-  else LAUNCH(name, st, launch_to_rows(*m, rows, cols, dt, to, o->ld, st));
+  const int late = *started;  // nothing before it in the call touches these operands
+  *started = true;
+  if (as_8bit) LAUNCH(name, st, launch_move_bytes(m->data, ld_of(m, cols), rows, cols, to, o->ld, late, st));
+  else LAUNCH(name, st, launch_to_rows(*m, rows, cols, dt, to, o->ld, late, st));
   return CONV2D_OK;
 }
 
@@ -394,8 +399,9 @@ int conv2d_dense_fwd(const conv2d_dense_desc* d, const conv2d_mat* x, const conv
   if (uses_ws && (!ws || ws_bytes < pl.total || (reinterpret_cast<uintptr_t>(ws) & 255u))) return CONV2D_ERR_WORKSPACE;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   Operand ox, ow;
-  if ((rc = make_operand(&ox, x, d->M, d->K, pl.fp8, d->dtype, pl.x, ws, "dense_x", st))) return rc;
-  if ((rc = make_operand(&ow, w, d->N, d->K, pl.fp8, d->dtype, pl.w, ws, "dense_w", st))) return rc;
+  bool started = false;
+  if ((rc = make_operand(&ox, x, d->M, d->K, pl.fp8, d->dtype, pl.x, ws, "dense_x", &started, st))) return rc;
+  if ((rc = make_operand(&ow, w, d->N, d->K, pl.fp8, d->dtype, pl.w, ws, "dense_w", &started, st))) return rc;
   DenseGemmParams p = {};
   if (pl.fp8) {
     p.ns = w->scale;
@@ -419,7 +425,7 @@ int conv2d_dense_fwd(const conv2d_dense_desc* d, const conv2d_mat* x, const conv
   }
   p.out = y->data;
   p.ldo = ld_of(y, d->N);
-  return run_gemm(p, pl.g, ox, ow, d->dtype, kDenseForward, at(ws, pl.join), "dense_fwd", dev, st);
+  return run_gemm(p, pl.g, ox, ow, d->dtype, kDenseForward, at(ws, pl.join), false, "dense_fwd", dev, st);
 }
 
 int conv2d_dense_bwd(const conv2d_dense_desc* d, const conv2d_mat* x, const conv2d_mat* w, const conv2d_mat* pre_act,
@@ -434,8 +440,8 @@ int conv2d_dense_bwd(const conv2d_dense_desc* d, const conv2d_mat* x, const conv
   if (d->M == 0) {  // sums over no rows
     if (d->accumulate || (!dw && !dbias)) return CONV2D_OK;
     if ((rc = device_info(&dev))) return rc;
-    if (dw) LAUNCH("zero", st, launch_zero_rows(d->N, d->K, dw->type, dw->data, ld_of(dw, d->K), st));
-    if (dbias) LAUNCH("zero", st, launch_zero_rows(1, d->N, CONV2D_FP32, dbias, d->N, st));
+    if (dw) LAUNCH("zero", st, launch_zero_rows(d->N, d->K, dw->type, dw->data, ld_of(dw, d->K), 0, st));
+    if (dbias) LAUNCH("zero", st, launch_zero_rows(1, d->N, CONV2D_FP32, dbias, d->N, 0, st));
     return CONV2D_OK;
   }
   const bool act = d->act != CONV2D_ACT_IDENTITY;
@@ -448,43 +454,48 @@ int conv2d_dense_bwd(const conv2d_dense_desc* d, const conv2d_mat* x, const conv
   if (!ws || ws_bytes < pl.total || (reinterpret_cast<uintptr_t>(ws) & 255u)) return CONV2D_ERR_WORKSPACE;
   char* base = static_cast<char*>(ws);
 
+  // What only reads the call's arguments goes first and side by side: the operands' copies and dz. Then dx, dW
+  // beside it (they share their inputs only), and the bias gradient beside both.
+  bool started = false;
+  Operand ow, ox;
+  if (dx && (rc = make_operand(&ow, w, d->N, d->K, false, d->dtype, pl.w, ws, "dense_w", &started, st))) return rc;
+  if (dw && (rc = make_operand(&ox, x, d->M, d->K, false, d->dtype, pl.x, ws, "dense_x", &started, st))) return rc;
   Operand odz = {dy->data, d->dtype, d->M, d->N, ld_of(dy, d->N)};
+  float* part = dbias ? reinterpret_cast<float*>(base + pl.dpart) : nullptr;
   if (pl.dz_own || dbias) {
     void* dz = pl.dz_own ? base + pl.dz : nullptr;
-    float* part = dbias ? reinterpret_cast<float*>(base + pl.dpart) : nullptr;
     LAUNCH("dense_dact", st,
-           launch_dact(act ? pre_act : nullptr, *dy, d->M, d->N, d->dtype, d->act, dz, pl.lddz, part, pl.dact, st));
-    if (dbias)
-      LAUNCH("column_sum", st, launch_column_sum(part, pl.dact.strips, d->N, dbias, d->accumulate != 0, st));
+           launch_dact(act ? pre_act : nullptr, *dy, d->M, d->N, d->dtype, d->act, dz, pl.lddz, part, pl.dact, started,
+                       st));
     if (dz) {
       odz.data = dz;
       odz.ld = pl.lddz;
     }
   }
   if (dx) {
-    Operand ow;
-    if ((rc = make_operand(&ow, w, d->N, d->K, false, d->dtype, pl.w, ws, "dense_w", st))) return rc;
     DenseGemmParams p = {};
     p.out = dx->data;
     p.ldo = ld_of(dx, d->K);
-    if ((rc = run_gemm(p, pl.gx, odz, ow, d->dtype, kDenseDx, at(ws, pl.joinx), "dense_dx", dev, st))) return rc;
+    if ((rc = run_gemm(p, pl.gx, odz, ow, d->dtype, kDenseDx, at(ws, pl.joinx), false, "dense_dx", dev, st))) return rc;
   }
+  const bool joined = dw && pl.gw.splits > 1;
   if (dw) {
-    Operand ox;
-    if ((rc = make_operand(&ox, x, d->M, d->K, false, d->dtype, pl.x, ws, "dense_x", st))) return rc;
     DenseGemmParams p = {};
-    const bool joined = pl.gw.splits > 1;
     p.out = joined ? static_cast<void*>(base + pl.spart) : dw->data;
     p.ldo = joined ? d->K : ld_of(dw, d->K);
     p.out_f32 = joined || dw->type == CONV2D_FP32;
     p.accumulate = !joined && d->accumulate;
     p.split_stride = static_cast<long>(d->N) * d->K;
-    if ((rc = run_gemm(p, pl.gw, odz, ox, d->dtype, kDenseDw, at(ws, pl.joinw), "dense_dw", dev, st))) return rc;
-    if (joined)
-      LAUNCH("dense_dw_join", st,
-             launch_split_join(reinterpret_cast<float*>(base + pl.spart), pl.gw.splits, d->N, d->K, dw->type, dw->data,
-                               ld_of(dw, d->K), d->accumulate != 0, st));
+    if ((rc = run_gemm(p, pl.gw, odz, ox, d->dtype, kDenseDw, at(ws, pl.joinw), dx != nullptr, "dense_dw", dev, st)))
+      return rc;
   }
+  if (dbias)
+    LAUNCH("column_sum", st,
+           launch_column_sum(part, pl.dact.strips, d->N, dbias, d->accumulate != 0, dx || dw, st));
+  if (joined)
+    LAUNCH("dense_dw_join", st,
+           launch_split_join(reinterpret_cast<float*>(base + pl.spart), pl.gw.splits, d->N, d->K, dw->type, dw->data,
+                             ld_of(dw, d->K), d->accumulate != 0, st));
   return CONV2D_OK;
 }
 

@@ -73,6 +73,8 @@ struct DenseGemmParams {
   void* out;
   long ldo;
   int tma_out, vec_res, tma_z;  // rows of out / res / z (zq) start on 16-byte boundaries: tout, tz are set
+  int late;   // runs beside the kernel before it (see pdl_entry)
+  int early;  // leaves SMs idle: the kernel after this one may start at once
   int* err;
 };
 
@@ -607,7 +609,8 @@ __global__ void __launch_bounds__(kPairThreads, 1) dense_pair_kernel(const __gri
   cluster_sync();  // the peer's barriers are initialised before any remote arrival
   tc_fence_after();
   const uint32_t tmem = *slot;
-  pdl_entry();  // the set-up above runs under the end of the kernel before
+  if (!p.late) pdl_entry();  // the set-up above runs under the end of the kernel before
+  if (p.early) pdl_release();
 
   if (warp == 0) {
     if (elect_one()) {
@@ -751,6 +754,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) dense_pair_kernel(const __gri
     tc_fence_after();
     tmem_dealloc_pair(tmem, tcols);
   }
+  if (p.late) pdl_entry();
 }
 
 template <typename T, int MODE, bool FP8>
@@ -792,7 +796,8 @@ __global__ void __launch_bounds__(kClusterThreads, 1) dense_cluster_kernel(const
   if (CL > 1) cluster_arrive();  // waited for before the other CTAs' shared memory is written
   tc_fence_after();
   const uint32_t tmem = *slot;
-  pdl_entry();  // the set-up above runs under the end of the kernel before
+  if (!p.late) pdl_entry();  // the set-up above runs under the end of the kernel before
+  if (p.early) pdl_release();
 
   int lt, ct, split;
   dense_unit(p, static_cast<int>(blockIdx.x) / CL, lt, ct, split);
@@ -921,6 +926,7 @@ __global__ void __launch_bounds__(kClusterThreads, 1) dense_cluster_kernel(const
     tc_fence_after();
     tmem_dealloc(tmem, tcols);
   }
+  if (p.late) pdl_entry();
 }
 
 }  // namespace c2d

@@ -542,8 +542,8 @@ cudaError_t norm_bwd(const NormBwdArgs& a, int grid, cudaStream_t st) {
 // thread in flight (200704 x 256 there and back: 46.5 us, 0.99 of the copy rate; 59 us with 16-byte accesses). total = rows * cols / 16 < 2^31; x rows on 32-byte, q rows on 16-byte boundaries.
 template <typename T, bool ENC>
 __global__ void __launch_bounds__(256) q8_flat_kernel(T* x, long ldx, uint8_t* q, long ldq, uint8_t* scale,
-                                                      uint32_t total, FastDiv div_nv) {
-  pdl_entry();
+                                                      uint32_t total, FastDiv div_nv, int late) {
+  if (!late) pdl_entry();
   pdl_release();
   constexpr int N = 2;
   const uint32_t step = gridDim.x * 256u;
@@ -613,12 +613,13 @@ __global__ void __launch_bounds__(256) q8_flat_kernel(T* x, long ldx, uint8_t* q
       }
     }
   }
+  if (late) pdl_entry();
 }
 int stream_grid(long items) { return static_cast<int>(std::max<long>(1, std::min<long>((items + 255) / 256, 152L * 64))); }
 
 // Whether the flat kernel takes it, and its launch.
 template <typename T, bool ENC>
-bool q8_flat(const void* x, long ldx, const void* q, long ldq, uint8_t* scale, int group, long rows, int cols,
+bool q8_flat(const void* x, long ldx, const void* q, long ldq, uint8_t* scale, int group, long rows, int cols, int late,
              cudaStream_t st, cudaError_t* e) {
   if (group != kQ8Group || cols % kQ8Group != 0 || ldx % 16 != 0 || ldq % 16 != 0 ||
       reinterpret_cast<uintptr_t>(x) % 32 != 0 || rows * (cols / 16) > 0x7fffffffL)
@@ -626,7 +627,7 @@ bool q8_flat(const void* x, long ldx, const void* q, long ldq, uint8_t* scale, i
   const long total = rows * (cols / 16);
   *e = launch_k(q8_flat_kernel<T, ENC>, dim3(stream_grid((total + 1) / 2)), dim3(256), 0, st, 1,
                 static_cast<T*>(const_cast<void*>(x)), ldx, static_cast<uint8_t*>(const_cast<void*>(q)), ldq, scale,
-                static_cast<uint32_t>(total), make_fastdiv(static_cast<uint32_t>(cols / 16)));
+                static_cast<uint32_t>(total), make_fastdiv(static_cast<uint32_t>(cols / 16)), late);
   return true;
 }
 
@@ -635,8 +636,9 @@ bool q8_flat(const void* x, long ldx, const void* q, long ldq, uint8_t* scale, i
 // their scale, two output vectors). rows * ceil(cols / V) below 2^31 (see to_rows).
 template <typename T, int V, bool Q>
 __global__ void __launch_bounds__(256) to_rows_kernel(const void* x, long ldx, const uint8_t* scale, int group, int ng,
-                                                      uint32_t total, int cols, FastDiv div_nv, T* out, long ldo) {
-  pdl_entry();
+                                                      uint32_t total, int cols, FastDiv div_nv, T* out, long ldo,
+                                                      int late) {
+  if (!late) pdl_entry();
   pdl_release();
   constexpr int VO = V * sizeof(T) > 16 ? 16 / static_cast<int>(sizeof(T)) : V;  // elements a store
   constexpr int N = 2;                                                          // steps in flight
@@ -680,14 +682,15 @@ __global__ void __launch_bounds__(256) to_rows_kernel(const void* x, long ldx, c
       for (int k = 0; k < V; k += VO) st_vec<T, VO>(o + k, *reinterpret_cast<const T(*)[VO]>(&e[i][k]));
     }
   }
+  if (late) pdl_entry();
 }
 
 // The same for rows that do not start on vector boundaries, or end within a vector: a warp takes 32 N W neighbouring
 // elements of a row, W neighbours a lane (W = 2: output rows start on boundaries of two elements).
 template <typename T, bool Q, int W>
 __global__ void __launch_bounds__(256) to_rows_ragged_kernel(const void* x, long ldx, const uint8_t* scale, int group,
-                                                             int ng, long rows, int cols, T* out, long ldo) {
-  pdl_entry();
+                                                             int ng, long rows, int cols, T* out, long ldo, int late) {
+  if (!late) pdl_entry();
   pdl_release();
   constexpr int N = 8 / W;
   const int lane = threadIdx.x & 31;
@@ -734,6 +737,7 @@ __global__ void __launch_bounds__(256) to_rows_ragged_kernel(const void* x, long
       }
     }
   }
+  if (late) pdl_entry();
 }
 
 // Rows that start on boundaries of a vector of V elements of es bytes (the base at least on 16 bytes by contract).
@@ -742,7 +746,7 @@ bool vec_ok(const void* p, long ld, int es, int V) {
 }
 
 template <typename T>
-cudaError_t to_rows(const conv2d_mat& x, long rows, int cols, void* out, long ldo, cudaStream_t st) {
+cudaError_t to_rows(const conv2d_mat& x, long rows, int cols, void* out, long ldo, int late, cudaStream_t st) {
   constexpr int VV = 16 / sizeof(T), VQ = 16;
   const bool q = x.type == CONV2D_E4M3;
   const long ldx = x.ld ? x.ld : cols, ld = ldo ? ldo : cols;
@@ -750,7 +754,7 @@ cudaError_t to_rows(const conv2d_mat& x, long rows, int cols, void* out, long ld
   // whole vectors only: cols a multiple of the vector, and both rows' starts aligned to theirs
   if constexpr (sizeof(T) == 2) {
     cudaError_t e;
-    if (q && q8_flat<T, false>(out, ld, x.data, ldx, x.scale, x.group, rows, cols, st, &e)) return e;
+    if (q && q8_flat<T, false>(out, ld, x.data, ldx, x.scale, x.group, rows, cols, late, st, &e)) return e;
   }
   const int V = q ? VQ : VV;
   const bool vec = cols % V == 0 && vec_ok(out, ld, sizeof(T), VV) && vec_ok(x.data, ldx, q ? 1 : sizeof(T), V);
@@ -760,7 +764,7 @@ cudaError_t to_rows(const conv2d_mat& x, long rows, int cols, void* out, long ld
     const void* src = x.data;
     const uint8_t* sc = x.scale;
 #define RAGGED(Q, W)                                                                                                     \
-  return launch_k(to_rows_ragged_kernel<T, Q, W>, grid, dim3(256), 0, st, 1, src, ldx, sc, x.group, ng, rows, cols, o, ld)
+  return launch_k(to_rows_ragged_kernel<T, Q, W>, grid, dim3(256), 0, st, 1, src, ldx, sc, x.group, ng, rows, cols, o, ld, late)
     if (sizeof(T) == 2 && ld % 2 == 0) {
       if (q) RAGGED(true, 2);
       RAGGED(false, 2);
@@ -781,7 +785,7 @@ cudaError_t to_rows(const conv2d_mat& x, long rows, int cols, void* out, long ld
     const FastDiv div = make_fastdiv(static_cast<uint32_t>(nv));
 #define TO_ROWS(V, Q)                                                                                              \
   launch_k(to_rows_kernel<T, V, Q>, grid, dim3(256), 0, st, 1, static_cast<const void*>(src), ldx, sc, x.group, ng, \
-           total, cols, div, o, ld)
+           total, cols, div, o, ld, late)
     const cudaError_t e = q ? TO_ROWS(VQ, true) : TO_ROWS(VV, false);
 #undef TO_ROWS
     if (e != cudaSuccess) return e;
@@ -798,6 +802,7 @@ struct DactArgs {
   long lddy, ldz, lddz;
   long rows, rows_per_strip;
   int cols, group, ng, act;
+  int late;
 };
 
 // A block is 32 lanes of V columns by 8 rows; it walks the rows of its strip and keeps the column sums of
@@ -806,7 +811,8 @@ struct DactArgs {
 // from 8-bit z moves 169 MB in 34 us, 0.74 of the copy rate (16 columns a lane; 70 against 63 us with 8 at twice the rows).
 template <typename T, int V, int ZK>
 __global__ void __launch_bounds__(256, V == 16 ? 2 : 3) dact_kernel(const DactArgs a) {
-  pdl_entry();
+  if (!a.late) pdl_entry();
+  pdl_release();
   constexpr int N = V == 1 ? 6 : V == 16 ? 2 : 3;  // rows in flight
   __shared__ float sums[8][32 * V];
   const int lane = threadIdx.x & 31, rl = threadIdx.x >> 5;
@@ -873,19 +879,20 @@ __global__ void __launch_bounds__(256, V == 16 ? 2 : 3) dact_kernel(const DactAr
       }
     });
   }
-  pdl_release();
-  if (!a.part) return;
+  if (a.part) {
 #pragma unroll
-  for (int k = 0; k < V; ++k) sums[rl][lane * V + k] = acc[k];
-  __syncthreads();
-  for (int i = threadIdx.x; i < 32 * V; i += 256) {
-    const int col = static_cast<int>(blockIdx.x) * 32 * V + i;
-    if (col >= a.cols) continue;
-    float v = 0.f;
+    for (int k = 0; k < V; ++k) sums[rl][lane * V + k] = acc[k];
+    __syncthreads();
+    for (int i = threadIdx.x; i < 32 * V; i += 256) {
+      const int col = static_cast<int>(blockIdx.x) * 32 * V + i;
+      if (col >= a.cols) continue;
+      float v = 0.f;
 #pragma unroll
-    for (int w = 0; w < 8; ++w) v += sums[w][i];
-    a.part[static_cast<long>(blockIdx.y) * a.cols + col] = v;
+      for (int w = 0; w < 8; ++w) v += sums[w][i];
+      a.part[static_cast<long>(blockIdx.y) * a.cols + col] = v;
+    }
   }
+  if (a.late) pdl_entry();
 }
 
 template <typename T, int V>
@@ -909,8 +916,8 @@ cudaError_t dact(const DactArgs& a, int zk, int strips, cudaStream_t st) {
 // ------------------------------------------------------------------ column sums, joins, zeroes
 // 32 columns a block, 8 warps over the partials, then the 8 sums in order.
 __global__ void __launch_bounds__(256) column_sum_kernel(const float* part, int G, int cols, float* out,
-                                                         int accumulate) {
-  pdl_entry();
+                                                         int accumulate, int late) {
+  if (!late) pdl_entry();
   pdl_release();
   __shared__ float s[8][33];
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
@@ -929,6 +936,7 @@ __global__ void __launch_bounds__(256) column_sum_kernel(const float* part, int 
     for (int i = 0; i < 8; ++i) sum += s[i][lane];
     out[c] = o + sum;
   }
+  if (late) pdl_entry();
 }
 
 template <typename T, int V>
@@ -960,28 +968,31 @@ __global__ void __launch_bounds__(256) split_join_kernel(const float* part, int 
 }
 
 template <typename T>
-__global__ void __launch_bounds__(256) zero_rows_kernel(long rows, int cols, T* out, long ld) {
-  pdl_entry();
+__global__ void __launch_bounds__(256) zero_rows_kernel(long rows, int cols, T* out, long ld, int late) {
+  if (!late) pdl_entry();
   pdl_release();
   const long total = rows * cols;
   for (long j = static_cast<long>(blockIdx.x) * 256 + threadIdx.x; j < total; j += static_cast<long>(gridDim.x) * 256) {
     const long row = j / cols;
     out[row * ld + (j - row * cols)] = from_f<T>(0.f);
   }
+  if (late) pdl_entry();
 }
 
 }  // namespace
 
-cudaError_t launch_to_rows(const conv2d_mat& x, long rows, int cols, int dt, void* out, long ldo, cudaStream_t st) {
-  if (dt == CONV2D_BF16) return to_rows<__nv_bfloat16>(x, rows, cols, out, ldo, st);
-  if (dt == CONV2D_FP16) return to_rows<__half>(x, rows, cols, out, ldo, st);
-  return to_rows<float>(x, rows, cols, out, ldo, st);
+cudaError_t launch_to_rows(const conv2d_mat& x, long rows, int cols, int dt, void* out, long ldo, int late,
+                           cudaStream_t st) {
+  if (dt == CONV2D_BF16) return to_rows<__nv_bfloat16>(x, rows, cols, out, ldo, late, st);
+  if (dt == CONV2D_FP16) return to_rows<__half>(x, rows, cols, out, ldo, late, st);
+  return to_rows<float>(x, rows, cols, out, ldo, late, st);
 }
 
-cudaError_t launch_move_bytes(const void* x, long ldx, long rows, int cols, void* out, long ldo, cudaStream_t st) {
+cudaError_t launch_move_bytes(const void* x, long ldx, long rows, int cols, void* out, long ldo, int late,
+                              cudaStream_t st) {
   const dim3 grid(static_cast<unsigned>(std::min<long>((rows * ((cols + 255) / 256) + 7) / 8, 152L * 64)));
   return launch_k(to_rows_ragged_kernel<uint8_t, false, 1>, grid, dim3(256), 0, st, 1, x, ldx,
-                  static_cast<const uint8_t*>(nullptr), 0, 1, rows, cols, static_cast<uint8_t*>(out), ldo);
+                  static_cast<const uint8_t*>(nullptr), 0, 1, rows, cols, static_cast<uint8_t*>(out), ldo, late);
 }
 
 DactPlan plan_dact(long rows, int cols, int sms) {
@@ -998,8 +1009,9 @@ DactPlan plan_dact(long rows, int cols, int sms) {
 }
 
 cudaError_t launch_dact(const conv2d_mat* z, const conv2d_mat& dy, long rows, int cols, int dt, int act, void* dz,
-                        long lddz, float* part, const DactPlan& pl, cudaStream_t st) {
+                        long lddz, float* part, const DactPlan& pl, int late, cudaStream_t st) {
   DactArgs a = {};
+  a.late = late;
   a.dy = dy.data;
   a.lddy = dy.ld ? dy.ld : cols;
   int zk = 0;
@@ -1021,8 +1033,9 @@ cudaError_t launch_dact(const conv2d_mat* z, const conv2d_mat& dy, long rows, in
   return dt == CONV2D_BF16 ? dact<__nv_bfloat16>(a, zk, pl.strips, st) : dact<__half>(a, zk, pl.strips, st);
 }
 
-cudaError_t launch_column_sum(const float* part, int G, int cols, float* out, int accumulate, cudaStream_t st) {
-  return launch_k(column_sum_kernel, dim3((cols + 31) / 32), dim3(256), 0, st, 1, part, G, cols, out, accumulate);
+cudaError_t launch_column_sum(const float* part, int G, int cols, float* out, int accumulate, int late,
+                              cudaStream_t st) {
+  return launch_k(column_sum_kernel, dim3((cols + 31) / 32), dim3(256), 0, st, 1, part, G, cols, out, accumulate, late);
 }
 
 template <typename T>
@@ -1043,13 +1056,13 @@ cudaError_t launch_split_join(const float* part, int splits, long rows, int cols
 }
 
 template <typename T>
-static cudaError_t zero_rows(long rows, int cols, T* out, long ld, cudaStream_t st) {
-  return launch_k(zero_rows_kernel<T>, dim3(stream_grid(rows * cols)), dim3(256), 0, st, 1, rows, cols, out, ld);
+static cudaError_t zero_rows(long rows, int cols, T* out, long ld, int late, cudaStream_t st) {
+  return launch_k(zero_rows_kernel<T>, dim3(stream_grid(rows * cols)), dim3(256), 0, st, 1, rows, cols, out, ld, late);
 }
-cudaError_t launch_zero_rows(long rows, int cols, int type, void* out, long ld, cudaStream_t st) {
-  if (type == CONV2D_FP32) return zero_rows(rows, cols, static_cast<float*>(out), ld, st);
-  if (type == CONV2D_BF16) return zero_rows(rows, cols, static_cast<__nv_bfloat16*>(out), ld, st);
-  return zero_rows(rows, cols, static_cast<__half*>(out), ld, st);
+cudaError_t launch_zero_rows(long rows, int cols, int type, void* out, long ld, int late, cudaStream_t st) {
+  if (type == CONV2D_FP32) return zero_rows(rows, cols, static_cast<float*>(out), ld, late, st);
+  if (type == CONV2D_BF16) return zero_rows(rows, cols, static_cast<__nv_bfloat16*>(out), ld, late, st);
+  return zero_rows(rows, cols, static_cast<__half*>(out), ld, late, st);
 }
 
 }  // namespace c2d
@@ -1139,9 +1152,9 @@ int conv2d_q8_encode(int64_t rows, int32_t cols, const conv2d_mat* x, const conv
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   auto run = [&]() -> cudaError_t {
     cudaError_t e = cudaSuccess;
-    if (x->type == CONV2D_BF16 && q8_flat<__nv_bfloat16, true>(a.x, a.ldx, a.q, a.ldq, a.qs, a.group, rows, cols, st, &e))
+    if (x->type == CONV2D_BF16 && q8_flat<__nv_bfloat16, true>(a.x, a.ldx, a.q, a.ldq, a.qs, a.group, rows, cols, 0, st, &e))
       return e;
-    if (x->type == CONV2D_FP16 && q8_flat<__half, true>(a.x, a.ldx, a.q, a.ldq, a.qs, a.group, rows, cols, st, &e))
+    if (x->type == CONV2D_FP16 && q8_flat<__half, true>(a.x, a.ldx, a.q, a.ldq, a.qs, a.group, rows, cols, 0, st, &e))
       return e;
     return rows_fwd_any<false>(a, x->type, st);
   };
@@ -1158,7 +1171,7 @@ int conv2d_q8_decode(int64_t rows, int32_t cols, const conv2d_mat* q8, const con
   DevInfo* dev = nullptr;
   if ((rc = device_info(&dev))) return rc;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  LAUNCH("q8_decode", st, launch_to_rows(*q8, rows, cols, x->type, x->data, x->ld, st));
+  LAUNCH("q8_decode", st, launch_to_rows(*q8, rows, cols, x->type, x->data, x->ld, 0, st));
   return CONV2D_OK;
 }
 
@@ -1224,7 +1237,7 @@ int conv2d_rms_norm_bwd(int64_t rows, int32_t cols, const conv2d_mat* h, const f
   if (rows == 0) {
     if (!dgamma || accumulate) return CONV2D_OK;
     if ((rc = device_info(&dev))) return rc;
-    LAUNCH("zero", st, launch_zero_rows(1, cols, CONV2D_FP32, dgamma, cols, st));
+    LAUNCH("zero", st, launch_zero_rows(1, cols, CONV2D_FP32, dgamma, cols, 0, st));
     return CONV2D_OK;
   }
   if (!inv_rms || !aligned16(inv_rms)) return CONV2D_ERR_INVALID_ARG;
@@ -1260,7 +1273,7 @@ int conv2d_rms_norm_bwd(int64_t rows, int32_t cols, const conv2d_mat* h, const f
     return norm_bwd_vec<float>(a, grid, st);
   };
   LAUNCH("rms_norm_bwd", st, run());
-  if (dgamma) LAUNCH("column_sum", st, launch_column_sum(a.part, grid, cols, dgamma, accumulate, st));
+  if (dgamma) LAUNCH("column_sum", st, launch_column_sum(a.part, grid, cols, dgamma, accumulate, 0, st));
   return CONV2D_OK;
 }
 
