@@ -464,8 +464,10 @@ int conv2d_dense_bwd(const conv2d_dense_desc* d, const conv2d_mat* x, const conv
   float* part = dbias ? reinterpret_cast<float*>(base + pl.dpart) : nullptr;
   if (pl.dz_own || dbias) {
     void* dz = pl.dz_own ? base + pl.dz : nullptr;
+    // beside the copies only where it does not fill the GPU by itself: a block that has finished waits for them
+    const bool beside = started && d->M * d->N < (int64_t(1) << 22);
     LAUNCH("dense_dact", st,
-           launch_dact(act ? pre_act : nullptr, *dy, d->M, d->N, d->dtype, d->act, dz, pl.lddz, part, pl.dact, started,
+           launch_dact(act ? pre_act : nullptr, *dy, d->M, d->N, d->dtype, d->act, dz, pl.lddz, part, pl.dact, beside,
                        st));
     if (dz) {
       odz.data = dz;

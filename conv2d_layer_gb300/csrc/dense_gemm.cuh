@@ -209,10 +209,30 @@ __device__ __forceinline__ uint4 lds128(uint32_t a) {
 }
 __device__ __forceinline__ void sts128(uint32_t a, const uint4& v) { st_shared_v4(a, v.x, v.y, v.z, v.w); }
 
-// The buffer's rows (nr of them) x nc elements of type E to memory at g (row length ld), element by element along
-// the rows: for rows that start off 16-byte boundaries, and for accumulating (added in fp32 to what is there).
+// The buffer's rows (nr of them) x nc elements of type E to memory at g (row length ld): for rows that start off
+// 16-byte boundaries, in 4-byte words where they start on those, and for accumulating (added in fp32 to what is
+// there), else element by element.
 template <typename E, int RB>
 __device__ __forceinline__ void rows_out(uint32_t buf, E* g, long ld, int nr, int nc, bool accumulate, int lane) {
+  constexpr int P = 4 / static_cast<int>(sizeof(E));  // elements a word
+  if (P > 1 && !accumulate && ld % P == 0) {
+    constexpr int WR = RB / 4;  // words a row
+    const int word = lane % WR;
+#pragma unroll 4
+    for (int r = lane / WR; r < nr; r += 32 / WR) {
+      uint32_t w;
+      asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w) : "r"(buf + row_piece<RB>(r, word / 4) + (word % 4) * 4u) : "memory");
+      E* o = g + r * ld + word * P;
+      if ((word + 1) * P <= nc) {
+        *reinterpret_cast<uint32_t*>(o) = w;
+      } else {
+#pragma unroll
+        for (int k = 0; k < P; ++k)
+          if (word * P + k < nc) o[k] = reinterpret_cast<const E*>(&w)[k];
+      }
+    }
+    return;
+  }
   constexpr int PE = 16 / static_cast<int>(sizeof(E));  // elements a piece
   constexpr int W = RB / static_cast<int>(sizeof(E));   // elements a row: 32 or 16
   const int col = lane % W;
@@ -271,8 +291,8 @@ __device__ __forceinline__ uint4 pack8(const float* v) {
   return w;
 }
 
-// The residual of 32 rows x 32 columns on its way to the buffer, in 16 registers: all of it as 16-byte pieces where
-// the rows allow it, else the elements of rows `from` .. from + 15, one column a lane.
+// The residual of 32 rows x 32 columns on its way to the buffer, in 16 registers: as 16-byte pieces where the rows
+// allow it, as pairs where they start on those, else the elements of rows `from` .. from + 15, one column a lane.
 template <typename T>
 __device__ __forceinline__ void residual_load(const DenseGemmParams& p, uint32_t (&w)[16], long m0, int n, int nr, int nc,
                                               int from, int lane) {
@@ -282,8 +302,15 @@ __device__ __forceinline__ void residual_load(const DenseGemmParams& p, uint32_t
     for (int i = 0; i < 4; ++i)
       if (i * 8 + (lane >> 2) < nr)
         *reinterpret_cast<uint4*>(w + 4 * i) = *reinterpret_cast<const uint4*>(r + i * 8 * p.ldr);
+  } else if (p.ldr % 2 == 0) {
+    const int c = (lane & 15) * 2;
+    const uint16_t* r = static_cast<const uint16_t*>(p.res) + (m0 + (lane >> 4)) * p.ldr + n + c;
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if (i * 2 + (lane >> 4) < nr && c < nc)
+        w[i] = c + 1 < nc ? *reinterpret_cast<const uint32_t*>(r + i * 2 * p.ldr) : r[i * 2 * p.ldr];
   } else if (lane < nc) {
-    const uint16_t* r = reinterpret_cast<const uint16_t*>(p.res) + (m0 + from) * p.ldr + n + lane;
+    const uint16_t* r = static_cast<const uint16_t*>(p.res) + (m0 + from) * p.ldr + n + lane;
 #pragma unroll
     for (int i = 0; i < 16; ++i)
       if (from + i < nr) w[i] = r[i * p.ldr];
@@ -295,7 +322,14 @@ __device__ __forceinline__ void residual_store(const DenseGemmParams& p, uint32_
   if (p.vec_res && nc == 32) {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      st_shared_v4(buf + row_piece<64>(i * 8 + (lane >> 2), lane & 3), w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+      st_shared_v4(buf + row_piece<64>(i * 8 + (lane >> 2), lane & 3), w[4 * i], w[4 * i + 1], w[4 * i + 2],
+                   w[4 * i + 3]);
+    return;
+  }
+  if (p.ldr % 2 == 0) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      st_shared_b32(buf + row_piece<64>(i * 2 + (lane >> 4), (lane & 15) >> 2) + (lane & 3) * 4u, w[i]);
     return;
   }
 #pragma unroll

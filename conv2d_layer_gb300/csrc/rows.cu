@@ -540,10 +540,10 @@ cudaError_t norm_bwd(const NormBwdArgs& a, int grid, cudaStream_t st) {
 // ------------------------------------------------------------------ 8 bits, 16-bit types in whole groups
 // Encode (ENC) or decode of rows of whole 32-column groups: two threads a group, 16 values each, two groups of a
 // thread in flight (200704 x 256 there and back: 46.5 us, 0.99 of the copy rate; 59 us with 16-byte accesses). total = rows * cols / 16 < 2^31; x rows on 32-byte, q rows on 16-byte boundaries.
-template <typename T, bool ENC>
+template <typename T, bool ENC, bool LATE>
 __global__ void __launch_bounds__(256) q8_flat_kernel(T* x, long ldx, uint8_t* q, long ldq, uint8_t* scale,
-                                                      uint32_t total, FastDiv div_nv, int late) {
-  if (!late) pdl_entry();
+                                                      uint32_t total, FastDiv div_nv) {
+  if (!LATE) pdl_entry();
   pdl_release();
   constexpr int N = 2;
   const uint32_t step = gridDim.x * 256u;
@@ -613,7 +613,7 @@ __global__ void __launch_bounds__(256) q8_flat_kernel(T* x, long ldx, uint8_t* q
       }
     }
   }
-  if (late) pdl_entry();
+  if (LATE) pdl_entry();
 }
 int stream_grid(long items) { return static_cast<int>(std::max<long>(1, std::min<long>((items + 255) / 256, 152L * 64))); }
 
@@ -625,20 +625,27 @@ bool q8_flat(const void* x, long ldx, const void* q, long ldq, uint8_t* scale, i
       reinterpret_cast<uintptr_t>(x) % 32 != 0 || rows * (cols / 16) > 0x7fffffffL)
     return false;
   const long total = rows * (cols / 16);
-  *e = launch_k(q8_flat_kernel<T, ENC>, dim3(stream_grid((total + 1) / 2)), dim3(256), 0, st, 1,
-                static_cast<T*>(const_cast<void*>(x)), ldx, static_cast<uint8_t*>(const_cast<void*>(q)), ldq, scale,
-                static_cast<uint32_t>(total), make_fastdiv(static_cast<uint32_t>(cols / 16)), late);
+  auto go = [&](auto kernel) {
+    return launch_k(kernel, dim3(stream_grid((total + 1) / 2)), dim3(256), 0, st, 1,
+                    static_cast<T*>(const_cast<void*>(x)), ldx, static_cast<uint8_t*>(const_cast<void*>(q)), ldq, scale,
+                    static_cast<uint32_t>(total), make_fastdiv(static_cast<uint32_t>(cols / 16)));
+  };
+  if constexpr (!ENC)
+    if (late) {
+      *e = go(q8_flat_kernel<T, ENC, true>);
+      return true;
+    }
+  *e = go(q8_flat_kernel<T, ENC, false>);
   return true;
 }
 
 // ------------------------------------------------------------------ decode / move
 // V elements a thread and step of a [rows][cols] matrix, dense steps of the grid (E4M3 source: V bytes and
 // their scale, two output vectors). rows * ceil(cols / V) below 2^31 (see to_rows).
-template <typename T, int V, bool Q>
+template <typename T, int V, bool Q, bool LATE>
 __global__ void __launch_bounds__(256) to_rows_kernel(const void* x, long ldx, const uint8_t* scale, int group, int ng,
-                                                      uint32_t total, int cols, FastDiv div_nv, T* out, long ldo,
-                                                      int late) {
-  if (!late) pdl_entry();
+                                                      uint32_t total, int cols, FastDiv div_nv, T* out, long ldo) {
+  if (!LATE) pdl_entry();
   pdl_release();
   constexpr int VO = V * sizeof(T) > 16 ? 16 / static_cast<int>(sizeof(T)) : V;  // elements a store
   constexpr int N = 2;                                                          // steps in flight
@@ -682,15 +689,15 @@ __global__ void __launch_bounds__(256) to_rows_kernel(const void* x, long ldx, c
       for (int k = 0; k < V; k += VO) st_vec<T, VO>(o + k, *reinterpret_cast<const T(*)[VO]>(&e[i][k]));
     }
   }
-  if (late) pdl_entry();
+  if (LATE) pdl_entry();
 }
 
 // The same for rows that do not start on vector boundaries, or end within a vector: a warp takes 32 N W neighbouring
 // elements of a row, W neighbours a lane (W = 2: output rows start on boundaries of two elements).
-template <typename T, bool Q, int W>
+template <typename T, bool Q, int W, bool LATE>
 __global__ void __launch_bounds__(256) to_rows_ragged_kernel(const void* x, long ldx, const uint8_t* scale, int group,
-                                                             int ng, long rows, int cols, T* out, long ldo, int late) {
-  if (!late) pdl_entry();
+                                                             int ng, long rows, int cols, T* out, long ldo) {
+  if (!LATE) pdl_entry();
   pdl_release();
   constexpr int N = 8 / W;
   const int lane = threadIdx.x & 31;
@@ -737,7 +744,7 @@ __global__ void __launch_bounds__(256) to_rows_ragged_kernel(const void* x, long
       }
     }
   }
-  if (late) pdl_entry();
+  if (LATE) pdl_entry();
 }
 
 // Rows that start on boundaries of a vector of V elements of es bytes (the base at least on 16 bytes by contract).
@@ -763,8 +770,11 @@ cudaError_t to_rows(const conv2d_mat& x, long rows, int cols, void* out, long ld
     T* o = static_cast<T*>(out);
     const void* src = x.data;
     const uint8_t* sc = x.scale;
-#define RAGGED(Q, W)                                                                                                     \
-  return launch_k(to_rows_ragged_kernel<T, Q, W>, grid, dim3(256), 0, st, 1, src, ldx, sc, x.group, ng, rows, cols, o, ld, late)
+#define RAGGED(Q, W)                                                                                                  \
+  return late ? launch_k(to_rows_ragged_kernel<T, Q, W, true>, grid, dim3(256), 0, st, 1, src, ldx, sc, x.group, ng,  \
+                         rows, cols, o, ld)                                                                           \
+              : launch_k(to_rows_ragged_kernel<T, Q, W, false>, grid, dim3(256), 0, st, 1, src, ldx, sc, x.group, ng, \
+                         rows, cols, o, ld)
     if (sizeof(T) == 2 && ld % 2 == 0) {
       if (q) RAGGED(true, 2);
       RAGGED(false, 2);
@@ -783,9 +793,11 @@ cudaError_t to_rows(const conv2d_mat& x, long rows, int cols, void* out, long ld
     const uint8_t* sc = q ? x.scale + r0 * ng : nullptr;
     T* o = static_cast<T*>(out) + r0 * ld;
     const FastDiv div = make_fastdiv(static_cast<uint32_t>(nv));
-#define TO_ROWS(V, Q)                                                                                              \
-  launch_k(to_rows_kernel<T, V, Q>, grid, dim3(256), 0, st, 1, static_cast<const void*>(src), ldx, sc, x.group, ng, \
-           total, cols, div, o, ld, late)
+#define TO_ROWS(V, Q)                                                                                                  \
+  (late ? launch_k(to_rows_kernel<T, V, Q, true>, grid, dim3(256), 0, st, 1, static_cast<const void*>(src), ldx, sc,  \
+                   x.group, ng, total, cols, div, o, ld)                                                               \
+        : launch_k(to_rows_kernel<T, V, Q, false>, grid, dim3(256), 0, st, 1, static_cast<const void*>(src), ldx, sc, \
+                   x.group, ng, total, cols, div, o, ld))
     const cudaError_t e = q ? TO_ROWS(VQ, true) : TO_ROWS(VV, false);
 #undef TO_ROWS
     if (e != cudaSuccess) return e;
@@ -802,17 +814,15 @@ struct DactArgs {
   long lddy, ldz, lddz;
   long rows, rows_per_strip;
   int cols, group, ng, act;
-  int late;
 };
 
 // A block is 32 lanes of V columns by 8 rows; it walks the rows of its strip and keeps the column sums of
 // the unrounded dz in registers, joined over the 8 row lanes at the end. ZK: 0 no activation, 1 z in T,
 // 2 z as E4M3. Memory bounds it, with two special-function operations a value close behind (gelu): 4096 x 8192
 // from 8-bit z moves 169 MB in 34 us, 0.74 of the copy rate (16 columns a lane; 70 against 63 us with 8 at twice the rows).
-template <typename T, int V, int ZK>
+template <typename T, int V, int ZK, bool LATE>
 __global__ void __launch_bounds__(256, V == 16 ? 2 : 3) dact_kernel(const DactArgs a) {
-  if (!a.late) pdl_entry();
-  pdl_release();
+  if (!LATE) pdl_entry();
   constexpr int N = V == 1 ? 6 : V == 16 ? 2 : 3;  // rows in flight
   __shared__ float sums[8][32 * V];
   const int lane = threadIdx.x & 31, rl = threadIdx.x >> 5;
@@ -879,6 +889,7 @@ __global__ void __launch_bounds__(256, V == 16 ? 2 : 3) dact_kernel(const DactAr
       }
     });
   }
+  pdl_release();
   if (a.part) {
 #pragma unroll
     for (int k = 0; k < V; ++k) sums[rl][lane * V + k] = acc[k];
@@ -892,25 +903,29 @@ __global__ void __launch_bounds__(256, V == 16 ? 2 : 3) dact_kernel(const DactAr
       a.part[static_cast<long>(blockIdx.y) * a.cols + col] = v;
     }
   }
-  if (a.late) pdl_entry();
+  if (LATE) pdl_entry();
 }
 
-template <typename T, int V>
+template <typename T, int V, bool LATE>
 cudaError_t dact_v(const DactArgs& a, int zk, int strips, cudaStream_t st) {
   const dim3 grid(static_cast<unsigned>((a.cols + 32 * V - 1) / (32 * V)), static_cast<unsigned>(strips));
-  if (zk == 0) return launch_k(dact_kernel<T, V, 0>, grid, dim3(256), 0, st, 1, a);
-  if (zk == 1) return launch_k(dact_kernel<T, V, 1>, grid, dim3(256), 0, st, 1, a);
-  return launch_k(dact_kernel<T, V, 2>, grid, dim3(256), 0, st, 1, a);
+  if (zk == 0) return launch_k(dact_kernel<T, V, 0, LATE>, grid, dim3(256), 0, st, 1, a);
+  if (zk == 1) return launch_k(dact_kernel<T, V, 1, LATE>, grid, dim3(256), 0, st, 1, a);
+  return launch_k(dact_kernel<T, V, 2, LATE>, grid, dim3(256), 0, st, 1, a);
+}
+template <typename T, int V>
+cudaError_t dact_late(const DactArgs& a, int zk, int strips, int late, cudaStream_t st) {
+  return late ? dact_v<T, V, true>(a, zk, strips, st) : dact_v<T, V, false>(a, zk, strips, st);
 }
 template <typename T>
-cudaError_t dact(const DactArgs& a, int zk, int strips, cudaStream_t st) {
+cudaError_t dact(const DactArgs& a, int zk, int strips, int late, cudaStream_t st) {
   auto ok = [&](int V) {
     return a.cols % V == 0 && vec_ok(a.dy, a.lddy, sizeof(T), V) && (!a.dz || vec_ok(a.dz, a.lddz, sizeof(T), V)) &&
            (zk == 0 || vec_ok(a.z, a.ldz, zk == 2 ? 1 : sizeof(T), V));
   };
   // 16 columns a lane only where a warp's 512 are there
-  if (a.cols >= 512 && ok(16)) return dact_v<T, 16>(a, zk, strips, st);
-  return ok(8) ? dact_v<T, 8>(a, zk, strips, st) : dact_v<T, 1>(a, zk, strips, st);
+  if (a.cols >= 512 && ok(16)) return dact_late<T, 16>(a, zk, strips, late, st);
+  return ok(8) ? dact_late<T, 8>(a, zk, strips, late, st) : dact_late<T, 1>(a, zk, strips, late, st);
 }
 
 // ------------------------------------------------------------------ column sums, joins, zeroes
@@ -991,8 +1006,11 @@ cudaError_t launch_to_rows(const conv2d_mat& x, long rows, int cols, int dt, voi
 cudaError_t launch_move_bytes(const void* x, long ldx, long rows, int cols, void* out, long ldo, int late,
                               cudaStream_t st) {
   const dim3 grid(static_cast<unsigned>(std::min<long>((rows * ((cols + 255) / 256) + 7) / 8, 152L * 64)));
-  return launch_k(to_rows_ragged_kernel<uint8_t, false, 1>, grid, dim3(256), 0, st, 1, x, ldx,
-                  static_cast<const uint8_t*>(nullptr), 0, 1, rows, cols, static_cast<uint8_t*>(out), ldo, late);
+  auto go = [&](auto kernel) {
+    return launch_k(kernel, grid, dim3(256), 0, st, 1, x, ldx, static_cast<const uint8_t*>(nullptr), 0, 1, rows, cols,
+                    static_cast<uint8_t*>(out), ldo);
+  };
+  return late ? go(to_rows_ragged_kernel<uint8_t, false, 1, true>) : go(to_rows_ragged_kernel<uint8_t, false, 1, false>);
 }
 
 DactPlan plan_dact(long rows, int cols, int sms) {
@@ -1011,7 +1029,6 @@ DactPlan plan_dact(long rows, int cols, int sms) {
 cudaError_t launch_dact(const conv2d_mat* z, const conv2d_mat& dy, long rows, int cols, int dt, int act, void* dz,
                         long lddz, float* part, const DactPlan& pl, int late, cudaStream_t st) {
   DactArgs a = {};
-  a.late = late;
   a.dy = dy.data;
   a.lddy = dy.ld ? dy.ld : cols;
   int zk = 0;
@@ -1030,7 +1047,7 @@ cudaError_t launch_dact(const conv2d_mat* z, const conv2d_mat& dy, long rows, in
   a.rows_per_strip = pl.rows_per_strip;
   a.cols = cols;
   a.act = act;
-  return dt == CONV2D_BF16 ? dact<__nv_bfloat16>(a, zk, pl.strips, st) : dact<__half>(a, zk, pl.strips, st);
+  return dt == CONV2D_BF16 ? dact<__nv_bfloat16>(a, zk, pl.strips, late, st) : dact<__half>(a, zk, pl.strips, late, st);
 }
 
 cudaError_t launch_column_sum(const float* part, int G, int cols, float* out, int accumulate, int late,
