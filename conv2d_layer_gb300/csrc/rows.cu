@@ -693,19 +693,21 @@ __global__ void __launch_bounds__(256) to_rows_kernel(const void* x, long ldx, c
 }
 
 // The same for rows that do not start on vector boundaries, or end within a vector: a warp takes 32 N W neighbouring
-// elements of a row, W neighbours a lane (W = 2: output rows start on boundaries of two elements).
+// elements of a row, W neighbours a lane (output rows start on boundaries of W elements; E4M3 with W = 4: the four
+// bytes come out of the two aligned words that hold them).
+__host__ __device__ constexpr int ragged_chunk(int W) { return W == 4 ? 512 : 256; }
 template <typename T, bool Q, int W, bool LATE>
 __global__ void __launch_bounds__(256) to_rows_ragged_kernel(const void* x, long ldx, const uint8_t* scale, int group,
-                                                             int ng, long rows, int cols, T* out, long ldo) {
+                                                             int ng, uint32_t total, FastDiv div_chunks, int cols, T* out,
+                                                             long ldo) {
   if (!LATE) pdl_entry();
   pdl_release();
-  constexpr int N = 8 / W;
+  constexpr int N = ragged_chunk(W) / (32 * W);
   const int lane = threadIdx.x & 31;
-  const int chunks = (cols + 255) / 256;
-  const long total = rows * chunks;
-  for (long j = static_cast<long>(blockIdx.x) * 8 + (threadIdx.x >> 5); j < total; j += static_cast<long>(gridDim.x) * 8) {
-    const long row = chunks == 1 ? j : j / chunks;
-    const int c0 = static_cast<int>(j - row * chunks) * 256 + lane * W;
+  for (uint32_t j = blockIdx.x * 8u + (threadIdx.x >> 5); j < total; j += gridDim.x * 8u) {
+    const uint32_t r = fdiv(j, div_chunks);
+    const long row = r;
+    const int c0 = static_cast<int>(j - r * div_chunks.d) * ragged_chunk(W) + lane * W;
     T e[N][W];
     uint32_t raw[N], sb[N];
 #pragma unroll
@@ -714,9 +716,17 @@ __global__ void __launch_bounds__(256) to_rows_ragged_kernel(const void* x, long
       if (c >= cols) continue;
       if constexpr (Q) {
         const uint8_t* p = static_cast<const uint8_t*>(x) + row * ldx + c;
-        raw[k] = p[0];
-        if (W == 2 && c + 1 < cols) raw[k] |= static_cast<uint32_t>(p[1]) << 8;
-        sb[k] = scale[row * ng + (group ? c / kQ8Group : 0)];  // c is even: both neighbours are of one group
+        if (W == 4 && c + 8 <= cols) {  // both words lie within the row's end (and after the 16-byte aligned base)
+          const uint32_t off = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p) & 3u);
+          const uint32_t* w = reinterpret_cast<const uint32_t*>(p - off);
+          raw[k] = __funnelshift_r(w[0], w[1], off * 8u);
+        } else {
+          raw[k] = p[0];
+#pragma unroll
+          for (int i = 1; i < W; ++i)
+            if (c + i < cols) raw[k] |= static_cast<uint32_t>(p[i]) << (8 * i);
+        }
+        sb[k] = scale[row * ng + (group ? c / kQ8Group : 0)];  // W divides c and a group: one scale for the neighbours
       } else {
 #pragma unroll
         for (int w = 0; w < W; ++w)
@@ -728,15 +738,19 @@ __global__ void __launch_bounds__(256) to_rows_ragged_kernel(const void* x, long
       const int c = c0 + 32 * W * k;
       if (c >= cols) continue;
       if constexpr (Q) {
-        const float2 f = q8_unpack2(raw[k]);
         const float sc = q8_scale(sb[k]);
-        e[k][0] = from_q8<T>(f.x * sc);
-        if constexpr (W == 2) e[k][1] = from_q8<T>(f.y * sc);
+#pragma unroll
+        for (int i = 0; i < W; i += 2) {
+          const float2 f = q8_unpack2(raw[k] >> (8 * i));
+          e[k][i] = from_q8<T>(f.x * sc);
+          if constexpr (W > 1) e[k][i + 1] = from_q8<T>(f.y * sc);
+        }
       }
       T* o = out + row * ldo + c;
-      if constexpr (W == 2 && sizeof(T) == 2) {
-        if (c + 1 < cols) *reinterpret_cast<uint32_t*>(o) = *reinterpret_cast<const uint32_t*>(e[k]);
-        else o[0] = e[k][0];
+      if (W * sizeof(T) == 8 && c + W <= cols) {
+        *reinterpret_cast<uint2*>(o) = *reinterpret_cast<const uint2*>(e[k]);
+      } else if (W * sizeof(T) == 4 && c + W <= cols) {
+        *reinterpret_cast<uint32_t*>(o) = *reinterpret_cast<const uint32_t*>(e[k]);
       } else {
 #pragma unroll
         for (int w = 0; w < W; ++w)
@@ -750,6 +764,29 @@ __global__ void __launch_bounds__(256) to_rows_ragged_kernel(const void* x, long
 // Rows that start on boundaries of a vector of V elements of es bytes (the base at least on 16 bytes by contract).
 bool vec_ok(const void* p, long ld, int es, int V) {
   return reinterpret_cast<uintptr_t>(p) % (V * es > 16 ? 32 : 16) == 0 && ld % V == 0;
+}
+
+template <typename T, bool Q, int W>
+cudaError_t to_rows_ragged(const void* x, long ldx, const uint8_t* scale, int group, int ng, long rows, int cols,
+                           void* out, long ldo, int late, cudaStream_t st) {
+  const int chunks = (cols + ragged_chunk(W) - 1) / ragged_chunk(W);
+  const long slab = std::max<long>(1, 0x7fffffffL / chunks);  // rows a launch indexes in 31 bits
+  const FastDiv div = make_fastdiv(static_cast<uint32_t>(chunks));
+  for (long r0 = 0; r0 < rows; r0 += slab) {
+    const long n = std::min(slab, rows - r0);
+    const uint32_t total = static_cast<uint32_t>(n * chunks);
+    const dim3 grid(static_cast<unsigned>(std::min<long>((n * chunks + 7) / 8, 152L * 64)));
+    const void* src = static_cast<const char*>(x) + r0 * ldx * (Q ? 1 : static_cast<long>(sizeof(T)));
+    const uint8_t* sc = Q ? scale + r0 * ng : nullptr;
+    T* o = static_cast<T*>(out) + r0 * ldo;
+    const cudaError_t e =
+        late ? launch_k(to_rows_ragged_kernel<T, Q, W, true>, grid, dim3(256), 0, st, 1, src, ldx, sc, group, ng, total,
+                        div, cols, o, ldo)
+             : launch_k(to_rows_ragged_kernel<T, Q, W, false>, grid, dim3(256), 0, st, 1, src, ldx, sc, group, ng, total,
+                        div, cols, o, ldo);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
 }
 
 template <typename T>
@@ -766,22 +803,14 @@ cudaError_t to_rows(const conv2d_mat& x, long rows, int cols, void* out, long ld
   const int V = q ? VQ : VV;
   const bool vec = cols % V == 0 && vec_ok(out, ld, sizeof(T), VV) && vec_ok(x.data, ldx, q ? 1 : sizeof(T), V);
   if (!vec) {
-    const dim3 grid(static_cast<unsigned>(std::min<long>((rows * ((cols + 255) / 256) + 7) / 8, 152L * 64)));
-    T* o = static_cast<T*>(out);
-    const void* src = x.data;
-    const uint8_t* sc = x.scale;
-#define RAGGED(Q, W)                                                                                                  \
-  return late ? launch_k(to_rows_ragged_kernel<T, Q, W, true>, grid, dim3(256), 0, st, 1, src, ldx, sc, x.group, ng,  \
-                         rows, cols, o, ld)                                                                           \
-              : launch_k(to_rows_ragged_kernel<T, Q, W, false>, grid, dim3(256), 0, st, 1, src, ldx, sc, x.group, ng, \
-                         rows, cols, o, ld)
-    if (sizeof(T) == 2 && ld % 2 == 0) {
-      if (q) RAGGED(true, 2);
-      RAGGED(false, 2);
+    if constexpr (sizeof(T) == 2) {
+      if (q && ld % 4 == 0) return to_rows_ragged<T, true, 4>(x.data, ldx, x.scale, x.group, ng, rows, cols, out, ld, late, st);
+      if (ld % 2 == 0)
+        return q ? to_rows_ragged<T, true, 2>(x.data, ldx, x.scale, x.group, ng, rows, cols, out, ld, late, st)
+                 : to_rows_ragged<T, false, 2>(x.data, ldx, nullptr, 0, 1, rows, cols, out, ld, late, st);
     }
-    if (q) RAGGED(true, 1);
-    RAGGED(false, 1);
-#undef RAGGED
+    return q ? to_rows_ragged<T, true, 1>(x.data, ldx, x.scale, x.group, ng, rows, cols, out, ld, late, st)
+             : to_rows_ragged<T, false, 1>(x.data, ldx, nullptr, 0, 1, rows, cols, out, ld, late, st);
   }
   const int nv = cols / V;
   const long slab = std::max<long>(1, 0x7fffffffL / nv);  // rows a launch indexes in 31 bits
@@ -1005,12 +1034,7 @@ cudaError_t launch_to_rows(const conv2d_mat& x, long rows, int cols, int dt, voi
 
 cudaError_t launch_move_bytes(const void* x, long ldx, long rows, int cols, void* out, long ldo, int late,
                               cudaStream_t st) {
-  const dim3 grid(static_cast<unsigned>(std::min<long>((rows * ((cols + 255) / 256) + 7) / 8, 152L * 64)));
-  auto go = [&](auto kernel) {
-    return launch_k(kernel, grid, dim3(256), 0, st, 1, x, ldx, static_cast<const uint8_t*>(nullptr), 0, 1, rows, cols,
-                    static_cast<uint8_t*>(out), ldo);
-  };
-  return late ? go(to_rows_ragged_kernel<uint8_t, false, 1, true>) : go(to_rows_ragged_kernel<uint8_t, false, 1, false>);
+  return to_rows_ragged<uint8_t, false, 1>(x, ldx, nullptr, 0, 1, rows, cols, out, ldo, late, st);
 }
 
 DactPlan plan_dact(long rows, int cols, int sms) {
