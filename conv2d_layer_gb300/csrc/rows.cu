@@ -323,6 +323,11 @@ cudaError_t rows_fwd(const NormArgs& a, cudaStream_t st) {
     if (nv <= 1024) ROWS_FWD(256, 4, 1);
     if (nv <= 2048) ROWS_FWD(512, 4, 1);
   }
+  if constexpr (V == 1) {  // single elements take few registers
+    if (nv <= 4096) ROWS_FWD(512, 8, 1);
+    if (nv <= 8192) ROWS_FWD(1024, 8, 1);
+    if (nv <= 16384) ROWS_FWD(1024, 16, 1);
+  }
   ROWS_FWD(1024, 0, 1);
 #undef ROWS_FWD
 }
@@ -532,7 +537,12 @@ cudaError_t norm_bwd(const NormBwdArgs& a, int grid, cudaStream_t st) {
     if (nv <= 1024) NORM_BWD(512, 2, true);
   if (nv <= 1024) NORM_BWD(512, 2, false);
   if constexpr (V < 16)
-    if (nv <= 2048) NORM_BWD(512, 4, false);
+    if (nv <= 2048) NORM_BWD(512, 4, V == 1);
+  if constexpr (V == 1) {
+    if (nv <= 4096) NORM_BWD(1024, 4, true);
+    if (nv <= 8192) NORM_BWD(1024, 8, true);
+    if (nv <= 16384) NORM_BWD(1024, 16, false);
+  }
   NORM_BWD(1024, 0, false);
 #undef NORM_BWD
 }
@@ -693,8 +703,8 @@ __global__ void __launch_bounds__(256) to_rows_kernel(const void* x, long ldx, c
 }
 
 // The same for rows that do not start on vector boundaries, or end within a vector: a warp takes 32 N W neighbouring
-// elements of a row, W neighbours a lane (output rows start on boundaries of W elements; E4M3 with W = 4: the four
-// bytes come out of the two aligned words that hold them).
+// elements of a row, W neighbours a lane (output rows start on boundaries of W elements). With W = 4 the neighbours
+// come out of the aligned words that hold them: two for E4M3, three for 16-bit elements.
 __host__ __device__ constexpr int ragged_chunk(int W) { return W == 4 ? 512 : 256; }
 template <typename T, bool Q, int W, bool LATE>
 __global__ void __launch_bounds__(256) to_rows_ragged_kernel(const void* x, long ldx, const uint8_t* scale, int group,
@@ -708,7 +718,7 @@ __global__ void __launch_bounds__(256) to_rows_ragged_kernel(const void* x, long
     const uint32_t r = fdiv(j, div_chunks);
     const long row = r;
     const int c0 = static_cast<int>(j - r * div_chunks.d) * ragged_chunk(W) + lane * W;
-    T e[N][W];
+    alignas(8) T e[N][W];
     uint32_t raw[N], sb[N];
 #pragma unroll
     for (int k = 0; k < N; ++k) {
@@ -728,9 +738,21 @@ __global__ void __launch_bounds__(256) to_rows_ragged_kernel(const void* x, long
         }
         sb[k] = scale[row * ng + (group ? c / kQ8Group : 0)];  // W divides c and a group: one scale for the neighbours
       } else {
+        const T* p = static_cast<const T*>(x) + row * ldx + c;
+        if constexpr (W == 4) {
+          if (c + 6 <= cols) {  // the words lie within the row's end
+            const uint32_t off = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p) & 2u);
+            const uint32_t* w = reinterpret_cast<const uint32_t*>(reinterpret_cast<const char*>(p) - off);
+            uint32_t* o = reinterpret_cast<uint32_t*>(e[k]);
+            const uint32_t a = w[0], b = w[1], d = off ? w[2] : 0u;
+            o[0] = __funnelshift_r(a, b, off * 8u);
+            o[1] = __funnelshift_r(b, d, off * 8u);
+            continue;
+          }
+        }
 #pragma unroll
         for (int w = 0; w < W; ++w)
-          if (w == 0 || c + w < cols) e[k][w] = static_cast<const T*>(x)[row * ldx + c + w];
+          if (w == 0 || c + w < cols) e[k][w] = p[w];
       }
     }
 #pragma unroll
@@ -804,7 +826,9 @@ cudaError_t to_rows(const conv2d_mat& x, long rows, int cols, void* out, long ld
   const bool vec = cols % V == 0 && vec_ok(out, ld, sizeof(T), VV) && vec_ok(x.data, ldx, q ? 1 : sizeof(T), V);
   if (!vec) {
     if constexpr (sizeof(T) == 2) {
-      if (q && ld % 4 == 0) return to_rows_ragged<T, true, 4>(x.data, ldx, x.scale, x.group, ng, rows, cols, out, ld, late, st);
+      if (ld % 4 == 0)
+        return q ? to_rows_ragged<T, true, 4>(x.data, ldx, x.scale, x.group, ng, rows, cols, out, ld, late, st)
+                 : to_rows_ragged<T, false, 4>(x.data, ldx, nullptr, 0, 1, rows, cols, out, ld, late, st);
       if (ld % 2 == 0)
         return q ? to_rows_ragged<T, true, 2>(x.data, ldx, x.scale, x.group, ng, rows, cols, out, ld, late, st)
                  : to_rows_ragged<T, false, 2>(x.data, ldx, nullptr, 0, 1, rows, cols, out, ld, late, st);
