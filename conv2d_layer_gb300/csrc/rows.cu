@@ -982,18 +982,18 @@ cudaError_t dact(const DactArgs& a, int zk, int strips, int late, cudaStream_t s
 }
 
 // ------------------------------------------------------------------ column sums, joins, zeroes
-// 32 columns a block, 8 warps over the partials, then the 8 sums in order.
-__global__ void __launch_bounds__(256) column_sum_kernel(const float* part, int G, int cols, float* out,
+// 32 columns a block, 16 warps over the partials, then their sums in order.
+__global__ void __launch_bounds__(512) column_sum_kernel(const float* part, int G, int cols, float* out,
                                                          int accumulate, int late) {
   if (!late) pdl_entry();
   pdl_release();
-  __shared__ float s[8][33];
+  __shared__ float s[16][33];
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int c = static_cast<int>(blockIdx.x) * 32 + lane;
   float v = 0.f;
   if (c < cols) {
-#pragma unroll 8
-    for (int g = w; g < G; g += 8) v += part[static_cast<long>(g) * cols + c];
+#pragma unroll 10
+    for (int g = w; g < G; g += 16) v += part[static_cast<long>(g) * cols + c];
   }
   s[w][lane] = v;
   __syncthreads();
@@ -1001,7 +1001,7 @@ __global__ void __launch_bounds__(256) column_sum_kernel(const float* part, int 
     float o = accumulate ? out[c] : 0.f;
     float sum = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) sum += s[i][lane];
+    for (int i = 0; i < 16; ++i) sum += s[i][lane];
     out[c] = o + sum;
   }
   if (late) pdl_entry();
@@ -1100,7 +1100,7 @@ cudaError_t launch_dact(const conv2d_mat* z, const conv2d_mat& dy, long rows, in
 
 cudaError_t launch_column_sum(const float* part, int G, int cols, float* out, int accumulate, int late,
                               cudaStream_t st) {
-  return launch_k(column_sum_kernel, dim3((cols + 31) / 32), dim3(256), 0, st, 1, part, G, cols, out, accumulate, late);
+  return launch_k(column_sum_kernel, dim3((cols + 31) / 32), dim3(512), 0, st, 1, part, G, cols, out, accumulate, late);
 }
 
 template <typename T>
