@@ -46,10 +46,10 @@ struct GemmPlan {
 // skewed products (16 to 8,192 in each direction; the choice was within 10 % of the fastest in all of them). A
 // k-block takes a CTA what its MMAs or its operands' way from L2 take, whichever is longer, which comes to a line
 // in BN; a unit has a fixed cost (launch, first operands, epilogue); clusters pay for joining their sums. Units
-// run in waves over the SMs; the pair kernel hides its epilogue under the next unit's loop. Weight gradients may
-// be split over k, with fp32 partials in the workspace; max_kb: bound on one accumulator's k-blocks (0: none).
-GemmPlan plan_gemm(int mode, long m, long n, int kb, int max_kb, int sms) {
-  const bool r_mn = dense_r_mn(mode), c_mn = dense_c_mn(mode), can_split = mode == kDenseDw;
+// run in waves over the SMs; the pair kernel hides its epilogue under the next unit's loop. can_split: the product
+// may be split over k, with fp32 partials in the workspace; max_kb: bound on one accumulator's k-blocks (0: none).
+GemmPlan plan_gemm(int mode, long m, long n, int kb, int max_kb, int sms, bool can_split = false) {
+  const bool r_mn = dense_r_mn(mode), c_mn = dense_c_mn(mode);
   GemmPlan best = {};
   double best_t = 1e300;
   auto consider = [&](bool pair, int BN, int cl, int splits) {
@@ -311,6 +311,7 @@ void plan_fwd(const conv2d_dense_desc& d, const conv2d_mat* x, const conv2d_mat*
 struct BwdPlan {
   bool dz_own;  // dz is formed in the workspace (else it is dy)
   long lddz;
+  long pass_rows;  // rows of a pass of dW (M: one pass)
   size_t dz, x, w, dpart, spart, joinx, joinw, total;
   DactPlan dact;
   GemmPlan gx, gw;
@@ -332,8 +333,18 @@ void plan_bwd(const conv2d_dense_desc& d, const conv2d_mat* x, const conv2d_mat*
   }
   if (dw) {
     pl->x = plan_copy(c, x, d.M, d.K, false);
-    pl->gw = plan_gemm(kDenseDw, d.N, d.K, static_cast<int>(ceil_div(d.M, 64)),
-                       dw->type == CONV2D_FP32 ? kFp32SplitKb : 0, sms);
+    // An fp32 dW over many rows is summed in pieces of kFp32SplitKb k-blocks: side by side, joined afterwards, or one
+    // after the other, added to dW. The second saves the partials' traffic but idles at each piece's last wave. It
+    // is taken for up to 4 pieces whose waves are four fifths full (8192 x 2048 x 8192: 176 us against 188; 16384 x
+    // 4096 x 4096: 344 to 358 against 353 to 355; 8 pieces, 32768 x 2048 x 8192: 722 against 674; waves 59 % full, 9000 x 2304 x
+    // 2560: 97 against 86), and where the partials would take more than 2 GB.
+    const int kb = static_cast<int>(ceil_div(d.M, 64)), bound = dw->type == CONV2D_FP32 ? kFp32SplitKb : 0;
+    const long pairs = sms / 2, tiles = ceil_div(d.N, 256) * ceil_div(d.K, 256), waves = ceil_div(tiles, pairs);
+    const long pieces = bound ? ceil_div(kb, bound) : 1;
+    const bool passes = pieces > 1 && ((pieces <= 4 && tiles * 5 >= waves * pairs * 4) ||
+                                       pieces * d.N * d.K * 4 > (2L << 30));
+    pl->pass_rows = passes ? bound * 64L : d.M;
+    pl->gw = passes ? plan_gemm(kDenseDw, d.N, d.K, bound, 0, sms) : plan_gemm(kDenseDw, d.N, d.K, kb, bound, sms, true);
     pl->joinw = plan_join(c, pl->gw);
     if (pl->gw.splits > 1) pl->spart = c.take(static_cast<size_t>(pl->gw.splits) * d.N * d.K * 4);
   }
@@ -482,14 +493,26 @@ int conv2d_dense_bwd(const conv2d_dense_desc* d, const conv2d_mat* x, const conv
   }
   const bool joined = dw && pl.gw.splits > 1;
   if (dw) {
-    DenseGemmParams p = {};
-    p.out = joined ? static_cast<void*>(base + pl.spart) : dw->data;
-    p.ldo = joined ? d->K : ld_of(dw, d->K);
-    p.out_f32 = joined || dw->type == CONV2D_FP32;
-    p.accumulate = !joined && d->accumulate;
-    p.split_stride = static_cast<long>(d->N) * d->K;
-    if ((rc = run_gemm(p, pl.gw, odz, ox, d->dtype, kDenseDw, at(ws, pl.joinw), dx != nullptr, "dense_dw", dev, st)))
-      return rc;
+    for (long r0 = 0; r0 < d->M; r0 += pl.pass_rows) {
+      DenseGemmParams p = {};
+      p.out = joined ? static_cast<void*>(base + pl.spart) : dw->data;
+      p.ldo = joined ? d->K : ld_of(dw, d->K);
+      p.out_f32 = joined || dw->type == CONV2D_FP32;
+      p.accumulate = !joined && (d->accumulate || r0 > 0);
+      p.split_stride = static_cast<long>(d->N) * d->K;
+      Operand oz = odz, oa = ox;
+      oz.rows = oa.rows = std::min(pl.pass_rows, d->M - r0);
+      oz.data = static_cast<const char*>(odz.data) + r0 * odz.ld * 2;  // row lengths are multiples of 16 bytes
+      oa.data = static_cast<const char*>(ox.data) + r0 * ox.ld * 2;
+      GemmPlan g = pl.gw;
+      if (oz.rows < pl.pass_rows) {  // the last pass: fewer k-blocks, whole units
+        g.kb_total = g.kb_per_split = static_cast<int>(ceil_div(oz.rows, 64));
+        g.full = g.l_tiles * g.c_tiles;
+        g.parts = 1;
+      }
+      if ((rc = run_gemm(p, g, oz, oa, d->dtype, kDenseDw, at(ws, pl.joinw), r0 == 0 && dx, "dense_dw", dev, st)))
+        return rc;
+    }
   }
   if (dbias)
     LAUNCH("column_sum", st,

@@ -109,6 +109,13 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap* m, uint32_t src,
                "r"(src), "r"(c0), "r"(c1), "r"(c2)
                : "memory");
 }
+// The same, added to what is there (fp32; sums below 2^-126 come out as zero).
+__device__ __forceinline__ void tma_add_3d(const CUtensorMap* m, uint32_t src, int c0, int c1, int c2) {
+  asm volatile("cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+                   reinterpret_cast<uint64_t>(m)),
+               "r"(src), "r"(c0), "r"(c1), "r"(c2)
+               : "memory");
+}
 __device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
 // Wait until this thread's bulk stores have read their shared memory / have completed.
 __device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
@@ -264,7 +271,8 @@ __device__ __forceinline__ void buffer_take(int lane) {
   if (lane == 0) bulk_wait_read();
   __syncwarp();
 }
-// Stores the written buffer: by TMA (whole rows, clipped at the matrix's ends), or element by element.
+// Stores the written buffer: by TMA (whole rows, clipped at the matrix's ends; fp32 sums are added there), or word
+// by word.
 template <typename E, int RB>
 __device__ __forceinline__ void buffer_store(uint32_t buf, bool tma, const CUtensorMap* map, int n, long m0, int split,
                                              E* g, long ld, int nr, int nc, bool accumulate, int lane) {
@@ -272,7 +280,8 @@ __device__ __forceinline__ void buffer_store(uint32_t buf, bool tma, const CUten
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) {
-      tma_store_3d(map, buf, n, static_cast<int>(m0), split);
+      if (sizeof(E) == 4 && accumulate) tma_add_3d(map, buf, n, static_cast<int>(m0), split);
+      else tma_store_3d(map, buf, n, static_cast<int>(m0), split);
       bulk_commit();
     }
   } else {
@@ -459,7 +468,7 @@ __device__ __forceinline__ void pair_epilogue(const DenseGemmParams& p, uint32_t
     tmem_ld32(taddr, a);
     tmem_ld_wait32(a);
     taken(a);
-    const bool tma = p.tma_out && !p.accumulate;
+    const bool tma = p.tma_out && (p.out_f32 || !p.accumulate);
     if (p.out_f32) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {

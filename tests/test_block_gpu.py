@@ -361,6 +361,52 @@ def test_dense_bwd_cut_units(M, K, N, dtype, act, q8, grad, pad):
     test_dense_bwd(M, K, N, dtype, act, q8, grad, pad)
 
 
+@pytest.mark.parametrize("M,K,N", [(9000, 2560, 3840), (4160, 2048, 8192)])
+def test_dense_bwd_fp32_passes(M, K, N):
+    """An fp32 dW that fills the GPU by itself is summed in passes of 4,096 rows; the workspace holds no partials."""
+    x, dy = normal(1, M, K, dtype=BF), normal(2, M, N, dtype=BF)
+    _, dw, _ = ops.dense_bwd(x, None, dy, need_dx=False, need_dbias=False)
+    ref = dy.double().t() @ x.double()
+    # at most 256 truncated additions (16 products each) in a pass, and three passes
+    steps = (256 + 20 + 3) * STEP * (dy.double().abs().t() @ x.double().abs())
+    close(dw, ref, rounded(ref, FP, steps), "dw")
+    d = abi.DenseDesc(M, K, N, 0, abi.BF16, 0)
+    m = abi.Mat(1 << 20, 0, abi.BF16, 0, None)
+    f = abi.Mat(1 << 20, 0, abi.FP32, 0, None)
+    assert abi.conv2d_dense_bwd_workspace_size(d, m, m, None, m, None, f, None) < 2 * N * K * 4
+    again, db = dw.clone(), torch.zeros(N, device="cuda")
+    ops.dense_bwd(x, None, dy, need_dx=False, dw=again, dbias=db)
+    close(again, 2 * dw.double(), 8 * U[FP] * ref.abs() + steps * 2.0 ** -3, "dw twice")
+
+
+@pytest.mark.parametrize("M,K,N", [(50, 136, 72), (600, 520, 1000)])
+def test_dense_strided_outputs(M, K, N):
+    """Every output into rows of a longer matrix: the same bits, nothing beside them."""
+    x, w, dy = normal(1, M, K, dtype=BF), normal(2, N, K, std=K ** -0.5, dtype=BF), normal(3, M, N, dtype=BF)
+
+    def wide(rows, cols, dtype, pad):
+        t = torch.full((rows, cols + pad), 7.0, device="cuda").to(dtype)
+        return t, t[:, :cols]
+
+    for pad in (8, 16, 3):
+        y0, z0 = ops.dense_fwd(x, w, None, "gelu", save="q8")
+        g0 = ops.dense_bwd(x, w, dy, z0, "gelu", grad_dtype=BF)
+        Y, y = wide(M, N, BF, pad)
+        Q = torch.full((M, N + pad), 1, device="cuda", dtype=torch.uint8)
+        z = ops.Q8(Q.view(torch.float8_e4m3fn)[:, :N], torch.empty_like(z0.scale), 32)
+        ops.dense_fwd(x, w, None, "gelu", save="q8", y=y, pre_act=z)
+        assert torch.equal(y, y0) and torch.equal(z.scale, z0.scale)
+        assert torch.equal(Q[:, :N], z0.q.view(torch.uint8)) and bool((Q[:, N:] == 1).all())
+        X, dx = wide(M, K, BF, pad)
+        W, dw = wide(N, K, BF, pad)
+        dw.zero_()
+        db = torch.zeros(N, device="cuda")
+        ops.dense_bwd(x, w, dy, z, "gelu", dx=dx, dw=dw, dbias=db)
+        assert torch.equal(dx, g0[0]) and torch.equal(dw, g0[1]) and torch.equal(db, g0[2])
+        for t, cols in ((Y, N), (X, K), (W, K)):
+            assert bool((t[:, cols:] == 7).all())
+
+
 TINY_OF = {BF: 2.0 ** -133, HF: 2.0 ** -24, FP: 2.0 ** -149}
 
 
