@@ -89,7 +89,9 @@ GemmPlan plan_gemm(int mode, long m, long n, int kb, int max_kb, int sms, bool c
       const double fit = cl == 8 ? sms * 15 / 19 : cl == 4 ? sms * 18 / 19 : sms;
       t = std::ceil(units * cl / fit) * (6300 + 38.0 * BN + loop * ((r_mn ? 480 : 300) + 0.45 * BN) + (cl > 1 ? 3500 + 22.0 * BN : 0));
     }
-    if (g.splits > 1) t += 4000 + static_cast<double>(m) * n * 4 * 2 * g.splits / 7000;
+    // the join is a launch of its own and waits for everything beside it (1777 x 1000 x 333 with dx: 19.7 us in 4
+    // splits, 17.3 in one; 4096 x 512 x 512: 22.1 in 8, 18.7 as a cluster of 4)
+    if (g.splits > 1) t += 8000 + static_cast<double>(m) * n * 4 * 2 * g.splits / 7000;
     if (t < best_t) {
       best_t = t;
       best = g;
@@ -336,8 +338,8 @@ void plan_bwd(const conv2d_dense_desc& d, const conv2d_mat* x, const conv2d_mat*
     // An fp32 dW over many rows is summed in pieces of kFp32SplitKb k-blocks: side by side, joined afterwards, or one
     // after the other, added to dW. The second saves the partials' traffic but idles at each piece's last wave. It
     // is taken for up to 4 pieces whose waves are four fifths full (8192 x 2048 x 8192: 176 us against 188; 16384 x
-    // 4096 x 4096: 344 to 358 against 353 to 355; 8 pieces, 32768 x 2048 x 8192: 722 against 674; waves 59 % full, 9000 x 2304 x
-    // 2560: 97 against 86), and where the partials would take more than 2 GB.
+    // 4096 x 4096: 344 to 358 against 353 to 355; 8 pieces, 32768 x 2048 x 8192: 722 against 674; waves 59 % full,
+    // 9000 x 2304 x 2560: 97 against 86), and where the partials would take more than 2 GB.
     const int kb = static_cast<int>(ceil_div(d.M, 64)), bound = dw->type == CONV2D_FP32 ? kFp32SplitKb : 0;
     const long pairs = sms / 2, tiles = ceil_div(d.N, 256) * ceil_div(d.K, 256), waves = ceil_div(tiles, pairs);
     const long pieces = bound ? ceil_div(kb, bound) : 1;
