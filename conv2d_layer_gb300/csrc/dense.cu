@@ -32,6 +32,9 @@ long ld_of(const conv2d_mat* m, int cols) { return m->ld ? m->ld : cols; }
 // tensor core's fp32 sums are not rounded to nearest and lose about 2^-25 of the sum at every MMA, so 4,096
 // rows (256 MMAs) stay below 1e-5; longer products are split and the splits joined with ordinary fp32 adds.
 constexpr int kFp32SplitKb = 64;
+// k-blocks whose sum is off by no more than 1e-6 (4,096 rows: 4e-6), taken where it costs little: everywhere, 8192 x
+// 2048 x 8192 would take 276 us instead of 176.
+constexpr int kFp32ShortKb = 16;
 
 struct GemmPlan {
   bool pair;
@@ -90,8 +93,10 @@ GemmPlan plan_gemm(int mode, long m, long n, int kb, int max_kb, int sms, bool c
       t = std::ceil(units * cl / fit) * (6300 + 38.0 * BN + loop * ((r_mn ? 480 : 300) + 0.45 * BN) + (cl > 1 ? 3500 + 22.0 * BN : 0));
     }
     // the join is a launch of its own and waits for everything beside it (1777 x 1000 x 333 with dx: 19.7 us in 4
-    // splits, 17.3 in one; 4096 x 512 x 512: 22.1 in 8, 18.7 as a cluster of 4)
-    if (g.splits > 1) t += 8000 + static_cast<double>(m) * n * 4 * 2 * g.splits / 7000;
+    // splits, 17.3 in one; 4096 x 512 x 512: 22.1 in 8, 18.7 as a cluster of 4); it reads a value's partials in turn
+    if (g.splits > 1) t += 8000 + 100.0 * g.splits + static_cast<double>(m) * n * 4 * 2 * g.splits / 7000;
+    // up to a tenth of the time goes into short fp32 sums
+    if (max_kb > 0 && ceil_div(g.kb_per_split, cl) > kFp32ShortKb) t *= 1.1;
     if (t < best_t) {
       best_t = t;
       best = g;
