@@ -466,8 +466,8 @@ __device__ __forceinline__ uint32_t fdiv(uint32_t n, const FastDiv& f) {
 // (The residual block's kernels do release theirs, once a block's main work is behind it: pdl_release. Of the kernels
 // of one of its calls, those that read nothing of the kernel before them run beside it, "late": they start when that
 // kernel releases them, which is after its own wait, so that everything before the call has completed, and wait for
-// its completion at their end instead of at their entry, so that whatever waits for them has waited for both. Where it matters the choice is made at compile
-// time: as a run-time test it cost a streaming kernel of 16 us two.)
+// its completion at their end instead of at their entry, so that whatever waits for them has waited for both. Where
+// it matters the choice is made at compile time: as a run-time test it cost a streaming kernel of 16 us two.)
 __device__ __forceinline__ void pdl_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void pdl_entry() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 

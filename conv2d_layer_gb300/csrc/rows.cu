@@ -71,7 +71,7 @@ struct NormArgs {
   float eps;
 };
 
-// RMS norm forward (NORM) or 8-bit encode (!NORM): TPR threads a row, blocks of max(TPR, 256) threads. Rows are
+// RMS norm forward (NORM) or 8-bit encode (!NORM): TPR threads a row, a block of them or (TPR = 32) eight warps. Rows are
 // held in registers between their sum of squares and their output, U vectors a thread, so memory is passed once;
 // U = 0 is the form for rows longer than that, which reads the row again for each phase (from L2, mostly). NR
 // rows are in flight at once where a row is a vector or two a thread (one row of 512 bytes a warp left a
@@ -79,10 +79,9 @@ struct NormArgs {
 // neighbouring lanes and its maximum is found by shuffles. Bound by memory: 8192 x 4096 bf16 with the residual, y
 // and its 8-bit form moves 303 MB in 47 us, 0.95 of the measured copy rate.
 template <typename T, int V, int TPR, int U, int NR, bool NORM>
-__global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) rows_fwd_kernel(const NormArgs a) {
+__global__ void __launch_bounds__(TPR == 32 ? 256 : TPR) rows_fwd_kernel(const NormArgs a) {
   pdl_entry();
-  constexpr int RPB = TPR < 256 ? 256 / TPR : 1;  // groups of NR rows per block
-  static_assert(RPB == 1 || TPR == 32, "rows that share a block are one warp each");
+  constexpr int RPB = TPR == 32 ? 8 : 1;  // groups of NR rows per block
   static_assert(U > 0 || NR == 1, "one row at a time where it is read again");
   constexpr int UC = U > 0 ? U : 1;
   __shared__ float red[32];
@@ -305,7 +304,7 @@ cudaError_t rows_fwd(const NormArgs& a, cudaStream_t st) {
   const int nv = (a.cols + V - 1) / V;
 #define ROWS_FWD(TPR, U, NR)                                                                                        \
   do {                                                                                                              \
-    constexpr int nt = TPR < 256 ? 256 : TPR, rpb = nt / TPR * (NR);                                               \
+    constexpr int nt = (TPR) == 32 ? 256 : (TPR), rpb = nt / (TPR) * (NR);                                         \
     return launch_k(rows_fwd_kernel<T, V, TPR, U, NR, NORM>, dim3(static_cast<unsigned>((a.rows + rpb - 1) / rpb)), \
                     dim3(nt), 0, st, 1, a);                                                                         \
   } while (0)
@@ -315,7 +314,18 @@ cudaError_t rows_fwd(const NormArgs& a, cudaStream_t st) {
   if (nv <= 64) ROWS_FWD(32, 2, (V == 16 ? 1 : V == 1 ? 4 : 2));
   if constexpr (V < 16)
     if (nv <= 128) ROWS_FWD(32, 4, (V == 1 ? 4 : 1));
+  // no more threads than a row has vectors, two each: 16384 x 2048 bf16 51 us with 256 threads, 42 with 64; 1536 columns
+  // 46 and 32; 4096 x 5120 33 and 29
+  if constexpr (V > 1) {
+    if constexpr (V == 16)
+      if (nv <= 128) ROWS_FWD(64, 2, 1);
+    if (nv <= 192) ROWS_FWD(96, 2, 1);
+  }
   if (nv <= 256) ROWS_FWD(256, 1, 1);
+  if constexpr (V > 1) {
+    if (nv <= 320) ROWS_FWD(160, 2, 1);
+    if (nv <= 384) ROWS_FWD(192, 2, 1);
+  }
   if (nv <= 512) ROWS_FWD(256, 2, 1);
   if constexpr (V == 16) {
     if (nv <= 1024) ROWS_FWD(512, 2, 1);
@@ -343,6 +353,12 @@ struct NormBwdArgs {
   int cols;
 };
 
+// Blocks that an SM holds and is given, by the threads of a row (32: blocks of 256): about 512 threads of up to 128
+// registers. A second wave of larger blocks only adds partial sums (8192 x 8192 bf16: 100 us, 91 without).
+constexpr int norm_bwd_resident(int tpr) {
+  return tpr > 256 ? 1 : tpr == 64 ? 8 : tpr == 128 ? 4 : tpr == 192 ? 3 : 2;
+}
+
 // Blocks walk the rows (row = block, block + grid, ...), TPR threads a row, and keep the sums of dgamma for their
 // columns in registers. AHEAD: gamma too, and the vectors of the next row are in flight while this one is reduced;
 // without it (rows whose values take the registers) gamma and dh are read where they are needed. U = 0: rows
@@ -350,9 +366,9 @@ struct NormBwdArgs {
 // Bound by memory: 8192 x 4096 bf16 with dh moves 268 MB in 46 us, 0.85 of the copy rate (64 us with one block of
 // 136 registers a thread an SM, before the registers were held to two).
 template <typename T, int V, int TPR, int U, bool AHEAD>
-__global__ void __launch_bounds__(TPR < 256 ? 256 : TPR, TPR <= 256 ? 2 : 1) norm_bwd_kernel(const NormBwdArgs a) {
+__global__ void __launch_bounds__(TPR == 32 ? 256 : TPR, norm_bwd_resident(TPR)) norm_bwd_kernel(const NormBwdArgs a) {
   pdl_entry();
-  constexpr int RPB = TPR < 256 ? 256 / TPR : 1;
+  constexpr int RPB = TPR == 32 ? 8 : 1;
   constexpr int UC = U > 0 ? U : 1;
   extern __shared__ float sums[];  // RPB > 1 with dgamma: [RPB][cols]
   __shared__ float red[32];
@@ -514,31 +530,47 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR, TPR <= 256 ? 2 : 1) nor
   }
 }
 
-// Blocks of the backward walk: two of 256 threads an SM fit their registers; fewer where the rows are few.
-int norm_bwd_grid(long rows, int sms) { return static_cast<int>(std::max<long>(1, std::min<long>(rows, 2L * sms))); }
+// The most blocks that the backward of rows of this length is launched with (norm_bwd's choices below).
+long norm_bwd_blocks(int64_t rows, int cols, int sms) {
+  return std::min<long>(rows, static_cast<long>(sms) * (cols <= 64 * 16 ? 8 : cols <= 128 * 16 ? 4 : cols <= 192 * 16 ? 3 : 2));
+}
 
+// grid: blocks launched, one row of partial sums each.
 template <typename T, int V>
-cudaError_t norm_bwd(const NormBwdArgs& a, int grid, cudaStream_t st) {
+cudaError_t norm_bwd(const NormBwdArgs& a, int sms, int* grid, cudaStream_t st) {
   const int nv = (a.cols + V - 1) / V;
-#define NORM_BWD(TPR, U, AHEAD)                                                                  \
-  do {                                                                                           \
-    constexpr int nt = TPR < 256 ? 256 : TPR;                                                    \
-    const size_t smem = nt > TPR && a.part ? static_cast<size_t>(nt / TPR) * a.cols * 4 : 0;     \
-    return launch_k(norm_bwd_kernel<T, V, TPR, U, AHEAD>, dim3(grid), dim3(nt), smem, st, 1, a); \
+#define NORM_BWD(TPR, U, AHEAD)                                                                   \
+  do {                                                                                            \
+    constexpr int nt = (TPR) == 32 ? 256 : (TPR);                                                 \
+    const size_t smem = nt > (TPR) && a.part ? static_cast<size_t>(nt / (TPR)) * a.cols * 4 : 0;  \
+    *grid = static_cast<int>(std::min<long>(a.rows, static_cast<long>(sms) * norm_bwd_resident(TPR))); \
+    return launch_k(norm_bwd_kernel<T, V, TPR, U, AHEAD>, dim3(*grid), dim3(nt), smem, st, 1, a); \
   } while (0)
+  // As many threads as the row has vectors (of two a thread where a vector is 16 bytes), so that an SM's threads all
+  // have loads in flight: 32768 x 1024 bf16 91 us with 256 threads, 50 with 64; 16384 x 1000 48 and 28.
   if (nv <= 32) NORM_BWD(32, 1, true);
-  if constexpr (V < 16)
+  if constexpr (V == 16) {
+    if (nv <= 64) NORM_BWD(64, 1, true);
+    if (nv <= 128) NORM_BWD(128, 1, true);
+    if (nv <= 256) NORM_BWD(256, 1, true);
+    if (nv <= 320) NORM_BWD(320, 1, true);
+    if (nv <= 512) NORM_BWD(512, 1, true);
+    if (nv <= 1024) NORM_BWD(512, 2, false);
+  } else if constexpr (V > 1) {
     if (nv <= 64) NORM_BWD(32, 2, true);
-  if (nv <= 256) NORM_BWD(256, 1, true);
-  if constexpr (V < 16)
+    if (nv <= 128) NORM_BWD(64, 2, true);
+    if (nv <= 256) NORM_BWD(128, 2, true);
+    if (nv <= 384) NORM_BWD(192, 2, true);
     if (nv <= 512) NORM_BWD(256, 2, true);
-  if (nv <= 512) NORM_BWD(512, 1, true);
-  if constexpr (V < 16)
+    if (nv <= 768) NORM_BWD(384, 2, true);
     if (nv <= 1024) NORM_BWD(512, 2, true);
-  if (nv <= 1024) NORM_BWD(512, 2, false);
-  if constexpr (V < 16)
-    if (nv <= 2048) NORM_BWD(512, 4, V == 1);
-  if constexpr (V == 1) {
+    if (nv <= 2048) NORM_BWD(512, 4, false);
+  } else {
+    if (nv <= 64) NORM_BWD(32, 2, true);
+    if (nv <= 256) NORM_BWD(256, 1, true);
+    if (nv <= 512) NORM_BWD(256, 2, true);
+    if (nv <= 1024) NORM_BWD(512, 2, true);
+    if (nv <= 2048) NORM_BWD(512, 4, true);
     if (nv <= 4096) NORM_BWD(1024, 4, true);
     if (nv <= 8192) NORM_BWD(1024, 8, true);
     if (nv <= 16384) NORM_BWD(1024, 16, false);
@@ -549,7 +581,8 @@ cudaError_t norm_bwd(const NormBwdArgs& a, int grid, cudaStream_t st) {
 
 // ------------------------------------------------------------------ 8 bits, 16-bit types in whole groups
 // Encode (ENC) or decode of rows of whole 32-column groups: two threads a group, 16 values each, two groups of a
-// thread in flight (200704 x 256 there and back: 46.5 us, 0.99 of the copy rate; 59 us with 16-byte accesses). total = rows * cols / 16 < 2^31; x rows on 32-byte, q rows on 16-byte boundaries.
+// thread in flight (200704 x 256 there and back: 46.5 us, 0.99 of the copy rate; 59 us with 16-byte accesses).
+// total = rows * cols / 16 < 2^31; x rows on 32-byte, q rows on 16-byte boundaries.
 template <typename T, bool ENC, bool LATE>
 __global__ void __launch_bounds__(256) q8_flat_kernel(T* x, long ldx, uint8_t* q, long ldq, uint8_t* scale,
                                                       uint32_t total, FastDiv div_nv) {
@@ -982,18 +1015,20 @@ cudaError_t dact(const DactArgs& a, int zk, int strips, int late, cudaStream_t s
 }
 
 // ------------------------------------------------------------------ column sums, joins, zeroes
-// 32 columns a block, 16 warps over the partials, then their sums in order.
-__global__ void __launch_bounds__(512) column_sum_kernel(const float* part, int G, int cols, float* out,
+// 32 columns a block, W warps over the partials (32 where there are many: a warp's loads come in rounds), then their
+// sums in order.
+template <int W>
+__global__ void __launch_bounds__(W * 32) column_sum_kernel(const float* part, int G, int cols, float* out,
                                                          int accumulate, int late) {
   if (!late) pdl_entry();
   pdl_release();
-  __shared__ float s[16][33];
+  __shared__ float s[W][33];
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int c = static_cast<int>(blockIdx.x) * 32 + lane;
   float v = 0.f;
   if (c < cols) {
 #pragma unroll 10
-    for (int g = w; g < G; g += 16) v += part[static_cast<long>(g) * cols + c];
+    for (int g = w; g < G; g += W) v += part[static_cast<long>(g) * cols + c];
   }
   s[w][lane] = v;
   __syncthreads();
@@ -1001,7 +1036,7 @@ __global__ void __launch_bounds__(512) column_sum_kernel(const float* part, int 
     float o = accumulate ? out[c] : 0.f;
     float sum = 0.f;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) sum += s[i][lane];
+    for (int i = 0; i < W; ++i) sum += s[i][lane];
     out[c] = o + sum;
   }
   if (late) pdl_entry();
@@ -1100,7 +1135,9 @@ cudaError_t launch_dact(const conv2d_mat* z, const conv2d_mat& dy, long rows, in
 
 cudaError_t launch_column_sum(const float* part, int G, int cols, float* out, int accumulate, int late,
                               cudaStream_t st) {
-  return launch_k(column_sum_kernel, dim3((cols + 31) / 32), dim3(512), 0, st, 1, part, G, cols, out, accumulate, late);
+  const dim3 grid((cols + 31) / 32);
+  if (G > 320) return launch_k(column_sum_kernel<32>, grid, dim3(1024), 0, st, 1, part, G, cols, out, accumulate, late);
+  return launch_k(column_sum_kernel<16>, grid, dim3(512), 0, st, 1, part, G, cols, out, accumulate, late);
 }
 
 template <typename T>
@@ -1168,7 +1205,8 @@ bool rows_fwd_ok(const NormArgs& a, int es, int V) {
 template <typename T, bool NORM>
 cudaError_t rows_fwd_vec(const NormArgs& a, cudaStream_t st) {
   constexpr int es = sizeof(T);
-  if (rows_fwd_ok<NORM>(a, es, 32 / es)) return rows_fwd<T, 32 / es, NORM>(a, st);
+  // at 16 vectors of 32 bytes and fewer half of the lanes would idle (200704 x 256 to 8 bits too: 93 us, now 88)
+  if (a.cols > 16 * 32 / es && rows_fwd_ok<NORM>(a, es, 32 / es)) return rows_fwd<T, 32 / es, NORM>(a, st);
   if (rows_fwd_ok<NORM>(a, es, 16 / es)) return rows_fwd<T, 16 / es, NORM>(a, st);
   return rows_fwd<T, 1, NORM>(a, st);
 }
@@ -1180,16 +1218,16 @@ cudaError_t rows_fwd_any(const NormArgs& a, int type, cudaStream_t st) {
 }
 
 template <typename T>
-cudaError_t norm_bwd_vec(const NormBwdArgs& a, int grid, cudaStream_t st) {
+cudaError_t norm_bwd_vec(const NormBwdArgs& a, int sms, int* grid, cudaStream_t st) {
   constexpr int es = sizeof(T);
   auto ok = [&](int V) {
     return a.cols % V == 0 && vec_ok(a.h, a.ldh, es, V) && vec_ok(a.dy, a.lddy, es, V) &&
            (!a.dx || vec_ok(a.dx, a.lddx, es, V)) && (!a.dh || vec_ok(a.dh, a.lddh, es, V));
   };
   if constexpr (es == 2)  // fp32 rows of 32-byte vectors take more registers than they win
-    if (ok(32 / es)) return norm_bwd<T, 32 / es>(a, grid, st);
-  if (ok(16 / es)) return norm_bwd<T, 16 / es>(a, grid, st);
-  return norm_bwd<T, 1>(a, grid, st);
+    if (a.cols > 16 * 32 / es && ok(32 / es)) return norm_bwd<T, 32 / es>(a, sms, grid, st);
+  if (ok(16 / es)) return norm_bwd<T, 16 / es>(a, sms, grid, st);
+  return norm_bwd<T, 1>(a, sms, grid, st);
 }
 
 }  // namespace
@@ -1288,7 +1326,7 @@ int conv2d_rms_norm_fwd(int64_t rows, int32_t cols, float eps, const conv2d_mat*
 
 size_t conv2d_rms_norm_bwd_workspace_size(int64_t rows, int32_t cols) {
   if (check_rows(rows, cols)) return 0;
-  return std::max<size_t>(256, static_cast<size_t>(norm_bwd_grid(rows, sms_for_sizing())) * cols * 4);
+  return std::max<size_t>(256, static_cast<size_t>(norm_bwd_blocks(rows, cols, sms_for_sizing())) * cols * 4);
 }
 
 int conv2d_rms_norm_bwd(int64_t rows, int32_t cols, const conv2d_mat* h, const float* gamma, const float* inv_rms,
@@ -1331,11 +1369,11 @@ int conv2d_rms_norm_bwd(int64_t rows, int32_t cols, const conv2d_mat* h, const f
   a.part = dgamma ? static_cast<float*>(ws) : nullptr;
   a.rows = rows;
   a.cols = cols;
-  const int grid = norm_bwd_grid(rows, dev->sms);
+  int grid = 0;
   auto run = [&]() -> cudaError_t {
-    if (h->type == CONV2D_BF16) return norm_bwd_vec<__nv_bfloat16>(a, grid, st);
-    if (h->type == CONV2D_FP16) return norm_bwd_vec<__half>(a, grid, st);
-    return norm_bwd_vec<float>(a, grid, st);
+    if (h->type == CONV2D_BF16) return norm_bwd_vec<__nv_bfloat16>(a, dev->sms, &grid, st);
+    if (h->type == CONV2D_FP16) return norm_bwd_vec<__half>(a, dev->sms, &grid, st);
+    return norm_bwd_vec<float>(a, dev->sms, &grid, st);
   };
   LAUNCH("rms_norm_bwd", st, run());
   if (dgamma) LAUNCH("column_sum", st, launch_column_sum(a.part, grid, cols, dgamma, accumulate, 0, st));

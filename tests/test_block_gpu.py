@@ -165,6 +165,20 @@ def test_rms_norm_bwd(rows, cols, dtype, pad, skip):
         assert none is None and (pad or torch.equal(only, dg))
 
 
+# one for each number of threads that a row gets: by length, type and alignment
+LENGTHS = [(37, 528, BF, 0), (37, 768, HF, 0), (900, 1024, BF, 0), (37, 1040, BF, 0), (1300, 2048, HF, 0), (37, 1536, BF, 0),
+           (37, 2576, BF, 0), (400, 5120, BF, 0), (37, 6144, HF, 0), (37, 8208, BF, 0), (37, 1000, BF, 0), (37, 1032, HF, 8),
+           (37, 2056, BF, 0), (37, 2568, BF, 8), (37, 6152, BF, 0), (37, 8200, HF, 0), (37, 516, FP, 0), (400, 1000, FP, 0),
+           (37, 1300, FP, 0), (37, 1536, FP, 0), (37, 2052, FP, 0), (37, 4100, FP, 0)]
+
+
+@pytest.mark.parametrize("rows,cols,dtype,pad", LENGTHS)
+def test_rms_norm_lengths(rows, cols, dtype, pad):
+    for group in (32, 0):
+        test_rms_norm_fwd(rows, cols, dtype, pad, True, group)
+    test_rms_norm_bwd(rows, cols, dtype, pad, True)
+
+
 def test_rms_norm_gradient_matches_differences():
     h, gamma, w = normal(1, 3, 48, dtype=FP).double(), normal(2, 48).double(), normal(3, 3, 48).double()
     _, inv = rms_ref(h, gamma, 1e-6)
