@@ -345,7 +345,7 @@ PyObject* dense_fwd(PyObject* const* a) {
   const conv2d_dense_desc d = {M, small(K, "x"), small(N, "w"), static_cast<int32_t>(PyLong_AsLong(a[3])), type_code(t), 0};
   run(s.dev, "conv2d_dense_fwd", [&](void* st) {
     const size_t n = lib.conv2d_dense_fwd_workspace_size(&d, &x, &w);
-    if (n > 256) ws = make({static_cast<int64_t>(n)}, at::kByte, s.dev);  // 256: nothing to decode or move
+    if (n > 256) ws = make({static_cast<int64_t>(n)}, at::kByte, s.dev);  // 256: nothing is kept in it
     return lib.conv2d_dense_fwd(&d, &x, &w, bias, given(a[4]) ? &mr : nullptr, save ? &mz : nullptr, &my,
                                 ws.defined() ? ws.data_ptr() : nullptr, ws.defined() ? n : 0, st);
   });

@@ -265,6 +265,9 @@ bool both_8bit(const conv2d_mat* x, const conv2d_mat* w) {
 }
 
 // ------------------------------------------------------------------ workspace
+// What a size query answers where nothing is kept in the workspace; ws may then be null. Anything that is kept makes
+// it larger, so a caller can tell the two apart.
+constexpr size_t kNoWorkspace = 256;
 struct Carver {
   size_t total = 0;
   size_t take(size_t bytes) {
@@ -272,6 +275,7 @@ struct Carver {
     total += static_cast<size_t>(round_up(static_cast<long>(bytes), 256));
     return at;
   }
+  size_t size() const { return total ? std::max(total, 2 * kNoWorkspace) : kNoWorkspace; }
 };
 constexpr size_t kNone = ~static_cast<size_t>(0);
 
@@ -312,7 +316,7 @@ void plan_fwd(const conv2d_dense_desc& d, const conv2d_mat* x, const conv2d_mat*
   pl->w = plan_copy(c, w, d.N, d.K, pl->fp8);
   pl->g = plan_gemm(kDenseForward, d.M, d.N, static_cast<int>(ceil_div(d.K, pl->fp8 ? 128 : 64)), 0, sms);
   pl->join = plan_join(c, pl->g);
-  pl->total = std::max<size_t>(c.total, 256);
+  pl->total = c.size();
 }
 
 struct BwdPlan {
@@ -355,7 +359,7 @@ void plan_bwd(const conv2d_dense_desc& d, const conv2d_mat* x, const conv2d_mat*
     pl->joinw = plan_join(c, pl->gw);
     if (pl->gw.splits > 1) pl->spart = c.take(static_cast<size_t>(pl->gw.splits) * d.N * d.K * 4);
   }
-  pl->total = std::max<size_t>(c.total, 256);
+  pl->total = c.size();
 }
 
 int check_bwd_shapes(const conv2d_dense_desc* d, const conv2d_mat* x, const conv2d_mat* w, const conv2d_mat* z,

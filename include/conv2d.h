@@ -277,7 +277,9 @@ typedef struct {
 } conv2d_dense_desc;
 
 /* Bytes of workspace (0 if the arguments are invalid); of the matrices only
- * data's alignment, ld, type and group are looked at. */
+ * data's alignment, ld, type and group are looked at. 256 stands for a call
+ * that keeps nothing in it: conv2d_dense_fwd then takes ws = NULL. A call
+ * that does needs more. */
 size_t conv2d_dense_fwd_workspace_size(const conv2d_dense_desc* desc, const conv2d_mat* x, const conv2d_mat* w);
 size_t conv2d_dense_bwd_workspace_size(const conv2d_dense_desc* desc, const conv2d_mat* x, const conv2d_mat* w,
                                        const conv2d_mat* pre_act, const conv2d_mat* dy, const conv2d_mat* dx,

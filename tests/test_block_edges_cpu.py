@@ -1,0 +1,33 @@
+"""The residual block's calls without a GPU, where a plan or a rule changes: workspace sizes, streams, stale 8-bit
+weights."""
+import pytest
+
+from conv2d_layer_gb300 import abi
+
+P = 1 << 20  # stands for an aligned device pointer: never read, every call below is sized or refused
+
+
+def mat(type=abi.BF16, ld=0):
+    return abi.Mat(P, ld, type, 0, None)
+
+
+def q8(group=32, ld=0):
+    return abi.Mat(P, ld, abi.E4M3, group, P)
+
+
+def dense(M, K, N, act=abi.ACT_IDENTITY, dtype=abi.BF16):
+    return abi.DenseDesc(M, K, N, act, dtype, 0)
+
+
+@pytest.mark.parametrize("d,x,w", [
+    (dense(1, 128, 8), q8(), mat()),                     # one token in groups of 32, decoded
+    (dense(4, 128, 1), mat(), q8()),                     # one output feature, decoded
+    (dense(2, 64, 8), mat(ld=65), mat()),                # two rows, moved to 16-byte boundaries
+    (dense(1, 100, 2), q8(0, ld=112), q8(0)),            # 8-bit operands, one of them moved
+    (dense(1, 1, 1), mat(), mat(ld=8)),
+])
+def test_a_copy_of_any_size_shows_in_the_workspace(d, x, w):
+    """256 says that nothing is kept (no workspace need be handed in), so the smallest copy makes it more."""
+    assert abi.conv2d_dense_fwd_workspace_size(d, x, w) > 256
+    n = abi.conv2d_dense_fwd_workspace_size(d, x, w)
+    assert abi.conv2d_dense_fwd_workspace_size(dense(d.M, 128, d.N), mat(), mat()) == 256 < n
