@@ -204,6 +204,11 @@ int run_gemm(DenseGemmParams& p, const GemmPlan& g, const Operand& r, const Oper
   p.fmt = r.type == CONV2D_BF16 ? 1u : 0u;
   p.m = r_mn ? r.cols : r.rows;
   p.n = static_cast<int>(c_mn ? c.cols : c.rows);
+  if (g.pair && p.accumulate && !p.out_f32) {
+    mode = kDenseDwAdd;
+    p.res = p.out;
+    p.ldr = p.ldo;
+  }
   p.vec_res = p.ldr % 8 == 0;
   if (g.pair) {
     const int zt = p.zq ? static_cast<int>(CONV2D_E4M3) : dt, ot = p.out_f32 ? static_cast<int>(CONV2D_FP32) : dt;

@@ -57,6 +57,9 @@ cudaError_t launch(int dt, int mode, bool fp8, F&& f) {
 
 cudaError_t launch_dense_pair(const DenseGemmParams& p, int dt, int mode, bool fp8, int grid, size_t smem,
                               cudaStream_t st) {
+  if (mode == kDenseDwAdd)
+    return dt == CONV2D_BF16 ? pair<__nv_bfloat16, kDenseDwAdd, false>(p, grid, smem, st)
+                             : pair<__half, kDenseDwAdd, false>(p, grid, smem, st);
   return launch(dt, mode, fp8, [&](auto t, auto m, auto f) {
     return pair<decltype(t), decltype(m)::value, decltype(f)::value>(p, grid, smem, st);
   });

@@ -36,9 +36,11 @@ constexpr int kPairThreads = 64 + 32 * kPairWarps;
 constexpr int kDenseMaxStages = 10;
 constexpr int kPairBuffers = kPairWarps * 2048;  // the pair kernel's epilogue: 32 rows x 64 bytes a warp
 enum : int { kSiteDenseFull = 11, kSiteDenseEmpty = 12, kSiteDenseTFull = 13, kSiteDenseTEmpty = 14, kSiteDenseJoin = 15 };
-// The three products: how the operands lie (R is MN-major for dW, C for dx and dW) and the epilogue.
-enum : int { kDenseForward = 0, kDenseDx = 1, kDenseDw = 2 };
-__host__ __device__ constexpr bool dense_r_mn(int mode) { return mode == kDenseDw; }
+// The three products: how the operands lie (R is MN-major for dW, C for dx and dW) and the epilogue. kDenseDwAdd: dW
+// added in T to what is there, by the pair kernel. A kernel of its own: as a branch of kDenseDw's epilogue it cost
+// the overwriting one a tenth (8192 x 2048 x 8192 bf16: 155 us, 170 with the branch).
+enum : int { kDenseForward = 0, kDenseDx = 1, kDenseDw = 2, kDenseDwAdd = 3 };
+__host__ __device__ constexpr bool dense_r_mn(int mode) { return mode >= kDenseDw; }
 __host__ __device__ constexpr bool dense_c_mn(int mode) { return mode != kDenseForward; }
 
 struct DenseGemmParams {
@@ -67,7 +69,8 @@ struct DenseGemmParams {
   uint8_t *zq, *zs;
   int zg;  // scale bytes a row of zq
   long ldr, ldz;
-  // kDenseDx, kDenseDw: out = acc (+ out): type T, or fp32 when out_f32; split s at out + s * split_stride
+  // kDenseDx, kDenseDw: out = acc (+ out): type T, or fp32 when out_f32; split s at out + s * split_stride.
+  // kDenseDwAdd reads out through res and ldr.
   int out_f32, accumulate;
   long split_stride;
   void* out;
@@ -216,9 +219,9 @@ __device__ __forceinline__ uint4 lds128(uint32_t a) {
 }
 __device__ __forceinline__ void sts128(uint32_t a, const uint4& v) { st_shared_v4(a, v.x, v.y, v.z, v.w); }
 
-// The buffer's rows (nr of them) x nc elements of type E to memory at g (row length ld): for rows that start off
-// 16-byte boundaries, in 4-byte words where they start on those, and for accumulating (added in fp32 to what is
-// there), else element by element.
+// The buffer's rows (nr of them) x nc elements of type E to memory at g (row length ld), for rows that start off
+// 16-byte boundaries: in 4-byte words where they start on those, else element by element; accumulate (fp32): added
+// to what is there.
 template <typename E, int RB>
 __device__ __forceinline__ void rows_out(uint32_t buf, E* g, long ld, int nr, int nc, bool accumulate, int lane) {
   constexpr int P = 4 / static_cast<int>(sizeof(E));  // elements a word
@@ -260,8 +263,8 @@ __device__ __forceinline__ void rows_out(uint32_t buf, E* g, long ld, int nr, in
       e = static_cast<E>(b);
     }
     E* o = g + r * ld + col;
-    if constexpr (sizeof(E) > 1) {
-      if (accumulate) e = from_f<E>(to_f(*o) + to_f(e));
+    if constexpr (sizeof(E) == 4) {
+      if (accumulate) e += *o;
     }
     *o = e;
   }
@@ -350,6 +353,18 @@ __device__ __forceinline__ void residual_store(const DenseGemmParams& p, uint32_
         asm volatile("st.shared.b16 [%0], %1;" ::"r"(buf + row_piece<64>(from + i, lane >> 3) + (lane & 7) * 2),
                      "h"(static_cast<uint16_t>(w[i]))
                      : "memory");
+  }
+}
+
+// Adds this thread's row of the residual in the buffer to its 32 values.
+template <typename T>
+__device__ __forceinline__ void residual_add(uint32_t buf, float* v, int lane) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint4 w = lds128(buf + row_piece<64>(lane, j));
+    const T* e = reinterpret_cast<const T*>(&w);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[8 * j + k] += to_f(e[k]);
   }
 }
 
@@ -452,13 +467,7 @@ __device__ __forceinline__ void pair_epilogue(const DenseGemmParams& p, uint32_t
       residual_store<T>(p, res, buf, m0, n, nr, nc, lane);
       if (n + 128 < end) residual_load<T>(p, res, m0, n + 128, nr, min(end - n - 128, 32), 0, lane);
       __syncwarp();
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const uint4 w = lds128(buf + row_piece<64>(lane, j));
-        const T* e = reinterpret_cast<const T*>(&w);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) v[8 * j + k] += to_f(e[k]);
-      }
+      residual_add<T>(buf, v, lane);
     }
 #pragma unroll
     for (int j = 0; j < 4; ++j) sts128(buf + row_piece<64>(lane, j), pack8<T>(v + 8 * j));
@@ -468,8 +477,20 @@ __device__ __forceinline__ void pair_epilogue(const DenseGemmParams& p, uint32_t
     tmem_ld32(taddr, a);
     tmem_ld_wait32(a);
     taken(a);
-    const bool tma = p.tma_out && (p.out_f32 || !p.accumulate);
-    if (p.out_f32) {
+    if constexpr (MODE == kDenseDwAdd) {
+      // what is there (p.res = p.out) is added to the fp32 sums: the result is rounded to T once
+      buffer_take(lane);
+      residual_load<T>(p, res, m0, n, nr, nc, 0, lane);
+      residual_store<T>(p, res, buf, m0, n, nr, nc, lane);
+      __syncwarp();
+      float v[32];
+#pragma unroll
+      for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(a[e]);
+      residual_add<T>(buf, v, lane);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) sts128(buf + row_piece<64>(lane, j), pack8<T>(v + 8 * j));
+      buffer_store<T, 64>(buf, p.tma_out, &p.tout, n, m0, 0, static_cast<T*>(p.out), p.ldo, nr, nc, false, lane);
+    } else if (p.out_f32) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         if (16 * h >= nc) break;  // uniform
@@ -478,7 +499,7 @@ __device__ __forceinline__ void pair_epilogue(const DenseGemmParams& p, uint32_t
         for (int j = 0; j < 4; ++j)
           st_shared_v4(buf + row_piece<64>(lane, j), a[16 * h + 4 * j], a[16 * h + 4 * j + 1], a[16 * h + 4 * j + 2],
                        a[16 * h + 4 * j + 3]);
-        buffer_store<float, 64>(buf, tma, &p.tout, n + 16 * h, m0, split,
+        buffer_store<float, 64>(buf, p.tma_out, &p.tout, n + 16 * h, m0, split,
                                 static_cast<float*>(p.out) + split * p.split_stride, p.ldo, nr, nc - 16 * h,
                                 p.accumulate, lane);
       }
@@ -486,7 +507,7 @@ __device__ __forceinline__ void pair_epilogue(const DenseGemmParams& p, uint32_t
       buffer_take(lane);
 #pragma unroll
       for (int j = 0; j < 4; ++j) sts128(buf + row_piece<64>(lane, j), pack8<T>(reinterpret_cast<const float*>(a) + 8 * j));
-      buffer_store<T, 64>(buf, tma, &p.tout, n, m0, 0, static_cast<T*>(p.out), p.ldo, nr, nc, p.accumulate, lane);
+      buffer_store<T, 64>(buf, p.tma_out, &p.tout, n, m0, 0, static_cast<T*>(p.out), p.ldo, nr, nc, false, lane);
     }
   }
 }

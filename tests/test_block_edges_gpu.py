@@ -50,3 +50,35 @@ def test_dense_fwd_with_one_small_copy(kind):
     # one truncated addition for 16 products and up to 20 joins
     err = (x64.shape[1] / 16 + 20) * STEP * (x64.abs() @ w64.abs().t())
     close(y, ref, rounded(ref, BF, err), kind)
+
+
+@pytest.mark.parametrize("M,K,N,dtype", [
+    (512, 2048, 2048, BF),    # whole units of the pair kernel, rows on 16-byte boundaries
+    (512, 2048, 2048, HF),
+    (500, 2050, 2000, HF),    # rows on 4-byte boundaries, ragged units
+    (512, 2049, 2048, BF),    # rows on 2-byte boundaries
+    (4096, 2600, 2048, BF),   # a last wave cut along k
+    (100, 136, 72, BF),       # the cluster kernel
+    (100, 137, 72, HF),
+    (20000, 256, 256, HF),    # splits and their join
+])
+def test_accumulating_into_a_16_bit_dw_rounds_once(M, K, N, dtype):
+    x, dy = normal(1, M, K, dtype=dtype), normal(2, M, N, dtype=dtype)
+    old = normal(3, N, K, std=M ** 0.5, dtype=dtype)
+    dw = old.clone()
+    ops.dense_bwd(x, None, dy, need_dx=False, need_dbias=False, dw=dw)
+    x64, dy64 = x.double(), dy.double()
+    ref = old.double() + dy64.t() @ x64
+    # what the fp32 sums lose (one truncated addition for 16 rows, up to 20 joins) and the fp32 addition of the old
+    # value; then one rounding of the result
+    extra = (M / 16 + 20) * STEP * (dy64.abs().t() @ x64.abs()) + STEP * old.double().abs()
+    close(dw, ref, rounded(ref, dtype, extra), "dw")
+
+
+@pytest.mark.parametrize("K,N", [(2048, 2048), (64, 40)])
+def test_accumulated_fp16_sums_may_pass_the_type_on_the_way(K, N):
+    """A product beyond 65504 onto an old value that brings it back."""
+    x, dy = torch.full((64, K), 40.0, device="cuda", dtype=HF), torch.full((64, N), 32.0, device="cuda", dtype=HF)
+    dw = torch.full((N, K), -60000.0, device="cuda", dtype=HF)
+    ops.dense_bwd(x, None, dy, need_dx=False, need_dbias=False, dw=dw)
+    assert torch.equal(dw, torch.full_like(dw, 64 * 40 * 32 - 60000))  # 21920: every sum on the way is exact
