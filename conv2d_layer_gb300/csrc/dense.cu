@@ -28,12 +28,14 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 long ld_of(const conv2d_mat* m, int cols) { return m->ld ? m->ld : cols; }
 
 // ------------------------------------------------------------------ tiles
-// The longest K loop (k-blocks of 64 rows) one accumulator sums for a weight gradient kept in fp32: the
-// tensor core's fp32 sums are not rounded to nearest and lose about 2^-25 of the sum at every MMA, so 4,096
-// rows (256 MMAs) stay below 1e-5; longer products are split and the splits joined with ordinary fp32 adds.
-constexpr int kFp32SplitKb = 64;
-// k-blocks whose sum is off by no more than 1e-6 (4,096 rows: 4e-6), taken where it costs little: everywhere, 8192 x
-// 2048 x 8192 would take 276 us instead of 176.
+// The longest K loop (k-blocks of 64 rows) one accumulator sums for a weight gradient, by its type. The tensor core's
+// fp32 sums are truncated, so terms of one sign lose up to 2^-23.3 of the sum at every MMA of 16 rows (fp16 operands;
+// 2^-24.4 with bf16 until the sums are long): 4,096 rows 2.3e-5, 16,384 rows 1e-4 (a fifth of fp16's half step),
+// 131,072 rows 8e-4 (a fifth of bf16's). Terms of either sign lose far less: 4,096 rows 5e-6 in the 2-norm. Longer
+// products are split and the splits joined with ordinary fp32 additions, rounded once.
+constexpr int kFp32SplitKb = 64, kFp16SplitKb = 256, kBf16SplitKb = 2048;
+// k-blocks whose sum is off by a quarter of that (1,024 rows: 5e-6, and 1.3e-6 in the 2-norm), taken for fp32 where it
+// costs little: everywhere, 8192 x 2048 x 8192 would take 276 us instead of 176.
 constexpr int kFp32ShortKb = 16;
 
 struct GemmPlan {
@@ -50,8 +52,9 @@ struct GemmPlan {
 // k-block takes a CTA what its MMAs or its operands' way from L2 take, whichever is longer, which comes to a line
 // in BN; a unit has a fixed cost (launch, first operands, epilogue); clusters pay for joining their sums. Units
 // run in waves over the SMs; the pair kernel hides its epilogue under the next unit's loop. can_split: the product
-// may be split over k, with fp32 partials in the workspace; max_kb: bound on one accumulator's k-blocks (0: none).
-GemmPlan plan_gemm(int mode, long m, long n, int kb, int max_kb, int sms, bool can_split = false) {
+// may be split over k, with fp32 partials in the workspace; max_kb: bound on one accumulator's k-blocks, short_kb: those
+// it had better not pass (0: none).
+GemmPlan plan_gemm(int mode, long m, long n, int kb, int sms, bool can_split = false, int max_kb = 0, int short_kb = 0) {
   const bool r_mn = dense_r_mn(mode), c_mn = dense_c_mn(mode);
   GemmPlan best = {};
   double best_t = 1e300;
@@ -96,7 +99,7 @@ GemmPlan plan_gemm(int mode, long m, long n, int kb, int max_kb, int sms, bool c
     // splits, 17.3 in one; 4096 x 512 x 512: 22.1 in 8, 18.7 as a cluster of 4); it reads a value's partials in turn
     if (g.splits > 1) t += 8000 + 100.0 * g.splits + static_cast<double>(m) * n * 4 * 2 * g.splits / 7000;
     // up to a tenth of the time goes into short fp32 sums
-    if (max_kb > 0 && ceil_div(g.kb_per_split, cl) > kFp32ShortKb) t *= 1.1;
+    if (short_kb > 0 && ceil_div(g.kb_per_split, cl) > short_kb) t *= 1.1;
     if (t < best_t) {
       best_t = t;
       best = g;
@@ -319,7 +322,7 @@ void plan_fwd(const conv2d_dense_desc& d, const conv2d_mat* x, const conv2d_mat*
   pl->fp8 = both_8bit(x, w);
   pl->x = plan_copy(c, x, d.M, d.K, pl->fp8);
   pl->w = plan_copy(c, w, d.N, d.K, pl->fp8);
-  pl->g = plan_gemm(kDenseForward, d.M, d.N, static_cast<int>(ceil_div(d.K, pl->fp8 ? 128 : 64)), 0, sms);
+  pl->g = plan_gemm(kDenseForward, d.M, d.N, static_cast<int>(ceil_div(d.K, pl->fp8 ? 128 : 64)), sms);
   pl->join = plan_join(c, pl->g);
   pl->total = c.size();
 }
@@ -328,6 +331,7 @@ struct BwdPlan {
   bool dz_own;  // dz is formed in the workspace (else it is dy)
   long lddz;
   long pass_rows;  // rows of a pass of dW (M: one pass)
+  int planes;      // fp32 partials of dW in the workspace, joined at the end (0: dW is written by the product)
   size_t dz, x, w, dpart, spart, joinx, joinw, total;
   DactPlan dact;
   GemmPlan gx, gw;
@@ -344,25 +348,29 @@ void plan_bwd(const conv2d_dense_desc& d, const conv2d_mat* x, const conv2d_mat*
   pl->w = pl->x = pl->spart = pl->joinx = pl->joinw = kNone;
   if (dx) {
     pl->w = plan_copy(c, w, d.N, d.K, false);
-    pl->gx = plan_gemm(kDenseDx, d.M, d.K, static_cast<int>(ceil_div(d.N, 64)), 0, sms);
+    pl->gx = plan_gemm(kDenseDx, d.M, d.K, static_cast<int>(ceil_div(d.N, 64)), sms);
     pl->joinx = plan_join(c, pl->gx);
   }
   if (dw) {
     pl->x = plan_copy(c, x, d.M, d.K, false);
-    // An fp32 dW over many rows is summed in pieces of kFp32SplitKb k-blocks: side by side, joined afterwards, or one
-    // after the other, added to dW. The second saves the partials' traffic but idles at each piece's last wave. It
-    // is taken for up to 4 pieces whose waves are four fifths full (8192 x 2048 x 8192: 176 us against 188; 16384 x
+    // A dW over many rows is summed in pieces: side by side, joined afterwards, or one after the other, added to dW (16
+    // bits: to one fp32 plane in the workspace, rounded at the end). The second saves the partials' traffic but idles
+    // at each piece's last wave. It is taken in fp32 for up to 4 pieces whose waves are four fifths full (8192 x 2048 x 8192: 176 us against 188; 16384 x
     // 4096 x 4096: 344 to 358 against 353 to 355; 8 pieces, 32768 x 2048 x 8192: 722 against 674; waves 59 % full,
     // 9000 x 2304 x 2560: 97 against 86), and where the partials would take more than 2 GB.
-    const int kb = static_cast<int>(ceil_div(d.M, 64)), bound = dw->type == CONV2D_FP32 ? kFp32SplitKb : 0;
+    const bool f32 = dw->type == CONV2D_FP32;
+    const int kb = static_cast<int>(ceil_div(d.M, 64));
+    const int bound = f32 ? kFp32SplitKb : d.dtype == CONV2D_FP16 ? kFp16SplitKb : kBf16SplitKb;
     const long pairs = sms / 2, tiles = ceil_div(d.N, 256) * ceil_div(d.K, 256), waves = ceil_div(tiles, pairs);
-    const long pieces = bound ? ceil_div(kb, bound) : 1;
-    const bool passes = pieces > 1 && ((pieces <= 4 && tiles * 5 >= waves * pairs * 4) ||
+    const long pieces = ceil_div(kb, bound);
+    const bool passes = pieces > 1 && ((f32 && pieces <= 4 && tiles * 5 >= waves * pairs * 4) ||
                                        pieces * d.N * d.K * 4 > (2L << 30));
     pl->pass_rows = passes ? bound * 64L : d.M;
-    pl->gw = passes ? plan_gemm(kDenseDw, d.N, d.K, bound, 0, sms) : plan_gemm(kDenseDw, d.N, d.K, kb, bound, sms, true);
+    pl->gw = passes ? plan_gemm(kDenseDw, d.N, d.K, bound, sms)
+                    : plan_gemm(kDenseDw, d.N, d.K, kb, sms, true, bound, f32 ? kFp32ShortKb : 0);
     pl->joinw = plan_join(c, pl->gw);
-    if (pl->gw.splits > 1) pl->spart = c.take(static_cast<size_t>(pl->gw.splits) * d.N * d.K * 4);
+    pl->planes = passes ? (f32 ? 0 : 1) : pl->gw.splits > 1 ? pl->gw.splits : 0;
+    if (pl->planes) pl->spart = c.take(static_cast<size_t>(pl->planes) * d.N * d.K * 4);
   }
   pl->total = c.size();
 }
@@ -507,14 +515,14 @@ int conv2d_dense_bwd(const conv2d_dense_desc* d, const conv2d_mat* x, const conv
     p.ldo = ld_of(dx, d->K);
     if ((rc = run_gemm(p, pl.gx, odz, ow, d->dtype, kDenseDx, at(ws, pl.joinx), false, "dense_dx", dev, st))) return rc;
   }
-  const bool joined = dw && pl.gw.splits > 1;
+  const bool joined = dw && pl.planes > 0;
   if (dw) {
     for (long r0 = 0; r0 < d->M; r0 += pl.pass_rows) {
       DenseGemmParams p = {};
       p.out = joined ? static_cast<void*>(base + pl.spart) : dw->data;
       p.ldo = joined ? d->K : ld_of(dw, d->K);
       p.out_f32 = joined || dw->type == CONV2D_FP32;
-      p.accumulate = !joined && (d->accumulate || r0 > 0);
+      p.accumulate = (d->accumulate && !joined) || r0 > 0;
       p.split_stride = static_cast<long>(d->N) * d->K;
       Operand oz = odz, oa = ox;
       oz.rows = oa.rows = std::min(pl.pass_rows, d->M - r0);
@@ -535,7 +543,7 @@ int conv2d_dense_bwd(const conv2d_dense_desc* d, const conv2d_mat* x, const conv
            launch_column_sum(part, pl.dact.strips, d->N, dbias, d->accumulate != 0, dx || dw, st));
   if (joined)
     LAUNCH("dense_dw_join", st,
-           launch_split_join(reinterpret_cast<float*>(base + pl.spart), pl.gw.splits, d->N, d->K, dw->type, dw->data,
+           launch_split_join(reinterpret_cast<float*>(base + pl.spart), pl.planes, d->N, d->K, dw->type, dw->data,
                              ld_of(dw, d->K), d->accumulate != 0, st));
   return CONV2D_OK;
 }

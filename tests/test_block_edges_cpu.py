@@ -31,3 +31,18 @@ def test_a_copy_of_any_size_shows_in_the_workspace(d, x, w):
     assert abi.conv2d_dense_fwd_workspace_size(d, x, w) > 256
     n = abi.conv2d_dense_fwd_workspace_size(d, x, w)
     assert abi.conv2d_dense_fwd_workspace_size(dense(d.M, 128, d.N), mat(), mat()) == 256 < n
+
+
+@pytest.mark.parametrize("dtype,M,planes", [(abi.FP16, 16384, 0), (abi.FP16, 16448, 2), (abi.FP16, 200704, 13),
+                                            (abi.BF16, 131072, 0), (abi.BF16, 200704, 2), (abi.BF16, 1000000, 8)])
+def test_a_16_bit_dw_over_very_many_rows_is_summed_in_pieces(dtype, M, planes):
+    """One accumulator sums at most 16,384 rows (fp16) or 131,072 (bf16): what it truncates stays below the rounding.
+    Longer sums have an fp32 plane in the workspace for each piece (here the product fills the GPU by itself)."""
+    d, m = dense(M, 2048, 2048, dtype=dtype), mat(dtype)
+    n = abi.conv2d_dense_bwd_workspace_size(d, m, m, None, m, None, m, None)
+    assert n // (2048 * 2048 * 4) == planes
+    # partials of more than 2 GB: one plane, added to pass by pass
+    d = dense(M, 16384, 16384, dtype=dtype)
+    n = abi.conv2d_dense_bwd_workspace_size(d, m, m, None, m, None, m, None)
+    one = 16384 * 16384 * 4
+    assert n < one // 2 if planes == 0 else planes * one <= n < (planes + 1) * one if planes == 2 else one <= n < 2 * one

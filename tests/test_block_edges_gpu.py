@@ -82,3 +82,44 @@ def test_accumulated_fp16_sums_may_pass_the_type_on_the_way(K, N):
     dw = torch.full((N, K), -60000.0, device="cuda", dtype=HF)
     ops.dense_bwd(x, None, dy, need_dx=False, need_dbias=False, dw=dw)
     assert torch.equal(dw, torch.full_like(dw, 64 * 40 * 32 - 60000))  # 21920: every sum on the way is exact
+
+
+def test_fp16_dw_over_very_many_rows():
+    """400,000 rows of positive terms: what the accumulators truncate must stay below the type's rounding.
+
+    The mean relative error of n elements is what truncation leaves (it always points down) and the mean of n
+    roundings of half a step at most each. Held to half of fp16's half step, 2^-12, and three standard deviations of
+    that mean (half a step 2^-11, spread evenly: / sqrt(3 n))."""
+    M, K, N = 400000, 2048, 2048
+    g = torch.Generator(device="cuda").manual_seed(7)
+    x = torch.rand(M, K, generator=g, device="cuda", dtype=HF)
+    dy = torch.rand(M, N, generator=g, device="cuda", dtype=HF) * 0.25
+    _, dw, _ = ops.dense_bwd(x, None, dy, need_dx=False, need_dbias=False, grad_dtype=HF)
+    n = 64
+    ref = dy[:, :n].double().t() @ x[:, :n].double()
+    rel = (dw[:n, :n].double() - ref) / ref
+    assert float(rel.mean().abs()) < 2.0 ** -12 + 3 * 2.0 ** -11 / (3 * n * n) ** 0.5
+    assert float(rel.abs().max()) < 2.0 ** -11 + 2.0 ** -12
+
+
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_fp16_dw_in_passes(accumulate):
+    """Pieces whose partials would take more than 2 GB: one after the other onto one fp32 plane, rounded once."""
+    M, K, N = 33000, 16384, 16128
+    g = torch.Generator(device="cuda").manual_seed(8)
+    x = torch.rand(M, K, generator=g, device="cuda", dtype=HF) - 0.5
+    dy = torch.rand(M, N, generator=g, device="cuda", dtype=HF) - 0.5
+    old = torch.rand(N, K, generator=g, device="cuda", dtype=HF) * 40 if accumulate else None
+    dw = old.clone() if accumulate else None
+    out = ops.dense_bwd(x, None, dy, need_dx=False, need_dbias=False, grad_dtype=HF, dw=dw)[1]
+    assert out is dw or not accumulate
+    n = 192
+    for r, c in ((slice(0, n), slice(0, n)), (slice(N - n, N), slice(K - n, K))):
+        ref = dy[:, r].double().t() @ x[:, c].double()
+        mag = dy[:, r].double().abs().t() @ x[:, c].double().abs()
+        # a pass adds 1,024 MMAs, each truncated; three passes are joined, then the old value
+        extra = (1024 + 20 + 3) * STEP * mag
+        if accumulate:
+            ref = ref + old[r, c].double()
+            extra = extra + STEP * old[r, c].double()
+        close(out[r, c], ref, rounded(ref, HF, extra), "dw")
