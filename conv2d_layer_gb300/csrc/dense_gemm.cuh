@@ -145,7 +145,7 @@ __device__ __forceinline__ float ld_shared_f32(uint32_t addr) {
 // of z takes a maximum over the warp's 32 columns, which are one group).
 template <typename T, int MODE, int NC>
 __device__ __forceinline__ void dense_epilogue(const DenseGemmParams& p, float (&v)[NC], int n, long m0, int split,
-                                               float nscale, float bias) {
+                                               float2 nscale, float bias) {
   const int nc = static_cast<int>(p.m - m0 < NC ? p.m - m0 : NC);  // uniform
   const bool on = n < p.n;
   if constexpr (MODE == kDenseForward) {
@@ -158,7 +158,7 @@ __device__ __forceinline__ void dense_epilogue(const DenseGemmParams& p, float (
     }
     if (p.ns) {
 #pragma unroll
-      for (int e = 0; e < NC; ++e) v[e] = e < nc ? v[e] * nscale * q8_scale(p.ms[m0 + e]) : 0.f;
+      for (int e = 0; e < NC; ++e) v[e] = e < nc ? v[e] * nscale.x * q8_scale(p.ms[m0 + e]) * nscale.y : 0.f;
     }
 #pragma unroll
     for (int e = 0; e < NC; ++e) v[e] += bias;
@@ -372,9 +372,9 @@ __device__ __forceinline__ void residual_add(uint32_t buf, float* v, int lane) {
 // res: the residual's registers, loaded for these columns and left loading for the columns from n + 128 (the
 // warp's next), so that its way from memory is hidden by the main loop or by the columns before. taken(a) is
 // called when the accumulator's columns are in a[] (it frees the accumulator, and adds other parts' sums).
-template <typename T, int MODE, typename F>
+template <typename T, int MODE, bool FP8, typename F>
 __device__ __forceinline__ void pair_epilogue(const DenseGemmParams& p, uint32_t taddr, uint32_t buf, long m0, int n,
-                                              int end, int nr, int split, float mscale, uint32_t (&res)[16], int lane,
+                                              int end, int nr, int split, uint32_t mscale, uint32_t (&res)[16], int lane,
                                               F&& taken) {
   const int nc = min(end - n, 32);
   if constexpr (MODE == kDenseForward) {
@@ -387,10 +387,19 @@ __device__ __forceinline__ void pair_epilogue(const DenseGemmParams& p, uint32_t
 #pragma unroll
       for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(a[e]);
     }
-    if (p.ns) {
+    if constexpr (FP8) {
+      const float2 f = q8_factors(mscale);
 #pragma unroll
-      for (int e = 0; e < 32; ++e)
-        if (e < nc) v[e] = v[e] * q8_scale(p.ns[n + e]) * mscale;
+      for (int e = 0; e < 32; e += 2) {
+        const float2 a = make_float2(e < nc ? q8_scale(p.ns[n + e]) : 1.f, e + 1 < nc ? q8_scale(p.ns[n + e + 1]) : 1.f);
+        const float2 s = __fmul2_rn(__fmul2_rn(make_float2(v[e], v[e + 1]), splat(f.x)), a);
+        v[e] = s.x;
+        v[e + 1] = s.y;
+      }
+      if (__any_sync(0xffffffffu, f.y != 1.f)) {  // a scale of one of the rows is beyond 2^-100 or 2^80
+#pragma unroll
+        for (int e = 0; e < 32; ++e) v[e] *= f.y;
+      }
     }
     if (p.bias) {
       if (nc == 32) {
@@ -749,7 +758,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) dense_pair_kernel(const __gri
       const int ct = w.ct;
       const long m0 = static_cast<long>(w.lt) * 256 + rank * 128 + q * 32;
       const int nr = static_cast<int>(min(p.m - m0, 32L));
-      const float mscale = MODE == kDenseForward && p.ms && lane < nr ? q8_scale(p.ms[m0 + lane]) : 1.f;
+      const uint32_t mscale = FP8 && lane < nr ? p.ms[m0 + lane] : 127u;
       const int end = min(p.n, ct * BN + BN);
       const int n0 = ct * BN + part * 32;
       uint32_t res[16];
@@ -795,7 +804,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) dense_pair_kernel(const __gri
         }
 #pragma unroll 1
         for (int n = n0; n < end; n += 128)
-          pair_epilogue<T, MODE>(p, t0 + n, buf0, m0, n, end, nr, w.split, mscale, res, lane,
+          pair_epilogue<T, MODE, FP8>(p, t0 + n, buf0, m0, n, end, nr, w.split, mscale, res, lane,
                                  [&](uint32_t (&a)[32]) {
                                    if (w.tail >= 0) {
                                      for (int j = 1; j < p.parts; ++j) {
@@ -917,9 +926,10 @@ __global__ void __launch_bounds__(kClusterThreads, 1) dense_cluster_kernel(const
   } else {
     const int q = warp & 3, half = (warp - 2) >> 2;
     const int n = lt * 128 + q * 32 + lane;
-    float nscale = 1.f, bias = 0.f;
+    float2 nscale = splat(1.f);
+    float bias = 0.f;
     if (MODE == kDenseForward && CL == 1 && n < p.n) {
-      if (p.ns) nscale = q8_scale(p.ns[n]);
+      if (p.ns) nscale = q8_factors(p.ns[n]);
       if (p.bias) bias = p.bias[n];
     }
     int ok = 1;
@@ -969,9 +979,10 @@ __global__ void __launch_bounds__(kClusterThreads, 1) dense_cluster_kernel(const
     for (int j = warp; j < own * 4; j += kClusterThreads / 32) {
       const int q = j & 3, i = j >> 2;
       const int n = lt * 128 + q * 32 + lane;
-      float nscale = 1.f, bias = 0.f;
+      float2 nscale = splat(1.f);
+      float bias = 0.f;
       if (MODE == kDenseForward && n < p.n) {
-        if (p.ns) nscale = q8_scale(p.ns[n]);
+        if (p.ns) nscale = q8_factors(p.ns[n]);
         if (p.bias) bias = p.bias[n];
       }
       float v[4] = {0.f, 0.f, 0.f, 0.f};

@@ -88,6 +88,14 @@ __device__ __forceinline__ uint32_t q8_scale_byte(uint32_t amax_bits) {
   return static_cast<uint32_t>(e < 1 ? 1 : e);
 }
 __device__ __forceinline__ float q8_scale(uint32_t byte) { return __uint_as_float(byte << 23); }  // 2^(byte - 127)
+// The scale of byte b in two factors, which are applied before and after another scale: for a product's sum v (0, or
+// 2^-18 to 2^46 in magnitude: e4m3 products, 2^28 of them at most) no step of v * f.x * q8_scale(a) * f.y overflows or
+// underflows where the result does not (one after the other, 2^111 and 2^-125 took a sum of 2^18 to infinity). f.y is 1
+// for scales of 2^-100 to 2^80; one beyond that comes in two halves of the same sign.
+__device__ __forceinline__ float2 q8_factors(uint32_t b) {
+  const uint32_t x = b < 27u ? 64u : (b > 207u ? 191u : b);
+  return make_float2(q8_scale(x), q8_scale(b - x + 127u));
+}
 __device__ __forceinline__ float q8_inv_scale(uint32_t byte) { return __uint_as_float((254u - byte) << 23); }
 // Two values, already divided by their scale, to e4m3 (a in the low byte). The conversion saturates, so
 // an infinity is turned into NaN first: t * 0 + t.

@@ -123,3 +123,13 @@ def test_fp16_dw_in_passes(accumulate):
             ref = ref + old[r, c].double()
             extra = extra + STEP * old[r, c].double()
         close(out[r, c], ref, rounded(ref, HF, extra), "dw")
+
+
+@pytest.mark.parametrize("M,N", [(3, 200), (2048, 4096)])
+@pytest.mark.parametrize("up,down", [(118, -118), (-118, 118)])
+def test_8_bit_scales_far_from_one(M, N, up, down):
+    """Scales of either operand near the ends of their range: only their product is applied to the sums."""
+    x, w = normal(1, M, 64).abs(), normal(2, N, 64).abs()
+    near, _ = ops.dense_fwd(ops.q8_encode(x, 0), ops.q8_encode(w, 0), dtype=BF)
+    far, _ = ops.dense_fwd(ops.q8_encode(x * 2.0 ** up, 0), ops.q8_encode(w * 2.0 ** down, 0), dtype=BF)
+    assert torch.equal(near, far)
