@@ -6,8 +6,9 @@ and new outputs come from torch's allocator, in the pool of the stream the call 
 before a launch (ValueError); a status of the library raises abi.Conv2dError. The checks are in csrc/binding.cpp,
 the arithmetic in the library's kernels.
 
-`stream`: a torch.cuda.Stream or None for the current stream of the tensors' device. With another stream than
-the current one, the caller orders the two (as for any torch operation on a side stream).
+`stream`: a torch.cuda.Stream of the tensors' device, a raw stream handle (an int) of that device, or None for its
+current stream. With another stream than the current one, the caller orders the two (as for any torch operation on a
+side stream).
 """
 import functools
 from typing import NamedTuple, Optional
@@ -68,13 +69,25 @@ def q8_empty(rows, cols, group=GROUP, device="cuda"):
               torch.empty((rows, q8_scales(cols, group)), dtype=torch.uint8, device=device), group)
 
 
+def _device_of(args):
+    """The device of the first tensor (or Q8) among a call's arguments."""
+    return next((a.device for a in args if isinstance(getattr(a, "device", None), torch.device)), None)
+
+
 def _streamed(f):
     """Runs a call on `stream`: made current, so that what the call allocates belongs to it."""
     @functools.wraps(f)
     def call(*args, stream=None, **kw):
         if stream is None:
             return f(*args, **kw)
-        with torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream):
+        dev = _device_of((*args, *kw.values()))
+        if dev is None or dev.type != "cuda":
+            return f(*args, **kw)  # refused there
+        if isinstance(stream, int):
+            stream = torch.cuda.ExternalStream(stream, device=dev)
+        elif stream.device != dev:
+            raise ValueError(f"stream: of {stream.device}, but the tensors are on {dev}")
+        with torch.cuda.stream(stream):
             return f(*args, **kw)
     return call
 

@@ -1,8 +1,11 @@
 """The residual block's calls without a GPU, where a plan or a rule changes: workspace sizes, streams, stale 8-bit
 weights."""
-import pytest
+import contextlib
 
-from conv2d_layer_gb300 import abi
+import pytest
+import torch
+
+from conv2d_layer_gb300 import abi, ops
 
 P = 1 << 20  # stands for an aligned device pointer: never read, every call below is sized or refused
 
@@ -46,3 +49,50 @@ def test_a_16_bit_dw_over_very_many_rows_is_summed_in_pieces(dtype, M, planes):
     n = abi.conv2d_dense_bwd_workspace_size(d, m, m, None, m, None, m, None)
     one = 16384 * 16384 * 4
     assert n < one // 2 if planes == 0 else planes * one <= n < (planes + 1) * one if planes == 2 else one <= n < 2 * one
+
+
+class OnDevice:
+    """Stands for a tensor or a stream of a device that this machine lacks."""
+
+    def __init__(self, device):
+        self.device = torch.device(device)
+
+
+@pytest.fixture
+def streams(monkeypatch):
+    """The streams made current around a call, as (pointer or object, device)."""
+    seen = []
+
+    class Binding:
+        def q8_encode(self, x, group, out):
+            return None
+
+        def dense_bwd(self, *a):
+            return None, None, None
+
+    @contextlib.contextmanager
+    def current(s):
+        seen.append(s)
+        yield
+
+    monkeypatch.setattr(ops, "_binding", lambda: Binding())
+    monkeypatch.setattr(torch.cuda, "stream", current)
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda p, device=None: (p, device))
+    return seen
+
+
+def test_a_raw_stream_belongs_to_the_tensors_device(streams):
+    ops.q8_encode(OnDevice("cuda:1"), stream=1234)
+    ops.q8_encode(ops.Q8(OnDevice("cuda:2"), None), stream=5)
+    # the first argument may be left out; the device is that of the first tensor there is
+    ops.dense_bwd(None, None, dy=OnDevice("cuda:3"), need_dx=False, need_dw=False, stream=6)
+    assert streams == [(1234, torch.device("cuda:1")), (5, torch.device("cuda:2")), (6, torch.device("cuda:3"))]
+
+
+def test_a_stream_of_another_device_is_refused(streams):
+    s = OnDevice("cuda:1")
+    ops.q8_encode(OnDevice("cuda:1"), stream=s)
+    assert streams == [s]
+    with pytest.raises(ValueError, match="stream: of cuda:1, but the tensors are on cuda:0"):
+        ops.q8_encode(OnDevice("cuda:0"), stream=s)
+    assert streams == [s]

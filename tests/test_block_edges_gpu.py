@@ -133,3 +133,13 @@ def test_8_bit_scales_far_from_one(M, N, up, down):
     near, _ = ops.dense_fwd(ops.q8_encode(x, 0), ops.q8_encode(w, 0), dtype=BF)
     far, _ = ops.dense_fwd(ops.q8_encode(x * 2.0 ** up, 0), ops.q8_encode(w * 2.0 ** down, 0), dtype=BF)
     assert torch.equal(near, far)
+
+
+def test_on_a_raw_stream():
+    x = normal(1, 300, 256, dtype=BF)
+    want = ops.q8_encode(x)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = ops.q8_encode(x, stream=side.cuda_stream)
+    side.synchronize()
+    assert torch.equal(got.scale, want.scale) and torch.equal(got.q.view(torch.uint8), want.q.view(torch.uint8))
