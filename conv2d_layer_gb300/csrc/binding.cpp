@@ -294,7 +294,6 @@ PyObject* rms_norm_bwd(PyObject* const* a) {
     mx = given(a[5]) ? mat(a[5], "dx", s.rows, s.cols, t, s.dev) : new_mat(dx, s.rows, s.cols, s.type, s.dev);
   const int32_t cols = small(s.cols, "h");
   float* pg = nullptr;
-  size_t n = 0;
   if (need_dg) {
     if (given(a[6])) {
       pg = vec(a[6], "dgamma", s.cols, s.dev);
@@ -302,10 +301,10 @@ PyObject* rms_norm_bwd(PyObject* const* a) {
       dg = make({s.cols}, at::kFloat, s.dev);
       pg = static_cast<float*>(dg.data_ptr());
     }
-    n = lib.conv2d_rms_norm_bwd_workspace_size(s.rows, cols);
-    ws = make({static_cast<int64_t>(n)}, at::kByte, s.dev);
   }
   run(s.dev, "conv2d_rms_norm_bwd", [&](void* st) {
+    const size_t n = need_dg ? lib.conv2d_rms_norm_bwd_workspace_size(s.rows, cols) : 0;  // of the current device
+    if (n) ws = make({static_cast<int64_t>(n)}, at::kByte, s.dev);
     return lib.conv2d_rms_norm_bwd(s.rows, cols, &h, gamma, inv, &dy, given(a[4]) ? &dh : nullptr,
                                    need_dx ? &mx : nullptr, pg, need_dg && given(a[6]), n ? ws.data_ptr() : nullptr, n, st);
   });

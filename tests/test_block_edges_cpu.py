@@ -1,6 +1,8 @@
 """The residual block's calls without a GPU, where a plan or a rule changes: workspace sizes, streams, stale 8-bit
 weights."""
 import contextlib
+import ctypes
+import subprocess
 
 import pytest
 import torch
@@ -96,3 +98,37 @@ def test_a_stream_of_another_device_is_refused(streams):
     with pytest.raises(ValueError, match="stream: of cuda:1, but the tensors are on cuda:0"):
         ops.q8_encode(OnDevice("cuda:0"), stream=s)
     assert streams == [s]
+
+
+FAKE = """
+#include <stddef.h>
+int asked = 0;
+size_t conv2d_rms_norm_bwd_workspace_size(long long rows, int cols) { ++asked; return 256; }
+size_t conv2d_dense_fwd_workspace_size() { ++asked; return 256; }
+size_t conv2d_dense_bwd_workspace_size() { ++asked; return 256; }
+int conv2d_q8_encode() { return 1; }
+int conv2d_q8_decode() { return 1; }
+int conv2d_rms_norm_fwd() { return 1; }
+int conv2d_rms_norm_bwd() { return 1; }
+int conv2d_dense_fwd() { return 1; }
+int conv2d_dense_bwd() { return 1; }
+"""
+
+
+def test_sizes_are_asked_for_on_the_tensors_device(tmp_path):
+    """A workspace is sized for the current device (its SMs), so the library is asked only once the tensors' device
+    has been made current: not at all for tensors that are refused before that. The library is a stand-in that counts."""
+    src, path = tmp_path / "fake.c", str(tmp_path / "fake.so")
+    src.write_text(FAKE)
+    subprocess.run(["gcc", "-shared", "-fPIC", "-o", path, str(src)], check=True)
+    h, gamma, inv = torch.zeros(4, 8), torch.ones(8), torch.ones(4)
+    binding = ops._binding()
+    binding.init(path)
+    try:
+        for call in (lambda: ops.rms_norm_bwd(h, gamma, inv, h), lambda: ops.dense_bwd(h.bfloat16(), h.bfloat16(), torch.zeros(4, 4).bfloat16()),
+                     lambda: ops.dense_fwd(h.bfloat16(), h.bfloat16())):
+            with pytest.raises(ValueError, match="CUDA device memory"):
+                call()
+    finally:
+        binding.init(abi.lib_path())
+    assert ctypes.c_int.in_dll(ctypes.CDLL(path), "asked").value == 0
