@@ -41,7 +41,7 @@ class FeedForward:
         self.dgamma, self.db1, self.db2 = (torch.zeros_like(t) for t in (self.gamma, self.b1, self.b2))
         self.dw1, self.dw2 = (torch.zeros(t.shape, device=dev, dtype=torch.float32) for t in (self.w1, self.w2))
         self.saved = None
-        self.w8 = None
+        self.w8 = self.w8_of = None
 
     def zero_grad(self):
         for t in (self.dgamma, self.dw1, self.db1, self.dw2, self.db2):
@@ -72,9 +72,16 @@ class FeedForward:
             return sum(size(p) for p in t[:2]) if isinstance(t, ops.Q8) else t.numel() * t.element_size()
         return 0 if self.saved is None else sum(size(t) for t in self.saved[1:])
 
+    def _weights(self):
+        # tensors made in inference mode carry no version
+        return [(t, None if t.is_inference() else t._version) for t in (self.w1, self.w2)]
+
     def quantize(self):
-        """Keeps 8-bit weights, one scale an output feature, for fwd_infer(bits8=True)."""
+        """Keeps 8-bit weights, one scale an output feature, for fwd_infer(bits8=True); again after each change of w1
+        or w2. fwd_infer refuses 8-bit weights older than a change that torch has seen (not one through .data, a raw
+        pointer, or of tensors made in inference mode)."""
         self.w8 = ops.q8_encode(self.w1, 0), ops.q8_encode(self.w2, 0)
+        self.w8_of = self._weights()
 
     def fwd_infer(self, x, residual=None, bits8=False):
         """(y, h) without saving anything, for any number of rows (one for a decoded token). bits8: 8-bit weights
@@ -85,6 +92,8 @@ class FeedForward:
             return ops.dense_fwd(u, self.w2, self.b2, residual=n.h)[0], n.h
         if self.w8 is None:
             raise RuntimeError("bits8 follows quantize()")
+        if self.w8_of and any(a is not b or u != v for (a, u), (b, v) in zip(self.w8_of, self._weights())):
+            raise RuntimeError("w1 or w2 has changed: bits8 needs another quantize()")
         n = ops.rms_norm_fwd(x, self.gamma, self.eps, residual=residual, y=False, group=0)
         u, _ = ops.dense_fwd(n.q8, self.w8[0], self.b1, self.act, dtype=self.dtype)
         return ops.dense_fwd(ops.q8_encode(u, 0), self.w8[1], self.b2, residual=n.h, dtype=self.dtype)[0], n.h

@@ -8,6 +8,7 @@ import pytest
 import torch
 
 from conv2d_layer_gb300 import abi, ops
+from conv2d_layer_gb300.block import FeedForward
 
 P = 1 << 20  # stands for an aligned device pointer: never read, every call below is sized or refused
 
@@ -132,3 +133,44 @@ def test_sizes_are_asked_for_on_the_tensors_device(tmp_path):
     finally:
         binding.init(abi.lib_path())
     assert ctypes.c_int.in_dll(ctypes.CDLL(path), "asked").value == 0
+
+
+def feed_forward(**kw):
+    n = lambda *s: torch.randn(*s, generator=torch.Generator().manual_seed(0))  # noqa: E731
+    return FeedForward(n(16), n(32, 16), n(32), n(16, 32), n(16), device="cpu", **kw)
+
+
+def change_in_place(ff):
+    ff.w1.mul_(2)
+
+
+def change_by_assignment(ff):
+    ff.w2 = ff.w2.clone()
+
+
+@pytest.mark.parametrize("change", [change_in_place, change_by_assignment])
+def test_8_bit_weights_are_not_served_once_the_weights_have_changed(monkeypatch, change):
+    monkeypatch.setattr(ops, "q8_encode", lambda t, group: ("8-bit", t, group))
+    ff, x = feed_forward(), torch.zeros(2, 16).bfloat16()
+    ff.quantize()
+    with pytest.raises(ValueError, match="CUDA device memory"):  # taken: the kernels are reached
+        ff.fwd_infer(x, bits8=True)
+    change(ff)
+    with pytest.raises(RuntimeError, match="quantize"):
+        ff.fwd_infer(x, bits8=True)
+    ff.quantize()
+    with pytest.raises(ValueError, match="CUDA device memory"):
+        ff.fwd_infer(x, bits8=True)
+
+
+def test_weights_made_in_inference_mode_can_be_quantized(monkeypatch):
+    """Such tensors have no version; another tensor in their place is still seen."""
+    monkeypatch.setattr(ops, "q8_encode", lambda t, group: ("8-bit", t, group))
+    with torch.inference_mode():
+        ff = feed_forward()
+        ff.quantize()
+        with pytest.raises(ValueError, match="CUDA device memory"):
+            ff.fwd_infer(torch.zeros(2, 16).bfloat16(), bits8=True)
+        change_by_assignment(ff)
+        with pytest.raises(RuntimeError, match="quantize"):
+            ff.fwd_infer(torch.zeros(2, 16).bfloat16(), bits8=True)

@@ -5,6 +5,7 @@ import torch
 
 from block_ref import STEP, close, q8_values, rounded
 from conv2d_layer_gb300 import abi, ops
+from conv2d_layer_gb300.block import FeedForward
 
 pytestmark = pytest.mark.gpu
 BF, HF, FP = torch.bfloat16, torch.float16, torch.float32
@@ -143,3 +144,19 @@ def test_on_a_raw_stream():
     got = ops.q8_encode(x, stream=side.cuda_stream)
     side.synchronize()
     assert torch.equal(got.scale, want.scale) and torch.equal(got.q.view(torch.uint8), want.q.view(torch.uint8))
+
+
+def test_8_bit_weights_follow_the_weights():
+    w1, w2 = normal(1, 64, 32, std=0.2), normal(2, 32, 64, std=0.2)
+    make = lambda w: FeedForward(torch.ones(32), w, torch.zeros(64), w2, torch.zeros(32))  # noqa: E731
+    ff, x = make(w1), normal(3, 5, 32, dtype=BF)
+    ff.quantize()
+    before = ff.fwd_infer(x, bits8=True)[0]
+    ff.w1.mul_(-1)
+    with pytest.raises(RuntimeError, match="quantize"):
+        ff.fwd_infer(x, bits8=True)
+    ff.quantize()
+    other = make(-w1)
+    other.quantize()
+    after = ff.fwd_infer(x, bits8=True)[0]
+    assert torch.equal(after, other.fwd_infer(x, bits8=True)[0]) and not torch.equal(after, before)
