@@ -29,6 +29,8 @@ class FeedForward:
             raise ValueError(f"checkpoint: q8 or full, got {checkpoint!r}")
         if act not in ops.ACTS:
             raise ValueError(f"act: one of {sorted(ops.ACTS)}, got {act!r}")
+        if dtype not in (torch.bfloat16, torch.float16):
+            raise ValueError(f"dtype: torch.bfloat16 or torch.float16, got {dtype!r}")
         inner, width = w1.shape
         for name, t, shape in (("gamma", gamma, (width,)), ("b1", b1, (inner,)), ("w2", w2, (width, inner)),
                                ("b2", b2, (width,))):

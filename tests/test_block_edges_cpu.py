@@ -174,3 +174,10 @@ def test_weights_made_in_inference_mode_can_be_quantized(monkeypatch):
         change_by_assignment(ff)
         with pytest.raises(RuntimeError, match="quantize"):
             ff.fwd_infer(torch.zeros(2, 16).bfloat16(), bits8=True)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.float64, torch.int8])
+def test_feed_forward_refuses_types_its_dense_layers_lack(dtype):
+    with pytest.raises(ValueError, match="dtype: torch.bfloat16 or torch.float16"):
+        feed_forward(dtype=dtype)
+    assert feed_forward(dtype=torch.float16).w1.dtype == torch.float16
