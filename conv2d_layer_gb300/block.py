@@ -5,6 +5,7 @@
     u = act(n w1^T + b1)
     y = u w2^T + b2 + h
 
+act is one of ops.ACTS; gelu is the tanh form (torch's gelu(approximate="tanh"), not its default).
 PyTorch supplies device memory and the stream; every step runs in the library's kernels (conv2d_layer_gb300.ops).
 The class holds the parameters, the gradients (fp32, accumulated until zero_grad, as in Conv2dLayer) and what the
 forward pass saves for the backward pass. With checkpoint="q8" that is kept in 8 bits, one scale for 32 features:

@@ -22,8 +22,8 @@
 //
 // Measured: pair kernel 9728 x 2048 x 8192 bf16 171 us, 1,906 TFLOP/s (the library's product of the same operands:
 // 171 us), bound by the tensor cores with the operands' way from L2 (32 KB a CTA for 512 clocks of MMA) as close
-// behind; 200704 x 1024 x 256 with relu and both z and y written 155 us, 0.88 of the copy rate; cluster kernel
-// 1 x 16384 x 4096 23 us, 0.86 of the copy rate, 1 x 4096 x 4096 8 us.
+// behind; 200704 x 1024 x 256 with relu and both z and y written 156 to 168 us, 0.81 to 0.87 of the copy rate; cluster
+// kernel 1 x 16384 x 4096 23 us, 0.86 of the copy rate, 1 x 4096 x 4096 8 to 9 us.
 #pragma once
 #include "ptx.cuh"
 #include "q8.cuh"

@@ -461,13 +461,14 @@ __device__ __forceinline__ uint32_t fdiv(uint32_t n, const FastDiv& f) {
 // Every kernel is launched with programmatic stream serialization (launch_k): its blocks may be
 // scheduled as the blocks of the kernel before it in the stream exit, and it waits here for that
 // kernel's completion and memory before any global-memory access (without the launch attribute the
-// wait does nothing). No kernel releases its successor earlier (griddepcontrol.launch_dependents):
-// successor blocks waiting on the SMs from a kernel's start slowed the kernels they shared SMs with.
-// (The residual block's kernels do release theirs, once a block's main work is behind it: pdl_release. Of the kernels
-// of one of its calls, those that read nothing of the kernel before them run beside it, "late": they start when that
-// kernel releases them, which is after its own wait, so that everything before the call has completed, and wait for
-// its completion at their end instead of at their entry, so that whatever waits for them has waited for both. Where
-// it matters the choice is made at compile time: as a run-time test it cost a streaming kernel of 16 us two.)
+// wait does nothing). The conv layers' kernels release their successors by ending only: successor
+// blocks waiting on the SMs from a kernel's start slowed the kernels they shared SMs with. The residual
+// block's kernels release theirs (griddepcontrol.launch_dependents, pdl_release) once a block's main
+// work is behind it. Of the kernels of one of its calls, those that read nothing of the kernel before
+// them run beside it, "late": they start when that kernel releases them, which is after its own wait,
+// so that everything before the call has completed, and wait for its completion at their end instead
+// of at their entry, so that whatever waits for them has waited for both. Where it matters the choice
+// is made at compile time: as a run-time test it cost a streaming kernel of 16 us two.
 __device__ __forceinline__ void pdl_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void pdl_entry() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 

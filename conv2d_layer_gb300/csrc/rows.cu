@@ -314,8 +314,8 @@ cudaError_t rows_fwd(const NormArgs& a, cudaStream_t st) {
   if (nv <= 64) ROWS_FWD(32, 2, (V == 16 ? 1 : V == 1 ? 4 : 2));
   if constexpr (V < 16)
     if (nv <= 128) ROWS_FWD(32, 4, (V == 1 ? 4 : 1));
-  // no more threads than a row has vectors, two each: 16384 x 2048 bf16 51 us with 256 threads, 42 with 64; 1536 columns
-  // 46 and 32; 4096 x 5120 33 and 29
+  // vectors: no more threads than a row has of them, two each (16384 x 2048 bf16 51 us with 256 threads, 42 with 64; 1536
+  // columns 46 and 32; 4096 x 5120 33 and 29); rows of single elements take 256 threads from 129 elements on
   if constexpr (V > 1) {
     if constexpr (V == 16)
       if (nv <= 128) ROWS_FWD(64, 2, 1);
@@ -546,8 +546,9 @@ cudaError_t norm_bwd(const NormBwdArgs& a, int sms, int* grid, cudaStream_t st) 
     *grid = static_cast<int>(std::min<long>(a.rows, static_cast<long>(sms) * norm_bwd_resident(TPR))); \
     return launch_k(norm_bwd_kernel<T, V, TPR, U, AHEAD>, dim3(*grid), dim3(nt), smem, st, 1, a); \
   } while (0)
-  // As many threads as the row has vectors (of two a thread where a vector is 16 bytes), so that an SM's threads all
-  // have loads in flight: 32768 x 1024 bf16 91 us with 256 threads, 50 with 64; 16384 x 1000 48 and 28.
+  // Vectors: as many threads as the row has of them (two a thread where a vector is 16 bytes), so that an SM's threads
+  // all have loads in flight: 32768 x 1024 bf16 91 us with 256 threads, 50 with 64; 16384 x 1000 48 and 28. Rows of
+  // single elements take 256 threads from 65 elements on, of which short rows leave most idle.
   if (nv <= 32) NORM_BWD(32, 1, true);
   if constexpr (V == 16) {
     if (nv <= 64) NORM_BWD(64, 1, true);

@@ -18,6 +18,7 @@ import torch
 from . import abi, build
 
 GROUP = 32  # columns of an 8-bit tensor that share a scale, when not a whole row (0)
+# gelu is the tanh form, z/2 (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))): torch's gelu(approximate="tanh"), not its default
 ACTS = {"identity": abi.ACT_IDENTITY, "relu": abi.ACT_RELU, "tanh": abi.ACT_TANH, "sigmoid": abi.ACT_SIGMOID,
         "gelu": abi.ACT_GELU, "silu": abi.ACT_SILU}
 _SAVES = {"none": 0, "full": 1, "q8": 2}
@@ -101,7 +102,8 @@ def _act(act):
 # ------------------------------------------------------------------ 8-bit checkpoints
 @_streamed
 def q8_encode(x, group=GROUP, out=None):
-    """x [rows, cols] (fp32, bf16, fp16) in 8 bits, with one scale for `group` columns (32, or 0: a row)."""
+    """x [rows, cols] (fp32, bf16, fp16) in 8 bits, with one scale for `group` columns (32, or 0: a row). out: an output
+    Q8, whose group then counts."""
     r = _binding().q8_encode(x, group, out)
     return Q8(r[0], r[1], group) if r is not None else out
 
@@ -118,7 +120,7 @@ def rms_norm_fwd(x, gamma, eps=1e-6, residual=None, y=True, group=None, h=None, 
     """h = x + residual; y = gamma * h / sqrt(mean(h^2) + eps), row by row.
 
     y: True (allocate), False (none) or an output tensor. group: None, or the group of an 8-bit form of y
-    (32, or 0: a row); q8: an output Q8 for it. h: output for x + residual (may be x or residual itself).
+    (32, or 0: a row); q8: an output Q8 for it, whose group then counts. h: output for x + residual (may be x or residual itself).
     Returns RmsNorm(h, y, q8, inv_rms); h and inv_rms are what rms_norm_bwd takes."""
     h, y, q, scale, inv_rms = _binding().rms_norm_fwd(x, gamma, eps, residual, y, group, h, q8, inv_rms)
     return RmsNorm(h, y, q8 if q is None else Q8(q, scale, group), inv_rms)
@@ -134,7 +136,8 @@ def rms_norm_bwd(h, gamma, inv_rms, dy, dh=None, dx=None, dgamma=None, need_dx=T
 # ------------------------------------------------------------------ dense layer
 @_streamed
 def dense_fwd(x, w, bias=None, act="identity", residual=None, save="none", dtype=None, y=None, pre_act=None):
-    """y = act(x w^T + bias) + residual; x [M, K], w [N, K], residual and y [M, N], bias [N] fp32.
+    """y = act(x w^T + bias) + residual; x [M, K], w [N, K], residual and y [M, N], bias [N] fp32. act: one of ACTS
+    (gelu is the tanh form).
 
     dtype (bf16 or fp16) is the type of y, residual and the operands that are not Q8; it is x's (or w's) where
     those are not Q8. Two Q8 operands with one scale a row run on the 8-bit tensor cores, other Q8 operands are
