@@ -246,7 +246,9 @@ int conv2d_q8_decode(int64_t rows, int32_t cols, const conv2d_mat* q8, const con
  *                h may be the same buffer as x or as residual.
  *   q8           E4M3 form of y, from the unrounded y (see conv2d_q8_encode)
  *   inv_rms [rows]  s, for conv2d_rms_norm_bwd
- * y, q8 and inv_rms may be NULL; one of y and q8 is not. */
+ * y, q8 and inv_rms may be NULL; one of y and q8 is not. The squares are
+ * summed in fp32: where that sum passes 3.4e38 (a root mean square of
+ * 1.8e19 / sqrt(cols) and more), s and the row's finite y become 0. */
 int conv2d_rms_norm_fwd(int64_t rows, int32_t cols, float eps, const conv2d_mat* x, const conv2d_mat* residual,
                         const float* gamma, const conv2d_mat* h, const conv2d_mat* y, const conv2d_mat* q8,
                         float* inv_rms, void* stream);
