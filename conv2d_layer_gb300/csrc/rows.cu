@@ -1,7 +1,6 @@
-// rows.cu - kernels over rows of features: RMS norm with the residual's
-// addition and its backward, 8-bit checkpoints (encode, decode), the backward
-// through a dense layer's activation, and the column sums and joins behind
-// them. All are bound by memory: each reads its inputs once and writes its
+// rows.cu - kernels over rows of features: 8-bit checkpoints (encode, decode),
+// the backward through a dense layer's activation, and the column sums and
+// joins behind it and the norms. All are bound by memory: each reads its inputs once and writes its
 // outputs once, in accesses of 32 bytes (a sector) a thread where the rows
 // start on such boundaries, of 16 bytes where they start on those, element by
 // element (V = 1) otherwise.
@@ -15,570 +14,10 @@
 #include "kernels.h"
 #include "q8.cuh"
 #include "rows.h"
+#include "rows_norm.cuh"
 
 namespace c2d {
 namespace {
-
-constexpr long kMaxGridX = 0x7fffffffL;
-
-__device__ __forceinline__ float warp_sum(float v) {
-#pragma unroll
-  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
-}
-
-// Sum (or maximum of magnitude bits) over the TPR threads of a row; red: one word per warp. Every thread
-// of the row gets the result, formed in the same order by all.
-template <int TPR>
-__device__ __forceinline__ float row_sum(float v, float* red) {
-  v = warp_sum(v);
-  if constexpr (TPR > 32) {
-    const int warp = threadIdx.x >> 5;
-    __syncthreads();  // the last use of red is over
-    if ((threadIdx.x & 31) == 0) red[warp] = v;
-    __syncthreads();
-    v = 0.f;
-#pragma unroll
-    for (int i = 0; i < TPR / 32; ++i) v += red[i];
-  }
-  return v;
-}
-template <int TPR>
-__device__ __forceinline__ uint32_t row_max(uint32_t v, uint32_t* red) {
-  v = __reduce_max_sync(0xffffffffu, v);
-  if constexpr (TPR > 32) {
-    const int warp = threadIdx.x >> 5;
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) red[warp] = v;
-    __syncthreads();
-    v = 0u;
-#pragma unroll
-    for (int i = 0; i < TPR / 32; ++i) v = max(v, red[i]);
-  }
-  return v;
-}
-
-struct NormArgs {
-  const void *x, *r;
-  const float* gamma;
-  void *h, *y;
-  uint8_t *q, *qs;
-  float* inv;
-  long ldx, ldr, ldh, ldy, ldq;
-  long rows;
-  int cols, ng;  // ng: scale bytes a row
-  int group;     // 32 or 0 (whole row)
-  float eps;
-};
-
-// RMS norm forward (NORM) or 8-bit encode (!NORM): TPR threads a row, a block of them or (TPR = 32) eight warps. Rows are
-// held in registers between their sum of squares and their output, U vectors a thread, so memory is passed once;
-// U = 0 is the form for rows longer than that, which reads the row again for each phase (from L2, mostly). NR
-// rows are in flight at once where a row is a vector or two a thread (one row of 512 bytes a warp left a
-// 200704 x 256 encode at 41 us). Threads hold neighbouring vectors, so a group of 32 columns lies in 32 / V
-// neighbouring lanes and its maximum is found by shuffles. Bound by memory: 8192 x 4096 bf16 with the residual, y
-// and its 8-bit form moves 303 MB in 47 us, 0.95 of the measured copy rate.
-template <typename T, int V, int TPR, int U, int NR, bool NORM>
-__global__ void __launch_bounds__(TPR == 32 ? 256 : TPR) rows_fwd_kernel(const NormArgs a) {
-  pdl_entry();
-  constexpr int RPB = TPR == 32 ? 8 : 1;  // groups of NR rows per block
-  static_assert(U > 0 || NR == 1, "one row at a time where it is read again");
-  constexpr int UC = U > 0 ? U : 1;
-  __shared__ float red[32];
-  const int t = RPB > 1 ? static_cast<int>(threadIdx.x) & 31 : static_cast<int>(threadIdx.x);
-  const long row0 = (static_cast<long>(blockIdx.x) * RPB + (RPB > 1 ? threadIdx.x >> 5 : 0)) * NR;
-  if (row0 >= a.rows) return;  // whole warps; rows that use block barriers are whole blocks
-  const int nr = static_cast<int>(min(a.rows - row0, static_cast<long>(NR)));
-  const int nv = (a.cols + V - 1) / V;
-  const int nu = U > 0 ? U : (nv + TPR - 1) / TPR;  // vectors a thread
-  const T* xb = static_cast<const T*>(a.x) + row0 * a.ldx;
-  const T* rb = static_cast<const T*>(a.r) + row0 * a.ldr;
-  T* hb = static_cast<T*>(a.h) + row0 * a.ldh;
-
-  float v[NR][UC][V];
-  auto widen = [](const T (&e)[V], float (&o)[V]) {
-#pragma unroll
-    for (int k = 0; k < V; ++k) o[k] = to_f(e[k]);
-  };
-  // x + r as stored (h is written); zeros past the end
-  auto load_all = [&](int u0, int n) {
-    T e[NR][UC][V], f[NR][UC][V];
-#pragma unroll
-    for (int i = 0; i < NR; ++i)
-#pragma unroll
-      for (int u = 0; u < UC; ++u) {
-        const int c = ((u0 + u) * TPR + t);
-        if (i < nr && c < nv && u < n) {
-          ld_vec<T, V>(xb + i * a.ldx + static_cast<long>(c) * V, e[i][u]);
-          if (a.r) ld_vec<T, V>(rb + i * a.ldr + static_cast<long>(c) * V, f[i][u]);
-        } else {
-#pragma unroll
-          for (int k = 0; k < V; ++k) e[i][u][k] = f[i][u][k] = from_f<T>(0.f);
-        }
-      }
-#pragma unroll
-    for (int i = 0; i < NR; ++i)
-#pragma unroll
-      for (int u = 0; u < UC; ++u) {
-        const int c = ((u0 + u) * TPR + t);
-        if (a.r) {
-#pragma unroll
-          for (int k = 0; k < V; ++k) e[i][u][k] = from_f<T>(to_f(e[i][u][k]) + to_f(f[i][u][k]));
-          if (i < nr && c < nv && u < n) st_vec<T, V>(hb + i * a.ldh + static_cast<long>(c) * V, e[i][u]);
-        }
-        widen(e[i][u], v[i][u]);
-      }
-  };
-  auto reload = [&](int u) {  // U = 0: this thread's own h (or x) again
-    const int c = u * TPR + t;
-    if (c < nv) {
-      T e[V];
-      ld_vec<T, V>((a.r ? static_cast<const T*>(hb) : xb) + static_cast<long>(c) * V, e);
-      widen(e, v[0][0]);
-    } else {
-#pragma unroll
-      for (int k = 0; k < V; ++k) v[0][0][k] = 0.f;
-    }
-  };
-
-  float inv[NR];
-#pragma unroll
-  for (int i = 0; i < NR; ++i) inv[i] = 1.f;
-  if constexpr (U > 0) load_all(0, UC);
-  if constexpr (NORM) {
-    float ss[NR];
-#pragma unroll
-    for (int i = 0; i < NR; ++i) ss[i] = 0.f;
-    if constexpr (U > 0) {
-#pragma unroll
-      for (int i = 0; i < NR; ++i)
-#pragma unroll
-        for (int u = 0; u < UC; ++u)
-#pragma unroll
-          for (int k = 0; k < V; ++k) ss[i] = fmaf(v[i][u][k], v[i][u][k], ss[i]);
-    } else {
-      for (int u = 0; u < nu; ++u) {
-        load_all(u, 1);
-#pragma unroll
-        for (int k = 0; k < V; ++k) ss[0] = fmaf(v[0][0][k], v[0][0][k], ss[0]);
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < NR; ++i) {
-      inv[i] = 1.f / sqrtf(row_sum<TPR>(ss[i], red) / static_cast<float>(a.cols) + a.eps);
-      if (t == 0 && i < nr && a.inv) a.inv[row0 + i] = inv[i];
-    }
-  }
-  pdl_release();
-  // y = gamma h s of vector u, in place, for all NR rows (U = 0: of the one vector at hand)
-  auto scale = [&](int u, int slot) {
-    const int c = u * TPR + t;
-    if (!NORM || c >= nv) return;
-    const float* gp = a.gamma + static_cast<long>(c) * V;
-    float g[V];
-    if constexpr (V >= 4) {
-#pragma unroll
-      for (int k = 0; k < V; k += 4) *reinterpret_cast<float4*>(g + k) = *reinterpret_cast<const float4*>(gp + k);
-    } else {
-      g[0] = gp[0];
-    }
-#pragma unroll
-    for (int i = 0; i < NR; ++i)
-#pragma unroll
-      for (int k = 0; k < V; ++k) v[i][slot][k] = v[i][slot][k] * inv[i] * g[k];
-  };
-  // Largest magnitude's bits; fmaxf passes NaN over, and infinities are looked for only where one shows.
-  auto absmax = [&](const float (&o)[V]) {
-    float m = 0.f;
-#pragma unroll
-    for (int k = 0; k < V; ++k) m = fmaxf(m, fabsf(o[k]));
-    return __float_as_uint(m);
-  };
-  auto absmax_finite = [&](const float (&o)[V]) {
-    uint32_t m = 0u;
-#pragma unroll
-    for (int k = 0; k < V; ++k) m = max(m, finite_bits(o[k]));
-    return m;
-  };
-  constexpr uint32_t kInf = 0x7f800000u;
-  uint32_t rowbyte[NR];
-  bool rowfinite[NR];
-  if (a.q && a.group == 0) {
-    if constexpr (U > 0) {
-#pragma unroll
-      for (int u = 0; u < UC; ++u) scale(u, u);
-    }
-#pragma unroll
-    for (int i = 0; i < NR; ++i) {
-      uint32_t m = 0u;
-      if constexpr (U > 0) {
-#pragma unroll
-        for (int u = 0; u < UC; ++u) m = max(m, absmax(v[i][u]));
-      } else {
-        for (int u = 0; u < nu; ++u) {
-          reload(u);
-          scale(u, 0);
-          m = max(m, absmax(v[0][0]));
-        }
-      }
-      m = row_max<TPR>(m, reinterpret_cast<uint32_t*>(red));
-      rowfinite[i] = m != kInf;
-      if (m == kInf) {  // the same for the whole row
-        m = 0u;
-        if constexpr (U > 0) {
-#pragma unroll
-          for (int u = 0; u < UC; ++u) m = max(m, absmax_finite(v[i][u]));
-        } else {
-          for (int u = 0; u < nu; ++u) {
-            reload(u);
-            scale(u, 0);
-            m = max(m, absmax_finite(v[0][0]));
-          }
-        }
-        m = row_max<TPR>(m, reinterpret_cast<uint32_t*>(red));
-      }
-      rowbyte[i] = q8_scale_byte(m);
-      if (t == 0 && i < nr) a.qs[(row0 + i) * a.ng] = static_cast<uint8_t>(rowbyte[i]);
-    }
-  }
-  auto finish = [&](int u, int slot) {
-    const int c = u * TPR + t;
-#pragma unroll
-    for (int i = 0; i < NR; ++i) {
-      const bool on = i < nr && c < nv;
-      float(&o)[V] = v[i][slot];
-      if (a.y && on) {
-        T e[V];
-#pragma unroll
-        for (int k = 0; k < V; ++k) e[k] = from_f<T>(o[k]);
-        st_vec<T, V>(static_cast<T*>(a.y) + (row0 + i) * a.ldy + static_cast<long>(c) * V, e);
-      }
-      if (a.q) {
-        uint32_t byte = rowbyte[i];
-        bool finite = rowfinite[i];
-        if (a.group != 0) {
-          auto group_max = [](uint32_t m) {
-            if constexpr (V == 1) {  // the group is the warp
-              return __reduce_max_sync(0xffffffffu, m);
-            } else {
-#pragma unroll
-              for (int s = 1; s < kQ8Group / V; s <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, s));
-              return m;
-            }
-          };
-          uint32_t m = group_max(absmax(o));
-          finite = true;
-          if (__any_sync(0xffffffffu, m == kInf)) {
-            finite = false;
-            m = group_max(absmax_finite(o));
-          }
-          byte = q8_scale_byte(m);
-          if (on && (t & (kQ8Group / V - 1)) == 0)
-            a.qs[(row0 + i) * a.ng + c / (kQ8Group / V)] = static_cast<uint8_t>(byte);
-        }
-        if (on) q8_store<V>(a.q + (row0 + i) * a.ldq + static_cast<long>(c) * V, o, q8_inv_scale(byte), finite);
-      }
-    }
-  };
-  if constexpr (U > 0) {
-#pragma unroll
-    for (int u = 0; u < UC; ++u) {
-      if (!(a.q && a.group == 0)) scale(u, u);
-      finish(u, u);
-    }
-  } else {
-    for (int u = 0; u < nu; ++u) {
-      if constexpr (NORM) {
-        reload(u);
-        scale(u, 0);
-      } else {
-        reload(u);
-      }
-      finish(u, 0);
-    }
-  }
-}
-
-template <typename T, int V, bool NORM>
-cudaError_t rows_fwd(const NormArgs& a, cudaStream_t st) {
-  const int nv = (a.cols + V - 1) / V;
-#define ROWS_FWD(TPR, U, NR)                                                                                        \
-  do {                                                                                                              \
-    constexpr int nt = (TPR) == 32 ? 256 : (TPR), rpb = nt / (TPR) * (NR);                                         \
-    return launch_k(rows_fwd_kernel<T, V, TPR, U, NR, NORM>, dim3(static_cast<unsigned>((a.rows + rpb - 1) / rpb)), \
-                    dim3(nt), 0, st, 1, a);                                                                         \
-  } while (0)
-  // 16 to 32 values a thread where a warp takes a row (8 to 16 when they are loaded one by one); long rows are
-  // spread over 256 or 512 threads
-  if (nv <= 32) ROWS_FWD(32, 1, (V == 16 ? 2 : V == 1 ? 8 : 4));
-  if (nv <= 64) ROWS_FWD(32, 2, (V == 16 ? 1 : V == 1 ? 4 : 2));
-  if constexpr (V < 16)
-    if (nv <= 128) ROWS_FWD(32, 4, (V == 1 ? 4 : 1));
-  // vectors: no more threads than a row has of them, two each (16384 x 2048 bf16 51 us with 256 threads, 42 with 64; 1536
-  // columns 46 and 32; 4096 x 5120 33 and 29); rows of single elements take 256 threads from 129 elements on
-  if constexpr (V > 1) {
-    if constexpr (V == 16)
-      if (nv <= 128) ROWS_FWD(64, 2, 1);
-    if (nv <= 192) ROWS_FWD(96, 2, 1);
-  }
-  if (nv <= 256) ROWS_FWD(256, 1, 1);
-  if constexpr (V > 1) {
-    if (nv <= 320) ROWS_FWD(160, 2, 1);
-    if (nv <= 384) ROWS_FWD(192, 2, 1);
-  }
-  if (nv <= 512) ROWS_FWD(256, 2, 1);
-  if constexpr (V == 16) {
-    if (nv <= 1024) ROWS_FWD(512, 2, 1);
-  } else {
-    if (nv <= 1024) ROWS_FWD(256, 4, 1);
-    if (nv <= 2048) ROWS_FWD(512, 4, 1);
-  }
-  if constexpr (V == 1) {  // single elements take few registers
-    if (nv <= 4096) ROWS_FWD(512, 8, 1);
-    if (nv <= 8192) ROWS_FWD(1024, 8, 1);
-    if (nv <= 16384) ROWS_FWD(1024, 16, 1);
-  }
-  ROWS_FWD(1024, 0, 1);
-#undef ROWS_FWD
-}
-
-// ------------------------------------------------------------------ RMS norm backward
-struct NormBwdArgs {
-  const void *h, *dy, *dh;
-  void* dx;
-  const float *gamma, *inv;
-  float* part;  // [gridDim.x][cols], null: no dgamma
-  long ldh, lddy, lddh, lddx;
-  long rows;
-  int cols;
-};
-
-// Blocks that an SM holds and is given, by the threads of a row (32: blocks of 256): about 512 threads of up to 128
-// registers. A second wave of larger blocks only adds partial sums (8192 x 8192 bf16: 100 us, 91 without).
-constexpr int norm_bwd_resident(int tpr) {
-  return tpr > 256 ? 1 : tpr == 64 ? 8 : tpr == 128 ? 4 : tpr == 192 ? 3 : 2;
-}
-
-// Blocks walk the rows (row = block, block + grid, ...), TPR threads a row, and keep the sums of dgamma for their
-// columns in registers. AHEAD: gamma too, and the vectors of the next row are in flight while this one is reduced;
-// without it (rows whose values take the registers) gamma and dh are read where they are needed. U = 0: rows
-// longer than the registers hold; each row is read twice and dgamma's sums live in this block's row of `part`.
-// Bound by memory: 8192 x 4096 bf16 with dh moves 268 MB in 46 us, 0.85 of the copy rate (64 us with one block of
-// 136 registers a thread an SM, before the registers were held to two).
-template <typename T, int V, int TPR, int U, bool AHEAD>
-__global__ void __launch_bounds__(TPR == 32 ? 256 : TPR, norm_bwd_resident(TPR)) norm_bwd_kernel(const NormBwdArgs a) {
-  pdl_entry();
-  constexpr int RPB = TPR == 32 ? 8 : 1;
-  constexpr int UC = U > 0 ? U : 1;
-  extern __shared__ float sums[];  // RPB > 1 with dgamma: [RPB][cols]
-  __shared__ float red[32];
-  const int t = RPB > 1 ? static_cast<int>(threadIdx.x) & 31 : static_cast<int>(threadIdx.x);
-  const int wr = RPB > 1 ? static_cast<int>(threadIdx.x >> 5) : 0;
-  const int nv = (a.cols + V - 1) / V;
-  const float invD = 1.f / static_cast<float>(a.cols);
-  const T* hb = static_cast<const T*>(a.h);
-  const T* db = static_cast<const T*>(a.dy);
-  const T* sb = static_cast<const T*>(a.dh);
-  T* xb = static_cast<T*>(a.dx);
-  const long step = static_cast<long>(gridDim.x) * RPB;
-  const long row0 = static_cast<long>(blockIdx.x) * RPB + wr;
-
-  if constexpr (U > 0) {
-    float g[AHEAD ? UC : 1][V], acc[UC][V];
-    auto load_gamma = [&](int u, float (&o)[V]) {
-      const int c = (u * TPR + t) * V;
-#pragma unroll
-      for (int k = 0; k < V; ++k) o[k] = 0.f;
-      if (c >= a.cols) return;
-      if constexpr (V >= 4) {
-#pragma unroll
-        for (int k = 0; k < V; k += 4) *reinterpret_cast<float4*>(o + k) = *reinterpret_cast<const float4*>(a.gamma + c + k);
-      } else {
-        o[0] = a.gamma[c];
-      }
-    };
-#pragma unroll
-    for (int u = 0; u < UC; ++u) {
-      if constexpr (AHEAD) load_gamma(u, g[u]);
-#pragma unroll
-      for (int k = 0; k < V; ++k) acc[u][k] = 0.f;
-    }
-    T h[UC][V], d[UC][V], s[AHEAD ? UC : 1][V];
-    float inv = 0.f;
-    auto fetch = [&](long row) {
-      if (row < a.rows) inv = a.inv[row];
-#pragma unroll
-      for (int u = 0; u < UC; ++u) {
-        const int i = u * TPR + t;
-        if (row < a.rows && i < nv) {
-          ld_vec<T, V>(hb + row * a.ldh + static_cast<long>(i) * V, h[u]);
-          ld_vec<T, V>(db + row * a.lddy + static_cast<long>(i) * V, d[u]);
-          if constexpr (AHEAD)
-            if (sb && xb) ld_vec<T, V>(sb + row * a.lddh + static_cast<long>(i) * V, s[u]);
-        } else {
-#pragma unroll
-          for (int k = 0; k < V; ++k) h[u][k] = d[u][k] = from_f<T>(0.f);
-        }
-      }
-    };
-    if constexpr (AHEAD) fetch(row0);
-    for (long row = row0; row < a.rows; row += step) {
-      if constexpr (!AHEAD) fetch(row);
-      float hf[UC][V], df[UC][V];
-      T sk[AHEAD ? UC : 1][V];
-      const float iv = inv;
-      float dot = 0.f;
-#pragma unroll
-      for (int u = 0; u < UC; ++u) {
-        float gu[V];
-        if constexpr (!AHEAD) load_gamma(u, gu);
-#pragma unroll
-        for (int k = 0; k < V; ++k) {
-          hf[u][k] = to_f(h[u][k]) * iv;  // the normalised value
-          df[u][k] = to_f(d[u][k]);
-          if constexpr (AHEAD) sk[u][k] = s[u][k];
-          acc[u][k] = fmaf(df[u][k], hf[u][k], acc[u][k]);
-          df[u][k] *= AHEAD ? g[AHEAD ? u : 0][k] : gu[k];
-          dot = fmaf(df[u][k], hf[u][k], dot);
-        }
-      }
-      if constexpr (AHEAD) fetch(row + step);
-      if (xb) {
-        dot = row_sum<TPR>(dot, red) * invD;
-#pragma unroll
-        for (int u = 0; u < UC; ++u) {
-          const int i = u * TPR + t;
-          if (i < nv) {
-            T o[V], sv[V];
-            if constexpr (!AHEAD)
-              if (sb) ld_vec<T, V>(sb + row * a.lddh + static_cast<long>(i) * V, sv);
-#pragma unroll
-            for (int k = 0; k < V; ++k) {
-              float v = iv * fmaf(-hf[u][k], dot, df[u][k]);
-              if (sb) v += to_f(AHEAD ? sk[AHEAD ? u : 0][k] : sv[k]);
-              o[k] = from_f<T>(v);
-            }
-            st_vec<T, V>(xb + row * a.lddx + static_cast<long>(i) * V, o);
-          }
-        }
-      }
-    }
-    pdl_release();
-    if (!a.part) return;
-    float* part = a.part + static_cast<long>(blockIdx.x) * a.cols;
-    if constexpr (RPB > 1) {
-#pragma unroll
-      for (int u = 0; u < UC; ++u)
-#pragma unroll
-        for (int k = 0; k < V; ++k) {
-          const int c = (u * TPR + t) * V + k;
-          if (c < a.cols) sums[wr * a.cols + c] = acc[u][k];
-        }
-      __syncthreads();
-      for (int c = threadIdx.x; c < a.cols; c += 256) {
-        float v = 0.f;
-#pragma unroll
-        for (int w = 0; w < RPB; ++w) v += sums[w * a.cols + c];
-        part[c] = v;
-      }
-    } else {
-#pragma unroll
-      for (int u = 0; u < UC; ++u)
-#pragma unroll
-        for (int k = 0; k < V; ++k) {
-          const int c = (u * TPR + t) * V + k;
-          if (c < a.cols) part[c] = acc[u][k];
-        }
-    }
-  } else {
-    float* part = a.part ? a.part + static_cast<long>(blockIdx.x) * a.cols : nullptr;
-    if (part)
-      for (int i = t; i < nv; i += TPR)
-        for (int k = 0; k < V; ++k) part[static_cast<long>(i) * V + k] = 0.f;
-    for (long row = row0; row < a.rows; row += step) {
-      const float iv = a.inv[row];
-      float dot = 0.f;
-      for (int i = t; i < nv; i += TPR) {
-        T h[V], d[V];
-        ld_vec<T, V>(hb + row * a.ldh + static_cast<long>(i) * V, h);
-        ld_vec<T, V>(db + row * a.lddy + static_cast<long>(i) * V, d);
-#pragma unroll
-        for (int k = 0; k < V; ++k) {
-          const long c = static_cast<long>(i) * V + k;
-          const float hn = to_f(h[k]) * iv, dv = to_f(d[k]);
-          if (part) part[c] = fmaf(dv, hn, part[c]);
-          dot = fmaf(dv * a.gamma[c], hn, dot);
-        }
-      }
-      if (!xb) continue;
-      dot = row_sum<TPR>(dot, red) * invD;
-      for (int i = t; i < nv; i += TPR) {
-        T h[V], d[V], s[V], o[V];
-        ld_vec<T, V>(hb + row * a.ldh + static_cast<long>(i) * V, h);
-        ld_vec<T, V>(db + row * a.lddy + static_cast<long>(i) * V, d);
-        if (sb) ld_vec<T, V>(sb + row * a.lddh + static_cast<long>(i) * V, s);
-#pragma unroll
-        for (int k = 0; k < V; ++k) {
-          const long c = static_cast<long>(i) * V + k;
-          float v = iv * fmaf(-to_f(h[k]) * iv, dot, to_f(d[k]) * a.gamma[c]);
-          if (sb) v += to_f(s[k]);
-          o[k] = from_f<T>(v);
-        }
-        st_vec<T, V>(xb + row * a.lddx + static_cast<long>(i) * V, o);
-      }
-    }
-  }
-}
-
-// The most blocks that the backward of rows of this length is launched with (norm_bwd's choices below).
-long norm_bwd_blocks(int64_t rows, int cols, int sms) {
-  return std::min<long>(rows, static_cast<long>(sms) * (cols <= 64 * 16 ? 8 : cols <= 128 * 16 ? 4 : cols <= 192 * 16 ? 3 : 2));
-}
-
-// grid: blocks launched, one row of partial sums each.
-template <typename T, int V>
-cudaError_t norm_bwd(const NormBwdArgs& a, int sms, int* grid, cudaStream_t st) {
-  const int nv = (a.cols + V - 1) / V;
-#define NORM_BWD(TPR, U, AHEAD)                                                                   \
-  do {                                                                                            \
-    constexpr int nt = (TPR) == 32 ? 256 : (TPR);                                                 \
-    const size_t smem = nt > (TPR) && a.part ? static_cast<size_t>(nt / (TPR)) * a.cols * 4 : 0;  \
-    *grid = static_cast<int>(std::min<long>(a.rows, static_cast<long>(sms) * norm_bwd_resident(TPR))); \
-    return launch_k(norm_bwd_kernel<T, V, TPR, U, AHEAD>, dim3(*grid), dim3(nt), smem, st, 1, a); \
-  } while (0)
-  // Vectors: as many threads as the row has of them (two a thread where a vector is 16 bytes), so that an SM's threads
-  // all have loads in flight: 32768 x 1024 bf16 91 us with 256 threads, 50 with 64; 16384 x 1000 48 and 28. Rows of
-  // single elements take 256 threads from 65 elements on, of which short rows leave most idle.
-  if (nv <= 32) NORM_BWD(32, 1, true);
-  if constexpr (V == 16) {
-    if (nv <= 64) NORM_BWD(64, 1, true);
-    if (nv <= 128) NORM_BWD(128, 1, true);
-    if (nv <= 256) NORM_BWD(256, 1, true);
-    if (nv <= 320) NORM_BWD(320, 1, true);
-    if (nv <= 512) NORM_BWD(512, 1, true);
-    if (nv <= 1024) NORM_BWD(512, 2, false);
-  } else if constexpr (V > 1) {
-    if (nv <= 64) NORM_BWD(32, 2, true);
-    if (nv <= 128) NORM_BWD(64, 2, true);
-    if (nv <= 256) NORM_BWD(128, 2, true);
-    if (nv <= 384) NORM_BWD(192, 2, true);
-    if (nv <= 512) NORM_BWD(256, 2, true);
-    if (nv <= 768) NORM_BWD(384, 2, true);
-    if (nv <= 1024) NORM_BWD(512, 2, true);
-    if (nv <= 2048) NORM_BWD(512, 4, false);
-  } else {
-    if (nv <= 64) NORM_BWD(32, 2, true);
-    if (nv <= 256) NORM_BWD(256, 1, true);
-    if (nv <= 512) NORM_BWD(256, 2, true);
-    if (nv <= 1024) NORM_BWD(512, 2, true);
-    if (nv <= 2048) NORM_BWD(512, 4, true);
-    if (nv <= 4096) NORM_BWD(1024, 4, true);
-    if (nv <= 8192) NORM_BWD(1024, 8, true);
-    if (nv <= 16384) NORM_BWD(1024, 16, false);
-  }
-  NORM_BWD(1024, 0, false);
-#undef NORM_BWD
-}
 
 // ------------------------------------------------------------------ 8 bits, 16-bit types in whole groups
 // Encode (ENC) or decode of rows of whole 32-column groups: two threads a group, 16 values each, two groups of a
@@ -815,11 +254,6 @@ __global__ void __launch_bounds__(256) to_rows_ragged_kernel(const void* x, long
     }
   }
   if (LATE) pdl_entry();
-}
-
-// Rows that start on boundaries of a vector of V elements of es bytes (the base at least on 16 bytes by contract).
-bool vec_ok(const void* p, long ld, int es, int V) {
-  return reinterpret_cast<uintptr_t>(p) % (V * es > 16 ? 32 : 16) == 0 && ld % V == 0;
 }
 
 template <typename T, bool Q, int W>
@@ -1173,66 +607,6 @@ cudaError_t launch_zero_rows(long rows, int cols, int type, void* out, long ld, 
 // ------------------------------------------------------------------ C entry points
 using namespace c2d;
 
-namespace {
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-bool is_float(int type) { return type == CONV2D_FP32 || type == CONV2D_BF16 || type == CONV2D_FP16; }
-
-// A matrix argument: data present and aligned, ld at least cols, E4M3 with a known group and scales.
-int check_mat(const conv2d_mat* m, int cols) {
-  if (!m || !m->data || !aligned16(m->data)) return CONV2D_ERR_INVALID_ARG;
-  if (m->ld != 0 && m->ld < cols) return CONV2D_ERR_INVALID_ARG;
-  if (m->type == CONV2D_E4M3) {
-    if (!m->scale || (m->group != 0 && m->group != kQ8Group)) return CONV2D_ERR_INVALID_ARG;
-  } else if (!is_float(m->type)) {
-    return CONV2D_ERR_INVALID_ARG;
-  }
-  return CONV2D_OK;
-}
-long ld_of(const conv2d_mat* m, int cols) { return m->ld ? m->ld : cols; }
-
-// rows x cols within what the kernels index: 2^31 - 1 rows (one block each), byte offsets in 62 bits.
-int check_rows(int64_t rows, int32_t cols) {
-  if (rows < 0 || cols < 1) return CONV2D_ERR_INVALID_ARG;
-  if (rows > kMaxGridX || cols > (1 << 28)) return CONV2D_ERR_UNSUPPORTED;
-  return CONV2D_OK;
-}
-
-template <bool NORM>
-bool rows_fwd_ok(const NormArgs& a, int es, int V) {
-  return a.cols % V == 0 && vec_ok(a.x, a.ldx, es, V) && (!a.r || (vec_ok(a.r, a.ldr, es, V) && vec_ok(a.h, a.ldh, es, V))) &&
-         (!a.y || vec_ok(a.y, a.ldy, es, V)) && (!a.q || vec_ok(a.q, a.ldq, 1, V));
-}
-template <typename T, bool NORM>
-cudaError_t rows_fwd_vec(const NormArgs& a, cudaStream_t st) {
-  constexpr int es = sizeof(T);
-  // at 16 vectors of 32 bytes and fewer half of the lanes would idle (200704 x 256 to 8 bits too: 93 us, now 88)
-  if (a.cols > 16 * 32 / es && rows_fwd_ok<NORM>(a, es, 32 / es)) return rows_fwd<T, 32 / es, NORM>(a, st);
-  if (rows_fwd_ok<NORM>(a, es, 16 / es)) return rows_fwd<T, 16 / es, NORM>(a, st);
-  return rows_fwd<T, 1, NORM>(a, st);
-}
-template <bool NORM>
-cudaError_t rows_fwd_any(const NormArgs& a, int type, cudaStream_t st) {
-  if (type == CONV2D_BF16) return rows_fwd_vec<__nv_bfloat16, NORM>(a, st);
-  if (type == CONV2D_FP16) return rows_fwd_vec<__half, NORM>(a, st);
-  return rows_fwd_vec<float, NORM>(a, st);
-}
-
-template <typename T>
-cudaError_t norm_bwd_vec(const NormBwdArgs& a, int sms, int* grid, cudaStream_t st) {
-  constexpr int es = sizeof(T);
-  auto ok = [&](int V) {
-    return a.cols % V == 0 && vec_ok(a.h, a.ldh, es, V) && vec_ok(a.dy, a.lddy, es, V) &&
-           (!a.dx || vec_ok(a.dx, a.lddx, es, V)) && (!a.dh || vec_ok(a.dh, a.lddh, es, V));
-  };
-  if constexpr (es == 2)  // fp32 rows of 32-byte vectors take more registers than they win
-    if (a.cols > 16 * 32 / es && ok(32 / es)) return norm_bwd<T, 32 / es>(a, sms, grid, st);
-  if (ok(16 / es)) return norm_bwd<T, 16 / es>(a, sms, grid, st);
-  return norm_bwd<T, 1>(a, sms, grid, st);
-}
-
-}  // namespace
-
 extern "C" {
 
 int conv2d_q8_encode(int64_t rows, int32_t cols, const conv2d_mat* x, const conv2d_mat* q8, void* stream) {
@@ -1276,108 +650,6 @@ int conv2d_q8_decode(int64_t rows, int32_t cols, const conv2d_mat* q8, const con
   if ((rc = device_info(&dev))) return rc;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   LAUNCH("q8_decode", st, launch_to_rows(*q8, rows, cols, x->type, x->data, x->ld, 0, st));
-  return CONV2D_OK;
-}
-
-int conv2d_rms_norm_fwd(int64_t rows, int32_t cols, float eps, const conv2d_mat* x, const conv2d_mat* residual,
-                        const float* gamma, const conv2d_mat* h, const conv2d_mat* y, const conv2d_mat* q8,
-                        float* inv_rms, void* stream) {
-  int rc = check_rows(rows, cols);
-  if (rc) return rc;
-  if (!(eps > 0.f) || !std::isfinite(eps) || !gamma || !aligned16(gamma) || !aligned16(inv_rms))
-    return CONV2D_ERR_INVALID_ARG;
-  if ((residual == nullptr) != (h == nullptr) || (!y && !q8)) return CONV2D_ERR_INVALID_ARG;
-  if (rows == 0) return CONV2D_OK;
-  if ((rc = check_mat(x, cols))) return rc;
-  if (!is_float(x->type)) return CONV2D_ERR_INVALID_ARG;
-  for (const conv2d_mat* m : {residual, h, y})
-    if (m && ((rc = check_mat(m, cols)) || m->type != x->type)) return CONV2D_ERR_INVALID_ARG;
-  if (q8 && (check_mat(q8, cols) || q8->type != CONV2D_E4M3)) return CONV2D_ERR_INVALID_ARG;
-  DevInfo* dev = nullptr;
-  if ((rc = device_info(&dev))) return rc;
-  NormArgs a = {};
-  a.x = x->data;
-  a.ldx = ld_of(x, cols);
-  if (residual) {
-    a.r = residual->data;
-    a.ldr = ld_of(residual, cols);
-    a.h = h->data;
-    a.ldh = ld_of(h, cols);
-  }
-  a.gamma = gamma;
-  if (y) {
-    a.y = y->data;
-    a.ldy = ld_of(y, cols);
-  }
-  if (q8) {
-    a.q = static_cast<uint8_t*>(q8->data);
-    a.qs = q8->scale;
-    a.ldq = ld_of(q8, cols);
-    a.group = q8->group;
-    a.ng = q8->group ? (cols + kQ8Group - 1) / kQ8Group : 1;
-  }
-  a.inv = inv_rms;
-  a.rows = rows;
-  a.cols = cols;
-  a.eps = eps;
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
-  LAUNCH("rms_norm_fwd", st, rows_fwd_any<true>(a, x->type, st));
-  return CONV2D_OK;
-}
-
-size_t conv2d_rms_norm_bwd_workspace_size(int64_t rows, int32_t cols) {
-  if (check_rows(rows, cols)) return 0;
-  return std::max<size_t>(256, static_cast<size_t>(norm_bwd_blocks(rows, cols, sms_for_sizing())) * cols * 4);
-}
-
-int conv2d_rms_norm_bwd(int64_t rows, int32_t cols, const conv2d_mat* h, const float* gamma, const float* inv_rms,
-                        const conv2d_mat* dy, const conv2d_mat* dh, const conv2d_mat* dx, float* dgamma,
-                        int accumulate, void* ws, size_t ws_bytes, void* stream) {
-  int rc = check_rows(rows, cols);
-  if (rc) return rc;
-  if ((!dx && !dgamma) || !gamma || !aligned16(gamma) || !aligned16(dgamma)) return CONV2D_ERR_INVALID_ARG;
-  DevInfo* dev = nullptr;
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (rows == 0) {
-    if (!dgamma || accumulate) return CONV2D_OK;
-    if ((rc = device_info(&dev))) return rc;
-    LAUNCH("zero", st, launch_zero_rows(1, cols, CONV2D_FP32, dgamma, cols, 0, st));
-    return CONV2D_OK;
-  }
-  if (!inv_rms || !aligned16(inv_rms)) return CONV2D_ERR_INVALID_ARG;
-  if ((rc = check_mat(h, cols)) || (rc = check_mat(dy, cols))) return rc;
-  if (!is_float(h->type) || dy->type != h->type) return CONV2D_ERR_INVALID_ARG;
-  for (const conv2d_mat* m : {dh, dx})
-    if (m && (check_mat(m, cols) || m->type != h->type)) return CONV2D_ERR_INVALID_ARG;
-  if ((rc = device_info(&dev))) return rc;
-  const size_t need = conv2d_rms_norm_bwd_workspace_size(rows, cols);
-  if (dgamma && (!ws || ws_bytes < need || (reinterpret_cast<uintptr_t>(ws) & 255u))) return CONV2D_ERR_WORKSPACE;
-  NormBwdArgs a = {};
-  a.h = h->data;
-  a.ldh = ld_of(h, cols);
-  a.dy = dy->data;
-  a.lddy = ld_of(dy, cols);
-  if (dx) {
-    a.dx = dx->data;
-    a.lddx = ld_of(dx, cols);
-  }
-  if (dh) {
-    a.dh = dh->data;
-    a.lddh = ld_of(dh, cols);
-  }
-  a.gamma = gamma;
-  a.inv = inv_rms;
-  a.part = dgamma ? static_cast<float*>(ws) : nullptr;
-  a.rows = rows;
-  a.cols = cols;
-  int grid = 0;
-  auto run = [&]() -> cudaError_t {
-    if (h->type == CONV2D_BF16) return norm_bwd_vec<__nv_bfloat16>(a, dev->sms, &grid, st);
-    if (h->type == CONV2D_FP16) return norm_bwd_vec<__half>(a, dev->sms, &grid, st);
-    return norm_bwd_vec<float>(a, dev->sms, &grid, st);
-  };
-  LAUNCH("rms_norm_bwd", st, run());
-  if (dgamma) LAUNCH("column_sum", st, launch_column_sum(a.part, grid, cols, dgamma, accumulate, 0, st));
   return CONV2D_OK;
 }
 
