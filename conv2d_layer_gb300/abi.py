@@ -18,6 +18,7 @@ ACT_IDENTITY, ACT_RELU, ACT_TANH, ACT_SIGMOID = 0, 1, 2, 3
 ACT_GELU, ACT_SILU = 4, 5  # dense layers only
 FP32, BF16 = 0, 1
 FP16, E4M3 = 2, 3  # conv2d_mat only
+TILE = -128  # conv2d_mat.group of a scale for 128 rows by 128 columns
 OP_FWD_TRAIN, OP_FWD_INFER, OP_BWD = 0, 1, 2
 
 EXPORTS = (
@@ -27,6 +28,7 @@ EXPORTS = (
     "conv2d_q8_encode", "conv2d_q8_decode", "conv2d_rms_norm_fwd", "conv2d_rms_norm_bwd",
     "conv2d_rms_norm_bwd_workspace_size", "conv2d_dense_fwd", "conv2d_dense_bwd", "conv2d_dense_fwd_workspace_size",
     "conv2d_dense_bwd_workspace_size",
+    "conv2d_layer_norm_fwd", "conv2d_layer_norm_bwd", "conv2d_layer_norm_bwd_workspace_size",
 )
 
 
@@ -89,6 +91,10 @@ def lib():
     L.conv2d_rms_norm_bwd.argtypes = [i64, i32, pm, vp, vp, pm, pm, pm, vp, i32, vp, sz, vp]
     L.conv2d_rms_norm_bwd_workspace_size.argtypes = [i64, i32]
     L.conv2d_rms_norm_bwd_workspace_size.restype = sz
+    L.conv2d_layer_norm_fwd.argtypes = [i64, i32, ctypes.c_float, pm, pm, vp, vp, pm, pm, pm, vp, vp, vp]
+    L.conv2d_layer_norm_bwd.argtypes = [i64, i32, pm, vp, vp, vp, pm, pm, pm, vp, vp, i32, vp, sz, vp]
+    L.conv2d_layer_norm_bwd_workspace_size.argtypes = [i64, i32]
+    L.conv2d_layer_norm_bwd_workspace_size.restype = sz
     L.conv2d_dense_fwd.argtypes = [pn, pm, pm, vp, pm, pm, pm, vp, sz, vp]
     L.conv2d_dense_bwd.argtypes = [pn, pm, pm, pm, pm, pm, pm, vp, vp, sz, vp]
     L.conv2d_dense_fwd_workspace_size.argtypes = [pn, pm, pm]
@@ -203,6 +209,21 @@ def conv2d_rms_norm_bwd_workspace_size(rows, cols):
 def conv2d_rms_norm_bwd(rows, cols, h, gamma, inv_rms, dy, dh, dx, dgamma, accumulate, ws, ws_bytes=None, stream=None):
     return lib().conv2d_rms_norm_bwd(rows, cols, h, _ptr(gamma), _ptr(inv_rms), dy, dh, dx,
                                      _ptr(dgamma), int(accumulate), _ptr(ws), _ws(ws, ws_bytes), _stream(stream))
+
+
+def conv2d_layer_norm_fwd(rows, cols, eps, x, residual, gamma, beta, h, y, q8, mean, inv_std, stream=None):
+    return lib().conv2d_layer_norm_fwd(rows, cols, eps, x, residual, _ptr(gamma), _ptr(beta), h, y, q8, _ptr(mean),
+                                       _ptr(inv_std), _stream(stream))
+
+
+def conv2d_layer_norm_bwd_workspace_size(rows, cols):
+    return int(lib().conv2d_layer_norm_bwd_workspace_size(rows, cols))
+
+
+def conv2d_layer_norm_bwd(rows, cols, h, gamma, mean, inv_std, dy, dh, dx, dgamma, dbeta, accumulate, ws, ws_bytes=None,
+                          stream=None):
+    return lib().conv2d_layer_norm_bwd(rows, cols, h, _ptr(gamma), _ptr(mean), _ptr(inv_std), dy, dh, dx, _ptr(dgamma),
+                                       _ptr(dbeta), int(accumulate), _ptr(ws), _ws(ws, ws_bytes), _stream(stream))
 
 
 def conv2d_dense_fwd_workspace_size(d, x, w):

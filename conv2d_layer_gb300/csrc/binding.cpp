@@ -22,16 +22,20 @@
 
 namespace {
 
-constexpr int64_t kGroup = 32;
+constexpr int64_t kGroup = 32, kWide = 128, kTile = CONV2D_TILE;
 
 // The library's entry points, resolved by init().
 #define ENTRIES(X)                                                                                                 \
   X(conv2d_q8_encode) X(conv2d_q8_decode) X(conv2d_rms_norm_fwd) X(conv2d_rms_norm_bwd)                            \
   X(conv2d_rms_norm_bwd_workspace_size) X(conv2d_dense_fwd) X(conv2d_dense_bwd) X(conv2d_dense_fwd_workspace_size) \
   X(conv2d_dense_bwd_workspace_size)
+// Those a library may lack: a call that needs one then raises.
+#define MORE_ENTRIES(X) \
+  X(conv2d_layer_norm_fwd) X(conv2d_layer_norm_bwd) X(conv2d_layer_norm_bwd_workspace_size)
 struct Lib {
 #define X(f) decltype(&::f) f = nullptr;
   ENTRIES(X)
+  MORE_ENTRIES(X)
 #undef X
 } lib;
 
@@ -93,10 +97,16 @@ bool is_q8(PyObject* o) { return PyTuple_Check(o) && PyTuple_GET_SIZE(o) == 3; }
 PyObject* q8_item(PyObject* o, int i) { return PyTuple_GET_ITEM(o, i); }
 int64_t group_arg(PyObject* o) {
   const int64_t g = PyLong_Check(o) ? PyLong_AsLongLong(o) : -1;
-  if (g != 0 && g != kGroup) throw Refused{"group: 0 (a whole row) or 32"};
+  if (g == -1 && PyErr_Occurred()) PyErr_Clear();  // beyond 64 bits
+  if (g != 0 && g != kGroup && g != kWide && g != kTile)
+    throw Refused{"group: 0 (a whole row), 32, 128 or TILE (128 rows by 128 columns)"};
   return g;
 }
-int64_t scale_columns(int64_t cols, int64_t group) { return group ? (cols + kGroup - 1) / kGroup : 1; }
+int64_t scale_columns(int64_t cols, int64_t group) {
+  const int64_t g = group == kTile ? kWide : group;
+  return group ? (cols + g - 1) / g : 1;
+}
+int64_t scale_rows(int64_t rows, int64_t group) { return group == kTile ? (rows + kWide - 1) / kWide : rows; }
 
 struct Source {
   int64_t rows, cols;
@@ -134,9 +144,9 @@ conv2d_mat mat(PyObject* o, const char* name, int64_t rows, int64_t cols, unsign
     if (!(types & kE4M3)) refuse(name, "an 8-bit matrix is not taken here");
     const int64_t group = group_arg(q8_item(o, 2));
     const at::Tensor& s = tensor(q8_item(o, 1), name);
-    const int64_t sc = scale_columns(cols, group);
-    if (s.scalar_type() != at::kByte || s.dim() != 2 || s.size(0) != rows || s.size(1) != sc)
-      refuse(name, "scales are uint8 of shape " + pair_name(rows, sc));
+    const int64_t sc = scale_columns(cols, group), sr = scale_rows(rows, group);
+    if (s.scalar_type() != at::kByte || s.dim() != 2 || s.size(0) != sr || s.size(1) != sc)
+      refuse(name, "scales are uint8 of shape " + pair_name(sr, sc));
     if (!s.is_contiguous() || s.device() != dev) refuse(name, "scales must be contiguous and on " + dev.str());
     conv2d_mat m = mat_of(tensor(q8_item(o, 0), name), name, rows, cols, kE4M3, dev);
     m.group = static_cast<int32_t>(group);
@@ -168,7 +178,7 @@ conv2d_mat new_mat(at::Tensor& t, int64_t rows, int64_t cols, at::ScalarType typ
 }
 conv2d_mat new_q8(at::Tensor& q, at::Tensor& s, int64_t rows, int64_t cols, int64_t group, at::Device dev) {
   q = make({rows, cols}, at::kFloat8_e4m3fn, dev);
-  s = make({rows, scale_columns(cols, group)}, at::kByte, dev);
+  s = make({scale_rows(rows, group), scale_columns(cols, group)}, at::kByte, dev);
   return {q.data_ptr(), cols, CONV2D_E4M3, static_cast<int32_t>(group), static_cast<uint8_t*>(s.data_ptr())};
 }
 
@@ -190,6 +200,15 @@ void run(at::Device dev, const char* name, F&& call) {
   Py_XDECREF(abi);
   if (!PyErr_Occurred()) PyErr_Format(PyExc_RuntimeError, "%s: status %d", name, rc);
   throw Raised{};
+}
+
+template <typename E, typename F>
+void run(at::Device dev, const char* name, E entry, F&& call) {
+  if (!entry) {
+    PyErr_Format(PyExc_RuntimeError, "%s: the loaded library lacks it", name);
+    throw Raised{};
+  }
+  run(dev, name, call);
 }
 
 PyObject* wrap(const at::Tensor& t) {
@@ -239,6 +258,12 @@ PyObject* q8_decode(PyObject* const* a) {
 
 // rms_norm_fwd(x, gamma, eps, residual, y, group, h, q8, inv_rms) -> (h, y, q, scale, inv_rms); q and scale are
 // None unless they were made here
+// The 8-bit output of a norm: no tiles, which several rows share.
+int64_t norm_group(PyObject* o, const char* name) {
+  const int64_t g = group_arg(o);
+  if (g == kTile) refuse(name, "a norm's rows share no scale (0, 32 or 128)");
+  return g;
+}
 PyObject* rms_norm_fwd(PyObject* const* a) {
   const Source s = source(a[0], "x", kFloats);
   const unsigned t = type_bit(s.type);
@@ -258,8 +283,8 @@ PyObject* rms_norm_fwd(PyObject* const* a) {
   }
   const bool has_y = a[4] != Py_False, has_q = given(a[5]) || given(a[7]);
   if (has_y) my = a[4] == Py_True ? new_mat(y, s.rows, s.cols, s.type, s.dev) : mat(a[4], "y", s.rows, s.cols, t, s.dev);
-  if (given(a[7])) mq = mat(a[7], "q8", s.rows, s.cols, kE4M3, s.dev);
-  else if (has_q) mq = new_q8(q, sc, s.rows, s.cols, group_arg(a[5]), s.dev);
+  if (given(a[7])) mq = mat(a[7], "q8", s.rows, s.cols, kE4M3, s.dev), norm_group(q8_item(a[7], 2), "q8");
+  else if (has_q) mq = new_q8(q, sc, s.rows, s.cols, norm_group(a[5], "group"), s.dev);
   float* pi;
   if (given(a[8])) {
     pi = vec(a[8], "inv_rms", s.rows, s.dev);
@@ -310,6 +335,84 @@ PyObject* rms_norm_bwd(PyObject* const* a) {
   });
   return tuple({!need_dx ? same(Py_None) : given(a[5]) ? same(a[5]) : wrap(dx),
                 !need_dg ? same(Py_None) : given(a[6]) ? same(a[6]) : wrap(dg)});
+}
+
+// layer_norm_fwd(x, gamma, beta, eps, residual, y, group, h, q8, mean, inv_std) -> (h, y, q, scale, mean, inv_std); q and
+// scale are None unless they were made here
+PyObject* layer_norm_fwd(PyObject* const* a) {
+  const Source s = source(a[0], "x", kFloats);
+  const unsigned t = type_bit(s.type);
+  const conv2d_mat x = mat(a[0], "x", s.rows, s.cols, t, s.dev);
+  const float* gamma = vec(a[1], "gamma", s.cols, s.dev);
+  const float* beta = given(a[2]) ? vec(a[2], "beta", s.cols, s.dev) : nullptr;
+  const double eps = PyFloat_AsDouble(a[3]);
+  if (eps == -1.0 && PyErr_Occurred()) throw Raised{};
+  if (!given(a[4]) && given(a[7])) refuse("h", "an output of x + residual, but there is no residual");
+  if (a[5] == Py_False && !given(a[6]) && !given(a[8]))
+    throw Refused{"y or an 8-bit form of it (group, q8) must be asked for"};
+  if (given(a[8]) && !is_q8(a[8])) refuse("q8", "expected a Q8");
+  at::Tensor h, y, q, sc, mean, inv;
+  conv2d_mat mr, mh, my, mq;
+  if (given(a[4])) {
+    mr = mat(a[4], "residual", s.rows, s.cols, t, s.dev);
+    mh = given(a[7]) ? mat(a[7], "h", s.rows, s.cols, t, s.dev) : new_mat(h, s.rows, s.cols, s.type, s.dev);
+  }
+  const bool has_y = a[5] != Py_False, has_q = given(a[6]) || given(a[8]);
+  if (has_y) my = a[5] == Py_True ? new_mat(y, s.rows, s.cols, s.type, s.dev) : mat(a[5], "y", s.rows, s.cols, t, s.dev);
+  if (given(a[8])) mq = mat(a[8], "q8", s.rows, s.cols, kE4M3, s.dev), norm_group(q8_item(a[8], 2), "q8");
+  else if (has_q) mq = new_q8(q, sc, s.rows, s.cols, norm_group(a[6], "group"), s.dev);
+  auto statistic = [&](PyObject* o, const char* name, at::Tensor& made) {
+    if (given(o)) return vec(o, name, s.rows, s.dev);
+    made = make({s.rows}, at::kFloat, s.dev);
+    return static_cast<float*>(made.data_ptr());
+  };
+  float *pm = statistic(a[9], "mean", mean), *pi = statistic(a[10], "inv_std", inv);
+  const int32_t cols = small(s.cols, "x");
+  run(s.dev, "conv2d_layer_norm_fwd", lib.conv2d_layer_norm_fwd, [&](void* st) {
+    return lib.conv2d_layer_norm_fwd(s.rows, cols, static_cast<float>(eps), &x, given(a[4]) ? &mr : nullptr, gamma, beta,
+                                     given(a[4]) ? &mh : nullptr, has_y ? &my : nullptr, has_q ? &mq : nullptr, pm, pi, st);
+  });
+  return tuple({!given(a[4]) ? same(a[0]) : given(a[7]) ? same(a[7]) : wrap(h),
+                !has_y ? same(Py_None) : a[5] == Py_True ? wrap(y) : same(a[5]), wrap(q), wrap(sc),
+                given(a[9]) ? same(a[9]) : wrap(mean), given(a[10]) ? same(a[10]) : wrap(inv)});
+}
+
+// layer_norm_bwd(h, gamma, mean, inv_std, dy, dh, dx, dgamma, dbeta, need_dx, need_dgamma, need_dbeta)
+//   -> (dx, dgamma, dbeta)
+PyObject* layer_norm_bwd(PyObject* const* a) {
+  const Source s = source(a[0], "h", kFloats);
+  const unsigned t = type_bit(s.type);
+  const bool need_dx = PyObject_IsTrue(a[9]) == 1, need_dg = PyObject_IsTrue(a[10]) == 1, need_db = PyObject_IsTrue(a[11]) == 1;
+  if (!need_dx && !need_dg && !need_db) throw Refused{"need_dx, need_dgamma or need_dbeta"};
+  if (need_dg && need_db && given(a[7]) != given(a[8]))
+    throw Refused{"dgamma and dbeta: hand in both to accumulate, or neither"};
+  const conv2d_mat h = mat(a[0], "h", s.rows, s.cols, t, s.dev);
+  const float* gamma = vec(a[1], "gamma", s.cols, s.dev);
+  const float *mean = vec(a[2], "mean", s.rows, s.dev), *inv = vec(a[3], "inv_std", s.rows, s.dev);
+  const conv2d_mat dy = mat(a[4], "dy", s.rows, s.cols, t, s.dev);
+  conv2d_mat dh, mx;
+  if (given(a[5])) dh = mat(a[5], "dh", s.rows, s.cols, t, s.dev);
+  at::Tensor dx, dg, db, ws;
+  if (need_dx)
+    mx = given(a[6]) ? mat(a[6], "dx", s.rows, s.cols, t, s.dev) : new_mat(dx, s.rows, s.cols, s.type, s.dev);
+  const int32_t cols = small(s.cols, "h");
+  auto sum = [&](bool need, PyObject* o, const char* name, at::Tensor& made) -> float* {
+    if (!need) return nullptr;
+    if (given(o)) return vec(o, name, s.cols, s.dev);
+    made = make({s.cols}, at::kFloat, s.dev);
+    return static_cast<float*>(made.data_ptr());
+  };
+  float *pg = sum(need_dg, a[7], "dgamma", dg), *pb = sum(need_db, a[8], "dbeta", db);
+  const bool accumulate = (need_dg && given(a[7])) || (need_db && given(a[8]));
+  run(s.dev, "conv2d_layer_norm_bwd", lib.conv2d_layer_norm_bwd, [&](void* st) {
+    const size_t n = pg || pb ? lib.conv2d_layer_norm_bwd_workspace_size(s.rows, cols) : 0;  // of the current device
+    if (n) ws = make({static_cast<int64_t>(n)}, at::kByte, s.dev);
+    return lib.conv2d_layer_norm_bwd(s.rows, cols, &h, gamma, mean, inv, &dy, given(a[5]) ? &dh : nullptr,
+                                     need_dx ? &mx : nullptr, pg, pb, accumulate, n ? ws.data_ptr() : nullptr, n, st);
+  });
+  return tuple({!need_dx ? same(Py_None) : given(a[6]) ? same(a[6]) : wrap(dx),
+                !need_dg ? same(Py_None) : given(a[7]) ? same(a[7]) : wrap(dg),
+                !need_db ? same(Py_None) : given(a[8]) ? same(a[8]) : wrap(db)});
 }
 
 // dense_fwd(x, w, bias, act, residual, save, dtype, y, pre_act) -> (y, z, scale); save: 0 none, 1 full, 2 q8; z and
@@ -439,6 +542,9 @@ PyObject* init(PyObject*, PyObject* path) {
   if (!lib.f) return PyErr_Format(PyExc_ImportError, "%s lacks %s", p, #f);
   ENTRIES(X)
 #undef X
+#define X(f) lib.f = reinterpret_cast<decltype(lib.f)>(dlsym(h, #f));
+  MORE_ENTRIES(X)
+#undef X
   Py_RETURN_NONE;
 }
 
@@ -448,6 +554,8 @@ PyMethodDef methods[] = {{"init", init, METH_O, "Resolves the library's entry po
                          ENTRY(q8_decode, 3),
                          ENTRY(rms_norm_fwd, 9),
                          ENTRY(rms_norm_bwd, 9),
+                         ENTRY(layer_norm_fwd, 11),
+                         ENTRY(layer_norm_bwd, 12),
                          ENTRY(dense_fwd, 9),
                          ENTRY(dense_bwd, 12),
                          {nullptr, nullptr, 0, nullptr}};

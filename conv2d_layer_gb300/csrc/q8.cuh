@@ -10,6 +10,21 @@
 namespace c2d {
 
 constexpr int kQ8Group = 32;  // columns that share a scale, when not a whole row
+constexpr int kQ8Wide = 128;  // the wider group
+constexpr int kQ8Tile = -128;  // a scale for 128 rows by 128 columns
+
+// Scales of an 8-bit matrix: scale(r, c) is byte (r >> row_shift) * ng + (c >> col_shift).
+struct Q8Layout {
+  int row_shift, col_shift, ng;
+};
+__host__ __device__ inline bool q8_known(int group) {
+  return group == 0 || group == kQ8Group || group == kQ8Wide || group == kQ8Tile;
+}
+__host__ __device__ inline Q8Layout q8_layout(int group, int cols) {
+  if (group == 0) return {0, 31, 1};
+  if (group == kQ8Group) return {0, 5, (cols + 31) / 32};
+  return {group == kQ8Tile ? 7 : 0, 7, (cols + 127) / 128};
+}
 
 template <typename T>
 __device__ __forceinline__ float to_f(T v) { return static_cast<float>(v); }

@@ -19,7 +19,7 @@ int conv2d_rms_norm_fwd(int64_t rows, int32_t cols, float eps, const conv2d_mat*
   if (!is_float(x->type)) return CONV2D_ERR_INVALID_ARG;
   for (const conv2d_mat* m : {residual, h, y})
     if (m && ((rc = check_mat(m, cols)) || m->type != x->type)) return CONV2D_ERR_INVALID_ARG;
-  if (q8 && (check_mat(q8, cols) || q8->type != CONV2D_E4M3)) return CONV2D_ERR_INVALID_ARG;
+  if (q8 && (check_mat(q8, cols) || q8->type != CONV2D_E4M3 || q8->group == kQ8Tile)) return CONV2D_ERR_INVALID_ARG;
   DevInfo* dev = nullptr;
   if ((rc = device_info(&dev))) return rc;
   NormArgs a = {};
@@ -36,19 +36,13 @@ int conv2d_rms_norm_fwd(int64_t rows, int32_t cols, float eps, const conv2d_mat*
     a.y = y->data;
     a.ldy = ld_of(y, cols);
   }
-  if (q8) {
-    a.q = static_cast<uint8_t*>(q8->data);
-    a.qs = q8->scale;
-    a.ldq = ld_of(q8, cols);
-    a.group = q8->group;
-    a.ng = q8->group ? (cols + kQ8Group - 1) / kQ8Group : 1;
-  }
+  if (q8) set_q8(a, q8, cols);
   a.inv = inv_rms;
   a.rows = rows;
   a.cols = cols;
   a.eps = eps;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  LAUNCH("rms_norm_fwd", st, rows_fwd_any<true>(a, x->type, st));
+  LAUNCH("rms_norm_fwd", st, rows_fwd_any<kRms>(a, x->type, st));
   return CONV2D_OK;
 }
 
@@ -99,9 +93,9 @@ int conv2d_rms_norm_bwd(int64_t rows, int32_t cols, const conv2d_mat* h, const f
   a.cols = cols;
   int grid = 0;
   auto run = [&]() -> cudaError_t {
-    if (h->type == CONV2D_BF16) return norm_bwd_vec<__nv_bfloat16>(a, dev->sms, &grid, st);
-    if (h->type == CONV2D_FP16) return norm_bwd_vec<__half>(a, dev->sms, &grid, st);
-    return norm_bwd_vec<float>(a, dev->sms, &grid, st);
+    if (h->type == CONV2D_BF16) return norm_bwd_vec<__nv_bfloat16, false>(a, dev->sms, &grid, st);
+    if (h->type == CONV2D_FP16) return norm_bwd_vec<__half, false>(a, dev->sms, &grid, st);
+    return norm_bwd_vec<float, false>(a, dev->sms, &grid, st);
   };
   LAUNCH("rms_norm_bwd", st, run());
   if (dgamma) LAUNCH("column_sum", st, launch_column_sum(a.part, grid, cols, dgamma, accumulate, 0, st));

@@ -122,12 +122,69 @@ bool q8_flat(const void* x, long ldx, const void* q, long ldq, uint8_t* scale, i
   return true;
 }
 
+// ------------------------------------------------------------------ 8 bits, tiles of 128 x 128
+// Encode with one scale for 128 rows by 128 columns: a block a tile, whose values stay in registers (64 a thread, all
+// loads in flight at once) between their maximum and their output. V values a vector; zeros past the ends.
+template <typename T, int V>
+__global__ void __launch_bounds__(256) q8_tile_kernel(const T* x, long ldx, uint8_t* q, long ldq, uint8_t* scale,
+                                                      long rows, int cols, int ng) {
+  pdl_entry();
+  constexpr int TPR = 128 / V, RP = 256 / TPR, N = 128 / RP;  // threads a row, rows a pass, passes
+  __shared__ uint32_t red[8];
+  const int tr = static_cast<int>(threadIdx.x) / TPR, tc = static_cast<int>(threadIdx.x) % TPR * V;
+  const long tiles = (rows + 127) / 128 * ng;
+  for (long tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+    const long row0 = tile / ng * 128 + tr;
+    const int c = static_cast<int>(tile % ng) * 128 + tc;
+    T e[N][V];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      if (c < cols && row0 + i * RP < rows) {
+        ld_vec<T, V>(x + (row0 + i * RP) * ldx + c, e[i]);
+      } else {
+#pragma unroll
+        for (int k = 0; k < V; ++k) e[i][k] = from_f<T>(0.f);
+      }
+    }
+    pdl_release();
+    uint32_t m = 0u;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+      for (int k = 0; k < V; ++k) m = max(m, finite_bits(to_f(e[i][k])));
+    m = row_max<256>(m, red);
+    const uint32_t byte = q8_scale_byte(m);
+    const float inv = q8_inv_scale(byte);
+    if (threadIdx.x == 0) scale[tile] = static_cast<uint8_t>(byte);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      float f[V];
+#pragma unroll
+      for (int k = 0; k < V; ++k) f[k] = to_f(e[i][k]);
+      if (c < cols && row0 + i * RP < rows) q8_store<V>(q + (row0 + i * RP) * ldq + c, f, inv, false);
+    }
+  }
+}
+template <typename T, int V>
+cudaError_t q8_tile_v(const NormArgs& a, cudaStream_t st) {
+  const long tiles = (a.rows + 127) / 128 * a.ng;
+  return launch_k(q8_tile_kernel<T, V>, dim3(static_cast<unsigned>(std::min(tiles, kMaxGridX))), dim3(256), 0, st, 1,
+                  static_cast<const T*>(a.x), a.ldx, a.q, a.ldq, a.qs, a.rows, a.cols, a.ng);
+}
+template <typename T>
+cudaError_t q8_tile(const NormArgs& a, cudaStream_t st) {
+  constexpr int es = sizeof(T);
+  if (rows_fwd_ok(a, es, 32 / es)) return q8_tile_v<T, 32 / es>(a, st);
+  if (rows_fwd_ok(a, es, 16 / es)) return q8_tile_v<T, 16 / es>(a, st);
+  return q8_tile_v<T, 1>(a, st);
+}
+
 // ------------------------------------------------------------------ decode / move
 // V elements a thread and step of a [rows][cols] matrix, dense steps of the grid (E4M3 source: V bytes and
 // their scale, two output vectors). rows * ceil(cols / V) below 2^31 (see to_rows).
 template <typename T, int V, bool Q, bool LATE>
-__global__ void __launch_bounds__(256) to_rows_kernel(const void* x, long ldx, const uint8_t* scale, int group, int ng,
-                                                      uint32_t total, int cols, FastDiv div_nv, T* out, long ldo) {
+__global__ void __launch_bounds__(256) to_rows_kernel(const void* x, long ldx, const uint8_t* scale, Q8Layout ql,
+                                                      long r0, uint32_t total, int cols, FastDiv div_nv, T* out, long ldo) {
   if (!LATE) pdl_entry();
   pdl_release();
   constexpr int VO = V * sizeof(T) > 16 ? 16 / static_cast<int>(sizeof(T)) : V;  // elements a store
@@ -148,7 +205,7 @@ __global__ void __launch_bounds__(256) to_rows_kernel(const void* x, long ldx, c
       c[i] = static_cast<int>(j - r * div_nv.d) * V;
       if constexpr (Q) {
         raw[i] = q8_load<V>(static_cast<const uint8_t*>(x) + row[i] * ldx + c[i]);
-        sc[i] = q8_scale(scale[row[i] * ng + (group ? c[i] / kQ8Group : 0)]);
+        sc[i] = q8_scale(scale[((row[i] + r0) >> ql.row_shift) * ql.ng + (c[i] >> ql.col_shift)]);
       } else {
         ld_vec<T, V>(static_cast<const T*>(x) + row[i] * ldx + c[i], e[i]);
       }
@@ -180,8 +237,8 @@ __global__ void __launch_bounds__(256) to_rows_kernel(const void* x, long ldx, c
 // come out of the aligned words that hold them: two for E4M3, three for 16-bit elements.
 __host__ __device__ constexpr int ragged_chunk(int W) { return W == 4 ? 512 : 256; }
 template <typename T, bool Q, int W, bool LATE>
-__global__ void __launch_bounds__(256) to_rows_ragged_kernel(const void* x, long ldx, const uint8_t* scale, int group,
-                                                             int ng, uint32_t total, FastDiv div_chunks, int cols, T* out,
+__global__ void __launch_bounds__(256) to_rows_ragged_kernel(const void* x, long ldx, const uint8_t* scale, Q8Layout ql,
+                                                             long r0, uint32_t total, FastDiv div_chunks, int cols, T* out,
                                                              long ldo) {
   if (!LATE) pdl_entry();
   pdl_release();
@@ -209,7 +266,7 @@ __global__ void __launch_bounds__(256) to_rows_ragged_kernel(const void* x, long
           for (int i = 1; i < W; ++i)
             if (c + i < cols) raw[k] |= static_cast<uint32_t>(p[i]) << (8 * i);
         }
-        sb[k] = scale[row * ng + (group ? c / kQ8Group : 0)];  // W divides c and a group: one scale for the neighbours
+        sb[k] = scale[((row + r0) >> ql.row_shift) * ql.ng + (c >> ql.col_shift)];  // W divides c and a group: one scale for the neighbours
       } else {
         const T* p = static_cast<const T*>(x) + row * ldx + c;
         if constexpr (W == 4) {
@@ -257,7 +314,7 @@ __global__ void __launch_bounds__(256) to_rows_ragged_kernel(const void* x, long
 }
 
 template <typename T, bool Q, int W>
-cudaError_t to_rows_ragged(const void* x, long ldx, const uint8_t* scale, int group, int ng, long rows, int cols,
+cudaError_t to_rows_ragged(const void* x, long ldx, const uint8_t* scale, Q8Layout ql, long rows, int cols,
                            void* out, long ldo, int late, cudaStream_t st) {
   const int chunks = (cols + ragged_chunk(W) - 1) / ragged_chunk(W);
   const long slab = std::max<long>(1, 0x7fffffffL / chunks);  // rows a launch indexes in 31 bits
@@ -267,12 +324,11 @@ cudaError_t to_rows_ragged(const void* x, long ldx, const uint8_t* scale, int gr
     const uint32_t total = static_cast<uint32_t>(n * chunks);
     const dim3 grid(static_cast<unsigned>(std::min<long>((n * chunks + 7) / 8, 152L * 64)));
     const void* src = static_cast<const char*>(x) + r0 * ldx * (Q ? 1 : static_cast<long>(sizeof(T)));
-    const uint8_t* sc = Q ? scale + r0 * ng : nullptr;
     T* o = static_cast<T*>(out) + r0 * ldo;
     const cudaError_t e =
-        late ? launch_k(to_rows_ragged_kernel<T, Q, W, true>, grid, dim3(256), 0, st, 1, src, ldx, sc, group, ng, total,
+        late ? launch_k(to_rows_ragged_kernel<T, Q, W, true>, grid, dim3(256), 0, st, 1, src, ldx, scale, ql, r0, total,
                         div, cols, o, ldo)
-             : launch_k(to_rows_ragged_kernel<T, Q, W, false>, grid, dim3(256), 0, st, 1, src, ldx, sc, group, ng, total,
+             : launch_k(to_rows_ragged_kernel<T, Q, W, false>, grid, dim3(256), 0, st, 1, src, ldx, scale, ql, r0, total,
                         div, cols, o, ldo);
     if (e != cudaSuccess) return e;
   }
@@ -284,7 +340,7 @@ cudaError_t to_rows(const conv2d_mat& x, long rows, int cols, void* out, long ld
   constexpr int VV = 16 / sizeof(T), VQ = 16;
   const bool q = x.type == CONV2D_E4M3;
   const long ldx = x.ld ? x.ld : cols, ld = ldo ? ldo : cols;
-  const int ng = x.group ? (cols + kQ8Group - 1) / kQ8Group : 1;
+  const Q8Layout ql = q8_layout(q ? x.group : 0, cols);
   // whole vectors only: cols a multiple of the vector, and both rows' starts aligned to theirs
   if constexpr (sizeof(T) == 2) {
     cudaError_t e;
@@ -295,14 +351,14 @@ cudaError_t to_rows(const conv2d_mat& x, long rows, int cols, void* out, long ld
   if (!vec) {
     if constexpr (sizeof(T) == 2) {
       if (ld % 4 == 0)
-        return q ? to_rows_ragged<T, true, 4>(x.data, ldx, x.scale, x.group, ng, rows, cols, out, ld, late, st)
-                 : to_rows_ragged<T, false, 4>(x.data, ldx, nullptr, 0, 1, rows, cols, out, ld, late, st);
+        return q ? to_rows_ragged<T, true, 4>(x.data, ldx, x.scale, ql, rows, cols, out, ld, late, st)
+                 : to_rows_ragged<T, false, 4>(x.data, ldx, nullptr, ql, rows, cols, out, ld, late, st);
       if (ld % 2 == 0)
-        return q ? to_rows_ragged<T, true, 2>(x.data, ldx, x.scale, x.group, ng, rows, cols, out, ld, late, st)
-                 : to_rows_ragged<T, false, 2>(x.data, ldx, nullptr, 0, 1, rows, cols, out, ld, late, st);
+        return q ? to_rows_ragged<T, true, 2>(x.data, ldx, x.scale, ql, rows, cols, out, ld, late, st)
+                 : to_rows_ragged<T, false, 2>(x.data, ldx, nullptr, ql, rows, cols, out, ld, late, st);
     }
-    return q ? to_rows_ragged<T, true, 1>(x.data, ldx, x.scale, x.group, ng, rows, cols, out, ld, late, st)
-             : to_rows_ragged<T, false, 1>(x.data, ldx, nullptr, 0, 1, rows, cols, out, ld, late, st);
+    return q ? to_rows_ragged<T, true, 1>(x.data, ldx, x.scale, ql, rows, cols, out, ld, late, st)
+             : to_rows_ragged<T, false, 1>(x.data, ldx, nullptr, ql, rows, cols, out, ld, late, st);
   }
   const int nv = cols / V;
   const long slab = std::max<long>(1, 0x7fffffffL / nv);  // rows a launch indexes in 31 bits
@@ -311,14 +367,14 @@ cudaError_t to_rows(const conv2d_mat& x, long rows, int cols, void* out, long ld
     const uint32_t total = static_cast<uint32_t>(n * nv);
     const dim3 grid(stream_grid((n * nv + 1) / 2));
     const char* src = static_cast<const char*>(x.data) + r0 * ldx * (q ? 1 : static_cast<long>(sizeof(T)));
-    const uint8_t* sc = q ? x.scale + r0 * ng : nullptr;
     T* o = static_cast<T*>(out) + r0 * ld;
+    const uint8_t* sc = x.scale;
     const FastDiv div = make_fastdiv(static_cast<uint32_t>(nv));
-#define TO_ROWS(V, Q)                                                                                                  \
-  (late ? launch_k(to_rows_kernel<T, V, Q, true>, grid, dim3(256), 0, st, 1, static_cast<const void*>(src), ldx, sc,  \
-                   x.group, ng, total, cols, div, o, ld)                                                               \
+#define TO_ROWS(V, Q)                                                                                                \
+  (late ? launch_k(to_rows_kernel<T, V, Q, true>, grid, dim3(256), 0, st, 1, static_cast<const void*>(src), ldx, sc, \
+                   ql, r0, total, cols, div, o, ld)                                                                  \
         : launch_k(to_rows_kernel<T, V, Q, false>, grid, dim3(256), 0, st, 1, static_cast<const void*>(src), ldx, sc, \
-                   x.group, ng, total, cols, div, o, ld))
+                   ql, r0, total, cols, div, o, ld))
     const cudaError_t e = q ? TO_ROWS(VQ, true) : TO_ROWS(VV, false);
 #undef TO_ROWS
     if (e != cudaSuccess) return e;
@@ -528,7 +584,7 @@ cudaError_t launch_to_rows(const conv2d_mat& x, long rows, int cols, int dt, voi
 
 cudaError_t launch_move_bytes(const void* x, long ldx, long rows, int cols, void* out, long ldo, int late,
                               cudaStream_t st) {
-  return to_rows_ragged<uint8_t, false, 1>(x, ldx, nullptr, 0, 1, rows, cols, out, ldo, late, st);
+  return to_rows_ragged<uint8_t, false, 1>(x, ldx, nullptr, Q8Layout{}, rows, cols, out, ldo, late, st);
 }
 
 DactPlan plan_dact(long rows, int cols, int sms) {
@@ -620,21 +676,20 @@ int conv2d_q8_encode(int64_t rows, int32_t cols, const conv2d_mat* x, const conv
   NormArgs a = {};
   a.x = x->data;
   a.ldx = ld_of(x, cols);
-  a.q = static_cast<uint8_t*>(q8->data);
-  a.qs = q8->scale;
-  a.ldq = ld_of(q8, cols);
   a.rows = rows;
   a.cols = cols;
-  a.group = q8->group;
-  a.ng = q8->group ? (cols + kQ8Group - 1) / kQ8Group : 1;
+  set_q8(a, q8, cols);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   auto run = [&]() -> cudaError_t {
     cudaError_t e = cudaSuccess;
+    if (a.group == kQ8Tile)
+      return x->type == CONV2D_BF16 ? q8_tile<__nv_bfloat16>(a, st) : x->type == CONV2D_FP16 ? q8_tile<__half>(a, st)
+                                                                                           : q8_tile<float>(a, st);
     if (x->type == CONV2D_BF16 && q8_flat<__nv_bfloat16, true>(a.x, a.ldx, a.q, a.ldq, a.qs, a.group, rows, cols, 0, st, &e))
       return e;
     if (x->type == CONV2D_FP16 && q8_flat<__half, true>(a.x, a.ldx, a.q, a.ldq, a.qs, a.group, rows, cols, 0, st, &e))
       return e;
-    return rows_fwd_any<false>(a, x->type, st);
+    return rows_fwd_any<kEncode>(a, x->type, st);
   };
   LAUNCH("q8_encode", st, run());
   return CONV2D_OK;

@@ -39,6 +39,28 @@ __device__ __forceinline__ float row_sum(float v, float* red) {
   }
   return v;
 }
+// Two sums at once; red: two words per warp.
+template <int TPR>
+__device__ __forceinline__ float2 row_sum2(float2 v, float* red) {
+  v.x = warp_sum(v.x);
+  v.y = warp_sum(v.y);
+  if constexpr (TPR > 32) {
+    const int warp = threadIdx.x >> 5;
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) {
+      red[2 * warp] = v.x;
+      red[2 * warp + 1] = v.y;
+    }
+    __syncthreads();
+    v = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < TPR / 32; ++i) {
+      v.x += red[2 * i];
+      v.y += red[2 * i + 1];
+    }
+  }
+  return v;
+}
 template <int TPR>
 __device__ __forceinline__ uint32_t row_max(uint32_t v, uint32_t* red) {
   v = __reduce_max_sync(0xffffffffu, v);
@@ -56,31 +78,33 @@ __device__ __forceinline__ uint32_t row_max(uint32_t v, uint32_t* red) {
 
 struct NormArgs {
   const void *x, *r;
-  const float* gamma;
+  const float *gamma, *beta;  // beta: layer norm, may be null
   void *h, *y;
   uint8_t *q, *qs;
-  float* inv;
+  float *inv, *mean;
   long ldx, ldr, ldh, ldy, ldq;
   long rows;
   int cols, ng;  // ng: scale bytes a row
-  int group;     // 32 or 0 (whole row)
+  int group;     // 32, 128 or 0 (whole row)
   float eps;
 };
+enum : int { kEncode = 0, kRms = 1, kLayer = 2 };  // what rows_fwd_kernel computes
 
-// RMS norm forward (NORM) or 8-bit encode (!NORM): TPR threads a row, a block of them or (TPR = 32) eight warps. Rows are
+// RMS norm or layer norm forward, or 8-bit encode (KIND): TPR threads a row, a block of them or (TPR = 32) eight warps. Rows are
 // held in registers between their sum of squares and their output, U vectors a thread, so memory is passed once;
 // U = 0 is the form for rows longer than that, which reads the row again for each phase (from L2, mostly). NR
 // rows are in flight at once where a row is a vector or two a thread (one row of 512 bytes a warp left a
 // 200704 x 256 encode at 41 us). Threads hold neighbouring vectors, so a group of 32 columns lies in 32 / V
 // neighbouring lanes and its maximum is found by shuffles. Bound by memory: 8192 x 4096 bf16 with the residual, y
 // and its 8-bit form moves 303 MB in 47 us, 0.95 of the measured copy rate.
-template <typename T, int V, int TPR, int U, int NR, bool NORM>
+template <typename T, int V, int TPR, int U, int NR, int KIND>
 __global__ void __launch_bounds__(TPR == 32 ? 256 : TPR) rows_fwd_kernel(const NormArgs a) {
   pdl_entry();
   constexpr int RPB = TPR == 32 ? 8 : 1;  // groups of NR rows per block
   static_assert(U > 0 || NR == 1, "one row at a time where it is read again");
   constexpr int UC = U > 0 ? U : 1;
   __shared__ float red[32];
+  [[maybe_unused]] __shared__ uint32_t wide[2][32];
   const int t = RPB > 1 ? static_cast<int>(threadIdx.x) & 31 : static_cast<int>(threadIdx.x);
   const long row0 = (static_cast<long>(blockIdx.x) * RPB + (RPB > 1 ? threadIdx.x >> 5 : 0)) * NR;
   if (row0 >= a.rows) return;  // whole warps; rows that use block barriers are whole blocks
@@ -125,12 +149,17 @@ __global__ void __launch_bounds__(TPR == 32 ? 256 : TPR) rows_fwd_kernel(const N
         widen(e[i][u], v[i][u]);
       }
   };
-  auto reload = [&](int u) {  // U = 0: this thread's own h (or x) again
+  [[maybe_unused]] float mean[NR];
+  auto reload = [&](int u) {  // U = 0: this thread's own h (or x) again; layer norm: its distance from the mean
     const int c = u * TPR + t;
     if (c < nv) {
       T e[V];
       ld_vec<T, V>((a.r ? static_cast<const T*>(hb) : xb) + static_cast<long>(c) * V, e);
       widen(e, v[0][0]);
+      if constexpr (KIND == kLayer) {
+#pragma unroll
+        for (int k = 0; k < V; ++k) v[0][0][k] -= mean[0];
+      }
     } else {
 #pragma unroll
       for (int k = 0; k < V; ++k) v[0][0][k] = 0.f;
@@ -141,7 +170,33 @@ __global__ void __launch_bounds__(TPR == 32 ? 256 : TPR) rows_fwd_kernel(const N
 #pragma unroll
   for (int i = 0; i < NR; ++i) inv[i] = 1.f;
   if constexpr (U > 0) load_all(0, UC);
-  if constexpr (NORM) {
+  if constexpr (KIND == kLayer) {
+    // The mean first, then the squares of the distances from it: their sum loses nothing where the mean is large
+    // against the deviation. Zeros past the end count in neither.
+    float sum[NR];
+#pragma unroll
+    for (int i = 0; i < NR; ++i) sum[i] = 0.f;
+    if constexpr (U > 0) {
+#pragma unroll
+      for (int i = 0; i < NR; ++i)
+#pragma unroll
+        for (int u = 0; u < UC; ++u)
+#pragma unroll
+          for (int k = 0; k < V; ++k) sum[i] += v[i][u][k];
+    } else {
+      for (int u = 0; u < nu; ++u) {
+        load_all(u, 1);
+#pragma unroll
+        for (int k = 0; k < V; ++k) sum[0] += v[0][0][k];
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < NR; ++i) {
+      mean[i] = row_sum<TPR>(sum[i], red) / static_cast<float>(a.cols);
+      if (t == 0 && i < nr && a.mean) a.mean[row0 + i] = mean[i];
+    }
+  }
+  if constexpr (KIND != kEncode) {
     float ss[NR];
 #pragma unroll
     for (int i = 0; i < NR; ++i) ss[i] = 0.f;
@@ -149,12 +204,18 @@ __global__ void __launch_bounds__(TPR == 32 ? 256 : TPR) rows_fwd_kernel(const N
 #pragma unroll
       for (int i = 0; i < NR; ++i)
 #pragma unroll
-        for (int u = 0; u < UC; ++u)
+        for (int u = 0; u < UC; ++u) {
+          if (KIND == kLayer && u * TPR + t >= nv) break;
 #pragma unroll
-          for (int k = 0; k < V; ++k) ss[i] = fmaf(v[i][u][k], v[i][u][k], ss[i]);
+          for (int k = 0; k < V; ++k) {
+            if constexpr (KIND == kLayer) v[i][u][k] -= mean[i];
+            ss[i] = fmaf(v[i][u][k], v[i][u][k], ss[i]);
+          }
+        }
     } else {
       for (int u = 0; u < nu; ++u) {
-        load_all(u, 1);
+        if constexpr (KIND == kLayer) reload(u);
+        else load_all(u, 1);
 #pragma unroll
         for (int k = 0; k < V; ++k) ss[0] = fmaf(v[0][0][k], v[0][0][k], ss[0]);
       }
@@ -166,22 +227,35 @@ __global__ void __launch_bounds__(TPR == 32 ? 256 : TPR) rows_fwd_kernel(const N
     }
   }
   pdl_release();
-  // y = gamma h s of vector u, in place, for all NR rows (U = 0: of the one vector at hand)
+  // y = gamma h s (layer norm: gamma (h - mean) s + beta) of vector u, in place, for all NR rows (U = 0: of the one
+  // vector at hand)
   auto scale = [&](int u, int slot) {
     const int c = u * TPR + t;
-    if (!NORM || c >= nv) return;
-    const float* gp = a.gamma + static_cast<long>(c) * V;
-    float g[V];
-    if constexpr (V >= 4) {
+    if (KIND == kEncode || c >= nv) return;
+    auto feature = [&](const float* p, float (&g)[V]) {
+      p += static_cast<long>(c) * V;
+      if constexpr (V >= 4) {
 #pragma unroll
-      for (int k = 0; k < V; k += 4) *reinterpret_cast<float4*>(g + k) = *reinterpret_cast<const float4*>(gp + k);
-    } else {
-      g[0] = gp[0];
-    }
+        for (int k = 0; k < V; k += 4) *reinterpret_cast<float4*>(g + k) = *reinterpret_cast<const float4*>(p + k);
+      } else {
+        g[0] = p[0];
+      }
+    };
+    float g[V];
+    feature(a.gamma, g);
 #pragma unroll
     for (int i = 0; i < NR; ++i)
 #pragma unroll
       for (int k = 0; k < V; ++k) v[i][slot][k] = v[i][slot][k] * inv[i] * g[k];
+    if constexpr (KIND == kLayer) {
+      if (a.beta) {
+        feature(a.beta, g);
+#pragma unroll
+        for (int i = 0; i < NR; ++i)
+#pragma unroll
+          for (int k = 0; k < V; ++k) v[i][slot][k] += g[k];
+      }
+    }
   };
   // Largest magnitude's bits; fmaxf passes NaN over, and infinities are looked for only where one shows.
   auto absmax = [&](const float (&o)[V]) {
@@ -253,24 +327,40 @@ __global__ void __launch_bounds__(TPR == 32 ? 256 : TPR) rows_fwd_kernel(const N
         uint32_t byte = rowbyte[i];
         bool finite = rowfinite[i];
         if (a.group != 0) {
-          auto group_max = [](uint32_t m) {
-            if constexpr (V == 1) {  // the group is the warp
-              return __reduce_max_sync(0xffffffffu, m);
-            } else {
+          uint32_t m;
+          if (V == 1 && TPR > 32 && a.group == kQ8Wide) {
+            // the group is four warps of the block, all of which are here
+            m = __reduce_max_sync(0xffffffffu, absmax_finite(o));
+            const int warp = threadIdx.x >> 5;
+            if ((threadIdx.x & 31) == 0) wide[u & 1][warp] = m;
+            __syncthreads();
 #pragma unroll
-              for (int s = 1; s < kQ8Group / V; s <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, s));
-              return m;
-            }
-          };
-          uint32_t m = group_max(absmax(o));
-          finite = true;
-          if (__any_sync(0xffffffffu, m == kInf)) {
+            for (int w = 0; w < 4; ++w) m = max(m, wide[u & 1][(warp & ~3) + w]);
             finite = false;
-            m = group_max(absmax_finite(o));
+          } else {
+            auto group_max = [&](uint32_t m) {
+              if constexpr (V == 1) {  // the group is the warp
+                return __reduce_max_sync(0xffffffffu, m);
+              } else {
+#pragma unroll
+                for (int s = 1; s < kQ8Group / V; s <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, s));
+                if (a.group == kQ8Wide) {
+#pragma unroll
+                  for (int s = kQ8Group / V; s < kQ8Wide / V; s <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, s));
+                }
+                return m;
+              }
+            };
+            m = group_max(absmax(o));
+            finite = true;
+            if (__any_sync(0xffffffffu, m == kInf)) {
+              finite = false;
+              m = group_max(absmax_finite(o));
+            }
           }
           byte = q8_scale_byte(m);
-          if (on && (t & (kQ8Group / V - 1)) == 0)
-            a.qs[(row0 + i) * a.ng + c / (kQ8Group / V)] = static_cast<uint8_t>(byte);
+          const int per = a.group / V;  // threads a group
+          if (on && (t & (per - 1)) == 0) a.qs[(row0 + i) * a.ng + c / per] = static_cast<uint8_t>(byte);
         }
         if (on) q8_store<V>(a.q + (row0 + i) * a.ldq + static_cast<long>(c) * V, o, q8_inv_scale(byte), finite);
       }
@@ -284,24 +374,20 @@ __global__ void __launch_bounds__(TPR == 32 ? 256 : TPR) rows_fwd_kernel(const N
     }
   } else {
     for (int u = 0; u < nu; ++u) {
-      if constexpr (NORM) {
-        reload(u);
-        scale(u, 0);
-      } else {
-        reload(u);
-      }
+      reload(u);
+      scale(u, 0);
       finish(u, 0);
     }
   }
 }
 
-template <typename T, int V, bool NORM>
+template <typename T, int V, int KIND>
 cudaError_t rows_fwd(const NormArgs& a, cudaStream_t st) {
   const int nv = (a.cols + V - 1) / V;
 #define ROWS_FWD(TPR, U, NR)                                                                                        \
   do {                                                                                                              \
     constexpr int nt = (TPR) == 32 ? 256 : (TPR), rpb = nt / (TPR) * (NR);                                         \
-    return launch_k(rows_fwd_kernel<T, V, TPR, U, NR, NORM>, dim3(static_cast<unsigned>((a.rows + rpb - 1) / rpb)), \
+    return launch_k(rows_fwd_kernel<T, V, TPR, U, NR, KIND>, dim3(static_cast<unsigned>((a.rows + rpb - 1) / rpb)), \
                     dim3(nt), 0, st, 1, a);                                                                         \
   } while (0)
   // 16 to 32 values a thread where a warp takes a row (8 to 16 when they are loaded one by one); long rows are
@@ -338,12 +424,12 @@ cudaError_t rows_fwd(const NormArgs& a, cudaStream_t st) {
 #undef ROWS_FWD
 }
 
-// ------------------------------------------------------------------ RMS norm backward
+// ------------------------------------------------------------------ norms, backward
 struct NormBwdArgs {
   const void *h, *dy, *dh;
   void* dx;
-  const float *gamma, *inv;
-  float* part;  // [gridDim.x][cols], null: no dgamma
+  const float *gamma, *inv, *mean;  // mean: layer norm
+  float *part, *partb;  // [gridDim.x][cols] of dgamma and (layer norm) dbeta; null: not asked for
   long ldh, lddy, lddh, lddx;
   long rows;
   int cols;
@@ -361,13 +447,13 @@ constexpr int norm_bwd_resident(int tpr) {
 // longer than the registers hold; each row is read twice and dgamma's sums live in this block's row of `part`.
 // Bound by memory: 8192 x 4096 bf16 with dh moves 268 MB in 46 us, 0.85 of the copy rate (64 us with one block of
 // 136 registers a thread an SM, before the registers were held to two).
-template <typename T, int V, int TPR, int U, bool AHEAD>
+template <typename T, int V, int TPR, int U, bool AHEAD, bool LAYER>
 __global__ void __launch_bounds__(TPR == 32 ? 256 : TPR, norm_bwd_resident(TPR)) norm_bwd_kernel(const NormBwdArgs a) {
   pdl_entry();
   constexpr int RPB = TPR == 32 ? 8 : 1;
   constexpr int UC = U > 0 ? U : 1;
   extern __shared__ float sums[];  // RPB > 1 with dgamma: [RPB][cols]
-  __shared__ float red[32];
+  __shared__ float red[LAYER ? 64 : 32];
   const int t = RPB > 1 ? static_cast<int>(threadIdx.x) & 31 : static_cast<int>(threadIdx.x);
   const int wr = RPB > 1 ? static_cast<int>(threadIdx.x >> 5) : 0;
   const int nv = (a.cols + V - 1) / V;
@@ -381,6 +467,7 @@ __global__ void __launch_bounds__(TPR == 32 ? 256 : TPR, norm_bwd_resident(TPR))
 
   if constexpr (U > 0) {
     float g[AHEAD ? UC : 1][V], acc[UC][V];
+    [[maybe_unused]] float accb[LAYER ? UC : 1][V];
     auto load_gamma = [&](int u, float (&o)[V]) {
       const int c = (u * TPR + t) * V;
 #pragma unroll
@@ -397,12 +484,19 @@ __global__ void __launch_bounds__(TPR == 32 ? 256 : TPR, norm_bwd_resident(TPR))
     for (int u = 0; u < UC; ++u) {
       if constexpr (AHEAD) load_gamma(u, g[u]);
 #pragma unroll
-      for (int k = 0; k < V; ++k) acc[u][k] = 0.f;
+      for (int k = 0; k < V; ++k) {
+        acc[u][k] = 0.f;
+        if constexpr (LAYER) accb[u][k] = 0.f;
+      }
     }
     T h[UC][V], d[UC][V], s[AHEAD ? UC : 1][V];
     float inv = 0.f;
+    [[maybe_unused]] float mean = 0.f;
     auto fetch = [&](long row) {
-      if (row < a.rows) inv = a.inv[row];
+      if (row < a.rows) {
+        inv = a.inv[row];
+        if constexpr (LAYER) mean = a.mean[row];
+      }
 #pragma unroll
       for (int u = 0; u < UC; ++u) {
         const int i = u * TPR + t;
@@ -423,24 +517,35 @@ __global__ void __launch_bounds__(TPR == 32 ? 256 : TPR, norm_bwd_resident(TPR))
       float hf[UC][V], df[UC][V];
       T sk[AHEAD ? UC : 1][V];
       const float iv = inv;
+      [[maybe_unused]] const float mu = mean;
       float dot = 0.f;
+      [[maybe_unused]] float sum = 0.f;
 #pragma unroll
       for (int u = 0; u < UC; ++u) {
         float gu[V];
         if constexpr (!AHEAD) load_gamma(u, gu);
 #pragma unroll
         for (int k = 0; k < V; ++k) {
-          hf[u][k] = to_f(h[u][k]) * iv;  // the normalised value
+          // the normalised value; past the row's end dy is zero, so it counts in no sum
+          hf[u][k] = (LAYER ? to_f(h[u][k]) - mu : to_f(h[u][k])) * iv;
           df[u][k] = to_f(d[u][k]);
+          if constexpr (LAYER) accb[u][k] += df[u][k];
           if constexpr (AHEAD) sk[u][k] = s[u][k];
           acc[u][k] = fmaf(df[u][k], hf[u][k], acc[u][k]);
           df[u][k] *= AHEAD ? g[AHEAD ? u : 0][k] : gu[k];
           dot = fmaf(df[u][k], hf[u][k], dot);
+          if constexpr (LAYER) sum += df[u][k];
         }
       }
       if constexpr (AHEAD) fetch(row + step);
       if (xb) {
-        dot = row_sum<TPR>(dot, red) * invD;
+        if constexpr (LAYER) {
+          const float2 both = row_sum2<TPR>(make_float2(dot, sum), red);
+          dot = both.x * invD;
+          sum = both.y * invD;
+        } else {
+          dot = row_sum<TPR>(dot, red) * invD;
+        }
 #pragma unroll
         for (int u = 0; u < UC; ++u) {
           const int i = u * TPR + t;
@@ -450,7 +555,7 @@ __global__ void __launch_bounds__(TPR == 32 ? 256 : TPR, norm_bwd_resident(TPR))
               if (sb) ld_vec<T, V>(sb + row * a.lddh + static_cast<long>(i) * V, sv);
 #pragma unroll
             for (int k = 0; k < V; ++k) {
-              float v = iv * fmaf(-hf[u][k], dot, df[u][k]);
+              float v = iv * fmaf(-hf[u][k], dot, LAYER ? df[u][k] - sum : df[u][k]);
               if (sb) v += to_f(AHEAD ? sk[AHEAD ? u : 0][k] : sv[k]);
               o[k] = from_f<T>(v);
             }
@@ -460,40 +565,50 @@ __global__ void __launch_bounds__(TPR == 32 ? 256 : TPR, norm_bwd_resident(TPR))
       }
     }
     pdl_release();
-    if (!a.part) return;
-    float* part = a.part + static_cast<long>(blockIdx.x) * a.cols;
-    if constexpr (RPB > 1) {
+    // this block's row of the partial sums
+    auto partials = [&](float* base, const float (&v)[UC][V]) {
+      if (!base) return;
+      float* part = base + static_cast<long>(blockIdx.x) * a.cols;
+      if constexpr (RPB > 1) {
+        __syncthreads();  // the last use of sums is over
 #pragma unroll
-      for (int u = 0; u < UC; ++u)
+        for (int u = 0; u < UC; ++u)
 #pragma unroll
-        for (int k = 0; k < V; ++k) {
-          const int c = (u * TPR + t) * V + k;
-          if (c < a.cols) sums[wr * a.cols + c] = acc[u][k];
+          for (int k = 0; k < V; ++k) {
+            const int c = (u * TPR + t) * V + k;
+            if (c < a.cols) sums[wr * a.cols + c] = v[u][k];
+          }
+        __syncthreads();
+        for (int c = threadIdx.x; c < a.cols; c += 256) {
+          float s = 0.f;
+#pragma unroll
+          for (int w = 0; w < RPB; ++w) s += sums[w * a.cols + c];
+          part[c] = s;
         }
-      __syncthreads();
-      for (int c = threadIdx.x; c < a.cols; c += 256) {
-        float v = 0.f;
+      } else {
 #pragma unroll
-        for (int w = 0; w < RPB; ++w) v += sums[w * a.cols + c];
-        part[c] = v;
+        for (int u = 0; u < UC; ++u)
+#pragma unroll
+          for (int k = 0; k < V; ++k) {
+            const int c = (u * TPR + t) * V + k;
+            if (c < a.cols) part[c] = v[u][k];
+          }
       }
-    } else {
-#pragma unroll
-      for (int u = 0; u < UC; ++u)
-#pragma unroll
-        for (int k = 0; k < V; ++k) {
-          const int c = (u * TPR + t) * V + k;
-          if (c < a.cols) part[c] = acc[u][k];
-        }
-    }
+    };
+    partials(a.part, acc);
+    if constexpr (LAYER) partials(a.partb, accb);
   } else {
     float* part = a.part ? a.part + static_cast<long>(blockIdx.x) * a.cols : nullptr;
-    if (part)
-      for (int i = t; i < nv; i += TPR)
-        for (int k = 0; k < V; ++k) part[static_cast<long>(i) * V + k] = 0.f;
+    [[maybe_unused]] float* partb = LAYER && a.partb ? a.partb + static_cast<long>(blockIdx.x) * a.cols : nullptr;
+    for (int i = t; i < nv; i += TPR)
+      for (int k = 0; k < V; ++k) {
+        if (part) part[static_cast<long>(i) * V + k] = 0.f;
+        if (LAYER && partb) partb[static_cast<long>(i) * V + k] = 0.f;
+      }
     for (long row = row0; row < a.rows; row += step) {
-      const float iv = a.inv[row];
+      const float iv = a.inv[row], mu = LAYER ? a.mean[row] : 0.f;
       float dot = 0.f;
+      [[maybe_unused]] float sum = 0.f;
       for (int i = t; i < nv; i += TPR) {
         T h[V], d[V];
         ld_vec<T, V>(hb + row * a.ldh + static_cast<long>(i) * V, h);
@@ -501,13 +616,23 @@ __global__ void __launch_bounds__(TPR == 32 ? 256 : TPR, norm_bwd_resident(TPR))
 #pragma unroll
         for (int k = 0; k < V; ++k) {
           const long c = static_cast<long>(i) * V + k;
-          const float hn = to_f(h[k]) * iv, dv = to_f(d[k]);
+          const float hn = (LAYER ? to_f(h[k]) - mu : to_f(h[k])) * iv, dv = to_f(d[k]);
           if (part) part[c] = fmaf(dv, hn, part[c]);
           dot = fmaf(dv * a.gamma[c], hn, dot);
+          if constexpr (LAYER) {
+            if (partb) partb[c] += dv;
+            sum = fmaf(dv, a.gamma[c], sum);
+          }
         }
       }
       if (!xb) continue;
-      dot = row_sum<TPR>(dot, red) * invD;
+      if constexpr (LAYER) {
+        const float2 both = row_sum2<TPR>(make_float2(dot, sum), red);
+        dot = both.x * invD;
+        sum = both.y * invD;
+      } else {
+        dot = row_sum<TPR>(dot, red) * invD;
+      }
       for (int i = t; i < nv; i += TPR) {
         T h[V], d[V], s[V], o[V];
         ld_vec<T, V>(hb + row * a.ldh + static_cast<long>(i) * V, h);
@@ -516,7 +641,8 @@ __global__ void __launch_bounds__(TPR == 32 ? 256 : TPR, norm_bwd_resident(TPR))
 #pragma unroll
         for (int k = 0; k < V; ++k) {
           const long c = static_cast<long>(i) * V + k;
-          float v = iv * fmaf(-to_f(h[k]) * iv, dot, to_f(d[k]) * a.gamma[c]);
+          float v = LAYER ? iv * fmaf((mu - to_f(h[k])) * iv, dot, fmaf(to_f(d[k]), a.gamma[c], -sum))
+                          : iv * fmaf(-to_f(h[k]) * iv, dot, to_f(d[k]) * a.gamma[c]);
           if (sb) v += to_f(s[k]);
           o[k] = from_f<T>(v);
         }
@@ -532,15 +658,15 @@ inline long norm_bwd_blocks(int64_t rows, int cols, int sms) {
 }
 
 // grid: blocks launched, one row of partial sums each.
-template <typename T, int V>
+template <typename T, int V, bool LAYER>
 cudaError_t norm_bwd(const NormBwdArgs& a, int sms, int* grid, cudaStream_t st) {
   const int nv = (a.cols + V - 1) / V;
 #define NORM_BWD(TPR, U, AHEAD)                                                                   \
   do {                                                                                            \
     constexpr int nt = (TPR) == 32 ? 256 : (TPR);                                                 \
-    const size_t smem = nt > (TPR) && a.part ? static_cast<size_t>(nt / (TPR)) * a.cols * 4 : 0;  \
+    const size_t smem = nt > (TPR) && (a.part || a.partb) ? static_cast<size_t>(nt / (TPR)) * a.cols * 4 : 0;  \
     *grid = static_cast<int>(std::min<long>(a.rows, static_cast<long>(sms) * norm_bwd_resident(TPR))); \
-    return launch_k(norm_bwd_kernel<T, V, TPR, U, AHEAD>, dim3(*grid), dim3(nt), smem, st, 1, a); \
+    return launch_k(norm_bwd_kernel<T, V, TPR, U, AHEAD, LAYER>, dim3(*grid), dim3(nt), smem, st, 1, a); \
   } while (0)
   // Vectors: as many threads as the row has of them (two a thread where a vector is 16 bytes), so that an SM's threads
   // all have loads in flight: 32768 x 1024 bf16 91 us with 256 threads, 50 with 64; 16384 x 1000 48 and 28. Rows of
@@ -589,7 +715,7 @@ inline int check_mat(const conv2d_mat* m, int cols) {
   if (!m || !m->data || !aligned16(m->data)) return CONV2D_ERR_INVALID_ARG;
   if (m->ld != 0 && m->ld < cols) return CONV2D_ERR_INVALID_ARG;
   if (m->type == CONV2D_E4M3) {
-    if (!m->scale || (m->group != 0 && m->group != kQ8Group)) return CONV2D_ERR_INVALID_ARG;
+    if (!m->scale || !q8_known(m->group)) return CONV2D_ERR_INVALID_ARG;
   } else if (!is_float(m->type)) {
     return CONV2D_ERR_INVALID_ARG;
   }
@@ -604,27 +730,35 @@ inline int check_rows(int64_t rows, int32_t cols) {
   return CONV2D_OK;
 }
 
-template <bool NORM>
-bool rows_fwd_ok(const NormArgs& a, int es, int V) {
+// The 8-bit output. A group of 128 in rows no longer than that is the row.
+inline void set_q8(NormArgs& a, const conv2d_mat* q8, int cols) {
+  a.q = static_cast<uint8_t*>(q8->data);
+  a.qs = q8->scale;
+  a.ldq = ld_of(q8, cols);
+  a.group = q8->group == kQ8Wide && cols <= kQ8Wide ? 0 : q8->group;
+  a.ng = q8_layout(a.group, cols).ng;
+}
+
+inline bool rows_fwd_ok(const NormArgs& a, int es, int V) {
   return a.cols % V == 0 && vec_ok(a.x, a.ldx, es, V) && (!a.r || (vec_ok(a.r, a.ldr, es, V) && vec_ok(a.h, a.ldh, es, V))) &&
          (!a.y || vec_ok(a.y, a.ldy, es, V)) && (!a.q || vec_ok(a.q, a.ldq, 1, V));
 }
-template <typename T, bool NORM>
+template <typename T, int KIND>
 cudaError_t rows_fwd_vec(const NormArgs& a, cudaStream_t st) {
   constexpr int es = sizeof(T);
   // at 16 vectors of 32 bytes and fewer half of the lanes would idle (200704 x 256 to 8 bits too: 93 us, now 88)
-  if (a.cols > 16 * 32 / es && rows_fwd_ok<NORM>(a, es, 32 / es)) return rows_fwd<T, 32 / es, NORM>(a, st);
-  if (rows_fwd_ok<NORM>(a, es, 16 / es)) return rows_fwd<T, 16 / es, NORM>(a, st);
-  return rows_fwd<T, 1, NORM>(a, st);
+  if (a.cols > 16 * 32 / es && rows_fwd_ok(a, es, 32 / es)) return rows_fwd<T, 32 / es, KIND>(a, st);
+  if (rows_fwd_ok(a, es, 16 / es)) return rows_fwd<T, 16 / es, KIND>(a, st);
+  return rows_fwd<T, 1, KIND>(a, st);
 }
-template <bool NORM>
+template <int KIND>
 cudaError_t rows_fwd_any(const NormArgs& a, int type, cudaStream_t st) {
-  if (type == CONV2D_BF16) return rows_fwd_vec<__nv_bfloat16, NORM>(a, st);
-  if (type == CONV2D_FP16) return rows_fwd_vec<__half, NORM>(a, st);
-  return rows_fwd_vec<float, NORM>(a, st);
+  if (type == CONV2D_BF16) return rows_fwd_vec<__nv_bfloat16, KIND>(a, st);
+  if (type == CONV2D_FP16) return rows_fwd_vec<__half, KIND>(a, st);
+  return rows_fwd_vec<float, KIND>(a, st);
 }
 
-template <typename T>
+template <typename T, bool LAYER>
 cudaError_t norm_bwd_vec(const NormBwdArgs& a, int sms, int* grid, cudaStream_t st) {
   constexpr int es = sizeof(T);
   auto ok = [&](int V) {
@@ -632,9 +766,9 @@ cudaError_t norm_bwd_vec(const NormBwdArgs& a, int sms, int* grid, cudaStream_t 
            (!a.dx || vec_ok(a.dx, a.lddx, es, V)) && (!a.dh || vec_ok(a.dh, a.lddh, es, V));
   };
   if constexpr (es == 2)  // fp32 rows of 32-byte vectors take more registers than they win
-    if (a.cols > 16 * 32 / es && ok(32 / es)) return norm_bwd<T, 32 / es>(a, sms, grid, st);
-  if (ok(16 / es)) return norm_bwd<T, 16 / es>(a, sms, grid, st);
-  return norm_bwd<T, 1>(a, sms, grid, st);
+    if (a.cols > 16 * 32 / es && ok(32 / es)) return norm_bwd<T, 32 / es, LAYER>(a, sms, grid, st);
+  if (ok(16 / es)) return norm_bwd<T, 16 / es, LAYER>(a, sms, grid, st);
+  return norm_bwd<T, 1, LAYER>(a, sms, grid, st);
 }
 
 }  // namespace

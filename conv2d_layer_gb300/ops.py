@@ -1,4 +1,4 @@
-"""The residual block's operators on torch tensors: RMS norm, dense layer, 8-bit checkpoints.
+"""The residual block's operators on torch tensors: RMS norm, layer norm, dense layer, 8-bit checkpoints.
 
 Matrices are 2-D CUDA tensors of rows by features; rows may be strided (the last dimension is contiguous, the
 first element on a 16-byte boundary). Outputs that are not handed in are allocated with torch; workspaces
@@ -18,6 +18,8 @@ import torch
 from . import abi, build
 
 GROUP = 32  # columns of an 8-bit tensor that share a scale, when not a whole row (0)
+WIDE = 128  # the wider group: what the 8-bit matrix product takes
+TILE = abi.TILE  # a group of 128 rows by 128 columns, for weights
 # gelu is the tanh form, z/2 (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))): torch's gelu(approximate="tanh"), not its default
 ACTS = {"identity": abi.ACT_IDENTITY, "relu": abi.ACT_RELU, "tanh": abi.ACT_TANH, "sigmoid": abi.ACT_SIGMOID,
         "gelu": abi.ACT_GELU, "silu": abi.ACT_SILU}
@@ -37,10 +39,11 @@ def _binding():
 
 
 class Q8(NamedTuple):
-    """A matrix in 8 bits: value(r, c) = q[r, c] * 2 ** (scale[r, c // group] - 127), or scale[r, 0] with group 0."""
+    """A matrix in 8 bits: value(r, c) = q[r, c] * 2 ** (scale[r, c // group] - 127), scale[r, 0] with group 0, or
+    scale[r // 128, c // 128] with group TILE."""
     q: torch.Tensor      # [rows, cols] torch.float8_e4m3fn
-    scale: torch.Tensor  # [rows, ceil(cols / group)] torch.uint8, contiguous
-    group: int = GROUP   # 32, or 0: one scale a row
+    scale: torch.Tensor  # [rows, ceil(cols / group)] (TILE: [ceil(rows / 128), ceil(cols / 128)]) torch.uint8, contiguous
+    group: int = GROUP   # 32, 128 (WIDE), 0: one scale a row, or TILE
 
     @property
     def shape(self):
@@ -58,16 +61,25 @@ class RmsNorm(NamedTuple):
     inv_rms: torch.Tensor      # [rows] fp32
 
 
+class LayerNorm(NamedTuple):
+    h: torch.Tensor            # x + residual (x itself without a residual)
+    y: Optional[torch.Tensor]
+    q8: Optional[Q8]
+    mean: torch.Tensor         # [rows] fp32
+    inv_std: torch.Tensor      # [rows] fp32
+
+
 def q8_scales(cols, group):
-    """Scale bytes a row."""
-    if group not in (0, GROUP):
-        raise ValueError(f"group: 0 (a whole row) or {GROUP}, got {group!r}")
-    return -(-cols // GROUP) if group else 1
+    """Scale bytes a row (TILE: a row of tiles)."""
+    if group not in (0, GROUP, WIDE, TILE):
+        raise ValueError(f"group: 0 (a whole row), {GROUP}, {WIDE} or TILE, got {group!r}")
+    return -(-cols // (WIDE if group == TILE else group)) if group else 1
 
 
 def q8_empty(rows, cols, group=GROUP, device="cuda"):
+    tall = -(-rows // 128) if group == TILE else rows
     return Q8(torch.empty((rows, cols), dtype=torch.float8_e4m3fn, device=device),
-              torch.empty((rows, q8_scales(cols, group)), dtype=torch.uint8, device=device), group)
+              torch.empty((tall, q8_scales(cols, group)), dtype=torch.uint8, device=device), group)
 
 
 def _device_of(args):
@@ -102,8 +114,8 @@ def _act(act):
 # ------------------------------------------------------------------ 8-bit checkpoints
 @_streamed
 def q8_encode(x, group=GROUP, out=None):
-    """x [rows, cols] (fp32, bf16, fp16) in 8 bits, with one scale for `group` columns (32, or 0: a row). out: an output
-    Q8, whose group then counts."""
+    """x [rows, cols] (fp32, bf16, fp16) in 8 bits, with one scale for `group` columns (32, 128, or 0: a row) or for 128
+    rows by 128 columns (TILE). out: an output Q8, whose group then counts."""
     r = _binding().q8_encode(x, group, out)
     return Q8(r[0], r[1], group) if r is not None else out
 
@@ -120,7 +132,7 @@ def rms_norm_fwd(x, gamma, eps=1e-6, residual=None, y=True, group=None, h=None, 
     """h = x + residual; y = gamma * h / sqrt(mean(h^2) + eps), row by row.
 
     y: True (allocate), False (none) or an output tensor. group: None, or the group of an 8-bit form of y
-    (32, or 0: a row); q8: an output Q8 for it, whose group then counts. h: output for x + residual (may be x or residual itself).
+    (32, 128, or 0: a row); q8: an output Q8 for it, whose group then counts. h: output for x + residual (may be x or residual itself).
     Returns RmsNorm(h, y, q8, inv_rms); h and inv_rms are what rms_norm_bwd takes."""
     h, y, q, scale, inv_rms = _binding().rms_norm_fwd(x, gamma, eps, residual, y, group, h, q8, inv_rms)
     return RmsNorm(h, y, q8 if q is None else Q8(q, scale, group), inv_rms)
@@ -131,6 +143,28 @@ def rms_norm_bwd(h, gamma, inv_rms, dy, dh=None, dx=None, dgamma=None, need_dx=T
     """(dx, dgamma) of rms_norm_fwd: dx is the gradient of x and of residual, dh the gradient that reaches h
     beside the norm. dx may be dh itself. A dgamma that is handed in is accumulated into."""
     return _binding().rms_norm_bwd(h, gamma, inv_rms, dy, dh, dx, dgamma, need_dx, need_dgamma)
+
+
+# ------------------------------------------------------------------ layer norm
+@_streamed
+def layer_norm_fwd(x, gamma, beta=None, eps=1e-5, residual=None, y=True, group=None, h=None, q8=None, mean=None,
+                   inv_std=None):
+    """h = x + residual; y = gamma * (h - m) / sqrt(mean((h - m)^2) + eps) + beta, m = mean(h), row by row. beta may be
+    None (zero).
+
+    y, group, q8 and h as in rms_norm_fwd. Returns LayerNorm(h, y, q8, mean, inv_std); h, mean and inv_std are what
+    layer_norm_bwd takes."""
+    h, y, q, scale, mean, inv_std = _binding().layer_norm_fwd(x, gamma, beta, eps, residual, y, group, h, q8, mean, inv_std)
+    return LayerNorm(h, y, q8 if q is None else Q8(q, scale, group), mean, inv_std)
+
+
+@_streamed
+def layer_norm_bwd(h, gamma, mean, inv_std, dy, dh=None, dx=None, dgamma=None, dbeta=None, need_dx=True, need_dgamma=True,
+                   need_dbeta=True):
+    """(dx, dgamma, dbeta) of layer_norm_fwd: dx is the gradient of x and of residual, dh the gradient that reaches h
+    beside the norm. dx may be dh itself. dgamma and dbeta that are handed in (both, or the one that is asked for) are
+    accumulated into."""
+    return _binding().layer_norm_bwd(h, gamma, mean, inv_std, dy, dh, dx, dgamma, dbeta, need_dx, need_dgamma, need_dbeta)
 
 
 # ------------------------------------------------------------------ dense layer
@@ -160,5 +194,5 @@ def dense_bwd(x, w, dy, pre_act=None, act="identity", need_dx=True, need_dw=True
     return _binding().dense_bwd(x, w, dy, pre_act, _act(act), grad_dtype, dx, dw, dbias, need_dx, need_dw, need_dbias)
 
 
-__all__ = ["Q8", "RmsNorm", "q8_empty", "q8_scales", "q8_encode", "q8_decode", "rms_norm_fwd", "rms_norm_bwd",
-           "dense_fwd", "dense_bwd", "ACTS", "GROUP"]
+__all__ = ["Q8", "RmsNorm", "LayerNorm", "q8_empty", "q8_scales", "q8_encode", "q8_decode", "rms_norm_fwd", "rms_norm_bwd",
+           "layer_norm_fwd", "layer_norm_bwd", "dense_fwd", "dense_bwd", "ACTS", "GROUP", "WIDE", "TILE"]

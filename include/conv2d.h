@@ -212,11 +212,14 @@ int conv2d_bwd(const conv2d_desc* desc, const void* x, const void* w, const floa
  *   type   FP32, BF16, FP16 or E4M3
  *   ld     elements from the start of one row to the next, at least the
  *          number of columns; 0 stands for the number of columns
- *   group, scale   E4M3 only: columns that share a scale (32, or 0 for a whole
- *          row) and the scales, one byte for each group, dense, row by row
- *          ([rows][ceil(columns / group)]): byte s stands for 2^(s - 127).
+ *   group, scale   E4M3 only: columns that share a scale (32, 128, or 0 for a
+ *          whole row) and the scales, one byte for each group, dense, row by
+ *          row ([rows][ceil(columns / group)]): byte s stands for 2^(s - 127).
  *          The element (r, c) has the value data[r][c] * scale(r, c).
- *          `scale` has no alignment rule. */
+ *          With group CONV2D_TILE 128 rows by 128 columns share one
+ *          ([ceil(rows / 128)][ceil(columns / 128)]). `scale` has no alignment
+ *          rule. */
+#define CONV2D_TILE (-128)
 typedef struct {
     void* data;
     int64_t ld;
@@ -264,6 +267,29 @@ size_t conv2d_rms_norm_bwd_workspace_size(int64_t rows, int32_t cols);
 int conv2d_rms_norm_bwd(int64_t rows, int32_t cols, const conv2d_mat* h, const float* gamma, const float* inv_rms,
                         const conv2d_mat* dy, const conv2d_mat* dh, const conv2d_mat* dx, float* dgamma,
                         int accumulate, void* ws, size_t ws_bytes, void* stream);
+
+/* Layer norm of the rows of h = x + residual:
+ *   m = mean_j h_j,   s = 1 / sqrt(mean_j (h_j - m)^2 + eps),
+ *   y_j = gamma_j (h_j - m) s + beta_j
+ * beta may be NULL (zero); mean [rows] and inv_std [rows] receive m and s for
+ * conv2d_layer_norm_bwd and may be NULL. The rest is as in
+ * conv2d_rms_norm_fwd; the squares are those of the distances from m, summed
+ * after it. */
+int conv2d_layer_norm_fwd(int64_t rows, int32_t cols, float eps, const conv2d_mat* x, const conv2d_mat* residual,
+                          const float* gamma, const float* beta, const conv2d_mat* h, const conv2d_mat* y,
+                          const conv2d_mat* q8, float* mean, float* inv_std, void* stream);
+
+/* Bytes of workspace of conv2d_layer_norm_bwd (0 if the sizes are invalid). */
+size_t conv2d_layer_norm_bwd_workspace_size(int64_t rows, int32_t cols);
+
+/* Backward of conv2d_layer_norm_fwd. With n = (h - m) s and g = gamma dy:
+ *   dx = s (g - mean_j g_j - n mean_j(g_j n_j)) + dh  (the gradient of x and of
+ *   residual); dgamma = sum over rows of dy n; dbeta = sum over rows of dy.
+ * dh may be NULL, and may be the same buffer as dx. Of dx, dgamma and dbeta
+ * one or two may be NULL; without the two sums ws may be NULL. */
+int conv2d_layer_norm_bwd(int64_t rows, int32_t cols, const conv2d_mat* h, const float* gamma, const float* mean,
+                          const float* inv_std, const conv2d_mat* dy, const conv2d_mat* dh, const conv2d_mat* dx,
+                          float* dgamma, float* dbeta, int accumulate, void* ws, size_t ws_bytes, void* stream);
 
 /* Dense layer: y = act(z) + residual, z = x w^T + bias.
  * x [M][K], w [N][K], residual, y, z [M][N]; dtype (BF16 or FP16) is the type
