@@ -2,6 +2,356 @@
 #include "rows.h"
 #include "rows_norm.cuh"
 
+namespace c2d {
+namespace {
+
+// Layer norm forward in one stream of rows: a block (WARP: a warp) walks the rows, NR at a time, with gamma and beta in
+// its registers (KEEP) and the next rows' vectors in flight while these are reduced and written; U vectors of V elements a
+// thread, as many threads as the row has vectors. The statistics are joined as in rows_fwd_kernel. Bound by memory: 8192 x
+// 4096 bf16 with the residual moves 268 MB in 45 us, 0.88 of the copy rate (61 us a row a block, with gamma and beta read
+// for each row; 49 with them read in whole sectors).
+template <typename T, int V, int U, int NR, bool WARP, bool KEEP, int MT, int MB>
+__global__ void __launch_bounds__(MT, MB) layer_stream_kernel(const NormArgs a) {
+  pdl_entry();
+  __shared__ float4 part[2][NR][32];
+  __shared__ uint32_t red[32];
+  const int tpr = WARP ? 32 : static_cast<int>(blockDim.x), nw = tpr / 32;
+  const int t = WARP ? static_cast<int>(threadIdx.x) & 31 : static_cast<int>(threadIdx.x);
+  const int warp = WARP ? 0 : t >> 5, lane = t & 31;
+  const int nv = a.cols / V;
+  const long per = (WARP ? blockDim.x / 32 : 1) * NR;  // rows a block takes at a time
+  const long row0 = blockIdx.x * per + (WARP ? (threadIdx.x >> 5) * NR : 0);
+  const long step = gridDim.x * per;
+  const float cols = static_cast<float>(a.cols);
+
+  auto feature = [&](const float* p, int u, float (&g)[V]) {
+    const int c = u * tpr + t;
+#pragma unroll
+    for (int k = 0; k < V; ++k) g[k] = 0.f;
+    if (!p || c >= nv) return;
+    p += static_cast<long>(c) * V;
+    if (V >= 8 && a.wide) {
+#pragma unroll
+      for (int k = 0; k < V; k += 8) ld_32b(p + k, reinterpret_cast<uint32_t(&)[8]>(g[k]));
+    } else {
+#pragma unroll
+      for (int k = 0; k < V; k += 4) *reinterpret_cast<float4*>(g + k) = *reinterpret_cast<const float4*>(p + k);
+    }
+  };
+  float g[KEEP ? U : 1][V], b[KEEP ? U : 1][V];
+  if constexpr (KEEP) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      feature(a.gamma, u, g[u]);
+      feature(a.beta, u, b[u]);
+    }
+  }
+  int count = 0;  // of this warp's values
+#pragma unroll
+  for (int u = 0; u < U; ++u) count += V * min(max(nv - u * tpr - warp * 32, 0), 32);
+  const float n = static_cast<float>(count), over = count > 0 ? 1.f / n : 0.f;
+
+  T e[NR][U][V], f[NR][U][V];
+  auto fetch = [&](long row) {
+#pragma unroll
+    for (int i = 0; i < NR; ++i)
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int c = u * tpr + t;
+        if (row + i < a.rows && c < nv) {
+          ld_vec<T, V>(static_cast<const T*>(a.x) + (row + i) * a.ldx + static_cast<long>(c) * V, e[i][u]);
+          if (a.r) ld_vec<T, V>(static_cast<const T*>(a.r) + (row + i) * a.ldr + static_cast<long>(c) * V, f[i][u]);
+        } else {
+#pragma unroll
+          for (int k = 0; k < V; ++k) e[i][u][k] = f[i][u][k] = from_f<T>(0.f);
+        }
+      }
+  };
+  fetch(row0);
+  int par = 0;
+  for (long row = row0; row < a.rows; row += step, par ^= 1) {
+    float v[NR][U][V];
+#pragma unroll
+    for (int i = 0; i < NR; ++i)
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int c = u * tpr + t;
+        if (a.r) {
+#pragma unroll
+          for (int k = 0; k < V; ++k) e[i][u][k] = from_f<T>(to_f(e[i][u][k]) + to_f(f[i][u][k]));
+          if (row + i < a.rows && c < nv)
+            st_vec<T, V>(static_cast<T*>(a.h) + (row + i) * a.ldh + static_cast<long>(c) * V, e[i][u]);
+        }
+#pragma unroll
+        for (int k = 0; k < V; ++k) v[i][u][k] = to_f(e[i][u][k]);
+      }
+    if (row + step < a.rows) fetch(row + step);
+    else pdl_release();
+    float mean[NR], ss[NR];
+#pragma unroll
+    for (int i = 0; i < NR; ++i) {
+      const float sum = warp_sum(row_fold<U, V>(v[i], [](float2 s, float2 x) { return __fadd2_rn(s, x); }));
+      mean[i] = WARP ? sum / n : sum * over;
+      const float2 shift = make_float2(-mean[i], -mean[i]);
+      ss[i] = 0.f;
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (u * tpr + t < nv)  // zeros past the end count in neither
+          ss[i] += row_fold<1, V>(reinterpret_cast<float(&)[1][V]>(v[i][u]), [&](float2 s, float2 x) {
+            const float2 d = __fadd2_rn(x, shift);
+            return __ffma2_rn(d, d, s);
+          });
+      ss[i] = warp_sum(ss[i]);
+      if (!WARP && lane == 0) part[par][i][warp] = make_float4(sum, ss[i], mean[i], n);
+    }
+    if constexpr (!WARP) {
+      __syncthreads();  // once a row: the next one writes the other half of part
+#pragma unroll
+      for (int i = 0; i < NR; ++i) {
+        float sum = 0.f;
+        ss[i] = 0.f;
+#pragma unroll 8
+        for (int w = 0; w < nw; ++w) sum += part[par][i][w].x;
+        mean[i] = sum / cols;
+#pragma unroll 8
+        for (int w = 0; w < nw; ++w) {
+          const float4 p = part[par][i][w];
+          const float d = p.z - mean[i];
+          ss[i] += fmaf(p.w * d, d, p.y);
+        }
+      }
+    }
+    float inv[NR];
+#pragma unroll
+    for (int i = 0; i < NR; ++i) {
+      inv[i] = 1.f / sqrtf(ss[i] / cols + a.eps);
+      if (t == 0 && row + i < a.rows) {
+        if (a.mean) a.mean[row + i] = mean[i];
+        if (a.inv) a.inv[row + i] = inv[i];
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if constexpr (!KEEP) {
+        feature(a.gamma, u, g[0]);
+        feature(a.beta, u, b[0]);
+      }
+      const int c = u * tpr + t;
+      if (c >= nv) continue;
+#pragma unroll
+      for (int i = 0; i < NR; ++i)
+#pragma unroll
+        for (int k = 0; k < V; k += 2) {
+          float2 x = __fadd2_rn(make_float2(v[i][u][k], v[i][u][k + 1]), make_float2(-mean[i], -mean[i]));
+          x = __fmul2_rn(x, make_float2(inv[i], inv[i]));
+          x = __ffma2_rn(x, make_float2(g[KEEP ? u : 0][k], g[KEEP ? u : 0][k + 1]),
+                         make_float2(b[KEEP ? u : 0][k], b[KEEP ? u : 0][k + 1]));
+          v[i][u][k] = x.x;
+          v[i][u][k + 1] = x.y;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < NR; ++i) {
+      uint32_t byte = 0u;
+      bool finite = true;
+      if (a.q && a.group == 0) {
+        auto whole = [&](auto&& top) {
+          uint32_t m = 0u;
+#pragma unroll
+          for (int u = 0; u < U; ++u) m = max(m, top(v[i][u]));
+          m = __reduce_max_sync(0xffffffffu, m);
+          if constexpr (!WARP) {
+            __syncthreads();  // the last use of red is over
+            if (lane == 0) red[warp] = m;
+            __syncthreads();
+            m = 0u;
+#pragma unroll 8
+            for (int w = 0; w < nw; ++w) m = max(m, red[w]);
+          }
+          return m;
+        };
+        uint32_t m = whole([](const float (&o)[V]) { return absmax(o); });
+        if (m == kInf) {  // the same for the whole row
+          finite = false;
+          m = whole([](const float (&o)[V]) { return absmax_finite(o); });
+        }
+        byte = q8_scale_byte(m);
+        if (t == 0 && row + i < a.rows) a.qs[(row + i) * a.ng] = static_cast<uint8_t>(byte);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int c = u * tpr + t;
+        const bool on = row + i < a.rows && c < nv;
+        float(&o)[V] = v[i][u];
+        if (a.y && on) {
+          T w[V];
+#pragma unroll
+          for (int k = 0; k < V; ++k) w[k] = from_f<T>(o[k]);
+          st_vec<T, V>(static_cast<T*>(a.y) + (row + i) * a.ldy + static_cast<long>(c) * V, w);
+        }
+        if (a.q) {
+          if (a.group != 0) {
+            byte = q8_scale_byte(q8_group_max(a.group, o, finite));
+            const int share = a.group / V;  // threads a group
+            if (on && (t & (share - 1)) == 0) a.qs[(row + i) * a.ng + c / share] = static_cast<uint8_t>(byte);
+          }
+          if (on) q8_store<V>(a.q + (row + i) * a.ldq + static_cast<long>(c) * V, o, q8_inv_scale(byte), finite);
+        }
+      }
+    }
+  }
+}
+
+template <typename T, int V, int U, int NR, bool WARP, bool KEEP, int MT, int MB>
+cudaError_t layer_stream(const NormArgs& a, int threads, int sms, cudaStream_t st) {
+  const long per = (WARP ? threads / 32 : 1) * NR;
+  const long blocks = std::min<long>((a.rows + per - 1) / per, static_cast<long>(sms) * std::max(1, MT * MB / threads));
+  return launch_k(layer_stream_kernel<T, V, U, NR, WARP, KEEP, MT, MB>, dim3(static_cast<unsigned>(blocks)), dim3(threads),
+                  0, st, 1, a);
+}
+
+template <typename T, int V>
+cudaError_t layer_vec(const NormArgs& a, int sms, cudaStream_t st) {
+  // The stream for 16-bit rows: in 32-byte vectors, or of up to a warp's vectors. Elsewhere a row has too few or too many
+  // threads for it (8192 x 1000 bf16 14.7 us, 11.0 in rows_fwd_kernel; fp32 8192 x 4096 92 and 79).
+  if constexpr (sizeof(T) == 2) {
+    const int nv = a.cols / V, threads = (nv + 31) / 32 * 32;
+    if (nv <= 32) return layer_stream<T, V, 1, (V == 16 ? 2 : 4), true, true, 256, 2>(a, 256, sms, st);
+    if constexpr (V == 16) {
+      if (threads <= 256) return layer_stream<T, V, 1, 1, false, true, 256, 3>(a, threads, sms, st);
+      if (threads <= 384) return layer_stream<T, V, 1, 1, false, true, 384, 2>(a, threads, sms, st);
+      if (threads <= 512) return layer_stream<T, V, 1, 1, false, true, 512, 1>(a, threads, sms, st);
+      if (nv <= 1024) return layer_stream<T, V, 2, 1, false, false, 512, 1>(a, (nv + 63) / 64 * 32, sms, st);
+    }
+  }
+  return rows_fwd<T, V, kLayer>(a, st);
+}
+template <typename T>
+cudaError_t layer_any(const NormArgs& a, int sms, cudaStream_t st) {
+  constexpr int es = sizeof(T);
+  if (a.cols > 16 * 32 / es && rows_fwd_ok(a, es, 32 / es)) return layer_vec<T, 32 / es>(a, sms, st);
+  if (rows_fwd_ok(a, es, 16 / es)) return layer_vec<T, 16 / es>(a, sms, st);
+  return rows_fwd<T, 1, kLayer>(a, st);
+}
+
+// Layer norm backward of 16-bit rows of 32-byte vectors, one a thread: as norm_bwd_kernel, with the arithmetic in packed
+// pairs, one meeting of the block a row, and the row at hand kept as it came (16 of its registers instead of 32). Bound by
+// memory: 8192 x 4096 bf16 with dh moves 268 MB in 57 us with the column sums (61 in norm_bwd_kernel), 0.70 of the copy
+// rate; 512 threads an SM of 126 registers each are all that its sums of dgamma and dbeta leave.
+template <typename T, int MT, int MB>
+__global__ void __launch_bounds__(MT, MB) layer_bwd_kernel(const NormBwdArgs a) {
+  pdl_entry();
+  constexpr int V = 16;
+  __shared__ float2 part[2][MT / 32];
+  const int t = static_cast<int>(threadIdx.x), nw = static_cast<int>(blockDim.x) >> 5;
+  const int c = t * V;
+  const bool on = c < a.cols;
+  const float over = 1.f / static_cast<float>(a.cols);
+  const T* hb = static_cast<const T*>(a.h) + c;
+  const T* db = static_cast<const T*>(a.dy) + c;
+  const T* sb = static_cast<const T*>(a.dh) + c;
+  T* xb = static_cast<T*>(a.dx) + c;
+  float2 g[V / 2], acc[V / 2], accb[V / 2];
+#pragma unroll
+  for (int k = 0; k < V / 2; ++k) {
+    g[k] = on ? *reinterpret_cast<const float2*>(a.gamma + c + 2 * k) : splat(0.f);
+    acc[k] = accb[k] = splat(0.f);
+  }
+  uint32_t h[8], d[8], s[8];
+  float inv = 0.f, mean = 0.f;
+  auto fetch = [&](long row) {
+    inv = a.inv[row];
+    mean = a.mean[row];
+    if (on) {
+      ld_32b(hb + row * a.ldh, h);
+      ld_32b(db + row * a.lddy, d);
+      if (a.dh && a.dx) ld_32b(sb + row * a.lddh, s);
+    }
+  };
+  auto pair = [](uint32_t w) {
+    const T* e = reinterpret_cast<const T*>(&w);
+    return make_float2(to_f(e[0]), to_f(e[1]));
+  };
+#pragma unroll
+  for (int k = 0; k < 8; ++k) h[k] = d[k] = s[k] = 0u;
+  const long step = gridDim.x;
+  long row = blockIdx.x;  // the grid has no more blocks than there are rows
+  fetch(row);
+  int par = 0;
+  for (; row < a.rows; row += step, par ^= 1) {
+    const float2 iv = splat(inv), mu = splat(-mean);
+    float2 dot = splat(0.f), sum = splat(0.f);
+    uint32_t hc[8], dc[8], sc[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      hc[k] = h[k];
+      dc[k] = d[k];
+      sc[k] = s[k];
+    }
+    if (row + step < a.rows) fetch(row + step);
+    else pdl_release();
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const float2 n = __fmul2_rn(__fadd2_rn(pair(hc[k]), mu), iv), y = pair(dc[k]), w = __fmul2_rn(y, g[k]);
+      acc[k] = __ffma2_rn(y, n, acc[k]);
+      accb[k] = __fadd2_rn(accb[k], y);
+      dot = __ffma2_rn(w, n, dot);
+      sum = __fadd2_rn(sum, w);
+    }
+    if (!a.dx) continue;
+    // past the row's end dy is zero, so it counts in no sum
+    float2 both = make_float2(warp_sum(dot.x + dot.y), warp_sum(sum.x + sum.y));
+    if ((t & 31) == 0) part[par][t >> 5] = both;
+    __syncthreads();  // once a row: the next one writes the other half of part
+    both = splat(0.f);
+#pragma unroll 8
+    for (int w = 0; w < nw; ++w) both = __fadd2_rn(both, part[par][w]);
+    const float2 md = splat(-both.x * over), ms = splat(-both.y * over);
+    if (on) {
+      uint32_t o[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float2 n = __fmul2_rn(__fadd2_rn(pair(hc[k]), mu), iv);
+        float2 v = __ffma2_rn(n, md, __ffma2_rn(pair(dc[k]), g[k], ms));
+        v = a.dh ? __ffma2_rn(v, iv, pair(sc[k])) : __fmul2_rn(v, iv);
+        T* e = reinterpret_cast<T*>(&o[k]);
+        e[0] = from_f<T>(v.x);
+        e[1] = from_f<T>(v.y);
+      }
+      st_32b(xb + row * a.lddx, o);
+    }
+  }
+  if (!on) return;
+  auto partials = [&](float* base, const float2 (&v)[V / 2]) {
+    if (!base) return;
+    float4* p = reinterpret_cast<float4*>(base + static_cast<long>(blockIdx.x) * a.cols + c);
+#pragma unroll
+    for (int k = 0; k < V / 4; ++k) p[k] = make_float4(v[2 * k].x, v[2 * k].y, v[2 * k + 1].x, v[2 * k + 1].y);
+  };
+  partials(a.part, acc);
+  partials(a.partb, accb);
+}
+template <typename T>
+cudaError_t layer_bwd(const NormBwdArgs& a, int sms, int* grid, cudaStream_t st) {
+  constexpr int V = 16;
+  if constexpr (sizeof(T) == 2) {
+    auto ok = [&](const void* p, long ld) { return !p || vec_ok(p, ld, 2, V); };
+    const int threads = (a.cols / V + 31) / 32 * 32;
+    // between 256 and 448 threads an SM holds one block that leaves it idle (8192 x 5120 84 us, 73 in norm_bwd_kernel)
+    if (a.cols % V == 0 && threads >= 64 && (threads <= 256 || (threads > 448 && threads <= 512)) && ok(a.h, a.ldh) && ok(a.dy, a.lddy) && ok(a.dx, a.lddx) &&
+        ok(a.dh, a.lddh)) {
+      // no more blocks than the workspace has rows for
+      *grid = static_cast<int>(std::min<long>(norm_bwd_blocks(a.rows, a.cols, sms), static_cast<long>(sms) * (512 / threads)));
+      if (threads <= 256) return launch_k(layer_bwd_kernel<T, 256, 2>, dim3(*grid), dim3(threads), 0, st, 1, a);
+      return launch_k(layer_bwd_kernel<T, 512, 1>, dim3(*grid), dim3(threads), 0, st, 1, a);
+    }
+  }
+  return norm_bwd_vec<T, true>(a, sms, grid, st);
+}
+
+}  // namespace
+}  // namespace c2d
+
 using namespace c2d;
 
 extern "C" {
@@ -43,9 +393,15 @@ int conv2d_layer_norm_fwd(int64_t rows, int32_t cols, float eps, const conv2d_ma
   a.inv = inv_std;
   a.rows = rows;
   a.cols = cols;
+  a.wide = ((reinterpret_cast<uintptr_t>(gamma) | reinterpret_cast<uintptr_t>(beta)) & 31u) == 0;
   a.eps = eps;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  LAUNCH("layer_norm_fwd", st, rows_fwd_any<kLayer>(a, x->type, st));
+  auto run = [&]() -> cudaError_t {
+    if (x->type == CONV2D_BF16) return layer_any<__nv_bfloat16>(a, dev->sms, st);
+    if (x->type == CONV2D_FP16) return layer_any<__half>(a, dev->sms, st);
+    return layer_any<float>(a, dev->sms, st);
+  };
+  LAUNCH("layer_norm_fwd", st, run());
   return CONV2D_OK;
 }
 
@@ -101,13 +457,15 @@ int conv2d_layer_norm_bwd(int64_t rows, int32_t cols, const conv2d_mat* h, const
   a.cols = cols;
   int grid = 0;
   auto run = [&]() -> cudaError_t {
-    if (h->type == CONV2D_BF16) return norm_bwd_vec<__nv_bfloat16, true>(a, dev->sms, &grid, st);
-    if (h->type == CONV2D_FP16) return norm_bwd_vec<__half, true>(a, dev->sms, &grid, st);
-    return norm_bwd_vec<float, true>(a, dev->sms, &grid, st);
+    if (h->type == CONV2D_BF16) return layer_bwd<__nv_bfloat16>(a, dev->sms, &grid, st);
+    if (h->type == CONV2D_FP16) return layer_bwd<__half>(a, dev->sms, &grid, st);
+    return layer_bwd<float>(a, dev->sms, &grid, st);
   };
   LAUNCH("layer_norm_bwd", st, run());
-  if (dgamma) LAUNCH("column_sum", st, launch_column_sum(a.part, grid, cols, dgamma, accumulate, 0, st));
-  if (dbeta) LAUNCH("column_sum", st, launch_column_sum(a.partb, grid, cols, dbeta, accumulate, dgamma != nullptr, st));
+  if (sums)
+    LAUNCH("column_sum", st,
+           launch_column_sum(dgamma ? a.part : a.partb, grid, cols, dgamma ? dgamma : dbeta, accumulate, 0, st, a.partb,
+                             dgamma ? dbeta : nullptr));
   return CONV2D_OK;
 }
 

@@ -510,9 +510,13 @@ cudaError_t dact(const DactArgs& a, int zk, int strips, int late, cudaStream_t s
 // sums in order.
 template <int W>
 __global__ void __launch_bounds__(W * 32) column_sum_kernel(const float* part, int G, int cols, float* out,
-                                                         int accumulate, int late) {
+                                                         const float* part2, float* out2, int accumulate, int late) {
   if (!late) pdl_entry();
   pdl_release();
+  if (blockIdx.y) {
+    part = part2;
+    out = out2;
+  }
   __shared__ float s[W][33];
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int c = static_cast<int>(blockIdx.x) * 32 + lane;
@@ -625,10 +629,11 @@ cudaError_t launch_dact(const conv2d_mat* z, const conv2d_mat& dy, long rows, in
 }
 
 cudaError_t launch_column_sum(const float* part, int G, int cols, float* out, int accumulate, int late,
-                              cudaStream_t st) {
-  const dim3 grid((cols + 31) / 32);
-  if (G > 320) return launch_k(column_sum_kernel<32>, grid, dim3(1024), 0, st, 1, part, G, cols, out, accumulate, late);
-  return launch_k(column_sum_kernel<16>, grid, dim3(512), 0, st, 1, part, G, cols, out, accumulate, late);
+                              cudaStream_t st, const float* part2, float* out2) {
+  const dim3 grid((cols + 31) / 32, out2 ? 2 : 1);
+  if (G > 320)
+    return launch_k(column_sum_kernel<32>, grid, dim3(1024), 0, st, 1, part, G, cols, out, part2, out2, accumulate, late);
+  return launch_k(column_sum_kernel<16>, grid, dim3(512), 0, st, 1, part, G, cols, out, part2, out2, accumulate, late);
 }
 
 template <typename T>

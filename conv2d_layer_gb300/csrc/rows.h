@@ -25,8 +25,9 @@ struct DactPlan {
 DactPlan plan_dact(long rows, int cols, int sms);
 cudaError_t launch_dact(const conv2d_mat* z, const conv2d_mat& dy, long rows, int cols, int dt, int act, void* dz,
                         long lddz, float* part, const DactPlan& pl, int late, cudaStream_t st);
-// out[c] = (accumulate ? out[c] : 0) + sum over g of part[g][c], in the order of g.
-cudaError_t launch_column_sum(const float* part, int G, int cols, float* out, int accumulate, int late, cudaStream_t st);
+// out[c] = (accumulate ? out[c] : 0) + sum over g of part[g][c], in the order of g; out2 (null: none) from part2.
+cudaError_t launch_column_sum(const float* part, int G, int cols, float* out, int accumulate, int late, cudaStream_t st,
+                              const float* part2 = nullptr, float* out2 = nullptr);
 // Joins the splits of a weight gradient: out[r][c] (fp32 or dt, row length ldo) = (accumulate ? out : 0) +
 // sum over s of part[s][r][c], in the order of s.
 cudaError_t launch_split_join(const float* part, int splits, long rows, int cols, int type, void* out, long ldo,

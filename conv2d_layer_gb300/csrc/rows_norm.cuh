@@ -76,6 +76,48 @@ __device__ __forceinline__ uint32_t row_max(uint32_t v, uint32_t* red) {
   return v;
 }
 
+// Largest magnitude's bits; fmaxf passes NaN over, and infinities are looked for only where one shows.
+constexpr uint32_t kInf = 0x7f800000u;
+template <int V>
+__device__ __forceinline__ uint32_t absmax(const float (&o)[V]) {
+  float m = 0.f;
+#pragma unroll
+  for (int k = 0; k < V; ++k) m = fmaxf(m, fabsf(o[k]));
+  return __float_as_uint(m);
+}
+template <int V>
+__device__ __forceinline__ uint32_t absmax_finite(const float (&o)[V]) {
+  uint32_t m = 0u;
+#pragma unroll
+  for (int k = 0; k < V; ++k) m = max(m, finite_bits(o[k]));
+  return m;
+}
+// Largest finite magnitude's bits over the warp's threads that share a group of 32 or 128 columns (V = 1: of 32);
+// finite: no infinity among the warp's values. Warp-collective.
+template <int V>
+__device__ __forceinline__ uint32_t q8_group_max(int group, const float (&o)[V], bool& finite) {
+  auto join = [&](uint32_t m) {
+    if constexpr (V == 1) {  // the group is the warp
+      return __reduce_max_sync(0xffffffffu, m);
+    } else {
+#pragma unroll
+      for (int s = 1; s < kQ8Group / V; s <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, s));
+      if (group == kQ8Wide) {
+#pragma unroll
+        for (int s = kQ8Group / V; s < kQ8Wide / V; s <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, s));
+      }
+      return m;
+    }
+  };
+  uint32_t m = join(absmax(o));
+  finite = true;
+  if (__any_sync(0xffffffffu, m == kInf)) {
+    finite = false;
+    m = join(absmax_finite(o));
+  }
+  return m;
+}
+
 struct NormArgs {
   const void *x, *r;
   const float *gamma, *beta;  // beta: layer norm, may be null
@@ -86,9 +128,26 @@ struct NormArgs {
   long rows;
   int cols, ng;  // ng: scale bytes a row
   int group;     // 32, 128 or 0 (whole row)
+  int wide;      // gamma and beta start on 32-byte boundaries
   float eps;
 };
 enum : int { kEncode = 0, kRms = 1, kLayer = 2 };  // what rows_fwd_kernel computes
+
+// f over the pairs of U vectors, folded into one number: from zero, even and odd elements apart, then the two.
+template <int U, int V, typename F>
+__device__ __forceinline__ float row_fold(const float (&v)[U][V], F&& f) {
+  float2 s = make_float2(0.f, 0.f);
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    if constexpr (V == 1) {
+      s = f(s, make_float2(v[u][0], 0.f));
+    } else {
+#pragma unroll
+      for (int k = 0; k < V; k += 2) s = f(s, make_float2(v[u][k], v[u][k + 1]));
+    }
+  }
+  return V == 1 ? s.x : s.x + s.y;
+}
 
 // RMS norm or layer norm forward, or 8-bit encode (KIND): TPR threads a row, a block of them or (TPR = 32) eight warps. Rows are
 // held in registers between their sum of squares and their output, U vectors a thread, so memory is passed once;
@@ -170,33 +229,78 @@ __global__ void __launch_bounds__(TPR == 32 ? 256 : TPR) rows_fwd_kernel(const N
 #pragma unroll
   for (int i = 0; i < NR; ++i) inv[i] = 1.f;
   if constexpr (U > 0) load_all(0, UC);
-  if constexpr (KIND == kLayer) {
-    // The mean first, then the squares of the distances from it: their sum loses nothing where the mean is large
-    // against the deviation. Zeros past the end count in neither.
-    float sum[NR];
+  if constexpr (KIND == kLayer && U > 0) {
+    // Each warp takes the mean of its values and the squares of their distances from it, and the row's are joined from
+    // those: sum of squares = sum over warps of (theirs + count (their mean - the row's mean)^2). So nothing is lost where
+    // the mean is large against the deviation, and the block meets once.
+    const int warp = TPR > 32 ? t >> 5 : 0;
+    int count = 0;  // of this warp's values
 #pragma unroll
-    for (int i = 0; i < NR; ++i) sum[i] = 0.f;
-    if constexpr (U > 0) {
+    for (int u = 0; u < UC; ++u) count += V * min(max(nv - u * TPR - warp * 32, 0), 32);
+    const float n = static_cast<float>(count), over = count > 0 ? 1.f / n : 0.f;
+    float ss[NR];
+    [[maybe_unused]] __shared__ float4 part[NR][TPR / 32];
 #pragma unroll
-      for (int i = 0; i < NR; ++i)
+    for (int i = 0; i < NR; ++i) {
+      float sum = row_fold<UC, V>(v[i], [](float2 s, float2 e) { return __fadd2_rn(s, e); });
+      sum = warp_sum(sum);
+      mean[i] = TPR > 32 ? sum * over : sum / n;
+      const float2 shift = make_float2(-mean[i], -mean[i]);
+      ss[i] = 0.f;
 #pragma unroll
-        for (int u = 0; u < UC; ++u)
+      for (int u = 0; u < UC; ++u)
+        if (u * TPR + t < nv)  // zeros past the end count in neither
+          ss[i] += row_fold<1, V>(reinterpret_cast<float(&)[1][V]>(v[i][u]), [&](float2 s, float2 e) {
+            const float2 d = __fadd2_rn(e, shift);
+            return __ffma2_rn(d, d, s);
+          });
+      ss[i] = warp_sum(ss[i]);
+      if (TPR > 32 && (t & 31) == 0) part[i][warp] = make_float4(sum, ss[i], mean[i], n);
+    }
+    if constexpr (TPR > 32) {
+      __syncthreads();
 #pragma unroll
-          for (int k = 0; k < V; ++k) sum[i] += v[i][u][k];
-    } else {
-      for (int u = 0; u < nu; ++u) {
-        load_all(u, 1);
+      for (int i = 0; i < NR; ++i) {
+        float sum = 0.f;
+        ss[i] = 0.f;
 #pragma unroll
-        for (int k = 0; k < V; ++k) sum[0] += v[0][0][k];
+        for (int w = 0; w < TPR / 32; ++w) sum += part[i][w].x;
+        mean[i] = sum / static_cast<float>(a.cols);
+#pragma unroll
+        for (int w = 0; w < TPR / 32; ++w) {
+          const float4 p = part[i][w];
+          const float d = p.z - mean[i];
+          ss[i] += fmaf(p.w * d, d, p.y);
+        }
       }
     }
 #pragma unroll
     for (int i = 0; i < NR; ++i) {
-      mean[i] = row_sum<TPR>(sum[i], red) / static_cast<float>(a.cols);
-      if (t == 0 && i < nr && a.mean) a.mean[row0 + i] = mean[i];
+      inv[i] = 1.f / sqrtf(ss[i] / static_cast<float>(a.cols) + a.eps);
+      if (t == 0 && i < nr) {
+        if (a.mean) a.mean[row0 + i] = mean[i];
+        if (a.inv) a.inv[row0 + i] = inv[i];
+      }
     }
-  }
-  if constexpr (KIND != kEncode) {
+  } else if constexpr (KIND == kLayer) {  // long rows, read again: the mean, then the squares of the distances from it
+    float sum = 0.f, ss = 0.f;
+    for (int u = 0; u < nu; ++u) {
+      load_all(u, 1);
+#pragma unroll
+      for (int k = 0; k < V; ++k) sum += v[0][0][k];
+    }
+    mean[0] = row_sum<TPR>(sum, red) / static_cast<float>(a.cols);
+    for (int u = 0; u < nu; ++u) {
+      reload(u);
+#pragma unroll
+      for (int k = 0; k < V; ++k) ss = fmaf(v[0][0][k], v[0][0][k], ss);
+    }
+    inv[0] = 1.f / sqrtf(row_sum<TPR>(ss, red) / static_cast<float>(a.cols) + a.eps);
+    if (t == 0) {
+      if (a.mean) a.mean[row0] = mean[0];
+      if (a.inv) a.inv[row0] = inv[0];
+    }
+  } else if constexpr (KIND == kRms) {
     float ss[NR];
 #pragma unroll
     for (int i = 0; i < NR; ++i) ss[i] = 0.f;
@@ -204,18 +308,12 @@ __global__ void __launch_bounds__(TPR == 32 ? 256 : TPR) rows_fwd_kernel(const N
 #pragma unroll
       for (int i = 0; i < NR; ++i)
 #pragma unroll
-        for (int u = 0; u < UC; ++u) {
-          if (KIND == kLayer && u * TPR + t >= nv) break;
+        for (int u = 0; u < UC; ++u)
 #pragma unroll
-          for (int k = 0; k < V; ++k) {
-            if constexpr (KIND == kLayer) v[i][u][k] -= mean[i];
-            ss[i] = fmaf(v[i][u][k], v[i][u][k], ss[i]);
-          }
-        }
+          for (int k = 0; k < V; ++k) ss[i] = fmaf(v[i][u][k], v[i][u][k], ss[i]);
     } else {
       for (int u = 0; u < nu; ++u) {
-        if constexpr (KIND == kLayer) reload(u);
-        else load_all(u, 1);
+        load_all(u, 1);
 #pragma unroll
         for (int k = 0; k < V; ++k) ss[0] = fmaf(v[0][0][k], v[0][0][k], ss[0]);
       }
@@ -242,35 +340,49 @@ __global__ void __launch_bounds__(TPR == 32 ? 256 : TPR) rows_fwd_kernel(const N
       }
     };
     float g[V];
-    feature(a.gamma, g);
+    if constexpr (KIND == kRms) {
+      feature(a.gamma, g);
 #pragma unroll
-    for (int i = 0; i < NR; ++i)
+      for (int i = 0; i < NR; ++i)
 #pragma unroll
-      for (int k = 0; k < V; ++k) v[i][slot][k] = v[i][slot][k] * inv[i] * g[k];
-    if constexpr (KIND == kLayer) {
-      if (a.beta) {
-        feature(a.beta, g);
+        for (int k = 0; k < V; ++k) v[i][slot][k] = v[i][slot][k] * inv[i] * g[k];
+    } else {
+      // in sectors where the vectors start on them: neighbouring threads' 16-byte pieces of 16 features lie 64 bytes
+      // apart, so that each such load passes four times the lines
+      if (V >= 8 && a.wide) {
 #pragma unroll
-        for (int i = 0; i < NR; ++i)
+        for (int k = 0; k < V; k += 8) ld_32b(a.gamma + static_cast<long>(c) * V + k, reinterpret_cast<uint32_t(&)[8]>(g[k]));
+      } else {
+        feature(a.gamma, g);
+      }
+      float b[V];
+      if (!a.beta) {
 #pragma unroll
-          for (int k = 0; k < V; ++k) v[i][slot][k] += g[k];
+        for (int k = 0; k < V; ++k) b[k] = 0.f;
+      } else if (V >= 8 && a.wide) {
+#pragma unroll
+        for (int k = 0; k < V; k += 8) ld_32b(a.beta + static_cast<long>(c) * V + k, reinterpret_cast<uint32_t(&)[8]>(b[k]));
+      } else {
+        feature(a.beta, b);
+      }
+#pragma unroll
+      for (int i = 0; i < NR; ++i) {
+        const float m = U > 0 ? mean[i] : 0.f;  // U = 0: taken off where the row is read again
+        if constexpr (V == 1) {
+          v[i][slot][0] = fmaf((v[i][slot][0] - m) * inv[i], g[0], b[0]);
+        } else {
+#pragma unroll
+          for (int k = 0; k < V; k += 2) {
+            float2 e = __fadd2_rn(make_float2(v[i][slot][k], v[i][slot][k + 1]), make_float2(-m, -m));
+            e = __fmul2_rn(e, make_float2(inv[i], inv[i]));
+            e = __ffma2_rn(e, make_float2(g[k], g[k + 1]), make_float2(b[k], b[k + 1]));
+            v[i][slot][k] = e.x;
+            v[i][slot][k + 1] = e.y;
+          }
+        }
       }
     }
   };
-  // Largest magnitude's bits; fmaxf passes NaN over, and infinities are looked for only where one shows.
-  auto absmax = [&](const float (&o)[V]) {
-    float m = 0.f;
-#pragma unroll
-    for (int k = 0; k < V; ++k) m = fmaxf(m, fabsf(o[k]));
-    return __float_as_uint(m);
-  };
-  auto absmax_finite = [&](const float (&o)[V]) {
-    uint32_t m = 0u;
-#pragma unroll
-    for (int k = 0; k < V; ++k) m = max(m, finite_bits(o[k]));
-    return m;
-  };
-  constexpr uint32_t kInf = 0x7f800000u;
   uint32_t rowbyte[NR];
   bool rowfinite[NR];
   if (a.q && a.group == 0) {
@@ -338,25 +450,7 @@ __global__ void __launch_bounds__(TPR == 32 ? 256 : TPR) rows_fwd_kernel(const N
             for (int w = 0; w < 4; ++w) m = max(m, wide[u & 1][(warp & ~3) + w]);
             finite = false;
           } else {
-            auto group_max = [&](uint32_t m) {
-              if constexpr (V == 1) {  // the group is the warp
-                return __reduce_max_sync(0xffffffffu, m);
-              } else {
-#pragma unroll
-                for (int s = 1; s < kQ8Group / V; s <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, s));
-                if (a.group == kQ8Wide) {
-#pragma unroll
-                  for (int s = kQ8Group / V; s < kQ8Wide / V; s <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, s));
-                }
-                return m;
-              }
-            };
-            m = group_max(absmax(o));
-            finite = true;
-            if (__any_sync(0xffffffffu, m == kInf)) {
-              finite = false;
-              m = group_max(absmax_finite(o));
-            }
+            m = q8_group_max(a.group, o, finite);
           }
           byte = q8_scale_byte(m);
           const int per = a.group / V;  // threads a group
