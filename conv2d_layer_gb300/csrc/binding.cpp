@@ -470,6 +470,7 @@ PyObject* dense_bwd(PyObject* const* a) {
   if (act) {
     if (!given(a[3])) refuse("pre_act", "needed behind an activation");
     z = mat(a[3], "pre_act", M, N, bit | kE4M3, s.dev);
+    if (is_q8(a[3]) && z.group != kGroup && z.group != 0) refuse("pre_act", "groups of 32 or a whole row");
   }
   if (need_dw && need_db && given(a[7]) != given(a[8]))
     throw Refused{"dw and dbias: hand in both to accumulate, or neither"};

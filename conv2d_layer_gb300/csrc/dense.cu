@@ -54,8 +54,9 @@ struct GemmPlan {
 // run in waves over the SMs; the pair kernel hides its epilogue under the next unit's loop. can_split: the product
 // may be split over k, with fp32 partials in the workspace; max_kb: bound on one accumulator's k-blocks, short_kb: those
 // it had better not pass (0: none).
-GemmPlan plan_gemm(int mode, long m, long n, int kb, int sms, bool can_split = false, int max_kb = 0, int short_kb = 0) {
-  const bool r_mn = dense_r_mn(mode), c_mn = dense_c_mn(mode);
+GemmPlan plan_gemm(int mode, long m, long n, int kb, int sms, int q = kHalves, bool can_split = false, int max_kb = 0,
+                   int short_kb = 0) {
+  const bool r_mn = dense_r_mn(mode), c_mn = dense_c_mn(mode), blocks = q == kBlockScaled;
   GemmPlan best = {};
   double best_t = 1e300;
   auto consider = [&](bool pair, int BN, int cl, int splits) {
@@ -117,22 +118,24 @@ GemmPlan plan_gemm(int mode, long m, long n, int kb, int sms, bool can_split = f
       if (s > 1) consider(pair, BN, cl, static_cast<int>(s));
     }
   };
-  for (int BN : {256, 224, 192, 160, 128}) splits_of(true, BN, 1);
+  for (int BN : {256, 224, 192, 160, 128})
+    if (!blocks || BN < 256) splits_of(true, BN, 1);  // blocks' scales need columns of the tensor memory beside the sums
   for (int BN : {128, 64, 32, 16}) {
     if (r_mn && BN < 64) continue;  // MN-major tiles are panels of 64
     for (int cl : {1, 2, 4, 8})
       if (cl == 1 || kb >= 2 * cl) splits_of(false, BN, cl);
   }
   int c_rows = best.BN;  // columns of C a CTA brings: MN-major in whole panels of 64
-  if (best.pair) c_rows = c_mn ? static_cast<int>(round_up(best.BN / 2, 64)) : best.BN / 2;
+  if (best.pair) c_rows = c_mn ? static_cast<int>(round_up(best.BN / 2, q == kHalves ? 64 : 128)) : best.BN / 2;
   const int need = static_cast<int>(ceil_div(best.kb_per_split, best.cluster));  // k-blocks of a CTA
-  const int stage = (128 + c_rows) * 128;
+  const int stage = (128 + c_rows) * 128 + (blocks ? dense_slot_bytes(best.BN) : 0);
   const int room = static_cast<int>(kMaxDynSmem) - 1536 - (best.pair ? kPairBuffers : 0);
   const long units = static_cast<long>(best.l_tiles) * best.c_tiles * best.splits;
   const int join = best.cluster > 1 ? best.cluster * dense_own_cols(best.BN, best.cluster) * 512 : 0;
   if (best.pair) {
     best.grid = 2 * static_cast<int>(std::min<long>(units, sms / 2));
     best.stages = std::min(kDenseMaxStages, room / stage);
+    if (blocks) best.stages = std::min(best.stages, (512 - 2 * best.BN) / dense_slot_cols(best.BN));
   } else {
     best.grid = static_cast<int>(units) * best.cluster;
     best.stages = std::max(2, std::min({kDenseMaxStages, (room - join) / stage, need}));
@@ -150,14 +153,14 @@ GemmPlan plan_gemm(int mode, long m, long n, int kb, int sms, bool can_split = f
 
 // ------------------------------------------------------------------ tensor maps
 // Row-major matrix [rows][cols] of row length ld as a GEMM operand, 128-byte swizzle: K-major, boxes of 128
-// bytes x box_rows; MN-major, boxes of 64 elements x 64 rows.
+// bytes x box_rows; MN-major, boxes of 128 bytes x a k-block: 64 x 64 of 16 bits, 128 x 128 of 8.
 bool encode_operand(CUtensorMap* m, const void* base, int type, long rows, long cols, long ld, bool mn, int box_rows) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return false;
   const int es = type == CONV2D_E4M3 ? 1 : 2;
   cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
   cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld) * es};
-  cuuint32_t box[2] = {static_cast<cuuint32_t>(128 / es), static_cast<cuuint32_t>(mn ? 64 : box_rows)};
+  cuuint32_t box[2] = {static_cast<cuuint32_t>(128 / es), static_cast<cuuint32_t>(mn ? 128 / es : box_rows)};
   cuuint32_t estr[2] = {1, 1};
   const CUtensorMapDataType dt = type == CONV2D_E4M3   ? CU_TENSOR_MAP_DATA_TYPE_UINT8
                                  : type == CONV2D_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
@@ -192,7 +195,22 @@ struct Operand {
   const void* data;
   int type;
   long rows, cols, ld;
+  DenseScales scales;  // of a block-scaled product
 };
+
+// Scales of an 8-bit matrix [rows][cols] with a scale for 128 columns or a tile, as an operand summed over its columns, or
+// (down) over its rows, which are tiled.
+DenseScales block_scales(const uint8_t* scale, int group, long rows, long cols, bool down) {
+  const long ng = ceil_div(cols, kQ8Wide);
+  DenseScales s = {};
+  s.p = scale;
+  s.row_shift = down || group == kQ8Tile ? 7 : 0;
+  s.row_step = down ? 1 : ng;
+  s.block_step = down ? ng : 1;
+  s.rows = down ? cols : rows;
+  s.words = !down && ng % 4 == 0 && (reinterpret_cast<uintptr_t>(scale) & 3u) == 0;
+  return s;
+}
 
 // out[m][n] = sum_k R[m][k] C[n][k]. The rows of the output are the accumulator's lanes in the pair kernel and its
 // columns in the cluster kernel.
@@ -203,7 +221,9 @@ int run_gemm(DenseGemmParams& p, const GemmPlan& g, const Operand& r, const Oper
   if (!encode_operand(&p.tl, lo.data, lo.type, lo.rows, lo.cols, lo.ld, g.pair ? r_mn : c_mn, 128) ||
       !encode_operand(&p.tc, co.data, co.type, co.rows, co.cols, co.ld, g.pair ? c_mn : r_mn, g.pair ? g.BN / 2 : g.BN))
     return CONV2D_ERR_CUDA;
-  const bool fp8 = r.type == CONV2D_E4M3;
+  const int q = r.type != CONV2D_E4M3 ? kHalves : r.scales.p ? kBlockScaled : kRowScaled;
+  p.sl = lo.scales;
+  p.sc = co.scales;
   p.fmt = r.type == CONV2D_BF16 ? 1u : 0u;
   p.m = r_mn ? r.cols : r.rows;
   p.n = static_cast<int>(c_mn ? c.cols : c.rows);
@@ -242,8 +262,8 @@ int run_gemm(DenseGemmParams& p, const GemmPlan& g, const Operand& r, const Oper
   p.stages = g.stages;
   p.cluster = g.cluster;
   p.err = dev->err;
-  LAUNCH(name, st, g.pair ? launch_dense_pair(p, dt, mode, fp8, g.grid, g.smem, st)
-                          : launch_dense_cluster(p, dt, mode, fp8, g.grid, g.smem, st));
+  LAUNCH(name, st, g.pair ? launch_dense_pair(p, dt, mode, q, g.grid, g.smem, st)
+                          : launch_dense_cluster(p, dt, mode, q, g.grid, g.smem, st));
   return CONV2D_OK;
 }
 
@@ -256,20 +276,22 @@ int check_desc(const conv2d_dense_desc* d) {
   if (d->M > INT_MAX / 2 || d->K > (1 << 28) || d->N > (1 << 28)) return CONV2D_ERR_UNSUPPORTED;
   return CONV2D_OK;
 }
-// The shape part of a matrix argument: type among the layer's, ld at least cols, known group.
-int check_shape(const conv2d_mat* m, int cols, int dtype, bool q8) {
+// The shape part of a matrix argument: type among the layer's, ld at least cols, known group (wide: those of 128 too).
+int check_shape(const conv2d_mat* m, int cols, int dtype, bool q8, bool wide = false) {
   if (!m || (m->ld != 0 && m->ld < cols)) return CONV2D_ERR_INVALID_ARG;
   if (m->type == CONV2D_E4M3)
-    return q8 && (m->group == 0 || m->group == kQ8Group) ? CONV2D_OK : CONV2D_ERR_INVALID_ARG;
+    return q8 && (wide ? q8_known(m->group) : m->group == 0 || m->group == kQ8Group) ? CONV2D_OK : CONV2D_ERR_INVALID_ARG;
   return m->type == dtype ? CONV2D_OK : CONV2D_ERR_INVALID_ARG;
 }
 int check_data(const conv2d_mat* m) {
   return m->data && aligned16(m->data) && (m->type != CONV2D_E4M3 || m->scale) ? CONV2D_OK : CONV2D_ERR_INVALID_ARG;
 }
 
-// Whether x and w run as they are on the 8-bit tensor core path.
-bool both_8bit(const conv2d_mat* x, const conv2d_mat* w) {
-  return x->type == CONV2D_E4M3 && w->type == CONV2D_E4M3 && x->group == 0 && w->group == 0;
+// How the forward product runs: on the 8-bit operands as they are, where their scales allow it.
+int product_kind(const conv2d_mat* x, const conv2d_mat* w) {
+  if (x->type != CONV2D_E4M3 || w->type != CONV2D_E4M3) return kHalves;
+  if (x->group == 0 && w->group == 0) return kRowScaled;
+  return x->group == kQ8Wide && (w->group == kQ8Wide || w->group == kQ8Tile) ? kBlockScaled : kHalves;
 }
 
 // ------------------------------------------------------------------ workspace
@@ -296,7 +318,7 @@ size_t plan_copy(Carver& c, const conv2d_mat* m, long rows, int cols, bool as_8b
 // The operand itself, or its copy in the workspace; *started: a kernel of this call has been launched.
 int make_operand(Operand* o, const conv2d_mat* m, long rows, int cols, bool as_8bit, int dt, size_t off, void* ws,
                  const char* name, bool* started, cudaStream_t st) {
-  *o = {m->data, as_8bit ? static_cast<int>(CONV2D_E4M3) : dt, rows, cols, ld_of(m, cols)};
+  *o = {m->data, as_8bit ? static_cast<int>(CONV2D_E4M3) : dt, rows, cols, ld_of(m, cols), {}};
   if (off == kNone) return CONV2D_OK;
   char* to = static_cast<char*>(ws) + off;
   o->data = to;
@@ -313,23 +335,26 @@ size_t plan_join(Carver& c, const GemmPlan& g) { return g.parts > 1 ? c.take(g.j
 void* at(void* ws, size_t off) { return off == kNone ? nullptr : static_cast<char*>(ws) + off; }
 
 struct FwdPlan {
-  bool fp8;
+  int kind;
   size_t x, w, join, total;
   GemmPlan g;
 };
 void plan_fwd(const conv2d_dense_desc& d, const conv2d_mat* x, const conv2d_mat* w, int sms, FwdPlan* pl) {
   Carver c;
-  pl->fp8 = both_8bit(x, w);
-  pl->x = plan_copy(c, x, d.M, d.K, pl->fp8);
-  pl->w = plan_copy(c, w, d.N, d.K, pl->fp8);
-  pl->g = plan_gemm(kDenseForward, d.M, d.N, static_cast<int>(ceil_div(d.K, pl->fp8 ? 128 : 64)), sms);
+  pl->kind = product_kind(x, w);
+  const bool as8 = pl->kind != kHalves;
+  pl->x = plan_copy(c, x, d.M, d.K, as8);
+  pl->w = plan_copy(c, w, d.N, d.K, as8);
+  pl->g = plan_gemm(kDenseForward, d.M, d.N, static_cast<int>(ceil_div(d.K, as8 ? 128 : 64)), sms, pl->kind);
   pl->join = plan_join(c, pl->g);
   pl->total = c.size();
 }
 
 struct BwdPlan {
   bool dz_own;  // dz is formed in the workspace (else it is dy)
-  long lddz;
+  bool dx8;     // dx is a product of 8-bit operands: dz goes to 8 bits, a scale for 128 columns
+  long lddz, lddz8;
+  size_t dz8, dz8s;
   long pass_rows;  // rows of a pass of dW (M: one pass)
   int planes;      // fp32 partials of dW in the workspace, joined at the end (0: dW is written by the product)
   size_t dz, x, w, dpart, spart, joinx, joinw, total;
@@ -339,16 +364,23 @@ struct BwdPlan {
 void plan_bwd(const conv2d_dense_desc& d, const conv2d_mat* x, const conv2d_mat* w, const conv2d_mat* dy, bool dx,
               const conv2d_mat* dw, bool dbias, int sms, BwdPlan* pl) {
   Carver c;
-  const bool gemm = dx || dw;
+  pl->dx8 = dx && w->type == CONV2D_E4M3 && w->group == kQ8Tile;
+  pl->lddz8 = round_up(d.N, 16);
   pl->lddz = round_up(d.N, 8);
-  pl->dz_own = gemm && (d.act != CONV2D_ACT_IDENTITY || ld_of(dy, d.N) % 8 != 0);
+  // dy itself where it is dz, in rows that a product takes; the encoder takes any
+  pl->dz_own = (dx || dw) && (d.act != CONV2D_ACT_IDENTITY || (ld_of(dy, d.N) % 8 != 0 && (dw || !pl->dx8)));
   pl->dz = pl->dz_own ? c.take(static_cast<size_t>(d.M) * pl->lddz * 2) : kNone;
   pl->dact = plan_dact(d.M, d.N, sms);
   pl->dpart = dbias ? c.take(static_cast<size_t>(pl->dact.strips) * d.N * 4) : kNone;
   pl->w = pl->x = pl->spart = pl->joinx = pl->joinw = kNone;
   if (dx) {
-    pl->w = plan_copy(c, w, d.N, d.K, false);
-    pl->gx = plan_gemm(kDenseDx, d.M, d.K, static_cast<int>(ceil_div(d.N, 64)), sms);
+    pl->w = plan_copy(c, w, d.N, d.K, pl->dx8);
+    if (pl->dx8) {
+      pl->dz8 = c.take(static_cast<size_t>(d.M) * pl->lddz8);
+      pl->dz8s = c.take(static_cast<size_t>(d.M) * ceil_div(d.N, kQ8Wide));
+    }
+    pl->gx = plan_gemm(kDenseDx, d.M, d.K, static_cast<int>(ceil_div(d.N, pl->dx8 ? 128 : 64)), sms,
+                       pl->dx8 ? kBlockScaled : kHalves);
     pl->joinx = plan_join(c, pl->gx);
   }
   if (dw) {
@@ -367,7 +399,7 @@ void plan_bwd(const conv2d_dense_desc& d, const conv2d_mat* x, const conv2d_mat*
                                        pieces * d.N * d.K * 4 > (2L << 30));
     pl->pass_rows = passes ? bound * 64L : d.M;
     pl->gw = passes ? plan_gemm(kDenseDw, d.N, d.K, bound, sms)
-                    : plan_gemm(kDenseDw, d.N, d.K, kb, sms, true, bound, f32 ? kFp32ShortKb : 0);
+                    : plan_gemm(kDenseDw, d.N, d.K, kb, sms, kHalves, true, bound, f32 ? kFp32ShortKb : 0);
     pl->joinw = plan_join(c, pl->gw);
     pl->planes = passes ? (f32 ? 0 : 1) : pl->gw.splits > 1 ? pl->gw.splits : 0;
     if (pl->planes) pl->spart = c.take(static_cast<size_t>(pl->planes) * d.N * d.K * 4);
@@ -382,10 +414,10 @@ int check_bwd_shapes(const conv2d_dense_desc* d, const conv2d_mat* x, const conv
   if (!dx && !dw && !dbias) return CONV2D_ERR_INVALID_ARG;
   if ((rc = check_shape(dy, d->N, d->dtype, false))) return rc;
   if (d->act != CONV2D_ACT_IDENTITY && (rc = check_shape(z, d->N, d->dtype, true))) return rc;
-  if (dx && ((rc = check_shape(dx, d->K, d->dtype, false)) || (rc = check_shape(w, d->K, d->dtype, true)))) return rc;
+  if (dx && ((rc = check_shape(dx, d->K, d->dtype, false)) || (rc = check_shape(w, d->K, d->dtype, true, true)))) return rc;
   if (dw) {
     if ((rc = check_shape(dw, d->K, dw->type == CONV2D_FP32 ? CONV2D_FP32 : d->dtype, false))) return rc;
-    if ((rc = check_shape(x, d->K, d->dtype, true))) return rc;
+    if ((rc = check_shape(x, d->K, d->dtype, true, true))) return rc;
   }
   return CONV2D_OK;
 }
@@ -395,7 +427,7 @@ int check_bwd_shapes(const conv2d_dense_desc* d, const conv2d_mat* x, const conv
 extern "C" {
 
 size_t conv2d_dense_fwd_workspace_size(const conv2d_dense_desc* d, const conv2d_mat* x, const conv2d_mat* w) {
-  if (check_desc(d) || check_shape(x, d->K, d->dtype, true) || check_shape(w, d->K, d->dtype, true)) return 0;
+  if (check_desc(d) || check_shape(x, d->K, d->dtype, true, true) || check_shape(w, d->K, d->dtype, true, true)) return 0;
   FwdPlan pl;
   plan_fwd(*d, x, w, sms_for_sizing(), &pl);
   return pl.total;
@@ -415,7 +447,7 @@ int conv2d_dense_fwd(const conv2d_dense_desc* d, const conv2d_mat* x, const conv
                      size_t ws_bytes, void* stream) {
   int rc = check_desc(d);
   if (rc) return rc;
-  if ((rc = check_shape(x, d->K, d->dtype, true)) || (rc = check_shape(w, d->K, d->dtype, true)) ||
+  if ((rc = check_shape(x, d->K, d->dtype, true, true)) || (rc = check_shape(w, d->K, d->dtype, true, true)) ||
       (rc = check_shape(y, d->N, d->dtype, false)))
     return rc;
   if (residual && (rc = check_shape(residual, d->N, d->dtype, false))) return rc;
@@ -435,12 +467,16 @@ int conv2d_dense_fwd(const conv2d_dense_desc* d, const conv2d_mat* x, const conv
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   Operand ox, ow;
   bool started = false;
-  if ((rc = make_operand(&ox, x, d->M, d->K, pl.fp8, d->dtype, pl.x, ws, "dense_x", &started, st))) return rc;
-  if ((rc = make_operand(&ow, w, d->N, d->K, pl.fp8, d->dtype, pl.w, ws, "dense_w", &started, st))) return rc;
+  const bool as8 = pl.kind != kHalves;
+  if ((rc = make_operand(&ox, x, d->M, d->K, as8, d->dtype, pl.x, ws, "dense_x", &started, st))) return rc;
+  if ((rc = make_operand(&ow, w, d->N, d->K, as8, d->dtype, pl.w, ws, "dense_w", &started, st))) return rc;
   DenseGemmParams p = {};
-  if (pl.fp8) {
+  if (pl.kind == kRowScaled) {
     p.ns = w->scale;
     p.ms = x->scale;
+  } else if (pl.kind == kBlockScaled) {
+    ox.scales = block_scales(x->scale, x->group, d->M, d->K, false);
+    ow.scales = block_scales(w->scale, w->group, d->N, d->K, false);
   }
   p.bias = bias;
   p.act = d->act;
@@ -493,9 +529,9 @@ int conv2d_dense_bwd(const conv2d_dense_desc* d, const conv2d_mat* x, const conv
   // beside it (they share their inputs only), and the bias gradient beside both.
   bool started = false;
   Operand ow, ox;
-  if (dx && (rc = make_operand(&ow, w, d->N, d->K, false, d->dtype, pl.w, ws, "dense_w", &started, st))) return rc;
+  if (dx && (rc = make_operand(&ow, w, d->N, d->K, pl.dx8, d->dtype, pl.w, ws, "dense_w", &started, st))) return rc;
   if (dw && (rc = make_operand(&ox, x, d->M, d->K, false, d->dtype, pl.x, ws, "dense_x", &started, st))) return rc;
-  Operand odz = {dy->data, d->dtype, d->M, d->N, ld_of(dy, d->N)};
+  Operand odz = {dy->data, d->dtype, d->M, d->N, ld_of(dy, d->N), {}};
   float* part = dbias ? reinterpret_cast<float*>(base + pl.dpart) : nullptr;
   if (pl.dz_own || dbias) {
     void* dz = pl.dz_own ? base + pl.dz : nullptr;
@@ -513,7 +549,15 @@ int conv2d_dense_bwd(const conv2d_dense_desc* d, const conv2d_mat* x, const conv
     DenseGemmParams p = {};
     p.out = dx->data;
     p.ldo = ld_of(dx, d->K);
-    if ((rc = run_gemm(p, pl.gx, odz, ow, d->dtype, kDenseDx, at(ws, pl.joinx), false, "dense_dx", dev, st))) return rc;
+    Operand o = odz;
+    if (pl.dx8) {
+      const conv2d_mat dz = {const_cast<void*>(odz.data), odz.ld, d->dtype, 0, nullptr};
+      const conv2d_mat dz8 = {base + pl.dz8, pl.lddz8, CONV2D_E4M3, kQ8Wide, reinterpret_cast<uint8_t*>(base + pl.dz8s)};
+      if ((rc = conv2d_q8_encode(d->M, d->N, &dz, &dz8, stream))) return rc;
+      o = {dz8.data, CONV2D_E4M3, d->M, d->N, pl.lddz8, block_scales(dz8.scale, kQ8Wide, d->M, d->N, false)};
+      ow.scales = block_scales(w->scale, kQ8Tile, d->N, d->K, true);
+    }
+    if ((rc = run_gemm(p, pl.gx, o, ow, d->dtype, kDenseDx, at(ws, pl.joinx), false, "dense_dx", dev, st))) return rc;
   }
   const bool joined = dw && pl.planes > 0;
   if (dw) {

@@ -43,10 +43,22 @@ enum : int { kDenseForward = 0, kDenseDx = 1, kDenseDw = 2, kDenseDwAdd = 3 };
 __host__ __device__ constexpr bool dense_r_mn(int mode) { return mode >= kDenseDw; }
 __host__ __device__ constexpr bool dense_c_mn(int mode) { return mode != kDenseForward; }
 
+// How a product's operands are held: 16 bits; 8 bits with a scale for each row, which the epilogue applies; 8 bits with a
+// scale for each row (or 128 of them) and block of 128 of k, which the tensor core applies.
+enum : int { kHalves = 0, kRowScaled = 1, kBlockScaled = 2 };
+// Scale bytes of a block-scaled operand: that of row i and block b is p[(i >> row_shift) * row_step + b * block_step];
+// words: four blocks' bytes of a row are an aligned word.
+struct DenseScales {
+  const uint8_t* p;
+  long row_step, block_step, rows;
+  int row_shift, words;
+};
+
 struct DenseGemmParams {
   CUtensorMap tl, tc;   // the operands whose rows are the accumulator's lanes / columns
   // pair kernel: out and z (zq) as {columns, rows, splits} for stores of 32 rows x 64 bytes (zq: 32 bytes)
   CUtensorMap tout, tz;
+  DenseScales sl, sc;   // kBlockScaled: their scales
   uint32_t fmt;         // instruction descriptor's operand format: fp16 0, bf16 1, e4m3 0
   int n;                // columns of the output
   long m;               // rows of the output
@@ -103,6 +115,65 @@ __device__ __forceinline__ void mma_f8_pair(uint32_t d, uint64_t a, uint64_t b, 
       "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
       "l"(a), "l"(b), "r"(idesc), "r"(acc)
       : "memory");
+}
+
+// The block-scaled product of e4m3 operands: the partial sums of each 32 of k are multiplied by the operands' scales
+// (2^(byte - 127)) before they are added up. The scales lie in tensor memory, row r's in lane r % 32 (of each lane
+// quarter) and column r / 32 from sfa / sfb, four bytes of which the descriptor picks one.
+__device__ __forceinline__ void mma_block(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa, uint32_t sfb,
+                                          uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void mma_block_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa,
+                                               uint32_t sfb, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(acc)
+      : "memory");
+}
+// 512 bytes of shared memory, 32 rows of 16 bytes, into four columns of tensor memory, the same in each lane quarter.
+// In order with the MMAs that this thread issues after it; a pair's both CTAs copy from their own shared memory.
+template <bool PAIR>
+__device__ __forceinline__ void tmem_copy_scales(uint32_t taddr, uint64_t desc) {
+  if (PAIR) asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+  else asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+}
+// Descriptor of those 512 bytes: no swizzle, 8 rows of 16 bytes after each other.
+__device__ __forceinline__ uint64_t scales_desc(uint32_t saddr) {
+  return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | static_cast<uint64_t>(128 >> 4) << 32 | static_cast<uint64_t>(1) << 46;
+}
+// Instruction descriptor of the block-scaled e4m3 product, without the scales' byte numbers (bits 4 and 29).
+__device__ __forceinline__ uint32_t idesc_block(int M, int N, bool a_mn, bool b_mn) {
+  return ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) | (static_cast<uint32_t>(N >> 3) << 17) | (1u << 23) |
+         (static_cast<uint32_t>(M >> 4) << 24);
+}
+// Bytes that a phase waits for, without an arrival.
+__device__ __forceinline__ void mbar_expect_tx(uint64_t* bar, uint32_t bytes) {
+  asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
+}
+// wait() for a phase that another CTA of the cluster arrives on after writing its own shared memory.
+__device__ __forceinline__ bool wait_cluster(uint64_t* bar, uint32_t parity, int* err, int site) {
+  const uint64_t t0 = globaltimer();
+#pragma unroll 1
+  for (uint32_t i = 0;; ++i) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, "
+        "p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    if (ok) return true;
+    if ((i & 1023u) == 1023u && globaltimer() - t0 > kWaitLimitNs) {
+      atomicCAS(err, 0, site);
+      return false;
+    }
+  }
 }
 
 // 3-D tiled store of a box from shared memory; part of the thread's current bulk group.
@@ -372,7 +443,7 @@ __device__ __forceinline__ void residual_add(uint32_t buf, float* v, int lane) {
 // res: the residual's registers, loaded for these columns and left loading for the columns from n + 128 (the
 // warp's next), so that its way from memory is hidden by the main loop or by the columns before. taken(a) is
 // called when the accumulator's columns are in a[] (it frees the accumulator, and adds other parts' sums).
-template <typename T, int MODE, bool FP8, typename F>
+template <typename T, int MODE, int Q, typename F>
 __device__ __forceinline__ void pair_epilogue(const DenseGemmParams& p, uint32_t taddr, uint32_t buf, long m0, int n,
                                               int end, int nr, int split, uint32_t mscale, uint32_t (&res)[16], int lane,
                                               F&& taken) {
@@ -387,7 +458,7 @@ __device__ __forceinline__ void pair_epilogue(const DenseGemmParams& p, uint32_t
 #pragma unroll
       for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(a[e]);
     }
-    if constexpr (FP8) {
+    if constexpr (Q == kRowScaled) {
       const float2 f = q8_factors(mscale);
 #pragma unroll
       for (int e = 0; e < 32; e += 2) {
@@ -523,12 +594,12 @@ __device__ __forceinline__ void pair_epilogue(const DenseGemmParams& p, uint32_t
 
 // ---------------------------------------------------------------- operands
 // One k-block of an operand's `rows` rows from row r0 into shared memory at dst. K-major: one box of 128
-// bytes x rows. MN-major: panels of 64 rows (128 bytes) x 64 k, 8 KB each.
-template <bool PAIR, bool MN>
+// bytes x rows. MN-major: panels of 128 bytes of rows x the k-block: 64 x 64 of 16 bits, 8 KB each, or 128 x 128 of 8 bits.
+template <bool PAIR, bool MN, bool BYTES>
 __device__ __forceinline__ void dense_load(const CUtensorMap* m, uint32_t dst, uint64_t* bar, uint32_t pbar, int kelem,
                                            int r0, int rows) {
   if (MN) {
-    for (int j = 0; j < rows; j += 64) {
+    for (int j = 0; j < rows; j += BYTES ? 128 : 64) {
       if (PAIR) tma_load_2d_pair(dst + j * 128, m, pbar, r0 + j, kelem);
       else tma_load_2d(dst + j * 128, m, bar, r0 + j, kelem);
     }
@@ -541,18 +612,22 @@ __device__ __forceinline__ void dense_load(const CUtensorMap* m, uint32_t dst, u
 // its address field (units of 16 bytes; the ring lies below 256 KB, so nothing carries into the next field):
 // what the issuing thread does between two MMAs is time that the tensor core may stand still (making the
 // descriptors anew for each MMA, with the layouts as variables, took 9728 x 2048 x 8192 from 179 to 210 us).
-template <bool MN>
+template <bool MN, bool BYTES>
 __device__ __forceinline__ uint64_t dense_desc(uint32_t addr) {
-  return sdesc_sw128(addr, MN ? 8192u : 16u, 1024);
+  return sdesc_sw128(addr, MN ? (BYTES ? 16384u : 8192u) : 16u, 1024);
 }
 // The MMAs of the k-block `offset` bytes into the ring: four of 32 bytes of k (16 16-bit or 32 8-bit elements).
-template <bool PAIR, bool FP8, bool LMN, bool CMN>
+template <bool PAIR, int Q, bool LMN, bool CMN>
 __device__ __forceinline__ void dense_mma(uint64_t l, uint64_t c, uint32_t d, uint32_t offset, uint32_t idesc,
-                                          uint32_t acc) {
+                                          uint32_t acc, uint32_t sfl = 0, uint32_t sfc = 0) {
+  constexpr int kMn = Q == kHalves ? 128 : 256;  // a step of k in an MN-major panel: 16 or 32 lines of 128 bytes
 #pragma unroll
   for (int kk = 0; kk < 4; ++kk) {
-    const uint64_t a = l + (offset >> 4) + kk * (LMN ? 128 : 2), b = c + (offset >> 4) + kk * (CMN ? 128 : 2);
-    if (FP8) {
+    const uint64_t a = l + (offset >> 4) + kk * (LMN ? kMn : 2), b = c + (offset >> 4) + kk * (CMN ? kMn : 2);
+    if (Q == kBlockScaled) {
+      if (PAIR) mma_block_pair(d, a, b, idesc, sfl, sfc, kk ? 1u : acc);
+      else mma_block(d, a, b, idesc, sfl, sfc, kk ? 1u : acc);
+    } else if (Q == kRowScaled) {
       if (PAIR) mma_f8_pair(d, a, b, idesc, kk ? 1u : acc);
       else mma_f8(d, a, b, idesc, kk ? 1u : acc);
     } else {
@@ -560,6 +635,45 @@ __device__ __forceinline__ void dense_mma(uint64_t l, uint64_t c, uint32_t d, ui
       else mma_bf16(d, a, b, idesc, kk ? 1u : acc);
     }
   }
+}
+
+// ---------------------------------------------------------------- scales of blocks
+// A stage's slot holds 512 bytes for the lanes' 128 rows and as many for each 128 of the columns: row r's four bytes,
+// those of k-blocks 4j .. 4j + 3, at (r % 32) * 16 + (r / 128) * 512 + r % 128 / 32 * 4, as tmem_copy_scales takes them. It
+// is written for the first k-block of each four (or of a CTA's share), and so is the stage's own place in tensor memory,
+// which is free when the stage is: no copy meets an MMA that still reads.
+__host__ __device__ constexpr int dense_slot_bytes(int BN) { return BN > 128 ? 1536 : 1024; }
+__host__ __device__ constexpr int dense_slot_cols(int BN) { return BN > 128 ? 12 : 8; }
+// The word of row i for k-blocks 4j .. 4j + 3; 1.0 (127) past the ends, where the elements are zero.
+__device__ __forceinline__ uint32_t scale_word(const DenseScales& s, long i, int j, int blocks) {
+  if (i >= s.rows) return 0x7f7f7f7fu;
+  const uint8_t* p = s.p + (i >> s.row_shift) * s.row_step + j * 4 * s.block_step;
+  if (s.words) return *reinterpret_cast<const uint32_t*>(p);
+  uint32_t w = 0u;
+#pragma unroll
+  for (int b = 0; b < 4; ++b) w |= (4 * j + b < blocks ? static_cast<uint32_t>(p[b * s.block_step]) : 127u) << (8 * b);
+  return w;
+}
+// A lane's words of 128 lane rows from l0 and up to 256 columns from c0 (BN), and their place in the slot.
+__device__ __forceinline__ void scales_load(const DenseGemmParams& p, uint32_t (&w)[12], long l0, long c0, int j, int lane) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w[i] = scale_word(p.sl, l0 + lane + 32 * i, j, p.kb_total);
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (32 * i < p.BN) w[4 + i] = scale_word(p.sc, c0 + lane + 32 * i, j, p.kb_total);
+}
+__device__ __forceinline__ void scales_store(const uint32_t (&w)[12], uint32_t slot, int BN, int lane) {
+  st_shared_v4(slot + lane * 16, w[0], w[1], w[2], w[3]);
+  st_shared_v4(slot + 512 + lane * 16, w[4], w[5], w[6], w[7]);
+  if (BN > 128) st_shared_v4(slot + 1024 + lane * 16, w[8], w[9], w[10], w[11]);
+  fence_proxy_async_smem();  // they are read by tcgen05.cp
+  __syncwarp();
+}
+template <bool PAIR>
+__device__ __forceinline__ void scales_copy(uint32_t slot, uint32_t taddr, int BN) {
+  tmem_copy_scales<PAIR>(taddr, scales_desc(slot));
+  tmem_copy_scales<PAIR>(taddr + 4, scales_desc(slot + 512));
+  if (BN > 128) tmem_copy_scales<PAIR>(taddr + 8, scales_desc(slot + 1024));
 }
 
 // Columns of a unit that one CTA of its cluster joins: groups of four, owned in turn.
@@ -636,17 +750,19 @@ __device__ __forceinline__ bool wait_flag(const uint32_t* f, int* err) {
   }
 }
 
-template <typename T, int MODE, bool FP8>
+template <typename T, int MODE, int Q>
 __global__ void __launch_bounds__(kPairThreads, 1) dense_pair_kernel(const __grid_constant__ DenseGemmParams p) {
-  constexpr bool RMN = dense_r_mn(MODE), CMN = dense_c_mn(MODE);
+  constexpr bool RMN = dense_r_mn(MODE), CMN = dense_c_mn(MODE), BYTES = Q != kHalves;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int BN = p.BN, S = p.stages;
   // this CTA's halves: 128 rows and BN / 2 columns (whole panels of 64 when MN-major)
-  const int c_rows = CMN ? (BN / 2 + 63) & ~63 : BN / 2;
+  const int c_rows = CMN ? (BN / 2 + (BYTES ? 127 : 63)) & ~(BYTES ? 127 : 63) : BN / 2;
   const uint32_t l_bytes = 128 * 128, c_bytes = static_cast<uint32_t>(c_rows) * 128;
   const uint32_t stage_bytes = l_bytes + c_bytes;
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + S * stage_bytes + kPairBuffers);
+  const uint32_t slot_bytes = Q == kBlockScaled ? dense_slot_bytes(BN) : 0u;
+  const uint32_t slots = S * stage_bytes + kPairBuffers;  // the scales' slots
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + slots + S * slot_bytes);
   uint64_t* empty = full + kDenseMaxStages;
   uint64_t* tfull = empty + kDenseMaxStages;
   uint64_t* tempty = tfull + 2;
@@ -656,11 +772,11 @@ __global__ void __launch_bounds__(kPairThreads, 1) dense_pair_kernel(const __gri
   const uint32_t rank = cluster_ctarank();
   const bool leader = rank == 0;
   const int cid = static_cast<int>(blockIdx.x >> 1), ncl = static_cast<int>(gridDim.x >> 1);
-  const uint32_t tcols = tmem_cols_for(2 * BN);
+  const uint32_t tcols = tmem_cols_for(2 * BN + (Q == kBlockScaled ? S * dense_slot_cols(BN) : 0));
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
-      mbar_init(&full[s], 1);
+      mbar_init(&full[s], Q == kBlockScaled ? 2 : 1);  // the leader's arrival, and for its scales the other CTA's
       mbar_init(&empty[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
@@ -685,12 +801,81 @@ __global__ void __launch_bounds__(kPairThreads, 1) dense_pair_kernel(const __gri
   if (!p.late) pdl_entry();  // the set-up above runs under the end of the kernel before
   if (p.early) pdl_release();
 
-  if (warp == 0) {
+  if (warp == 0 && Q == kBlockScaled) {
+    // The whole warp: the scales of the next four k-blocks are on their way while those at hand are used. The first
+    // ones come from memory while the first stages are loading: their arrivals follow together.
+    int s = 0, it = 0;
+    uint32_t par = 0;
+    uint32_t words[12];
+    DenseItem w;
+    auto request = [&](int j) {
+      scales_load(p, words, w.lt * 256L + rank * 128, static_cast<long>(w.ct) * BN, j, lane);
+    };
+    bool alive = dense_item(p, 0, cid, ncl, w);
+    if (alive) request(w.kb0 >> 2);
+    int pending = alive ? min(min(S, 4 - (w.kb0 & 3)), w.kb1 - w.kb0) : 0;  // stages to load before the first scales
+    int held = 0;
+    while (alive) {
+      for (int kb = w.kb0; kb < w.kb1; ++kb) {
+        int ok = 1;
+        if (lane == 0) ok = wait(&empty[s], par ^ 1, p.err, kSiteDenseEmpty) ? 1 : 0;
+        if (!__shfl_sync(0xffffffffu, ok, 0)) {
+          alive = false;
+          break;
+        }
+        if (elect_one()) {
+          const int lr = w.lt * 256 + static_cast<int>(rank) * 128, cr = w.ct * BN + static_cast<int>(rank) * (BN / 2);
+          const uint32_t bar = mapa_shared(smem_u32(&full[s]), 0);
+          if (leader) mbar_expect_tx(&full[s], 2 * stage_bytes);
+          const uint32_t l0 = sbase + s * stage_bytes;
+          dense_load<true, RMN, BYTES>(&p.tl, l0, nullptr, bar, kb * 128, lr, 128);
+          dense_load<true, CMN, BYTES>(&p.tc, l0 + l_bytes, nullptr, bar, kb * 128, cr, c_rows);
+        }
+        ++held;
+        const bool now = held >= pending;
+        if (now) {
+          // the stages held since the last arrival: s - held + 1 .. s; scales belong to the first of them
+          const int from = s - held + 1;
+          if (const int k0 = kb - held + 1; k0 == w.kb0 || (k0 & 3) == 0) {
+            scales_store(words, sbase + slots + from * slot_bytes, BN, lane);
+            // then the next four: of this unit, or the first of the next
+            const int j = (k0 >> 2) + 1;
+            if (4 * j < w.kb1) {
+              request(j);
+            } else {
+              const DenseItem here = w;
+              if (dense_item(p, it + 1, cid, ncl, w)) request(w.kb0 >> 2);
+              w = here;
+            }
+          }
+          __syncwarp();  // the bytes are expected
+          if (lane == 0)
+            for (int q = from; q <= s; ++q) mbar_arrive_cluster(mapa_shared(smem_u32(&full[q]), 0));
+          pending = 1;
+          held = 0;
+        }
+        if (++s == S) {
+          s = 0;
+          par ^= 1;
+        }
+      }
+      if (alive) alive = dense_item(p, ++it, cid, ncl, w);
+    }
+    if (lane == 0)
+      for (int i = 0; i < S; ++i) {  // as below
+        if (!wait(&empty[s], par ^ 1, p.err, kSiteDenseEmpty)) break;
+        if (++s == S) {
+          s = 0;
+          par ^= 1;
+        }
+      }
+    __syncwarp();
+  } else if (warp == 0) {
     if (elect_one()) {
       int s = 0;
       uint32_t par = 0;
       bool alive = true;
-      const int kelems = FP8 ? 128 : 64;
+      const int kelems = BYTES ? 128 : 64;
       DenseItem w;
       for (int it = 0; alive && dense_item(p, it, cid, ncl, w); ++it) {
         const int lr = w.lt * 256 + static_cast<int>(rank) * 128, cr = w.ct * BN + static_cast<int>(rank) * (BN / 2);
@@ -703,8 +888,8 @@ __global__ void __launch_bounds__(kPairThreads, 1) dense_pair_kernel(const __gri
           const uint32_t bar = mapa_shared(smem_u32(&full[s]), 0);
           if (leader) mbar_arrive_expect_tx(&full[s], 2 * stage_bytes);
           const uint32_t l0 = sbase + s * stage_bytes;
-          dense_load<true, RMN>(&p.tl, l0, nullptr, bar, kb * kelems, lr, 128);
-          dense_load<true, CMN>(&p.tc, l0 + l_bytes, nullptr, bar, kb * kelems, cr, c_rows);
+          dense_load<true, RMN, BYTES>(&p.tl, l0, nullptr, bar, kb * kelems, lr, 128);
+          dense_load<true, CMN, BYTES>(&p.tc, l0 + l_bytes, nullptr, bar, kb * kelems, cr, c_rows);
           if (++s == S) {
             s = 0;
             par ^= 1;
@@ -723,8 +908,9 @@ __global__ void __launch_bounds__(kPairThreads, 1) dense_pair_kernel(const __gri
     }
   } else if (warp == 1) {
     if (leader && elect_one()) {
-      const uint32_t idesc = idesc_f32acc(256, BN, p.fmt, RMN, CMN);
-      const uint64_t l = dense_desc<RMN>(sbase), c = dense_desc<CMN>(sbase + l_bytes);
+      const uint32_t idesc = Q == kBlockScaled ? idesc_block(256, BN, RMN, CMN) : idesc_f32acc(256, BN, p.fmt, RMN, CMN);
+      const uint64_t l = dense_desc<RMN, BYTES>(sbase), c = dense_desc<CMN, BYTES>(sbase + l_bytes);
+      [[maybe_unused]] uint32_t sf = 0;  // where the scales at hand lie in tensor memory
       int s = 0, tc = 0;
       uint32_t par = 0;
       bool alive = true;
@@ -734,12 +920,23 @@ __global__ void __launch_bounds__(kPairThreads, 1) dense_pair_kernel(const __gri
         if (!wait(&tempty[buf], ((tc >> 1) & 1) ^ 1, p.err, kSiteDenseTEmpty)) break;
         tc_fence_after();
         for (int kb = w.kb0; kb < w.kb1; ++kb) {
-          if (!wait(&full[s], par, p.err, kSiteDenseFull)) {
+          if (!(Q == kBlockScaled ? wait_cluster(&full[s], par, p.err, kSiteDenseFull)
+                                  : wait(&full[s], par, p.err, kSiteDenseFull))) {
             alive = false;
             break;
           }
           tc_fence_after();
-          dense_mma<true, FP8, RMN, CMN>(l, c, tmem + buf * BN, s * stage_bytes, idesc, kb > w.kb0);
+          if constexpr (Q == kBlockScaled) {
+            if (kb == w.kb0 || (kb & 3) == 0) {
+              sf = tmem + 2 * BN + s * dense_slot_cols(BN);
+              scales_copy<true>(sbase + slots + s * slot_bytes, sf, BN);
+            }
+            const uint32_t byte = kb & 3;
+            dense_mma<true, Q, RMN, CMN>(l, c, tmem + buf * BN, s * stage_bytes, idesc | byte << 4 | byte << 29, kb > w.kb0,
+                                         sf, sf + 4);
+          } else {
+            dense_mma<true, Q, RMN, CMN>(l, c, tmem + buf * BN, s * stage_bytes, idesc, kb > w.kb0);
+          }
           mma_commit_pair(&empty[s]);
           if (++s == S) {
             s = 0;
@@ -758,7 +955,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) dense_pair_kernel(const __gri
       const int ct = w.ct;
       const long m0 = static_cast<long>(w.lt) * 256 + rank * 128 + q * 32;
       const int nr = static_cast<int>(min(p.m - m0, 32L));
-      const uint32_t mscale = FP8 && lane < nr ? p.ms[m0 + lane] : 127u;
+      const uint32_t mscale = Q == kRowScaled && lane < nr ? p.ms[m0 + lane] : 127u;
       const int end = min(p.n, ct * BN + BN);
       const int n0 = ct * BN + part * 32;
       uint32_t res[16];
@@ -804,7 +1001,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) dense_pair_kernel(const __gri
         }
 #pragma unroll 1
         for (int n = n0; n < end; n += 128)
-          pair_epilogue<T, MODE, FP8>(p, t0 + n, buf0, m0, n, end, nr, w.split, mscale, res, lane,
+          pair_epilogue<T, MODE, Q>(p, t0 + n, buf0, m0, n, end, nr, w.split, mscale, res, lane,
                                  [&](uint32_t (&a)[32]) {
                                    if (w.tail >= 0) {
                                      for (int j = 1; j < p.parts; ++j) {
@@ -830,9 +1027,10 @@ __global__ void __launch_bounds__(kPairThreads, 1) dense_pair_kernel(const __gri
   if (p.late) pdl_entry();
 }
 
-template <typename T, int MODE, bool FP8>
+template <typename T, int MODE, int Q>
 __global__ void __launch_bounds__(kClusterThreads, 1) dense_cluster_kernel(const __grid_constant__ DenseGemmParams p) {
   constexpr bool LMN = dense_c_mn(MODE), CMN = dense_r_mn(MODE);  // the lanes are the output's columns
+  constexpr bool BYTES = Q != kHalves;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int BN = p.BN, S = p.stages, CL = p.cluster;
@@ -841,14 +1039,16 @@ __global__ void __launch_bounds__(kClusterThreads, 1) dense_cluster_kernel(const
   // CL > 1: the sums that the cluster's CTAs hand this one, [CL][own_cols][128], behind the ring
   const int own_cols = dense_own_cols(BN, CL);
   const uint32_t join_bytes = CL > 1 ? static_cast<uint32_t>(CL * own_cols) * 512u : 0u;
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + S * stage_bytes + join_bytes);
+  const uint32_t slot_bytes = Q == kBlockScaled ? dense_slot_bytes(BN) : 0u;
+  const uint32_t slots = S * stage_bytes + join_bytes;  // the scales' slots
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + slots + S * slot_bytes);
   uint64_t* empty = full + kDenseMaxStages;
   uint64_t* tfull = empty + kDenseMaxStages;
   uint32_t* slot = reinterpret_cast<uint32_t*>(tfull + 1);
   const uint32_t sbase = smem_u32(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = CL > 1 ? static_cast<int>(cluster_ctarank()) : 0;
-  const uint32_t tcols = tmem_cols_for(BN);
+  const uint32_t tcols = tmem_cols_for(BN + (Q == kBlockScaled ? S * dense_slot_cols(BN) : 0));
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
@@ -879,18 +1079,61 @@ __global__ void __launch_bounds__(kClusterThreads, 1) dense_cluster_kernel(const
   const int kb0 = s0 + static_cast<int>(static_cast<long>(s1 - s0) * rank / CL);
   const int kb1 = s0 + static_cast<int>(static_cast<long>(s1 - s0) * (rank + 1) / CL);
 
-  if (warp == 0) {
+  if (warp == 0 && Q == kBlockScaled) {
+    // The whole warp, as in the pair kernel: the scales of four k-blocks go into the slot of the first one's stage.
+    uint32_t words[12];
+    auto request = [&](int j) { scales_load(p, words, lt * 128L, static_cast<long>(ct) * BN, j, lane); };
+    if (kb0 < kb1) request(kb0 >> 2);
+    int s = 0, held = 0, pending = min(min(S, 4 - (kb0 & 3)), kb1 - kb0);
+    uint32_t par = 0;
+    int kb = kb0;
+    for (; kb < kb1; ++kb) {
+      int ok = 1;
+      if (lane == 0) ok = wait(&empty[s], par ^ 1, p.err, kSiteDenseEmpty) ? 1 : 0;
+      if (!__shfl_sync(0xffffffffu, ok, 0)) break;
+      if (elect_one()) {
+        mbar_expect_tx(&full[s], stage_bytes);
+        const uint32_t l0 = sbase + s * stage_bytes;
+        dense_load<false, LMN, BYTES>(&p.tl, l0, &full[s], 0u, kb * 128, lt * 128, 128);
+        dense_load<false, CMN, BYTES>(&p.tc, l0 + l_bytes, &full[s], 0u, kb * 128, ct * BN, BN);
+      }
+      if (++held >= pending) {
+        const int from = s - held + 1;
+        if (const int k0 = kb - held + 1; k0 == kb0 || (k0 & 3) == 0) {
+          scales_store(words, sbase + slots + from * slot_bytes, BN, lane);
+          if (const int j = (k0 >> 2) + 1; 4 * j < kb1) request(j);
+        }
+        __syncwarp();  // the bytes are expected
+        if (lane == 0)
+          for (int q = from; q <= s; ++q) mbar_arrive(&full[q]);
+        pending = 1;
+        held = 0;
+      }
+      if (++s == S) {
+        s = 0;
+        par ^= 1;
+      }
+    }
+    if (kb < kb1 && lane == 0) {  // gave up: as below
+      const int n = kb - kb0 - held;
+      for (int i = min(S, n); i > 0; --i) {
+        const int j = n - i;
+        (void)wait(&full[j % S], static_cast<uint32_t>(j / S) & 1u, p.err, kSiteDenseFull);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 0) {
     if (elect_one()) {
       int s = 0;
       uint32_t par = 0;
-      const int kelems = FP8 ? 128 : 64;
+      const int kelems = BYTES ? 128 : 64;
       int kb = kb0;
       for (; kb < kb1; ++kb) {
         if (!wait(&empty[s], par ^ 1, p.err, kSiteDenseEmpty)) break;
         mbar_arrive_expect_tx(&full[s], stage_bytes);
         const uint32_t l0 = sbase + s * stage_bytes;
-        dense_load<false, LMN>(&p.tl, l0, &full[s], 0u, kb * kelems, lt * 128, 128);
-        dense_load<false, CMN>(&p.tc, l0 + l_bytes, &full[s], 0u, kb * kelems, ct * BN, BN);
+        dense_load<false, LMN, BYTES>(&p.tl, l0, &full[s], 0u, kb * kelems, lt * 128, 128);
+        dense_load<false, CMN, BYTES>(&p.tc, l0 + l_bytes, &full[s], 0u, kb * kelems, ct * BN, BN);
         if (++s == S) {
           s = 0;
           par ^= 1;
@@ -906,14 +1149,24 @@ __global__ void __launch_bounds__(kClusterThreads, 1) dense_cluster_kernel(const
     }
   } else if (warp == 1) {
     if (elect_one()) {
-      const uint32_t idesc = idesc_f32acc(128, BN, p.fmt, LMN, CMN);
-      const uint64_t l = dense_desc<LMN>(sbase), c = dense_desc<CMN>(sbase + l_bytes);
+      const uint32_t idesc = Q == kBlockScaled ? idesc_block(128, BN, LMN, CMN) : idesc_f32acc(128, BN, p.fmt, LMN, CMN);
+      const uint64_t l = dense_desc<LMN, BYTES>(sbase), c = dense_desc<CMN, BYTES>(sbase + l_bytes);
+      [[maybe_unused]] uint32_t sf = 0;  // where the scales at hand lie in tensor memory
       int s = 0;
       uint32_t par = 0;
       for (int kb = kb0; kb < kb1; ++kb) {
         if (!wait(&full[s], par, p.err, kSiteDenseFull)) break;
         tc_fence_after();
-        dense_mma<false, FP8, LMN, CMN>(l, c, tmem, s * stage_bytes, idesc, kb > kb0);
+        if constexpr (Q == kBlockScaled) {
+          if (kb == kb0 || (kb & 3) == 0) {
+            sf = tmem + BN + s * dense_slot_cols(BN);
+            scales_copy<false>(sbase + slots + s * slot_bytes, sf, BN);
+          }
+          const uint32_t byte = kb & 3;
+          dense_mma<false, Q, LMN, CMN>(l, c, tmem, s * stage_bytes, idesc | byte << 4 | byte << 29, kb > kb0, sf, sf + 4);
+        } else {
+          dense_mma<false, Q, LMN, CMN>(l, c, tmem, s * stage_bytes, idesc, kb > kb0);
+        }
         mma_commit(&empty[s]);
         if (++s == S) {
           s = 0;
