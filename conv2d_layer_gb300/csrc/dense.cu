@@ -128,8 +128,9 @@ GemmPlan plan_gemm(int mode, long m, long n, int kb, int sms, int q = kHalves, b
   int c_rows = best.BN;  // columns of C a CTA brings: MN-major in whole panels of 64
   if (best.pair) c_rows = c_mn ? static_cast<int>(round_up(best.BN / 2, q == kHalves ? 64 : 128)) : best.BN / 2;
   const int need = static_cast<int>(ceil_div(best.kb_per_split, best.cluster));  // k-blocks of a CTA
-  const int stage = (128 + c_rows) * 128 + (blocks ? dense_slot_bytes(best.BN) : 0);
-  const int room = static_cast<int>(kMaxDynSmem) - 1536 - (best.pair ? kPairBuffers : 0);
+  const int stage = (128 + c_rows) * 128;
+  const int slots = blocks ? dense_slots_bytes(best.BN) : 0;
+  const int room = static_cast<int>(kMaxDynSmem) - 1536 - (best.pair ? kPairBuffers : 0) - slots;
   const long units = static_cast<long>(best.l_tiles) * best.c_tiles * best.splits;
   const int join = best.cluster > 1 ? best.cluster * dense_own_cols(best.BN, best.cluster) * 512 : 0;
   if (best.pair) {
@@ -146,8 +147,7 @@ GemmPlan plan_gemm(int mode, long m, long n, int kb, int sms, int q = kHalves, b
     best.join_flags = rem * kPairWarps;
   }
   // alignment slack, barriers
-  best.smem = static_cast<size_t>(best.stages) * stage + 1024 + 512 +
-              (best.pair ? kPairBuffers : join);
+  best.smem = static_cast<size_t>(best.stages) * stage + 1024 + 512 + slots + (best.pair ? kPairBuffers : join);
   return best;
 }
 
@@ -208,7 +208,10 @@ DenseScales block_scales(const uint8_t* scale, int group, long rows, long cols, 
   s.row_step = down ? 1 : ng;
   s.block_step = down ? ng : 1;
   s.rows = down ? cols : rows;
-  s.words = !down && ng % 4 == 0 && (reinterpret_cast<uintptr_t>(scale) & 3u) == 0;
+  if (!down) {
+    const uintptr_t at = reinterpret_cast<uintptr_t>(scale);
+    s.words = ng % 16 == 0 && at % 16 == 0 ? 4 : ng % 4 == 0 && at % 4 == 0 ? 1 : 0;
+  }
   return s;
 }
 

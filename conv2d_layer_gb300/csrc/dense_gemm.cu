@@ -28,7 +28,7 @@ cudaError_t pair(const DenseGemmParams& p, int grid, size_t smem, cudaStream_t s
   const auto k = dense_pair_kernel<T, MODE, Q>;
   static std::atomic<uint64_t> done{0};
   const cudaError_t e = opt_in(k, done);
-  return e != cudaSuccess ? e : launch_k(k, dim3(grid), dim3(kPairThreads), smem, st, 2, p);
+  return e != cudaSuccess ? e : launch_k(k, dim3(grid), dim3(kPairThreads + dense_scale_threads(Q)), smem, st, 2, p);
 }
 
 template <typename T, int MODE, int Q>
@@ -36,7 +36,7 @@ cudaError_t cluster(const DenseGemmParams& p, int grid, size_t smem, cudaStream_
   const auto k = dense_cluster_kernel<T, MODE, Q>;
   static std::atomic<uint64_t> done{0};
   const cudaError_t e = opt_in(k, done);
-  return e != cudaSuccess ? e : launch_k(k, dim3(grid), dim3(kClusterThreads), smem, st, p.cluster, p);
+  return e != cudaSuccess ? e : launch_k(k, dim3(grid), dim3(kClusterThreads + dense_scale_threads(Q)), smem, st, p.cluster, p);
 }
 
 // Calls f(T{}, mode, q) with the type and constants of the instantiation.

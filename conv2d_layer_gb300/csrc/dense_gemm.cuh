@@ -47,12 +47,15 @@ __host__ __device__ constexpr bool dense_c_mn(int mode) { return mode != kDenseF
 // scale for each row (or 128 of them) and block of 128 of k, which the tensor core applies.
 enum : int { kHalves = 0, kRowScaled = 1, kBlockScaled = 2 };
 // Scale bytes of a block-scaled operand: that of row i and block b is p[(i >> row_shift) * row_step + b * block_step];
-// words: four blocks' bytes of a row are an aligned word.
+// words: four blocks' bytes of a row are an aligned word (1), or sixteen an aligned 16 bytes too (4).
 struct DenseScales {
   const uint8_t* p;
   long row_step, block_step, rows;
   int row_shift, words;
 };
+
+// One more warp brings the scales of blocks.
+__host__ __device__ constexpr int dense_scale_threads(int q) { return q == kBlockScaled ? 32 : 0; }
 
 struct DenseGemmParams {
   CUtensorMap tl, tc;   // the operands whose rows are the accumulator's lanes / columns
@@ -151,10 +154,6 @@ __device__ __forceinline__ uint64_t scales_desc(uint32_t saddr) {
 __device__ __forceinline__ uint32_t idesc_block(int M, int N, bool a_mn, bool b_mn) {
   return ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) | (static_cast<uint32_t>(N >> 3) << 17) | (1u << 23) |
          (static_cast<uint32_t>(M >> 4) << 24);
-}
-// Bytes that a phase waits for, without an arrival.
-__device__ __forceinline__ void mbar_expect_tx(uint64_t* bar, uint32_t bytes) {
-  asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
 }
 // wait() for a phase that another CTA of the cluster arrives on after writing its own shared memory.
 __device__ __forceinline__ bool wait_cluster(uint64_t* bar, uint32_t parity, int* err, int site) {
@@ -638,34 +637,58 @@ __device__ __forceinline__ void dense_mma(uint64_t l, uint64_t c, uint32_t d, ui
 }
 
 // ---------------------------------------------------------------- scales of blocks
-// A stage's slot holds 512 bytes for the lanes' 128 rows and as many for each 128 of the columns: row r's four bytes,
-// those of k-blocks 4j .. 4j + 3, at (r % 32) * 16 + (r / 128) * 512 + r % 128 / 32 * 4, as tmem_copy_scales takes them. It
-// is written for the first k-block of each four (or of a CTA's share), and so is the stage's own place in tensor memory,
-// which is free when the stage is: no copy meets an MMA that still reads.
+// A slot holds the scales of four k-blocks 4j .. 4j + 3: 512 bytes for the lanes' 128 rows and as many for each 128 of the
+// columns; row r's four bytes at (r % 32) * 16 + (r / 128) * 512 + r % 128 / 32 * 4, as tmem_copy_scales takes them. A warp
+// writes the slots of 16 k-blocks at a time, into one of two sets, and runs that far ahead of the MMAs: what it writes is
+// released at the scope of the cluster, which takes as long as a stage's MMAs two or three times over (with a slot in each
+// stage, written when the stage was free: 8192 x 8192 x 2048 182 us; a scale a thread in the loading warp 314). The MMA
+// thread copies a slot to the tensor memory with the first of its k-blocks, to a place that belongs to that k-block's
+// stage and so is free when the stage is: no copy meets an MMA that still reads.
+constexpr int kScaleBlocks = 16;
 __host__ __device__ constexpr int dense_slot_bytes(int BN) { return BN > 128 ? 1536 : 1024; }
 __host__ __device__ constexpr int dense_slot_cols(int BN) { return BN > 128 ? 12 : 8; }
-// The word of row i for k-blocks 4j .. 4j + 3; 1.0 (127) past the ends, where the elements are zero.
-__device__ __forceinline__ uint32_t scale_word(const DenseScales& s, long i, int j, int blocks) {
-  if (i >= s.rows) return 0x7f7f7f7fu;
-  const uint8_t* p = s.p + (i >> s.row_shift) * s.row_step + j * 4 * s.block_step;
-  if (s.words) return *reinterpret_cast<const uint32_t*>(p);
-  uint32_t w = 0u;
+__host__ __device__ constexpr int dense_slots_bytes(int BN) { return 2 * (kScaleBlocks / 4) * dense_slot_bytes(BN); }
+// The words of row i for k-blocks 16j .. 16j + 15; 1.0 (127) past the ends, where the elements are zero.
+__device__ __forceinline__ void scale_words(const DenseScales& s, long i, int j, int blocks, uint32_t (&w)[4]) {
 #pragma unroll
-  for (int b = 0; b < 4; ++b) w |= (4 * j + b < blocks ? static_cast<uint32_t>(p[b * s.block_step]) : 127u) << (8 * b);
-  return w;
+  for (int g = 0; g < 4; ++g) w[g] = 0x7f7f7f7fu;
+  if (i >= s.rows) return;
+  const uint8_t* p = s.p + (i >> s.row_shift) * s.row_step + j * kScaleBlocks * s.block_step;
+  const int left = blocks - j * kScaleBlocks;
+  if (s.words == 4 && left >= kScaleBlocks) {
+    const uint4 v = *reinterpret_cast<const uint4*>(p);
+    w[0] = v.x;
+    w[1] = v.y;
+    w[2] = v.z;
+    w[3] = v.w;
+  } else if (s.words) {
+#pragma unroll
+    for (int g = 0; g < 4; ++g)
+      if (4 * g < left) w[g] = reinterpret_cast<const uint32_t*>(p)[g];
+  } else {
+#pragma unroll
+    for (int g = 0; g < 4; ++g)
+#pragma unroll
+      for (int b = 0; b < 4; ++b)
+        if (4 * g + b < left) w[g] = (w[g] & ~(255u << (8 * b))) | static_cast<uint32_t>(p[(4 * g + b) * s.block_step]) << (8 * b);
+  }
 }
-// A lane's words of 128 lane rows from l0 and up to 256 columns from c0 (BN), and their place in the slot.
-__device__ __forceinline__ void scales_load(const DenseGemmParams& p, uint32_t (&w)[12], long l0, long c0, int j, int lane) {
+// A lane's words of 128 lane rows from l0 and up to 256 columns from c0 (BN), and their place in a set of slots.
+__device__ __forceinline__ void scales_load(const DenseGemmParams& p, uint32_t (&w)[12][4], long l0, long c0, int j, int lane) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) w[i] = scale_word(p.sl, l0 + lane + 32 * i, j, p.kb_total);
+  for (int i = 0; i < 4; ++i) scale_words(p.sl, l0 + lane + 32 * i, j, p.kb_total, w[i]);
 #pragma unroll
   for (int i = 0; i < 8; ++i)
-    if (32 * i < p.BN) w[4 + i] = scale_word(p.sc, c0 + lane + 32 * i, j, p.kb_total);
+    if (32 * i < p.BN) scale_words(p.sc, c0 + lane + 32 * i, j, p.kb_total, w[4 + i]);
 }
-__device__ __forceinline__ void scales_store(const uint32_t (&w)[12], uint32_t slot, int BN, int lane) {
-  st_shared_v4(slot + lane * 16, w[0], w[1], w[2], w[3]);
-  st_shared_v4(slot + 512 + lane * 16, w[4], w[5], w[6], w[7]);
-  if (BN > 128) st_shared_v4(slot + 1024 + lane * 16, w[8], w[9], w[10], w[11]);
+__device__ __forceinline__ void scales_store(const uint32_t (&w)[12][4], uint32_t set, int BN, int lane) {
+#pragma unroll
+  for (int g = 0; g < 4; ++g) {
+    const uint32_t slot = set + g * dense_slot_bytes(BN) + lane * 16;
+    st_shared_v4(slot, w[0][g], w[1][g], w[2][g], w[3][g]);
+    st_shared_v4(slot + 512, w[4][g], w[5][g], w[6][g], w[7][g]);
+    if (BN > 128) st_shared_v4(slot + 1024, w[8][g], w[9][g], w[10][g], w[11][g]);
+  }
   fence_proxy_async_smem();  // they are read by tcgen05.cp
   __syncwarp();
 }
@@ -675,6 +698,10 @@ __device__ __forceinline__ void scales_copy(uint32_t slot, uint32_t taddr, int B
   tmem_copy_scales<PAIR>(taddr + 4, scales_desc(slot + 512));
   if (BN > 128) tmem_copy_scales<PAIR>(taddr + 8, scales_desc(slot + 1024));
 }
+// Where k-block kb's slot lies in its set, and whether it is the first or last of a set for a loop over kb0 .. kb1 - 1.
+__device__ __forceinline__ uint32_t slot_of(int kb, int BN) { return (kb % kScaleBlocks / 4) * dense_slot_bytes(BN); }
+__device__ __forceinline__ bool set_begins(int kb, int kb0) { return kb == kb0 || kb % kScaleBlocks == 0; }
+__device__ __forceinline__ bool set_ends(int kb, int kb1) { return kb == kb1 - 1 || kb % kScaleBlocks == kScaleBlocks - 1; }
 
 // Columns of a unit that one CTA of its cluster joins: groups of four, owned in turn.
 __host__ __device__ constexpr int dense_own_cols(int BN, int cluster) { return (BN / 4 + cluster - 1) / cluster * 4; }
@@ -751,7 +778,7 @@ __device__ __forceinline__ bool wait_flag(const uint32_t* f, int* err) {
 }
 
 template <typename T, int MODE, int Q>
-__global__ void __launch_bounds__(kPairThreads, 1) dense_pair_kernel(const __grid_constant__ DenseGemmParams p) {
+__global__ void __launch_bounds__(kPairThreads + dense_scale_threads(Q), 1) dense_pair_kernel(const __grid_constant__ DenseGemmParams p) {
   constexpr bool RMN = dense_r_mn(MODE), CMN = dense_c_mn(MODE), BYTES = Q != kHalves;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -760,13 +787,14 @@ __global__ void __launch_bounds__(kPairThreads, 1) dense_pair_kernel(const __gri
   const int c_rows = CMN ? (BN / 2 + (BYTES ? 127 : 63)) & ~(BYTES ? 127 : 63) : BN / 2;
   const uint32_t l_bytes = 128 * 128, c_bytes = static_cast<uint32_t>(c_rows) * 128;
   const uint32_t stage_bytes = l_bytes + c_bytes;
-  const uint32_t slot_bytes = Q == kBlockScaled ? dense_slot_bytes(BN) : 0u;
-  const uint32_t slots = S * stage_bytes + kPairBuffers;  // the scales' slots
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + slots + S * slot_bytes);
+  const uint32_t slots = S * stage_bytes + kPairBuffers;  // the scales' two sets
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + slots + (Q == kBlockScaled ? dense_slots_bytes(BN) : 0));
   uint64_t* empty = full + kDenseMaxStages;
   uint64_t* tfull = empty + kDenseMaxStages;
   uint64_t* tempty = tfull + 2;
-  uint32_t* slot = reinterpret_cast<uint32_t*>(tempty + 2);
+  uint64_t* sfull = tempty + 2;
+  uint64_t* sempty = sfull + 2;
+  uint32_t* slot = reinterpret_cast<uint32_t*>(sempty + 2);
   const uint32_t sbase = smem_u32(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
@@ -776,12 +804,14 @@ __global__ void __launch_bounds__(kPairThreads, 1) dense_pair_kernel(const __gri
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
-      mbar_init(&full[s], Q == kBlockScaled ? 2 : 1);  // the leader's arrival, and for its scales the other CTA's
+      mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&tfull[b], 1);
       mbar_init(&tempty[b], 2 * kPairWarps);  // one arrival per epilogue warp of both CTAs
+      mbar_init(&sfull[b], 2);                // both CTAs' scales
+      mbar_init(&sempty[b], 1);
     }
     fence_mbar_init();
     tma_prefetch_desc(&p.tl);
@@ -801,73 +831,33 @@ __global__ void __launch_bounds__(kPairThreads, 1) dense_pair_kernel(const __gri
   if (!p.late) pdl_entry();  // the set-up above runs under the end of the kernel before
   if (p.early) pdl_release();
 
-  if (warp == 0 && Q == kBlockScaled) {
-    // The whole warp: the scales of the next four k-blocks are on their way while those at hand are used. The first
-    // ones come from memory while the first stages are loading: their arrivals follow together.
-    int s = 0, it = 0;
-    uint32_t par = 0;
-    uint32_t words[12];
+  if (Q == kBlockScaled && warp == kPairThreads / 32) {
+    // The scales' warp: the next set's words are on their way while the one at hand waits for its slots.
+    int b = 0;
+    uint32_t par = 0, words[12][4];
     DenseItem w;
     auto request = [&](int j) {
       scales_load(p, words, w.lt * 256L + rank * 128, static_cast<long>(w.ct) * BN, j, lane);
     };
     bool alive = dense_item(p, 0, cid, ncl, w);
-    if (alive) request(w.kb0 >> 2);
-    int pending = alive ? min(min(S, 4 - (w.kb0 & 3)), w.kb1 - w.kb0) : 0;  // stages to load before the first scales
-    int held = 0;
-    while (alive) {
-      for (int kb = w.kb0; kb < w.kb1; ++kb) {
-        int ok = 1;
-        if (lane == 0) ok = wait(&empty[s], par ^ 1, p.err, kSiteDenseEmpty) ? 1 : 0;
-        if (!__shfl_sync(0xffffffffu, ok, 0)) {
-          alive = false;
-          break;
-        }
-        if (elect_one()) {
-          const int lr = w.lt * 256 + static_cast<int>(rank) * 128, cr = w.ct * BN + static_cast<int>(rank) * (BN / 2);
-          const uint32_t bar = mapa_shared(smem_u32(&full[s]), 0);
-          if (leader) mbar_expect_tx(&full[s], 2 * stage_bytes);
-          const uint32_t l0 = sbase + s * stage_bytes;
-          dense_load<true, RMN, BYTES>(&p.tl, l0, nullptr, bar, kb * 128, lr, 128);
-          dense_load<true, CMN, BYTES>(&p.tc, l0 + l_bytes, nullptr, bar, kb * 128, cr, c_rows);
-        }
-        ++held;
-        const bool now = held >= pending;
-        if (now) {
-          // the stages held since the last arrival: s - held + 1 .. s; scales belong to the first of them
-          const int from = s - held + 1;
-          if (const int k0 = kb - held + 1; k0 == w.kb0 || (k0 & 3) == 0) {
-            scales_store(words, sbase + slots + from * slot_bytes, BN, lane);
-            // then the next four: of this unit, or the first of the next
-            const int j = (k0 >> 2) + 1;
-            if (4 * j < w.kb1) {
-              request(j);
-            } else {
-              const DenseItem here = w;
-              if (dense_item(p, it + 1, cid, ncl, w)) request(w.kb0 >> 2);
-              w = here;
-            }
-          }
-          __syncwarp();  // the bytes are expected
-          if (lane == 0)
-            for (int q = from; q <= s; ++q) mbar_arrive_cluster(mapa_shared(smem_u32(&full[q]), 0));
-          pending = 1;
-          held = 0;
-        }
-        if (++s == S) {
-          s = 0;
-          par ^= 1;
-        }
-      }
-      if (alive) alive = dense_item(p, ++it, cid, ncl, w);
+    if (alive) request(w.kb0 / kScaleBlocks);
+    for (int it = 0; alive;) {
+      int j = w.kb0 / kScaleBlocks, ok = 1;
+      if (lane == 0) ok = wait(&sempty[b], par ^ 1, p.err, kSiteDenseEmpty) ? 1 : 0;
+      if (!__shfl_sync(0xffffffffu, ok, 0)) break;
+      scales_store(words, sbase + slots + b * (dense_slots_bytes(BN) / 2), BN, lane);
+      if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&sfull[b]), 0));
+      b ^= 1;
+      if (b == 0) par ^= 1;
+      if (++j * kScaleBlocks < w.kb1) w.kb0 = j * kScaleBlocks;
+      else alive = dense_item(p, ++it, cid, ncl, w);
+      if (alive) request(w.kb0 / kScaleBlocks);
     }
-    if (lane == 0)
-      for (int i = 0; i < S; ++i) {  // as below
-        if (!wait(&empty[s], par ^ 1, p.err, kSiteDenseEmpty)) break;
-        if (++s == S) {
-          s = 0;
-          par ^= 1;
-        }
+    if (lane == 0)  // the even CTA's commits land in this CTA's barriers, as those of the stages below
+      for (int i = 0; i < 2; ++i) {
+        if (!wait(&sempty[b], par ^ 1, p.err, kSiteDenseEmpty)) break;
+        b ^= 1;
+        if (b == 0) par ^= 1;
       }
     __syncwarp();
   } else if (warp == 0) {
@@ -910,7 +900,8 @@ __global__ void __launch_bounds__(kPairThreads, 1) dense_pair_kernel(const __gri
     if (leader && elect_one()) {
       const uint32_t idesc = Q == kBlockScaled ? idesc_block(256, BN, RMN, CMN) : idesc_f32acc(256, BN, p.fmt, RMN, CMN);
       const uint64_t l = dense_desc<RMN, BYTES>(sbase), c = dense_desc<CMN, BYTES>(sbase + l_bytes);
-      [[maybe_unused]] uint32_t sf = 0;  // where the scales at hand lie in tensor memory
+      // where the scales at hand lie in tensor memory, and the set they come from
+      [[maybe_unused]] uint32_t sf = 0, sb = 0, spar = 0;
       int s = 0, tc = 0;
       uint32_t par = 0;
       bool alive = true;
@@ -920,8 +911,8 @@ __global__ void __launch_bounds__(kPairThreads, 1) dense_pair_kernel(const __gri
         if (!wait(&tempty[buf], ((tc >> 1) & 1) ^ 1, p.err, kSiteDenseTEmpty)) break;
         tc_fence_after();
         for (int kb = w.kb0; kb < w.kb1; ++kb) {
-          if (!(Q == kBlockScaled ? wait_cluster(&full[s], par, p.err, kSiteDenseFull)
-                                  : wait(&full[s], par, p.err, kSiteDenseFull))) {
+          if (!wait(&full[s], par, p.err, kSiteDenseFull) ||
+              (Q == kBlockScaled && set_begins(kb, w.kb0) && !wait_cluster(&sfull[sb], spar, p.err, kSiteDenseFull))) {
             alive = false;
             break;
           }
@@ -929,11 +920,16 @@ __global__ void __launch_bounds__(kPairThreads, 1) dense_pair_kernel(const __gri
           if constexpr (Q == kBlockScaled) {
             if (kb == w.kb0 || (kb & 3) == 0) {
               sf = tmem + 2 * BN + s * dense_slot_cols(BN);
-              scales_copy<true>(sbase + slots + s * slot_bytes, sf, BN);
+              scales_copy<true>(sbase + slots + sb * (dense_slots_bytes(BN) / 2) + slot_of(kb, BN), sf, BN);
             }
             const uint32_t byte = kb & 3;
             dense_mma<true, Q, RMN, CMN>(l, c, tmem + buf * BN, s * stage_bytes, idesc | byte << 4 | byte << 29, kb > w.kb0,
                                          sf, sf + 4);
+            if (set_ends(kb, w.kb1)) {
+              mma_commit_pair(&sempty[sb]);
+              sb ^= 1;
+              if (sb == 0) spar ^= 1;
+            }
           } else {
             dense_mma<true, Q, RMN, CMN>(l, c, tmem + buf * BN, s * stage_bytes, idesc, kb > w.kb0);
           }
@@ -1028,7 +1024,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) dense_pair_kernel(const __gri
 }
 
 template <typename T, int MODE, int Q>
-__global__ void __launch_bounds__(kClusterThreads, 1) dense_cluster_kernel(const __grid_constant__ DenseGemmParams p) {
+__global__ void __launch_bounds__(kClusterThreads + dense_scale_threads(Q), 1) dense_cluster_kernel(const __grid_constant__ DenseGemmParams p) {
   constexpr bool LMN = dense_c_mn(MODE), CMN = dense_r_mn(MODE);  // the lanes are the output's columns
   constexpr bool BYTES = Q != kHalves;
   extern __shared__ uint8_t smem_raw[];
@@ -1039,12 +1035,13 @@ __global__ void __launch_bounds__(kClusterThreads, 1) dense_cluster_kernel(const
   // CL > 1: the sums that the cluster's CTAs hand this one, [CL][own_cols][128], behind the ring
   const int own_cols = dense_own_cols(BN, CL);
   const uint32_t join_bytes = CL > 1 ? static_cast<uint32_t>(CL * own_cols) * 512u : 0u;
-  const uint32_t slot_bytes = Q == kBlockScaled ? dense_slot_bytes(BN) : 0u;
-  const uint32_t slots = S * stage_bytes + join_bytes;  // the scales' slots
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + slots + S * slot_bytes);
+  const uint32_t slots = S * stage_bytes + join_bytes;  // the scales' two sets
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + slots + (Q == kBlockScaled ? dense_slots_bytes(BN) : 0));
   uint64_t* empty = full + kDenseMaxStages;
   uint64_t* tfull = empty + kDenseMaxStages;
-  uint32_t* slot = reinterpret_cast<uint32_t*>(tfull + 1);
+  uint64_t* sfull = tfull + 1;
+  uint64_t* sempty = sfull + 2;
+  uint32_t* slot = reinterpret_cast<uint32_t*>(sempty + 2);
   const uint32_t sbase = smem_u32(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = CL > 1 ? static_cast<int>(cluster_ctarank()) : 0;
@@ -1056,6 +1053,10 @@ __global__ void __launch_bounds__(kClusterThreads, 1) dense_cluster_kernel(const
       mbar_init(&empty[s], 1);
     }
     mbar_init(tfull, 1);
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&sfull[b], 1);
+      mbar_init(&sempty[b], 1);
+    }
     fence_mbar_init();
     tma_prefetch_desc(&p.tl);
     tma_prefetch_desc(&p.tc);
@@ -1079,49 +1080,24 @@ __global__ void __launch_bounds__(kClusterThreads, 1) dense_cluster_kernel(const
   const int kb0 = s0 + static_cast<int>(static_cast<long>(s1 - s0) * rank / CL);
   const int kb1 = s0 + static_cast<int>(static_cast<long>(s1 - s0) * (rank + 1) / CL);
 
-  if (warp == 0 && Q == kBlockScaled) {
-    // The whole warp, as in the pair kernel: the scales of four k-blocks go into the slot of the first one's stage.
-    uint32_t words[12];
+  if (Q == kBlockScaled && warp == kClusterThreads / 32) {
+    // The scales' warp, as in the pair kernel.
+    uint32_t par = 0, words[12][4];
+    int b = 0;
     auto request = [&](int j) { scales_load(p, words, lt * 128L, static_cast<long>(ct) * BN, j, lane); };
-    if (kb0 < kb1) request(kb0 >> 2);
-    int s = 0, held = 0, pending = min(min(S, 4 - (kb0 & 3)), kb1 - kb0);
-    uint32_t par = 0;
-    int kb = kb0;
-    for (; kb < kb1; ++kb) {
+    if (kb0 < kb1) request(kb0 / kScaleBlocks);
+    for (int j = kb0 / kScaleBlocks; kb0 < kb1 && j * kScaleBlocks < kb1; ++j) {
       int ok = 1;
-      if (lane == 0) ok = wait(&empty[s], par ^ 1, p.err, kSiteDenseEmpty) ? 1 : 0;
+      if (lane == 0) ok = wait(&sempty[b], par ^ 1, p.err, kSiteDenseEmpty) ? 1 : 0;
       if (!__shfl_sync(0xffffffffu, ok, 0)) break;
-      if (elect_one()) {
-        mbar_expect_tx(&full[s], stage_bytes);
-        const uint32_t l0 = sbase + s * stage_bytes;
-        dense_load<false, LMN, BYTES>(&p.tl, l0, &full[s], 0u, kb * 128, lt * 128, 128);
-        dense_load<false, CMN, BYTES>(&p.tc, l0 + l_bytes, &full[s], 0u, kb * 128, ct * BN, BN);
-      }
-      if (++held >= pending) {
-        const int from = s - held + 1;
-        if (const int k0 = kb - held + 1; k0 == kb0 || (k0 & 3) == 0) {
-          scales_store(words, sbase + slots + from * slot_bytes, BN, lane);
-          if (const int j = (k0 >> 2) + 1; 4 * j < kb1) request(j);
-        }
-        __syncwarp();  // the bytes are expected
-        if (lane == 0)
-          for (int q = from; q <= s; ++q) mbar_arrive(&full[q]);
-        pending = 1;
-        held = 0;
-      }
-      if (++s == S) {
-        s = 0;
-        par ^= 1;
-      }
-    }
-    if (kb < kb1 && lane == 0) {  // gave up: as below
-      const int n = kb - kb0 - held;
-      for (int i = min(S, n); i > 0; --i) {
-        const int j = n - i;
-        (void)wait(&full[j % S], static_cast<uint32_t>(j / S) & 1u, p.err, kSiteDenseFull);
-      }
+      scales_store(words, sbase + slots + b * (dense_slots_bytes(BN) / 2), BN, lane);
+      if (lane == 0) mbar_arrive(&sfull[b]);
+      b ^= 1;
+      if (b == 0) par ^= 1;
+      if ((j + 1) * kScaleBlocks < kb1) request(j + 1);
     }
     __syncwarp();
+    if (CL > 1) cluster_wait();  // the others have started
   } else if (warp == 0) {
     if (elect_one()) {
       int s = 0;
@@ -1151,19 +1127,26 @@ __global__ void __launch_bounds__(kClusterThreads, 1) dense_cluster_kernel(const
     if (elect_one()) {
       const uint32_t idesc = Q == kBlockScaled ? idesc_block(128, BN, LMN, CMN) : idesc_f32acc(128, BN, p.fmt, LMN, CMN);
       const uint64_t l = dense_desc<LMN, BYTES>(sbase), c = dense_desc<CMN, BYTES>(sbase + l_bytes);
-      [[maybe_unused]] uint32_t sf = 0;  // where the scales at hand lie in tensor memory
+      // where the scales at hand lie in tensor memory, and the set they come from
+      [[maybe_unused]] uint32_t sf = 0, sb = 0, spar = 0;
       int s = 0;
       uint32_t par = 0;
       for (int kb = kb0; kb < kb1; ++kb) {
         if (!wait(&full[s], par, p.err, kSiteDenseFull)) break;
+        if (Q == kBlockScaled && set_begins(kb, kb0) && !wait(&sfull[sb], spar, p.err, kSiteDenseFull)) break;
         tc_fence_after();
         if constexpr (Q == kBlockScaled) {
           if (kb == kb0 || (kb & 3) == 0) {
             sf = tmem + BN + s * dense_slot_cols(BN);
-            scales_copy<false>(sbase + slots + s * slot_bytes, sf, BN);
+            scales_copy<false>(sbase + slots + sb * (dense_slots_bytes(BN) / 2) + slot_of(kb, BN), sf, BN);
           }
           const uint32_t byte = kb & 3;
           dense_mma<false, Q, LMN, CMN>(l, c, tmem, s * stage_bytes, idesc | byte << 4 | byte << 29, kb > kb0, sf, sf + 4);
+          if (set_ends(kb, kb1)) {
+            mma_commit(&sempty[sb]);
+            sb ^= 1;
+            if (sb == 0) spar ^= 1;
+          }
         } else {
           dense_mma<false, Q, LMN, CMN>(l, c, tmem, s * stage_bytes, idesc, kb > kb0);
         }
@@ -1229,7 +1212,7 @@ __global__ void __launch_bounds__(kClusterThreads, 1) dense_cluster_kernel(const
     const int quads = (nc + 3) / 4;
     const int own = (quads - rank + CL - 1) / CL;  // quads rank, rank + CL, ...
     const uint32_t join = sbase + S * stage_bytes;
-    for (int j = warp; j < own * 4; j += kClusterThreads / 32) {
+    for (int j = warp; j < own * 4; j += static_cast<int>(blockDim.x) / 32) {
       const int q = j & 3, i = j >> 2;
       const int n = lt * 128 + q * 32 + lane;
       float2 nscale = splat(1.f);
