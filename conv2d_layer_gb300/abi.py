@@ -29,6 +29,7 @@ EXPORTS = (
     "conv2d_rms_norm_bwd_workspace_size", "conv2d_dense_fwd", "conv2d_dense_bwd", "conv2d_dense_fwd_workspace_size",
     "conv2d_dense_bwd_workspace_size",
     "conv2d_layer_norm_fwd", "conv2d_layer_norm_bwd", "conv2d_layer_norm_bwd_workspace_size",
+    "conv2d_moe_fwd", "conv2d_moe_fwd_workspace_size",
 )
 
 
@@ -46,6 +47,10 @@ class Mat(ctypes.Structure):
 
 class DenseDesc(ctypes.Structure):
     _fields_ = [("M", ctypes.c_int64)] + [(n, ctypes.c_int32) for n in ("K", "N", "act", "dtype", "accumulate")]
+
+
+class MoeDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("T", "D", "F", "E", "k", "act", "gated", "normalize", "dtype")]
 
 
 class Conv2dError(RuntimeError):
@@ -103,6 +108,10 @@ def lib():
     L.conv2d_dense_bwd_workspace_size.restype = sz
     L.conv2d_prof_enable.argtypes = [i32]
     L.conv2d_prof_read.argtypes = [ctypes.POINTER(ctypes.c_char_p), fp, i32]
+    po = ctypes.POINTER(MoeDesc)
+    L.conv2d_moe_fwd.argtypes = [po, pm, pm, pm, vp, pm, vp, pm, pm, vp, vp, vp, sz, vp]
+    L.conv2d_moe_fwd_workspace_size.argtypes = [po, pm, pm]
+    L.conv2d_moe_fwd_workspace_size.restype = sz
     _lib = L
     return L
 
@@ -243,6 +252,15 @@ def conv2d_dense_bwd_workspace_size(d, x, w, pre_act, dy, dx, dw, dbias):
 def conv2d_dense_bwd(d, x, w, pre_act, dy, dx, dw, dbias, ws, ws_bytes=None, stream=None):
     return lib().conv2d_dense_bwd(d, x, w, pre_act, dy, dx, dw,
                                   _ptr(dbias), _ptr(ws), _ws(ws, ws_bytes), _stream(stream))
+
+
+def conv2d_moe_fwd_workspace_size(d, w1, w2):
+    return int(lib().conv2d_moe_fwd_workspace_size(d, w1, w2))
+
+
+def conv2d_moe_fwd(d, x, router, w1, b1, w2, b2, residual, y, experts, weights, ws, ws_bytes=None, stream=None):
+    return lib().conv2d_moe_fwd(d, x, router, w1, _ptr(b1), w2, _ptr(b2), residual, y, _ptr(experts), _ptr(weights),
+                                _ptr(ws), _ws(ws, ws_bytes), _stream(stream))
 
 
 def conv2d_device_status(stream=None):

@@ -19,8 +19,8 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 OUT = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT, "libconv2d.so")
-SOURCES = ["api.cu", "bn_kernels.cu", "dense.cu", "dense_gemm.cu", "gemm_bf16.cu", "gemm_tf32.cu", "layer_norm.cu", "noalloc.cu",
-           "rms_norm.cu", "rows.cu"]
+SOURCES = ["api.cu", "bn_kernels.cu", "dense.cu", "dense_gemm.cu", "gemm_bf16.cu", "gemm_tf32.cu", "layer_norm.cu", "moe.cu",
+           "noalloc.cu", "rms_norm.cu", "rows.cu"]
 BINDING = os.path.join(OUT, "_binding.so")
 BINDING_SRC = os.path.join(CSRC, "binding.cpp")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

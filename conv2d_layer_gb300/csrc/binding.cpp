@@ -31,7 +31,8 @@ constexpr int64_t kGroup = 32, kWide = 128, kTile = CONV2D_TILE;
   X(conv2d_dense_bwd_workspace_size)
 // Those a library may lack: a call that needs one then raises.
 #define MORE_ENTRIES(X) \
-  X(conv2d_layer_norm_fwd) X(conv2d_layer_norm_bwd) X(conv2d_layer_norm_bwd_workspace_size)
+  X(conv2d_layer_norm_fwd) X(conv2d_layer_norm_bwd) X(conv2d_layer_norm_bwd_workspace_size)                        \
+  X(conv2d_moe_fwd) X(conv2d_moe_fwd_workspace_size)
 struct Lib {
 #define X(f) decltype(&::f) f = nullptr;
   ENTRIES(X)
@@ -508,6 +509,90 @@ PyObject* dense_bwd(PyObject* const* a) {
                 !need_db ? same(Py_None) : given(a[8]) ? same(a[8]) : wrap(db)});
 }
 
+std::string triple_name(int64_t a, int64_t b, int64_t c) {
+  return "(" + std::to_string(a) + ", " + std::to_string(b) + ", " + std::to_string(c) + ")";
+}
+// A stack of E matrices [rows, cols] below each other; a Q8 has tiles, whole ones in each matrix.
+conv2d_mat stack(PyObject* o, const char* name, int64_t E, int64_t rows, int64_t cols, unsigned bit, at::Device dev) {
+  const bool q8 = is_q8(o);
+  const at::Tensor& t = tensor(q8 ? q8_item(o, 0) : o, name);
+  if (t.dim() != 3 || t.size(0) != E || t.size(1) != rows || t.size(2) != cols)
+    refuse(name, "shape " + shape_name(t) + " does not match " + triple_name(E, rows, cols));
+  if (q8 ? t.scalar_type() != at::kFloat8_e4m3fn : !(type_bit(t.scalar_type()) & bit))
+    refuse(name, "dtype " + type_name(t.scalar_type()) + " is not " + (q8 ? "torch.float8_e4m3fn" : type_names(bit)));
+  if (t.device() != dev) refuse(name, "must be on " + dev.str() + " (got " + t.device().str() + ")");
+  const int64_t ld = rows > 1 ? t.stride(1) : E > 1 ? t.stride(0) : cols;
+  if ((cols > 1 && t.stride(2) != 1) || ld < cols || (E > 1 && t.stride(0) != rows * ld))
+    refuse(name, "features must be contiguous and the experts' rows evenly spaced, below each other");
+  void* data = t.data_ptr();
+  const int64_t unit = q8 ? 16 : 8;
+  if (reinterpret_cast<uintptr_t>(data) & 15 || ld % unit) refuse(name, "rows must start on 16-byte boundaries");
+  conv2d_mat m = {data, ld, q8 ? CONV2D_E4M3 : type_code(t.scalar_type()), 0, nullptr};
+  if (q8) {
+    if (group_arg(q8_item(o, 2)) != kTile) refuse(name, "8-bit experts have tiles (group TILE)");
+    if (rows % kWide || cols % kWide) refuse(name, "8-bit experts have whole tiles: features in multiples of 128");
+    const at::Tensor& sc = tensor(q8_item(o, 1), name);
+    if (sc.scalar_type() != at::kByte || sc.dim() != 3 || sc.size(0) != E || sc.size(1) != rows / kWide || sc.size(2) != cols / kWide)
+      refuse(name, "scales are uint8 of shape " + triple_name(E, rows / kWide, cols / kWide));
+    if (!sc.is_contiguous() || sc.device() != dev) refuse(name, "scales must be contiguous and on " + dev.str());
+    m.group = static_cast<int32_t>(kTile);
+    m.scale = static_cast<uint8_t*>(sc.data_ptr());
+  }
+  return m;
+}
+const float* biases(PyObject* o, const char* name, int64_t E, int64_t n, at::Device dev) {
+  if (!given(o)) return nullptr;
+  const at::Tensor& t = tensor(o, name);
+  if (t.scalar_type() != at::kFloat || t.dim() != 2 || t.size(0) != E || t.size(1) != n || !t.is_contiguous() || t.device() != dev)
+    refuse(name, "expected a contiguous float32 tensor of shape " + pair_name(E, n) + " on " + dev.str() + ", got " +
+                     type_name(t.scalar_type()) + " " + shape_name(t) + " on " + t.device().str());
+  const float* p = static_cast<const float*>(t.data_ptr());
+  if (reinterpret_cast<uintptr_t>(p) & 15) refuse(name, "must start on a 16-byte boundary");
+  return p;
+}
+
+// moe_fwd(x, router, w1, w2, k, b1, b2, act, gated, normalize, residual, y) -> (y, experts, weights)
+PyObject* moe_fwd(PyObject* const* a) {
+  const Source s = source(a[0], "x", kHalf);
+  const Source sr = source(a[1], "router", kHalf | kF32);
+  const unsigned bit = type_bit(s.type);
+  const int64_t T = s.rows, D = s.cols, E = sr.rows;
+  const conv2d_mat x = mat(a[0], "x", T, D, bit, s.dev), router = mat(a[1], "router", E, D, bit | kF32, s.dev);
+  if (T > 64) refuse("x", "at most 64 tokens (got " + std::to_string(T) + ")");
+  if (E < 1 || E > 256) refuse("router", "1 to 256 experts (got " + std::to_string(E) + ")");
+  const int64_t k = PyLong_Check(a[4]) ? PyLong_AsLongLong(a[4]) : -1;
+  if (k == -1 && PyErr_Occurred()) PyErr_Clear();  // beyond 64 bits
+  if (k < 1 || k > 16 || k > E) refuse("k", "1 to 16 experts a token, and no more than there are");
+  if (D % 8) refuse("x", "features in multiples of 8");
+  if (x.ld % 8) refuse("x", "rows must start on 16-byte boundaries");
+  if (router.ld % 8) refuse("router", "rows must start on 16-byte boundaries");
+  const bool gated = PyObject_IsTrue(a[8]) == 1, normalize = PyObject_IsTrue(a[9]) == 1;
+  const at::Tensor& t2 = tensor(is_q8(a[3]) ? q8_item(a[3], 0) : a[3], "w2");
+  if (t2.dim() != 3) refuse("w2", "expected experts by output by inner features, got shape " + shape_name(t2));
+  const int64_t F = t2.size(2), up = gated ? 2 * F : F;
+  if (F < 1 || F % 8) refuse("w2", "inner features in multiples of 8");
+  if (is_q8(a[2]) != is_q8(a[3])) throw Refused{"w1 and w2: both Q8 or neither"};
+  const conv2d_mat w1 = stack(a[2], "w1", E, up, D, bit, s.dev), w2 = stack(a[3], "w2", E, D, F, bit, s.dev);
+  const float *b1 = biases(a[5], "b1", E, up, s.dev), *b2 = biases(a[6], "b2", E, D, s.dev);
+  conv2d_mat mr, my;
+  if (given(a[10])) mr = mat(a[10], "residual", T, D, bit, s.dev);
+  at::Tensor y, experts, weights, ws;
+  my = given(a[11]) ? mat(a[11], "y", T, D, bit, s.dev) : new_mat(y, T, D, s.type, s.dev);
+  experts = make({T, k}, at::kInt, s.dev);
+  weights = make({T, k}, at::kFloat, s.dev);
+  const conv2d_moe_desc d = {static_cast<int32_t>(T), small(D, "x"),      small(F, "w2"),
+                             static_cast<int32_t>(E), static_cast<int32_t>(k), static_cast<int32_t>(PyLong_AsLong(a[7])),
+                             gated,                   normalize,          type_code(s.type)};
+  run(s.dev, "conv2d_moe_fwd", lib.conv2d_moe_fwd, [&](void* st) {
+    const size_t n = lib.conv2d_moe_fwd_workspace_size(&d, &w1, &w2);
+    ws = make({static_cast<int64_t>(n)}, at::kByte, s.dev);
+    return lib.conv2d_moe_fwd(&d, &x, &router, &w1, b1, &w2, b2, given(a[10]) ? &mr : nullptr, &my,
+                              static_cast<int32_t*>(experts.data_ptr()), static_cast<float*>(weights.data_ptr()),
+                              ws.data_ptr(), n, st);
+  });
+  return tuple({given(a[11]) ? same(a[11]) : wrap(y), wrap(experts), wrap(weights)});
+}
+
 // ---------------------------------------------------------------- module
 // No C++ exception leaves a call: what torch throws (out of memory, say) becomes a RuntimeError.
 template <PyObject* (*F)(PyObject* const*), Py_ssize_t N>
@@ -559,6 +644,7 @@ PyMethodDef methods[] = {{"init", init, METH_O, "Resolves the library's entry po
                          ENTRY(layer_norm_bwd, 12),
                          ENTRY(dense_fwd, 9),
                          ENTRY(dense_bwd, 12),
+                         ENTRY(moe_fwd, 12),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

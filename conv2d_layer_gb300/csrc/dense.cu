@@ -18,6 +18,45 @@
 #include "host.h"
 #include "rows.h"
 
+namespace c2d {
+
+// Row-major matrix [rows][cols] of row length ld as a GEMM operand, 128-byte swizzle: K-major, boxes of 128
+// bytes x box_rows; MN-major, boxes of 128 bytes x a k-block: 64 x 64 of 16 bits, 128 x 128 of 8.
+bool encode_operand(CUtensorMap* m, const void* base, int type, long rows, long cols, long ld, bool mn, int box_rows) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  const int es = type == CONV2D_E4M3 ? 1 : 2;
+  cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+  cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld) * es};
+  cuuint32_t box[2] = {static_cast<cuuint32_t>(128 / es), static_cast<cuuint32_t>(mn ? 128 / es : box_rows)};
+  cuuint32_t estr[2] = {1, 1};
+  const CUtensorMapDataType dt = type == CONV2D_E4M3   ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                                 : type == CONV2D_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                       : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  return fn(m, dt, 2, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Scales of an 8-bit matrix [rows][cols] with a scale for 128 columns or a tile, as an operand summed over its columns, or
+// (down) over its rows, which are tiled.
+DenseScales block_scales(const uint8_t* scale, int group, long rows, long cols, bool down) {
+  const long ng = (cols + kQ8Wide - 1) / kQ8Wide;
+  DenseScales s = {};
+  s.p = scale;
+  s.row_shift = down || group == kQ8Tile ? 7 : 0;
+  s.row_step = down ? 1 : ng;
+  s.block_step = down ? ng : 1;
+  s.rows = down ? cols : rows;
+  if (!down) {
+    const uintptr_t at = reinterpret_cast<uintptr_t>(scale);
+    s.words = ng % 16 == 0 && at % 16 == 0 ? 4 : ng % 4 == 0 && at % 4 == 0 ? 1 : 0;
+  }
+  return s;
+}
+
+}  // namespace c2d
+
 using namespace c2d;
 
 namespace {
@@ -152,24 +191,6 @@ GemmPlan plan_gemm(int mode, long m, long n, int kb, int sms, int q = kHalves, b
 }
 
 // ------------------------------------------------------------------ tensor maps
-// Row-major matrix [rows][cols] of row length ld as a GEMM operand, 128-byte swizzle: K-major, boxes of 128
-// bytes x box_rows; MN-major, boxes of 128 bytes x a k-block: 64 x 64 of 16 bits, 128 x 128 of 8.
-bool encode_operand(CUtensorMap* m, const void* base, int type, long rows, long cols, long ld, bool mn, int box_rows) {
-  EncodeTiledFn fn = encode_fn();
-  if (!fn) return false;
-  const int es = type == CONV2D_E4M3 ? 1 : 2;
-  cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
-  cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld) * es};
-  cuuint32_t box[2] = {static_cast<cuuint32_t>(128 / es), static_cast<cuuint32_t>(mn ? 128 / es : box_rows)};
-  cuuint32_t estr[2] = {1, 1};
-  const CUtensorMapDataType dt = type == CONV2D_E4M3   ? CU_TENSOR_MAP_DATA_TYPE_UINT8
-                                 : type == CONV2D_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
-                                                       : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
-  return fn(m, dt, 2, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 // Output [splits][rows][cols] of row length ld for the pair kernel's stores: boxes of 32 rows x RB bytes, swizzled
 // over RB bytes (32 or 64).
 bool encode_output(CUtensorMap* m, const void* base, int type, long rows, long cols, long ld, long splits) {
@@ -197,23 +218,6 @@ struct Operand {
   long rows, cols, ld;
   DenseScales scales;  // of a block-scaled product
 };
-
-// Scales of an 8-bit matrix [rows][cols] with a scale for 128 columns or a tile, as an operand summed over its columns, or
-// (down) over its rows, which are tiled.
-DenseScales block_scales(const uint8_t* scale, int group, long rows, long cols, bool down) {
-  const long ng = ceil_div(cols, kQ8Wide);
-  DenseScales s = {};
-  s.p = scale;
-  s.row_shift = down || group == kQ8Tile ? 7 : 0;
-  s.row_step = down ? 1 : ng;
-  s.block_step = down ? ng : 1;
-  s.rows = down ? cols : rows;
-  if (!down) {
-    const uintptr_t at = reinterpret_cast<uintptr_t>(scale);
-    s.words = ng % 16 == 0 && at % 16 == 0 ? 4 : ng % 4 == 0 && at % 4 == 0 ? 1 : 0;
-  }
-  return s;
-}
 
 // out[m][n] = sum_k R[m][k] C[n][k]. The rows of the output are the accumulator's lanes in the pair kernel and its
 // columns in the cluster kernel.

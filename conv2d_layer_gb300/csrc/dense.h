@@ -13,4 +13,8 @@ cudaError_t launch_dense_pair(const DenseGemmParams& p, int dt, int mode, int q,
 cudaError_t launch_dense_cluster(const DenseGemmParams& p, int dt, int mode, int q, int grid, size_t smem,
                                  cudaStream_t st);
 
+// Shared with the mixture-of-experts layer (dense.cu).
+bool encode_operand(CUtensorMap* m, const void* base, int type, long rows, long cols, long ld, bool mn, int box_rows);
+DenseScales block_scales(const uint8_t* scale, int group, long rows, long cols, bool down);
+
 }  // namespace c2d

@@ -194,5 +194,36 @@ def dense_bwd(x, w, dy, pre_act=None, act="identity", need_dx=True, need_dw=True
     return _binding().dense_bwd(x, w, dy, pre_act, _act(act), grad_dtype, dx, dw, dbias, need_dx, need_dw, need_dbias)
 
 
+# ------------------------------------------------------------------ mixture of experts
+class Moe(NamedTuple):
+    y: torch.Tensor
+    experts: torch.Tensor   # [rows, k] int32, by falling weight
+    weights: torch.Tensor   # [rows, k] fp32
+
+
+def moe_encode(w):
+    """Experts' weights [E, rows, cols] (rows a multiple of 128) as the Q8 that moe_fwd takes: one scale for 128 rows by
+    128 columns, none across two experts."""
+    if w.dim() != 3 or w.shape[1] % 128:
+        raise ValueError(f"w: experts by rows (a multiple of 128) by columns, got shape {tuple(w.shape)}")
+    q = q8_encode(w.reshape(-1, w.shape[2]), TILE)
+    return Q8(q.q.view(w.shape), q.scale.view(w.shape[0], w.shape[1] // 128, -1), TILE)
+
+
+@_streamed
+def moe_fwd(x, router, w1, w2, k, b1=None, b2=None, act="silu", gated=False, normalize=True, residual=None, y=None):
+    """A mixture-of-experts layer for 0 to 64 rows (decoded tokens): each goes through the k experts with the largest
+    logits x router^T (of equal ones the lower index first), y = sum of p_e (h_e w2_e^T + b2_e) + residual,
+    h_e = act(x w1_e^T + b1_e), times (x w3_e^T + b3_e) where gated.
+
+    x, residual, y [rows, D] bf16 or fp16; router [E, D] of that type or fp32, at most 256 experts; w1 [E, F, D] (gated:
+    [E, 2 F, D], w3's rows behind w1's) and w2 [E, D, F], of x's type, or both Q8 (moe_encode), which takes x and h to 8
+    bits too, one scale for 128 features; b1 [E, F] (gated: [E, 2 F]) and b2 [E, D] fp32. D and F are multiples of 8 (Q8:
+    of 128). p is the softmax over the chosen logits (normalize) or over all. residual may be y itself.
+    Returns Moe(y, experts, weights). Nothing is saved for a backward pass."""
+    return Moe(*_binding().moe_fwd(x, router, w1, w2, k, b1, b2, _act(act), gated, normalize, residual, y))
+
+
 __all__ = ["Q8", "RmsNorm", "LayerNorm", "q8_empty", "q8_scales", "q8_encode", "q8_decode", "rms_norm_fwd", "rms_norm_bwd",
-           "layer_norm_fwd", "layer_norm_bwd", "dense_fwd", "dense_bwd", "ACTS", "GROUP", "WIDE", "TILE"]
+           "layer_norm_fwd", "layer_norm_bwd", "dense_fwd", "dense_bwd",
+           "Moe", "moe_encode", "moe_fwd", "ACTS", "GROUP", "WIDE", "TILE"]

@@ -334,6 +334,45 @@ int conv2d_dense_bwd(const conv2d_dense_desc* desc, const conv2d_mat* x, const c
                      const conv2d_mat* pre_act, const conv2d_mat* dy, const conv2d_mat* dx, const conv2d_mat* dw,
                      float* dbias, void* ws, size_t ws_bytes, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Mixture of experts, for a few tokens (serving).
+ *   l = x R^T; a token's experts are the k largest of its logits (of equal ones
+ *   the lower index first; NaN counts as the largest), their weights
+ *   p = exp(l - max) / sum of exp(l - max) over the chosen experts (normalize)
+ *   or over all
+ *   h_e = act(x w1_e^T + b1_e), or gated: act(x w1_e^T + b1_e) times
+ *   (x w3_e^T + b3_e), where w3_e follows w1_e: rows F .. 2F - 1
+ *   y = sum over the chosen experts of p_e (h_e w2_e^T + b2_e) + residual
+ * The logits and p are formed in fp32; h is rounded to dtype once, and the
+ * experts' outputs are weighted and added in fp32. Experts in 8 bits take x
+ * and h in 8 bits too, one scale for 128 columns (h from its fp32 values),
+ * and run on the 8-bit operands. What an expert's weights hold reaches only
+ * the tokens that chose it.
+ * ------------------------------------------------------------------------ */
+typedef struct {
+    int32_t T;         /* tokens, at most 64 */
+    int32_t D, F;      /* features of a token, inner features of an expert: multiples of 8 (8 bits: of 128) */
+    int32_t E, k;      /* experts, at most 256, and chosen ones for each token, at most 16 */
+    int32_t act;
+    int32_t gated, normalize;
+    int32_t dtype;     /* BF16 or FP16: x, residual, y, and weights that are not E4M3 */
+} conv2d_moe_desc;
+
+/* Bytes of workspace (0 if the arguments are invalid); of the matrices only
+ * type, ld and group are looked at. */
+size_t conv2d_moe_fwd_workspace_size(const conv2d_moe_desc* desc, const conv2d_mat* w1, const conv2d_mat* w2);
+
+/* x, residual, y [T][D]; router [E][D] in dtype or FP32; w1 [E F][D] (gated:
+ * [E 2F][D]) and w2 [E D][F], the experts' matrices below each other, both in
+ * dtype or both E4M3 with group CONV2D_TILE; b1 [E][F] (gated: [E][2F]) and
+ * b2 [E][D] fp32, or NULL; residual may be NULL, and may be the same buffer
+ * as y. Rows of x, router, w1 and w2 start on 16-byte boundaries
+ * (CONV2D_ERR_UNSUPPORTED otherwise). experts [T][k] and weights [T][k]
+ * receive the chosen experts and p, the largest first. */
+int conv2d_moe_fwd(const conv2d_moe_desc* desc, const conv2d_mat* x, const conv2d_mat* router, const conv2d_mat* w1,
+                   const float* b1, const conv2d_mat* w2, const float* b2, const conv2d_mat* residual, const conv2d_mat* y,
+                   int32_t* experts, float* weights, void* ws, size_t ws_bytes, void* stream);
+
 /* Synchronises `stream`, then reads and clears this device's error word,
  * which kernels set when a bounded wait expires. Returns CONV2D_OK,
  * CONV2D_ERR_TIMEOUT (with *site, if non-NULL, set to the wait site code) or

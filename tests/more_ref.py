@@ -39,3 +39,31 @@ def layer_bwd_ref(h, gamma, mean, inv, dy, dh=None):
     g = dy * gamma
     dx = inv[:, None] * (g - g.mean(1, keepdim=True) - n * (g * n).mean(1, keepdim=True))
     return (dx if dh is None else dx + dh), (dy * n).sum(0), dy.sum(0)
+
+
+def moe_ref(x, router, w1, w2, k, b1, b2, act, gated, normalize, residual, hold):
+    """The layer in 64 bits, token by token: (y, experts, weights, magnitudes of y's terms). hold(v): what rows of 64-bit
+    values are once they are stored for the second product."""
+    T, D = x.shape
+    F = w2.shape[2]
+    logits = x @ router.t()
+    ys, mags, experts, weights = [], [], [], []
+    for t in range(T):
+        order = sorted(range(router.shape[0]), key=lambda e: (-float(logits[t, e]), e))[:k]
+        p = torch.softmax(logits[t, order] if normalize else logits[t], 0)
+        p = p if normalize else p[order]
+        y = torch.zeros(D, dtype=torch.float64, device=x.device) if residual is None else residual[t].clone()
+        mag = y.abs()
+        for j, e in enumerate(order):
+            z = w1[e] @ x[t] + (0 if b1 is None else b1[e])
+            h = act_ref(act, z[:F])
+            if gated:
+                h = h * z[F:]
+            h = hold(h[None])[0]
+            y = y + p[j] * (w2[e] @ h + (0 if b2 is None else b2[e]))
+            mag = mag + p[j] * (w2[e].abs() @ h.abs() + (0 if b2 is None else b2[e].abs()))
+        ys.append(y)
+        mags.append(mag)
+        experts.append(order)
+        weights.append(p)
+    return torch.stack(ys), torch.tensor(experts, dtype=torch.int32, device=x.device), torch.stack(weights), torch.stack(mags)
