@@ -673,10 +673,33 @@ __device__ __forceinline__ void scale_words(const DenseScales& s, long i, int j,
         if (4 * g + b < left) w[g] = (w[g] & ~(255u << (8 * b))) | static_cast<uint32_t>(p[(4 * g + b) * s.block_step]) << (8 * b);
   }
 }
+// The words of 128 rows from i (a multiple of 128) that share their scales: a lane a block, one load for the warp.
+__device__ __forceinline__ void tile_words(const DenseScales& s, long i, int j, int blocks, uint32_t (&w)[4], int lane) {
+  const int b = j * kScaleBlocks + (lane & (kScaleBlocks - 1));
+  uint32_t v = 127u;
+  if (i < s.rows && b < blocks) v = s.p[(i >> s.row_shift) * s.row_step + b * s.block_step];
+  v <<= 8 * (lane & 3);
+  v |= __shfl_xor_sync(0xffffffffu, v, 1);
+  v |= __shfl_xor_sync(0xffffffffu, v, 2);
+#pragma unroll
+  for (int g = 0; g < 4; ++g) w[g] = __shfl_sync(0xffffffffu, v, 4 * g);
+}
+// The words of a lane's four rows of the 128 lane rows from l0 (a multiple of 128).
+__device__ __forceinline__ void lane_words(const DenseScales& s, long l0, int j, int blocks, uint32_t (*w)[4], int lane) {
+  if (s.row_shift == 7) {  // uniform
+    tile_words(s, l0, j, blocks, w[0], lane);
+#pragma unroll
+    for (int i = 1; i < 4; ++i)
+#pragma unroll
+      for (int g = 0; g < 4; ++g) w[i][g] = w[0][g];
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) scale_words(s, l0 + lane + 32 * i, j, blocks, w[i]);
+  }
+}
 // A lane's words of 128 lane rows from l0 and up to 256 columns from c0 (BN), and their place in a set of slots.
 __device__ __forceinline__ void scales_load(const DenseGemmParams& p, uint32_t (&w)[12][4], long l0, long c0, int j, int lane) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) scale_words(p.sl, l0 + lane + 32 * i, j, p.kb_total, w[i]);
+  lane_words(p.sl, l0, j, p.kb_total, w, lane);
 #pragma unroll
   for (int i = 0; i < 8; ++i)
     if (32 * i < p.BN) scale_words(p.sc, c0 + lane + 32 * i, j, p.kb_total, w[4 + i]);

@@ -27,8 +27,8 @@ int check_desc(const conv2d_moe_desc* d) {
     return CONV2D_ERR_INVALID_ARG;
   if (d->T > kMoeTokens || d->E > kMoeExperts || d->k > kMoeChosen || d->D % 8 != 0 || d->F % 8 != 0)
     return CONV2D_ERR_UNSUPPORTED;
-  // TMA coordinates are 32-bit
-  if (2L * d->E * d->F > INT_MAX / 2 || static_cast<long>(d->E) * d->D > INT_MAX / 2) return CONV2D_ERR_UNSUPPORTED;
+  // TMA coordinates and the kernels' counts of k-blocks are 32-bit
+  if (d->D > (1 << 24) || d->F > (1 << 24) || 2L * d->E * d->F > INT_MAX / 2 || static_cast<long>(d->E) * d->D > INT_MAX / 2) return CONV2D_ERR_UNSUPPORTED;
   return CONV2D_OK;
 }
 int check_weights(const conv2d_moe_desc* d, const conv2d_mat* w1, const conv2d_mat* w2) {
@@ -68,16 +68,19 @@ MoePlan plan(const conv2d_moe_desc& d, bool q8) {
   return p;
 }
 
-// CTAs that split a unit's k-blocks (kb of them): as many as keep the GPU's two CTAs an SM in one wave, two k-blocks each
-// at least. units: those expected to have work.
-int cluster_for(double units, long kb, int sms) {
+#ifndef MOE_WAVE
+#define MOE_WAVE 2.0
+#endif
+// CTAs that split a unit's k-blocks (kb of them): as many as keep two on each SM, two k-blocks each at least. units: those
+// expected to have work.
+int cluster_for(double units, long kb, int sms, bool up) {
   int cl = 8;
-  while (cl > 1 && (units * cl > 2.0 * sms || kb < 2L * cl)) cl /= 2;
+  while (cl > 1 && (units * cl > (up ? MOE_WAVE : 2.0) * sms || kb < 2L * cl)) cl /= 2;
   return cl;
 }
 
 template <typename T, bool UP, int L, int Q>
-cudaError_t launch_experts(ExpertParams& p, int units, long kb, cudaStream_t st) {
+cudaError_t launch_experts(ExpertParams& p, int units, long kb, int sms, cudaStream_t st) {
   const auto kernel = expert_kernel<T, UP, L, Q>;
   static std::atomic<uint64_t> done{0};
   int dev = 0;
@@ -96,16 +99,18 @@ cudaError_t launch_experts(ExpertParams& p, int units, long kb, cudaStream_t st)
   static_assert(2 * moe_stage_bytes(L, 16) >= moe_join_bytes(L, 16, 8) && 2 * moe_stage_bytes(L, 32) >= moe_join_bytes(L, 32, 8) &&
                     2 * moe_stage_bytes(L, 64) >= moe_join_bytes(L, 64, 8) && 2 * moe_stage_bytes(L, 64) >= moe_join_bytes(L, 64, 2),
                 "the joined sums lie in the ring");
-  return launch_k(kernel, dim3(static_cast<unsigned>(units * p.cluster)), dim3(kMoeThreads + dense_scale_threads(Q)),
+  // CTAs without a cluster walk through the up product's units; the down product has one for each
+  const int grid = UP && p.cluster == 1 ? std::min(units, 2 * sms) : units * p.cluster;
+  return launch_k(kernel, dim3(static_cast<unsigned>(grid)), dim3(kMoeThreads + dense_scale_threads(Q)),
                   p.stages * stage + fixed, st, p.cluster, p);
 }
 template <bool UP, int L>
-cudaError_t launch_experts(ExpertParams& p, int dt, bool q8, int units, long kb, cudaStream_t st) {
+cudaError_t launch_experts(ExpertParams& p, int dt, bool q8, int units, long kb, int sms, cudaStream_t st) {
   if (dt == CONV2D_BF16)
-    return q8 ? launch_experts<__nv_bfloat16, UP, L, kBlockScaled>(p, units, kb, st)
-              : launch_experts<__nv_bfloat16, UP, L, kHalves>(p, units, kb, st);
-  return q8 ? launch_experts<__half, UP, L, kBlockScaled>(p, units, kb, st)
-            : launch_experts<__half, UP, L, kHalves>(p, units, kb, st);
+    return q8 ? launch_experts<__nv_bfloat16, UP, L, kBlockScaled>(p, units, kb, sms, st)
+              : launch_experts<__nv_bfloat16, UP, L, kHalves>(p, units, kb, sms, st);
+  return q8 ? launch_experts<__half, UP, L, kBlockScaled>(p, units, kb, sms, st)
+            : launch_experts<__half, UP, L, kHalves>(p, units, kb, sms, st);
 }
 
 template <typename T, typename R>
@@ -114,10 +119,9 @@ cudaError_t route(const RouteParams& p, cudaStream_t st) {
     return launch_k(kernel, dim3(static_cast<unsigned>(ceil_div(p.T, nt) * kRouteCluster)), dim3(kRouteThreads), 0, st,
                     kRouteCluster, p);
   };
-  if (p.T == 1) return go(route_kernel<T, R, 1>, 1);
-  if (p.T == 2) return go(route_kernel<T, R, 2>, 2);
-  if (p.T <= 4) return go(route_kernel<T, R, 4>, 4);
-  return go(route_kernel<T, R, 8>, 8);
+  if (p.T <= 16) return go(route_kernel<T, R, 1>, 1);
+  if (p.T <= 32) return go(route_kernel<T, R, 2>, 2);
+  return go(route_kernel<T, R, 4>, 4);
 }
 
 }  // namespace
@@ -197,7 +201,7 @@ int conv2d_moe_fwd(const conv2d_moe_desc* d, const conv2d_mat* x, const conv2d_m
   up.width = d->F;
   up.tiles = up_tiles;
   up.kb_total = static_cast<int>(ceil_div(d->D, kblock));
-  up.cluster = cluster_for(likely * up_tiles, up.kb_total, dev->sms);
+  up.cluster = cluster_for(likely * up_tiles, up.kb_total, dev->sms, true);
   up.bias = b1;
   up.h = base + pl.h;
   up.hq = reinterpret_cast<uint8_t*>(base + pl.h);
@@ -205,7 +209,8 @@ int conv2d_moe_fwd(const conv2d_moe_desc* d, const conv2d_mat* x, const conv2d_m
   down.rows = down.width = d->D;
   down.tiles = down_tiles;
   down.kb_total = static_cast<int>(ceil_div(d->F, kblock));
-  down.cluster = cluster_for(down_tiles, down.kb_total, dev->sms);
+  const long down_kb = static_cast<long>(likely * down.kb_total) + 1;
+  down.cluster = cluster_for(down_tiles, down_kb, dev->sms, false);
   down.bias = b2;
   down.y = y->data;
   down.ldy = ld_of(y, d->D);
@@ -231,11 +236,11 @@ int conv2d_moe_fwd(const conv2d_moe_desc* d, const conv2d_mat* x, const conv2d_m
   };
   LAUNCH("moe_route", st, run_route());
   auto run_up = [&] {
-    return d->gated ? launch_experts<true, 2>(up, d->dtype, q8, pl.slots * up_tiles, up.kb_total, st)
-                    : launch_experts<true, 1>(up, d->dtype, q8, pl.slots * up_tiles, up.kb_total, st);
+    return d->gated ? launch_experts<true, 2>(up, d->dtype, q8, pl.slots * up_tiles, up.kb_total, dev->sms, st)
+                    : launch_experts<true, 1>(up, d->dtype, q8, pl.slots * up_tiles, up.kb_total, dev->sms, st);
   };
   auto run_down = [&] {
-    return launch_experts<false, 1>(down, d->dtype, q8, down_tiles, static_cast<long>(likely * down.kb_total) + 1, st);
+    return launch_experts<false, 1>(down, d->dtype, q8, down_tiles, down_kb, dev->sms, st);
   };
   LAUNCH("moe_up", st, run_up());
   LAUNCH("moe_down", st, run_down());

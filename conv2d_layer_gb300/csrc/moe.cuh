@@ -16,8 +16,7 @@
 // walks through the experts, a segment of k each, with two accumulators, so that one expert's sums are weighted and added
 // in fp32 registers under the next one's MMAs. Sums have a fixed order: by rank, within a rank by expert.
 //
-// The down kernel's CTAs are resident beside the up kernel's (at most 113 KB of shared memory and 256 columns of tensor
-// memory each): they fill their rings with w2 while the up kernel ends. They take the routing from the kernel before the
+// The down kernel's CTAs are resident beside the up kernel's (at most 113 KB of shared memory and 256 columns of tensor memory each): they fill their rings with w2 while the up kernel ends. They take the routing from the kernel before the
 // up kernel, which that one has waited for.
 #pragma once
 #include "dense_gemm.cuh"
@@ -27,7 +26,7 @@ namespace c2d {
 constexpr int kMoeTokens = 64, kMoeExperts = 256, kMoeChosen = 16;
 constexpr int kMoeThreads = 320;  // TMA warp, MMA warp, 8 epilogue warps; one more for the scales of blocks
 constexpr int kMoeMaxStages = 8;
-constexpr int kRouteThreads = 256, kRouteCluster = 8;
+constexpr int kRouteThreads = 512, kRouteWarps = kRouteThreads / 32, kRouteCluster = 8;
 enum : int { kSiteMoeFull = 16, kSiteMoeEmpty = 17, kSiteMoeTFull = 18, kSiteMoeTEmpty = 19 };
 
 struct RouteParams {
@@ -74,11 +73,12 @@ __device__ __forceinline__ uint32_t logit_key(float v) {
 
 // A cluster of eight CTAs takes NT tokens: each CTA an eighth of the experts, a warp two of them at a time (or a slice of
 // their columns), for all NT tokens; token i's logits are gathered by CTA i, whose first warp chooses while the others
-// bring the token to 8 bits. Bound by latency (two passes through memory and a cluster's meeting): 3 us.
+// bring the token to 8 bits. Bound by latency (two passes through memory and a cluster's meeting), so the tokens are spread
+// over as many clusters as run at once (8 tokens, 128 experts of 4096: 64 us with eight tokens a cluster).
 template <typename T, typename R, int NT>
 __global__ void __launch_bounds__(kRouteThreads) route_kernel(const RouteParams p) {
   __shared__ float logits[kMoeExperts];
-  __shared__ float part[8][2][NT];
+  __shared__ float part[kRouteWarps][2][NT];
   pdl_entry();
   pdl_release();
   cluster_arrive();  // waited for before the other CTAs' shared memory is written
@@ -86,14 +86,14 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(const RouteParams 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int mine = rank < p.E ? (p.E - rank + kRouteCluster - 1) / kRouteCluster : 0;  // experts rank, rank + 8, ...
   const int pairs = (mine + 1) / 2;
-  const int slices = pairs >= 8 || pairs == 0 ? 1 : 8 / pairs;
+  const int slices = pairs >= kRouteWarps || pairs == 0 ? 1 : kRouteWarps / pairs;
   const int nv = p.D / 8;
   auto send = [&](int t, int e, float v) {
     const uint32_t at = mapa_shared(smem_u32(&logits[e]), static_cast<uint32_t>(t));
     st_shared_cluster_f32(at, v);
   };
   bool started = false;  // the other CTAs
-  for (int pair = slices > 1 ? warp % pairs : warp; pair < pairs; pair += slices > 1 ? pairs : 8) {
+  for (int pair = slices > 1 ? warp % pairs : warp; pair < pairs; pair += slices > 1 ? pairs : kRouteWarps) {
     const int slice = slices > 1 ? warp / pairs : 0;
     if (slice >= slices) break;
     const int e0 = rank + 2 * pair * kRouteCluster, e1 = min(e0 + kRouteCluster, p.E - 1);
@@ -103,7 +103,7 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(const RouteParams 
     float acc[2][NT];
 #pragma unroll
     for (int t = 0; t < NT; ++t) acc[0][t] = acc[1][t] = 0.f;
-#pragma unroll(NT >= 8 ? 1 : NT >= 2 ? 2 : 4)
+#pragma unroll(NT >= 4 ? 2 : 4)
     for (int v = slice * 32 + lane; v < nv; v += 32 * slices) {
       float w[2][8];
       if constexpr (sizeof(R) == 4) {
@@ -236,9 +236,9 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(const RouteParams 
 }
 
 // ---------------------------------------------------------------- experts' products
-// A segment of a CTA's work: k-blocks kb0 .. kb1 - 1 of the slot'th chosen expert.
+// A segment of a CTA's work: k-blocks kb0 .. kb1 - 1 of features f0 .. of the slot'th chosen expert.
 struct Segment {
-  int slot, kb0, kb1;
+  int slot, f0, kb0, kb1;
 };
 
 // Bytes of a stage, of the scales' two sets and of the joined sums (in the ring's place, once it is free).
@@ -247,6 +247,10 @@ __host__ __device__ constexpr int moe_slot_bytes(int L) { return 512 * (L + 1); 
 __host__ __device__ constexpr int moe_slots_bytes(int L) { return 2 * (kScaleBlocks / 4) * moe_slot_bytes(L); }
 __host__ __device__ constexpr int moe_join_bytes(int L, int BN, int cluster) {
   return cluster > 1 ? L * cluster * dense_own_cols(BN, cluster) * 512 : 0;
+}
+// Accumulators: two where a CTA has several segments, as far as 256 columns of tensor memory allow (two CTAs an SM).
+__host__ __device__ constexpr int moe_buffers(bool up, int L, int BN, int cluster, int q) {
+  return (up && cluster > 1) || (q == kBlockScaled && L * BN > 64) ? 1 : 2;
 }
 // Barriers, routing tables and what the epilogue's warps tell each other.
 constexpr int kMoeFixedBytes = 512 + kMoeTokens * kMoeChosen * 6 + kMoeExperts * 2 + 512;
@@ -270,7 +274,6 @@ __global__ void __launch_bounds__(kMoeThreads + dense_scale_threads(Q), 2) exper
   uint64_t* sempty = sfull + 2;
   uint32_t* tslot = reinterpret_cast<uint32_t*>(sempty + 2);
   uint32_t* mask = tslot + 1;              // chosen experts, one bit each
-  uint32_t* routed = mask + 8;             // up: tokens that chose this expert
   float* gate = reinterpret_cast<float*>(fixed + 512);                              // [T][k]
   int16_t* slot_of_choice = reinterpret_cast<int16_t*>(gate + kMoeTokens * kMoeChosen);  // [T][k]
   int16_t* list = slot_of_choice + kMoeTokens * kMoeChosen;                         // chosen experts in order
@@ -278,7 +281,7 @@ __global__ void __launch_bounds__(kMoeThreads + dense_scale_threads(Q), 2) exper
   const uint32_t sbase = smem_u32(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = CL > 1 ? static_cast<int>(cluster_ctarank()) : 0;
-  const int buffers = UP ? 1 : 2;
+  const int buffers = moe_buffers(UP, L, BN, CL, Q);
   const uint32_t tcols = tmem_cols_for(buffers * L * BN + (Q == kBlockScaled ? S * 4 * (L + 1) : 0));
 
   if (threadIdx.x == 0) {
@@ -296,104 +299,125 @@ __global__ void __launch_bounds__(kMoeThreads + dense_scale_threads(Q), 2) exper
     tma_prefetch_desc(&p.tl);
     tma_prefetch_desc(&p.tc);
   }
-  if (threadIdx.x < 10) mask[threadIdx.x] = 0u;  // and routed
-  __syncthreads();
+  if (threadIdx.x < 8) mask[threadIdx.x] = 0u;
   // The down kernel reads the routing without waiting for the up kernel, which has waited for the one that wrote it.
   if (UP) pdl_entry();
   const int choices = p.T * p.k;
-  for (int i = threadIdx.x; i < choices; i += blockDim.x) {
-    const int e = __ldcg(p.experts + i);
-    atomicOr(&mask[e >> 5], 1u << (e & 31));
-  }
-  __syncthreads();
-  int n = 0;  // chosen experts
-#pragma unroll
-  for (int i = 0; i < 8; ++i) n += __popc(mask[i]);
-  auto order = [&](int e) {  // of a chosen expert among them
-    int r = __popc(mask[e >> 5] & ((1u << (e & 31)) - 1u));
-    for (int i = 0; i < e >> 5; ++i) r += __popc(mask[i]);
-    return r;
-  };
-  for (int e = threadIdx.x; e < p.E; e += blockDim.x)
-    if (mask[e >> 5] >> (e & 31) & 1u) list[order(e)] = static_cast<int16_t>(e);
-  const int unit = static_cast<int>(blockIdx.x) / CL;
-  const int my_slot = UP ? unit / p.tiles : 0, f0 = (UP ? unit % p.tiles : unit) * 128;
-  if (UP && my_slot >= n) return;  // the whole cluster
-  __syncthreads();
-  const int my_expert = UP ? list[my_slot] : 0;
-  for (int i = threadIdx.x; i < choices; i += blockDim.x) {
-    const int e = __ldcg(p.experts + i);
-    if (UP) {
-      if (e == my_expert) atomicOr(&routed[i / p.k >> 5], 1u << (i / p.k & 31));
-    } else {
-      slot_of_choice[i] = static_cast<int16_t>(order(e));
-      gate[i] = __ldcg(p.weights + i);
-    }
-  }
+  // the first choice of each thread stays in a register (there are more than threads only from 20 tokens on)
+  const int tid = static_cast<int>(threadIdx.x);
+  const int choice = tid < choices ? __ldcg(p.experts + tid) : -1;
+  const float weight = !UP && tid < choices ? __ldcg(p.weights + tid) : 0.f;
   if (warp == 1) {
     tmem_alloc(tslot, tcols);
     tmem_relinquish();
   }
+  __syncthreads();
+  auto each_choice = [&](auto&& f) {
+    if (tid < choices) f(tid, choice, weight);
+    for (int i = tid + static_cast<int>(blockDim.x); i < choices; i += blockDim.x)
+      f(i, __ldcg(p.experts + i), UP ? 0.f : __ldcg(p.weights + i));
+  };
+  each_choice([&](int, int e, float) { atomicOr(&mask[e >> 5], 1u << (e & 31)); });
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tslot;
+  int n = 0;  // chosen experts
+#pragma unroll
+  for (int i = 0; i < 8; ++i) n += __popc(mask[i]);
+  // Units: tiles of the chosen experts (up), of the output (down). A CTA of its own takes one after the other (up), a
+  // cluster one.
+  const int unit0 = static_cast<int>(blockIdx.x) / CL, units = UP ? n * p.tiles : p.tiles;
+  if (UP && unit0 >= units) {  // the whole cluster
+    if (warp == 1) tmem_dealloc(tmem, tcols);
+    return;
+  }
+  each_choice([&](int i, int e, float w) {
+    // its order among the chosen ones
+    int r = __popc(mask[e >> 5] & ((1u << (e & 31)) - 1u));
+    for (int m = 0; m < e >> 5; ++m) r += __popc(mask[m]);
+    list[r] = static_cast<int16_t>(e);  // by each token that chose it, the same
+    slot_of_choice[i] = static_cast<int16_t>(r);
+    if (!UP) gate[i] = w;
+  });
+  __syncthreads();
   // Not before the tensor memory is taken: the down kernel's CTAs hold theirs until this kernel has ended.
   if (UP) pdl_release();
 
-  // This CTA's segments: its share of the expert's k-blocks (up) or of all chosen experts' (down).
-  const long all = UP ? p.kb_total : static_cast<long>(n) * p.kb_total;
-  const long g0 = all * rank / CL, g1 = all * (rank + 1) / CL;
-  const int segments = g1 > g0 ? static_cast<int>((g1 - 1) / p.kb_total - g0 / p.kb_total) + 1 : 0;
+  // This CTA's segments: units' k-blocks (up), or its share of all chosen experts' (down). In 32 bits (at most 256 experts
+  // of 2^28 / 64 k-blocks between eight CTAs; a cluster has 1, 2, 4 or 8), because the first copies wait for this.
+  const bool many = UP && CL == 1;
+  const uint32_t all = UP ? p.kb_total : static_cast<uint32_t>(n) * p.kb_total, share = 31 - __clz(CL);
+  const int g0 = static_cast<int>(all * rank >> share), g1 = static_cast<int>(all * (rank + 1) >> share);
+  const int slot0 = UP ? 0 : g0 / p.kb_total;
+  int segments = g1 > g0 ? 1 : 0;
+  if (many) segments = (units - unit0 + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x);
+  if (!UP && g1 > g0) segments = (g1 - 1) / p.kb_total - slot0 + 1;
+  const int blocks = many ? segments * p.kb_total : g1 - g0;  // k-blocks of this CTA
   auto segment = [&](int i) {
-    const int s = static_cast<int>(g0 / p.kb_total) + i;
-    const long base = static_cast<long>(s) * p.kb_total;
     Segment w;
-    w.kb0 = static_cast<int>(max(g0 - base, 0L));
-    w.kb1 = static_cast<int>(min(g1 - base, static_cast<long>(p.kb_total)));
-    w.slot = UP ? my_slot : s;
+    if constexpr (UP) {
+      const int u = unit0 + i * static_cast<int>(gridDim.x);
+      w.slot = u / p.tiles;
+      w.f0 = (u - w.slot * p.tiles) * 128;
+      w.kb0 = g0;
+      w.kb1 = g1;
+    } else {
+      w.slot = slot0 + i;
+      const int base = w.slot * p.kb_total;
+      w.kb0 = max(g0 - base, 0);
+      w.kb1 = min(g1 - base, p.kb_total);
+      w.f0 = unit0 * 128;
+    }
     return w;
   };
-  auto lane_row = [&](int slot) { return list[slot] * p.rows + f0; };  // of the first matrix
-  auto column_row = [&](int slot) { return UP ? 0 : slot * p.T; };
+  auto lane_row = [&](const Segment& w) { return list[w.slot] * p.rows + w.f0; };  // of the first matrix
+  auto column_row = [&](const Segment& w) { return UP ? 0 : w.slot * p.T; };
 
   if (Q == kBlockScaled && warp == kMoeThreads / 32) {
-    // The scales' warp (see scales_store): sets of 16 k-blocks, two ahead of the MMAs.
+    // The scales' warp (see scales_store): sets of 16 k-blocks, two ahead of the MMAs, the next one's words on their way.
+    int b = 0, i = 0, j = 0;
+    uint32_t par = 0, words[4 * L + 2][4];
+    Segment w = segment(0);
+    auto weights = [&] {
+#pragma unroll
+      for (int l = 0; l < L; ++l) lane_words(p.sl, lane_row(w) + l * p.second, j, p.kb_total, words + 4 * l, lane);
+    };
+    auto tokens = [&] {
+#pragma unroll
+      for (int r = 0; r < 2; ++r)
+        if (32 * r < BN) scale_words(p.sc, column_row(w) + lane + 32 * r, j, p.kb_total, words[4 * L + r]);
+    };
+#pragma unroll
+    for (int g = 0; g < 4; ++g) words[4 * L + 1][g] = 0x7f7f7f7fu;
+    j = w.kb0 / kScaleBlocks;
+    if (segments > 0) weights();
     if (!UP) pdl_entry();  // h's scales
-    int b = 0;
-    uint32_t par = 0;
-    for (int i = 0; i < segments; ++i) {
-      const Segment w = segment(i);
-      for (int j = w.kb0 / kScaleBlocks; j * kScaleBlocks < w.kb1; ++j) {
-        uint32_t words[4 * L + 2][4];
+    if (segments > 0) tokens();
+    while (i < segments) {
+      int ok = 1;
+      if (lane == 0) ok = wait(&sempty[b], par ^ 1, p.err, kSiteMoeEmpty) ? 1 : 0;
+      if (!__shfl_sync(0xffffffffu, ok, 0)) break;
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const uint32_t slot = sbase + slots + b * (moe_slots_bytes(L) / 2) + g * moe_slot_bytes(L) + lane * 16;
 #pragma unroll
         for (int l = 0; l < L; ++l)
-#pragma unroll
-          for (int r = 0; r < 4; ++r)
-            scale_words(p.sl, static_cast<long>(lane_row(w.slot)) + l * p.second + lane + 32 * r, j, p.kb_total, words[4 * l + r]);
-#pragma unroll
-        for (int r = 0; r < 2; ++r)
-          scale_words(p.sc, static_cast<long>(column_row(w.slot)) + lane + 32 * r, j, p.kb_total, words[4 * L + r]);
-        int ok = 1;
-        if (lane == 0) ok = wait(&sempty[b], par ^ 1, p.err, kSiteMoeEmpty) ? 1 : 0;
-        if (!__shfl_sync(0xffffffffu, ok, 0)) {
-          i = segments;
-          break;
-        }
-#pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          const uint32_t slot = sbase + slots + b * (moe_slots_bytes(L) / 2) + g * moe_slot_bytes(L) + lane * 16;
-#pragma unroll
-          for (int l = 0; l < L; ++l)
-            st_shared_v4(slot + 512 * l, words[4 * l][g], words[4 * l + 1][g], words[4 * l + 2][g], words[4 * l + 3][g]);
-          st_shared_v4(slot + 512 * L, words[4 * L][g], words[4 * L + 1][g], 0x7f7f7f7fu, 0x7f7f7f7fu);
-        }
-        fence_proxy_async_smem();  // they are read by tcgen05.cp
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sfull[b]);
-        b ^= 1;
-        if (b == 0) par ^= 1;
+          st_shared_v4(slot + 512 * l, words[4 * l][g], words[4 * l + 1][g], words[4 * l + 2][g], words[4 * l + 3][g]);
+        st_shared_v4(slot + 512 * L, words[4 * L][g], words[4 * L + 1][g], 0x7f7f7f7fu, 0x7f7f7f7fu);
       }
+      fence_proxy_async_smem();  // they are read by tcgen05.cp
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sfull[b]);
+      b ^= 1;
+      if (b == 0) par ^= 1;
+      if (++j * kScaleBlocks >= w.kb1) {
+        if (++i >= segments) break;
+        w = segment(i);
+        j = w.kb0 / kScaleBlocks;
+      }
+      weights();
+      tokens();
     }
     __syncwarp();
   } else if (warp == 0) {
@@ -404,14 +428,14 @@ __global__ void __launch_bounds__(kMoeThreads + dense_scale_threads(Q), 2) exper
         mbar_arrive_expect_tx(&full[st], stage_bytes);
 #pragma unroll
         for (int l = 0; l < L; ++l)
-          tma_load_2d(sbase + st * stage_bytes + l * 16384, &p.tl, &full[st], kb * kElems, lane_row(w.slot) + l * p.second);
+          tma_load_2d(sbase + st * stage_bytes + l * 16384, &p.tl, &full[st], kb * kElems, lane_row(w) + l * p.second);
       };
       auto columns = [&](const Segment& w, int kb, int st) {
-        tma_load_2d(sbase + st * stage_bytes + L * 16384, &p.tc, &full[st], kb * kElems, column_row(w.slot));
+        tma_load_2d(sbase + st * stage_bytes + L * 16384, &p.tc, &full[st], kb * kElems, column_row(w));
       };
       // The ring's first round: the weights, then (down: once the up kernel has ended) the tokens.
       int i = 0, kb = 0;
-      const int first = static_cast<int>(min(static_cast<long>(S), g1 - g0));
+      const int first = min(S, blocks);
       for (int pass = 0; pass < 2; ++pass) {
         if (pass == 1 && !UP) pdl_entry();
         i = 0;
@@ -428,8 +452,8 @@ __global__ void __launch_bounds__(kMoeThreads + dense_scale_threads(Q), 2) exper
       }
       if (first == S) par = 1;
       else s = first;
-      bool alive = g1 - g0 > first;
-      long done = first;
+      bool alive = blocks > first;
+      int done = first;
       while (alive) {
         const Segment w = segment(i);
         for (; kb < w.kb1; ++kb) {
@@ -448,8 +472,8 @@ __global__ void __launch_bounds__(kMoeThreads + dense_scale_threads(Q), 2) exper
         if (alive && ++i < segments) kb = segment(i).kb0;
         else if (alive) break;
       }
-      if (!alive && g1 - g0 > first)  // gave up: the copies of the stages before land before the CTA goes on
-        for (long j = max(0L, done - S); j < done; ++j)
+      if (!alive && blocks > first)  // gave up: the copies of the stages before land before the CTA goes on
+        for (int j = max(0, done - S); j < done; ++j)
           (void)wait(&full[j % S], static_cast<uint32_t>(j / S) & 1u, p.err, kSiteMoeFull);
     }
   } else if (warp == 1) {
@@ -462,8 +486,8 @@ __global__ void __launch_bounds__(kMoeThreads + dense_scale_threads(Q), 2) exper
       bool alive = true;
       for (int i = 0; alive && i < segments; ++i) {
         const Segment w = segment(i);
-        const int buf = i & 1;
-        if (!wait(&tempty[buf], ((i >> 1) & 1) ^ 1, p.err, kSiteMoeTEmpty)) break;
+        const int buf = buffers == 2 ? i & 1 : 0, round = buffers == 2 ? i >> 1 : i;
+        if (!wait(&tempty[buf], (round & 1) ^ 1, p.err, kSiteMoeTEmpty)) break;
         tc_fence_after();
         for (int kb = w.kb0; kb < w.kb1; ++kb) {
           if (!wait(&full[s], par, p.err, kSiteMoeFull) ||
@@ -472,7 +496,7 @@ __global__ void __launch_bounds__(kMoeThreads + dense_scale_threads(Q), 2) exper
             break;
           }
           tc_fence_after();
-          const uint32_t acc = kb > w.kb0, d = tmem + buf * BN;
+          const uint32_t acc = kb > w.kb0, d = tmem + buf * L * BN;
           if constexpr (Q == kBlockScaled) {
             if (kb == w.kb0 || (kb & 3) == 0) {
               sf = tmem + buffers * L * BN + s * 4 * (L + 1);
@@ -508,17 +532,24 @@ __global__ void __launch_bounds__(kMoeThreads + dense_scale_threads(Q), 2) exper
   // ---------------- epilogue: warps 2 .. 9, two groups of 128 lanes
   const int q = warp & 3, group = (warp - 2) >> 2;
   const bool epilogue = warp >= 2 && warp < kMoeThreads / 32;
-  const int feature = f0 + q * 32 + lane;
+  const int feature = unit0 * 128 + q * 32 + lane;  // down
   const bool on = feature < p.width;
   const uint32_t t0 = tmem + (static_cast<uint32_t>(q * 32) << 16);
   int ok = 1;
   float v[UP ? 1 : 2][16];
 
-  // Up: four tokens' sums of one feature a thread (m0 ..), from first to last: bias, activation, factor, 16 or 8 bits.
-  // Collective over a group (the 8-bit form takes a maximum over its 128 features).
+  // Up: four tokens' sums of one feature a thread (m0 ..): bias, activation, factor, 16 or 8 bits; for the tokens that
+  // chose the expert. Collective over a group (the 8-bit form takes a maximum over its 128 features).
   [[maybe_unused]] int flip = 0;
-  [[maybe_unused]] auto up_finish = [&](float (&a)[4], float (&b)[4], int m0) {
-    const float* bias = p.bias ? p.bias + static_cast<long>(my_expert) * p.rows + feature : nullptr;
+  [[maybe_unused]] auto up_finish = [&](const Segment& w, float (&a)[4], float (&b)[4], int m0) {
+    const int feature = w.f0 + q * 32 + lane;
+    const bool on = feature < p.width;
+    // lanes 0 .. 3 look whether their token is among those
+    bool mine = false;
+    if (lane < 4 && m0 + lane < p.T)
+      for (int j = 0; j < p.k; ++j) mine |= slot_of_choice[(m0 + lane) * p.k + j] == w.slot;
+    const uint32_t chose = __ballot_sync(0xffffffffu, mine);
+    const float* bias = p.bias ? p.bias + static_cast<long>(list[w.slot]) * p.rows + feature : nullptr;
     if (bias && on) {
       const float b1 = bias[0], b3 = L == 2 ? bias[p.second] : 0.f;
 #pragma unroll
@@ -548,17 +579,19 @@ __global__ void __launch_bounds__(kMoeThreads + dense_scale_threads(Q), 2) exper
       if (lane < 4) box[lane * 4 + q] = lane == 0 ? top[0] : lane == 1 ? top[1] : lane == 2 ? top[2] : top[3];
       named_bar_sync(1 + group, 128);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) top[e] = max(max(box[e * 4], box[e * 4 + 1]), max(box[e * 4 + 2], box[e * 4 + 3]));
+      for (int e = 0; e < 4; ++e) {
+        const uint4 m = *reinterpret_cast<const uint4*>(box + e * 4);
+        top[e] = max(max(m.x, m.y), max(m.z, m.w));
+      }
     }
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const int t = m0 + e;
-      if (t >= p.T || !(routed[t >> 5] >> (t & 31) & 1u)) continue;
-      const long row = static_cast<long>(my_slot) * p.T + t;
+      if (!(chose >> e & 1u)) continue;
+      const long row = static_cast<long>(w.slot) * p.T + m0 + e;
       if constexpr (Q == kBlockScaled) {
         const uint32_t byte = q8_scale_byte(top[e]);
         if (on) p.hq[row * p.width + feature] = static_cast<uint8_t>(q8_pack2(a[e] * q8_inv_scale(byte), 0.f));
-        if (q == 0 && lane == 0) p.hs[row * p.tiles + f0 / 128] = static_cast<uint8_t>(byte);
+        if (q == 0 && lane == 0) p.hs[row * p.tiles + w.f0 / 128] = static_cast<uint8_t>(byte);
       } else {
         if (on) static_cast<T*>(p.h)[row * p.width + feature] = from_f<T>(a[e]);
       }
@@ -576,11 +609,40 @@ __global__ void __launch_bounds__(kMoeThreads + dense_scale_threads(Q), 2) exper
 
   if (epilogue) {
     if constexpr (UP) {
-      if (segments > 0) {
-        // (a wait that ran out leaves garbage and its mark: the group's warps go on together)
-        if (lane == 0) (void)wait(&tfull[0], 0, p.err, kSiteMoeTFull);
+      // (A wait that ran out leaves garbage and its mark: a group's warps go on together.)
+      if (CL > 1) {
+        if (segments > 0 && lane == 0) (void)wait(&tfull[0], 0, p.err, kSiteMoeTFull);
         __syncwarp();
         tc_fence_after();
+      }
+      for (int i = 0; CL == 1 && i < segments; ++i) {
+        const Segment w = segment(i);
+        const int buf = buffers == 2 ? i & 1 : 0, round = buffers == 2 ? i >> 1 : i;
+        if (lane == 0) (void)wait(&tfull[buf], round & 1, p.err, kSiteMoeTFull);
+        __syncwarp();
+        tc_fence_after();
+#pragma unroll 1
+        for (int c = group * 16; c < BN && c < p.T; c += 32) {
+          uint32_t r[L][16];
+#pragma unroll
+          for (int m = 0; m < L; ++m) {
+            tmem_ld16(t0 + (buf * L + m) * BN + c, r[m]);
+            tmem_ld_wait(r[m]);
+          }
+#pragma unroll
+          for (int e = 0; e < 16; e += 4) {
+            if (c + e >= p.T) break;  // uniform
+            float o[L][4];
+#pragma unroll
+            for (int m = 0; m < L; ++m)
+#pragma unroll
+              for (int j = 0; j < 4; ++j) o[m][j] = __uint_as_float(r[m][e + j]);
+            up_finish(w, o[0], o[L - 1], c + e);
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&tempty[buf]);
       }
     } else {
 #pragma unroll
@@ -588,7 +650,7 @@ __global__ void __launch_bounds__(kMoeThreads + dense_scale_threads(Q), 2) exper
 #pragma unroll
         for (int e = 0; e < 16; ++e) v[j][e] = 0.f;
       for (int i = 0; i < segments && ok; ++i) {
-        const int buf = i & 1, slot = segment(i).slot;
+        const int buf = i & 1, slot = segment(i).slot;  // two accumulators
         if (lane == 0) ok = wait(&tfull[buf], (i >> 1) & 1, p.err, kSiteMoeTFull) ? 1 : 0;
         ok = __shfl_sync(0xffffffffu, ok, 0);
         if (!ok) break;
@@ -635,24 +697,15 @@ __global__ void __launch_bounds__(kMoeThreads + dense_scale_threads(Q), 2) exper
     }
   };
   if (CL == 1) {
-    if (epilogue) {
+    if (!UP && epilogue) {
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const int c = group * 16 + 32 * j;
         if (c >= BN || c >= p.T) break;  // uniform
-        float o[16], o2[16];
+        float o[16];
         sums(j, c, 0, o);
-        if (L == 2) sums(j, c, 1, o2);
-        if constexpr (UP) {
 #pragma unroll
-          for (int e = 0; e < 16; e += 4) {
-            if (c + e >= p.T) break;  // uniform
-            up_finish(*reinterpret_cast<float(*)[4]>(o + e), *reinterpret_cast<float(*)[4]>(o2 + e), c + e);
-          }
-        } else {
-#pragma unroll
-          for (int e = 0; e < 16; ++e) down_finish(o[e], c + e);
-        }
+        for (int e = 0; e < 16; ++e) down_finish(o[e], c + e);
       }
     }
   } else {
@@ -674,6 +727,7 @@ __global__ void __launch_bounds__(kMoeThreads + dense_scale_threads(Q), 2) exper
 #pragma unroll
           for (int g = 0; g < 4; ++g) {
             const int quad = c / 4 + g;
+            if (quad * 4 >= p.T) break;  // uniform
             const uint32_t at = sbase + static_cast<uint32_t>((((m * CL + rank) * own_cols + quad / CL * 4) * 128 + q * 32 + lane) * 4);
             const uint32_t to = mapa_shared(at, static_cast<uint32_t>(quad % CL));
 #pragma unroll
@@ -701,7 +755,7 @@ __global__ void __launch_bounds__(kMoeThreads + dense_scale_threads(Q), 2) exper
         }
         const int m0 = (i * CL + rank) * 4;
         if constexpr (UP) {
-          up_finish(o[0], o[L - 1], m0);
+          up_finish(segment(0), o[0], o[L - 1], m0);
         } else {
 #pragma unroll
           for (int e = 0; e < 4; ++e) down_finish(o[0][e], m0 + e);
