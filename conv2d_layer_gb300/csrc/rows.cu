@@ -20,17 +20,18 @@ namespace c2d {
 namespace {
 
 // ------------------------------------------------------------------ 8 bits, 16-bit types in whole groups
-// Encode (ENC) or decode of rows of whole 32-column groups: two threads a group, 16 values each, two groups of a
-// thread in flight (200704 x 256 there and back: 46.5 us, 0.99 of the copy rate; 59 us with 16-byte accesses).
+// Encode (ENC) or decode of rows of whole groups (32 or 128 columns; TILE, decode only: tiles of 128 x 128): GL = 2 or 8
+// threads a group, 16 values each, two groups of a thread in flight (200704 x 256 there and back in groups of 32: 46.5
+// us, 0.99 of the copy rate; 59 us with 16-byte accesses).
 // total = rows * cols / 16 < 2^31; x rows on 32-byte, q rows on 16-byte boundaries.
-template <typename T, bool ENC, bool LATE>
+template <typename T, bool ENC, int GL, bool TILE, bool LATE>
 __global__ void __launch_bounds__(256) q8_flat_kernel(T* x, long ldx, uint8_t* q, long ldq, uint8_t* scale,
                                                       uint32_t total, FastDiv div_nv) {
   if (!LATE) pdl_entry();
   pdl_release();
   constexpr int N = 2;
   const uint32_t step = gridDim.x * 256u;
-  const int ng = static_cast<int>(div_nv.d / 2);
+  const int ng = static_cast<int>(div_nv.d / GL);
   for (uint32_t j0 = blockIdx.x * 256u + threadIdx.x; j0 < total; j0 += N * step) {
     uint32_t w[N][8];
     uint4 raw[N];
@@ -48,12 +49,12 @@ __global__ void __launch_bounds__(256) q8_flat_kernel(T* x, long ldx, uint8_t* q
         ld_32b(x + row[i] * ldx + v[i] * 16, w[i]);
       } else {
         raw[i] = *reinterpret_cast<const uint4*>(q + row[i] * ldq + v[i] * 16);
-        sb[i] = scale[row[i] * ng + (v[i] >> 1)];
+        sb[i] = scale[(TILE ? row[i] >> 7 : row[i]) * ng + v[i] / GL];
       }
     }
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      if (j0 + i * step >= total) break;  // the two threads of a group go on together (total is even)
+      if (j0 + i * step >= total) break;  // the threads of a group go on together (total is a multiple of them)
       float f[16];
       if constexpr (ENC) {
         const T* e = reinterpret_cast<const T*>(w[i]);
@@ -63,23 +64,27 @@ __global__ void __launch_bounds__(256) q8_flat_kernel(T* x, long ldx, uint8_t* q
           f[k] = to_f(e[k]);
           m = fmaxf(m, fabsf(f[k]));
         }
-        const uint32_t pair = 3u << (threadIdx.x & 30u);
-        uint32_t top = __float_as_uint(m);
-        top = max(top, __shfl_xor_sync(pair, top, 1));
+        const uint32_t group = ((1u << GL) - 1u) << (threadIdx.x & (32u - GL));
+        auto join = [&](uint32_t x) {
+#pragma unroll
+          for (int o = 1; o < GL; o <<= 1) x = max(x, __shfl_xor_sync(group, x, o));
+          return x;
+        };
+        uint32_t top = join(__float_as_uint(m));
         bool finite = true;
         if (top == 0x7f800000u) {
           finite = false;
           top = 0u;
 #pragma unroll
           for (int k = 0; k < 16; ++k) top = max(top, finite_bits(f[k]));
-          top = max(top, __shfl_xor_sync(pair, top, 1));
+          top = join(top);
         }
         const uint32_t byte = q8_scale_byte(top);
         const float inv = q8_inv_scale(byte);
         *reinterpret_cast<uint4*>(q + row[i] * ldq + v[i] * 16) =
             make_uint4(q8_pack4(f, inv, finite), q8_pack4(f + 4, inv, finite), q8_pack4(f + 8, inv, finite),
                        q8_pack4(f + 12, inv, finite));
-        if ((v[i] & 1) == 0) scale[row[i] * ng + (v[i] >> 1)] = static_cast<uint8_t>(byte);
+        if (v[i] % GL == 0) scale[row[i] * ng + v[i] / GL] = static_cast<uint8_t>(byte);
       } else {
         const Q8Raw<16> rw = {{raw[i].x, raw[i].y, raw[i].z, raw[i].w}};
         const float sc = q8_scale(sb[i]);
@@ -104,7 +109,8 @@ int stream_grid(long items) { return static_cast<int>(std::max<long>(1, std::min
 template <typename T, bool ENC>
 bool q8_flat(const void* x, long ldx, const void* q, long ldq, uint8_t* scale, int group, long rows, int cols, int late,
              cudaStream_t st, cudaError_t* e) {
-  if (group != kQ8Group || cols % kQ8Group != 0 || ldx % 16 != 0 || ldq % 16 != 0 ||
+  const int width = group == kQ8Tile ? 128 : group;
+  if (width == 0 || (ENC && group == kQ8Tile) || cols % width != 0 || ldx % 16 != 0 || ldq % 16 != 0 ||
       reinterpret_cast<uintptr_t>(x) % 32 != 0 || rows * (cols / 16) > 0x7fffffffL)
     return false;
   const long total = rows * (cols / 16);
@@ -113,12 +119,16 @@ bool q8_flat(const void* x, long ldx, const void* q, long ldq, uint8_t* scale, i
                     static_cast<T*>(const_cast<void*>(x)), ldx, static_cast<uint8_t*>(const_cast<void*>(q)), ldq, scale,
                     static_cast<uint32_t>(total), make_fastdiv(static_cast<uint32_t>(cols / 16)));
   };
-  if constexpr (!ENC)
-    if (late) {
-      *e = go(q8_flat_kernel<T, ENC, true>);
-      return true;
-    }
-  *e = go(q8_flat_kernel<T, ENC, false>);
+  auto with = [&](auto gl, auto tile) {
+    constexpr int GL = decltype(gl)::value;
+    constexpr bool TILE = decltype(tile)::value;
+    if constexpr (!ENC)
+      if (late) return go(q8_flat_kernel<T, ENC, GL, TILE, true>);
+    return go(q8_flat_kernel<T, ENC, GL, TILE, false>);
+  };
+  if (group == kQ8Group) *e = with(std::integral_constant<int, 2>{}, std::false_type{});
+  else if (group == kQ8Wide) *e = with(std::integral_constant<int, 8>{}, std::false_type{});
+  else if constexpr (!ENC) *e = with(std::integral_constant<int, 8>{}, std::true_type{});
   return true;
 }
 
@@ -126,7 +136,7 @@ bool q8_flat(const void* x, long ldx, const void* q, long ldq, uint8_t* scale, i
 // Encode with one scale for 128 rows by 128 columns: a block a tile, whose values stay in registers (64 a thread, all
 // loads in flight at once) between their maximum and their output. V values a vector; zeros past the ends.
 template <typename T, int V>
-__global__ void __launch_bounds__(256) q8_tile_kernel(const T* x, long ldx, uint8_t* q, long ldq, uint8_t* scale,
+__global__ void __launch_bounds__(256, V == 1 || sizeof(T) == 4 ? 2 : 3) q8_tile_kernel(const T* x, long ldx, uint8_t* q, long ldq, uint8_t* scale,
                                                       long rows, int cols, int ng) {
   pdl_entry();
   constexpr int TPR = 128 / V, RP = 256 / TPR, N = 128 / RP;  // threads a row, rows a pass, passes
@@ -136,32 +146,65 @@ __global__ void __launch_bounds__(256) q8_tile_kernel(const T* x, long ldx, uint
   for (long tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
     const long row0 = tile / ng * 128 + tr;
     const int c = static_cast<int>(tile % ng) * 128 + tc;
-    T e[N][V];
+    // The values stay as they came: widened for the maximum and again for the output, not kept widened in between (83
+    // registers and two blocks an SM then: 16384 x 4096 bf16 60 us).
+    constexpr int W = V * sizeof(T) < 4 ? 1 : V * static_cast<int>(sizeof(T)) / 4;
+    uint32_t e[N][W];
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      if (c < cols && row0 + i * RP < rows) {
-        ld_vec<T, V>(x + (row0 + i * RP) * ldx + c, e[i]);
-      } else {
 #pragma unroll
-        for (int k = 0; k < V; ++k) e[i][k] = from_f<T>(0.f);
+      for (int k = 0; k < W; ++k) e[i][k] = 0u;
+      if (c < cols && row0 + i * RP < rows) {
+        const T* p = x + (row0 + i * RP) * ldx + c;
+        if constexpr (W == 8) ld_32b(p, e[i]);
+        else if constexpr (W == 4) *reinterpret_cast<uint4*>(e[i]) = *reinterpret_cast<const uint4*>(p);
+        else if constexpr (sizeof(T) == 4) e[i][0] = *reinterpret_cast<const uint32_t*>(p);
+        else e[i][0] = *reinterpret_cast<const uint16_t*>(p);
       }
     }
     pdl_release();
-    uint32_t m = 0u;
+    auto widen = [&](int i, float (&f)[V]) {
 #pragma unroll
-    for (int i = 0; i < N; ++i)
+      for (int k = 0; k < V; ++k) {
+        if constexpr (sizeof(T) == 4) {
+          f[k] = __uint_as_float(e[i][k]);
+        } else {
+          const uint16_t h = static_cast<uint16_t>(e[i][k / 2] >> (16 * (k & 1)));
+          f[k] = to_f(*reinterpret_cast<const T*>(&h));
+        }
+      }
+    };
+    auto top = [&](auto&& of) {
+      uint32_t m = 0u;
 #pragma unroll
-      for (int k = 0; k < V; ++k) m = max(m, finite_bits(to_f(e[i][k])));
-    m = row_max<256>(m, red);
+      for (int i = 0; i < N; ++i) {
+        float f[V];
+        widen(i, f);
+        m = max(m, of(f));
+      }
+      return row_max<256>(m, red);
+    };
+    uint32_t m = top([](const float (&f)[V]) { return absmax(f); });
+    auto narrow = [&] {
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+#pragma unroll
+        for (int k = 0; k < W; ++k) asm volatile("" : "+r"(e[i][k]));
+    };
+    narrow();
+    const bool finite = m != kInf;
+    if (!finite) {  // the same for the whole block
+      m = top([](const float (&f)[V]) { return absmax_finite(f); });
+      narrow();
+    }
     const uint32_t byte = q8_scale_byte(m);
     const float inv = q8_inv_scale(byte);
     if (threadIdx.x == 0) scale[tile] = static_cast<uint8_t>(byte);
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       float f[V];
-#pragma unroll
-      for (int k = 0; k < V; ++k) f[k] = to_f(e[i][k]);
-      if (c < cols && row0 + i * RP < rows) q8_store<V>(q + (row0 + i * RP) * ldq + c, f, inv, false);
+      widen(i, f);
+      if (c < cols && row0 + i * RP < rows) q8_store<V>(q + (row0 + i * RP) * ldq + c, f, inv, finite);
     }
   }
 }
