@@ -673,7 +673,11 @@ __device__ __forceinline__ void scale_words(const DenseScales& s, long i, int j,
         if (4 * g + b < left) w[g] = (w[g] & ~(255u << (8 * b))) | static_cast<uint32_t>(p[(4 * g + b) * s.block_step]) << (8 * b);
   }
 }
-// The words of 128 rows from i (a multiple of 128) that share their scales: a lane a block, one load for the warp.
+// The words of rows that share their scales, those of a tile, where these are not read in words: a lane takes a block's
+// byte, and the lanes are put together. (One byte after the other in each lane, the 16 of a set took the scales' warp as
+// long as the MMAs of the set: gradients of 8192 x 8192 x 2048 334 us, 320 so; 329 with the lanes put together only where
+// the words are used.)
+__device__ __forceinline__ bool by_tile(const DenseScales& s) { return s.row_shift == 7 && !s.words; }  // uniform
 __device__ __forceinline__ void tile_words(const DenseScales& s, long i, int j, int blocks, uint32_t (&w)[4], int lane) {
   const int b = j * kScaleBlocks + (lane & (kScaleBlocks - 1));
   uint32_t v = 127u;
@@ -686,7 +690,7 @@ __device__ __forceinline__ void tile_words(const DenseScales& s, long i, int j, 
 }
 // The words of a lane's four rows of the 128 lane rows from l0 (a multiple of 128).
 __device__ __forceinline__ void lane_words(const DenseScales& s, long l0, int j, int blocks, uint32_t (*w)[4], int lane) {
-  if (s.row_shift == 7) {  // uniform
+  if (by_tile(s)) {
     tile_words(s, l0, j, blocks, w[0], lane);
 #pragma unroll
     for (int i = 1; i < 4; ++i)
@@ -701,8 +705,12 @@ __device__ __forceinline__ void lane_words(const DenseScales& s, long l0, int j,
 __device__ __forceinline__ void scales_load(const DenseGemmParams& p, uint32_t (&w)[12][4], long l0, long c0, int j, int lane) {
   lane_words(p.sl, l0, j, p.kb_total, w, lane);
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
-    if (32 * i < p.BN) scale_words(p.sc, c0 + lane + 32 * i, j, p.kb_total, w[4 + i]);
+  for (int i = 0; i < 8; ++i) {
+    if (32 * i >= p.BN) break;  // uniform
+    // (tiles are the columns of the pair kernel, whose own tiles start at multiples of 32)
+    if (by_tile(p.sc)) tile_words(p.sc, c0 + 32 * i, j, p.kb_total, w[4 + i], lane);
+    else scale_words(p.sc, c0 + lane + 32 * i, j, p.kb_total, w[4 + i]);
+  }
 }
 __device__ __forceinline__ void scales_store(const uint32_t (&w)[12][4], uint32_t set, int BN, int lane) {
 #pragma unroll
