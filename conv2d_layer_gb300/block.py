@@ -95,7 +95,7 @@ class FeedForward(_Norm):
             y, _ = ops.dense_fwd(u, self.w2, self.b2, residual=n.h)
             kept_n, kept_u = (n.q8, ops.q8_encode(u)) if self.q8 else (n.y, u)
         self.saved = (n.h, n.inv_std if self.layer else n.inv_rms, kept_n, z, kept_u) + ((n.mean,) if self.layer else ())
-        self.trained = self.w8 if bits8 else (self.w1, self.w2)
+        self.trained = self.w8 if bits8 else None
         return y
 
     def bwd(self, dy):
@@ -103,7 +103,7 @@ class FeedForward(_Norm):
         if self.saved is None:
             raise RuntimeError("bwd follows a fwd_train")
         (h, inv, n, z, u, *mean), self.saved = self.saved, None
-        (w1, w2), self.trained = self.trained, None
+        (w1, w2), self.trained = self.trained or (self.w1, self.w2), None
         du, _, _ = ops.dense_bwd(u, w2, dy, dw=self.dw2, dbias=self.db2)
         dn, _, _ = ops.dense_bwd(n, w1, du, z, self.act, dw=self.dw1, dbias=self.db1)
         if self.layer:

@@ -68,14 +68,11 @@ MoePlan plan(const conv2d_moe_desc& d, bool q8) {
   return p;
 }
 
-#ifndef MOE_WAVE
-#define MOE_WAVE 2.0
-#endif
-// CTAs that split a unit's k-blocks (kb of them): as many as keep two on each SM, two k-blocks each at least. units: those
-// expected to have work.
-int cluster_for(double units, long kb, int sms, bool up) {
+// CTAs that split a unit's k-blocks (kb of them): as many as keep two on each SM, two k-blocks each at least (one
+// token, 8 of 64 experts of (2048, 1024) bf16 25.7 us from L2, 27.6 with one on each). units: those expected to have work.
+int cluster_for(double units, long kb, int sms) {
   int cl = 8;
-  while (cl > 1 && (units * cl > (up ? MOE_WAVE : 2.0) * sms || kb < 2L * cl)) cl /= 2;
+  while (cl > 1 && (units * cl > 2.0 * sms || kb < 2L * cl)) cl /= 2;
   return cl;
 }
 
@@ -187,7 +184,6 @@ int conv2d_moe_fwd(const conv2d_moe_desc* d, const conv2d_mat* x, const conv2d_m
     p->BN = bn;
     p->E = d->E;
     p->k = d->k;
-    p->slots_max = pl.slots;
     p->act = d->act;
     p->experts = experts;
     p->weights = weights;
@@ -201,7 +197,7 @@ int conv2d_moe_fwd(const conv2d_moe_desc* d, const conv2d_mat* x, const conv2d_m
   up.width = d->F;
   up.tiles = up_tiles;
   up.kb_total = static_cast<int>(ceil_div(d->D, kblock));
-  up.cluster = cluster_for(likely * up_tiles, up.kb_total, dev->sms, true);
+  up.cluster = cluster_for(likely * up_tiles, up.kb_total, dev->sms);
   up.bias = b1;
   up.h = base + pl.h;
   up.hq = reinterpret_cast<uint8_t*>(base + pl.h);
@@ -210,7 +206,7 @@ int conv2d_moe_fwd(const conv2d_moe_desc* d, const conv2d_mat* x, const conv2d_m
   down.tiles = down_tiles;
   down.kb_total = static_cast<int>(ceil_div(d->F, kblock));
   const long down_kb = static_cast<long>(likely * down.kb_total) + 1;
-  down.cluster = cluster_for(down_tiles, down_kb, dev->sms, false);
+  down.cluster = cluster_for(down_tiles, down_kb, dev->sms);
   down.bias = b2;
   down.y = y->data;
   down.ldy = ld_of(y, d->D);

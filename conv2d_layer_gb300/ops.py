@@ -1,4 +1,5 @@
-"""The residual block's operators on torch tensors: RMS norm, layer norm, dense layer, 8-bit checkpoints.
+"""The residual block's operators on torch tensors: RMS norm, layer norm, dense layer, 8-bit checkpoints, and a mixture
+of experts.
 
 Matrices are 2-D CUDA tensors of rows by features; rows may be strided (the last dimension is contiguous, the
 first element on a 16-byte boundary). Outputs that are not handed in are allocated with torch; workspaces
@@ -174,8 +175,8 @@ def dense_fwd(x, w, bias=None, act="identity", residual=None, save="none", dtype
     (gelu is the tanh form).
 
     dtype (bf16 or fp16) is the type of y, residual and the operands that are not Q8; it is x's (or w's) where
-    those are not Q8. Two Q8 operands with one scale a row run on the 8-bit tensor cores, other Q8 operands are
-    decoded first. save: "none", "full" or "q8" (groups of 32) keeps the activation's input for dense_bwd;
+    those are not Q8. Two Q8 operands run on the 8-bit tensor cores where both have one scale a row, or where x has one
+    for 128 columns (WIDE) and w that or TILE; other Q8 operands are decoded first. save: "none", "full" or "q8" (groups of 32) keeps the activation's input for dense_bwd;
     pre_act: an output for it. residual may be y itself. Returns (y, pre_act)."""
     if save not in _SAVES:
         raise ValueError(f"save: one of {sorted(_SAVES)}, got {save!r}")
@@ -190,7 +191,8 @@ def dense_bwd(x, w, dy, pre_act=None, act="identity", need_dx=True, need_dw=True
               grad_dtype=torch.float32, dx=None, dw=None, dbias=None):
     """(dx, dw, dbias) of dense_fwd. x, w and pre_act may be Q8; pre_act is what dense_fwd saved (not needed
     without an activation). dw is fp32 or dy's type (grad_dtype); dw and dbias that are handed in (both, or all
-    that is asked for) are accumulated into. The gradient of the residual is dy."""
+    that is asked for) are accumulated into. The gradient of the residual is dy. With w of TILE dx is a product of 8-bit
+    operands (dz with a scale for 128 columns); other Q8 operands are decoded first."""
     return _binding().dense_bwd(x, w, dy, pre_act, _act(act), grad_dtype, dx, dw, dbias, need_dx, need_dw, need_dbias)
 
 

@@ -192,7 +192,8 @@ int conv2d_bwd(const conv2d_desc* desc, const void* x, const void* w, const floa
                float* dgamma, float* dbeta, void* ws, size_t ws_bytes, void* stream);
 
 /* ------------------------------------------------------------------------
- * The residual block: RMS norm, dense layer, 8-bit activation checkpoints.
+ * The residual block: RMS norm, layer norm, dense layer, 8-bit activation
+ * checkpoints.
  *
  * These calls take matrices of rows (tokens, or the pixels of an NHWC tensor:
  * N*H*W rows of C columns) by columns (features), each described by a
@@ -300,8 +301,12 @@ int conv2d_layer_norm_bwd(int64_t rows, int32_t cols, const conv2d_mat* h, const
  * for y over K and dx over N; dw is summed in pieces over M, so that no more is
  * lost than 2.4e-5 in FP32 and a fifth of the rounding of FP16 or BF16.
  * Where x and w are both E4M3 with one scale a row, the product runs on the
- * 8-bit operands and the scales are applied to its sums; any other E4M3
- * operand is decoded to dtype first. */
+ * 8-bit operands and the scales are applied to its sums. Where x has a scale
+ * for each row and 128 columns, and w that or one for 128 rows by 128 columns
+ * (CONV2D_TILE), it runs on the 8-bit operands too: the tensor core multiplies
+ * the partial sums of every 32 columns by both scales (bytes 1 to 254, as
+ * conv2d_q8_encode writes them) before it adds them up. Any other E4M3 operand
+ * is decoded to dtype first. */
 typedef struct {
     int64_t M;          /* rows of x and y */
     int32_t K, N;       /* features in and out */
@@ -329,7 +334,10 @@ int conv2d_dense_fwd(const conv2d_dense_desc* desc, const conv2d_mat* x, const c
  * dz (the gradient of residual is dy itself). x, w and pre_act may be E4M3
  * (checkpoints); pre_act may be NULL when act is IDENTITY. dz is stored in
  * dtype for the two products (with IDENTITY dz is dy); dbias sums the
- * unrounded dz. dx, dw, dbias may be NULL, not all; dw is FP32 or dtype. */
+ * unrounded dz. dx, dw, dbias may be NULL, not all; dw is FP32 or dtype.
+ * Where w is E4M3 with CONV2D_TILE, dx is a product of 8-bit operands: dz, as
+ * it is stored in dtype, goes to E4M3 with a scale for each row and 128
+ * columns. Other E4M3 operands of the two products are decoded. */
 int conv2d_dense_bwd(const conv2d_dense_desc* desc, const conv2d_mat* x, const conv2d_mat* w,
                      const conv2d_mat* pre_act, const conv2d_mat* dy, const conv2d_mat* dx, const conv2d_mat* dw,
                      float* dbias, void* ws, size_t ws_bytes, void* stream);
