@@ -648,26 +648,24 @@ constexpr int kScaleBlocks = 16;
 __host__ __device__ constexpr int dense_slot_bytes(int BN) { return BN > 128 ? 1536 : 1024; }
 __host__ __device__ constexpr int dense_slot_cols(int BN) { return BN > 128 ? 12 : 8; }
 __host__ __device__ constexpr int dense_slots_bytes(int BN) { return 2 * (kScaleBlocks / 4) * dense_slot_bytes(BN); }
-// The words of row i for k-blocks 16j .. 16j + 15; 1.0 (127) past the ends, where the elements are zero.
-__device__ __forceinline__ void scale_words(const DenseScales& s, long i, int j, int blocks, uint32_t (&w)[4]) {
+// The words of row i for the k-blocks of set j (4 G of them); 1.0 (127) past the ends, where the elements are zero.
+template <int G>
+__device__ __forceinline__ void scale_words(const DenseScales& s, long i, int j, int blocks, uint32_t (&w)[G]) {
 #pragma unroll
-  for (int g = 0; g < 4; ++g) w[g] = 0x7f7f7f7fu;
+  for (int g = 0; g < G; ++g) w[g] = 0x7f7f7f7fu;
   if (i >= s.rows) return;
-  const uint8_t* p = s.p + (i >> s.row_shift) * s.row_step + j * kScaleBlocks * s.block_step;
-  const int left = blocks - j * kScaleBlocks;
-  if (s.words == 4 && left >= kScaleBlocks) {
-    const uint4 v = *reinterpret_cast<const uint4*>(p);
-    w[0] = v.x;
-    w[1] = v.y;
-    w[2] = v.z;
-    w[3] = v.w;
+  const uint8_t* p = s.p + (i >> s.row_shift) * s.row_step + j * (4 * G) * s.block_step;
+  const int left = blocks - j * (4 * G);
+  if (s.words == 4 && left >= 4 * G) {
+    if constexpr (G == 4) *reinterpret_cast<uint4*>(w) = *reinterpret_cast<const uint4*>(p);
+    else *reinterpret_cast<uint2*>(w) = *reinterpret_cast<const uint2*>(p);
   } else if (s.words) {
 #pragma unroll
-    for (int g = 0; g < 4; ++g)
+    for (int g = 0; g < G; ++g)
       if (4 * g < left) w[g] = reinterpret_cast<const uint32_t*>(p)[g];
   } else {
 #pragma unroll
-    for (int g = 0; g < 4; ++g)
+    for (int g = 0; g < G; ++g)
 #pragma unroll
       for (int b = 0; b < 4; ++b)
         if (4 * g + b < left) w[g] = (w[g] & ~(255u << (8 * b))) | static_cast<uint32_t>(p[(4 * g + b) * s.block_step]) << (8 * b);
@@ -678,38 +676,40 @@ __device__ __forceinline__ void scale_words(const DenseScales& s, long i, int j,
 // long as the MMAs of the set: gradients of 8192 x 8192 x 2048 334 us, 320 so; 329 with the lanes put together only where
 // the words are used.)
 __device__ __forceinline__ bool by_tile(const DenseScales& s) { return s.row_shift == 7 && !s.words; }  // uniform
-__device__ __forceinline__ void tile_words(const DenseScales& s, long i, int j, int blocks, uint32_t (&w)[4], int lane) {
-  const int b = j * kScaleBlocks + (lane & (kScaleBlocks - 1));
+template <int G>
+__device__ __forceinline__ void tile_words(const DenseScales& s, long i, int j, int blocks, uint32_t (&w)[G], int lane) {
+  const int b = j * (4 * G) + (lane & (4 * G - 1));
   uint32_t v = 127u;
   if (i < s.rows && b < blocks) v = s.p[(i >> s.row_shift) * s.row_step + b * s.block_step];
   v <<= 8 * (lane & 3);
   v |= __shfl_xor_sync(0xffffffffu, v, 1);
   v |= __shfl_xor_sync(0xffffffffu, v, 2);
 #pragma unroll
-  for (int g = 0; g < 4; ++g) w[g] = __shfl_sync(0xffffffffu, v, 4 * g);
+  for (int g = 0; g < G; ++g) w[g] = __shfl_sync(0xffffffffu, v, 4 * g);
 }
 // The words of a lane's four rows of the 128 lane rows from l0 (a multiple of 128).
-__device__ __forceinline__ void lane_words(const DenseScales& s, long l0, int j, int blocks, uint32_t (*w)[4], int lane) {
+template <int G>
+__device__ __forceinline__ void lane_words(const DenseScales& s, long l0, int j, int blocks, uint32_t (*w)[G], int lane) {
   if (by_tile(s)) {
-    tile_words(s, l0, j, blocks, w[0], lane);
+    tile_words<G>(s, l0, j, blocks, w[0], lane);
 #pragma unroll
     for (int i = 1; i < 4; ++i)
 #pragma unroll
-      for (int g = 0; g < 4; ++g) w[i][g] = w[0][g];
+      for (int g = 0; g < G; ++g) w[i][g] = w[0][g];
   } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) scale_words(s, l0 + lane + 32 * i, j, blocks, w[i]);
+    for (int i = 0; i < 4; ++i) scale_words<G>(s, l0 + lane + 32 * i, j, blocks, w[i]);
   }
 }
 // A lane's words of 128 lane rows from l0 and up to 256 columns from c0 (BN), and their place in a set of slots.
 __device__ __forceinline__ void scales_load(const DenseGemmParams& p, uint32_t (&w)[12][4], long l0, long c0, int j, int lane) {
-  lane_words(p.sl, l0, j, p.kb_total, w, lane);
+  lane_words<4>(p.sl, l0, j, p.kb_total, w, lane);
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     if (32 * i >= p.BN) break;  // uniform
     // (tiles are the columns of the pair kernel, whose own tiles start at multiples of 32)
-    if (by_tile(p.sc)) tile_words(p.sc, c0 + 32 * i, j, p.kb_total, w[4 + i], lane);
-    else scale_words(p.sc, c0 + lane + 32 * i, j, p.kb_total, w[4 + i]);
+    if (by_tile(p.sc)) tile_words<4>(p.sc, c0 + 32 * i, j, p.kb_total, w[4 + i], lane);
+    else scale_words<4>(p.sc, c0 + lane + 32 * i, j, p.kb_total, w[4 + i]);
   }
 }
 __device__ __forceinline__ void scales_store(const uint32_t (&w)[12][4], uint32_t set, int BN, int lane) {
@@ -731,8 +731,10 @@ __device__ __forceinline__ void scales_copy(uint32_t slot, uint32_t taddr, int B
 }
 // Where k-block kb's slot lies in its set, and whether it is the first or last of a set for a loop over kb0 .. kb1 - 1.
 __device__ __forceinline__ uint32_t slot_of(int kb, int BN) { return (kb % kScaleBlocks / 4) * dense_slot_bytes(BN); }
-__device__ __forceinline__ bool set_begins(int kb, int kb0) { return kb == kb0 || kb % kScaleBlocks == 0; }
-__device__ __forceinline__ bool set_ends(int kb, int kb1) { return kb == kb1 - 1 || kb % kScaleBlocks == kScaleBlocks - 1; }
+template <int N = kScaleBlocks>
+__device__ __forceinline__ bool set_begins(int kb, int kb0) { return kb == kb0 || kb % N == 0; }
+template <int N = kScaleBlocks>
+__device__ __forceinline__ bool set_ends(int kb, int kb1) { return kb == kb1 - 1 || kb % N == N - 1; }
 
 // Columns of a unit that one CTA of its cluster joins: groups of four, owned in turn.
 __host__ __device__ constexpr int dense_own_cols(int BN, int cluster) { return (BN / 4 + cluster - 1) / cluster * 4; }

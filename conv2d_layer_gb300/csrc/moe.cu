@@ -89,7 +89,7 @@ cudaError_t launch_experts(ExpertParams& p, int units, long kb, int sms, cudaStr
     done.fetch_or(uint64_t(1) << dev);
   }
   const size_t stage = moe_stage_bytes(L, p.BN);
-  const size_t fixed = 1024 + kMoeFixedBytes + (Q == kBlockScaled ? moe_slots_bytes(L) : 0);
+  const size_t fixed = 1024 + moe_fixed_bytes(UP) + (Q == kBlockScaled ? moe_slots_bytes(L) : 0);
   // k-blocks of a CTA, but never less than two stages: the joined sums take the ring's place
   p.stages = static_cast<int>(std::min<size_t>({static_cast<size_t>(kMoeMaxStages), (kMoeSmem - fixed) / stage,
                                                 static_cast<size_t>(std::max<long>(2, ceil_div(kb, p.cluster)))}));

@@ -190,7 +190,10 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(const RouteParams 
     for (int j = 0; j < p.k; ++j) {
       uint32_t best = 0u;
 #pragma unroll
-      for (int i = 0; i < kMoeExperts / 32; ++i) best = max(best, key[i]);
+      for (int i = 0; i < kMoeExperts / 32; ++i) {
+        if (32 * i >= p.E) break;  // uniform
+        best = max(best, key[i]);
+      }
       best = __reduce_max_sync(0xffffffffu, best);
       int at = kMoeExperts;
 #pragma unroll
@@ -251,7 +254,8 @@ struct Segment {
 // Bytes of a stage, of the scales' two sets and of the joined sums (in the ring's place, once it is free).
 __host__ __device__ constexpr int moe_stage_bytes(int L, int BN) { return L * 16384 + BN * 128; }
 __host__ __device__ constexpr int moe_slot_bytes(int L) { return 512 * (L + 1); }
-__host__ __device__ constexpr int moe_slots_bytes(int L) { return 2 * (kScaleBlocks / 4) * moe_slot_bytes(L); }
+constexpr int kMoeGroups = 2, kMoeSet = 4 * kMoeGroups;  // k-blocks of a set of scales: three stages fit beside its slots
+__host__ __device__ constexpr int moe_slots_bytes(int L) { return 2 * kMoeGroups * moe_slot_bytes(L); }
 __host__ __device__ constexpr int moe_join_bytes(int L, int BN, int cluster) {
   return cluster > 1 ? L * cluster * dense_own_cols(BN, cluster) * 512 : 0;
 }
@@ -259,8 +263,10 @@ __host__ __device__ constexpr int moe_join_bytes(int L, int BN, int cluster) {
 __host__ __device__ constexpr int moe_buffers(bool up, int L, int BN, int cluster, int q) {
   return (up && cluster > 1) || (q == kBlockScaled && L * BN > 64) ? 1 : 2;
 }
-// Barriers, routing tables and what the epilogue's warps tell each other.
-constexpr int kMoeFixedBytes = 512 + kMoeTokens * kMoeChosen * 6 + kMoeExperts * 2 + 512;
+// Barriers (512 bytes), routing tables (down: gates too) and what the epilogue's warps tell each other.
+__host__ __device__ constexpr int moe_fixed_bytes(bool up) {
+  return 512 + kMoeTokens * kMoeChosen * (up ? 2 : 6) + kMoeExperts * 2 + 256;
+}
 
 template <typename T, bool UP, int L, int Q>
 __global__ void __launch_bounds__(kMoeThreads + dense_scale_threads(Q), 2) expert_kernel(const __grid_constant__ ExpertParams p) {
@@ -281,8 +287,8 @@ __global__ void __launch_bounds__(kMoeThreads + dense_scale_threads(Q), 2) exper
   uint64_t* sempty = sfull + 2;
   uint32_t* tslot = reinterpret_cast<uint32_t*>(sempty + 2);
   uint32_t* mask = tslot + 1;              // chosen experts, one bit each
-  float* gate = reinterpret_cast<float*>(fixed + 512);                              // [T][k]
-  int16_t* slot_of_choice = reinterpret_cast<int16_t*>(gate + kMoeTokens * kMoeChosen);  // [T][k]
+  float* gate = reinterpret_cast<float*>(fixed + 512);                                               // down: [T][k]
+  int16_t* slot_of_choice = reinterpret_cast<int16_t*>(gate + (UP ? 0 : kMoeTokens * kMoeChosen));  // [T][k]
   int16_t* list = slot_of_choice + kMoeTokens * kMoeChosen;                         // chosen experts in order
   uint32_t* group_max = reinterpret_cast<uint32_t*>(list + kMoeExperts);            // [2][2][4][4]
   const uint32_t sbase = smem_u32(smem);
@@ -352,7 +358,7 @@ __global__ void __launch_bounds__(kMoeThreads + dense_scale_threads(Q), 2) exper
   if (UP) pdl_release();
 
   // This CTA's segments: units' k-blocks (up), or its share of all chosen experts' (down). In 32 bits (at most 256 experts
-  // of 2^28 / 64 k-blocks between eight CTAs; a cluster has 1, 2, 4 or 8), because the first copies wait for this.
+  // of 2^24 / 64 k-blocks between eight CTAs, E F at most 2^29; a cluster has a power of two of CTAs), because the first copies wait for this.
   const bool many = UP && CL == 1;
   const uint32_t all = UP ? p.kb_total : static_cast<uint32_t>(n) * p.kb_total, share = 31 - __clz(CL);
   const int g0 = static_cast<int>(all * rank >> share), g1 = static_cast<int>(all * (rank + 1) >> share);
@@ -382,22 +388,22 @@ __global__ void __launch_bounds__(kMoeThreads + dense_scale_threads(Q), 2) exper
   auto column_row = [&](const Segment& w) { return UP ? 0 : w.slot * p.T; };
 
   if (Q == kBlockScaled && warp == kMoeThreads / 32) {
-    // The scales' warp (see scales_store): sets of 16 k-blocks, two ahead of the MMAs, the next one's words on their way.
+    // The scales' warp (see scales_store): sets of eight k-blocks, two ahead of the MMAs, the next one's words on their way.
     int b = 0, i = 0, j = 0;
-    uint32_t par = 0, words[4 * L + 2][4];
+    uint32_t par = 0, words[4 * L + 2][kMoeGroups];
     Segment w = segment(0);
     auto weights = [&] {
 #pragma unroll
-      for (int l = 0; l < L; ++l) lane_words(p.sl, lane_row(w) + l * p.second, j, p.kb_total, words + 4 * l, lane);
+      for (int l = 0; l < L; ++l) lane_words<kMoeGroups>(p.sl, lane_row(w) + l * p.second, j, p.kb_total, words + 4 * l, lane);
     };
     auto tokens = [&] {
 #pragma unroll
       for (int r = 0; r < 2; ++r)
-        if (32 * r < BN) scale_words(p.sc, column_row(w) + lane + 32 * r, j, p.kb_total, words[4 * L + r]);
+        if (32 * r < BN) scale_words<kMoeGroups>(p.sc, column_row(w) + lane + 32 * r, j, p.kb_total, words[4 * L + r]);
     };
 #pragma unroll
-    for (int g = 0; g < 4; ++g) words[4 * L + 1][g] = 0x7f7f7f7fu;
-    j = w.kb0 / kScaleBlocks;
+    for (int g = 0; g < kMoeGroups; ++g) words[4 * L + 1][g] = 0x7f7f7f7fu;
+    j = w.kb0 / kMoeSet;
     if (segments > 0) weights();
     if (!UP) pdl_entry();  // h's scales
     if (segments > 0) tokens();
@@ -406,7 +412,7 @@ __global__ void __launch_bounds__(kMoeThreads + dense_scale_threads(Q), 2) exper
       if (lane == 0) ok = wait(&sempty[b], par ^ 1, p.err, kSiteMoeEmpty) ? 1 : 0;
       if (!__shfl_sync(0xffffffffu, ok, 0)) break;
 #pragma unroll
-      for (int g = 0; g < 4; ++g) {
+      for (int g = 0; g < kMoeGroups; ++g) {
         const uint32_t slot = sbase + slots + b * (moe_slots_bytes(L) / 2) + g * moe_slot_bytes(L) + lane * 16;
 #pragma unroll
         for (int l = 0; l < L; ++l)
@@ -418,10 +424,10 @@ __global__ void __launch_bounds__(kMoeThreads + dense_scale_threads(Q), 2) exper
       if (lane == 0) mbar_arrive(&sfull[b]);
       b ^= 1;
       if (b == 0) par ^= 1;
-      if (++j * kScaleBlocks >= w.kb1) {
+      if (++j * kMoeSet >= w.kb1) {
         if (++i >= segments) break;
         w = segment(i);
-        j = w.kb0 / kScaleBlocks;
+        j = w.kb0 / kMoeSet;
       }
       weights();
       tokens();
@@ -498,7 +504,7 @@ __global__ void __launch_bounds__(kMoeThreads + dense_scale_threads(Q), 2) exper
         tc_fence_after();
         for (int kb = w.kb0; kb < w.kb1; ++kb) {
           if (!wait(&full[s], par, p.err, kSiteMoeFull) ||
-              (Q == kBlockScaled && set_begins(kb, w.kb0) && !wait(&sfull[sb], spar, p.err, kSiteMoeFull))) {
+              (Q == kBlockScaled && set_begins<kMoeSet>(kb, w.kb0) && !wait(&sfull[sb], spar, p.err, kSiteMoeFull))) {
             alive = false;
             break;
           }
@@ -507,7 +513,7 @@ __global__ void __launch_bounds__(kMoeThreads + dense_scale_threads(Q), 2) exper
           if constexpr (Q == kBlockScaled) {
             if (kb == w.kb0 || (kb & 3) == 0) {
               sf = tmem + buffers * L * BN + s * 4 * (L + 1);
-              const uint32_t slot = sbase + slots + sb * (moe_slots_bytes(L) / 2) + (kb % kScaleBlocks / 4) * moe_slot_bytes(L);
+              const uint32_t slot = sbase + slots + sb * (moe_slots_bytes(L) / 2) + (kb % kMoeSet / 4) * moe_slot_bytes(L);
 #pragma unroll
               for (int m = 0; m <= L; ++m) tmem_copy_scales<false>(sf + 4 * m, scales_desc(slot + 512 * m));
             }
@@ -515,7 +521,7 @@ __global__ void __launch_bounds__(kMoeThreads + dense_scale_threads(Q), 2) exper
 #pragma unroll
             for (int m = 0; m < L; ++m)
               dense_mma<false, Q, false, false>(l + m * 1024, c, d + m * BN, s * stage_bytes, id, acc, sf + 4 * m, sf + 4 * L);
-            if (set_ends(kb, w.kb1)) {
+            if (set_ends<kMoeSet>(kb, w.kb1)) {
               mma_commit(&sempty[sb]);
               sb ^= 1;
               if (sb == 0) spar ^= 1;
@@ -720,7 +726,6 @@ __global__ void __launch_bounds__(kMoeThreads + dense_scale_threads(Q), 2) exper
     // MMAs are done with theirs; columns are owned four at a time in turn.
     const int own_cols = dense_own_cols(BN, CL);
     __syncwarp();
-    __syncthreads();
     cluster_sync();
     if (epilogue) {
 #pragma unroll
@@ -744,7 +749,6 @@ __global__ void __launch_bounds__(kMoeThreads + dense_scale_threads(Q), 2) exper
       }
     }
     __syncwarp();
-    __syncthreads();
     cluster_sync();  // every CTA's sums have arrived; from here on a CTA reads its own shared memory only
     if (epilogue) {
       const int quads = (p.T + 3) / 4, own = quads > rank ? (quads - rank + CL - 1) / CL : 0;
