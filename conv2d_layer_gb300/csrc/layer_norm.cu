@@ -1,4 +1,6 @@
 // layer_norm.cu - layer norm's C entry points (kernels in rows_norm.cuh).
+#include <atomic>
+
 #include "rows.h"
 #include "rows_norm.cuh"
 
@@ -234,75 +236,104 @@ cudaError_t layer_any(const NormArgs& a, int sms, cudaStream_t st) {
   return rows_fwd<T, 1, kLayer>(a, st);
 }
 
-// Layer norm backward of 16-bit rows of 32-byte vectors, one a thread: as norm_bwd_kernel, with the arithmetic in packed
-// pairs, one meeting of the block a row, and the row at hand kept as it came (16 of its registers instead of 32). Bound by
-// memory: 8192 x 4096 bf16 with dh moves 268 MB in 57 us with the column sums (61 in norm_bwd_kernel), 0.70 of the copy
-// rate; 512 threads an SM of 126 registers each are all that its sums of dgamma and dbeta leave.
+// Layer norm backward of 16-bit rows: as norm_bwd_kernel, with the arithmetic in packed pairs and one meeting of the block
+// a row. A row's h, dy and dh come by bulk copies into one of kRing places in shared memory, four rows ahead (192 KB an SM):
+// the sums of dgamma and dbeta leave no registers for that (512 threads an SM of 126 each, with one row ahead in registers:
+// 8192 x 4096 bf16 54 us, 48 KB in flight). A thread has eight features in each half of the row, so that its 16-byte
+// accesses meet no bank twice. Bound by memory: 8192 x 4096 bf16 with dh moves 268 MB in 44 us, 0.90 of the copy rate, then
+// the column sums in 5.
+constexpr int kRing = 4;
+constexpr int kSiteLayerBwd = 20;
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
+               "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
 template <typename T, int MT, int MB>
 __global__ void __launch_bounds__(MT, MB) layer_bwd_kernel(const NormBwdArgs a) {
-  pdl_entry();
-  constexpr int V = 16;
+  extern __shared__ uint4 ring[];  // [kRing][h, dy, dh][cols]
+  __shared__ uint64_t full[kRing];
   __shared__ float2 part[2][MT / 32];
   const int t = static_cast<int>(threadIdx.x), nw = static_cast<int>(blockDim.x) >> 5;
-  const int c = t * V;
-  const bool on = c < a.cols;
+  const int half = a.cols / 2, c = t * 8;
+  const bool on = c < half, skip = a.dh && a.dx;
   const float over = 1.f / static_cast<float>(a.cols);
-  const T* hb = static_cast<const T*>(a.h) + c;
-  const T* db = static_cast<const T*>(a.dy) + c;
-  const T* sb = static_cast<const T*>(a.dh) + c;
-  T* xb = static_cast<T*>(a.dx) + c;
-  float2 g[V / 2], acc[V / 2], accb[V / 2];
+  const uint32_t bytes = static_cast<uint32_t>(a.cols) * 2u, place = 3u * bytes, base = smem_u32(ring);
+  if (t == 0) {
+    for (int i = 0; i < kRing; ++i) mbar_init(&full[i], 1);
+    fence_mbar_init();
+  }
+  pdl_entry();
+  __syncthreads();
+  const long step = gridDim.x;
+  auto request = [&](long row, int i) {  // one thread
+    if (row >= a.rows) return;
+    mbar_arrive_expect_tx(&full[i], (skip ? 3u : 2u) * bytes);
+    const uint32_t to = base + i * place;
+    bulk_load(to, static_cast<const T*>(a.h) + row * a.ldh, bytes, &full[i]);
+    bulk_load(to + bytes, static_cast<const T*>(a.dy) + row * a.lddy, bytes, &full[i]);
+    if (skip) bulk_load(to + 2 * bytes, static_cast<const T*>(a.dh) + row * a.lddh, bytes, &full[i]);
+  };
+  long row = blockIdx.x;  // the grid has no more blocks than there are rows
+  if (t == 0)
+    for (int i = 0; i < kRing; ++i) request(row + i * step, i);
+
+  float2 g[8], acc[8], accb[8];
 #pragma unroll
-  for (int k = 0; k < V / 2; ++k) {
-    g[k] = on ? *reinterpret_cast<const float2*>(a.gamma + c + 2 * k) : splat(0.f);
+  for (int k = 0; k < 8; ++k) {
+    g[k] = on ? *reinterpret_cast<const float2*>(a.gamma + (k < 4 ? c : half + c - 8) + 2 * k) : splat(0.f);
     acc[k] = accb[k] = splat(0.f);
   }
-  uint32_t h[8], d[8], s[8];
-  float inv = 0.f, mean = 0.f;
-  auto fetch = [&](long row) {
-    inv = a.inv[row];
-    mean = a.mean[row];
-    if (on) {
-      ld_32b(hb + row * a.ldh, h);
-      ld_32b(db + row * a.lddy, d);
-      if (a.dh && a.dx) ld_32b(sb + row * a.lddh, s);
-    }
-  };
   auto pair = [](uint32_t w) {
     const T* e = reinterpret_cast<const T*>(&w);
     return make_float2(to_f(e[0]), to_f(e[1]));
   };
-#pragma unroll
-  for (int k = 0; k < 8; ++k) h[k] = d[k] = s[k] = 0u;
-  const long step = gridDim.x;
-  long row = blockIdx.x;  // the grid has no more blocks than there are rows
-  fetch(row);
-  int par = 0;
+  auto take = [&](uint32_t from, uint32_t (&w)[8]) {
+    const uint32_t at = from + c * 2;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(at) : "memory");
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7]) : "r"(at + half * 2) : "memory");
+  };
+  float inv = a.inv[row], mean = a.mean[row];
+  int par = 0, slot = 0;
+  uint32_t phase = 0;
+  bool ok = true;
   for (; row < a.rows; row += step, par ^= 1) {
     const float2 iv = splat(inv), mu = splat(-mean);
-    float2 dot = splat(0.f), sum = splat(0.f);
-    uint32_t hc[8], dc[8], sc[8];
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      hc[k] = h[k];
-      dc[k] = d[k];
-      sc[k] = s[k];
+    if (row + step < a.rows) {
+      inv = a.inv[row + step];
+      mean = a.mean[row + step];
+    } else {
+      pdl_release();
     }
-    if (row + step < a.rows) fetch(row + step);
-    else pdl_release();
+    uint32_t h[8], d[8], s[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) h[k] = d[k] = s[k] = 0u;
+    ok = ok && wait(&full[slot], phase, a.err, kSiteLayerBwd);  // (one that ran out leaves garbage and its mark)
+    if (on) {
+      const uint32_t from = base + slot * place;
+      take(from, h);
+      take(from + bytes, d);
+      if (skip) take(from + 2 * bytes, s);
+    }
+    float2 dot = splat(0.f), sum = splat(0.f);
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      const float2 n = __fmul2_rn(__fadd2_rn(pair(hc[k]), mu), iv), y = pair(dc[k]), w = __fmul2_rn(y, g[k]);
+      const float2 n = __fmul2_rn(__fadd2_rn(pair(h[k]), mu), iv), y = pair(d[k]), w = __fmul2_rn(y, g[k]);
       acc[k] = __ffma2_rn(y, n, acc[k]);
       accb[k] = __fadd2_rn(accb[k], y);
       dot = __ffma2_rn(w, n, dot);
       sum = __fadd2_rn(sum, w);
     }
-    if (!a.dx) continue;
     // past the row's end dy is zero, so it counts in no sum
     float2 both = make_float2(warp_sum(dot.x + dot.y), warp_sum(sum.x + sum.y));
     if ((t & 31) == 0) part[par][t >> 5] = both;
-    __syncthreads();  // once a row: the next one writes the other half of part
+    __syncthreads();  // once a row: the next one writes the other half of part; this row's place is free
+    if (t == 0) request(row + kRing * step, slot);
+    if (++slot == kRing) {
+      slot = 0;
+      phase ^= 1;
+    }
+    if (!a.dx) continue;
     both = splat(0.f);
 #pragma unroll 8
     for (int w = 0; w < nw; ++w) both = __fadd2_rn(both, part[par][w]);
@@ -311,39 +342,60 @@ __global__ void __launch_bounds__(MT, MB) layer_bwd_kernel(const NormBwdArgs a) 
       uint32_t o[8];
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        const float2 n = __fmul2_rn(__fadd2_rn(pair(hc[k]), mu), iv);
-        float2 v = __ffma2_rn(n, md, __ffma2_rn(pair(dc[k]), g[k], ms));
-        v = a.dh ? __ffma2_rn(v, iv, pair(sc[k])) : __fmul2_rn(v, iv);
+        const float2 n = __fmul2_rn(__fadd2_rn(pair(h[k]), mu), iv);
+        float2 v = __ffma2_rn(n, md, __ffma2_rn(pair(d[k]), g[k], ms));
+        v = a.dh ? __ffma2_rn(v, iv, pair(s[k])) : __fmul2_rn(v, iv);
         T* e = reinterpret_cast<T*>(&o[k]);
         e[0] = from_f<T>(v.x);
         e[1] = from_f<T>(v.y);
       }
-      st_32b(xb + row * a.lddx, o);
+      T* x = static_cast<T*>(a.dx) + row * a.lddx + c;
+      *reinterpret_cast<uint4*>(x) = make_uint4(o[0], o[1], o[2], o[3]);
+      *reinterpret_cast<uint4*>(x + half) = make_uint4(o[4], o[5], o[6], o[7]);
     }
   }
+  if (!ok && t == 0) {  // gave up: the copies in flight land before the block goes; row n of this block in place n % kRing
+    const long n = (a.rows - blockIdx.x + step - 1) / step;
+    for (long i = n > kRing ? n - kRing : 0; i < n; ++i)
+      (void)wait(&full[i % kRing], static_cast<uint32_t>(i / kRing) & 1u, a.err, kSiteLayerBwd);
+  }
   if (!on) return;
-  auto partials = [&](float* base, const float2 (&v)[V / 2]) {
-    if (!base) return;
-    float4* p = reinterpret_cast<float4*>(base + static_cast<long>(blockIdx.x) * a.cols + c);
+  auto partials = [&](float* sums, const float2 (&v)[8]) {
+    if (!sums) return;
+    float* p = sums + static_cast<long>(blockIdx.x) * a.cols + c;
 #pragma unroll
-    for (int k = 0; k < V / 4; ++k) p[k] = make_float4(v[2 * k].x, v[2 * k].y, v[2 * k + 1].x, v[2 * k + 1].y);
+    for (int k = 0; k < 4; ++k) {
+      float* q = k < 2 ? p + 4 * k : p + half + 4 * (k - 2);
+      *reinterpret_cast<float4*>(q) = make_float4(v[2 * k].x, v[2 * k].y, v[2 * k + 1].x, v[2 * k + 1].y);
+    }
   };
   partials(a.part, acc);
   partials(a.partb, accb);
 }
+template <typename T, int MT, int MB>
+cudaError_t layer_bwd_launch(const NormBwdArgs& a, int threads, int grid, cudaStream_t st) {
+  const auto kernel = layer_bwd_kernel<T, MT, MB>;
+  static std::atomic<uint64_t> done{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (!(done.load(std::memory_order_relaxed) >> dev & 1)) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRing * 3 * 16 * 2 * MT);
+    if (e != cudaSuccess) return e;
+    done.fetch_or(uint64_t(1) << dev);
+  }
+  return launch_k(kernel, dim3(grid), dim3(threads), static_cast<size_t>(kRing) * 3 * 2 * a.cols, st, 1, a);
+}
 template <typename T>
 cudaError_t layer_bwd(const NormBwdArgs& a, int sms, int* grid, cudaStream_t st) {
-  constexpr int V = 16;
   if constexpr (sizeof(T) == 2) {
-    auto ok = [&](const void* p, long ld) { return !p || vec_ok(p, ld, 2, V); };
-    const int threads = (a.cols / V + 31) / 32 * 32;
-    // between 256 and 448 threads an SM holds one block that leaves it idle (8192 x 5120 84 us, 73 in norm_bwd_kernel)
-    if (a.cols % V == 0 && threads >= 64 && (threads <= 256 || (threads > 448 && threads <= 512)) && ok(a.h, a.ldh) && ok(a.dy, a.lddy) && ok(a.dx, a.lddx) &&
+    auto ok = [&](const void* p, long ld) { return !p || vec_ok(p, ld, 2, 8); };
+    const int threads = (a.cols / 16 + 31) / 32 * 32;
+    if (a.cols % 16 == 0 && threads >= 64 && threads <= 512 && ok(a.h, a.ldh) && ok(a.dy, a.lddy) && ok(a.dx, a.lddx) &&
         ok(a.dh, a.lddh)) {
       // no more blocks than the workspace has rows for
       *grid = static_cast<int>(std::min<long>(norm_bwd_blocks(a.rows, a.cols, sms), static_cast<long>(sms) * (512 / threads)));
-      if (threads <= 256) return launch_k(layer_bwd_kernel<T, 256, 2>, dim3(*grid), dim3(threads), 0, st, 1, a);
-      return launch_k(layer_bwd_kernel<T, 512, 1>, dim3(*grid), dim3(threads), 0, st, 1, a);
+      return threads <= 256 ? layer_bwd_launch<T, 256, 2>(a, threads, *grid, st) : layer_bwd_launch<T, 512, 1>(a, threads, *grid, st);
     }
   }
   return norm_bwd_vec<T, true>(a, sms, grid, st);
@@ -451,6 +503,7 @@ int conv2d_layer_norm_bwd(int64_t rows, int32_t cols, const conv2d_mat* h, const
   a.gamma = gamma;
   a.mean = mean;
   a.inv = inv_std;
+  a.err = dev->err;
   a.part = dgamma ? static_cast<float*>(ws) : nullptr;
   a.partb = dbeta ? static_cast<float*>(ws) + need / 8 : nullptr;
   a.rows = rows;

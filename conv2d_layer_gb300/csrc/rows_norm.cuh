@@ -527,6 +527,7 @@ struct NormBwdArgs {
   long ldh, lddy, lddh, lddx;
   long rows;
   int cols;
+  int* err;  // layer norm: device error word for bounded waits
 };
 
 // Blocks that an SM holds and is given, by the threads of a row (32: blocks of 256): about 512 threads of up to 128
