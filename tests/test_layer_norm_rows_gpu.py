@@ -169,7 +169,10 @@ def test_layer_norm_in_place_and_special_rows():
                                                          (37, 1032, HF, 8), (37, 2056, BF, 0), (37, 2568, BF, 8),
                                                          (37, 6152, BF, 0), (37, 516, FP, 0), (400, 1000, FP, 0),
                                                          (37, 1536, FP, 0), (37, 2052, FP, 0), (37, 4100, FP, 0),
-                                                         (40, 12001, BF, 0), (5, 4097, FP, 0)])
+                                                         (40, 12001, BF, 0), (5, 4097, FP, 0),
+                                                         (700, 1021, BF, 0), (1, 513, HF, 0), (2, 514, BF, 0), (37, 777, HF, 3),
+                                                         (400, 528, BF, 3), (333, 1000, BF, 0), (3, 8191, BF, 0), (2, 8192, HF, 1),
+                                                         (1500, 2047, HF, 1), (310, 4095, BF, 0)])
 @pytest.mark.parametrize("skip", [False, True])
 def test_layer_norm_bwd(rows, cols, dtype, pad, skip):
     h, gamma, dy = (normal(1, rows, cols) + 0.5).to(dtype), normal(2, cols), normal(3, rows, cols, dtype=dtype)

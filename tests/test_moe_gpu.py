@@ -105,6 +105,7 @@ CASES = [
     (33, 512, 136, 16, 4, BF, False, "gelu", True, True, True, False),
     (64, 1152, 640, 12, 2, BF, True, "silu", False, True, True, False),
     (64, 200, 96, 40, 8, HF, True, "relu", True, False, False, False),
+    (64, 128, 64, 256, 16, BF, True, "silu", True, True, False, False),
     (1, 128, 128, 1, 1, BF, False, "identity", False, True, False, True),
     (1, 2048, 1024, 16, 4, BF, True, "silu", False, True, True, True),
     (7, 384, 256, 6, 2, HF, True, "silu", True, False, True, True),
