@@ -155,25 +155,6 @@ __device__ __forceinline__ uint32_t idesc_block(int M, int N, bool a_mn, bool b_
   return ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) | (static_cast<uint32_t>(N >> 3) << 17) | (1u << 23) |
          (static_cast<uint32_t>(M >> 4) << 24);
 }
-// wait() for a phase that another CTA of the cluster arrives on after writing its own shared memory.
-__device__ __forceinline__ bool wait_cluster(uint64_t* bar, uint32_t parity, int* err, int site) {
-  const uint64_t t0 = globaltimer();
-#pragma unroll 1
-  for (uint32_t i = 0;; ++i) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, "
-        "p;\n\t}"
-        : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(parity)
-        : "memory");
-    if (ok) return true;
-    if ((i & 1023u) == 1023u && globaltimer() - t0 > kWaitLimitNs) {
-      atomicCAS(err, 0, site);
-      return false;
-    }
-  }
-}
 
 // 3-D tiled store of a box from shared memory; part of the thread's current bulk group.
 __device__ __forceinline__ void tma_store_3d(const CUtensorMap* m, uint32_t src, int c0, int c1, int c2) {

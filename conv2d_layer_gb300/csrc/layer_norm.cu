@@ -241,7 +241,9 @@ cudaError_t layer_any(const NormArgs& a, int sms, cudaStream_t st) {
 // the sums of dgamma and dbeta leave no registers for that (512 threads an SM of 126 each, with one row ahead in registers:
 // 8192 x 4096 bf16 54 us, 48 KB in flight). A thread has eight features in each half of the row, so that its 16-byte
 // accesses meet no bank twice. Bound by memory: 8192 x 4096 bf16 with dh moves 268 MB in 44 us, 0.90 of the copy rate, then
-// the column sums in 5.
+// the column sums in 5. Rows of more than 8,192 features are shared by a cluster of two CTAs, or four (up to 32,768): a
+// thread has no registers for more than 16 features, and norm_bwd_kernel leaves the row in L2 in between. 2048 x 16384 bf16
+// 113 us there, 55 here; 3000 x 10240 129 and 60; 1024 x 32768 560 and 66; 32 x 16384 28 and 10.
 constexpr int kRing = 4;
 constexpr int kSiteLayerBwd = 20;
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
@@ -249,39 +251,54 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
                "r"(bytes), "r"(smem_u32(bar))
                : "memory");
 }
-template <typename T, int MT, int MB>
+__device__ __forceinline__ void send_pair(uint32_t to, float2 v, uint32_t bar) {  // both in one CTA of the cluster
+  asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v2.b32 [%0], {%1, %2}, [%3];" ::"r"(to),
+               "r"(__float_as_uint(v.x)), "r"(__float_as_uint(v.y)), "r"(bar)
+               : "memory");
+}
+// CL: CTAs of a cluster, which share a row.
+template <typename T, int MT, int MB, int CL>
 __global__ void __launch_bounds__(MT, MB) layer_bwd_kernel(const NormBwdArgs a) {
   extern __shared__ uint4 ring[];  // [kRing][h, dy, dh][cols]
-  __shared__ uint64_t full[kRing];
-  __shared__ float2 part[2][MT / 32];
+  __shared__ uint64_t full[kRing], met[2];
+  __shared__ float2 part[2][CL * MT / 32];
   const int t = static_cast<int>(threadIdx.x), nw = static_cast<int>(blockDim.x) >> 5;
-  const int half = a.cols / 2, c = t * 8;
+  const int rank = CL > 1 ? static_cast<int>(cluster_ctarank()) : 0, cols = a.cols / CL, from_col = rank * cols;
+  const int half = cols / 2, c = t * 8;
   const bool on = c < half, skip = a.dh && a.dx;
   const float over = 1.f / static_cast<float>(a.cols);
-  const uint32_t bytes = static_cast<uint32_t>(a.cols) * 2u, place = 3u * bytes, base = smem_u32(ring);
+  const uint32_t bytes = static_cast<uint32_t>(cols) * 2u, place = 3u * bytes, base = smem_u32(ring);
+  const uint32_t sent = static_cast<uint32_t>(CL * nw) * 8u;  // bytes of all warps' sums of a row
   if (t == 0) {
     for (int i = 0; i < kRing; ++i) mbar_init(&full[i], 1);
+    if (CL > 1)
+      for (int i = 0; i < 2; ++i) mbar_init(&met[i], 1);
     fence_mbar_init();
+    if (CL > 1)
+      for (int i = 0; i < 2; ++i) mbar_arrive_expect_tx(&met[i], sent);
   }
   pdl_entry();
-  __syncthreads();
-  const long step = gridDim.x;
+  if (CL > 1)
+    cluster_sync();
+  else
+    __syncthreads();
+  const long step = gridDim.x / CL, first = blockIdx.x / CL;
   auto request = [&](long row, int i) {  // one thread
     if (row >= a.rows) return;
     mbar_arrive_expect_tx(&full[i], (skip ? 3u : 2u) * bytes);
     const uint32_t to = base + i * place;
-    bulk_load(to, static_cast<const T*>(a.h) + row * a.ldh, bytes, &full[i]);
-    bulk_load(to + bytes, static_cast<const T*>(a.dy) + row * a.lddy, bytes, &full[i]);
-    if (skip) bulk_load(to + 2 * bytes, static_cast<const T*>(a.dh) + row * a.lddh, bytes, &full[i]);
+    bulk_load(to, static_cast<const T*>(a.h) + row * a.ldh + from_col, bytes, &full[i]);
+    bulk_load(to + bytes, static_cast<const T*>(a.dy) + row * a.lddy + from_col, bytes, &full[i]);
+    if (skip) bulk_load(to + 2 * bytes, static_cast<const T*>(a.dh) + row * a.lddh + from_col, bytes, &full[i]);
   };
-  long row = blockIdx.x;  // the grid has no more blocks than there are rows
+  long row = first;  // the grid has no more blocks (or clusters) than there are rows
   if (t == 0)
     for (int i = 0; i < kRing; ++i) request(row + i * step, i);
 
   float2 g[8], acc[8], accb[8];
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
-    g[k] = on ? *reinterpret_cast<const float2*>(a.gamma + (k < 4 ? c : half + c - 8) + 2 * k) : splat(0.f);
+    g[k] = on ? *reinterpret_cast<const float2*>(a.gamma + from_col + (k < 4 ? c : half + c - 8) + 2 * k) : splat(0.f);
     acc[k] = accb[k] = splat(0.f);
   }
   auto pair = [](uint32_t w) {
@@ -295,7 +312,7 @@ __global__ void __launch_bounds__(MT, MB) layer_bwd_kernel(const NormBwdArgs a) 
   };
   float inv = a.inv[row], mean = a.mean[row];
   int par = 0, slot = 0;
-  uint32_t phase = 0;
+  uint32_t phase = 0, meet = 0;
   bool ok = true;
   for (; row < a.rows; row += step, par ^= 1) {
     const float2 iv = splat(inv), mu = splat(-mean);
@@ -326,8 +343,20 @@ __global__ void __launch_bounds__(MT, MB) layer_bwd_kernel(const NormBwdArgs a) 
     }
     // past the row's end dy is zero, so it counts in no sum
     float2 both = make_float2(warp_sum(dot.x + dot.y), warp_sum(sum.x + sum.y));
-    if ((t & 31) == 0) part[par][t >> 5] = both;
-    __syncthreads();  // once a row: the next one writes the other half of part; this row's place is free
+    // Once a row all warps meet: the next row writes the other half of part, this row's place is free. In a cluster each
+    // warp sends its sums to every CTA, whose barrier counts the bytes.
+    if constexpr (CL > 1) {
+      const int lane = t & 31;
+      if (lane < CL)
+        send_pair(mapa_shared(smem_u32(&part[par][rank * nw + (t >> 5)]), static_cast<uint32_t>(lane)), both,
+                  mapa_shared(smem_u32(&met[par]), static_cast<uint32_t>(lane)));
+      ok = ok && wait_cluster(&met[par], meet, a.err, kSiteLayerBwd);
+      if (t == 0) mbar_arrive_expect_tx(&met[par], sent);  // for the row after next: none sends its sums before this warp
+      if (par) meet ^= 1;
+    } else {
+      if ((t & 31) == 0) part[par][t >> 5] = both;
+      __syncthreads();
+    }
     if (t == 0) request(row + kRing * step, slot);
     if (++slot == kRing) {
       slot = 0;
@@ -336,7 +365,7 @@ __global__ void __launch_bounds__(MT, MB) layer_bwd_kernel(const NormBwdArgs a) 
     if (!a.dx) continue;
     both = splat(0.f);
 #pragma unroll 8
-    for (int w = 0; w < nw; ++w) both = __fadd2_rn(both, part[par][w]);
+    for (int w = 0; w < CL * nw; ++w) both = __fadd2_rn(both, part[par][w]);
     const float2 md = splat(-both.x * over), ms = splat(-both.y * over);
     if (on) {
       uint32_t o[8];
@@ -349,20 +378,21 @@ __global__ void __launch_bounds__(MT, MB) layer_bwd_kernel(const NormBwdArgs a) 
         e[0] = from_f<T>(v.x);
         e[1] = from_f<T>(v.y);
       }
-      T* x = static_cast<T*>(a.dx) + row * a.lddx + c;
+      T* x = static_cast<T*>(a.dx) + row * a.lddx + from_col + c;
       *reinterpret_cast<uint4*>(x) = make_uint4(o[0], o[1], o[2], o[3]);
       *reinterpret_cast<uint4*>(x + half) = make_uint4(o[4], o[5], o[6], o[7]);
     }
   }
   if (!ok && t == 0) {  // gave up: the copies in flight land before the block goes; row n of this block in place n % kRing
-    const long n = (a.rows - blockIdx.x + step - 1) / step;
+    const long n = (a.rows - first + step - 1) / step;
     for (long i = n > kRing ? n - kRing : 0; i < n; ++i)
       (void)wait(&full[i % kRing], static_cast<uint32_t>(i / kRing) & 1u, a.err, kSiteLayerBwd);
   }
+  if (CL > 1) cluster_sync();  // (after a wait that ran out: no CTA goes while another may still send to it)
   if (!on) return;
   auto partials = [&](float* sums, const float2 (&v)[8]) {
     if (!sums) return;
-    float* p = sums + static_cast<long>(blockIdx.x) * a.cols + c;
+    float* p = sums + first * a.cols + from_col + c;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       float* q = k < 2 ? p + 4 * k : p + half + 4 * (k - 2);
@@ -372,30 +402,58 @@ __global__ void __launch_bounds__(MT, MB) layer_bwd_kernel(const NormBwdArgs a) 
   partials(a.part, acc);
   partials(a.partb, accb);
 }
-template <typename T, int MT, int MB>
-cudaError_t layer_bwd_launch(const NormBwdArgs& a, int threads, int grid, cudaStream_t st) {
-  const auto kernel = layer_bwd_kernel<T, MT, MB>;
-  static std::atomic<uint64_t> done{0};
+// Blocks or clusters that are resident together: a later one would begin when the others end, with as many rows. CTAs of a
+// cluster come from one GPC, so the device says how many clusters fit (36 of four here, not 38: 1024 x 32768 66 us, with 38
+// 111).
+template <typename T, int MT, int MB, int CL>
+cudaError_t layer_bwd_launch(const NormBwdArgs& a, int threads, long blocks, int* grid, cudaStream_t st) {
+  const auto kernel = layer_bwd_kernel<T, MT, MB, CL>;
+  static std::atomic<int> fit[64];  // by device; 0: not asked yet
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  if (!(done.load(std::memory_order_relaxed) >> dev & 1)) {
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRing * 3 * 16 * 2 * MT);
+  int most = dev < 64 ? fit[dev].load(std::memory_order_relaxed) : 0;
+  if (!most) {
+    constexpr int bytes = kRing * 3 * 16 * 2 * MT;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
-    done.fetch_or(uint64_t(1) << dev);
+    most = 1 << 30;
+    if (CL > 1) {
+      cudaLaunchAttribute at = {};
+      at.id = cudaLaunchAttributeClusterDimension;
+      at.val.clusterDim.x = CL;
+      at.val.clusterDim.y = at.val.clusterDim.z = 1;
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3(CL);
+      cfg.blockDim = dim3(MT);
+      cfg.dynamicSmemBytes = bytes;
+      cfg.attrs = &at;
+      cfg.numAttrs = 1;
+      e = cudaOccupancyMaxActiveClusters(&most, kernel, &cfg);
+      if (e != cudaSuccess) return e;
+      if (most < 1) return cudaErrorInvalidConfiguration;
+    }
+    if (dev < 64) fit[dev].store(most, std::memory_order_relaxed);
   }
-  return launch_k(kernel, dim3(grid), dim3(threads), static_cast<size_t>(kRing) * 3 * 2 * a.cols, st, 1, a);
+  *grid = static_cast<int>(std::min<long>(blocks, most));
+  return launch_k(kernel, dim3(*grid * CL), dim3(threads), static_cast<size_t>(kRing) * 3 * 2 * (a.cols / CL), st, CL, a);
 }
+// grid: rows of partial sums.
 template <typename T>
 cudaError_t layer_bwd(const NormBwdArgs& a, int sms, int* grid, cudaStream_t st) {
   if constexpr (sizeof(T) == 2) {
     auto ok = [&](const void* p, long ld) { return !p || vec_ok(p, ld, 2, 8); };
-    const int threads = (a.cols / 16 + 31) / 32 * 32;
-    if (a.cols % 16 == 0 && threads >= 64 && threads <= 512 && ok(a.h, a.ldh) && ok(a.dy, a.lddy) && ok(a.dx, a.lddx) &&
-        ok(a.dh, a.lddh)) {
+    const int cl = a.cols <= 16 * 512 ? 1 : a.cols <= 2 * 16 * 512 ? 2 : 4;
+    const int threads = (a.cols / (16 * cl) + 31) / 32 * 32;
+    if (a.cols % (16 * cl) == 0 && threads >= 64 && threads <= 512 && ok(a.h, a.ldh) && ok(a.dy, a.lddy) &&
+        ok(a.dx, a.lddx) && ok(a.dh, a.lddh)) {
       // no more blocks than the workspace has rows for
-      *grid = static_cast<int>(std::min<long>(norm_bwd_blocks(a.rows, a.cols, sms), static_cast<long>(sms) * (512 / threads)));
-      return threads <= 256 ? layer_bwd_launch<T, 256, 2>(a, threads, *grid, st) : layer_bwd_launch<T, 512, 1>(a, threads, *grid, st);
+      const long blocks = std::min<long>(norm_bwd_blocks(a.rows, a.cols, sms),
+                                         static_cast<long>(sms) * (cl > 1 ? 1 : 512 / threads));
+      if (cl == 4) return layer_bwd_launch<T, 512, 1, 4>(a, threads, blocks, grid, st);
+      if (cl == 2) return layer_bwd_launch<T, 512, 1, 2>(a, threads, blocks, grid, st);
+      return threads <= 256 ? layer_bwd_launch<T, 256, 2, 1>(a, threads, blocks, grid, st)
+                            : layer_bwd_launch<T, 512, 1, 1>(a, threads, blocks, grid, st);
     }
   }
   return norm_bwd_vec<T, true>(a, sms, grid, st);

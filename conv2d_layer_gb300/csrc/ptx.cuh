@@ -66,6 +66,28 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, int* err, i
   }
 }
 
+// wait() for a phase that another CTA of the cluster arrives on after writing its own shared memory, or completes with what
+// it writes to this one's.
+__device__ __forceinline__ bool wait_cluster(uint64_t* bar, uint32_t parity, int* err, int site) {
+  uint64_t t0 = 0;
+#pragma unroll 1
+  for (uint32_t i = 0;; ++i) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, "
+        "p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    if (ok) return true;
+    if (i == 0) t0 = globaltimer();
+    if ((i & 1023u) == 1023u && globaltimer() - t0 > kWaitLimitNs) {
+      atomicCAS(err, 0, site);
+      return false;
+    }
+  }
+}
+
 // ---------------------------------------------------------------- named barriers
 __device__ __forceinline__ void named_bar_sync(int id, int nthreads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(nthreads) : "memory");

@@ -1,5 +1,9 @@
 """Layer norm of rows, and 8-bit matrices with a scale for 128 columns or a tile of 128 x 128, against their 64-bit
 forms, at the sizes, strides and values where they can go wrong."""
+import os
+import subprocess
+import sys
+
 import pytest
 import torch
 
@@ -172,7 +176,10 @@ def test_layer_norm_in_place_and_special_rows():
                                                          (40, 12001, BF, 0), (5, 4097, FP, 0),
                                                          (700, 1021, BF, 0), (1, 513, HF, 0), (2, 514, BF, 0), (37, 777, HF, 3),
                                                          (400, 528, BF, 3), (333, 1000, BF, 0), (3, 8191, BF, 0), (2, 8192, HF, 1),
-                                                         (1500, 2047, HF, 1), (310, 4095, BF, 0)])
+                                                         (1500, 2047, HF, 1), (310, 4095, BF, 0), (1, 8224, BF, 0),
+                                                         (76, 8224, HF, 8), (153, 10240, BF, 0), (700, 16384, HF, 0),
+                                                         (2, 16416, BF, 0), (39, 16448, BF, 0), (200, 32768, HF, 0),
+                                                         (7, 32832, BF, 0)])
 @pytest.mark.parametrize("skip", [False, True])
 def test_layer_norm_bwd(rows, cols, dtype, pad, skip):
     h, gamma, dy = (normal(1, rows, cols) + 0.5).to(dtype), normal(2, cols), normal(3, rows, cols, dtype=dtype)
@@ -210,6 +217,30 @@ def test_layer_norm_bwd(rows, cols, dtype, pad, skip):
         assert only[0] is None and only[2] is None and (pad or torch.equal(only[1], dg))
         only = ops.layer_norm_bwd(h, gamma, mean, inv, dy, need_dx=False, need_dgamma=False)
         assert only[:2] == (None, None) and (pad or torch.equal(only[2], db))
+
+
+FIRST_CALL_CAPTURED = """
+import torch
+from conv2d_layer_gb300 import ops
+g = torch.Generator(device="cuda").manual_seed(0)
+n = lambda *s: torch.randn(*s, generator=g, device="cuda")
+h, dy, gamma, mean, inv = n(5, COLS).half(), n(5, COLS).half(), n(COLS), n(5), n(5).abs()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    out = ops.layer_norm_bwd(h, gamma, mean, inv, dy, dh=dy)
+for t in out:
+    t.zero_()
+graph.replay()
+want = ops.layer_norm_bwd(h, gamma, mean, inv, dy, dh=dy)
+assert all(torch.equal(a, b) and bool(a.any()) for a, b in zip(out, want))
+"""
+
+
+@pytest.mark.parametrize("cols", [2048, 8224, 20480])
+def test_layer_norm_bwd_first_called_under_capture(cols):
+    """What a kernel's first launch asks the device for is asked during a capture as well."""
+    subprocess.run([sys.executable, "-c", FIRST_CALL_CAPTURED.replace("COLS", str(cols))], check=True, timeout=300,
+                   cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 
 
 def test_layer_norm_without_rows():
