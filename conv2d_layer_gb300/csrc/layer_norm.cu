@@ -402,12 +402,223 @@ __global__ void __launch_bounds__(MT, MB) layer_bwd_kernel(const NormBwdArgs a) 
   partials(a.part, acc);
   partials(a.partb, accb);
 }
+// The same for rows of any length and type, whose starts may lie anywhere: a block's rows are a multiple of eight apart, so
+// that they all start `m` features behind a 16-byte boundary, and a thread has the same features in each. A copy takes whole
+// 16 bytes; what is of the rows beside is set to zero where it is taken, and the end of the last row, behind which nothing
+// may be read, comes feature by feature, as do the ends of a row of dx go. Those ends hold the whole block up: 8192 x 4088
+// bf16, which has none, 67 us, 8192 x 4095 96 (floor 40).
+template <typename T, int MT, int MB, int CL>
+__global__ void __launch_bounds__(MT, MB) layer_bwd_shift_kernel(const NormBwdArgs a) {
+  constexpr int V = 16 / static_cast<int>(sizeof(T));  // features of a vector; a thread has two vectors, V pairs
+  extern __shared__ uint4 ring[];                      // [kRing][h, dy, dh][n]
+  __shared__ uint64_t full[kRing], met[2];
+  __shared__ float2 part[2][CL * MT / 32];
+  const int t = static_cast<int>(threadIdx.x), nw = static_cast<int>(blockDim.x) >> 5;
+  const int rank = CL > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+  const long step = gridDim.x / CL, first = blockIdx.x / CL;
+  const int m = static_cast<int>(first * a.ldh % V);
+  const int all = (m + a.cols + V - 1) / V, per = (all + CL - 1) / CL, v0 = rank * per, n = min(per, all - v0);
+  const int half = (n + 1) / 2, c0 = (v0 + t) * V - m, c1 = c0 + half * V;  // the first columns of the thread's vectors
+  const bool on0 = t < half, on1 = t < n - half, skip = a.dh && a.dx;
+  const bool whole0 = c0 >= 0 && c0 + V <= a.cols, whole1 = c1 + V <= a.cols;  // (no second vector is the row's first)
+  const bool edge = (on0 && !whole0) || (on1 && !whole1);
+  const float over = 1.f / static_cast<float>(a.cols);
+  const uint32_t bytes = static_cast<uint32_t>(n) * 16u, place = 3u * bytes, base = smem_u32(ring);
+  // of the last row: without the vector that its end cuts
+  const uint32_t bytes_end = bytes - (v0 + n == all && (m + a.cols) % V ? 16u : 0u);
+  const uint32_t sent = static_cast<uint32_t>(CL * nw) * 8u;
+  if (t == 0) {
+    for (int i = 0; i < kRing; ++i) mbar_init(&full[i], 1);
+    if (CL > 1)
+      for (int i = 0; i < 2; ++i) mbar_init(&met[i], 1);
+    fence_mbar_init();
+    if (CL > 1)
+      for (int i = 0; i < 2; ++i) mbar_arrive_expect_tx(&met[i], sent);
+  }
+  pdl_entry();
+  if (CL > 1)
+    cluster_sync();
+  else
+    __syncthreads();
+  auto request = [&](long row, int i) {  // one thread
+    if (row >= a.rows) return;
+    const uint32_t b = row == a.rows - 1 ? bytes_end : bytes;
+    mbar_arrive_expect_tx(&full[i], (skip ? 3u : 2u) * b);
+    if (b == 0) return;
+    const uint32_t to = base + i * place;
+    const long at = static_cast<long>(v0) * V - m;
+    bulk_load(to, static_cast<const T*>(a.h) + row * a.ldh + at, b, &full[i]);
+    bulk_load(to + bytes, static_cast<const T*>(a.dy) + row * a.lddy + at, b, &full[i]);
+    if (skip) bulk_load(to + 2 * bytes, static_cast<const T*>(a.dh) + row * a.lddh + at, b, &full[i]);
+  };
+  long row = first;
+  if (t == 0)
+    for (int i = 0; i < kRing; ++i) request(row + i * step, i);
+
+  auto column = [&](int e) { return e < V ? c0 + e : c1 + e - V; };  // of the thread's feature e
+  auto there = [&](int e) { return (e < V ? on0 : on1) && column(e) >= 0 && column(e) < a.cols; };
+  uint32_t valid = 0;  // the thread's features that are there
+#pragma unroll
+  for (int e = 0; e < 2 * V; ++e) valid |= there(e) ? 1u << e : 0u;
+  float2 g[V], acc[V], accb[V];
+#pragma unroll
+  for (int k = 0; k < V; ++k) {
+    g[k] = make_float2(there(2 * k) ? a.gamma[column(2 * k)] : 0.f, there(2 * k + 1) ? a.gamma[column(2 * k + 1)] : 0.f);
+    acc[k] = accb[k] = splat(0.f);
+  }
+  auto pair = [](const uint32_t (&w)[8], int k) {
+    if constexpr (sizeof(T) == 2) {
+      const T* e = reinterpret_cast<const T*>(&w[k]);
+      return make_float2(to_f(e[0]), to_f(e[1]));
+    } else {
+      return make_float2(__uint_as_float(w[2 * k]), __uint_as_float(w[2 * k + 1]));
+    }
+  };
+  auto take = [&](uint32_t from, uint32_t (&w)[8]) {
+    const uint32_t at = from + t * 16;
+    if (on0) asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(at) : "memory");
+    if (on1) asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7]) : "r"(at + half * 16) : "memory");
+  };
+  // Of a vector at an end of the row: only the features that are there.
+  auto mask = [&](uint32_t* w, uint32_t there) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if constexpr (sizeof(T) == 2)
+        w[k] &= (there >> 2 * k & 1u ? 0xffffu : 0u) | (there >> (2 * k + 1) & 1u ? 0xffff0000u : 0u);
+      else
+        w[k] = there >> k & 1u ? w[k] : 0u;
+    }
+  };
+  // The end of the last row (at), which no copy brought: in place of what was taken.
+  auto last = [&](const T* at, uint32_t (&w)[8]) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      if ((k < 4 ? c0 : c1) + V <= a.cols) continue;
+      if constexpr (sizeof(T) == 2) {
+        const uint16_t* e = reinterpret_cast<const uint16_t*>(at) + column(2 * k);
+        w[k] = (valid >> 2 * k & 1u ? e[0] : 0u) | (valid >> (2 * k + 1) & 1u ? static_cast<uint32_t>(e[1]) << 16 : 0u);
+      } else {
+        w[k] = valid >> k & 1u ? reinterpret_cast<const uint32_t*>(at)[column(k)] : 0u;
+      }
+    }
+  };
+  float inv = a.inv[row], mean = a.mean[row];
+  int par = 0, slot = 0;
+  uint32_t phase = 0, meet = 0;
+  bool ok = true;
+  for (; row < a.rows; row += step, par ^= 1) {
+    const float2 iv = splat(inv), mu = splat(-mean);
+    if (row + step < a.rows) {
+      inv = a.inv[row + step];
+      mean = a.mean[row + step];
+    } else {
+      pdl_release();
+    }
+    uint32_t h[8], d[8], s[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) h[k] = d[k] = s[k] = 0u;
+    ok = ok && wait(&full[slot], phase, a.err, kSiteLayerBwd);
+    const uint32_t from = base + slot * place;
+    take(from, h);
+    take(from + bytes, d);
+    if (skip) take(from + 2 * bytes, s);
+    if (edge) {
+      if (row == a.rows - 1) {
+        last(static_cast<const T*>(a.h) + row * a.ldh, h);
+        last(static_cast<const T*>(a.dy) + row * a.lddy, d);
+        if (skip) last(static_cast<const T*>(a.dh) + row * a.lddh, s);
+      }
+      if (on0 && !whole0) {
+        mask(h, valid);
+        mask(d, valid);
+        mask(s, valid);
+      }
+      if (on1 && !whole1) {
+        mask(h + 4, valid >> V);
+        mask(d + 4, valid >> V);
+        mask(s + 4, valid >> V);
+      }
+    }
+    float2 dot = splat(0.f), sum = splat(0.f);
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+      const float2 x = __fmul2_rn(__fadd2_rn(pair(h, k), mu), iv), y = pair(d, k), w = __fmul2_rn(y, g[k]);
+      acc[k] = __ffma2_rn(y, x, acc[k]);
+      accb[k] = __fadd2_rn(accb[k], y);
+      dot = __ffma2_rn(w, x, dot);
+      sum = __fadd2_rn(sum, w);
+    }
+    float2 both = make_float2(warp_sum(dot.x + dot.y), warp_sum(sum.x + sum.y));
+    if constexpr (CL > 1) {
+      const int lane = t & 31;
+      if (lane < CL)
+        send_pair(mapa_shared(smem_u32(&part[par][rank * nw + (t >> 5)]), static_cast<uint32_t>(lane)), both,
+                  mapa_shared(smem_u32(&met[par]), static_cast<uint32_t>(lane)));
+      ok = ok && wait_cluster(&met[par], meet, a.err, kSiteLayerBwd);
+      if (t == 0) mbar_arrive_expect_tx(&met[par], sent);
+      if (par) meet ^= 1;
+    } else {
+      if ((t & 31) == 0) part[par][t >> 5] = both;
+      __syncthreads();
+    }
+    if (t == 0) request(row + kRing * step, slot);
+    if (++slot == kRing) {
+      slot = 0;
+      phase ^= 1;
+    }
+    if (!a.dx) continue;
+    both = splat(0.f);
+#pragma unroll 8
+    for (int w = 0; w < CL * nw; ++w) both = __fadd2_rn(both, part[par][w]);
+    const float2 md = splat(-both.x * over), ms = splat(-both.y * over);
+    uint32_t o[8];
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+      const float2 x = __fmul2_rn(__fadd2_rn(pair(h, k), mu), iv);
+      float2 v = __ffma2_rn(x, md, __ffma2_rn(pair(d, k), g[k], ms));
+      v = a.dh ? __ffma2_rn(v, iv, pair(s, k)) : __fmul2_rn(v, iv);
+      T* e = reinterpret_cast<T*>(o) + 2 * k;
+      e[0] = from_f<T>(v.x);
+      e[1] = from_f<T>(v.y);
+    }
+    T* x = static_cast<T*>(a.dx) + row * a.lddx;
+    auto put = [&](int col, bool whole, uint32_t there, const uint32_t* w) {
+      if (whole) {
+        *reinterpret_cast<uint4*>(x + col) = make_uint4(w[0], w[1], w[2], w[3]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < V; ++e)
+          if (there >> e & 1u) x[col + e] = reinterpret_cast<const T*>(w)[e];
+      }
+    };
+    if (on0) put(c0, whole0, valid, o);
+    if (on1) put(c1, whole1, valid >> V, o + 4);
+  }
+  if (!ok && t == 0) {  // gave up: as above
+    const long mine = (a.rows - first + step - 1) / step;
+    for (long i = mine > kRing ? mine - kRing : 0; i < mine; ++i)
+      (void)wait(&full[i % kRing], static_cast<uint32_t>(i / kRing) & 1u, a.err, kSiteLayerBwd);
+  }
+  if (CL > 1) cluster_sync();
+  auto partials = [&](float* sums, const float2 (&v)[V]) {
+    if (!sums) return;
+    float* p = sums + first * a.cols;
+#pragma unroll
+    for (int e = 0; e < 2 * V; ++e)
+      if (there(e)) p[column(e)] = e % 2 ? v[e / 2].y : v[e / 2].x;
+  };
+  partials(a.part, acc);
+  partials(a.partb, accb);
+}
 // Blocks or clusters that are resident together: a later one would begin when the others end, with as many rows. CTAs of a
 // cluster come from one GPC, so the device says how many clusters fit (36 of four here, not 38: 1024 x 32768 66 us, with 38
 // 111).
-template <typename T, int MT, int MB, int CL>
-cudaError_t layer_bwd_launch(const NormBwdArgs& a, int threads, long blocks, int* grid, cudaStream_t st) {
-  const auto kernel = layer_bwd_kernel<T, MT, MB, CL>;
+template <typename T, int MT, int MB, int CL, bool SHIFT>
+cudaError_t layer_bwd_launch(const NormBwdArgs& a, int threads, int vectors, long blocks, int* grid, cudaStream_t st) {
+  const auto kernel = [] {
+    if constexpr (SHIFT) return layer_bwd_shift_kernel<T, MT, MB, CL>;
+    else return layer_bwd_kernel<T, MT, MB, CL>;
+  }();
   static std::atomic<int> fit[64];  // by device; 0: not asked yet
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -435,27 +646,45 @@ cudaError_t layer_bwd_launch(const NormBwdArgs& a, int threads, long blocks, int
     }
     if (dev < 64) fit[dev].store(most, std::memory_order_relaxed);
   }
-  *grid = static_cast<int>(std::min<long>(blocks, most));
-  return launch_k(kernel, dim3(*grid * CL), dim3(threads), static_cast<size_t>(kRing) * 3 * 2 * (a.cols / CL), st, CL, a);
+  blocks = std::min<long>(blocks, most);
+  if (SHIFT && blocks < a.rows) blocks = std::max<long>(8, blocks / 8 * 8);  // rows of a block begin alike
+  *grid = static_cast<int>(blocks);
+  return launch_k(kernel, dim3(*grid * CL), dim3(threads), static_cast<size_t>(kRing) * 3 * 16 * vectors, st, CL, a);
+}
+template <typename T, bool SHIFT>
+cudaError_t layer_bwd_ring(const NormBwdArgs& a, int cl, int threads, int vectors, int sms, int* grid, cudaStream_t st) {
+  // no more blocks than the workspace has rows for
+  const long blocks = std::min<long>(norm_bwd_blocks(a.rows, a.cols, sms),
+                                     static_cast<long>(sms) * (cl > 1 ? 1 : 512 / threads));
+  if (cl == 4) return layer_bwd_launch<T, 512, 1, 4, SHIFT>(a, threads, vectors, blocks, grid, st);
+  if (cl == 2) return layer_bwd_launch<T, 512, 1, 2, SHIFT>(a, threads, vectors, blocks, grid, st);
+  return threads <= 256 ? layer_bwd_launch<T, 256, 2, 1, SHIFT>(a, threads, vectors, blocks, grid, st)
+                        : layer_bwd_launch<T, 512, 1, 1, SHIFT>(a, threads, vectors, blocks, grid, st);
 }
 // grid: rows of partial sums.
 template <typename T>
 cudaError_t layer_bwd(const NormBwdArgs& a, int sms, int* grid, cudaStream_t st) {
-  if constexpr (sizeof(T) == 2) {
-    auto ok = [&](const void* p, long ld) { return !p || vec_ok(p, ld, 2, 8); };
+  constexpr int es = sizeof(T), V = 16 / es;
+  auto whole = [&](const void* p, long ld) { return !p || vec_ok(p, ld, es, V); };
+  auto alike = [&](const void* p, long ld) { return !p || ld % V == a.ldh % V; };
+  const bool even = whole(a.h, a.ldh) && whole(a.dy, a.lddy) && whole(a.dx, a.lddx) && whole(a.dh, a.lddh);
+  if constexpr (es == 2) {
     const int cl = a.cols <= 16 * 512 ? 1 : a.cols <= 2 * 16 * 512 ? 2 : 4;
     const int threads = (a.cols / (16 * cl) + 31) / 32 * 32;
-    if (a.cols % (16 * cl) == 0 && threads >= 64 && threads <= 512 && ok(a.h, a.ldh) && ok(a.dy, a.lddy) &&
-        ok(a.dx, a.lddx) && ok(a.dh, a.lddh)) {
-      // no more blocks than the workspace has rows for
-      const long blocks = std::min<long>(norm_bwd_blocks(a.rows, a.cols, sms),
-                                         static_cast<long>(sms) * (cl > 1 ? 1 : 512 / threads));
-      if (cl == 4) return layer_bwd_launch<T, 512, 1, 4>(a, threads, blocks, grid, st);
-      if (cl == 2) return layer_bwd_launch<T, 512, 1, 2>(a, threads, blocks, grid, st);
-      return threads <= 256 ? layer_bwd_launch<T, 256, 2, 1>(a, threads, blocks, grid, st)
-                            : layer_bwd_launch<T, 512, 1, 1>(a, threads, blocks, grid, st);
-    }
+    if (a.cols % (16 * cl) == 0 && threads >= 64 && threads <= 512 && even)
+      return layer_bwd_ring<T, false>(a, cl, threads, a.cols / (8 * cl), sms, grid, st);
   }
+  // vectors of a row that begins within one, of a CTA
+  const long all = (static_cast<long>(a.cols) + 2 * V - 2) / V;
+  const int cl = all <= 1024 ? 1 : all <= 2048 ? 2 : 4;
+  const int vectors = static_cast<int>((all + cl - 1) / cl), threads = ((vectors + 1) / 2 + 31) / 32 * 32;
+  // The alternative takes features one by one, or 16-byte vectors through the caches. us there and here: fp32 8192 x 1021 47
+  // and 30, 8192 x 5119 255 and 139, 100 x 1021 level; bf16 8192 x 1021 36 and 27, 20000 x 601 80 and 39, but 2000 x 1021
+  // 13.6 and 15.5; beyond 8,192 features bf16 2048 x 12001 162 and 70, fp32 16 x 13496 25 and 8, 2048 x 16384 level. Shorter
+  // rows of whole vectors stay: bf16 8192 x 1000 22 and 25, fp32 8192 x 4096 87 and 114 to 127.
+  const bool better = a.cols > 8192 || ((!even || a.cols % V) && (es == 4 || a.rows >= 4096));
+  if (better && threads >= 64 && threads <= 512 && alike(a.dy, a.lddy) && alike(a.dx, a.lddx) && alike(a.dh, a.lddh))
+    return layer_bwd_ring<T, true>(a, cl, threads, vectors, sms, grid, st);
   return norm_bwd_vec<T, true>(a, sms, grid, st);
 }
 

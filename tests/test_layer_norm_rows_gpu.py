@@ -179,7 +179,10 @@ def test_layer_norm_in_place_and_special_rows():
                                                          (1500, 2047, HF, 1), (310, 4095, BF, 0), (1, 8224, BF, 0),
                                                          (76, 8224, HF, 8), (153, 10240, BF, 0), (700, 16384, HF, 0),
                                                          (2, 16416, BF, 0), (39, 16448, BF, 0), (200, 32768, HF, 0),
-                                                         (7, 32832, BF, 0)])
+                                                         (7, 32832, BF, 0),
+                                                         (37, 1021, BF, 8), (300, 4099, FP, 4), (20, 9001, HF, 16),
+                                                         (5, 30001, BF, 8), (16, 13496, FP, 0), (900, 4093, BF, 0),
+                                                         (160, 8195, FP, 0), (90, 16391, BF, 0), (41, 15999, HF, 0)])
 @pytest.mark.parametrize("skip", [False, True])
 def test_layer_norm_bwd(rows, cols, dtype, pad, skip):
     h, gamma, dy = (normal(1, rows, cols) + 0.5).to(dtype), normal(2, cols), normal(3, rows, cols, dtype=dtype)
