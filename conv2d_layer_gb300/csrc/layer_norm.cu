@@ -228,11 +228,156 @@ cudaError_t layer_vec(const NormArgs& a, int sms, cudaStream_t st) {
   }
   return rows_fwd<T, V, kLayer>(a, st);
 }
+// Rows that start off 16-byte boundaries, without an 8-bit output: the stream's rows are a multiple of eight apart, so that all
+// of a thread's rows start `m` features behind a boundary and its features stay the same. Vectors of 16 bytes in the middle
+// of a row, single features at its ends. With the residual, feature by feature in rows_fwd_kernel and here: bf16 8192 x 1021
+// 30 and 24 us, 8192 x 2047 137 and 52, 4096 x 7001 370 and 92 (floors 10, 20, 34), 300 x 4095 8.0 and 6.1; fp32 37312 x 399
+// 105 and 51 (35), 100 x 1021 bf16 3.5 and 3.7. Rows of 77, whose warps are half idle, stay there: 31 and 92.
+template <typename T, int U, bool WARP, int MT, int MB>
+__global__ void __launch_bounds__(MT, MB) layer_shift_kernel(const NormArgs a) {
+  constexpr int V = 16 / static_cast<int>(sizeof(T));
+  constexpr uint32_t kWhole = (1u << V) - 1u;
+  pdl_entry();
+  __shared__ float4 part[2][32];
+  const int tpr = WARP ? 32 : static_cast<int>(blockDim.x), nw = tpr / 32;
+  const int t = WARP ? static_cast<int>(threadIdx.x) & 31 : static_cast<int>(threadIdx.x);
+  const int warp = WARP ? 0 : t >> 5, lane = t & 31, per = WARP ? static_cast<int>(blockDim.x) / 32 : 1;
+  const long row0 = static_cast<long>(blockIdx.x) * per + (WARP ? threadIdx.x >> 5 : 0);
+  const long step = static_cast<long>(gridDim.x) * per;
+  const float cols = static_cast<float>(a.cols);
+  const int m = static_cast<int>(row0 * a.ldx % V);
+  int c[U], count = 0;   // the vectors' first columns; this warp's features
+  uint32_t there[U];     // a bit for each feature of a vector that is in the row
+  float g[U][V], b[U][V];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    c[u] = (u * tpr + t) * V - m;
+    there[u] = 0u;
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+      const bool on = c[u] + k >= 0 && c[u] + k < a.cols;
+      there[u] |= on ? 1u << k : 0u;
+      g[u][k] = on ? a.gamma[c[u] + k] : 0.f;
+      b[u][k] = on && a.beta ? a.beta[c[u] + k] : 0.f;
+    }
+    count += __popc(there[u]);
+  }
+  const float n = static_cast<float>(__reduce_add_sync(0xffffffffu, count)), over = n > 0.f ? 1.f / n : 0.f;
+  auto read = [&](const void* from, long ld, long row, T (&e)[U][V]) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const T* x = static_cast<const T*>(from) + row * ld + c[u];
+      if (there[u] == kWhole) {
+        ld_vec<T, V>(x, e[u]);
+      } else {
+#pragma unroll
+        for (int k = 0; k < V; ++k) e[u][k] = there[u] >> k & 1u ? x[k] : from_f<T>(0.f);
+      }
+    }
+  };
+  auto write = [&](void* to, long ld, long row, int u, const T (&e)[V]) {
+    T* x = static_cast<T*>(to) + row * ld + c[u];
+    if (there[u] == kWhole) {
+      st_vec<T, V>(x, e);
+    } else {
+#pragma unroll
+      for (int k = 0; k < V; ++k)
+        if (there[u] >> k & 1u) x[k] = e[k];
+    }
+  };
+  T e[U][V], f[U][V];
+  auto fetch = [&](long row) {
+    read(a.x, a.ldx, row, e);
+    if (a.r) read(a.r, a.ldr, row, f);
+  };
+  if (row0 < a.rows) fetch(row0);
+  int par = 0;
+  for (long row = row0; row < a.rows; row += step, par ^= 1) {
+    float v[U][V];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (a.r) {
+#pragma unroll
+        for (int k = 0; k < V; ++k) e[u][k] = from_f<T>(to_f(e[u][k]) + to_f(f[u][k]));
+        write(a.h, a.ldh, row, u, e[u]);
+      }
+#pragma unroll
+      for (int k = 0; k < V; ++k) v[u][k] = to_f(e[u][k]);
+    }
+    if (row + step < a.rows) fetch(row + step);
+    else pdl_release();
+    float sum = warp_sum(row_fold<U, V>(v, [](float2 s, float2 x) { return __fadd2_rn(s, x); }));  // zeros beside the row
+    float mean = WARP ? sum / n : sum * over, ss = 0.f;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (there[u] == kWhole) {
+        ss += row_fold<1, V>(reinterpret_cast<float(&)[1][V]>(v[u]), [&](float2 s, float2 x) {
+          const float2 d = __fadd2_rn(x, make_float2(-mean, -mean));
+          return __ffma2_rn(d, d, s);
+        });
+      } else {
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+          const float d = there[u] >> k & 1u ? v[u][k] - mean : 0.f;
+          ss = fmaf(d, d, ss);
+        }
+      }
+    }
+    ss = warp_sum(ss);
+    if constexpr (!WARP) {
+      if (lane == 0) part[par][warp] = make_float4(sum, ss, mean, n);
+      __syncthreads();  // once a row: the next one writes the other half of part
+      sum = ss = 0.f;
+#pragma unroll 8
+      for (int w = 0; w < nw; ++w) sum += part[par][w].x;
+      mean = sum / cols;
+#pragma unroll 8
+      for (int w = 0; w < nw; ++w) {
+        const float4 p = part[par][w];
+        const float d = p.z - mean;
+        ss += fmaf(p.w * d, d, p.y);
+      }
+    }
+    const float inv = 1.f / sqrtf(ss / cols + a.eps);
+    if (t == 0) {
+      if (a.mean) a.mean[row] = mean;
+      if (a.inv) a.inv[row] = inv;
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      T w[V];
+#pragma unroll
+      for (int k = 0; k < V; k += 2) {
+        float2 x = __fadd2_rn(make_float2(v[u][k], v[u][k + 1]), make_float2(-mean, -mean));
+        x = __fmul2_rn(x, make_float2(inv, inv));
+        x = __ffma2_rn(x, make_float2(g[u][k], g[u][k + 1]), make_float2(b[u][k], b[u][k + 1]));
+        w[k] = from_f<T>(x.x);
+        w[k + 1] = from_f<T>(x.y);
+      }
+      write(a.y, a.ldy, row, u, w);
+    }
+  }
+}
+template <typename T, int U, bool WARP, int MT, int MB>
+cudaError_t layer_shift(const NormArgs& a, int threads, int sms, cudaStream_t st) {
+  const long per = WARP ? threads / 32 : 1, need = (a.rows + per - 1) / per;
+  long blocks = std::min<long>(need, static_cast<long>(sms) * std::max(1, MT * MB / threads));
+  if (!WARP && blocks < need) blocks = std::max<long>(8, blocks / 8 * 8);  // a warp's rows are eight apart anyway
+  return launch_k(layer_shift_kernel<T, U, WARP, MT, MB>, dim3(static_cast<unsigned>(blocks)), dim3(threads), 0, st, 1, a);
+}
 template <typename T>
 cudaError_t layer_any(const NormArgs& a, int sms, cudaStream_t st) {
-  constexpr int es = sizeof(T);
+  constexpr int es = sizeof(T), V = 16 / es;
   if (a.cols > 16 * 32 / es && rows_fwd_ok(a, es, 32 / es)) return layer_vec<T, 32 / es>(a, sms, st);
   if (rows_fwd_ok(a, es, 16 / es)) return layer_vec<T, 16 / es>(a, sms, st);
+  auto alike = [&](const void* p, long ld) { return !p || ld % V == a.ldx % V; };
+  if (!a.q && a.cols > 256 && alike(a.r, a.ldr) && alike(a.h, a.ldh) && alike(a.y, a.ldy)) {
+    const int nv = (a.cols + 2 * V - 2) / V, threads = (nv + 31) / 32 * 32;
+    constexpr int UW = es == 2 ? 2 : 4;
+    if (nv <= 32 * UW) return layer_shift<T, UW, true, 256, 2>(a, 256, sms, st);
+    if (threads <= 512) return layer_shift<T, 1, false, 512, 2>(a, threads, sms, st);
+    if (threads <= 1024) return layer_shift<T, 2, false, 512, 1>(a, threads / 2 + threads / 2 % 32, sms, st);
+  }
   return rows_fwd<T, 1, kLayer>(a, st);
 }
 
