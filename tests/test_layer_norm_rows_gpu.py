@@ -246,6 +246,33 @@ def test_layer_norm_bwd_first_called_under_capture(cols):
                    cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 
 
+@pytest.mark.parametrize("rows,cols,dtype", [(40, 1021, BF), (37, 9001, HF), (37, 5119, FP), (4100, 777, BF), (500, 257, FP),
+                                             (9, 20001, BF)])
+def test_odd_rows_do_not_mix(rows, cols, dtype):
+    """Rows of NaN and infinities between others: those come out bit by bit as beside rows of zeros, and the columns behind
+    a strided output's rows stay as they were."""
+    gamma, beta = normal(1, cols), normal(2, cols)
+    x, r, dy = (normal(3 + i, rows, cols, dtype=dtype) for i in range(3))
+    bad = torch.arange(rows, device="cuda") % 2 == 1
+
+    def out():
+        return torch.full((rows, cols + 8), 7.0, device="cuda", dtype=dtype)
+
+    def run(v):
+        a, b, d = (torch.where(bad[:, None], torch.full_like(t, v), t) for t in (x, r, dy))
+        h, y, dx = out(), out(), out()
+        n = ops.layer_norm_fwd(strided(a, 8), gamma, beta, EPS, residual=strided(b, 8), h=h[:, :cols], y=y[:, :cols])
+        ops.layer_norm_bwd(h[:, :cols], gamma, n.mean, n.inv_std, strided(d, 8), dh=strided(d, 8), dx=dx[:, :cols],
+                           need_dgamma=False, need_dbeta=False)
+        return h, y, dx
+
+    zero = run(0.0)
+    for v in (float("nan"), float("inf")):
+        for got, want in zip(run(v), zero):
+            assert torch.equal(got[~bad], want[~bad]) and bool(got[~bad].isfinite().all())
+            assert bool((got[:, cols:] == 7).all())
+
+
 def test_layer_norm_without_rows():
     x, gamma = torch.empty(0, 64, device="cuda", dtype=BF), torch.ones(64, device="cuda")
     out = ops.layer_norm_fwd(x, gamma, gamma, residual=x, group=128)
