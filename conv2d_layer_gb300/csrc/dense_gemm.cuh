@@ -27,6 +27,7 @@
 #pragma once
 #include "ptx.cuh"
 #include "q8.cuh"
+#include "schedule.h"
 
 namespace c2d {
 
@@ -623,8 +624,8 @@ __device__ __forceinline__ void dense_mma(uint64_t l, uint64_t c, uint32_t d, ui
 // writes the slots of 16 k-blocks at a time, into one of two sets, and runs that far ahead of the MMAs: what it writes is
 // released at the scope of the cluster, which takes as long as a stage's MMAs two or three times over (with a slot in each
 // stage, written when the stage was free: 8192 x 8192 x 2048 182 us; a scale a thread in the loading warp 314). The MMA
-// thread copies a slot to the tensor memory with the first of its k-blocks, to a place that belongs to that k-block's
-// stage and so is free when the stage is: no copy meets an MMA that still reads.
+// thread copies a slot to the tensor memory with the first of its k-blocks, to the next of S places in turn (ScalePlaces):
+// no copy meets an MMA that still reads.
 constexpr int kScaleBlocks = 16;
 __host__ __device__ constexpr int dense_slot_bytes(int BN) { return BN > 128 ? 1536 : 1024; }
 __host__ __device__ constexpr int dense_slot_cols(int BN) { return BN > 128 ? 12 : 8; }
@@ -916,6 +917,7 @@ __global__ void __launch_bounds__(kPairThreads + dense_scale_threads(Q), 1) dens
       const uint64_t l = dense_desc<RMN, BYTES>(sbase), c = dense_desc<CMN, BYTES>(sbase + l_bytes);
       // where the scales at hand lie in tensor memory, and the set they come from
       [[maybe_unused]] uint32_t sf = 0, sb = 0, spar = 0;
+      [[maybe_unused]] ScalePlaces places = {static_cast<uint32_t>(S), 0};
       int s = 0, tc = 0;
       uint32_t par = 0;
       bool alive = true;
@@ -932,8 +934,8 @@ __global__ void __launch_bounds__(kPairThreads + dense_scale_threads(Q), 1) dens
           }
           tc_fence_after();
           if constexpr (Q == kBlockScaled) {
-            if (kb == w.kb0 || (kb & 3) == 0) {
-              sf = tmem + 2 * BN + s * dense_slot_cols(BN);
+            if (scales_begin(kb, w.kb0)) {
+              sf = tmem + 2 * BN + places.next() * dense_slot_cols(BN);
               scales_copy<true>(sbase + slots + sb * (dense_slots_bytes(BN) / 2) + slot_of(kb, BN), sf, BN);
             }
             const uint32_t byte = kb & 3;
@@ -1143,6 +1145,7 @@ __global__ void __launch_bounds__(kClusterThreads + dense_scale_threads(Q), 1) d
       const uint64_t l = dense_desc<LMN, BYTES>(sbase), c = dense_desc<CMN, BYTES>(sbase + l_bytes);
       // where the scales at hand lie in tensor memory, and the set they come from
       [[maybe_unused]] uint32_t sf = 0, sb = 0, spar = 0;
+      [[maybe_unused]] ScalePlaces places = {static_cast<uint32_t>(S), 0};
       int s = 0;
       uint32_t par = 0;
       for (int kb = kb0; kb < kb1; ++kb) {
@@ -1150,8 +1153,8 @@ __global__ void __launch_bounds__(kClusterThreads + dense_scale_threads(Q), 1) d
         if (Q == kBlockScaled && set_begins(kb, kb0) && !wait(&sfull[sb], spar, p.err, kSiteDenseFull)) break;
         tc_fence_after();
         if constexpr (Q == kBlockScaled) {
-          if (kb == kb0 || (kb & 3) == 0) {
-            sf = tmem + BN + s * dense_slot_cols(BN);
+          if (scales_begin(kb, kb0)) {
+            sf = tmem + BN + places.next() * dense_slot_cols(BN);
             scales_copy<false>(sbase + slots + sb * (dense_slots_bytes(BN) / 2) + slot_of(kb, BN), sf, BN);
           }
           const uint32_t byte = kb & 3;

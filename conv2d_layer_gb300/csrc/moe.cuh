@@ -494,6 +494,7 @@ __global__ void __launch_bounds__(kMoeThreads + dense_scale_threads(Q), 2) exper
       const uint32_t idesc = Q == kBlockScaled ? idesc_block(128, BN, false, false) : idesc_f32acc(128, BN, p.fmt, false, false);
       const uint64_t l = dense_desc<false, BYTES>(sbase), c = dense_desc<false, BYTES>(sbase + L * 16384);
       [[maybe_unused]] uint32_t sf = 0, sb = 0, spar = 0;
+      [[maybe_unused]] ScalePlaces places = {static_cast<uint32_t>(S), 0};
       int s = 0;
       uint32_t par = 0;
       bool alive = true;
@@ -511,8 +512,8 @@ __global__ void __launch_bounds__(kMoeThreads + dense_scale_threads(Q), 2) exper
           tc_fence_after();
           const uint32_t acc = kb > w.kb0, d = tmem + buf * L * BN;
           if constexpr (Q == kBlockScaled) {
-            if (kb == w.kb0 || (kb & 3) == 0) {
-              sf = tmem + buffers * L * BN + s * 4 * (L + 1);
+            if (scales_begin(kb, w.kb0)) {
+              sf = tmem + buffers * L * BN + places.next() * 4 * (L + 1);
               const uint32_t slot = sbase + slots + sb * (moe_slots_bytes(L) / 2) + (kb % kMoeSet / 4) * moe_slot_bytes(L);
 #pragma unroll
               for (int m = 0; m <= L; ++m) tmem_copy_scales<false>(sf + 4 * m, scales_desc(slot + 512 * m));
