@@ -174,8 +174,13 @@ class MixtureFeedForward(_Norm):
                                ("b1", b1, (experts, up)), ("b2", b2, (experts, width))):
             if t is not None and tuple(t.shape) != shape:
                 raise ValueError(f"{name}: shape {tuple(t.shape)} does not match {shape}")
-        if not 1 <= k <= experts:
-            raise ValueError(f"k: 1 to {experts} experts, got {k!r}")
+        if not 1 <= experts <= 256:
+            raise ValueError(f"router: 1 to 256 experts, got {experts}")
+        if not isinstance(k, int) or not 1 <= k <= min(experts, 16):
+            raise ValueError(f"k: 1 to {min(experts, 16)} experts, got {k!r}")
+        for name, n in (("width", width), ("inner features", inner)):
+            if n < 8 or n % 8:
+                raise ValueError(f"{name}: a multiple of 8, got {n}")
         dev = torch.device(device)
         self.k, self.act, self.gated, self.normalize, self.dtype = k, act, gated, normalize, dtype
         self._norm_init(norm, gamma, beta, eps, dev)
@@ -184,7 +189,13 @@ class MixtureFeedForward(_Norm):
         self.b1, self.b2 = (None if t is None else t.to(dev, torch.float32).contiguous() for t in (b1, b2))
 
     def quantize(self):
-        """Takes the experts to 8 bits, one scale for 128 x 128 weights, in place of what they were."""
+        """Takes the experts to 8 bits, one scale for 128 x 128 weights, in place of what they were (once: later calls change
+        nothing). Width and inner features must be multiples of 128."""
+        if isinstance(self.w1, ops.Q8):
+            return
+        width, inner = self.w2.shape[1:]
+        if width % 128 or inner % 128:
+            raise ValueError(f"8-bit experts have whole tiles: width and inner features in multiples of 128, got {width} and {inner}")
         self.w1, self.w2 = ops.moe_encode(self.w1), ops.moe_encode(self.w2)
 
     def fwd_infer(self, x, residual=None):

@@ -204,10 +204,11 @@ class Moe(NamedTuple):
 
 
 def moe_encode(w):
-    """Experts' weights [E, rows, cols] (rows a multiple of 128) as the Q8 that moe_fwd takes: one scale for 128 rows by
-    128 columns, none across two experts."""
-    if w.dim() != 3 or w.shape[1] % 128:
-        raise ValueError(f"w: experts by rows (a multiple of 128) by columns, got shape {tuple(w.shape)}")
+    """Experts' weights [E, rows, cols] (multiples of 128) as the Q8 that moe_fwd takes: one scale for 128 rows by 128
+    columns, none across two experts."""
+    if not isinstance(w, torch.Tensor) or w.dim() != 3 or w.shape[1] % 128 or w.shape[2] % 128:
+        got = f"shape {tuple(w.shape)}" if isinstance(w, torch.Tensor) else type(w).__name__
+        raise ValueError(f"w: experts by rows by columns (multiples of 128), got {got}")
     q = q8_encode(w.reshape(-1, w.shape[2]), TILE)
     return Q8(q.q.view(w.shape), q.scale.view(w.shape[0], w.shape[1] // 128, -1), TILE)
 
