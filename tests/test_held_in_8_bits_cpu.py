@@ -3,7 +3,7 @@ it does not pass them."""
 import pytest
 import torch
 
-from block_ref import U
+from block_ref import U, act_ref, dact_ref
 from held_ref import exponents, held_between
 from more_ref import q8_wide_ref
 from test_held_in_8_bits_gpu import down_bound, up_bound
@@ -63,3 +63,20 @@ def test_mistakes_in_the_experts_second_product_show(D, F, act, gated):
     wrong = held[0].clone()
     wrong[:128] *= 2  # a scale of h for another
     assert shows(w2 @ wrong) > 0.5
+
+
+def test_mistakes_in_the_gradients_8_bit_form_show():
+    M, K, N = 40, 200, 640
+    dy, z = normal(1, M, N).to(BF).double(), normal(2, M, N, std=1.5).to(BF).double()
+    w, _ = q8_wide_ref(normal(3, N, K, std=N ** -0.5), -128)
+    dz = dy * dact_ref("gelu", z)
+    low, high = held_between(dz, 2e-5 * dz.abs() + 2e-7 * dy.abs(), BF)
+    ref, tol = (low + high) / 2 @ w, (high - low) / 2 @ w.abs()
+    tol = tol + U[BF] * (ref.abs() + tol)
+    assert float(tol.norm()) < 0.02 * float(ref.norm())
+    right, _ = q8_wide_ref(dz.float().to(BF).double(), 128)
+    assert bool(((right @ w - ref).abs() <= tol).all())
+    before, _ = q8_wide_ref(dz, 128)  # encoded before it is rounded to the element type
+    wrong, _ = q8_wide_ref((dy * act_ref("sigmoid", z)).to(BF).double(), 128)
+    for other in (before, wrong, dz):
+        assert float(((other @ w - ref).abs() > tol).double().mean()) > 0.01

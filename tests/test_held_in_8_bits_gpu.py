@@ -1,9 +1,10 @@
-"""Products whose left operand the library itself takes to 8 bits on the way: h of the experts. A value's 8-bit form is known but where its own error reaches over the middle between two of them, so the bounds
+"""Products whose left operand the library itself takes to 8 bits on the way: h of the experts, dz of the block-scaled
+gradient. A value's 8-bit form is known but where its own error reaches over the middle between two of them, so the bounds
 stay a few percent of the results; and whole numbers, whose 8-bit forms are exact, have to come out bit by bit."""
 import pytest
 import torch
 
-from block_ref import STEP, U, act_ref, close, rounded
+from block_ref import STEP, U, act_ref, close, dact_ref, rounded
 from conv2d_layer_gb300 import abi, ops
 from held_ref import held_between
 from more_ref import q8_wide_ref, q8_wide_values
@@ -126,3 +127,35 @@ def test_experts_of_whole_numbers(T, D, F, pairs, k, gated, has_res):
             want[t] += (w2[e] @ h + b2[e].double()) / k
     assert float(want.abs().max()) < 2 ** 20
     assert torch.equal(got.y, want.float().to(BF))
+
+
+@pytest.mark.parametrize("M,K,N,dtype,act", [(65, 64, 200, BF, "tanh"), (500, 264, 136, HF, "sigmoid"), (4097, 256, 512, BF, "gelu"),
+                                             (3, 1001, 77, HF, "gelu"), (1, 300, 4096, BF, "silu"), (1000, 1000, 1000, BF, "silu")])
+def test_gradient_from_dz_in_8_bits(M, K, N, dtype, act):
+    w = ops.q8_encode(normal(1, N, K, std=K ** -0.5), ops.TILE)
+    dy, z = normal(2, M, N, dtype=dtype), normal(3, M, N, std=1.5, dtype=dtype)
+    dx, _, _ = ops.dense_bwd(None, w, dy, z, act, need_dw=False, need_dbias=False)
+    dz = dy.double() * dact_ref(act, z.double())
+    low, high = held_between(dz, 2e-5 * dz.abs() + 2e-7 * dy.double().abs(), dtype)
+    h, r = (low + high) / 2, (high - low) / 2
+    w64 = q8_wide_values(w)
+    ref = h @ w64
+    tol = r @ w64.abs() + (N / 16 + 20) * STEP * ((h.abs() + r) @ w64.abs())
+    assert float(tol.norm()) < 0.02 * float(ref.norm())
+    close(dx, ref, rounded(ref, dtype, tol), "dx")
+
+
+@pytest.mark.parametrize("M,K,N,dtype", [(1, 64, 300, BF), (333, 520, 700, HF), (3000, 1024, 2300, BF)])
+def test_gradient_behind_relu(M, K, N, dtype):
+    """dz is dy or zero, without an error: the bits of the product of dz taken to 8 bits beforehand."""
+    w = ops.q8_encode(normal(1, N, K, std=K ** -0.5), ops.TILE)
+    dy, z = normal(2, M, N, dtype=dtype), normal(3, M, N, dtype=dtype)
+    dx, _, _ = ops.dense_bwd(None, w, dy, z, "relu", need_dw=False, need_dbias=False)
+    dz = torch.where(z > 0, dy, torch.zeros_like(dy))
+    want, _, _ = ops.dense_bwd(None, w, dz, need_dw=False, need_dbias=False)
+    assert torch.equal(dx, want)
+    held = q8_wide_values(ops.q8_encode(dz, 128))
+    assert torch.equal(held, q8_wide_ref(dz.double(), 128)[0])
+    w64 = q8_wide_values(w)
+    ref = held @ w64
+    close(dx, ref, rounded(ref, dtype, (N / 16 + 20) * STEP * (held.abs() @ w64.abs())), "dx")
