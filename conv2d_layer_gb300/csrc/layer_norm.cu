@@ -417,7 +417,7 @@ __global__ void __launch_bounds__(MT, MB) layer_bwd_kernel(const NormBwdArgs a) 
   if (t == 0) {
     for (int i = 0; i < kRing; ++i) mbar_init(&full[i], 1);
     if (CL > 1)
-      for (int i = 0; i < 2; ++i) mbar_init(&met[i], 1);
+      for (int i = 0; i < 2; ++i) mbar_init(&met[i], 1 + static_cast<uint32_t>(nw));  // the bytes' count, and this CTA's warps
     fence_mbar_init();
     if (CL > 1)
       for (int i = 0; i < 2; ++i) mbar_arrive_expect_tx(&met[i], sent);
@@ -489,12 +489,15 @@ __global__ void __launch_bounds__(MT, MB) layer_bwd_kernel(const NormBwdArgs a) 
     // past the row's end dy is zero, so it counts in no sum
     float2 both = make_float2(warp_sum(dot.x + dot.y), warp_sum(sum.x + sum.y));
     // Once a row all warps meet: the next row writes the other half of part, this row's place is free. In a cluster each
-    // warp sends its sums to every CTA, whose barrier counts the bytes.
+    // warp sends its sums to every CTA, whose barrier counts the bytes; what is sent orders nothing before it, so the warp
+    // arrives there itself too, once it has read the row's place.
     if constexpr (CL > 1) {
       const int lane = t & 31;
       if (lane < CL)
         send_pair(mapa_shared(smem_u32(&part[par][rank * nw + (t >> 5)]), static_cast<uint32_t>(lane)), both,
                   mapa_shared(smem_u32(&met[par]), static_cast<uint32_t>(lane)));
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&met[par]);
       ok = ok && wait_cluster(&met[par], meet, a.err, kSiteLayerBwd);
       if (t == 0) mbar_arrive_expect_tx(&met[par], sent);  // for the row after next: none sends its sums before this warp
       if (par) meet ^= 1;
@@ -575,7 +578,7 @@ __global__ void __launch_bounds__(MT, MB) layer_bwd_shift_kernel(const NormBwdAr
   if (t == 0) {
     for (int i = 0; i < kRing; ++i) mbar_init(&full[i], 1);
     if (CL > 1)
-      for (int i = 0; i < 2; ++i) mbar_init(&met[i], 1);
+      for (int i = 0; i < 2; ++i) mbar_init(&met[i], 1 + static_cast<uint32_t>(nw));  // the bytes' count, and this CTA's warps
     fence_mbar_init();
     if (CL > 1)
       for (int i = 0; i < 2; ++i) mbar_arrive_expect_tx(&met[i], sent);
@@ -699,6 +702,8 @@ __global__ void __launch_bounds__(MT, MB) layer_bwd_shift_kernel(const NormBwdAr
       if (lane < CL)
         send_pair(mapa_shared(smem_u32(&part[par][rank * nw + (t >> 5)]), static_cast<uint32_t>(lane)), both,
                   mapa_shared(smem_u32(&met[par]), static_cast<uint32_t>(lane)));
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&met[par]);
       ok = ok && wait_cluster(&met[par], meet, a.err, kSiteLayerBwd);
       if (t == 0) mbar_arrive_expect_tx(&met[par], sent);
       if (par) meet ^= 1;
