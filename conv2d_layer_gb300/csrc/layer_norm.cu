@@ -3,6 +3,7 @@
 
 #include "rows.h"
 #include "rows_norm.cuh"
+#include "schedule.h"
 
 namespace c2d {
 namespace {
@@ -797,10 +798,13 @@ cudaError_t layer_bwd_launch(const NormBwdArgs& a, int threads, int vectors, lon
     if (dev < 64) fit[dev].store(most, std::memory_order_relaxed);
   }
   blocks = std::min<long>(blocks, most);
-  if (SHIFT && blocks < a.rows) blocks = std::max<long>(8, blocks / 8 * 8);  // rows of a block begin alike
+  if (SHIFT) blocks = blocks_alike(blocks, a.rows);
   *grid = static_cast<int>(blocks);
+  if (blocks == 0) return cudaSuccess;
   return launch_k(kernel, dim3(*grid * CL), dim3(threads), static_cast<size_t>(kRing) * 3 * 16 * vectors, st, CL, a);
 }
+// (grid 0: nothing was launched, because fewer than eight blocks fit the device, or the part of it that there is, and
+// there are more rows)
 template <typename T, bool SHIFT>
 cudaError_t layer_bwd_ring(const NormBwdArgs& a, int cl, int threads, int vectors, int sms, int* grid, cudaStream_t st) {
   // no more blocks than the workspace has rows for
@@ -833,8 +837,10 @@ cudaError_t layer_bwd(const NormBwdArgs& a, int sms, int* grid, cudaStream_t st)
   // 13.6 and 15.5; beyond 8,192 features bf16 2048 x 12001 162 and 70, fp32 16 x 13496 25 and 8, 2048 x 16384 level. Shorter
   // rows of whole vectors stay: bf16 8192 x 1000 22 and 25, fp32 8192 x 4096 87 and 114 to 127.
   const bool better = a.cols > 8192 || ((!even || a.cols % V) && (es == 4 || a.rows >= 4096));
-  if (better && threads >= 64 && threads <= 512 && alike(a.dy, a.lddy) && alike(a.dx, a.lddx) && alike(a.dh, a.lddh))
-    return layer_bwd_ring<T, true>(a, cl, threads, vectors, sms, grid, st);
+  if (better && threads >= 64 && threads <= 512 && alike(a.dy, a.lddy) && alike(a.dx, a.lddx) && alike(a.dh, a.lddh)) {
+    const cudaError_t e = layer_bwd_ring<T, true>(a, cl, threads, vectors, sms, grid, st);
+    if (e != cudaSuccess || *grid > 0) return e;
+  }
   return norm_bwd_vec<T, true>(a, sms, grid, st);
 }
 

@@ -29,4 +29,8 @@ struct ScalePlaces {
 // Whether k-block kb begins a group, for a loop that starts with kb0.
 C2D_HD bool scales_begin(int kb, int kb0) { return kb == kb0 || (kb & 3) == 0; }
 
+// Blocks (or clusters) that walk `rows` rows, block i those of i, i + blocks, ..., where all rows of a block must begin
+// alike: a block for each row, or a multiple of eight of them. Never more than `most`; 0 where neither is possible.
+C2D_HD long blocks_alike(long most, long rows) { return most >= rows ? rows : most / 8 * 8; }
+
 }  // namespace c2d

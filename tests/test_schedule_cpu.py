@@ -61,3 +61,31 @@ def test_places_of_scales_are_read_no_more_when_they_are_written(tmp_path):
     assert by_stage > 0  # what the count is for: places that belong to the stages
 
 
+
+
+BLOCKS = """
+#include <algorithm>
+#include <cstdio>
+#include "schedule.h"
+int main() {
+  // what there was: never fewer than eight
+  auto before = [](long most, long rows) { return most < rows ? std::max(8L, most / 8 * 8) : rows; };
+  for (int old = 0; old < 2; ++old) {
+    long many = 0, unlike = 0, idle = 0;
+    for (long most = 1; most <= 320; ++most)
+      for (long rows = 1; rows <= 700; ++rows) {
+        const long b = old ? before(most, rows) : c2d::blocks_alike(most, rows);
+        many += b > most || b > rows;
+        unlike += b < rows && b % 8 != 0;
+        idle += b == 0 && (most >= 8 || rows <= most);
+      }
+    std::printf("%ld %ld %ld\\n", many, unlike, idle);
+  }
+}
+"""
+
+
+def test_no_more_blocks_than_rows_or_than_the_workspace_has_room_for(tmp_path):
+    here, before = run(tmp_path, BLOCKS).splitlines()
+    assert here == "0 0 0"
+    assert int(before.split()[0]) > 0  # what the count is for
