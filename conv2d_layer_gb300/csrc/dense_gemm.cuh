@@ -327,11 +327,13 @@ __device__ __forceinline__ void buffer_take(int lane) {
   __syncwarp();
 }
 // Stores the written buffer: by TMA (whole rows, clipped at the matrix's ends; fp32 sums are added there), or word
-// by word.
+// by word. A TMA store writes whole 16 bytes: where a row ends within some, it would write over what lies behind the row
+// in a wider buffer, so the last columns go word by word there.
 template <typename E, int RB>
 __device__ __forceinline__ void buffer_store(uint32_t buf, bool tma, const CUtensorMap* map, int n, long m0, int split,
                                              E* g, long ld, int nr, int nc, bool accumulate, int lane) {
-  if (tma) {
+  constexpr int W = RB / static_cast<int>(sizeof(E));  // columns of the buffer
+  if (tma && (nc >= W || nc * static_cast<int>(sizeof(E)) % 16 == 0)) {
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) {
