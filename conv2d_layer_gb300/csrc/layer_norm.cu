@@ -555,7 +555,7 @@ __global__ void __launch_bounds__(MT, MB) layer_bwd_kernel(const NormBwdArgs a) 
 // that they all start `m` features behind a 16-byte boundary, and a thread has the same features in each. A copy takes whole
 // 16 bytes; what is of the rows beside is set to zero where it is taken, and the end of the last row, behind which nothing
 // may be read, comes feature by feature, as do the ends of a row of dx go. Those ends hold the whole block up: 8192 x 4088
-// bf16, which has none, 67 us, 8192 x 4095 96 (floor 40).
+// bf16, which has none, 63 us, 8192 x 4095 100 (floor 40; 8192 x 4096 in layer_bwd_kernel 49).
 template <typename T, int MT, int MB, int CL>
 __global__ void __launch_bounds__(MT, MB) layer_bwd_shift_kernel(const NormBwdArgs a) {
   constexpr int V = 16 / static_cast<int>(sizeof(T));  // features of a vector; a thread has two vectors, V pairs
@@ -835,7 +835,8 @@ cudaError_t layer_bwd(const NormBwdArgs& a, int sms, int* grid, cudaStream_t st)
   // The alternative takes features one by one, or 16-byte vectors through the caches. us there and here: fp32 8192 x 1021 47
   // and 30, 8192 x 5119 255 and 139, 100 x 1021 level; bf16 8192 x 1021 36 and 27, 20000 x 601 80 and 39, but 2000 x 1021
   // 13.6 and 15.5; beyond 8,192 features bf16 2048 x 12001 162 and 70, fp32 16 x 13496 25 and 8, 2048 x 16384 level. Shorter
-  // rows of whole vectors stay: bf16 8192 x 1000 22 and 25, fp32 8192 x 4096 87 and 114 to 127.
+  // rows of whole vectors stay: bf16 8192 x 1000 22 and 25, fp32 8192 x 4096 87 and 114 to 127. (The 4,096 rows were fitted
+  // at 601 to 1,021 features and are too many for long rows: 4095 x 8191, there, 154; 4096 x 8191, here, 105.)
   const bool better = a.cols > 8192 || ((!even || a.cols % V) && (es == 4 || a.rows >= 4096));
   if (better && threads >= 64 && threads <= 512 && alike(a.dy, a.lddy) && alike(a.dx, a.lddx) && alike(a.dh, a.lddh)) {
     const cudaError_t e = layer_bwd_ring<T, true>(a, cl, threads, vectors, sms, grid, st);

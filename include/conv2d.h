@@ -199,7 +199,8 @@ int conv2d_bwd(const conv2d_desc* desc, const void* x, const void* w, const floa
  * N*H*W rows of C columns) by columns (features), each described by a
  * conv2d_mat. The conventions above hold (device pointers aligned to 16
  * bytes, caller-owned memory, asynchronous on `stream`, status codes), with
- * these differences: rows may be strided, a row count of zero is valid (the
+ * these differences: rows may be strided (what lies between the rows of an
+ * output stays as it was), a row count of zero is valid (the
  * call writes nothing, except that gradients to be overwritten become zero),
  * and gradients are accumulated only where `accumulate` is nonzero and
  * overwritten otherwise.
