@@ -21,6 +21,12 @@
 // before the up kernel, which that one has waited for. An up CTA releases them only once it holds its own tensor memory:
 // they keep theirs until the up kernel has ended.
 //
+// Clusters that each hold tensor memory on one SM and wait for it on another would wait for ever, so what runs on an SM at
+// once must never want more than its 512 columns together. Registers see to that: these kernels take 72 to 96 a thread, so a
+// third CTA does not fit, nor the dense layer's beside two; beside one there is room for one forward CTA of at most 128
+// columns or two of the gradients' (the block-scaled ones and the pairs fill an SM by themselves), or of the conv layer's
+// kernels for a weight gradient of 64 columns.
+//
 // Measured: 16 tokens, 8 experts of (4096, 8192), gated, bf16: 1.6 GB in 241 to 255 us, 0.92 to 0.98 of the copy rate. One
 // token, 8 of 64 experts of (2048, 1024): 101 MB in 33 us, where memory takes 15: three starts of 3 to 4 us each (launch,
 // routing, first copies) and as much for the joins. As one kernel, whose down CTAs waited for counters that the up CTAs
